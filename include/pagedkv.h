@@ -83,7 +83,7 @@ typedef enum pkv_kv_dtype { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1 } pkv_kv_dtype;
 
 /* Device error word values (bit flags, OR-ed together by the kernels). */
 #define PKV_DEVERR_BLOCK_ID 1   /* block table entry outside [0, num_blocks) */
-#define PKV_DEVERR_LENGTH 2     /* q_len > context_len, or a negative length */
+#define PKV_DEVERR_LENGTH 2     /* q_len > context_len, a negative length, or rows past a buffer's end */
 #define PKV_DEVERR_SLOT 4       /* slot >= num_blocks * 16 in an append */
 #define PKV_DEVERR_TIMEOUT 8    /* a bounded wait inside a kernel expired */
 #define PKV_DEVERR_RANGE 16     /* pkv_paged_prefill: a finite V value of magnitude >= 65536;
@@ -376,6 +376,189 @@ PKV_API pkv_status pkv_paged_attention_noalloc(const pkv_cache* cache, const voi
                                                const int32_t* context_lens, const int32_t* q_lens,
                                                int32_t num_seqs, int32_t max_q_len, float scale, void* out,
                                                int32_t num_ctas, int32_t* device_error, void* stream);
+
+/* ------------------------------------------------------------------ rows
+ *
+ * Entry points over rows of projections (queries, keys and values before they
+ * are cached, or read back from the cache).
+ */
+typedef enum pkv_dtype { PKV_BF16 = 0, PKV_FP16 = 1, PKV_FP32 = 2 } pkv_dtype;
+
+/* A tensor of rows: element (token t, head h, dim d) sits at element
+ * t * token_stride + h * head_stride + d of `data` (device), so a view of a
+ * fused projection's output needs no copy.  data and, where there is more
+ * than one token or head, both strides in bytes must be multiples of 16 (else
+ * PKV_ERR_INVALID_ARG).  An output's rows must not overlap each other. */
+typedef struct pkv_rows {
+    void* data;
+    int64_t token_stride;      /* elements */
+    int64_t head_stride;       /* elements */
+    int32_t num_heads;
+} pkv_rows;
+
+/* A rotation: pair i turns by position * inv_freq[i] radians.  Host memory;
+ * it is passed to the kernels by value. */
+#define PKV_ROPE_MAX_PAIRS 128
+typedef struct pkv_rope {
+    int32_t rotary_dim;        /* rotated leading dimensions of a head, even; 0: no rotation */
+    int32_t interleaved;       /* 0: pairs (i, i + rotary_dim / 2); else pairs (2i, 2i + 1) */
+    float magnitude;           /* factor of cos and sin (1 but for some scalings) */
+    int32_t reserved;          /* 0 */
+    double inv_freq[PKV_ROPE_MAX_PAIRS];
+} pkv_rope;
+
+/* How the frequencies f_i = theta^(-2i / rotary_dim) are scaled for contexts
+ * `factor` times longer than the one trained on (original_len tokens):
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   NTK     theta replaced by theta * factor^(rotary_dim / (rotary_dim - 2))
+ *   BANDS   by the turns r = original_len f_i / 2 pi that a pair makes over the
+ *           original context: t = clamp((r - low) / (high - low), 0, 1),
+ *           f_i (t + (1 - t) / factor)
+ *   RAMP    the same between two pair indices: idx(r) = rotary_dim
+ *           ln(original_len / 2 pi r) / (2 ln theta), from lo = max(0,
+ *           floor(idx(high))) to hi = min(rotary_dim - 1, ceil(idx(low))),
+ *           u = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *           f_i ((1 - u) + u / factor), magnitude 0.1 ln(factor) + 1 */
+typedef enum pkv_rope_scaling {
+    PKV_ROPE_NONE = 0, PKV_ROPE_LINEAR = 1, PKV_ROPE_NTK = 2, PKV_ROPE_BANDS = 3, PKV_ROPE_RAMP = 4
+} pkv_rope_scaling;
+
+/* Fill *rope (host only).  rotary_dim even, 2 .. 256 (NTK: at least 4);
+ * theta > 1; factor >= 1 unless scaling is NONE; BANDS and RAMP:
+ * original_len >= 1 and 0 < low < high.  Otherwise PKV_ERR_INVALID_ARG.
+ * A caller with frequencies of its own fills the struct itself. */
+PKV_API pkv_status pkv_rope_init(pkv_rope* rope, int32_t rotary_dim, int32_t interleaved, double theta,
+                                 int32_t scaling, double factor, int64_t original_len, double low, double high);
+
+/*
+ * Norm and rotation of query and key rows, per head row x:
+ *   y = x / sqrt(mean(x^2) + eps) * w       (norm_eps >= 0; w = 1 where the weight is NULL)
+ *   y = rotation of y at the token's position (rope not NULL and rotary_dim > 0)
+ * in fp32 and rounded once (nearest even) to the rows' type.  The angle of
+ * any 32-bit position is exact to 2^-32 of a turn.
+ *
+ *   q_in, q_out    query rows and where they go (the same views: in place)
+ *   k_in, k_out    key rows, both NULL if there are none; otherwise as q
+ *   dtype          pkv_dtype of rows and weights
+ *   head_dim       a multiple of 16 bytes, at most 256; rotary_dim <= head_dim
+ *   positions      device int32 [num_tokens], any sign; NULL without a rotation
+ *   inverse        rotate by the negated angles: the transpose of the rotation
+ *                  (its gradient; for magnitude 1 also its inverse).  Without a
+ *                  norm only (else PKV_ERR_INVALID_ARG).
+ *   q_weight, k_weight  device [head_dim], 16-byte aligned, or NULL
+ *   norm_eps       < 0: no norm (weights must be NULL)
+ *
+ * One launch, one CTA per token; num_tokens <= 2^31 - 1.  It lets the next
+ * kernel on the stream start only once it has completed (an attention reads
+ * q before its own dependency wait).
+ */
+PKV_API pkv_status pkv_qk_norm_rope(const pkv_rows* q_in, const pkv_rows* q_out, const pkv_rows* k_in,
+                                    const pkv_rows* k_out, int32_t dtype, int32_t head_dim, int64_t num_tokens,
+                                    const int32_t* positions, const pkv_rope* rope, int32_t inverse,
+                                    const void* q_weight, const void* k_weight, float norm_eps, void* stream);
+
+/*
+ * The same pass over a step's bf16 query, key and value rows, which also
+ * writes K (normed and rotated) and V (as given) into their cache slots: one
+ * read of each row, one launch.
+ *
+ *   q_in, q_out    optional query rows (both NULL: none; num_heads a multiple of Hkv)
+ *   k, v           key and value rows, num_heads = the cache's num_kv_heads
+ *   k_out          optional: the normed and rotated key rows too (bf16), for an
+ *                  attention over rows (pkv_prompt_attention); NULL: not wanted.
+ *                  It may be the same view as k.
+ *   slot_mapping, positions, device_error   as for pkv_paged_kv_append_rope: a
+ *                  token with a negative slot has its q (and k_out) rows written
+ *                  and no cache row; a slot at or beyond num_blocks * 16 likewise,
+ *                  with PKV_DEVERR_SLOT.
+ *   fp8_scales_from_values   the rule of pkv_paged_kv_append_rope (FP8 caches;
+ *                  a block whose offset-0 slot this call writes gets the scale
+ *                  max |value| / 448 of the call's values in it; other blocks
+ *                  keep theirs).  The tokens of a block may stand anywhere in
+ *                  the call; consecutive ones are fastest (others cost a scan of
+ *                  the slots per token).
+ *
+ * A bf16 cache receives exactly the rows that k_out does.  An FP8 cache
+ * receives the codes of the fp32 rows divided by the page's scale (IEEE fp32
+ * division, nearest even, saturating), and scales chosen here come from the
+ * fp32 rows: one rounding between projection and code.
+ */
+PKV_API pkv_status pkv_paged_kv_append_norm_rope(const pkv_cache* cache, const pkv_rows* q_in, const pkv_rows* q_out,
+                                                 const pkv_rows* k, const pkv_rows* v, const pkv_rows* k_out,
+                                                 const int64_t* slot_mapping, int64_t num_tokens,
+                                                 const int32_t* positions, const pkv_rope* rope, const void* q_weight,
+                                                 const void* k_weight, float norm_eps,
+                                                 int32_t fp8_scales_from_values, int32_t* device_error, void* stream);
+
+/*
+ * Read cached tokens back into rows (the inverse of the appends): sequence
+ * b's positions starts[b] .. starts[b] + lens[b] - 1, packed by sequence
+ * (rows lens[0] + ... + lens[b-1] onwards), K to k_out and V to v_out.
+ * bf16 caches: the stored values; FP8 caches: code * scale in fp32, rounded
+ * once.  Converted to dtype (bf16 from a bf16 cache: the bits).
+ *
+ *   block_tables, max_blocks_per_seq   as for pkv_paged_attention
+ *   starts, lens   device int32 [num_seqs]; starts NULL: all 0
+ *   num_rows       rows of the outputs, >= the sum of lens.  Rows at and past it
+ *                  are not written (PKV_DEVERR_LENGTH); rows behind the last
+ *                  sequence's are left as they were.
+ *   k_out, v_out   either may be NULL; num_heads = the cache's num_kv_heads
+ * A sequence with a negative start or length, or past its block-table row,
+ * sets PKV_DEVERR_LENGTH and leaves its rows unwritten; a bad block id sets
+ * PKV_DEVERR_BLOCK_ID and leaves its page's rows unwritten.
+ */
+PKV_API pkv_status pkv_paged_kv_read(const pkv_cache* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* starts, const int32_t* lens, int32_t num_seqs, int64_t num_rows,
+                                     const pkv_rows* k_out, const pkv_rows* v_out, int32_t dtype,
+                                     int32_t* device_error, void* stream);
+
+/*
+ * Causal attention of packed prompts, or prompt chunks, over key and value
+ * rows: the prompt path for what pkv_paged_prefill does not take (FP8 caches,
+ * whose prompts attend their rows before or beside the encoding, and whose
+ * later chunks attend rows read back by pkv_paged_kv_read; fp16; any group
+ * size).  Query i (0 <= i < Q_b) of sequence b and head h sees keys
+ * j = 0 .. L_b - Q_b + i of kv-head h / G:
+ *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j).
+ * A query that sees no key (L_b - Q_b + i < 0) gets out = 0 and lse = -inf.
+ *
+ *   q, out         rows of sum(q_lens) queries, num_heads = Hq; k, v rows of
+ *                  sum(kv_lens) keys, num_heads = Hkv; Hq = G * Hkv, G <= 128.
+ *                  Inputs: head and token strides positive where there is more
+ *                  than one head or token.
+ *   lse            optional device fp32 [num_q_rows][Hq]
+ *   dtype          PKV_BF16 or PKV_FP16 (q, k, v and out); head_dim 64 or 128
+ *   num_q_rows, num_kv_rows   rows of the tensors (fewer than 2^31)
+ *   q_lens, kv_lens   device int32 [num_seqs]
+ *   q_starts, kv_starts   device int64 [num_seqs], each sequence's first row, or
+ *                  NULL: packed (padded batches and slices of larger tensors give
+ *                  starts).  Rows outside every sequence are left as they were.
+ *   max_q_len      host upper bound of q_lens, >= 1
+ *   scale          finite, > 0
+ *   workspace      >= pkv_prompt_workspace_size() bytes, 16-byte aligned, not
+ *                  shared by concurrent calls (or by graphs that may run at the
+ *                  same time); it needs no initialisation.  With it, few rows
+ *                  over long contexts are split along the keys and joined by a
+ *                  second launch; NULL: never split.
+ *   device_error   optional device int32 error word
+ * A sequence with a negative or too long q_len, or with rows outside its
+ * tensors, sets PKV_DEVERR_LENGTH and its rows are left as they were.
+ *
+ * Precision: q.k and weights times V on the tensor cores in the inputs' type
+ * with fp32 accumulation; the weights 2^(s - m) are rounded to the inputs'
+ * type (bf16: 8 significant bits, fp16: 11), sums and statistics are fp32.
+ * NaN or infinity in a key or value row reaches the queries that see it, and
+ * no other.  Deterministic.  Reads nothing before the previous kernel on the
+ * stream has completed.  The wait limit of pkv_debug_set_wait_limit applies.
+ */
+PKV_API size_t pkv_prompt_workspace_size(void);
+PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, const pkv_rows* v, const pkv_rows* out,
+                                        float* lse, int32_t dtype, int32_t head_dim, int64_t num_q_rows,
+                                        int64_t num_kv_rows, const int32_t* q_lens, const int32_t* kv_lens,
+                                        const int64_t* q_starts, const int64_t* kv_starts, int32_t num_seqs,
+                                        int32_t max_q_len, float scale, void* workspace, size_t workspace_bytes,
+                                        int32_t* device_error, void* stream);
 
 /*
  * Read and clear a device error word: either the first 4 bytes of an

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -39,6 +40,14 @@ class CacheDesc(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
                 ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+ROPE_MAX_PAIRS = 128
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("inv_freq", ctypes.c_double * ROPE_MAX_PAIRS)]
 
 
 def lib():
@@ -96,6 +105,22 @@ def lib():
             L.pkv_paged_kv_append_rope.restype = c.c_int
             L.pkv_paged_kv_append_rope.argtypes = [c.POINTER(CacheDesc), vp, vp, vp, i64, vp, c.c_float, vp, i32,
                                                    i32, vp, vp]
+            pc = c.POINTER(CacheDesc)
+            L.pkv_rope_init.restype = c.c_int
+            L.pkv_rope_init.argtypes = [c.POINTER(RopeDesc), i32, i32, c.c_double, i32, c.c_double, i64, c.c_double,
+                                        c.c_double]
+            L.pkv_qk_norm_rope.restype = c.c_int
+            L.pkv_qk_norm_rope.argtypes = [vp, vp, vp, vp, i32, i32, i64, vp, vp, i32, vp, vp, c.c_float, vp]
+            L.pkv_paged_kv_append_norm_rope.restype = c.c_int
+            L.pkv_paged_kv_append_norm_rope.argtypes = [pc, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, c.c_float,
+                                                        i32, vp, vp]
+            L.pkv_paged_kv_read.restype = c.c_int
+            L.pkv_paged_kv_read.argtypes = [pc, vp, i32, vp, vp, i32, i64, vp, vp, i32, vp, vp]
+            L.pkv_prompt_workspace_size.restype = c.c_size_t
+            L.pkv_prompt_workspace_size.argtypes = []
+            L.pkv_prompt_attention.restype = c.c_int
+            L.pkv_prompt_attention.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, i32, i32,
+                                               c.c_float, vp, c.c_size_t, vp, vp]
             L.pkv_copy_blocks.restype = c.c_int
             L.pkv_copy_blocks.argtypes = [c.POINTER(CacheDesc), vp, i32, vp, vp, vp]
             L.pkv_debug_set_wait_limit.restype = None
@@ -306,6 +331,226 @@ def prefill(cache: PagedKVCache, q, block_tables, context_lens, q_lens, max_q_le
                                  _ptr(device_error), _stream(stream))
     _check(st, "pkv_paged_prefill")
     return out
+
+
+# ------------------------------------------------------------------ rows
+
+_ROWS = struct.Struct("@Pqqi4x")            # pkv_rows
+_ROW_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "ramp": 4}
+
+
+class Rope:
+    """A rotation (pkv_rope_init): the first `rotary_dim` dimensions of a head,
+    in pairs (i, i + rotary_dim / 2) or, interleaved, (2i, 2i + 1), with
+    frequencies theta^(-2i / rotary_dim) scaled by one of ROPE_SCALINGS.
+    `inv_freq` and `magnitude` are the values in use."""
+
+    def __init__(self, rotary_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, original_len: int = 0, low: float = 1.0, high: float = 4.0):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+        self.desc = RopeDesc()
+        _check(lib().pkv_rope_init(ctypes.byref(self.desc), int(rotary_dim), int(bool(interleaved)), float(theta),
+                                   ROPE_SCALINGS[scaling], float(factor), int(original_len), float(low), float(high)),
+               "pkv_rope_init")
+        self._ref = ctypes.addressof(self.desc)
+
+    @property
+    def rotary_dim(self) -> int:
+        return int(self.desc.rotary_dim)
+
+    @property
+    def magnitude(self) -> float:
+        return float(self.desc.magnitude)
+
+    @property
+    def inv_freq(self):
+        return list(self.desc.inv_freq[:self.rotary_dim // 2])
+
+
+def _row_view(t, name, dtype, device, tokens, dim, heads=None):
+    """pkv_rows of t [tokens, heads, dim] (any strides but the last)."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [{tokens}, {'heads' if heads is None else heads}, {dim}], got {list(shape)}")
+    if t.dtype is not dtype or strides[2] != 1 or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} on the same GPU with consecutive elements in a row")
+    return _ROWS.pack(t.data_ptr(), strides[0], strides[1], shape[1])
+
+
+def _vector(t, name, dtype, device, numel):
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be {numel} contiguous {dtype} values on the same GPU")
+    return t.data_ptr()
+
+
+def _weight(t, name, dtype, device, dim):
+    return None if t is None else _vector(t, name, dtype, device, dim)
+
+
+def _error_word(t, device):
+    return None if t is None else _vector(t, "device_error", torch.int32, device, 1)
+
+
+def _device_of(t, name):
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be on a GPU")
+    return device
+
+
+def _call(fn, what, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current and, unless one is
+    given, on that device's current stream."""
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream))
+    else:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else int(stream.cuda_stream))
+    if st != 0:
+        raise PagedKVError(st, what)
+
+
+def qk_norm_rope(q, k=None, positions=None, rope: Rope | None = None, q_weight=None, k_weight=None, eps=None,
+                 q_out=None, k_out=None, inverse: bool = False, stream=None):
+    """pkv_qk_norm_rope: query rows q [T, Hq, D] and key rows k [T, Hkv, D]
+    (views of a fused projection are fine; bf16, fp16 or fp32), normed per head
+    where eps is given, rotated at int32 positions [T] where rope is.  Returns
+    (q_out, k_out): new tensors unless given (q_out=q: in place)."""
+    device, dtype = _device_of(q, "q"), q.dtype
+    if q.dim() != 3 or dtype not in _ROW_DTYPES:
+        raise ValueError("q must be [tokens, heads, head_dim] in bfloat16, float16 or float32")
+    T, _, D = q.shape
+    if q_out is None:
+        q_out = q.new_empty(q.shape)
+    if k is not None and k_out is None:
+        k_out = k.new_empty(k.shape)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    if eps is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights without eps")
+    if eps is not None and not eps >= 0:
+        raise ValueError("eps must not be negative")
+    if rope is not None and positions is None:
+        raise ValueError("rope without positions")
+    _call(lib().pkv_qk_norm_rope, "pkv_qk_norm_rope", device, stream,
+          _row_view(q, "q", dtype, device, T, D), _row_view(q_out, "q_out", dtype, device, T, D, q.shape[1]),
+          None if k is None else _row_view(k, "k", dtype, device, T, D),
+          None if k is None else _row_view(k_out, "k_out", dtype, device, T, D, k.shape[1]),
+          _ROW_DTYPES[dtype], D, T,
+          None if positions is None else _vector(positions, "positions", torch.int32, device, T),
+          None if rope is None else rope._ref, inverse, _weight(q_weight, "q_weight", dtype, device, D),
+          _weight(k_weight, "k_weight", dtype, device, D), -1.0 if eps is None else eps)
+    return q_out, k_out
+
+
+def append_norm_rope(cache: PagedKVCache, q, k, v, slot_mapping, positions=None, rope: Rope | None = None,
+                     q_weight=None, k_weight=None, eps=None, q_out=None, k_out=None,
+                     fp8_scales_from_values: bool = False, device_error=None, stream=None):
+    """pkv_paged_kv_append_norm_rope: the rows of a step normed and rotated as
+    by qk_norm_rope (bf16), K and V written into their slots (int64 [T]).
+    Returns q_out (a new tensor unless given; None for q=None).  k_out, if
+    given, receives the normed and rotated key rows too."""
+    device, bf16 = _device_of(k, "k"), torch.bfloat16
+    T, H, D = k.shape[0], cache.num_kv_heads, cache.head_dim
+    for t in (cache.k, cache.v, cache.k_scales, cache.v_scales):
+        if t is not None and t.get_device() != device:
+            raise ValueError("the cache must be on the rows' GPU")
+    if q is not None and q_out is None:
+        q_out = q.new_empty(q.shape)
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if eps is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights without eps")
+    if eps is not None and not eps >= 0:
+        raise ValueError("eps must not be negative")
+    if rope is not None and positions is None:
+        raise ValueError("rope without positions")
+    _call(lib().pkv_paged_kv_append_norm_rope, "pkv_paged_kv_append_norm_rope", device, stream,
+          ctypes.byref(cache.desc()), None if q is None else _row_view(q, "q", bf16, device, T, D),
+          None if q is None else _row_view(q_out, "q_out", bf16, device, T, D, q.shape[1]),
+          _row_view(k, "k", bf16, device, T, D, H), _row_view(v, "v", bf16, device, T, D, H),
+          None if k_out is None else _row_view(k_out, "k_out", bf16, device, T, D, H),
+          _vector(slot_mapping, "slot_mapping", torch.int64, device, T), T,
+          None if positions is None else _vector(positions, "positions", torch.int32, device, T),
+          None if rope is None else rope._ref, _weight(q_weight, "q_weight", bf16, device, D),
+          _weight(k_weight, "k_weight", bf16, device, D), -1.0 if eps is None else eps,
+          bool(fp8_scales_from_values), _error_word(device_error, device))
+    return q_out
+
+
+def read_cache(cache: PagedKVCache, block_tables, lens, num_rows: int, starts=None, dtype=torch.bfloat16, k_out=None,
+               v_out=None, device_error=None, stream=None):
+    """pkv_paged_kv_read: positions starts[b] .. starts[b] + lens[b] - 1 of each
+    sequence (starts None: 0) as packed rows; num_rows >= sum(lens).  Returns
+    (k, v) [num_rows, Hkv, D]: new tensors of `dtype` unless given."""
+    device, n = _device_of(block_tables, "block_tables"), lens.numel()
+    shape = (int(num_rows), cache.num_kv_heads, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=block_tables.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=block_tables.device)
+    dtype = k_out.dtype
+    if dtype not in _ROW_DTYPES:
+        raise ValueError("rows must be bfloat16, float16 or float32")
+    for t in (cache.k, cache.v, cache.k_scales, cache.v_scales):
+        if t is not None and t.get_device() != device:
+            raise ValueError("the cache must be on the block tables' GPU")
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    _call(lib().pkv_paged_kv_read, "pkv_paged_kv_read", device, stream, ctypes.byref(cache.desc()),
+          _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()), block_tables.shape[1],
+          None if starts is None else _vector(starts, "starts", torch.int32, device, n),
+          _vector(lens, "lens", torch.int32, device, n), n, shape[0],
+          _row_view(k_out, "k_out", dtype, device, shape[0], shape[2], shape[1]),
+          _row_view(v_out, "v_out", dtype, device, shape[0], shape[2], shape[1]), _ROW_DTYPES[dtype],
+          _error_word(device_error, device))
+    return k_out, v_out
+
+
+def prompt_workspace_size() -> int:
+    n = lib().pkv_prompt_workspace_size()
+    if n == 0:
+        raise PagedKVError(4, "pkv_prompt_workspace_size")
+    return int(n)
+
+
+def make_prompt_workspace(device="cuda"):
+    """A workspace for prompt_attention on the given device (uninitialised:
+    it needs none)."""
+    with torch.cuda.device(device):
+        return torch.empty(prompt_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def prompt_attention(q, k, v, q_lens, kv_lens, max_q_len: int, scale: float, out=None, lse=None, q_starts=None,
+                     kv_starts=None, workspace=None, device_error=None, stream=None):
+    """pkv_prompt_attention: causal attention of packed prompts over key and
+    value rows (bf16 or fp16; q [Tq, Hq, D], k and v [Tk, Hkv, D], views are
+    fine).  Returns (out, lse): new tensors unless given; lse fp32 [Tq, Hq],
+    natural logarithm.  With starts, rows outside every sequence are not
+    written."""
+    device, dtype = _device_of(q, "q"), q.dtype
+    if q.dim() != 3 or dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be [rows, heads, head_dim] in bfloat16 or float16")
+    (Tq, Hq, D), Tk, n = q.shape, k.shape[0], q_lens.numel()
+    if out is None:
+        out = q.new_empty(q.shape)
+    if lse is None:
+        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+    if workspace is not None and (workspace.get_device() != device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous on the same GPU")
+    kr = _row_view(k, "k", dtype, device, Tk, D)
+    _call(lib().pkv_prompt_attention, "pkv_prompt_attention", device, stream,
+          _row_view(q, "q", dtype, device, Tq, D), kr, _row_view(v, "v", dtype, device, Tk, D, k.shape[1]),
+          _row_view(out, "out", dtype, device, Tq, D, Hq), _vector(lse, "lse", torch.float32, device, Tq * Hq),
+          _ROW_DTYPES[dtype], D, Tq, Tk, _vector(q_lens, "q_lens", torch.int32, device, n),
+          _vector(kv_lens, "kv_lens", torch.int32, device, n),
+          None if q_starts is None else _vector(q_starts, "q_starts", torch.int64, device, n),
+          None if kv_starts is None else _vector(kv_starts, "kv_starts", torch.int64, device, n), n, max_q_len, scale,
+          None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel() * workspace.element_size(), _error_word(device_error, device))
+    return out, lse
 
 
 def read_device_error(error_word, stream=None) -> int:

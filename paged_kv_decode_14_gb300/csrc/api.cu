@@ -66,6 +66,10 @@ constexpr int kMaxDevices = 64;
 int g_num_sms[kMaxDevices] = {0};
 std::mutex g_mu;
 
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+}  // namespace
+
 int num_sms_current() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
@@ -78,8 +82,6 @@ int num_sms_current() {
     return g_num_sms[dev];
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 pkv_status check_cache(const pkv_cache* c) {
     if (!c || !c->k_cache || !c->v_cache) return PKV_ERR_INVALID_ARG;
     if (c->num_blocks <= 0 || c->num_kv_heads <= 0) return PKV_ERR_INVALID_ARG;
@@ -90,6 +92,8 @@ pkv_status check_cache(const pkv_cache* c) {
     if (!aligned16(c->k_cache) || !aligned16(c->v_cache)) return PKV_ERR_INVALID_ARG;
     return PKV_OK;
 }
+
+namespace {
 
 // Workspace sizing without a kernel choice covers either kernel: the larger
 // default grid and 32 slot rows.

@@ -1,0 +1,193 @@
+// Paged cache -> rows: the inverse of the appends.  Contract:
+// include/pagedkv.h, pkv_paged_kv_read.
+//
+// Pure data movement (FP8: one multiply a value), so the bound is HBM: each
+// cache byte read once, each row byte written once.  A CTA takes one page
+// position of one sequence, all its kv-heads (adjacent in the cache: one
+// contiguous piece of a block's K and of its V).  Inside a page a 16-byte
+// chunk holds consecutive elements of one token, and the 8 chunks of 8 tokens
+// are adjacent; a warp takes 4 tokens x 8 chunks of the head dimension, so
+// its loads cover whole 64-byte pieces and its stores whole 128-byte (or
+// longer) pieces of rows.
+#include <type_traits>
+
+#include "rows.cuh"
+
+namespace pkv {
+namespace cache_read {
+
+using rows::View;
+
+constexpr int kThreads = 256;
+
+struct Arg {
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scales, *v_scales;
+    View k, v;                         // data nullptr: not wanted
+    const int32_t *tables, *lens, *starts;
+    int* err;
+    int64_t num_blocks, num_rows;
+    int num_seqs, max_blocks, Hkv;
+};
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(uint8_t* dst, const float* x, int n) {
+    // n elements of T, 16 bytes at a time
+#pragma unroll
+    for (int e = 0; e < 16; e += rows::Chunk<T>::N)
+        if (e < n) *reinterpret_cast<uint4*>(dst + e * sizeof(T)) = rows::Chunk<T>::pack(x + e);
+}
+
+// E: bytes of a cache element (2: bf16, 1: e4m3)
+template <typename T, int E, int D>
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Arg a) {
+    constexpr int C = 16 / E, NCH = D / C;                 // elements a chunk, chunks a row
+    constexpr int PAGE = kBlock * D * E;
+    __shared__ int s_seq, s_page;
+    __shared__ int64_t s_row;
+    griddep_wait();                                        // (no early trigger: an append reads its rows before its own wait)
+    // this CTA's unit: the page position `blockIdx.x` of the sequences' pages laid end to end
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int64_t unit = blockIdx.x, row = 0;
+        int seq = -1, page = 0;
+        for (int b0 = 0; b0 < a.num_seqs; b0 += 32) {
+            const int b = b0 + lane;
+            int n = b < a.num_seqs ? a.lens[b] : 0;
+            const int st = b < a.num_seqs && a.starts ? a.starts[b] : 0;
+            if (n < 0 || st < 0 || (n > 0 && ((int64_t)st + n + kBlock - 1) / kBlock > a.max_blocks)) {
+                raise_error(a.err, PKV_DEVERR_LENGTH);     // (the grid has a spare CTA per such sequence: one sees it)
+                n = max(n, 0);                             // (its rows stay reserved, its pages are not read)
+            }
+            const bool bad = n > 0 && (st < 0 || ((int64_t)st + n + kBlock - 1) / kBlock > a.max_blocks);
+            int64_t pages = n > 0 && !bad ? (st + n - 1) / kBlock - st / kBlock + 1 : 0;
+            int64_t pu = pages, pr = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, pu, o), y = __shfl_up_sync(0xffffffffu, pr, o);
+                if (lane >= o) {
+                    pu += x;
+                    pr += y;
+                }
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, pu > unit);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                seq = b0 + l;
+                page = (int)(unit - __shfl_sync(0xffffffffu, pu - pages, l));
+                row += __shfl_sync(0xffffffffu, pr - n, l);
+                break;
+            }
+            unit -= __shfl_sync(0xffffffffu, pu, 31);
+            row += __shfl_sync(0xffffffffu, pr, 31);
+        }
+        if (lane == 0) {
+            s_seq = seq;
+            s_page = page;
+            s_row = row;
+        }
+    }
+    __syncthreads();
+    const int b = s_seq;
+    if (b < 0) return;
+    const int n = a.lens[b], st = a.starts ? a.starts[b] : 0;
+    const int pg = st / kBlock + s_page;                   // page of the sequence
+    const int32_t blk = a.tables[(size_t)b * a.max_blocks + pg];
+    if (blk < 0 || blk >= a.num_blocks) {
+        if (threadIdx.x == 0) raise_error(a.err, PKV_DEVERR_BLOCK_ID);
+        return;
+    }
+    // tokens [lo, hi) of the page are wanted; token off's row is row0 + off
+    const int lo = max(st - pg * kBlock, 0), hi = min(st + n - pg * kBlock, kBlock);
+    const int64_t row0 = s_row + (int64_t)pg * kBlock - st;
+    if (row0 + hi > a.num_rows && threadIdx.x == 0) raise_error(a.err, PKV_DEVERR_LENGTH);
+    const int per_head = kBlock * NCH, total = a.Hkv * per_head;   // chunks
+    auto which = [&](const uint8_t* cache, const float* scales, const View& out) {
+        if (!out.data) return;
+        const uint8_t* src = cache + (size_t)blk * a.Hkv * PAGE;
+        constexpr int U = 4;
+        for (int x0 = threadIdx.x; x0 < total; x0 += U * kThreads) {
+            uint4 raw[U];
+            int off[U], ch[U], g[U];
+            bool ok[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // 8 chunks of the head dimension x 4 tokens per warp (NCH = 4: 4 chunks x 8 tokens)
+                const int x = x0 + u * kThreads;
+                constexpr int CW = NCH < 8 ? NCH : 8, TW = 32 / CW;
+                g[u] = x / per_head;
+                const int y = x % per_head, l = y % 32, wv = y / 32;
+                ch[u] = (wv % (NCH / CW)) * CW + l % CW;
+                off[u] = (wv / (NCH / CW)) * TW + l / CW;
+                ok[u] = x < total && off[u] >= lo && off[u] < hi && row0 + off[u] < a.num_rows;
+                if (ok[u])
+                    raw[u] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)g[u] * PAGE +
+                                                                  ((off[u] >> 3) * NCH + ch[u]) * 128 + (off[u] & 7) * 16));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!ok[u]) continue;
+                uint8_t* dst = out.row(row0 + off[u], g[u]) + ch[u] * C * sizeof(T);
+                float v[16];
+                if constexpr (E == 2) {
+                    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                        *reinterpret_cast<uint4*>(dst) = raw[u];
+                    } else {
+                        rows::Chunk<__nv_bfloat16>::unpack(raw[u], v);
+                        store_chunk<T>(dst, v, 8);
+                    }
+                } else {
+                    const float sc = scales[(size_t)blk * a.Hkv + g[u]];
+                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 p = e4m3x2_to_float2(w[j]), q = e4m3x2_to_float2(w[j] >> 16);
+                        v[4 * j] = p.x * sc;
+                        v[4 * j + 1] = p.y * sc;
+                        v[4 * j + 2] = q.x * sc;
+                        v[4 * j + 3] = q.y * sc;
+                    }
+                    store_chunk<T>(dst, v, 16);
+                }
+            }
+        }
+    };
+    which(a.k_cache, a.k_scales, a.k);
+    which(a.v_cache, a.v_scales, a.v);
+}
+
+}  // namespace cache_read
+
+cudaError_t launch_cache_read(const pkv_cache& c, const int32_t* tables, int max_blocks, const int32_t* starts,
+                              const int32_t* lens, int num_seqs, int64_t num_rows, const pkv_rows* k,
+                              const pkv_rows* v, int dtype, int* err, cudaStream_t st) {
+    using namespace cache_read;
+    const int e = dtype == PKV_FP32 ? 4 : 2;
+    auto view = [&](const pkv_rows* r) {
+        View x = {};
+        if (r) {
+            x.data = (uint8_t*)r->data;
+            x.ts = r->token_stride * e;
+            x.hs = r->head_stride * e;
+            x.heads = r->num_heads;
+        }
+        return x;
+    };
+    Arg a = {(const uint8_t*)c.k_cache, (const uint8_t*)c.v_cache, c.k_scales, c.v_scales, view(k), view(v), tables,
+             lens, starts, err, c.num_blocks, num_rows, num_seqs, max_blocks, c.num_kv_heads};
+    // every sequence's rows touch at most ceil(len / 16) pages, one more where it starts inside a page
+    const int64_t units = num_rows / kBlock + (int64_t)num_seqs * (starts ? 2 : 1);
+    if (units > 0x7fffffff) return cudaErrorInvalidValue;
+    auto go = [&](auto kern) { return launch_pdl(kern, dim3((unsigned)units), dim3(kThreads), (size_t)0, st, a); };
+    auto of = [&](auto zero) {
+        using T = decltype(zero);
+        if (c.kv_dtype == PKV_KV_FP8_E4M3)
+            return c.head_dim == 128 ? go(read_kernel<T, 1, 128>) : go(read_kernel<T, 1, 64>);
+        return c.head_dim == 128 ? go(read_kernel<T, 2, 128>) : go(read_kernel<T, 2, 64>);
+    };
+    if (dtype == PKV_BF16) return of(__nv_bfloat16());
+    if (dtype == PKV_FP16) return of(__half());
+    return of(float());
+}
+
+}  // namespace pkv
