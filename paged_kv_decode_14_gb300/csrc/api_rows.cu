@@ -21,7 +21,8 @@ cudaError_t launch_cache_read(const pkv_cache& c, const int32_t* tables, int max
 cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* v, const pkv_rows* out, float* lse,
                           int dtype, int head_dim, int64_t num_q_rows, int64_t num_kv_rows, const int32_t* q_lens,
                           const int32_t* kv_lens, const int64_t* q_starts, const int64_t* kv_starts, int num_seqs,
-                          int max_q_len, float scale, int* err, cudaStream_t st);
+                          int max_q_len, float scale, void* workspace, int* err, cudaStream_t st);
+size_t prompt_workspace_bytes();
 
 namespace {
 
@@ -178,7 +179,7 @@ PKV_API pkv_status pkv_paged_kv_read(const pkv_cache* cache, const int32_t* bloc
                : PKV_ERR_CUDA;
 }
 
-PKV_API size_t pkv_prompt_workspace_size(void) { return 256; }
+PKV_API size_t pkv_prompt_workspace_size(void) { return prompt_workspace_bytes(); }
 
 PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, const pkv_rows* v, const pkv_rows* out,
                                         float* lse, int32_t dtype, int32_t head_dim, int64_t num_q_rows,
@@ -210,7 +211,7 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, co
     if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
     if (workspace && workspace_bytes < pkv_prompt_workspace_size()) return PKV_ERR_WORKSPACE;
     return launch_prompt(q, k, v, out, lse, dtype, head_dim, num_q_rows, num_kv_rows, q_lens, kv_lens, q_starts,
-                         kv_starts, num_seqs, max_q_len, scale, device_error, (cudaStream_t)stream) == cudaSuccess
+                         kv_starts, num_seqs, max_q_len, scale, workspace, device_error, (cudaStream_t)stream) == cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;
 }

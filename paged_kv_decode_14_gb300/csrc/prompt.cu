@@ -1,97 +1,1021 @@
 // Causal attention of packed prompts whose keys and values are rows, not
-// pages.  Contract: include/pagedkv.h, pkv_prompt_attention.
+// pages, on the 5th-generation tensor cores.  Contract: include/pagedkv.h,
+// pkv_prompt_attention.
 //
-// One warp per (query row, head): lanes hold D / 32 dimensions, keys one by
-// one with the running maximum and sum of the softmax in fp32.
+// A work item is up to 256 query rows of one (sequence, kv-head): 2 x PB
+// consecutive query positions, PB = floor(128 / G), times the G heads of the
+// group, as two 128-row tiles (row r of a tile = position r / G, head r % G),
+// so every key tile a CTA loads serves both.  Per key tile t (128 keys) and
+// row tile i, with the reference maximum m of each row:
+//   S_i[128 rows, 128 keys] = Q_i . K_t^T      (A and B K-major in shared memory)
+//   P_i = 2^(S_i scale log2(e) - m), l += sum P_i    (one thread per row = TMEM lane)
+//   O_i[128 rows, D] += P_i . V_t              (A = P from TMEM, B MN-major in shared memory)
+// and out = O / l at the end.  m is raised (O and l rescaled) only when a
+// row's maximum exceeds it by more than 2^8, so most tiles leave O alone; P
+// is rounded to the inputs' type because both operands of one MMA have the
+// same type (bf16 keeps the fp32 range; fp16 P stays below 2^9).
+//
+// Q, K and V tiles arrive by tensor copies (TMA) in the 128-byte swizzle,
+// straight from strided rows: K-major operands for Q and K, an MN-major one
+// for V, without a pass over the data.
+//
+// Roles (384 threads): warps 0-3 the softmax of row tile 0, warps 4-7 of row
+// tile 1 (they also write the results), warp 8 the producer, warps 9 and 10
+// the MMA issuers of row tiles 0 and 1, warp 11 the V guard.  Per tile issuer
+// i runs  PV_i(t) first 64 keys | PV_i(t) rest | S_i(t + 1)  while the other
+// row tile is in its softmax.  One thread's tcgen05 operations complete in
+// order, so when S_i(t + 1) signals, PV_i(t) is done and O_i may be rescaled,
+// and S_i(t + 1) overwrites P_i(t) only after PV_i(t) has read it.
+//
+// The V guard makes keys that some rows do not see harmless: a weight of 0
+// times NaN or infinity is NaN, so rows of V past the sequence's end are
+// cleared in shared memory, and non-finite values among the keys that only
+// part of the item's rows see are replaced by 0 there and added back, row by
+// row, when the result is written (from global memory: rare).
+//
+// Few rows over many keys (fewer items than the SMs can share): the key tiles
+// of all items are laid end to end and cut into equal ranges, one per CTA; a
+// cut item leaves partial (O, m, l) in the workspace, joined in order by a
+// second kernel.  Every wait is bounded.
+#include <cuda.h>
+
+#include <algorithm>
+#include <type_traits>
+
 #include "rows.cuh"
+#include "tc_ptx.cuh"
 
 namespace pkv {
+int num_sms_current();
+
 namespace prompt {
 
+using namespace ptx;
 using rows::View;
 
+constexpr int kRows = 128;                 // rows of a row tile (MMA M)
+constexpr int kKeys = 128;                 // keys of a key tile
+constexpr int kThreads = 384;
+constexpr int kProducer = 8, kMma = 9;   // (the guard: warp 11)
+constexpr float kSlack = 8.f;              // raise m (and rescale O) past 2^8 only
+constexpr int kTable = 128;                // entries of the sequence table
+constexpr int kFlags = 8;                  // items whose "non-finite V" flags are kept
+
 struct Arg {
-    View q, k, v, out;
+    CUtensorMap q, k, v;
+    View vrows, out;                       // V rows again, for the guard's slow path
     float* lse;
     const int32_t *q_lens, *kv_lens;
     const int64_t *q_starts, *kv_starts;
     int* err;
+    float* partials;                       // split launches: [CTA][2] slots
+    uint64_t wait_limit_ns;
+    const int* hold;
     int64_t num_q_rows, num_kv_rows;
-    int num_seqs, max_q_len, group;
-    float scale;
+    int num_seqs, max_q_len, Hq, Hkv, group;
+    int pb;                                // query positions of a row tile
+    int split;                             // key tiles cut into equal ranges
+    float scale_log2;
 };
 
+// A partial slot: O as [D / 4][256 rows][4] fp32, then m and l, [256] each.
+__host__ __device__ constexpr int slot_floats(int D) { return 2 * kRows * (D + 2); }
+
+template <int D>
+struct Cfg {
+    static constexpr int SLABS = D / 64;                  // 128-byte wide slabs of a row
+    static constexpr int SLAB = kRows * 128;              // bytes of one slab of a tile
+    static constexpr int TILE = SLABS * SLAB;
+    static constexpr int NSK = D == 128 ? 2 : 4;          // K ring depth
+    static constexpr int NSV = D == 128 ? 3 : 4;          // V ring depth
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + 2 * TILE;
+    static constexpr int OFF_V = OFF_K + NSK * TILE;
+    static constexpr int OFF_BAR = OFF_V + NSV * TILE;
+    // barriers: KFULL[NSK] KEMPTY[NSK] VFULL[NSV] VREADY[NSV] VEMPTY[NSV], then pairs by row tile
+    static constexpr int KFULL = 0, KEMPTY = NSK, VFULL = 2 * NSK, VREADY = VFULL + NSV, VEMPTY = VREADY + NSV,
+                         SFULL = VEMPTY + NSV, PFA = SFULL + 2, PFB = SFULL + 4, QFULL = SFULL + 6,
+                         QEMPTY = SFULL + 8, ODONE = SFULL + 10, OFREE = SFULL + 12, DRAIN = SFULL + 14;
+    static constexpr int NBAR = SFULL + 15;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
+    static constexpr int OFF_FLAG = OFF_MISC + 16;        // int[kFlags]
+    static constexpr int OFF_TABLE = OFF_FLAG + 4 * kFlags;   // int[3][kTable + 1]: units, q rows, kv rows before
+    static constexpr int SMEM = OFF_TABLE + 12 * (kTable + 1) + 1024;   // (+ alignment)
+    static constexpr int COL_O = 2 * kKeys;
+    static constexpr int TMEM_COLS = 512;
+    static_assert(COL_O + 2 * D <= TMEM_COLS, "tensor memory budget");
+    static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// ------------------------------------------------------------------ work
+
+struct Seq {
+    int64_t q0, k0;         // first rows
+    int Q, L;               // 0 queries where the lengths are bad
+};
+
+// Sequence b, given the packed rows before it.
+__device__ __forceinline__ Seq seq_at(const Arg& a, int b, int64_t qb, int64_t kb, bool* bad = nullptr) {
+    Seq s;
+    s.Q = a.q_lens[b];
+    s.L = a.kv_lens[b];
+    s.q0 = a.q_starts ? a.q_starts[b] : qb;
+    s.k0 = a.kv_starts ? a.kv_starts[b] : kb;
+    const bool wrong = s.Q < 0 || s.Q > a.max_q_len || s.L < 0 || s.q0 < 0 || s.k0 < 0 ||
+                       s.q0 > a.num_q_rows - s.Q || s.k0 > a.num_kv_rows - s.L;
+    if (wrong) s.Q = 0;
+    if (bad) *bad = wrong;
+    return s;
+}
+
+__device__ __forceinline__ int items_of(const Arg& a, const Seq& s) { return (s.Q + 2 * a.pb - 1) / (2 * a.pb); }
+// key tiles of query block qb: up to its last row's limit
+__device__ __forceinline__ int tiles_of(const Arg& a, const Seq& s, int qb) {
+    const int keys = s.L - s.Q + min((qb + 1) * 2 * a.pb, s.Q);
+    return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+}
+// A sequence's share of the work, per kv-head: items, or (split) key tiles, at least one an item.
+__device__ __forceinline__ int units_of(const Arg& a, const Seq& s) {
+    const int n = items_of(a, s);
+    if (!a.split) return n;
+    int u = 0;
+    for (int i = 0; i < n; ++i) u += max(tiles_of(a, s, i), 1);
+    return u;
+}
+
+// The sequences' shares summed up in chunks of consecutive sequences, one chunk per table entry:
+// tab[0] units, tab[1] query rows, tab[2] key rows before the chunk.
+struct Table {
+    const int* tab;
+    int chunk;              // sequences a chunk
+};
+__device__ __forceinline__ void build_table(const Arg& a, int* tab, int chunk, int tid, bool report) {
+    // (threads 0 .. kTable - 1; the sums over chunks follow in warp 0)
+    int u = 0;
+    int64_t q = 0, k = 0;
+    for (int b = tid * chunk; b < min((tid + 1) * chunk, a.num_seqs); ++b) {
+        // (bounds of packed rows are checked where a sequence is located, with the rows before it)
+        const int Q = a.q_lens[b], L = a.kv_lens[b];
+        if (report) {
+            if (Q < 0 || Q > a.max_q_len || L < 0) raise_error(a.err, PKV_DEVERR_LENGTH);
+        }
+        q += max(Q, 0);
+        k += max(L, 0);
+        Seq s{0, 0, Q, L};
+        if (Q < 0 || Q > a.max_q_len || L < 0) s.Q = 0;
+        u += units_of(a, s) * a.Hkv;
+    }
+    tab[tid + 1] = u;
+    tab[kTable + 1 + tid + 1] = (int)min(q, (int64_t)0x7fffffff);
+    tab[2 * (kTable + 1) + tid + 1] = (int)min(k, (int64_t)0x7fffffff);
+}
+__device__ __forceinline__ void sum_table(int* tab, int lane) {
+    for (int j = 0; j < 3; ++j) {
+        int* t = tab + j * (kTable + 1);
+        int64_t base = 0;
+        if (lane == 0) t[0] = 0;
+        for (int c = 0; c < kTable; c += 32) {
+            int64_t x = t[c + lane + 1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            x += base;
+            t[c + lane + 1] = (int)min(x, (int64_t)0x7fffffff);   // (rows past 2^31 - 1 fail the bounds check)
+            base = __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+    __syncwarp();
+}
+
+// A piece of work: key tiles [t0, t1) of query block qb of sequence s, kv-head g.
+struct Piece {
+    Seq s;
+    int g, q0, nq, T, t0, t1;
+    bool two;               // row tile 1 holds rows
+    bool whole;             // all of the item's tiles: the result is written at once
+};
+
+// The piece at unit u of [u, end) (not split: one unit an item).  False: the unit belongs to a
+// sequence whose rows lie outside the tensors; *step units are to be passed over.
+__device__ __forceinline__ bool locate(const Arg& a, const Table& tb, int u, int end, Piece& p, int* step) {
+    int lo = 0, hi = kTable - 1;                          // the last chunk with units before it <= u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tb.tab[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    u -= tb.tab[lo];
+    int64_t qb = tb.tab[kTable + 1 + lo], kb = tb.tab[2 * (kTable + 1) + lo];
+    int b = lo * tb.chunk;
+    for (;; ++b) {
+        const int Q = a.q_lens[b], L = a.kv_lens[b];
+        Seq s{0, 0, Q, L};
+        if (Q < 0 || Q > a.max_q_len || L < 0) s.Q = 0;
+        const int n = units_of(a, s) * a.Hkv;
+        if (u < n) {
+            *step = n - u;
+            break;
+        }
+        u -= n;
+        qb += max(Q, 0);
+        kb += max(L, 0);
+    }
+    bool bad;
+    p.s = seq_at(a, b, qb, kb, &bad);
+    if (bad) {
+        raise_error(a.err, PKV_DEVERR_LENGTH);
+        return false;
+    }
+    int blk;
+    if (!a.split) {
+        // the last query blocks first: they see the most keys
+        blk = items_of(a, p.s) - 1 - u / a.Hkv;
+        p.g = u % a.Hkv;
+        p.t0 = 0;
+        p.T = p.t1 = tiles_of(a, p.s, blk);
+        *step = 1;
+    } else {
+        blk = 0;
+        for (;; ++blk) {
+            p.T = tiles_of(a, p.s, blk);
+            const int n = max(p.T, 1) * a.Hkv;
+            if (u < n) break;
+            u -= n;
+        }
+        const int w = max(p.T, 1);
+        p.g = u / w;
+        p.t0 = u % w;
+        *step = min(w - p.t0, end);                       // (end: the units left in the CTA's range)
+        p.t1 = min(p.t0 + *step, p.T);
+    }
+    p.whole = p.t0 == 0 && p.t1 == p.T;
+    p.q0 = blk * 2 * a.pb;
+    p.nq = min(2 * a.pb, p.s.Q - p.q0);
+    p.two = p.nq > a.pb;
+    return true;
+}
+
+// A CTA's units: every gridDim-th item in serpentine rounds, or (split) one range of key tiles.
+// Split launches use as many CTAs as keep at least kMinTiles tiles each.
+constexpr int kMinTiles = 2;
+__device__ __forceinline__ int split_ctas(int total, int grid) { return min(grid, max(total / kMinTiles, 1)); }
+__device__ __forceinline__ int split_start(int total, int ctas, int c) { return (int)((int64_t)total * c / ctas); }
+
+struct Walk {
+    int u, end, round, total;
+    __device__ __forceinline__ void start(const Arg& a, const Table& tb) {
+        total = tb.tab[kTable];
+        round = -1;
+        u = end = 0;
+        if (a.split) {
+            const int n = split_ctas(total, gridDim.x), c = blockIdx.x;
+            if (c < n && total > 0) {
+                u = split_start(total, n, c);
+                end = split_start(total, n, c + 1);
+            }
+        }
+    }
+    __device__ __forceinline__ bool next(const Arg& a, const Table& tb, Piece& p) {
+        int step;
+        if (a.split) {
+            while (u < end) {
+                const bool ok = locate(a, tb, u, end - u, p, &step);
+                u += step;
+                if (ok) return true;
+            }
+            return false;
+        }
+        const int grid = gridDim.x, c = blockIdx.x;
+        for (++round; (int64_t)round * grid < total; ++round) {
+            const int64_t j = (int64_t)round * grid + ((round & 1) ? grid - 1 - c : c);
+            if (j < total && locate(a, tb, (int)j, 0, p, &step)) return true;
+        }
+        return false;
+    }
+};
+
+// ------------------------------------------------------------------ PTX pieces of this kernel
+
+struct Ctl {
+    volatile int* abort;
+    int* err;
+    uint64_t limit;
+};
+__device__ __noinline__ bool wait_spin(uint32_t bar, uint32_t parity, volatile int* abort, int* err, uint64_t limit) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 63) == 0) {
+            if (*abort) return false;
+            if (globaltimer_ns() - t0 > limit) {
+                raise_error(err, PKV_DEVERR_TIMEOUT);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return wait_spin(bar, parity, c.abort, c.err, c.limit);
+}
+
+// A box of a 3-D tensor (dim, head, token) -> shared memory.
+__device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap* map, int d, int h, int t, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+            dst),
+        "l"(map), "r"(d), "r"(h), "r"(t), "r"(bar)
+        : "memory");
+}
+
+// Shared-memory matrix descriptor of a 128-byte-swizzled operand.  K-major: sbo = bytes between
+// groups of 8 rows (lbo unused).  MN-major: lbo = bytes between 64-element slabs, sbo between groups of 8 k.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+           (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2pack(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void f2unpack(uint64_t r, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2add(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// Orders later uses of r behind the last tcgen05.wait::ld (no instruction).
+__device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                          "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
 template <typename T>
-__device__ __forceinline__ float get(const uint8_t* p, int d);
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <>
-__device__ __forceinline__ float get<__nv_bfloat16>(const uint8_t* p, int d) {
-    return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[d]);
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <>
-__device__ __forceinline__ float get<__half>(const uint8_t* p, int d) {
-    return __half2float(reinterpret_cast<const __half*>(p)[d]);
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+struct Type;
+template <>
+struct Type<__nv_bfloat16> {
+    static constexpr uint32_t INF = 0x7f80u;              // exponent bits of infinities and NaN
+    static constexpr uint32_t id(int M, int N, bool b_mn) { return idesc_bf16_f32(M, N, false, b_mn); }
+    static __device__ __forceinline__ float get(const uint8_t* p) { return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p)); }
+};
+template <>
+struct Type<__half> {
+    static constexpr uint32_t INF = 0x7c00u;
+    static constexpr uint32_t id(int M, int N, bool b_mn) { return idesc_f16_f32(M, N, false, b_mn); }
+    static __device__ __forceinline__ float get(const uint8_t* p) { return __half2float(*reinterpret_cast<const __half*>(p)); }
+};
+
+// ------------------------------------------------------------------ kernel
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Arg a, int chunk) {
+    using K = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int i) -> uint32_t { return sb + K::OFF_BAR + 8 * i; };
+    constexpr int NSK = K::NSK, NSV = K::NSV;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 4);
+    volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 8);   // (drain waits at the end)
+    volatile int* nonfinite = reinterpret_cast<volatile int*>(smem + K::OFF_FLAG);
+    int* tab = reinterpret_cast<int*>(smem + K::OFF_TABLE);
+    const Table table{tab, chunk};
+    const Ctl ctl{abort_flag, a.err, a.wait_limit_ns};
+
+    if (tid == 0) {
+        for (int i = 0; i < NSK; ++i) {
+            mbar_init(bar(K::KFULL + i), 1);
+            mbar_init(bar(K::KEMPTY + i), 2);             // both issuers release every tile
+        }
+        for (int i = 0; i < NSV; ++i) {
+            mbar_init(bar(K::VFULL + i), 1);
+            mbar_init(bar(K::VREADY + i), 1);
+            mbar_init(bar(K::VEMPTY + i), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(K::SFULL + i), 1);
+            mbar_init(bar(K::PFA + i), 4);                // one arrival a softmax warp
+            mbar_init(bar(K::PFB + i), 4);
+            mbar_init(bar(K::QFULL + i), 1);
+            mbar_init(bar(K::QEMPTY + i), 1);
+            mbar_init(bar(K::ODONE + i), 1);
+            mbar_init(bar(K::OFREE + i), 4);
+        }
+        mbar_init(bar(K::DRAIN), 2);
+        *abort_flag = 0;
+        *drain_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == 11) {
+        tmem_alloc(smem_u32(tmem_slot), K::TMEM_COLS);
+        tmem_relinquish();
+    }
+    griddep_wait();
+    if (tid < kTable) build_table(a, tab, chunk, tid, blockIdx.x == 0);
+    cta_bar_sync();
+    if (warp == 0) sum_table(tab, lane);
+    tc_fence_before();
+    cta_bar_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < 8) {
+        // ------------------------------------------------ softmax of row tile i, thread r = row r
+        const int i = warp >> 2, r = tid & (kRows - 1);
+        const int G = a.group, pos = r / G, hl = r - pos * G;
+        const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t scol = tmem + lbase + i * kKeys;   // S_i / P_i
+        const uint32_t ocol = tmem + lbase + K::COL_O + i * D;
+        const float sc = a.scale_log2;
+        // every wait and every TMEM access is warp-uniform (tcgen05.ld / st are .aligned)
+        auto wait_all = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, wait(bb, parity, ctl)); };
+        auto signal = [&](uint32_t bb) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bb);
+        };
+        Walk w;
+        w.start(a, table);
+        Piece p;
+        bool more = w.next(a, table, p), ok = true;
+        int scnt = 0, ocnt = 0, item = 0;                 // this row tile's S tiles and items; the CTA's items with tiles
+        while (more && ok) {
+            const bool act = i == 0 || p.two;
+            const int qi = p.q0 + i * a.pb + pos;         // query position
+            const bool row_ok = pos < a.pb && qi < p.q0 + p.nq;
+            // keys 0 .. lim are visible (rows of no query: everything, so that they ask for no mask)
+            const int lim = row_ok ? p.s.L - p.s.Q + qi : 0x3fffffff;
+            float m = -INFINITY, l = 0.f;
+            for (int t = p.t0; act && t < p.t1; ++t, ++scnt) {
+                if (!(ok = wait_all(bar(K::SFULL + i), scnt & 1))) break;
+                tc_fence_after();
+                const int rem = lim - t * kKeys;          // column c is visible iff c <= rem
+                const bool masked = !__all_sync(0xffffffffu, rem >= kKeys - 1);
+                uint64_t acc[2] = {0, 0};
+                auto tile = [&](auto mask) {
+                    // the last 64 columns first, for the maximum only: they are loaded again, behind the first
+                    // 64 columns' exponentials (TMEM reads cost little, 128 live registers more)
+                    uint32_t sa[32], sb_[32], sc_[32];
+                    tmem_ld32_async(scol + 64, sa);
+                    tmem_ld32_async(scol + 96, sb_);
+                    tmem_wait_ld_into(sa);
+                    tie32(sb_);
+                    tmem_ld32_async(scol, sc_);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto maxima = [&](const uint32_t (&s)[32], int c, auto mask) {
+                        if constexpr (!decltype(mask)::value) {
+    #pragma unroll
+                            for (int x = 0; x < 32; x += 2)
+                                mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                        } else {
+    #pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                mx[x & 3] = fmaxf(mx[x & 3], c + x <= rem ? __uint_as_float(s[x]) : -INFINITY);
+                        }
+                    };
+                    maxima(sa, 64, mask);
+                    maxima(sb_, 96, mask);
+                    tmem_wait_ld_into(sc_);
+                    tmem_ld32_async(scol + 32, sa);
+                    maxima(sc_, 0, mask);
+                    tmem_wait_ld_into(sa);
+                    maxima(sa, 32, mask);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+                    const bool up = top > m + kSlack;         // (m = -inf: any finite maximum)
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float alpha = up && m > -INFINITY ? exp2_fast(m - top) : 1.f;
+                        if (t > p.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+    #pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                float o[16];
+                                tmem_ld16(ocol + c, o);
+                                uint32_t v[16];
+    #pragma unroll
+                                for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(o[x] * alpha);
+                                tmem_st16u(ocol + c, v);
+                            }
+                        }
+                        l *= alpha;
+                        if (up) m = top;
+                    }
+                    // rows with nothing visible so far keep m = -inf, and P = 2^-inf = 0 by the mask
+                    const float mref = m == -INFINITY ? 0.f : m;
+                    const uint64_t sc2 = f2pack(__float_as_uint(sc), __float_as_uint(sc));
+                    const uint64_t nm2 = f2pack(__float_as_uint(-mref), __float_as_uint(-mref));
+                                        // P of 32 keys, two per packed fp32 operation, into 16 columns (the even key in the low half)
+                    auto emit = [&](const uint32_t (&s)[32], int c, auto mask) {
+                        uint32_t v[16];
+    #pragma unroll
+                        for (int x = 0; x < 32; x += 2) {
+                            float x0, x1;
+                            f2unpack(f2fma(f2pack(s[x], s[x + 1]), sc2, nm2), x0, x1);
+                            float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
+                            if constexpr (decltype(mask)::value) {
+                                p0 = c + x <= rem ? p0 : 0.f;
+                                p1 = c + x + 1 <= rem ? p1 : 0.f;
+                            }
+                            acc[(x >> 1) & 1] = f2add(acc[(x >> 1) & 1], f2pack(__float_as_uint(p0), __float_as_uint(p1)));
+                            v[x >> 1] = pack2<T>(p0, p1);
+                        }
+                        tmem_st16u(scol + (c >> 1), v);
+                    };
+                    tmem_ld32_async(scol + 64, sb_);
+                    emit(sc_, 0, mask);
+                    emit(sa, 32, mask);
+                    tmem_wait_st();
+                    signal(bar(K::PFA + i));                  // PV of the first 64 keys may run meanwhile
+                    tmem_wait_ld_into(sb_);
+                    tmem_ld32_async(scol + 96, sa);
+                    emit(sb_, 64, mask);
+                    tmem_wait_ld_into(sa);
+                    emit(sa, 96, mask);
+                    tmem_wait_st();
+                    signal(bar(K::PFB + i));
+                };
+                if (masked) tile(std::true_type{});
+                else tile(std::false_type{});
+                float a0, a1;
+                f2unpack(f2add(acc[0], acc[1]), a0, a1);
+                l += a0 + a1;
+            }
+            if (!ok) break;
+            // the result of this piece; the next one is looked up while the last MMAs run
+            const Piece cur = p;
+            const bool tiles = cur.t1 > cur.t0;
+            const int it = item;
+            item += tiles;
+            more = w.next(a, table, p);
+            if (!act) continue;
+            if (tiles) {
+                if (!(ok = wait_all(bar(K::ODONE + i), ocnt & 1))) break;
+                ++ocnt;
+                tc_fence_after();
+            }
+            const int64_t row = cur.s.q0 + qi;
+            if (cur.whole) {
+                const bool sees = lim >= 0;
+                const float inv = sees ? 1.f / l : 0.f;
+                const bool fix = tiles && nonfinite[it & (kFlags - 1)] != 0;
+                uint8_t* dst = a.out.row(row, cur.g * G + hl);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (tiles) tmem_ld32(ocol + c, o);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] = tiles && sees ? o[x] * inv : 0.f;
+                    if (fix && row_ok) {
+                        for (int j = max(cur.s.L - cur.s.Q + cur.q0 + 1, 0); j <= lim; ++j) {
+                            const uint8_t* v = a.vrows.row(cur.s.k0 + j, cur.g) + c * 2;
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) {
+                                const float f = Type<T>::get(v + 2 * x);
+                                if (!(fabsf(f) < INFINITY)) o[x] += f;
+                            }
+                        }
+                    }
+                    if (row_ok) {
+#pragma unroll
+                        for (int h = 0; h < 32; h += 8)
+                            *reinterpret_cast<uint4*>(dst + (c + h) * 2) =
+                                make_uint4(pack2<T>(o[h], o[h + 1]), pack2<T>(o[h + 2], o[h + 3]),
+                                           pack2<T>(o[h + 4], o[h + 5]), pack2<T>(o[h + 6], o[h + 7]));
+                    }
+                }
+                if (row_ok && a.lse)
+                    a.lse[row * a.Hq + cur.g * G + hl] = sees ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+            } else {
+                // (split) a part of the item: unnormalised O, m and l.  The part that starts the item is the
+                // CTA's last piece (slot 1), any other its first (slot 0).
+                float* slot = a.partials + ((size_t)blockIdx.x * 2 + (cur.t0 == 0 ? 1 : 0)) * slot_floats(D);
+                const bool fix = nonfinite[it & (kFlags - 1)] != 0;
+                const int R = i * kRows + r;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(ocol + c, o);
+                    if (fix && row_ok) {
+                        const int first = max(cur.s.L - cur.s.Q + cur.q0 + 1, cur.t0 * kKeys);
+                        for (int j = first; j <= min(lim, cur.t1 * kKeys - 1); ++j) {
+                            const uint8_t* v = a.vrows.row(cur.s.k0 + j, cur.g) + c * 2;
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) {
+                                const float f = Type<T>::get(v + 2 * x);
+                                if (!(fabsf(f) < INFINITY)) o[x] += f;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4)
+                        *reinterpret_cast<float4*>(slot + ((size_t)((c + x) / 4) * 2 * kRows + R) * 4) =
+                            make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                }
+                slot[(size_t)2 * kRows * D + R] = m;
+                slot[(size_t)2 * kRows * (D + 1) + R] = l;
+            }
+            if (tiles) signal(bar(K::OFREE + i));         // the next item's first PV may overwrite O_i
+        }
+    } else {
+        Walk w;
+        w.start(a, table);
+        Piece p;
+        if (warp == kProducer) {
+            // -------------------------------------------- tensor copies: Q tiles, K and V tiles in order
+            bool ok = true;
+            if (lane == 0) {
+                if (a.hold != nullptr) {
+                    // (tests of the timeout path only) wait, bounded, for a flag that nothing sets
+                    const uint64_t h0 = globaltimer_ns();
+                    while (ok && *reinterpret_cast<const volatile int*>(a.hold) == 0) {
+                        if (*abort_flag || globaltimer_ns() - h0 > a.wait_limit_ns) {
+                            if (!*abort_flag) raise_error(a.err, PKV_DEVERR_TIMEOUT);
+                            *abort_flag = 1;
+                            ok = false;
+                        }
+                        __nanosleep(256);
+                    }
+                }
+                int nk = 0, nv = 0, nq[2] = {0, 0};       // copies issued: K, V and Q tiles
+                while (ok && w.next(a, table, p)) {
+                    if (p.t1 == p.t0) continue;
+                    for (int i = 0; i < (p.two ? 2 : 1) && ok; ++i) {
+                        if (nq[i] > 0 && !(ok = wait(bar(K::QEMPTY + i), (nq[i] - 1) & 1, ctl))) break;
+                        ++nq[i];
+                        mbar_arrive_expect_tx(bar(K::QFULL + i), K::SLABS * a.pb * a.group * 128);
+                        for (int s = 0; s < K::SLABS; ++s)
+                            tensor_g2s(sb + K::OFF_Q + i * K::TILE + s * K::SLAB, &a.q, s * 64, p.g * a.group,
+                                       (int)(p.s.q0 + p.q0 + i * a.pb), bar(K::QFULL + i));
+                    }
+                    for (int t = p.t0; t < p.t1 && ok; ++t) {
+                        const int key = (int)(p.s.k0 + (int64_t)t * kKeys);
+                        const int sk = nk % NSK, sv = nv % NSV;
+                        if (nk >= NSK && !(ok = wait(bar(K::KEMPTY + sk), ((nk - NSK) / NSK) & 1, ctl))) break;
+                        ++nk;
+                        mbar_arrive_expect_tx(bar(K::KFULL + sk), K::TILE);
+                        for (int s = 0; s < K::SLABS; ++s)
+                            tensor_g2s(sb + K::OFF_K + sk * K::TILE + s * K::SLAB, &a.k, s * 64, p.g, key, bar(K::KFULL + sk));
+                        if (nv >= NSV && !(ok = wait(bar(K::VEMPTY + sv), ((nv - NSV) / NSV) & 1, ctl))) break;
+                        ++nv;
+                        mbar_arrive_expect_tx(bar(K::VFULL + sv), K::TILE);
+                        for (int s = 0; s < K::SLABS; ++s)
+                            tensor_g2s(sb + K::OFF_V + sv * K::TILE + s * K::SLAB, &a.v, s * 64, p.g, key, bar(K::VFULL + sv));
+                    }
+                }
+                // drain: every copy in flight lands before the CTA exits
+                const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
+                for (int t = max(0, nk - NSK); t < nk; ++t) wait(bar(K::KFULL + t % NSK), (t / NSK) & 1, drain);
+                for (int t = max(0, nv - NSV); t < nv; ++t) wait(bar(K::VFULL + t % NSV), (t / NSV) & 1, drain);
+                for (int i = 0; i < 2; ++i)
+                    if (nq[i] > 0) wait(bar(K::QFULL + i), (nq[i] - 1) & 1, drain);
+            }
+            __syncwarp();
+        } else if (warp == kMma || warp == kMma + 1) {
+            // -------------------------------------------- MMA issuer of row tile i
+            const int i = warp - kMma;
+            if (lane == 0) {
+                constexpr uint32_t idS = Type<T>::id(kRows, kKeys, false);
+                constexpr uint32_t idPV = Type<T>::id(kRows, D, true);
+                const uint32_t qbase = sb + K::OFF_Q + i * K::TILE, s_i = tmem + i * kKeys, o_i = tmem + K::COL_O + i * D;
+                int n = 0, scnt = 0, ocnt = 0;            // tiles; this row tile's P tiles and items
+                bool ok = true;
+                while (ok && w.next(a, table, p)) {
+                    const int tiles = p.t1 - p.t0;
+                    if (tiles == 0) continue;
+                    if (i == 1 && !p.two) {
+                        // no rows here: release this row tile's share of every slot once its tile has landed
+                        for (int x = 0; x < tiles && ok; ++x, ++n) {
+                            if (!(ok = wait(bar(K::KFULL + n % NSK), (n / NSK) & 1, ctl))) break;
+                            mbar_arrive(bar(K::KEMPTY + n % NSK));
+                            if (!(ok = wait(bar(K::VREADY + n % NSV), (n / NSV) & 1, ctl))) break;
+                            mbar_arrive(bar(K::VEMPTY + n % NSV));
+                        }
+                        continue;
+                    }
+                    if (!(ok = wait(bar(K::QFULL + i), ocnt & 1, ctl))) break;
+                    auto issue_s = [&](int x) -> bool {   // tile x of the piece
+                        const int sk = (n + x) % NSK;
+                        if (!wait(bar(K::KFULL + sk), ((n + x) / NSK) & 1, ctl)) return false;
+                        tc_fence_after();
+                        const uint32_t kbase = sb + K::OFF_K + sk * K::TILE;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint32_t off = (k / 4) * K::SLAB + (k % 4) * 32;
+                            mma_bf16(s_i, desc_sw128(qbase + off, 16, 1024), desc_sw128(kbase + off, 16, 1024), idS,
+                                     k > 0 ? 1u : 0u);
+                        }
+                        mma_commit(bar(K::SFULL + i));
+                        mma_commit(bar(K::KEMPTY + sk));
+                        if (x + 1 == tiles) mma_commit(bar(K::QEMPTY + i));
+                        return true;
+                    };
+                    if (!(ok = issue_s(0))) break;
+                    // keys that any row of this row tile sees, from the piece's first tile on
+                    const int last = p.s.L - p.s.Q + p.q0 + min(p.nq, (i + 1) * a.pb) - p.t0 * kKeys;
+                    for (int x = 0; x < tiles && ok; ++x) {
+                        const int sv = (n + x) % NSV;
+                        const uint32_t vbase = sb + K::OFF_V + sv * K::TILE;
+                        const int steps = min(max((last - x * kKeys + 15) / 16, 1), kKeys / 16);   // 16 keys an MMA
+                        auto pv = [&](int k0, int k1) {
+                            for (int k = k0; k < k1; ++k)
+                                mma_bf16_tmem_a(o_i, s_i + k * 8, desc_sw128(vbase + k * 2048, K::SLAB, 1024), idPV,
+                                                x > 0 || k > 0 ? 1u : 0u);
+                        };
+                        if (!(ok = wait(bar(K::VREADY + sv), ((n + x) / NSV) & 1, ctl))) break;
+                        if (!(ok = wait(bar(K::PFA + i), scnt & 1, ctl))) break;
+                        // the first PV of an item starts O_i afresh: the last one's result has been read
+                        if (x == 0 && ocnt > 0 && !(ok = wait(bar(K::OFREE + i), (ocnt - 1) & 1, ctl))) break;
+                        tc_fence_after();
+                        pv(0, min(steps, 4));
+                        if (!(ok = wait(bar(K::PFB + i), scnt & 1, ctl))) break;
+                        ++scnt;
+                        tc_fence_after();
+                        pv(4, steps);
+                        mma_commit(bar(K::VEMPTY + sv));
+                        if (x + 1 < tiles) ok = issue_s(x + 1);
+                        else mma_commit(bar(K::ODONE + i));
+                    }
+                    ++ocnt;
+                    n += tiles;
+                }
+                mma_commit(bar(K::DRAIN));
+                // every MMA issued has completed before TMEM is freed
+                const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
+                wait(bar(K::DRAIN), 0, drain);
+            }
+            __syncwarp();
+        } else {
+            // -------------------------------------------- V guard
+            int n = 0, item = 0;
+            bool ok = true;
+            while (ok && w.next(a, table, p)) {
+                const int it = item;
+                item += p.t1 > p.t0;
+                // keys past `all` are not seen by every row of the item; L and beyond by none
+                const int all = p.s.L - p.s.Q + p.q0;
+                bool found = false;
+                for (int t = p.t0; t < p.t1 && ok; ++t, ++n) {
+                    const int sv = n % NSV;
+                    if (!(ok = __all_sync(0xffffffffu, wait(bar(K::VFULL + sv), (n / NSV) & 1, ctl)))) break;
+                    const int r0 = max(all + 1 - t * kKeys, 0), r1 = min(p.s.L - t * kKeys, kKeys);
+                    if (t == p.t0 && lane == 0) nonfinite[it & (kFlags - 1)] = 0;
+                    __syncwarp();
+                    if (r0 < kKeys) {
+                        uint8_t* base = smem + K::OFF_V + sv * K::TILE;
+                        for (int s = 0; s < K::SLABS; ++s)
+                            for (int x = r0 * 8 + lane; x < kKeys * 8; x += 32) {
+                                uint4* at = reinterpret_cast<uint4*>(base + s * K::SLAB + x * 16);
+                                if (x / 8 >= r1) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                    continue;
+                                }
+                                uint4 v = *at;
+                                uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+                                bool bad = false;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    constexpr uint32_t I = Type<T>::INF;
+                                    if ((e[j] & I) == I) {
+                                        e[j] &= 0xffff0000u;
+                                        bad = true;
+                                    }
+                                    if ((e[j] & (I << 16)) == (I << 16)) {
+                                        e[j] &= 0xffffu;
+                                        bad = true;
+                                    }
+                                }
+                                if (bad) {
+                                    *at = v;
+                                    found = true;
+                                }
+                            }
+                        if (__any_sync(0xffffffffu, found) && lane == 0) nonfinite[it & (kFlags - 1)] = 1;
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
+                }
+            }
+        }
+    }
+
+    // teardown: every role arrives from its own code path (non-.aligned barrier)
+    __syncwarp();
+    tc_fence_before();
+    cta_bar_sync();
+    if (warp == 11) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, K::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------ join
+
+// Joins the parts of the items that a split launch cut: CTA (c, y) takes the item whose first part
+// CTA c left in its slot 1, rows 32 y .. 32 y + 31; a warp's lanes are rows (the slots' layout makes
+// its loads contiguous) and warps share the dimensions.  Parts are added in the keys' order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Arg a, int chunk, int grid) {
+    __shared__ int tab[3 * (kTable + 1)];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Table table{tab, chunk};
+    griddep_wait();
+    if (tid < kTable) build_table(a, tab, chunk, tid, false);
+    __syncthreads();
+    if (warp == 0) sum_table(tab, lane);
+    __syncthreads();
+    const int total = tab[kTable], ctas = split_ctas(total, grid), c = blockIdx.x;
+    if (c >= ctas || total == 0) return;
+    const int u0 = split_start(total, ctas, c), u1 = split_start(total, ctas, c + 1);
+    if (u0 == u1) return;
+    // the CTA's last piece: does it start an item that goes on past the range?
+    Piece p;
+    int step;
+    if (!locate(a, table, u1 - 1, 1, p, &step)) return;
+    const int first = u1 - 1 - p.t0, end = first + p.T;   // the item's units
+    if (first < u0 || end <= u1) return;
+    const int R = blockIdx.y * 32 + lane, i = R / kRows, r = R % kRows;
+    const int pos = r / a.group, hl = r - pos * a.group, qi = p.q0 + i * a.pb + pos;
+    if (!(pos < a.pb && qi < p.q0 + p.nq) || (i == 1 && !p.two)) return;
+    const float* slots = a.partials;
+    auto slot = [&](int x) { return slots + ((size_t)x * 2 + (x == c ? 1 : 0)) * slot_floats(D); };
+    float m = -INFINITY;
+    int last = c;
+    for (int x = c; x < ctas; ++x) {
+        m = fmaxf(m, slot(x)[(size_t)2 * kRows * D + R]);
+        last = x;
+        if (split_start(total, ctas, x + 1) >= end) break;
+    }
+    const float mref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float o[D / 8];
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d) o[d] = 0.f;
+    for (int x = c; x <= last; ++x) {
+        const float* s = slot(x);
+        const float mx = s[(size_t)2 * kRows * D + R];
+        const float f = mx == -INFINITY ? (s[(size_t)2 * kRows * (D + 1) + R] == 0.f ? 0.f : 1.f) : exp2f(mx - mref);
+        l += f * s[(size_t)2 * kRows * (D + 1) + R];
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+            const float4 v = *reinterpret_cast<const float4*>(s + ((size_t)(warp * (D / 32) + d) * 2 * kRows + R) * 4);
+            // (a part that saw nothing holds zeros, or non-finite values of V that its rows do see)
+            const float g = mx == -INFINITY ? 1.f : f;
+            o[4 * d] = fmaf(v.x, g, o[4 * d]);
+            o[4 * d + 1] = fmaf(v.y, g, o[4 * d + 1]);
+            o[4 * d + 2] = fmaf(v.z, g, o[4 * d + 2]);
+            o[4 * d + 3] = fmaf(v.w, g, o[4 * d + 3]);
+        }
+    }
+    const bool sees = p.s.L - p.s.Q + qi >= 0;
+    const float inv = sees ? 1.f / l : 0.f;
+    const int64_t row = p.s.q0 + qi;
+    uint8_t* dst = a.out.row(row, p.g * a.group + hl) + warp * (D / 8) * 2;
+#pragma unroll
+    for (int d = 0; d < D / 8; d += 8) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = sees ? o[d + e] * inv : 0.f;
+        *reinterpret_cast<uint4*>(dst + d * 2) =
+            make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+    }
+    if (warp == 0 && a.lse) a.lse[row * a.Hq + p.g * a.group + hl] = sees ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+}
+
+// ------------------------------------------------------------------ host
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+Encode encoder() {
+    static const Encode fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult st;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+            st != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return (Encode)p;
+    }();
+    return fn;
+}
+
+// Map of rows [tokens][heads][D] in boxes of 64 dims x `bh` heads x `bt` tokens.
+bool make_map(CUtensorMap* m, const pkv_rows* r, const void* fallback, int dtype, int D, int64_t tokens, int bh, int bt) {
+    const bool none = tokens < 1;                         // (nothing is ever copied: any valid map)
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)r->num_heads, (cuuint64_t)(none ? 1 : tokens)};
+    // strides of dimensions of extent 1 are never used, but are checked
+    const cuuint64_t strides[2] = {none || r->num_heads == 1 ? (cuuint64_t)D * 2 : (cuuint64_t)r->head_stride * 2,
+                                   none || tokens == 1 ? (cuuint64_t)D * 2 : (cuuint64_t)r->token_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)bh, (cuuint32_t)bt}, one[3] = {1, 1, 1};
+    return encoder()(m, dtype == PKV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                     none ? const_cast<void*>(fallback) : r->data, dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256) prompt_kernel(const __grid_constant__ Arg a) {
-    griddep_wait();
-    const int b = blockIdx.x / a.max_q_len, i = blockIdx.x % a.max_q_len;
-    const int Q = a.q_lens[b], L = a.kv_lens[b];
-    int64_t q0 = 0, k0 = 0;
-    if (a.q_starts) q0 = a.q_starts[b];
-    else for (int x = 0; x < b; ++x) q0 += max(a.q_lens[x], 0);
-    if (a.kv_starts) k0 = a.kv_starts[b];
-    else for (int x = 0; x < b; ++x) k0 += max(a.kv_lens[x], 0);
-    if (Q < 0 || Q > a.max_q_len || L < 0 || q0 < 0 || k0 < 0 || q0 + Q > a.num_q_rows || k0 + L > a.num_kv_rows) {
-        if (threadIdx.x == 0) raise_error(a.err, PKV_DEVERR_LENGTH);
-        return;
-    }
-    if (i >= Q) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int vis = max(0, L - Q + i + 1);
-    for (int h = warp; h < a.q.heads; h += 8) {
-        const uint8_t* q = a.q.row(q0 + i, h);
-        float x[D / 32], o[D / 32];
-        for (int e = 0; e < D / 32; ++e) {
-            x[e] = get<T>(q, lane + 32 * e) * a.scale;
-            o[e] = 0.f;
-        }
-        float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < vis; ++j) {
-            const uint8_t* k = a.k.row(k0 + j, h / a.group);
-            float s = 0.f;
-            for (int e = 0; e < D / 32; ++e) s = fmaf(x[e], get<T>(k, lane + 32 * e), s);
-            for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-            const uint8_t* v = a.v.row(k0 + j, h / a.group);
-            const float mn = fmaxf(m, s), c = m == mn ? 1.f : expf(m - mn), p = expf(s - mn);
-            m = mn;
-            l = l * c + p;
-            for (int e = 0; e < D / 32; ++e) o[e] = fmaf(p, get<T>(v, lane + 32 * e), o[e] * c);
-        }
-        T* out = reinterpret_cast<T*>(a.out.row(q0 + i, h));
-        for (int e = 0; e < D / 32; ++e) out[lane + 32 * e] = T(vis ? o[e] / l : 0.f);
-        if (a.lse && lane == 0) a.lse[(q0 + i) * a.q.heads + h] = vis ? m + logf(l) : -INFINITY;
-    }
+cudaError_t launch(const Arg& a, int chunk, unsigned grid, cudaStream_t st) {
+    static std::atomic<uint64_t> set{0};
+    cudaError_t e = launch_pdl_bigsmem(set, prompt_kernel<T, D>, dim3(grid), dim3(kThreads), (size_t)Cfg<D>::SMEM, st, a,
+                                       chunk);
+    if (e == cudaSuccess && a.split)
+        e = launch_pdl(join_kernel<T, D>, dim3(grid, 2 * kRows / 32), dim3(256), (size_t)0, st, a, chunk, (int)grid);
+    return e;
 }
 
 }  // namespace prompt
 
+size_t prompt_workspace_bytes() {
+    const int sms = num_sms_current();
+    return sms > 0 ? (size_t)sms * 2 * prompt::slot_floats(128) * sizeof(float) : 0;
+}
+
 cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* v, const pkv_rows* out, float* lse,
                           int dtype, int head_dim, int64_t num_q_rows, int64_t num_kv_rows, const int32_t* q_lens,
                           const int32_t* kv_lens, const int64_t* q_starts, const int64_t* kv_starts, int num_seqs,
-                          int max_q_len, float scale, int* err, cudaStream_t st) {
+                          int max_q_len, float scale, void* workspace, int* err, cudaStream_t st) {
     using namespace prompt;
-    auto view = [&](const pkv_rows* r) {
+    const int sms = num_sms_current();
+    if (sms <= 0 || !encoder()) return cudaErrorUnknown;
+    const int G = q->num_heads / k->num_heads, Hkv = k->num_heads;
+    Arg a = {};
+    a.pb = kRows / G;
+    if (!make_map(&a.q, q, q->data, dtype, head_dim, num_q_rows, G, a.pb)) return cudaErrorInvalidValue;
+    if (!make_map(&a.k, k, q->data, dtype, head_dim, num_kv_rows, 1, kKeys)) return cudaErrorInvalidValue;
+    if (!make_map(&a.v, v, q->data, dtype, head_dim, num_kv_rows, 1, kKeys)) return cudaErrorInvalidValue;
+    auto view = [](const pkv_rows* r) {
         View x = {(uint8_t*)r->data, r->token_stride * 2, r->head_stride * 2, r->num_heads};
         return x;
     };
-    Arg a = {view(q), view(k), view(v), view(out), lse, q_lens, kv_lens, q_starts, kv_starts, err, num_q_rows,
-             num_kv_rows, num_seqs, max_q_len, q->num_heads / k->num_heads, scale};
-    const int64_t grid = (int64_t)num_seqs * max_q_len;
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    auto go = [&](auto kern) { return launch_pdl(kern, dim3((unsigned)grid), dim3(256), (size_t)0, st, a); };
-    if (dtype == PKV_BF16) return head_dim == 128 ? go(prompt_kernel<__nv_bfloat16, 128>) : go(prompt_kernel<__nv_bfloat16, 64>);
-    return head_dim == 128 ? go(prompt_kernel<__half, 128>) : go(prompt_kernel<__half, 64>);
+    a.vrows = view(v);
+    a.out = view(out);
+    a.lse = lse;
+    a.q_lens = q_lens;
+    a.kv_lens = kv_lens;
+    a.q_starts = q_starts;
+    a.kv_starts = kv_starts;
+    a.err = err;
+    a.partials = (float*)workspace;
+    AttnParams dbg = {};
+    fill_debug(dbg);
+    a.wait_limit_ns = dbg.wait_limit_ns;
+    a.hold = dbg.hold;
+    a.num_q_rows = num_q_rows;
+    a.num_kv_rows = num_kv_rows;
+    a.num_seqs = num_seqs;
+    a.max_q_len = max_q_len;
+    a.Hq = q->num_heads;
+    a.Hkv = Hkv;
+    a.group = G;
+    a.scale_log2 = scale * kLog2e;
+    // at most this many items (their number depends on the lengths, which the host does not see)
+    const int64_t per = 2 * a.pb;
+    const int64_t items = Hkv * std::min<int64_t>((int64_t)num_seqs * ((max_q_len + per - 1) / per),
+                                                  num_q_rows / per + num_seqs);
+    if (items > 0x7fffffff) return cudaErrorInvalidValue;
+    a.split = workspace != nullptr && items < 2 * sms && items * ((num_kv_rows + kKeys - 1) / kKeys + 1) < 0x7fffffff;
+    const unsigned grid = (unsigned)(a.split ? sms : std::min<int64_t>(std::max<int64_t>(items, 1), sms));
+    const int chunk = (num_seqs + kTable - 1) / kTable;
+    if (dtype == PKV_BF16)
+        return head_dim == 128 ? launch<__nv_bfloat16, 128>(a, chunk, grid, st) : launch<__nv_bfloat16, 64>(a, chunk, grid, st);
+    return head_dim == 128 ? launch<__half, 128>(a, chunk, grid, st) : launch<__half, 64>(a, chunk, grid, st);
 }
 
 }  // namespace pkv
