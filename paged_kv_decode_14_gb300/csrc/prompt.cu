@@ -10,22 +10,28 @@
 //   S_i[128 rows, 128 keys] = Q_i . K_t^T      (A and B K-major in shared memory)
 //   P_i = 2^(S_i scale log2(e) - m), l += sum P_i    (one thread per row = TMEM lane)
 //   O_i[128 rows, D] += P_i . V_t              (A = P from TMEM, B MN-major in shared memory)
-// and out = O / l at the end.  m is raised (O and l rescaled) only when a
-// row's maximum exceeds it by more than 2^8, so most tiles leave O alone; P
-// is rounded to the inputs' type because both operands of one MMA have the
-// same type (bf16 keeps the fp32 range; fp16 P stays below 2^9).
+// and out = O / l at the end.  m is the maximum of the row's first tile; after
+// that no maximum is taken: a tile's sum of P bounds its largest P, and m rises
+// (O and l rescaled, by exact powers of 2) only after a tile whose sum reached
+// 2^8, or at once before 32 keys whose P would reach 2^15 (fp16's range).  P is
+// rounded to the inputs' type because both operands of one MMA have the same
+// type.
 //
 // Q, K and V tiles arrive by tensor copies (TMA) in the 128-byte swizzle,
 // straight from strided rows: K-major operands for Q and K, an MN-major one
 // for V, without a pass over the data.
 //
-// Roles (384 threads): warps 0-3 the softmax of row tile 0, warps 4-7 of row
-// tile 1 (they also write the results), warp 8 the producer, warps 9 and 10
-// the MMA issuers of row tiles 0 and 1, warp 11 the V guard.  Per tile issuer
-// i runs  PV_i(t) first 64 keys | PV_i(t) rest | S_i(t + 1)  while the other
-// row tile is in its softmax.  One thread's tcgen05 operations complete in
-// order, so when S_i(t + 1) signals, PV_i(t) is done and O_i may be rescaled,
-// and S_i(t + 1) overwrites P_i(t) only after PV_i(t) has read it.
+// Roles (512 threads): warps 0-3 the softmax of row tile 0, warps 4-7 of row
+// tile 1, warps 8-11 the epilogue of both, warp 12 the producer, warps 13 and
+// 14 the MMA issuers of row tiles 0 and 1, warp 15 the V guard.  Per tile
+// issuer i runs  PV_i(t), first 64 keys as soon as their P is written | PV_i(t)
+// rest, S_i(t + 1).  The second block runs in turns (0, 1, 0, 1, ...): left
+// alone, the MMAs of both interleave, both S finish together and the tensor
+// core idles through two simultaneous softmaxes; in turns the row tiles stay
+// half a period apart.  The last tile of an item is followed by the next
+// item's first S.  One thread's tcgen05 operations complete in order, so when
+// S_i(t + 1) signals, PV_i(t) is done and O_i may be rescaled, and S_i(t + 1)
+// overwrites P_i(t) only after PV_i(t) has read it.
 //
 // The V guard makes keys that some rows do not see harmless: a weight of 0
 // times NaN or infinity is NaN, so rows of V past the sequence's end are
@@ -55,11 +61,14 @@ using rows::View;
 
 constexpr int kRows = 128;                 // rows of a row tile (MMA M)
 constexpr int kKeys = 128;                 // keys of a key tile
-constexpr int kThreads = 384;
-constexpr int kProducer = 8, kMma = 9;   // (the guard: warp 11)
-constexpr float kSlack = 8.f;              // raise m (and rescale O) past 2^8 only
-constexpr int kTable = 128;                // entries of the sequence table
+constexpr int kThreads = 512;
+// Registers a thread: the launch gives every thread 128, and the roles' shares add up to as many.
+constexpr int kRegsSoftmax = 168, kRegsEpilogue = 112, kRegsOther = 64;
+static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOther == 4 * 128, "register file");
+constexpr int kProducer = 12, kMma = 13, kGuard = 15;   // (0-7: softmax, 8-11: epilogue)
+constexpr int kTable = 32;                 // entries of the sequence table
 constexpr int kFlags = 8;                  // items whose "non-finite V" flags are kept
+constexpr int kPieces = 4;                 // pieces of work the producer may be ahead
 
 struct Arg {
     CUtensorMap q, k, v;
@@ -75,11 +84,27 @@ struct Arg {
     int num_seqs, max_q_len, Hq, Hkv, group;
     int pb;                                // query positions of a row tile
     int split;                             // key tiles cut into equal ranges
+    int wide;                              // out's rows are 32-byte aligned
     float scale_log2;
 };
 
 // A partial slot: O as [D / 4][256 rows][4] fp32, then m and l, [256] each.
 __host__ __device__ constexpr int slot_floats(int D) { return 2 * kRows * (D + 2); }
+
+struct Seq {
+    int64_t q0, k0;         // first rows
+    int Q, L;               // 0 queries where the lengths are bad
+};
+
+// A piece of work: key tiles [t0, t1) of query block qb of sequence s, kv-head g.
+struct Piece {
+    Seq s;
+    int g, q0, nq, T, t0, t1;
+    bool two;               // row tile 1 holds rows
+    bool whole;             // all of the item's tiles: the result is written at once
+    bool end;               // no more work (the other fields are unset)
+};
+static_assert(sizeof(Piece) % 8 == 0, "aligned ring entries");
 
 template <int D>
 struct Cfg {
@@ -95,12 +120,16 @@ struct Cfg {
     // barriers: KFULL[NSK] KEMPTY[NSK] VFULL[NSV] VREADY[NSV] VEMPTY[NSV], then pairs by row tile
     static constexpr int KFULL = 0, KEMPTY = NSK, VFULL = 2 * NSK, VREADY = VFULL + NSV, VEMPTY = VREADY + NSV,
                          SFULL = VEMPTY + NSV, PFA = SFULL + 2, PFB = SFULL + 4, QFULL = SFULL + 6,
-                         QEMPTY = SFULL + 8, ODONE = SFULL + 10, OFREE = SFULL + 12, DRAIN = SFULL + 14;
-    static constexpr int NBAR = SFULL + 15;
+                         QEMPTY = SFULL + 8, ODONE = SFULL + 10, OFREE = SFULL + 12, LREADY = SFULL + 14,
+                         PVA = SFULL + 16, TURN = SFULL + 18, PCFULL = SFULL + 20, PCEMPTY = PCFULL + kPieces,
+                         DRAIN = PCEMPTY + kPieces;
+    static constexpr int NBAR = DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
     static constexpr int OFF_FLAG = OFF_MISC + 16;        // int[kFlags]
     static constexpr int OFF_TABLE = OFF_FLAG + 4 * kFlags;   // int[3][kTable + 1]: units, q rows, kv rows before
-    static constexpr int SMEM = OFF_TABLE + 12 * (kTable + 1) + 1024;   // (+ alignment)
+    static constexpr int OFF_INV = (OFF_TABLE + 12 * (kTable + 1) + 15) / 16 * 16;   // float[2][kRows]: 1 / l
+    static constexpr int OFF_PIECE = OFF_INV + 8 * kRows;     // Piece[kPieces]
+    static constexpr int SMEM = OFF_PIECE + kPieces * (int)sizeof(Piece);
     static constexpr int COL_O = 2 * kKeys;
     static constexpr int TMEM_COLS = 512;
     static_assert(COL_O + 2 * D <= TMEM_COLS, "tensor memory budget");
@@ -108,11 +137,6 @@ struct Cfg {
 };
 
 // ------------------------------------------------------------------ work
-
-struct Seq {
-    int64_t q0, k0;         // first rows
-    int Q, L;               // 0 queries where the lengths are bad
-};
 
 // Sequence b, given the packed rows before it.
 __device__ __forceinline__ Seq seq_at(const Arg& a, int b, int64_t qb, int64_t kb, bool* bad = nullptr) {
@@ -150,7 +174,7 @@ struct Table {
     int chunk;              // sequences a chunk
 };
 __device__ __forceinline__ void build_table(const Arg& a, int* tab, int chunk, int tid, bool report) {
-    // (threads 0 .. kTable - 1; the sums over chunks follow in warp 0)
+    // (lanes 0 .. kTable - 1; the sums over chunks follow)
     int u = 0;
     int64_t q = 0, k = 0;
     for (int b = tid * chunk; b < min((tid + 1) * chunk, a.num_seqs); ++b) {
@@ -188,14 +212,6 @@ __device__ __forceinline__ void sum_table(int* tab, int lane) {
     }
     __syncwarp();
 }
-
-// A piece of work: key tiles [t0, t1) of query block qb of sequence s, kv-head g.
-struct Piece {
-    Seq s;
-    int g, q0, nq, T, t0, t1;
-    bool two;               // row tile 1 holds rows
-    bool whole;             // all of the item's tiles: the result is written at once
-};
 
 // The piece at unit u of [u, end) (not split: one unit an item).  False: the unit belongs to a
 // sequence whose rows lie outside the tensors; *step units are to be passed over.
@@ -254,6 +270,7 @@ __device__ __forceinline__ bool locate(const Arg& a, const Table& tb, int u, int
     p.q0 = blk * 2 * a.pb;
     p.nq = min(2 * a.pb, p.s.Q - p.q0);
     p.two = p.nq > a.pb;
+    p.end = false;
     return true;
 }
 
@@ -303,7 +320,8 @@ struct Ctl {
     int* err;
     uint64_t limit;
 };
-__device__ __noinline__ bool wait_spin(uint32_t bar, uint32_t parity, volatile int* abort, int* err, uint64_t limit) {
+// (inlined: a call would keep ptxas from giving the roles registers of their own)
+__device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, volatile int* abort, int* err, uint64_t limit) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -338,6 +356,31 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
            (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// The issuer's operations run in warp-uniform code with one lane's predicate: in code that one lane
+// runs alone, every descriptor is moved to a uniform register first, which cost ~107 clocks a MMA
+// against the 64 that the tensor core needs for it.
+__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(bool lead, uint32_t bar) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"((uint32_t)lead)
+        : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -366,12 +409,19 @@ __device__ __forceinline__ uint64_t f2add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// Orders later uses of r behind the last tcgen05.wait::ld (no instruction).
-__device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                          "+r"(r[i + 6]), "+r"(r[i + 7]));
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred P;\nelect.sync _|P, 0xffffffff;\nselp.b32 %0, 1, 0, P;\n}\n" : "=r"(p));
+    return p != 0;
 }
 
 template <typename T>
@@ -403,13 +453,28 @@ struct Type<__half> {
 
 // ------------------------------------------------------------------ kernel
 
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store32(uint8_t* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// (split) where a part of an item goes: the part that starts the item is its CTA's last piece (slot
+// 1), any other its CTA's first (slot 0).
+template <int D>
+__device__ __forceinline__ float* part_slot(const Arg& a, const Piece& p) {
+    return a.partials + ((size_t)blockIdx.x * 2 + (p.t0 == 0 ? 1 : 0)) * slot_floats(D);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Arg a, int chunk) {
     using K = Cfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];     // (the swizzle needs it; checked below)
     const uint32_t sb = smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (the warp's number by a shuffle: known to be uniform, and with it the roles' control flow, which the
+    // MMA issue needs -- 12 MMAs 926 -> 856 clocks)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return sb + K::OFF_BAR + 8 * i; };
     constexpr int NSK = K::NSK, NSV = K::NSV;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::OFF_MISC);
@@ -417,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 8);   // (drain waits at the end)
     volatile int* nonfinite = reinterpret_cast<volatile int*>(smem + K::OFF_FLAG);
     int* tab = reinterpret_cast<int*>(smem + K::OFF_TABLE);
+    float* inv_l = reinterpret_cast<float*>(smem + K::OFF_INV);
     const Table table{tab, chunk};
     const Ctl ctl{abort_flag, a.err, a.wait_limit_ns};
 
@@ -438,27 +504,57 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             mbar_init(bar(K::QEMPTY + i), 1);
             mbar_init(bar(K::ODONE + i), 1);
             mbar_init(bar(K::OFREE + i), 4);
+            mbar_init(bar(K::LREADY + i), 4);
+            mbar_init(bar(K::PVA + i), 1);
+            mbar_init(bar(K::TURN + i), 1);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bar(K::PCFULL + i), 1);
+            mbar_init(bar(K::PCEMPTY + i), 15);           // every warp but the producer
         }
         mbar_init(bar(K::DRAIN), 2);
         *abort_flag = 0;
         *drain_flag = 0;
         mbar_fence_init();
     }
-    if (warp == 11) {
+    if (warp == kProducer && lane < 3)
+        asm volatile("prefetch.tensormap [%0];\n" ::"l"(lane == 0 ? &a.q : lane == 1 ? &a.k : &a.v) : "memory");
+    if (warp == kGuard) {
         tmem_alloc(smem_u32(tmem_slot), K::TMEM_COLS);
         tmem_relinquish();
     }
     griddep_wait();
-    if (tid < kTable) build_table(a, tab, chunk, tid, blockIdx.x == 0);
-    cta_bar_sync();
-    if (warp == 0) sum_table(tab, lane);
+    static_assert(kTable == 32, "one lane a chunk");
+    if (warp == 0) {
+        build_table(a, tab, chunk, lane, blockIdx.x == 0);
+        __syncwarp();
+        sum_table(tab, lane);
+    }
+    if ((sb & 1023) != 0 && tid == 0) {
+        raise_error(a.err, PKV_DEVERR_TIMEOUT);           // (never: the declaration above aligns it)
+        *abort_flag = 1;
+    }
     tc_fence_before();
     cta_bar_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
+    // The pieces of work, found by the producer and read here by the other warps: the n-th piece
+    // (nullptr: a wait gave up), until its release.  The search costs registers and instruction
+    // cache, which 15 warps that each did their own paid for in their loops.
+    const Piece* ring = reinterpret_cast<const Piece*>(smem + K::OFF_PIECE);
+    auto piece_at = [&](int n) -> const Piece* {
+        return __all_sync(0xffffffffu, wait(bar(K::PCFULL + n % kPieces), (n / kPieces) & 1, ctl)) ? ring + n % kPieces
+                                                                                                  : nullptr;
+    };
+    auto release = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(K::PCEMPTY + n % kPieces));
+    };
+
     if (warp < 8) {
         // ------------------------------------------------ softmax of row tile i, thread r = row r
+        regs_inc<kRegsSoftmax>();
         const int i = warp >> 2, r = tid & (kRows - 1);
         const int G = a.group, pos = r / G, hl = r - pos * G;
         const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
@@ -472,190 +568,285 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(bb);
         };
-        Walk w;
-        w.start(a, table);
-        Piece p;
-        bool more = w.next(a, table, p), ok = true;
-        int scnt = 0, ocnt = 0, item = 0;                 // this row tile's S tiles and items; the CTA's items with tiles
-        while (more && ok) {
-            const bool act = i == 0 || p.two;
-            const int qi = p.q0 + i * a.pb + pos;         // query position
-            const bool row_ok = pos < a.pb && qi < p.q0 + p.nq;
+        bool ok = true;
+        int scnt = 0, ocnt = 0;                           // this row tile's S tiles and items
+        for (int n = 0; ok; ++n) {
+            const Piece* p = piece_at(n);
+            if (!p || p->end) break;
+            if (i == 1 && !p->two) {
+                release(n);
+                continue;
+            }
+            const int t0 = p->t0, t1 = p->t1, q0 = p->q0 + i * a.pb, nq = p->nq - i * a.pb;
+            const bool row_ok = pos < a.pb && pos < nq;
+            const int shift = p->s.L - p->s.Q + q0;       // the last key that the row tile's first row sees
             // keys 0 .. lim are visible (rows of no query: everything, so that they ask for no mask)
-            const int lim = row_ok ? p.s.L - p.s.Q + qi : 0x3fffffff;
-            float m = -INFINITY, l = 0.f;
-            for (int t = p.t0; act && t < p.t1; ++t, ++scnt) {
+            const int lim = row_ok ? shift + pos : 0x3fffffff;
+            const int top_lim = shift + min(nq, a.pb);    // keys that any of its rows sees
+            // m: the reference maximum (exp2 units), l: the sum of P; pend: octaves that m is to rise
+            float m = row_ok ? -INFINITY : 0.f, l = 0.f;
+            int pend = 0;
+            for (int t = t0; t < t1; ++t, ++scnt) {
                 if (!(ok = wait_all(bar(K::SFULL + i), scnt & 1))) break;
                 tc_fence_after();
                 const int rem = lim - t * kKeys;          // column c is visible iff c <= rem
                 const bool masked = !__all_sync(0xffffffffu, rem >= kKeys - 1);
-                uint64_t acc[2] = {0, 0};
-                auto tile = [&](auto mask) {
-                    // the last 64 columns first, for the maximum only: they are loaded again, behind the first
-                    // 64 columns' exponentials (TMEM reads cost little, 128 live registers more)
-                    uint32_t sa[32], sb_[32], sc_[32];
-                    tmem_ld32_async(scol + 64, sa);
-                    tmem_ld32_async(scol + 96, sb_);
-                    tmem_wait_ld_into(sa);
-                    tie32(sb_);
-                    tmem_ld32_async(scol, sc_);
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto maxima = [&](const uint32_t (&s)[32], int c, auto mask) {
-                        if constexpr (!decltype(mask)::value) {
-    #pragma unroll
-                            for (int x = 0; x < 32; x += 2)
-                                mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
-                        } else {
-    #pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                mx[x & 3] = fmaxf(mx[x & 3], c + x <= rem ? __uint_as_float(s[x]) : -INFINITY);
-                        }
-                    };
-                    maxima(sa, 64, mask);
-                    maxima(sb_, 96, mask);
-                    tmem_wait_ld_into(sc_);
-                    tmem_ld32_async(scol + 32, sa);
-                    maxima(sc_, 0, mask);
-                    tmem_wait_ld_into(sa);
-                    maxima(sa, 32, mask);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
-                    const bool up = top > m + kSlack;         // (m = -inf: any finite maximum)
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float alpha = up && m > -INFINITY ? exp2_fast(m - top) : 1.f;
-                        if (t > p.t0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-    #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                float o[16];
-                                tmem_ld16(ocol + c, o);
-                                uint32_t v[16];
-    #pragma unroll
-                                for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(o[x] * alpha);
-                                tmem_st16u(ocol + c, v);
-                            }
-                        }
-                        l *= alpha;
-                        if (up) m = top;
-                    }
-                    // rows with nothing visible so far keep m = -inf, and P = 2^-inf = 0 by the mask
-                    const float mref = m == -INFINITY ? 0.f : m;
-                    const uint64_t sc2 = f2pack(__float_as_uint(sc), __float_as_uint(sc));
-                    const uint64_t nm2 = f2pack(__float_as_uint(-mref), __float_as_uint(-mref));
-                                        // P of 32 keys, two per packed fp32 operation, into 16 columns (the even key in the low half)
-                    auto emit = [&](const uint32_t (&s)[32], int c, auto mask) {
+                uint32_t sa[32], sb_[32];
+                tmem_ld32_async(scol, sa);
+                // O_i *= alpha (exact powers of 2, or 1)
+                auto rescale_o = [&](float alpha) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        tmem_ld16(ocol + c, o);
                         uint32_t v[16];
-    #pragma unroll
-                        for (int x = 0; x < 32; x += 2) {
-                            float x0, x1;
-                            f2unpack(f2fma(f2pack(s[x], s[x + 1]), sc2, nm2), x0, x1);
-                            float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
-                            if constexpr (decltype(mask)::value) {
-                                p0 = c + x <= rem ? p0 : 0.f;
-                                p1 = c + x + 1 <= rem ? p1 : 0.f;
-                            }
-                            acc[(x >> 1) & 1] = f2add(acc[(x >> 1) & 1], f2pack(__float_as_uint(p0), __float_as_uint(p1)));
-                            v[x >> 1] = pack2<T>(p0, p1);
-                        }
-                        tmem_st16u(scol + (c >> 1), v);
-                    };
-                    tmem_ld32_async(scol + 64, sb_);
-                    emit(sc_, 0, mask);
-                    emit(sa, 32, mask);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(o[x] * alpha);
+                        tmem_st16u(ocol + c, v);
+                    }
                     tmem_wait_st();
-                    signal(bar(K::PFA + i));                  // PV of the first 64 keys may run meanwhile
-                    tmem_wait_ld_into(sb_);
-                    tmem_ld32_async(scol + 96, sa);
-                    emit(sb_, 64, mask);
-                    tmem_wait_ld_into(sa);
-                    emit(sa, 96, mask);
-                    tmem_wait_st();
-                    signal(bar(K::PFB + i));
                 };
-                if (masked) tile(std::true_type{});
-                else tile(std::false_type{});
-                float a0, a1;
-                f2unpack(f2add(acc[0], acc[1]), a0, a1);
-                l += a0 + a1;
+                tmem_wait_ld_into(sa);
+                if (__any_sync(0xffffffffu, pend > 0)) {
+                    // the last tile's sum asked for a higher reference
+                    const float alpha = pend < 127 ? __uint_as_float((uint32_t)(127 - pend) << 23) : 0.f;
+                    if (t > t0) rescale_o(alpha);
+                    l *= alpha;
+                    m += (float)pend;
+                    pend = 0;
+                }
+                // the largest visible S of columns [c0, c1)
+                auto maximum = [&](int c0, int c1) -> float {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t s[32];
+                        tmem_ld32_async(scol + c, s);
+                        tmem_wait_ld_into(s);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            mx[x & 3] = fmaxf(mx[x & 3], x <= rem - c ? __uint_as_float(s[x]) : -INFINITY);
+                    }
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                };
+                if (!__all_sync(0xffffffffu, m > -INFINITY)) {
+                    // no reference yet (a piece's first tile): the row's maximum.  (O and l are 0 so far, or NaN)
+                    const float top = maximum(0, kKeys) * sc;
+                    if (m == -INFINITY) m = top;
+                }
+                float ts = 0.f;                           // this tile's sum of P
+                // (rare) P of a half tile at column c would reach 2^15: m rises by a whole number of octaves,
+                // and the P written in this tile, O and l are scaled down by as many (exact but for what
+                // falls below the type's range, far below the new maximum)
+                auto raise_ref = [&](float target, int c) {
+                    const float inc = target > m ? ceilf(target - m) : 0.f;
+                    const int k = (int)fminf(inc, 127.f);
+                    const float alpha = k < 127 ? __uint_as_float((uint32_t)(127 - k) << 23) : 0.f;
+                    if (c > 0) {                          // the first half's P is being used: it ends in O
+                        wait_all(bar(K::PVA + i), scnt & 1);
+                        tc_fence_after();
+                    }
+                    if (t > t0 || c > 0) rescale_o(alpha);
+                    l *= alpha;
+                    ts *= alpha;
+                    m += inc;
+                };
+                // P of 32 keys at column c, two per packed fp32 operation (the even key in the low half);
+                // adds them to acc.  (Rows with nothing visible so far keep m = -inf: all their P are masked.)
+                const uint64_t sc2 = f2pack(__float_as_uint(sc), __float_as_uint(sc));
+                auto neg_m = [&] {
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    return f2pack(__float_as_uint(nm), __float_as_uint(nm));
+                };
+                auto emit = [&](const uint32_t (&s)[32], int c, uint32_t* v, uint64_t& acc, uint64_t nm2, auto mask) {
+                    uint64_t ca = 0, cb = 0;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 2) {
+                        float x0, x1;
+                        f2unpack(f2fma(f2pack(s[x], s[x + 1]), sc2, nm2), x0, x1);
+                        float p0 = exp2_fast(x0), p1 = exp2_fast(x1);
+                        if constexpr (decltype(mask)::value) {
+                            p0 = x <= rem - c ? p0 : 0.f;
+                            p1 = x + 1 <= rem - c ? p1 : 0.f;
+                        }
+                        if ((x >> 1) & 1) cb = f2add(cb, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
+                        else ca = f2add(ca, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
+                        v[x >> 1] = pack2<T>(p0, p1);
+                    }
+                    acc = f2add(acc, f2add(ca, cb));
+                };
+                // The P of 64 keys is written once its sum, which bounds the largest, is known to be below
+                // 2^15 (fp16's range).  True: written.
+                auto write = [&](uint64_t acc, int c, const uint32_t (&v)[32], bool force) -> bool {
+                    float a0, a1;
+                    f2unpack(acc, a0, a1);
+                    if (__any_sync(0xffffffffu, row_ok && !(a0 + a1 < 32768.f)) && !force) return false;
+                    ts += a0 + a1;
+                    tmem_st32u(scol + (c >> 1), v);
+                    tmem_wait_st();
+                    return true;
+                };
+                // 64 keys at column c, masked; a second time, with m raised, where the first is too large
+                // (NaN logits pass then).  A second half that no row sees is not read by the PV.
+                auto careful = [&](int c) {
+                    if (c > 0 && c >= top_lim - t * kKeys) return;
+                    for (bool force = false;; force = true) {
+                        uint32_t v[32];
+                        uint64_t acc = 0;
+                        const uint64_t nm2 = neg_m();
+                        tmem_ld32_async(scol + c, sa);
+                        tmem_wait_ld_into(sa);
+                        tmem_ld32_async(scol + c + 32, sb_);
+                        emit(sa, c, v, acc, nm2, std::true_type{});
+                        tmem_wait_ld_into(sb_);
+                        emit(sb_, c + 32, v + 16, acc, nm2, std::true_type{});
+                        if (write(acc, c, v, force)) break;
+                        const float top = maximum(c, c + 64);
+                        raise_ref(row_ok ? top * sc : -INFINITY, c);
+                    }
+                };
+                // (one copy of either path: the instruction cache holds little more than a tile's code)
+#pragma unroll 1
+                for (int c = 0; c < kKeys; c += 64) {
+                    bool done = false;
+                    if (!masked) {                        // loads in flight behind the arithmetic
+                        uint32_t v[32];
+                        uint64_t acc = 0;
+                        const uint64_t nm2 = neg_m();
+                        tmem_ld32_async(scol + c + 32, sb_);
+                        emit(sa, c, v, acc, nm2, std::false_type{});
+                        tmem_wait_ld_into(sb_);
+                        tmem_ld32_async(scol + 64, sa);   // (for the second half; after it, for nothing)
+                        emit(sb_, c + 32, v + 16, acc, nm2, std::false_type{});
+                        tmem_wait_ld_into(sa);
+                        done = write(acc, c, v, false);
+                    }
+                    if (!done) {
+                        careful(c);
+                        tmem_ld32_async(scol + 64, sa);
+                        tmem_wait_ld_into(sa);
+                    }
+                    // P of the first 64 keys: their PV may run while the rest is computed
+                    signal(bar(K::PFA + i) + (c ? 8 * (K::PFB - K::PFA) : 0));
+                }
+                l += ts;
+                // a tile sum of 2^8 or more (it bounds the largest P) moves the reference past it at the next tile
+                if (row_ok && ts >= 256.f && ts < INFINITY) pend = (int)(__float_as_uint(ts) >> 23) - 127 + 1;
             }
             if (!ok) break;
-            // the result of this piece; the next one is looked up while the last MMAs run
-            const Piece cur = p;
-            const bool tiles = cur.t1 > cur.t0;
-            const int it = item;
-            item += tiles;
-            more = w.next(a, table, p);
-            if (!act) continue;
-            if (tiles) {
-                if (!(ok = wait_all(bar(K::ODONE + i), ocnt & 1))) break;
-                ++ocnt;
-                tc_fence_after();
-            }
-            const int64_t row = cur.s.q0 + qi;
-            if (cur.whole) {
-                const bool sees = lim >= 0;
-                const float inv = sees ? 1.f / l : 0.f;
-                const bool fix = tiles && nonfinite[it & (kFlags - 1)] != 0;
-                uint8_t* dst = a.out.row(row, cur.g * G + hl);
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    if (tiles) tmem_ld32(ocol + c, o);
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = tiles && sees ? o[x] * inv : 0.f;
-                    if (fix && row_ok) {
-                        for (int j = max(cur.s.L - cur.s.Q + cur.q0 + 1, 0); j <= lim; ++j) {
-                            const uint8_t* v = a.vrows.row(cur.s.k0 + j, cur.g) + c * 2;
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) {
-                                const float f = Type<T>::get(v + 2 * x);
-                                if (!(fabsf(f) < INFINITY)) o[x] += f;
-                            }
-                        }
-                    }
-                    if (row_ok) {
-#pragma unroll
-                        for (int h = 0; h < 32; h += 8)
-                            *reinterpret_cast<uint4*>(dst + (c + h) * 2) =
-                                make_uint4(pack2<T>(o[h], o[h + 1]), pack2<T>(o[h + 2], o[h + 3]),
-                                           pack2<T>(o[h + 4], o[h + 5]), pack2<T>(o[h + 6], o[h + 7]));
-                    }
+            // this piece's sums go to the epilogue (1 / l) and to memory (lse, or the part's m and l)
+            const bool tiles = t1 > t0, sees = lim >= 0;
+            // (an item of a single tile gets here before its PV: the epilogue may still hold the last item's)
+            if (tiles && ocnt++ > 0 && !(ok = wait_all(bar(K::OFREE + i), ocnt & 1))) break;
+            if (p->whole) {
+                const int64_t row = p->s.q0 + q0 + pos;
+                const int h = p->g * G + hl;
+                if (row_ok && a.lse) a.lse[row * a.Hq + h] = sees ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+                if (tiles) {
+                    inv_l[i * kRows + r] = 1.f / l;
+                } else if (row_ok) {                      // no keys at all
+                    uint8_t* dst = a.out.row(row, h);
+                    for (int c = 0; c < D * 2; c += 16) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
                 }
-                if (row_ok && a.lse)
-                    a.lse[row * a.Hq + cur.g * G + hl] = sees ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
             } else {
-                // (split) a part of the item: unnormalised O, m and l.  The part that starts the item is the
-                // CTA's last piece (slot 1), any other its first (slot 0).
-                float* slot = a.partials + ((size_t)blockIdx.x * 2 + (cur.t0 == 0 ? 1 : 0)) * slot_floats(D);
-                const bool fix = nonfinite[it & (kFlags - 1)] != 0;
-                const int R = i * kRows + r;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tmem_ld32(ocol + c, o);
-                    if (fix && row_ok) {
-                        const int first = max(cur.s.L - cur.s.Q + cur.q0 + 1, cur.t0 * kKeys);
-                        for (int j = first; j <= min(lim, cur.t1 * kKeys - 1); ++j) {
-                            const uint8_t* v = a.vrows.row(cur.s.k0 + j, cur.g) + c * 2;
+                float* slot = part_slot<D>(a, *p);
+                slot[(size_t)2 * kRows * D + i * kRows + r] = m;
+                slot[(size_t)2 * kRows * (D + 1) + i * kRows + r] = l;
+            }
+            if (tiles) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(K::LREADY + i));
+            }
+            release(n);
+        }
+    } else if (warp < kProducer) {
+        // ------------------------------------------------ epilogue of both row tiles, thread r = row r
+        regs_dec<kRegsEpilogue>();
+        const int r = tid & (kRows - 1);
+        const int G = a.group, pos = r / G, hl = r - pos * G;
+        const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
+        auto wait_all = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, wait(bb, parity, ctl)); };
+        int cnt[2] = {0, 0}, item = 0;                    // items of either row tile; the CTA's items with tiles
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            const Piece* at = piece_at(n);
+            if (!at || at->end) break;
+            const Piece p = *at;
+            release(n);
+            if (p.t1 == p.t0) continue;
+            const int it = item++;
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) {
-                                const float f = Type<T>::get(v + 2 * x);
-                                if (!(fabsf(f) < INFINITY)) o[x] += f;
-                            }
+            for (int i = 0; i < 2; ++i) {
+                if (!ok || (i == 1 && !p.two)) break;
+                const uint32_t ocol = tmem + lbase + K::COL_O + i * D;
+                const int qi = p.q0 + i * a.pb + pos;
+                const bool row_ok = pos < a.pb && qi < p.q0 + p.nq;
+                const int lim = p.s.L - p.s.Q + qi;
+                if (!(ok = wait_all(bar(K::LREADY + i), cnt[i] & 1))) break;
+                const float inv = inv_l[i * kRows + r];
+                if (!(ok = wait_all(bar(K::ODONE + i), cnt[i] & 1))) break;
+                ++cnt[i];
+                tc_fence_after();
+                // infinities and NaN that the guard took out of V, for the rows that see them
+                const bool fix = nonfinite[it & (kFlags - 1)] != 0;
+                auto add_back = [&](float (&o)[32], int c) {
+                    const int first = max(p.s.L - p.s.Q + p.q0 + 1, p.t0 * kKeys);
+                    for (int j = first; j <= min(lim, p.t1 * kKeys - 1); ++j) {
+                        const uint8_t* v = a.vrows.row(p.s.k0 + j, p.g) + c * 2;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            const float f = Type<T>::get(v + 2 * x);
+                            if (!(fabsf(f) < INFINITY)) o[x] += f;
                         }
                     }
+                };
+                auto free_o = [&] {                       // O_i read: the next item's first PV may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(K::OFREE + i));
+                };
+                if (p.whole) {
+                    uint32_t v[D / 2];                    // the whole row, packed, so that O_i is free before the stores
 #pragma unroll
-                    for (int x = 0; x < 32; x += 4)
-                        *reinterpret_cast<float4*>(slot + ((size_t)((c + x) / 4) * 2 * kRows + R) * 4) =
-                            make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(ocol + c, o);
+                        if (fix && row_ok) add_back(o, c);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2)
+                            v[(c + x) >> 1] = lim >= 0 ? pack2<T>(o[x] * inv, o[x + 1] * inv) : 0u;
+                    }
+                    free_o();
+                    if (row_ok) {
+                        uint8_t* dst = a.out.row(p.s.q0 + qi, p.g * G + hl);
+                        if (a.wide) {
+#pragma unroll
+                            for (int c = 0; c < D / 2; c += 8) store32(dst + c * 4, v + c);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < D / 2; c += 4)
+                                *reinterpret_cast<uint4*>(dst + c * 4) = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                        }
+                    }
+                } else {
+                    float* slot = part_slot<D>(a, p);
+                    const int R = i * kRows + r;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld32(ocol + c, o);
+                        if (fix && row_ok) add_back(o, c);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4)
+                            *reinterpret_cast<float4*>(slot + ((size_t)((c + x) / 4) * 2 * kRows + R) * 4) =
+                                make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    }
+                    free_o();
                 }
-                slot[(size_t)2 * kRows * D + R] = m;
-                slot[(size_t)2 * kRows * (D + 1) + R] = l;
             }
-            if (tiles) signal(bar(K::OFREE + i));         // the next item's first PV may overwrite O_i
         }
     } else {
-        Walk w;
-        w.start(a, table);
-        Piece p;
+        regs_dec<kRegsOther>();
         if (warp == kProducer) {
             // -------------------------------------------- tensor copies: Q tiles, K and V tiles in order
             bool ok = true;
@@ -673,7 +864,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                 }
                 int nk = 0, nv = 0, nq[2] = {0, 0};       // copies issued: K, V and Q tiles
-                while (ok && w.next(a, table, p)) {
+                Walk w;
+                w.start(a, table);
+                Piece p;
+                for (int n = 0; ok; ++n) {
+                    p.end = !w.next(a, table, p);
+                    if (n >= kPieces && !(ok = wait(bar(K::PCEMPTY + n % kPieces), ((n - kPieces) / kPieces) & 1, ctl))) break;
+                    const_cast<Piece*>(ring)[n % kPieces] = p;
+                    mbar_arrive(bar(K::PCFULL + n % kPieces));
+                    if (p.end) break;
                     if (p.t1 == p.t0) continue;
                     for (int i = 0; i < (p.two ? 2 : 1) && ok; ++i) {
                         if (nq[i] > 0 && !(ok = wait(bar(K::QEMPTY + i), (nq[i] - 1) & 1, ctl))) break;
@@ -709,82 +908,138 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         } else if (warp == kMma || warp == kMma + 1) {
             // -------------------------------------------- MMA issuer of row tile i
             const int i = warp - kMma;
-            if (lane == 0) {
-                constexpr uint32_t idS = Type<T>::id(kRows, kKeys, false);
-                constexpr uint32_t idPV = Type<T>::id(kRows, D, true);
-                const uint32_t qbase = sb + K::OFF_Q + i * K::TILE, s_i = tmem + i * kKeys, o_i = tmem + K::COL_O + i * D;
-                int n = 0, scnt = 0, ocnt = 0;            // tiles; this row tile's P tiles and items
-                bool ok = true;
-                while (ok && w.next(a, table, p)) {
-                    const int tiles = p.t1 - p.t0;
-                    if (tiles == 0) continue;
-                    if (i == 1 && !p.two) {
-                        // no rows here: release this row tile's share of every slot once its tile has landed
-                        for (int x = 0; x < tiles && ok; ++x, ++n) {
-                            if (!(ok = wait(bar(K::KFULL + n % NSK), (n / NSK) & 1, ctl))) break;
-                            mbar_arrive(bar(K::KEMPTY + n % NSK));
-                            if (!(ok = wait(bar(K::VREADY + n % NSV), (n / NSV) & 1, ctl))) break;
-                            mbar_arrive(bar(K::VEMPTY + n % NSV));
-                        }
-                        continue;
-                    }
-                    if (!(ok = wait(bar(K::QFULL + i), ocnt & 1, ctl))) break;
-                    auto issue_s = [&](int x) -> bool {   // tile x of the piece
-                        const int sk = (n + x) % NSK;
-                        if (!wait(bar(K::KFULL + sk), ((n + x) / NSK) & 1, ctl)) return false;
-                        tc_fence_after();
-                        const uint32_t kbase = sb + K::OFF_K + sk * K::TILE;
+            const bool lead = elect_one();                // (8% faster over all than lane == 0)
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);       // (known to be uniform)
+            const uint32_t s_i = tm + __shfl_sync(0xffffffffu, i, 0) * kKeys;
+            const uint32_t o_i = tm + K::COL_O + __shfl_sync(0xffffffffu, i, 0) * D;
+            const uint32_t qbase = __shfl_sync(0xffffffffu, sb + K::OFF_Q + i * K::TILE, 0);
+            auto wait_all = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, wait(bb, parity, ctl)); };
+            constexpr uint32_t idS = Type<T>::id(kRows, kKeys, false);
+            constexpr uint32_t idPV = Type<T>::id(kRows, D, true);
+            int nk = 0, nv = 0;                           // K and V tiles passed (ring slots, phases)
+            int pcnt = 0, qcnt = 0, ocnt = 0, turn = 0;   // P tiles, Q tiles, results of this row tile; turns
+            bool ok = true;
+            auto wait_k = [&] { return wait_all(bar(K::KFULL + nk % NSK), (nk / NSK) & 1); };
+            // S_i of the next K tile (waited for); last: the item's last, after which Q_i is free
+            auto issue_s = [&](bool last) {
+                const int sk = nk++ % NSK;
+                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::TILE, 0);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint32_t off = (k / 4) * K::SLAB + (k % 4) * 32;
-                            mma_bf16(s_i, desc_sw128(qbase + off, 16, 1024), desc_sw128(kbase + off, 16, 1024), idS,
-                                     k > 0 ? 1u : 0u);
-                        }
-                        mma_commit(bar(K::SFULL + i));
-                        mma_commit(bar(K::KEMPTY + sk));
-                        if (x + 1 == tiles) mma_commit(bar(K::QEMPTY + i));
-                        return true;
-                    };
-                    if (!(ok = issue_s(0))) break;
-                    // keys that any row of this row tile sees, from the piece's first tile on
-                    const int last = p.s.L - p.s.Q + p.q0 + min(p.nq, (i + 1) * a.pb) - p.t0 * kKeys;
-                    for (int x = 0; x < tiles && ok; ++x) {
-                        const int sv = (n + x) % NSV;
-                        const uint32_t vbase = sb + K::OFF_V + sv * K::TILE;
-                        const int steps = min(max((last - x * kKeys + 15) / 16, 1), kKeys / 16);   // 16 keys an MMA
-                        auto pv = [&](int k0, int k1) {
-                            for (int k = k0; k < k1; ++k)
-                                mma_bf16_tmem_a(o_i, s_i + k * 8, desc_sw128(vbase + k * 2048, K::SLAB, 1024), idPV,
-                                                x > 0 || k > 0 ? 1u : 0u);
-                        };
-                        if (!(ok = wait(bar(K::VREADY + sv), ((n + x) / NSV) & 1, ctl))) break;
-                        if (!(ok = wait(bar(K::PFA + i), scnt & 1, ctl))) break;
-                        // the first PV of an item starts O_i afresh: the last one's result has been read
-                        if (x == 0 && ocnt > 0 && !(ok = wait(bar(K::OFREE + i), (ocnt - 1) & 1, ctl))) break;
-                        tc_fence_after();
-                        pv(0, min(steps, 4));
-                        if (!(ok = wait(bar(K::PFB + i), scnt & 1, ctl))) break;
-                        ++scnt;
-                        tc_fence_after();
-                        pv(4, steps);
-                        mma_commit(bar(K::VEMPTY + sv));
-                        if (x + 1 < tiles) ok = issue_s(x + 1);
-                        else mma_commit(bar(K::ODONE + i));
-                    }
-                    ++ocnt;
-                    n += tiles;
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * K::SLAB + (k % 4) * 32;
+                    mma_ss(lead, s_i, desc_sw128(qbase + off, 16, 1024), desc_sw128(kbase + off, 16, 1024), idS,
+                           k > 0 ? 1u : 0u);
                 }
-                mma_commit(bar(K::DRAIN));
-                // every MMA issued has completed before TMEM is freed
-                const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
-                wait(bar(K::DRAIN), 0, drain);
+                commit(lead, bar(K::SFULL + i));
+                commit(lead, bar(K::KEMPTY + sk));
+                if (last) commit(lead, bar(K::QEMPTY + i));
+            };
+            int n = 0;
+            auto next = [&](Piece& x) {                   // the next piece with tiles
+                for (;; ++n) {
+                    const Piece* at = piece_at(n);
+                    if (!at || at->end) return false;
+                    x = *at;
+                    release(n);
+                    if (x.t1 > x.t0) break;
+                }
+                ++n;
+                return true;
+            };
+            Piece p;
+            bool more = next(p), begun = false;           // begun: this piece's first S is issued
+            while (more && ok) {
+                const int tiles = p.t1 - p.t0;
+                if (i == 1 && !p.two) {
+                    // no rows here: release this row tile's share of every slot once its tile has landed
+                    for (int x = 0; x < tiles && ok; ++x, ++nk, ++nv) {
+                        if (!(ok = wait_k())) break;
+                        if (lead) mbar_arrive(bar(K::KEMPTY + nk % NSK));
+                        if (!(ok = wait_all(bar(K::VREADY + nv % NSV), (nv / NSV) & 1))) break;
+                        if (lead) mbar_arrive(bar(K::VEMPTY + nv % NSV));
+                    }
+                    more = next(p);
+                    begun = false;
+                    continue;
+                }
+                if (!begun) {
+                    if (!(ok = wait_all(bar(K::QFULL + i), qcnt & 1)) || !(ok = wait_k())) break;
+                    ++qcnt;
+                    tc_fence_after();
+                    issue_s(tiles == 1);
+                }
+                // keys that any row of this row tile sees, from the piece's first tile on
+                const int last = p.s.L - p.s.Q + p.q0 + min(p.nq, (i + 1) * a.pb) - p.t0 * kKeys;
+                Piece q;
+                bool after = false, follow = false;       // another piece; this row tile has rows in it
+                for (int x = 0; x < tiles; ++x, ++nv, ++pcnt) {
+                    const bool end = x + 1 == tiles;
+                    if (end) {
+                        after = next(q);
+                        follow = after && (i == 0 || q.two);
+                    }
+                    const int sv = nv % NSV;
+                    const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::TILE, 0);
+                    const int steps = min(max((last - x * kKeys + 15) / 16, 1), kKeys / 16);   // 16 keys an MMA
+                    auto pv = [&](int k0) {               // 64 keys (unrolled: 12 MMAs issue in 740 clocks, rolled in 1000)
+                        if (steps == kKeys / 16) {
+#pragma unroll
+                            for (int k = k0; k < k0 + 4; ++k)
+                                mma_ts(lead, o_i, s_i + k * 8, desc_sw128(vbase + k * 2048, K::SLAB, 1024), idPV,
+                                       x > 0 || k > 0 ? 1u : 0u);
+                        } else {
+#pragma unroll 1
+                            for (int k = k0; k < min(k0 + 4, steps); ++k)
+                                mma_ts(lead, o_i, s_i + k * 8, desc_sw128(vbase + k * 2048, K::SLAB, 1024), idPV,
+                                       x > 0 || k > 0 ? 1u : 0u);
+                        }
+                    };
+                    if (!(ok = wait_all(bar(K::VREADY + sv), (nv / NSV) & 1))) break;
+                    // an item's first PV starts O_i afresh: the last one's result has been read
+                    if (x == 0 && ocnt > 0 && !(ok = wait_all(bar(K::OFREE + i), (ocnt - 1) & 1))) break;
+                    // (what the turn needs is waited for before P, off the path from P to the next S)
+                    if (follow && !(ok = wait_all(bar(K::QFULL + i), qcnt & 1))) break;
+                    if ((!end || follow) && !(ok = wait_k())) break;
+                    if (!(ok = wait_all(bar(K::PFA + i), pcnt & 1))) break;
+                    tc_fence_after();
+                    pv(0);
+                    commit(lead, bar(K::PVA + i));
+                    if (p.two) {
+                        if ((i == 1 || turn > 0) && !(ok = wait_all(bar(K::TURN + i), (i == 1 ? turn : turn - 1) & 1))) break;
+                        ++turn;
+                    }
+                    if (!(ok = wait_all(bar(K::PFB + i), pcnt & 1))) break;
+                    tc_fence_after();
+                    pv(4);
+                    if (end) commit(lead, bar(K::ODONE + i));
+                    commit(lead, bar(K::VEMPTY + sv));
+                    if (!end) issue_s(x + 2 == tiles);
+                    else if (follow) {
+                        ++qcnt;
+                        issue_s(q.t1 - q.t0 == 1);
+                    }
+                    if (p.two && lead) mbar_arrive(bar(K::TURN + 1 - i));
+                }
+                if (!ok) break;
+                ++ocnt;
+                more = after;
+                begun = follow;
+                p = q;
             }
+            commit(lead, bar(K::DRAIN));
+            // every MMA issued has completed before TMEM is freed
+            const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
+            wait(bar(K::DRAIN), 0, drain);
             __syncwarp();
-        } else {
+        } else if (warp == kGuard) {
             // -------------------------------------------- V guard
             int n = 0, item = 0;
             bool ok = true;
-            while (ok && w.next(a, table, p)) {
+            for (int m = 0; ok; ++m) {
+                const Piece* at = piece_at(m);
+                if (!at || at->end) break;
+                const Piece p = *at;
+                release(m);
                 const int it = item;
                 item += p.t1 > p.t0;
                 // keys past `all` are not seen by every row of the item; L and beyond by none
@@ -800,12 +1055,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         uint8_t* base = smem + K::OFF_V + sv * K::TILE;
                         for (int s = 0; s < K::SLABS; ++s)
                             for (int x = r0 * 8 + lane; x < kKeys * 8; x += 32) {
-                                uint4* at = reinterpret_cast<uint4*>(base + s * K::SLAB + x * 16);
+                                uint4* e16 = reinterpret_cast<uint4*>(base + s * K::SLAB + x * 16);
                                 if (x / 8 >= r1) {
-                                    *at = make_uint4(0, 0, 0, 0);
+                                    *e16 = make_uint4(0, 0, 0, 0);
                                     continue;
                                 }
-                                uint4 v = *at;
+                                uint4 v = *e16;
                                 uint32_t* e = reinterpret_cast<uint32_t*>(&v);
                                 bool bad = false;
 #pragma unroll
@@ -821,7 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                                     }
                                 }
                                 if (bad) {
-                                    *at = v;
+                                    *e16 = v;
                                     found = true;
                                 }
                             }
@@ -839,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     __syncwarp();
     tc_fence_before();
     cta_bar_sync();
-    if (warp == 11) {
+    if (warp == kGuard) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, K::TMEM_COLS);
@@ -854,12 +1109,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Arg a, int chunk, int grid) {
     __shared__ int tab[3 * (kTable + 1)];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Table table{tab, chunk};
     griddep_wait();
-    if (tid < kTable) build_table(a, tab, chunk, tid, false);
-    __syncthreads();
-    if (warp == 0) sum_table(tab, lane);
+    if (warp == 0) {
+        build_table(a, tab, chunk, lane, false);
+        __syncwarp();
+        sum_table(tab, lane);
+    }
     __syncthreads();
     const int total = tab[kTable], ctas = split_ctas(total, grid), c = blockIdx.x;
     if (c >= ctas || total == 0) return;
@@ -1005,6 +1262,7 @@ cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* 
     a.Hkv = Hkv;
     a.group = G;
     a.scale_log2 = scale * kLog2e;
+    a.wide = (((uintptr_t)a.out.data | (uintptr_t)a.out.ts | (uintptr_t)a.out.hs) & 31) == 0;
     // at most this many items (their number depends on the lengths, which the host does not see)
     const int64_t per = 2 * a.pb;
     const int64_t items = Hkv * std::min<int64_t>((int64_t)num_seqs * ((max_q_len + per - 1) / per),
