@@ -449,7 +449,7 @@ PKV_API pkv_status pkv_rope_init(pkv_rope* rope, int32_t rotary_dim, int32_t int
  *   q_weight, k_weight  device [head_dim], 16-byte aligned, or NULL
  *   norm_eps       < 0: no norm (weights must be NULL)
  *
- * One launch, one CTA per token; num_tokens <= 2^31 - 1.  It lets the next
+ * One launch; num_tokens <= 2^31 - 1.  It lets the next
  * kernel on the stream start only once it has completed (an attention reads
  * q before its own dependency wait).
  */

@@ -369,14 +369,21 @@ class Rope:
         return list(self.desc.inv_freq[:self.rotary_dim // 2])
 
 
-def _row_view(t, name, dtype, device, tokens, dim, heads=None):
-    """pkv_rows of t [tokens, heads, dim] (any strides but the last)."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} must be [{tokens}, {'heads' if heads is None else heads}, {dim}], got {list(shape)}")
-    if t.dtype is not dtype or strides[2] != 1 or t.get_device() != device:
-        raise ValueError(f"{name} must be {dtype} on the same GPU with consecutive elements in a row")
+def _row_view(t, name, dtype, device, shape):
+    """pkv_rows of t, of the given [tokens, heads, dim] (any strides but the last)."""
+    strides = t.stride()
+    if t.shape != shape or t.dtype is not dtype or strides[2] != 1 or t.get_device() != device:
+        raise ValueError(f"{name} must be {list(shape)} in {dtype} on the same GPU, with consecutive elements in a "
+                         f"row: got {list(t.shape)} in {t.dtype}, strides {list(strides)}")
     return _ROWS.pack(t.data_ptr(), strides[0], strides[1], shape[1])
+
+
+def _row_output(t, name, like, dtype, device, shape):
+    """(output, its pkv_rows): t, or a new contiguous tensor of the shape."""
+    if t is not None:
+        return t, _row_view(t, name, dtype, device, shape)
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    return t, _ROWS.pack(t.data_ptr(), shape[1] * shape[2], shape[2], shape[1])
 
 
 def _vector(t, name, dtype, device, numel):
@@ -400,16 +407,33 @@ def _device_of(t, name):
     return device
 
 
-def _call(fn, what, device, stream, *args):
-    """fn(*args, stream) with the tensors' device current and, unless one is
-    given, on that device's current stream."""
+def _call(name, device, stream, *args):
+    """Entry point `name` with the tensors' device current and, unless a stream
+    is given, on that device's current stream."""
+    fn = getattr(_lib or lib(), name)
     if device != torch.cuda.current_device():
         with torch.cuda.device(device):
             st = fn(*args, _stream(stream))
     else:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else int(stream.cuda_stream))
     if st != 0:
-        raise PagedKVError(st, what)
+        raise PagedKVError(st, name)
+
+
+def _check_norm_rope(q_weight, k_weight, eps, rope, positions):
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights without eps")
+    elif not eps >= 0:
+        raise ValueError("eps must not be negative")
+    if rope is not None and positions is None:
+        raise ValueError("rope without positions")
+
+
+def _check_cache_device(cache, device):
+    for t in (cache.k, cache.v, cache.k_scales, cache.v_scales):
+        if t is not None and t.get_device() != device:
+            raise ValueError("the cache must be on the same GPU as the other tensors")
 
 
 def qk_norm_rope(q, k=None, positions=None, rope: Rope | None = None, q_weight=None, k_weight=None, eps=None,
@@ -418,27 +442,21 @@ def qk_norm_rope(q, k=None, positions=None, rope: Rope | None = None, q_weight=N
     (views of a fused projection are fine; bf16, fp16 or fp32), normed per head
     where eps is given, rotated at int32 positions [T] where rope is.  Returns
     (q_out, k_out): new tensors unless given (q_out=q: in place)."""
-    device, dtype = _device_of(q, "q"), q.dtype
-    if q.dim() != 3 or dtype not in _ROW_DTYPES:
+    device, dtype, shape = _device_of(q, "q"), q.dtype, q.shape
+    if len(shape) != 3 or dtype not in _ROW_DTYPES:
         raise ValueError("q must be [tokens, heads, head_dim] in bfloat16, float16 or float32")
-    T, _, D = q.shape
-    if q_out is None:
-        q_out = q.new_empty(q.shape)
-    if k is not None and k_out is None:
-        k_out = k.new_empty(k.shape)
-    if k is None and k_out is not None:
+    T, _, D = shape
+    _check_norm_rope(q_weight, k_weight, eps, rope, positions)
+    qr = _row_view(q, "q", dtype, device, shape)
+    q_out, qo = _row_output(q_out, "q_out", q, dtype, device, shape)
+    kr = ko = None
+    if k is not None:
+        kshape = (T, k.shape[1] if k.dim() == 3 else 0, D)
+        kr = _row_view(k, "k", dtype, device, kshape)
+        k_out, ko = _row_output(k_out, "k_out", k, dtype, device, kshape)
+    elif k_out is not None:
         raise ValueError("k_out without k")
-    if eps is None and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights without eps")
-    if eps is not None and not eps >= 0:
-        raise ValueError("eps must not be negative")
-    if rope is not None and positions is None:
-        raise ValueError("rope without positions")
-    _call(lib().pkv_qk_norm_rope, "pkv_qk_norm_rope", device, stream,
-          _row_view(q, "q", dtype, device, T, D), _row_view(q_out, "q_out", dtype, device, T, D, q.shape[1]),
-          None if k is None else _row_view(k, "k", dtype, device, T, D),
-          None if k is None else _row_view(k_out, "k_out", dtype, device, T, D, k.shape[1]),
-          _ROW_DTYPES[dtype], D, T,
+    _call("pkv_qk_norm_rope", device, stream, qr, qo, kr, ko, _ROW_DTYPES[dtype], D, T,
           None if positions is None else _vector(positions, "positions", torch.int32, device, T),
           None if rope is None else rope._ref, inverse, _weight(q_weight, "q_weight", dtype, device, D),
           _weight(k_weight, "k_weight", dtype, device, D), -1.0 if eps is None else eps)
@@ -453,25 +471,20 @@ def append_norm_rope(cache: PagedKVCache, q, k, v, slot_mapping, positions=None,
     Returns q_out (a new tensor unless given; None for q=None).  k_out, if
     given, receives the normed and rotated key rows too."""
     device, bf16 = _device_of(k, "k"), torch.bfloat16
-    T, H, D = k.shape[0], cache.num_kv_heads, cache.head_dim
-    for t in (cache.k, cache.v, cache.k_scales, cache.v_scales):
-        if t is not None and t.get_device() != device:
-            raise ValueError("the cache must be on the rows' GPU")
-    if q is not None and q_out is None:
-        q_out = q.new_empty(q.shape)
-    if q is None and q_out is not None:
+    T, D = k.shape[0], cache.head_dim
+    kshape = (T, cache.num_kv_heads, D)
+    _check_cache_device(cache, device)
+    _check_norm_rope(q_weight, k_weight, eps, rope, positions)
+    qr = qo = None
+    if q is not None:
+        qshape = (T, q.shape[1] if q.dim() == 3 else 0, D)
+        qr = _row_view(q, "q", bf16, device, qshape)
+        q_out, qo = _row_output(q_out, "q_out", q, bf16, device, qshape)
+    elif q_out is not None:
         raise ValueError("q_out without q")
-    if eps is None and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights without eps")
-    if eps is not None and not eps >= 0:
-        raise ValueError("eps must not be negative")
-    if rope is not None and positions is None:
-        raise ValueError("rope without positions")
-    _call(lib().pkv_paged_kv_append_norm_rope, "pkv_paged_kv_append_norm_rope", device, stream,
-          ctypes.byref(cache.desc()), None if q is None else _row_view(q, "q", bf16, device, T, D),
-          None if q is None else _row_view(q_out, "q_out", bf16, device, T, D, q.shape[1]),
-          _row_view(k, "k", bf16, device, T, D, H), _row_view(v, "v", bf16, device, T, D, H),
-          None if k_out is None else _row_view(k_out, "k_out", bf16, device, T, D, H),
+    _call("pkv_paged_kv_append_norm_rope", device, stream, ctypes.byref(cache.desc()), qr, qo,
+          _row_view(k, "k", bf16, device, kshape), _row_view(v, "v", bf16, device, kshape),
+          None if k_out is None else _row_view(k_out, "k_out", bf16, device, kshape),
           _vector(slot_mapping, "slot_mapping", torch.int64, device, T), T,
           None if positions is None else _vector(positions, "positions", torch.int32, device, T),
           None if rope is None else rope._ref, _weight(q_weight, "q_weight", bf16, device, D),
@@ -488,24 +501,19 @@ def read_cache(cache: PagedKVCache, block_tables, lens, num_rows: int, starts=No
     device, n = _device_of(block_tables, "block_tables"), lens.numel()
     shape = (int(num_rows), cache.num_kv_heads, cache.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=block_tables.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=block_tables.device)
+        k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=block_tables.device)
     dtype = k_out.dtype
     if dtype not in _ROW_DTYPES:
         raise ValueError("rows must be bfloat16, float16 or float32")
-    for t in (cache.k, cache.v, cache.k_scales, cache.v_scales):
-        if t is not None and t.get_device() != device:
-            raise ValueError("the cache must be on the block tables' GPU")
+    v_out, vr = _row_output(v_out, "v_out", k_out, dtype, device, shape)
+    _check_cache_device(cache, device)
     if block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    _call(lib().pkv_paged_kv_read, "pkv_paged_kv_read", device, stream, ctypes.byref(cache.desc()),
+    _call("pkv_paged_kv_read", device, stream, ctypes.byref(cache.desc()),
           _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()), block_tables.shape[1],
           None if starts is None else _vector(starts, "starts", torch.int32, device, n),
-          _vector(lens, "lens", torch.int32, device, n), n, shape[0],
-          _row_view(k_out, "k_out", dtype, device, shape[0], shape[2], shape[1]),
-          _row_view(v_out, "v_out", dtype, device, shape[0], shape[2], shape[1]), _ROW_DTYPES[dtype],
-          _error_word(device_error, device))
+          _vector(lens, "lens", torch.int32, device, n), n, shape[0], _row_view(k_out, "k_out", dtype, device, shape),
+          vr, _ROW_DTYPES[dtype], _error_word(device_error, device))
     return k_out, v_out
 
 
@@ -530,21 +538,20 @@ def prompt_attention(q, k, v, q_lens, kv_lens, max_q_len: int, scale: float, out
     fine).  Returns (out, lse): new tensors unless given; lse fp32 [Tq, Hq],
     natural logarithm.  With starts, rows outside every sequence are not
     written."""
-    device, dtype = _device_of(q, "q"), q.dtype
-    if q.dim() != 3 or dtype not in (torch.bfloat16, torch.float16):
+    device, dtype, shape = _device_of(q, "q"), q.dtype, q.shape
+    if len(shape) != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
         raise ValueError("q must be [rows, heads, head_dim] in bfloat16 or float16")
-    (Tq, Hq, D), Tk, n = q.shape, k.shape[0], q_lens.numel()
-    if out is None:
-        out = q.new_empty(q.shape)
+    (Tq, Hq, D), n = shape, q_lens.numel()
+    kshape = (k.shape[0], k.shape[1] if k.dim() == 3 else 0, D)
+    qr, kr = _row_view(q, "q", dtype, device, shape), _row_view(k, "k", dtype, device, kshape)
+    vr = _row_view(v, "v", dtype, device, kshape)
+    out, orow = _row_output(out, "out", q, dtype, device, shape)
     if lse is None:
         lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
     if workspace is not None and (workspace.get_device() != device or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous on the same GPU")
-    kr = _row_view(k, "k", dtype, device, Tk, D)
-    _call(lib().pkv_prompt_attention, "pkv_prompt_attention", device, stream,
-          _row_view(q, "q", dtype, device, Tq, D), kr, _row_view(v, "v", dtype, device, Tk, D, k.shape[1]),
-          _row_view(out, "out", dtype, device, Tq, D, Hq), _vector(lse, "lse", torch.float32, device, Tq * Hq),
-          _ROW_DTYPES[dtype], D, Tq, Tk, _vector(q_lens, "q_lens", torch.int32, device, n),
+    _call("pkv_prompt_attention", device, stream, qr, kr, vr, orow, _vector(lse, "lse", torch.float32, device, Tq * Hq),
+          _ROW_DTYPES[dtype], D, Tq, kshape[0], _vector(q_lens, "q_lens", torch.int32, device, n),
           _vector(kv_lens, "kv_lens", torch.int32, device, n),
           None if q_starts is None else _vector(q_starts, "q_starts", torch.int64, device, n),
           None if kv_starts is None else _vector(kv_starts, "kv_starts", torch.int64, device, n), n, max_q_len, scale,

@@ -19,8 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["api.cu", "api_noalloc.cu", "api_rows.cu", "append.cu", "attn_simt.cu", "attn_tc.cu", "cache_read.cu",
-           "prefill.cu", "prompt.cu", "qk_norm_rope.cu", "rope_append.cu", "kvmgr.cpp"]
+SOURCES = ["append_norm_rope.cu", "api.cu", "api_noalloc.cu", "api_rows.cu", "append.cu", "attn_simt.cu", "attn_tc.cu",
+           "cache_read.cu", "prefill.cu", "prompt.cu", "qk_norm_rope.cu", "rope_append.cu", "kvmgr.cpp"]
 
 
 def nvcc() -> str:

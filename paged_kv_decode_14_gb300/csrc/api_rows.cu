@@ -10,7 +10,7 @@ int num_sms_current();
 cudaError_t launch_qk_norm_rope(const pkv_rows* q_in, const pkv_rows* q_out, const pkv_rows* k_in,
                                 const pkv_rows* k_out, int dtype, int D, int64_t T, const int32_t* positions,
                                 const pkv_rope* rope, bool inverse, const void* qw, const void* kw, float eps,
-                                cudaStream_t st);
+                                cudaStream_t st, int num_sms);
 cudaError_t launch_append_norm_rope(const pkv_cache& c, const pkv_rows* q_in, const pkv_rows* q_out, const pkv_rows* k,
                                     const pkv_rows* v, const pkv_rows* k_out, const int64_t* slots, int64_t T,
                                     const int32_t* positions, const pkv_rope* rope, const void* qw, const void* kw,
@@ -119,8 +119,10 @@ PKV_API pkv_status pkv_qk_norm_rope(const pkv_rows* q_in, const pkv_rows* q_out,
             return PKV_ERR_INVALID_ARG;
         if (k_in->num_heads != k_out->num_heads) return PKV_ERR_INVALID_ARG;
     }
+    const int sms = num_sms_current();
+    if (sms <= 0) return PKV_ERR_CUDA;
     return launch_qk_norm_rope(q_in, q_out, k_in, k_out, dtype, head_dim, num_tokens, positions, rope, inverse != 0,
-                               q_weight, k_weight, norm_eps, (cudaStream_t)stream) == cudaSuccess
+                               q_weight, k_weight, norm_eps, (cudaStream_t)stream, sms) == cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;
 }

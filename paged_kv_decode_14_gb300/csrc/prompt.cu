@@ -68,6 +68,7 @@ static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOther == 4 * 128, "registe
 constexpr int kProducer = 12, kMma = 13, kGuard = 15;   // (0-7: softmax, 8-11: epilogue)
 constexpr int kTable = 32;                 // entries of the sequence table
 constexpr int kFlags = 8;                  // items whose "non-finite V" flags are kept
+constexpr int kMaxSplit = 160;             // CTAs of a split launch (two workspace slots each)
 constexpr int kPieces = 4;                 // pieces of work the producer may be ahead
 
 struct Arg {
@@ -1219,10 +1220,7 @@ cudaError_t launch(const Arg& a, int chunk, unsigned grid, cudaStream_t st) {
 
 }  // namespace prompt
 
-size_t prompt_workspace_bytes() {
-    const int sms = num_sms_current();
-    return sms > 0 ? (size_t)sms * 2 * prompt::slot_floats(128) * sizeof(float) : 0;
-}
+size_t prompt_workspace_bytes() { return (size_t)prompt::kMaxSplit * 2 * prompt::slot_floats(128) * sizeof(float); }
 
 cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* v, const pkv_rows* out, float* lse,
                           int dtype, int head_dim, int64_t num_q_rows, int64_t num_kv_rows, const int32_t* q_lens,
@@ -1269,7 +1267,7 @@ cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* 
                                                   num_q_rows / per + num_seqs);
     if (items > 0x7fffffff) return cudaErrorInvalidValue;
     a.split = workspace != nullptr && items < 2 * sms && items * ((num_kv_rows + kKeys - 1) / kKeys + 1) < 0x7fffffff;
-    const unsigned grid = (unsigned)(a.split ? sms : std::min<int64_t>(std::max<int64_t>(items, 1), sms));
+    const unsigned grid = (unsigned)(a.split ? std::min(sms, kMaxSplit) : std::min<int64_t>(std::max<int64_t>(items, 1), sms));
     const int chunk = (num_seqs + kTable - 1) / kTable;
     if (dtype == PKV_BF16)
         return head_dim == 128 ? launch<__nv_bfloat16, 128>(a, chunk, grid, st) : launch<__nv_bfloat16, 64>(a, chunk, grid, st);

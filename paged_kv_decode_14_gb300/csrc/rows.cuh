@@ -3,6 +3,9 @@
 // write such rows.
 #pragma once
 
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace pkv {
@@ -100,92 +103,112 @@ struct Chunk<float> {
     }
 };
 
-// Rotates rows held across the GS lanes of a group, CPL chunks of 16 bytes
-// a lane (chunk c of a row: lane c % GS, register set c / GS).
-//   (a, b) -> (a c - b s, b c + a s) for the two elements of a pair.
+// A row is held by a group of GS lanes, two 16-byte chunks a lane: chunk c by
+// lane c % GS in register set c / GS.  (Two chunks: the usual rotate-half pair,
+// which spans half a head, then lies in one lane's two sets.)
+constexpr int kSets = 2;
+template <typename T>
+__host__ __device__ constexpr int lanes_of(int dim) {      // the fewest that hold a row
+    return dim / Chunk<T>::N <= 8 ? 4 : dim / Chunk<T>::N <= 16 ? 8 : dim / Chunk<T>::N <= 32 ? 16 : 32;
+}
+
+// How a kernel rotates: pairs inside a lane's chunk (interleaved), pairs in a
+// lane's two sets (rotate-half over the whole head), pairs whole chunks apart,
+// anything else (or nothing).
+enum Kind { kInside = 0, kSetPairs = 1, kChunks = 2, kGeneral = 3 };
+template <typename T>
+__host__ inline Kind rope_kind(const Rope& r, int lanes) {
+    if (r.pairs == 0) return kGeneral;
+    if (r.interleaved) return kInside;
+    if (r.pairs == lanes * Chunk<T>::N) return kSetPairs;
+    return r.pairs % Chunk<T>::N == 0 ? kChunks : kGeneral;
+}
+
+// Rotates rows: (a, b) -> (a c - b s, b c + a s) for the two elements of a pair.
 // A lane's elements keep their places for every row, so the (cos, sin) of its
-// elements sit in registers for all heads of a token.
-template <typename T, int GS, int CPL>
+// elements are loaded once a token and serve all its heads.
+template <typename T, int GS, int KIND>
 struct Rotator {
     static constexpr int N = Chunk<T>::N;
-    float c[CPL][N], s[CPL][N];       // s: negative for a pair's first element
-    int lane, pairs, rd;
-    bool inter, aligned;              // aligned: a pair's two elements lie whole chunks apart
+    static constexpr int S = KIND == kSetPairs ? 1 : kSets, M = KIND == kInside ? N / 2 : N;   // (cos, sin) held
+    float c[S][M], s[S][M];           // s: negative for a pair's first element (kInside, kSetPairs: the pair's)
+    int lane, pairs;
+    int part[kSets];                  // rotated elements of a chunk
 
-    // cs: (cos, sin) of the token's pairs in shared memory
-    __device__ __forceinline__ void load(const Rope& r, const float2* cs, int lane_) {
+    __device__ __forceinline__ void init(const Rope& r, int lane_) {
         lane = lane_;
         pairs = r.pairs;
-        rd = 2 * r.pairs;
-        inter = r.interleaved != 0;
-        aligned = pairs % N == 0;
 #pragma unroll
-        for (int j = 0; j < CPL; ++j)
+        for (int j = 0; j < kSets; ++j) part[j] = min(max(2 * pairs - (lane + j * GS) * N, 0), N);
+    }
+    // cs: (cos, sin) of a token's pairs
+    __device__ __forceinline__ void load(const float2* cs) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const int d = (lane + j * GS) * N + e;
-                c[j][e] = 1.f;
-                s[j][e] = 0.f;
-                if (d < rd) {
-                    const int i = inter ? d >> 1 : d < pairs ? d : d - pairs;
-                    const bool first = inter ? !(d & 1) : d < pairs;
-                    const float2 v = cs[i];
-                    c[j][e] = v.x;
-                    s[j][e] = first ? -v.y : v.y;
-                }
+        for (int j = 0; j < S; ++j)
+#pragma unroll
+            for (int e = 0; e < M; ++e) {
+                const int el = KIND == kInside ? 2 * e : e;
+                if (KIND != kSetPairs && el >= part[j]) continue;
+                const int d = (lane + j * GS) * N + el;
+                const bool first = KIND == kInside || KIND == kSetPairs || d < pairs;
+                const float2 v = cs[KIND == kInside ? d >> 1 : first ? d : d - pairs];
+                c[j][e] = v.x;
+                s[j][e] = first && (KIND == kChunks || KIND == kGeneral) ? -v.y : v.y;
             }
     }
-    // stage: this group's [rows of D floats] in shared memory (unaligned rotate-half pairs only)
-    __device__ __forceinline__ void apply(float (&x)[CPL][N], float* stage) const {
-        if (rd == 0) return;
-        if (inter) {
+    // stage: this group's row of D floats in shared memory (kGeneral, which covers rotate-half only)
+    __device__ __forceinline__ void apply(float (&x)[kSets][N], float* stage) const {
+        if constexpr (KIND == kInside) {
 #pragma unroll
-            for (int j = 0; j < CPL; ++j)
+            for (int j = 0; j < kSets; ++j)
 #pragma unroll
                 for (int e = 0; e < N; e += 2) {
-                    if ((lane + j * GS) * N + e >= rd) continue;
+                    if (e >= part[j]) continue;
                     const float a = x[j][e], b = x[j][e + 1];
-                    x[j][e] = fmaf(a, c[j][e], b * s[j][e]);
-                    x[j][e + 1] = fmaf(b, c[j][e + 1], a * s[j][e + 1]);
+                    x[j][e] = fmaf(a, c[j][e / 2], -b * s[j][e / 2]);
+                    x[j][e + 1] = fmaf(b, c[j][e / 2], a * s[j][e / 2]);
                 }
-        } else if (aligned) {
-            const int pc = pairs / N;                      // chunks between a pair's elements
-            float y[CPL][N];
+        } else if constexpr (KIND == kSetPairs) {
 #pragma unroll
-            for (int j = 0; j < CPL; ++j) {
+            for (int e = 0; e < N; ++e) {
+                const float a = x[0][e], b = x[1][e];
+                x[0][e] = fmaf(a, c[0][e], -b * s[0][e]);
+                x[1][e] = fmaf(b, c[0][e], a * s[0][e]);
+            }
+        } else if constexpr (KIND == kChunks) {
+            const int pc = pairs / N;                      // chunks between a pair's elements
+            float y[kSets][N];
+#pragma unroll
+            for (int j = 0; j < kSets; ++j) {
                 const int ch = lane + j * GS, p = ch < pc ? ch + pc : ch - pc;   // the partner chunk
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    if constexpr (CPL == 1) {
-                        y[j][e] = __shfl_sync(0xffffffffu, x[0][e], p & (GS - 1), GS);
-                    } else {
-                        const float u = __shfl_sync(0xffffffffu, x[0][e], p & (GS - 1), GS);
-                        const float v = __shfl_sync(0xffffffffu, x[1][e], p & (GS - 1), GS);
-                        y[j][e] = (p / GS) & 1 ? v : u;
-                    }
+                    const float u = __shfl_sync(0xffffffffu, x[0][e], p & (GS - 1), GS);
+                    const float v = __shfl_sync(0xffffffffu, x[1][e], p & (GS - 1), GS);
+                    y[j][e] = (p / GS) & 1 ? v : u;
                 }
             }
 #pragma unroll
-            for (int j = 0; j < CPL; ++j)
-                if (lane + j * GS < 2 * pc)
+            for (int j = 0; j < kSets; ++j)
+                if (part[j] > 0)                           // (whole chunks)
 #pragma unroll
                     for (int e = 0; e < N; ++e) x[j][e] = fmaf(x[j][e], c[j][e], y[j][e] * s[j][e]);
         } else {
+            if (pairs == 0) return;
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < CPL; ++j)
+            for (int j = 0; j < kSets; ++j)
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const int d = (lane + j * GS) * N + e;
-                    if (d < rd) stage[d] = x[j][e];
-                }
+                for (int e = 0; e < N; ++e)
+                    if (e < part[j]) stage[(lane + j * GS) * N + e] = x[j][e];
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < CPL; ++j)
+            for (int j = 0; j < kSets; ++j)
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
+                    if (e >= part[j]) continue;
                     const int d = (lane + j * GS) * N + e;
-                    if (d < rd) x[j][e] = fmaf(x[j][e], c[j][e], stage[d < pairs ? d + pairs : d - pairs] * s[j][e]);
+                    x[j][e] = fmaf(x[j][e], c[j][e], stage[d < pairs ? d + pairs : d - pairs] * s[j][e]);
                 }
         }
     }
@@ -193,20 +216,21 @@ struct Rotator {
 
 // x *= w / sqrt(mean(x^2) + eps) over the row held by a group of GS lanes
 // (lanes past the row hold zeros); sums and statistics in fp32.
-template <typename T, int GS, int CPL>
-__device__ __forceinline__ void rms_norm(float (&x)[CPL][Chunk<T>::N], const uint4 (&w)[CPL], bool weighted, float eps,
-                                         float inv_dim) {
+template <typename T, int GS>
+__device__ __forceinline__ void rms_norm(float (&x)[kSets][Chunk<T>::N], const uint4 (&w)[kSets], bool weighted,
+                                         float eps, float inv_dim) {
     constexpr int N = Chunk<T>::N;
-    float ss = 0.f;
+    float ss[kSets] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < CPL; ++j)
+    for (int e = 0; e < N; ++e)
 #pragma unroll
-        for (int e = 0; e < N; ++e) ss = fmaf(x[j][e], x[j][e], ss);
+        for (int j = 0; j < kSets; ++j) ss[j] = fmaf(x[j][e], x[j][e], ss[j]);
+    float sum = ss[0] + ss[1];
 #pragma unroll
-    for (int o = GS / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, GS);
-    const float inv = rsqrtf(fmaf(ss, inv_dim, eps));
+    for (int o = GS / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, GS);
+    const float inv = rsqrtf(fmaf(sum, inv_dim, eps));
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) {
+    for (int j = 0; j < kSets; ++j) {
         float g[N];
         if (weighted) Chunk<T>::unpack(w[j], g);
 #pragma unroll
@@ -233,6 +257,191 @@ __host__ inline Rope rope_arg(const pkv_rope* r, bool negate) {
         a.turn[i] = f >= 1.0 ? 0 : (uint64_t)(int64_t)(f * 0x1p63) << 1;
     }
     return a;
+}
+
+// ------------------------------------------------------------------ a warp's share of the rows
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAhead = 4;                 // row groups whose loads a warp has in flight
+constexpr int kWarpsPerSm = 32;
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+// A warp's shared memory: the ring of row groups in flight, the (cos, sin) of
+// one token's pairs, and (unaligned rotate-half pairs) a group's rows in fp32.
+constexpr int kRing = kAhead * kSets * 512;
+template <typename T, int GS>
+__host__ inline size_t rows_smem(const Rope& r, int D) {
+    const size_t stage = r.pairs > 0 && !r.interleaved && r.pairs % Chunk<T>::N ? (size_t)(32 / GS) * D * 4 : 0;
+    return kWarps * (kRing + (((size_t)r.pairs * 8 + 15) / 16 * 16) + (stage + 15) / 16 * 16);
+}
+
+// Where a warp is in its share: a group of 32 / GS rows of one tensor's heads,
+// of one token.  A token's groups are q's, then k's.
+template <int GS>
+struct Cursor {
+    static constexpr int RPW = 32 / GS;
+    const uint8_t* p;       // this lane's first 16 bytes of its row
+    int64_t t;
+    int step;               // bytes to the next group's row (head strides below 2^31 / RPW)
+    int rows;               // heads from this lane's row on (<= 0: none)
+    int left;               // groups left of this tensor's heads
+    bool k;                 // in k's heads
+    __device__ __forceinline__ void open(const View& v, int64_t t_, int g, int l, int sub) {
+        t = t_;
+        p = v.row(t, g * RPW + sub) + l * 16;
+        step = (int)(v.hs * RPW);
+        rows = v.heads - g * RPW - sub;
+        left = (v.heads + RPW - 1) / RPW - g;
+    }
+    __device__ __forceinline__ void start(const View& q, const View& kk, int64_t u, int l, int sub) {
+        const int gq = (q.heads + RPW - 1) / RPW, gk = (kk.heads + RPW - 1) / RPW;
+        const int64_t tt = u / (gq + gk);
+        const int g = (int)(u - tt * (gq + gk));
+        k = g >= gq;
+        open(k ? kk : q, tt, k ? g - gq : g, l, sub);
+    }
+    __device__ __forceinline__ void next(const View& q, const View& kk, int l, int sub) {
+        p += step;
+        rows -= RPW;
+        if (--left > 0) return;
+        const bool to_k = !k && kk.heads > 0;
+        const int64_t tt = to_k ? t : t + 1;
+        k = to_k;
+        open(to_k ? kk : q, tt, 0, l, sub);
+    }
+};
+
+// The norm and rotation of one warp's share of the rows, GS lanes a row: row
+// groups [u, end) of all tokens' groups laid end to end.  A lane copies its own
+// 16 bytes of a row to shared memory kAhead groups before it uses them
+// (cp.async), so the bytes in flight do not cost registers and warps never wait
+// for each other.  What bounds it beside HBM is the instructions of a group, so
+// pointers step from head to head.  (8192 tokens of 40 heads of 128 bf16, 168
+// MB: direct loads, a CTA a token with its angles behind a barrier, 52 us; this
+// with the addresses computed from scratch, 39 us.)
+template <typename T, int GS, int KIND, bool NORM>
+__device__ __forceinline__ void warp_rows(const View& qi, const View& qo, const View& ki, const View& ko, const T* qw,
+                                          const T* kw, float eps, int D, const Rope& rope,
+                                          const int32_t* positions, int64_t tokens, int64_t u, int64_t end,
+                                          uint8_t* smem) {
+    constexpr int N = Chunk<T>::N;
+    if (u >= end) return;
+    const int lane = threadIdx.x & 31, l = lane & (GS - 1), sub = lane / GS;
+    const int nch = D / N;
+    float2* cs = reinterpret_cast<float2*>(smem + kRing);
+    float* stage = reinterpret_cast<float*>(smem + kRing + (rope.pairs * 8 + 15) / 16 * 16) + sub * D;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + lane * 16, ring_end = ring + kRing;
+    Cursor<GS> from, to;
+    from.start(qi, ki, u, l, sub);
+    to.start(qo, ko, u, l, sub);
+    const int count = (int)(end - u);
+    int fetched = 0;
+    uint32_t fill = ring, use = ring;
+    auto fetch = [&] {
+        if (fetched < count) {
+#pragma unroll
+            for (int j = 0; j < kSets; ++j)
+                if (l + j * GS < nch && from.rows > 0) cp_async_16(fill + j * 512, from.p + j * GS * 16);
+            ++fetched;
+            from.next(qi, ki, l, sub);
+        }
+        cp_async_commit();
+        fill += kSets * 512;
+        if (fill == ring_end) fill = ring;
+    };
+#pragma unroll 1
+    for (int x = 0; x < kAhead; ++x) fetch();
+    uint4 wq[kSets], wk[kSets];
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+        const int ch = l + j * GS;
+        wq[j] = NORM && qw && ch < nch ? *reinterpret_cast<const uint4*>(qw + ch * N) : make_uint4(0, 0, 0, 0);
+        wk[j] = NORM && kw && ch < nch ? *reinterpret_cast<const uint4*>(kw + ch * N) : make_uint4(0, 0, 0, 0);
+    }
+    Rotator<T, GS, KIND> rot;
+    rot.init(rope, l);
+    const float inv_dim = 1.f / (float)D;
+    int64_t have = -1;                                     // the token whose angles rot holds
+    int pos = rope.pairs > 0 ? positions[to.t] : 0;
+    for (int n = 0; n < count; ++n) {
+        if (rope.pairs > 0 && to.t != have) {
+            have = to.t;
+            __syncwarp();
+            for (int i = lane; i < rope.pairs; i += 32) cs[i] = angle(rope, i, pos);
+            __syncwarp();
+            rot.load(cs);
+            if (have + 1 < tokens) pos = positions[have + 1];   // (the next token's, long before it is needed)
+        }
+        cp_async_wait<kAhead - 1>();                       // (a lane reads what it copied itself)
+        float x[kSets][N];
+#pragma unroll
+        for (int j = 0; j < kSets; ++j) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (l + j * GS < nch && to.rows > 0)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(use + j * 512)
+                             : "memory");
+            Chunk<T>::unpack(v, x[j]);
+        }
+        if constexpr (NORM) rms_norm<T, GS>(x, to.k ? wk : wq, (to.k ? kw : qw) != nullptr, eps, inv_dim);
+        rot.apply(x, stage);
+#pragma unroll
+        for (int j = 0; j < kSets; ++j)
+            if (l + j * GS < nch && to.rows > 0)
+                *reinterpret_cast<uint4*>(const_cast<uint8_t*>(to.p) + j * GS * 16) = Chunk<T>::pack(x[j]);
+        use += kSets * 512;
+        if (use == ring_end) use = ring;
+        to.next(qo, ko, l, sub);
+        fetch();
+    }
+    cp_async_wait<0>();
+}
+
+// Row groups of `tokens` tokens with these heads.
+__host__ inline int64_t row_units(int64_t tokens, int q_heads, int k_heads, int rpw) {
+    return tokens * ((q_heads + rpw - 1) / rpw + (k_heads + rpw - 1) / rpw);
+}
+
+// CTAs for `units` row groups: every warp one group at least, as many as are resident at most.
+__host__ inline unsigned rows_ctas(int64_t units, int num_sms) {
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((units + kWarps - 1) / kWarps, (int64_t)num_sms * kWarpsPerSm / kWarps));
+}
+
+// ------------------------------------------------------------------ host
+
+__host__ inline View view(const pkv_rows* r, int e) {
+    View v = {};
+    if (r) {
+        v.data = (uint8_t*)r->data;
+        v.ts = r->token_stride * e;
+        v.hs = r->head_stride * e;
+        v.heads = r->num_heads;
+    }
+    return v;
+}
+
+// f with the launch's kind of rotation and whether it has a norm, as constants.
+template <typename F>
+__host__ inline cudaError_t for_kind(Kind k, bool norm, F f) {
+    auto g = [&](auto n) {
+        switch (k) {
+            case kInside: return f(std::integral_constant<int, kInside>(), n);
+            case kSetPairs: return f(std::integral_constant<int, kSetPairs>(), n);
+            case kChunks: return f(std::integral_constant<int, kChunks>(), n);
+            default: return f(std::integral_constant<int, kGeneral>(), n);
+        }
+    };
+    return norm ? g(std::true_type()) : g(std::false_type());
 }
 
 }  // namespace rows
