@@ -10,12 +10,14 @@
 //   S_i[128 rows, 128 keys] = Q_i . K_t^T      (A and B K-major in shared memory)
 //   P_i = 2^(S_i scale log2(e) - m), l += sum P_i    (one thread per row = TMEM lane)
 //   O_i[128 rows, D] += P_i . V_t              (A = P from TMEM, B MN-major in shared memory)
-// and out = O / l at the end.  m is the maximum of the row's first tile; after
-// that no maximum is taken: a tile's sum of P bounds its largest P, and m rises
-// (O and l rescaled, by exact powers of 2) only after a tile whose sum reached
-// 2^8, or at once before 32 keys whose P would reach 2^15 (fp16's range).  P is
-// rounded to the inputs' type because both operands of one MMA have the same
-// type.
+// and out = O / l at the end.  m is the maximum of the row's first tile plus
+// 2^4 of headroom; after that no maximum is taken.  P below 2 has a clear top
+// exponent bit in either type, so one OR over the packed P of 64 keys tells
+// whether any reaches 2; only then (a logit 5 octaves above the first tile's
+// largest) m rises, by whole octaves (O and l are rescaled by exact powers of
+// 2), and those P are computed again.  P is rounded to the inputs' type because
+// both operands of one MMA have the same type; the headroom costs bf16 nothing
+// and leaves fp16 11 bits down to 2^-10 of the largest weight.
 //
 // Q, K and V tiles arrive by tensor copies (TMA) in the 128-byte swizzle,
 // straight from strided rows: K-major operands for Q and K, an MN-major one
@@ -63,14 +65,17 @@ constexpr int kRows = 128;                 // rows of a row tile (MMA M)
 constexpr int kKeys = 128;                 // keys of a key tile
 constexpr int kThreads = 512;
 // Registers a thread: the launch gives every thread 128, and the roles' shares add up to as many.
-constexpr int kRegsSoftmax = 168, kRegsEpilogue = 112, kRegsOther = 64;
+constexpr int kRegsSoftmax = 160, kRegsEpilogue = 112, kRegsOther = 80;
 static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOther == 4 * 128, "register file");
 constexpr int kProducer = 12, kMma = 13, kGuard = 15;   // (0-7: softmax, 8-11: epilogue)
-constexpr int kTable = 32;                 // entries of the sequence table
+constexpr int kMinTiles = 2;               // key tiles that a CTA of a split range has at least
+constexpr int kCutCost = 10;               // what cutting a round of items costs, in key tiles (about 20 us)
 constexpr int kFlags = 8;                  // items whose "non-finite V" flags are kept
 constexpr int kMaxSplit = 160;             // CTAs of a split launch (two workspace slots each)
+constexpr float kHeadroom = 4.f;           // octaves of m above the largest logit it was set by
 constexpr int kPieces = 4;                 // pieces of work the producer may be ahead
 
+struct Join;
 struct Arg {
     CUtensorMap q, k, v;
     View vrows, out;                       // V rows again, for the guard's slow path
@@ -79,12 +84,13 @@ struct Arg {
     const int64_t *q_starts, *kv_starts;
     int* err;
     float* partials;                       // split launches: [CTA][2] slots
+    Join* joins;                    // and [CTA]
     uint64_t wait_limit_ns;
     const int* hold;
     int64_t num_q_rows, num_kv_rows;
     int num_seqs, max_q_len, Hq, Hkv, group;
     int pb;                                // query positions of a row tile
-    int split;                             // key tiles cut into equal ranges
+    int split;                             // the items that do not come out even are cut along the keys
     int wide;                              // out's rows are 32-byte aligned
     float scale_log2;
 };
@@ -107,6 +113,13 @@ struct Piece {
 };
 static_assert(sizeof(Piece) % 8 == 0, "aligned ring entries");
 
+// What a CTA leaves for the join: the item that its last piece starts and others go on with.
+struct Join {
+    Piece p;
+    int parts;              // CTAs that hold parts of it, from this one on; 0: none
+    int pad;
+};
+
 template <int D>
 struct Cfg {
     static constexpr int SLABS = D / 64;                  // 128-byte wide slabs of a row
@@ -127,8 +140,7 @@ struct Cfg {
     static constexpr int NBAR = DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
     static constexpr int OFF_FLAG = OFF_MISC + 16;        // int[kFlags]
-    static constexpr int OFF_TABLE = OFF_FLAG + 4 * kFlags;   // int[3][kTable + 1]: units, q rows, kv rows before
-    static constexpr int OFF_INV = (OFF_TABLE + 12 * (kTable + 1) + 15) / 16 * 16;   // float[2][kRows]: 1 / l
+    static constexpr int OFF_INV = OFF_FLAG + 4 * kFlags;     // float[2][kRows]: 1 / l
     static constexpr int OFF_PIECE = OFF_INV + 8 * kRows;     // Piece[kPieces]
     static constexpr int SMEM = OFF_PIECE + kPieces * (int)sizeof(Piece);
     static constexpr int COL_O = 2 * kKeys;
@@ -139,178 +151,252 @@ struct Cfg {
 
 // ------------------------------------------------------------------ work
 
-// Sequence b, given the packed rows before it.
-__device__ __forceinline__ Seq seq_at(const Arg& a, int b, int64_t qb, int64_t kb, bool* bad = nullptr) {
-    Seq s;
-    s.Q = a.q_lens[b];
-    s.L = a.kv_lens[b];
-    s.q0 = a.q_starts ? a.q_starts[b] : qb;
-    s.k0 = a.kv_starts ? a.kv_starts[b] : kb;
-    const bool wrong = s.Q < 0 || s.Q > a.max_q_len || s.L < 0 || s.q0 < 0 || s.k0 < 0 ||
-                       s.q0 > a.num_q_rows - s.Q || s.k0 > a.num_kv_rows - s.L;
-    if (wrong) s.Q = 0;
-    if (bad) *bad = wrong;
-    return s;
-}
+// The plan of a launch, made by one warp of every CTA alike (the CTA's producer;
+// the join's first warp).  Items are dealt in the order of their key tiles, most
+// first, whatever sequence they are of: the first `whole` of them as a whole,
+// every CTA the same number in serpentine rounds; and (split launches) the key
+// tiles of the rest, fewer items than CTAs, laid end to end and cut into equal
+// ranges.  So long and short sequences, a last round that is not full and few
+// rows over long contexts all leave the CTAs within a tile or so of each other.
+// (4 prompts of 2048: in the order of the sequences 172 us, by tiles 140.)
+//
+// The items of a sequence with at least tau tiles are its last blocks, and
+// their number has a closed form, so no list is kept: a lane stands for `chunk`
+// consecutive sequences (one where there are at most 32).
+struct Plan {
+    const Arg& a;
+    int lane, chunk, grid;
+    int64_t rows_q, rows_k;     // packed rows before this lane's sequences
+    Seq one;                    // this lane's sequence, where it has one
+    int items, whole;           // all items; those dealt as a whole
+    int tau, base, upto;        // the level being dealt: its tiles, items with more, items with as many or more
+    int units, ctas;            // the rest: key tiles, CTAs that share them
+    int mine, before;           // of them this lane's and earlier lanes'
 
-__device__ __forceinline__ int items_of(const Arg& a, const Seq& s) { return (s.Q + 2 * a.pb - 1) / (2 * a.pb); }
-// key tiles of query block qb: up to its last row's limit
-__device__ __forceinline__ int tiles_of(const Arg& a, const Seq& s, int qb) {
-    const int keys = s.L - s.Q + min((qb + 1) * 2 * a.pb, s.Q);
-    return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
-}
-// A sequence's share of the work, per kv-head: items, or (split) key tiles, at least one an item.
-__device__ __forceinline__ int units_of(const Arg& a, const Seq& s) {
-    const int n = items_of(a, s);
-    if (!a.split) return n;
-    int u = 0;
-    for (int i = 0; i < n; ++i) u += max(tiles_of(a, s, i), 1);
-    return u;
-}
-
-// The sequences' shares summed up in chunks of consecutive sequences, one chunk per table entry:
-// tab[0] units, tab[1] query rows, tab[2] key rows before the chunk.
-struct Table {
-    const int* tab;
-    int chunk;              // sequences a chunk
-};
-__device__ __forceinline__ void build_table(const Arg& a, int* tab, int chunk, int tid, bool report) {
-    // (lanes 0 .. kTable - 1; the sums over chunks follow)
-    int u = 0;
-    int64_t q = 0, k = 0;
-    for (int b = tid * chunk; b < min((tid + 1) * chunk, a.num_seqs); ++b) {
-        // (bounds of packed rows are checked where a sequence is located, with the rows before it)
-        const int Q = a.q_lens[b], L = a.kv_lens[b];
-        if (report) {
-            if (Q < 0 || Q > a.max_q_len || L < 0) raise_error(a.err, PKV_DEVERR_LENGTH);
-        }
-        q += max(Q, 0);
-        k += max(L, 0);
-        Seq s{0, 0, Q, L};
-        if (Q < 0 || Q > a.max_q_len || L < 0) s.Q = 0;
-        u += units_of(a, s) * a.Hkv;
+    __device__ __forceinline__ Plan(const Arg& a_, int lane_, int grid_) : a(a_), lane(lane_), grid(grid_) {}
+    __device__ __forceinline__ int per() const { return 2 * a.pb; }
+    __device__ __forceinline__ int blocks(const Seq& s) const { return (s.Q + per() - 1) / per(); }
+    // key tiles of query block blk: up to its last row's limit
+    __device__ __forceinline__ int tiles(const Seq& s, int blk) const {
+        const int keys = s.L - s.Q + min((blk + 1) * per(), s.Q);
+        return keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
     }
-    tab[tid + 1] = u;
-    tab[kTable + 1 + tid + 1] = (int)min(q, (int64_t)0x7fffffff);
-    tab[2 * (kTable + 1) + tid + 1] = (int)min(k, (int64_t)0x7fffffff);
-}
-__device__ __forceinline__ void sum_table(int* tab, int lane) {
-    for (int j = 0; j < 3; ++j) {
-        int* t = tab + j * (kTable + 1);
-        int64_t base = 0;
-        if (lane == 0) t[0] = 0;
-        for (int c = 0; c < kTable; c += 32) {
-            int64_t x = t[c + lane + 1];
+    // query blocks with at least t tiles
+    __device__ __forceinline__ int blocks_of(const Seq& s, int t) const {
+        const int n = blocks(s);
+        if (t <= 0) return n;
+        if (t > (s.L + kKeys - 1) / kKeys) return 0;
+        const int need = (t - 1) * kKeys + 1 - s.L + s.Q;    // queries up to the block's end, at least (<= Q)
+        return need <= 0 ? n : n - (int)((unsigned)(need - 1) / (unsigned)per());
+    }
+    // f(sequence number, sequence) for this lane's sequences; bad lengths and rows outside the tensors: Q = 0
+    template <typename F>
+    __device__ __forceinline__ void each(F f, bool report = false) const {
+        const int b0 = lane * chunk;
+        if (chunk == 1 && !report) {
+            if (b0 < a.num_seqs) f(b0, one);
+            return;
+        }
+        int64_t q = rows_q, k = rows_k;
+        for (int b = b0; b < min(b0 + chunk, a.num_seqs); ++b) {
+            Seq s;
+            s.Q = a.q_lens[b];
+            s.L = a.kv_lens[b];
+            s.q0 = a.q_starts ? a.q_starts[b] : q;
+            s.k0 = a.kv_starts ? a.kv_starts[b] : k;
+            q += max(s.Q, 0);
+            k += max(s.L, 0);
+            if (s.Q < 0 || s.Q > a.max_q_len || s.L < 0 || s.q0 < 0 || s.k0 < 0 || s.q0 > a.num_q_rows - s.Q ||
+                s.k0 > a.num_kv_rows - s.L) {
+                if (report && (s.Q != 0 || s.L < 0)) raise_error(a.err, PKV_DEVERR_LENGTH);
+                s.Q = 0;
+                s.L = max(s.L, 0);
+            }
+            f(b, s);
+        }
+    }
+    template <typename V>
+    __device__ __forceinline__ V scan(V x) const {           // the sum over earlier lanes
+        V y = x;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
+        for (int o = 1; o < 32; o <<= 1) {
+            const V z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        return y - x;
+    }
+    __device__ __forceinline__ int count(int t) const {      // items with at least t tiles
+        int n = 0;
+        each([&](int, const Seq& s) { n += blocks_of(s, t); });
+        return __reduce_add_sync(0xffffffffu, n) * a.Hkv;
+    }
+    // The level that holds this item: the most tiles t with more than `item` items of at least t, at
+    // or below the present level (the next one, mostly; else a search -- stepping through 64 levels
+    // took a join of 8k rows 170 us).
+    __device__ __forceinline__ void level(int item) {
+        if (item < upto) return;
+        int hi = tau - 1, lo = 0;                            // (count(0) is all of them)
+        int n = hi >= 0 ? count(hi) : 0;
+        if (n > item) {
+            lo = hi;
+        } else {
+            --hi;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (count(mid) > item) lo = mid;
+                else hi = mid - 1;
             }
-            x += base;
-            t[c + lane + 1] = (int)min(x, (int64_t)0x7fffffff);   // (rows past 2^31 - 1 fail the bounds check)
-            base = __shfl_sync(0xffffffffu, x, 31);
+            n = count(lo);
+        }
+        tau = lo;
+        upto = n;
+        base = count(lo + 1);
+    }
+    // before the first level: above the most tiles of any item
+    __device__ __forceinline__ void top() {
+        int m = -1;
+        each([&](int, const Seq& s) {
+            if (s.Q > 0) m = max(m, tiles(s, blocks(s) - 1));
+        });
+        tau = __reduce_max_sync(0xffffffffu, m) + 1;
+        base = upto = 0;
+    }
+    __device__ __forceinline__ void begin() {
+        chunk = (a.num_seqs + 31) / 32;
+        rows_q = rows_k = 0;
+        int64_t q = 0, k = 0;
+        for (int b = lane * chunk; b < min((lane + 1) * chunk, a.num_seqs); ++b) {
+            q += max(a.q_lens[b], 0);
+            k += max(a.kv_lens[b], 0);
+        }
+        rows_q = scan(q);
+        rows_k = scan(k);
+        one = Seq{0, 0, 0, 0};
+        each([&](int, const Seq& s) { one = s; }, true);     // (reads the lengths)
+        top();
+        items = count(0);
+        whole = a.split ? items / grid * grid : items;
+        units = ctas = 0;
+    }
+    // the rest's shares; leaves the level at the rest's first item's
+    __device__ __forceinline__ void begin_rest() {
+        if (whole == items) return;                          // (also the second time)
+        level(whole);
+        int n = 0;
+        rest([&](int, const Seq&, int, int, int w) { n += w; });
+        before = scan(n);
+        mine = n;
+        units = __reduce_add_sync(0xffffffffu, n);
+        ctas = min(grid, max(units / kMinTiles, items - whole));
+        // a round of whole items takes as long as its first, the longest; cutting it takes an equal
+        // share, and about kCutCost tiles more for the parts and their join
+        if (tau <= units / grid + kCutCost) {
+            ctas = 0;
+            whole = items;
         }
     }
-    __syncwarp();
-}
-
-// The piece at unit u of [u, end) (not split: one unit an item).  False: the unit belongs to a
-// sequence whose rows lie outside the tensors; *step units are to be passed over.
-__device__ __forceinline__ bool locate(const Arg& a, const Table& tb, int u, int end, Piece& p, int* step) {
-    int lo = 0, hi = kTable - 1;                          // the last chunk with units before it <= u
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tb.tab[mid] <= u) lo = mid;
-        else hi = mid - 1;
+    // f(sequence number, sequence, block, first head, units of the block's heads from there on) for the
+    // rest's items among this lane's, given the level of the first of them
+    template <typename F>
+    __device__ __forceinline__ void rest(F f) const {
+        int n = 0;
+        each([&](int, const Seq& s) { n += (blocks_of(s, tau) - blocks_of(s, tau + 1)) * a.Hkv; });
+        int left = whole - base - scan(n);                   // of this level dealt as a whole, from this lane on
+        each([&](int b, const Seq& s) {
+            const int more = blocks_of(s, tau + 1), level_items = (blocks_of(s, tau) - more) * a.Hkv;
+            const int taken = more * a.Hkv + min(max(left, 0), level_items);
+            left -= level_items;
+            int g = taken % a.Hkv;
+            for (int blk = blocks(s) - 1 - taken / a.Hkv; blk >= 0; --blk, g = 0)
+                f(b, s, blk, g, (a.Hkv - g) * max(tiles(s, blk), 1));
+        });
     }
-    u -= tb.tab[lo];
-    int64_t qb = tb.tab[kTable + 1 + lo], kb = tb.tab[2 * (kTable + 1) + lo];
-    int b = lo * tb.chunk;
-    for (;; ++b) {
-        const int Q = a.q_lens[b], L = a.kv_lens[b];
-        Seq s{0, 0, Q, L};
-        if (Q < 0 || Q > a.max_q_len || L < 0) s.Q = 0;
-        const int n = units_of(a, s) * a.Hkv;
-        if (u < n) {
-            *step = n - u;
-            break;
-        }
-        u -= n;
-        qb += max(Q, 0);
-        kb += max(L, 0);
-    }
-    bool bad;
-    p.s = seq_at(a, b, qb, kb, &bad);
-    if (bad) {
-        raise_error(a.err, PKV_DEVERR_LENGTH);
-        return false;
-    }
-    int blk;
-    if (!a.split) {
-        // the last query blocks first: they see the most keys
-        blk = items_of(a, p.s) - 1 - u / a.Hkv;
-        p.g = u % a.Hkv;
+    __device__ __forceinline__ void fill(Piece& p, const Seq& s, int blk, int g) const {
+        p.s = s;
+        p.g = g;
+        p.q0 = blk * per();
+        p.nq = min(per(), s.Q - p.q0);
+        p.two = p.nq > a.pb;
+        p.T = tiles(s, blk);
         p.t0 = 0;
-        p.T = p.t1 = tiles_of(a, p.s, blk);
-        *step = 1;
-    } else {
-        blk = 0;
-        for (;; ++blk) {
-            p.T = tiles_of(a, p.s, blk);
-            const int n = max(p.T, 1) * a.Hkv;
-            if (u < n) break;
-            u -= n;
-        }
-        const int w = max(p.T, 1);
-        p.g = u / w;
-        p.t0 = u % w;
-        *step = min(w - p.t0, end);                       // (end: the units left in the CTA's range)
-        p.t1 = min(p.t0 + *step, p.T);
+        p.t1 = p.T;
+        p.whole = true;
+        p.end = false;
     }
-    p.whole = p.t0 == 0 && p.t1 == p.T;
-    p.q0 = blk * 2 * a.pb;
-    p.nq = min(2 * a.pb, p.s.Q - p.q0);
-    p.two = p.nq > a.pb;
-    p.end = false;
-    return true;
-}
+    // (the piece that one lane has found, to all of them)
+    __device__ __forceinline__ void share(Piece& p, bool mine_) const {
+        const int from = __ffs(__ballot_sync(0xffffffffu, mine_)) - 1;
+        int* w = reinterpret_cast<int*>(&p);
+#pragma unroll
+        for (int x = 0; x < (int)sizeof(Piece) / 4; ++x) w[x] = __shfl_sync(0xffffffffu, w[x], from);
+    }
+    // item j < whole
+    __device__ __forceinline__ void item(int j, Piece& p) {
+        level(j);
+        int n = 0;
+        each([&](int, const Seq& s) { n += (blocks_of(s, tau) - blocks_of(s, tau + 1)) * a.Hkv; });
+        int r = j - base - scan(n);
+        const bool here = r >= 0 && r < n;
+        if (here)
+            each([&](int, const Seq& s) {
+                const int more = blocks_of(s, tau + 1), m = (blocks_of(s, tau) - more) * a.Hkv;
+                if (r >= 0 && r < m) fill(p, s, blocks(s) - 1 - more - r / a.Hkv, r % a.Hkv);
+                r -= m;
+            });
+        share(p, here);
+    }
+    // the rest's unit u, and up to `room` units of its item from there on; the level must be that of `whole`
+    __device__ __forceinline__ void unit(int u, int room, Piece& p) const {
+        int r = u - before;
+        const bool here = r >= 0 && r < mine;
+        bool found = false;
+        rest([&](int, const Seq& s, int blk, int g, int w) {
+            if (here && !found && r < w) {
+                found = true;
+                fill(p, s, blk, g + r / max(tiles(s, blk), 1));
+                p.t0 = r % max(p.T, 1);
+                p.t1 = min(p.t0 + room, p.T);
+                p.whole = p.t0 == 0 && p.t1 == p.T;
+            }
+            r -= w;
+        });
+        share(p, here);
+    }
+    __device__ __forceinline__ int range(int c) const { return (int)((int64_t)units * c / ctas); }
+};
 
-// A CTA's units: every gridDim-th item in serpentine rounds, or (split) one range of key tiles.
-// Split launches use as many CTAs as keep at least kMinTiles tiles each.
-constexpr int kMinTiles = 2;
-__device__ __forceinline__ int split_ctas(int total, int grid) { return min(grid, max(total / kMinTiles, 1)); }
-__device__ __forceinline__ int split_start(int total, int ctas, int c) { return (int)((int64_t)total * c / ctas); }
-
+// A CTA's pieces in order: its whole items, then its range of the rest (planned
+// only then, behind the whole items' work).
 struct Walk {
-    int u, end, round, total;
-    __device__ __forceinline__ void start(const Arg& a, const Table& tb) {
-        total = tb.tab[kTable];
-        round = -1;
-        u = end = 0;
-        if (a.split) {
-            const int n = split_ctas(total, gridDim.x), c = blockIdx.x;
-            if (c < n && total > 0) {
-                u = split_start(total, n, c);
-                end = split_start(total, n, c + 1);
-            }
-        }
-    }
-    __device__ __forceinline__ bool next(const Arg& a, const Table& tb, Piece& p) {
-        int step;
-        if (a.split) {
-            while (u < end) {
-                const bool ok = locate(a, tb, u, end - u, p, &step);
-                u += step;
-                if (ok) return true;
-            }
-            return false;
-        }
-        const int grid = gridDim.x, c = blockIdx.x;
-        for (++round; (int64_t)round * grid < total; ++round) {
+    int round, u, end;
+    int parts;                  // CTAs that share the item that the last piece starts, from this one on (0: none)
+    __device__ __forceinline__ void start() { round = parts = 0; }
+    __device__ __forceinline__ bool next(Plan& plan, Piece& p) {
+        const int grid = plan.grid, c = blockIdx.x;
+        if (round >= 0) {
             const int64_t j = (int64_t)round * grid + ((round & 1) ? grid - 1 - c : c);
-            if (j < total && locate(a, tb, (int)j, 0, p, &step)) return true;
+            ++round;
+            if (j >= plan.whole) plan.begin_rest();       // (which may find them better dealt as a whole)
+            if (j < plan.whole) {
+                plan.item((int)j, p);
+                return true;
+            }
+            round = -1;
+            u = end = 0;
+            if (c < plan.ctas) {
+                u = plan.range(c);
+                end = plan.range(c + 1);
+            }
         }
-        return false;
+        if (u >= end) return false;
+        plan.unit(u, end - u, p);
+        if (p.t0 == 0 && p.t1 < p.T) {
+            int x = c + 1;
+            while (plan.range(x + 1) < u + p.T) ++x;
+            parts = x - c + 1;
+        }
+        u += max(p.t1 - p.t0, 1);
+        return true;
     }
 };
 
@@ -469,7 +555,7 @@ __device__ __forceinline__ float* part_slot(const Arg& a, const Piece& p) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Arg a, int chunk) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Arg a) {
     using K = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];     // (the swizzle needs it; checked below)
     const uint32_t sb = smem_u32(smem);
@@ -482,9 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 4);
     volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 8);   // (drain waits at the end)
     volatile int* nonfinite = reinterpret_cast<volatile int*>(smem + K::OFF_FLAG);
-    int* tab = reinterpret_cast<int*>(smem + K::OFF_TABLE);
     float* inv_l = reinterpret_cast<float*>(smem + K::OFF_INV);
-    const Table table{tab, chunk};
     const Ctl ctl{abort_flag, a.err, a.wait_limit_ns};
 
     if (tid == 0) {
@@ -525,12 +609,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         tmem_relinquish();
     }
     griddep_wait();
-    static_assert(kTable == 32, "one lane a chunk");
-    if (warp == 0) {
-        build_table(a, tab, chunk, lane, blockIdx.x == 0);
-        __syncwarp();
-        sum_table(tab, lane);
-    }
     if ((sb & 1023) != 0 && tid == 0) {
         raise_error(a.err, PKV_DEVERR_TIMEOUT);           // (never: the declaration above aligns it)
         *abort_flag = 1;
@@ -584,9 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             // keys 0 .. lim are visible (rows of no query: everything, so that they ask for no mask)
             const int lim = row_ok ? shift + pos : 0x3fffffff;
             const int top_lim = shift + min(nq, a.pb);    // keys that any of its rows sees
-            // m: the reference maximum (exp2 units), l: the sum of P; pend: octaves that m is to rise
+            // m: the reference maximum (exp2 units), l: the sum of P
             float m = row_ok ? -INFINITY : 0.f, l = 0.f;
-            int pend = 0;
             for (int t = t0; t < t1; ++t, ++scnt) {
                 if (!(ok = wait_all(bar(K::SFULL + i), scnt & 1))) break;
                 tc_fence_after();
@@ -608,14 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     tmem_wait_st();
                 };
                 tmem_wait_ld_into(sa);
-                if (__any_sync(0xffffffffu, pend > 0)) {
-                    // the last tile's sum asked for a higher reference
-                    const float alpha = pend < 127 ? __uint_as_float((uint32_t)(127 - pend) << 23) : 0.f;
-                    if (t > t0) rescale_o(alpha);
-                    l *= alpha;
-                    m += (float)pend;
-                    pend = 0;
-                }
                 // the largest visible S of columns [c0, c1)
                 auto maximum = [&](int c0, int c1) -> float {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -633,14 +702,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 if (!__all_sync(0xffffffffu, m > -INFINITY)) {
                     // no reference yet (a piece's first tile): the row's maximum.  (O and l are 0 so far, or NaN)
                     const float top = maximum(0, kKeys) * sc;
-                    if (m == -INFINITY) m = top;
+                    if (m == -INFINITY) m = top + kHeadroom;
                 }
-                float ts = 0.f;                           // this tile's sum of P
-                // (rare) P of a half tile at column c would reach 2^15: m rises by a whole number of octaves,
-                // and the P written in this tile, O and l are scaled down by as many (exact but for what
-                // falls below the type's range, far below the new maximum)
+                // (rare) a P of 64 keys at column c reaches 2: m rises by a whole number of octaves, and the P
+                // written in this tile, O and l are scaled down by as many (exact but for what falls below
+                // the type's range, far below the new maximum)
                 auto raise_ref = [&](float target, int c) {
-                    const float inc = target > m ? ceilf(target - m) : 0.f;
+                    const float inc = target + kHeadroom > m ? ceilf(target + kHeadroom - m) : 0.f;
                     const int k = (int)fminf(inc, 127.f);
                     const float alpha = k < 127 ? __uint_as_float((uint32_t)(127 - k) << 23) : 0.f;
                     if (c > 0) {                          // the first half's P is being used: it ends in O
@@ -649,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                     if (t > t0 || c > 0) rescale_o(alpha);
                     l *= alpha;
-                    ts *= alpha;
                     m += inc;
                 };
                 // P of 32 keys at column c, two per packed fp32 operation (the even key in the low half);
@@ -676,14 +743,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                     acc = f2add(acc, f2add(ca, cb));
                 };
-                // The P of 64 keys is written once its sum, which bounds the largest, is known to be below
-                // 2^15 (fp16's range).  True: written.
+                // The P of 64 keys is written once none is known to reach 2.  True: written.
                 auto write = [&](uint64_t acc, int c, const uint32_t (&v)[32], bool force) -> bool {
+                    uint32_t any[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int x = 4; x < 32; ++x) any[x & 3] |= v[x];
+                    const bool high = ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
+                    if (__any_sync(0xffffffffu, row_ok && high) && !force) return false;
+                    tmem_st32u(scol + (c >> 1), v);
                     float a0, a1;
                     f2unpack(acc, a0, a1);
-                    if (__any_sync(0xffffffffu, row_ok && !(a0 + a1 < 32768.f)) && !force) return false;
-                    ts += a0 + a1;
-                    tmem_st32u(scol + (c >> 1), v);
+                    l += a0 + a1;                         // (behind the store)
                     tmem_wait_st();
                     return true;
                 };
@@ -730,9 +800,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     // P of the first 64 keys: their PV may run while the rest is computed
                     signal(bar(K::PFA + i) + (c ? 8 * (K::PFB - K::PFA) : 0));
                 }
-                l += ts;
-                // a tile sum of 2^8 or more (it bounds the largest P) moves the reference past it at the next tile
-                if (row_ok && ts >= 256.f && ts < INFINITY) pend = (int)(__float_as_uint(ts) >> 23) - 127 + 1;
             }
             if (!ok) break;
             // this piece's sums go to the epilogue (1 / l) and to memory (lse, or the part's m and l)
@@ -851,53 +918,68 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (warp == kProducer) {
             // -------------------------------------------- tensor copies: Q tiles, K and V tiles in order
             bool ok = true;
+            int nk = 0, nv = 0, nq[2] = {0, 0};           // copies issued: K, V and Q tiles
+            Plan plan(a, lane, gridDim.x);
+            plan.begin();
+            if (a.hold != nullptr && lane == 0) {
+                // (tests of the timeout path only) wait, bounded, for a flag that nothing sets
+                const uint64_t h0 = globaltimer_ns();
+                while (ok && *reinterpret_cast<const volatile int*>(a.hold) == 0) {
+                    if (*abort_flag || globaltimer_ns() - h0 > a.wait_limit_ns) {
+                        if (!*abort_flag) raise_error(a.err, PKV_DEVERR_TIMEOUT);
+                        *abort_flag = 1;
+                        ok = false;
+                    }
+                    __nanosleep(256);
+                }
+            }
+            // one lane: piece n to the other warps, and its tiles' copies
+            auto produce = [&](int n, const Piece& p) -> bool {
+                if (n >= kPieces && !wait(bar(K::PCEMPTY + n % kPieces), ((n - kPieces) / kPieces) & 1, ctl)) return false;
+                const_cast<Piece*>(ring)[n % kPieces] = p;
+                mbar_arrive(bar(K::PCFULL + n % kPieces));
+                if (p.end || p.t1 == p.t0) return true;
+                for (int i = 0; i < (p.two ? 2 : 1); ++i) {
+                    if (nq[i] > 0 && !wait(bar(K::QEMPTY + i), (nq[i] - 1) & 1, ctl)) return false;
+                    ++nq[i];
+                    mbar_arrive_expect_tx(bar(K::QFULL + i), K::SLABS * a.pb * a.group * 128);
+                    for (int s = 0; s < K::SLABS; ++s)
+                        tensor_g2s(sb + K::OFF_Q + i * K::TILE + s * K::SLAB, &a.q, s * 64, p.g * a.group,
+                                   (int)(p.s.q0 + p.q0 + i * a.pb), bar(K::QFULL + i));
+                }
+                for (int t = p.t0; t < p.t1; ++t) {
+                    const int key = (int)(p.s.k0 + (int64_t)t * kKeys);
+                    const int sk = nk % NSK, sv = nv % NSV;
+                    if (nk >= NSK && !wait(bar(K::KEMPTY + sk), ((nk - NSK) / NSK) & 1, ctl)) return false;
+                    ++nk;
+                    mbar_arrive_expect_tx(bar(K::KFULL + sk), K::TILE);
+                    for (int s = 0; s < K::SLABS; ++s)
+                        tensor_g2s(sb + K::OFF_K + sk * K::TILE + s * K::SLAB, &a.k, s * 64, p.g, key, bar(K::KFULL + sk));
+                    if (nv >= NSV && !wait(bar(K::VEMPTY + sv), ((nv - NSV) / NSV) & 1, ctl)) return false;
+                    ++nv;
+                    mbar_arrive_expect_tx(bar(K::VFULL + sv), K::TILE);
+                    for (int s = 0; s < K::SLABS; ++s)
+                        tensor_g2s(sb + K::OFF_V + sv * K::TILE + s * K::SLAB, &a.v, s * 64, p.g, key, bar(K::VFULL + sv));
+                }
+                return true;
+            };
+            Walk w;
+            w.start();
+            Join join = {};
+            for (int n = 0; __all_sync(0xffffffffu, ok); ++n) {
+                Piece p = {};
+                const bool have = w.next(plan, p);        // (the whole warp; the same in every lane)
+                p.end = !have;
+                if (lane == 0) ok = produce(n, p);
+                __syncwarp();
+                if (!have) break;
+                join.p = p;
+            }
+            if (a.split && lane == 0) {
+                join.parts = w.parts;
+                a.joins[blockIdx.x] = join;
+            }
             if (lane == 0) {
-                if (a.hold != nullptr) {
-                    // (tests of the timeout path only) wait, bounded, for a flag that nothing sets
-                    const uint64_t h0 = globaltimer_ns();
-                    while (ok && *reinterpret_cast<const volatile int*>(a.hold) == 0) {
-                        if (*abort_flag || globaltimer_ns() - h0 > a.wait_limit_ns) {
-                            if (!*abort_flag) raise_error(a.err, PKV_DEVERR_TIMEOUT);
-                            *abort_flag = 1;
-                            ok = false;
-                        }
-                        __nanosleep(256);
-                    }
-                }
-                int nk = 0, nv = 0, nq[2] = {0, 0};       // copies issued: K, V and Q tiles
-                Walk w;
-                w.start(a, table);
-                Piece p;
-                for (int n = 0; ok; ++n) {
-                    p.end = !w.next(a, table, p);
-                    if (n >= kPieces && !(ok = wait(bar(K::PCEMPTY + n % kPieces), ((n - kPieces) / kPieces) & 1, ctl))) break;
-                    const_cast<Piece*>(ring)[n % kPieces] = p;
-                    mbar_arrive(bar(K::PCFULL + n % kPieces));
-                    if (p.end) break;
-                    if (p.t1 == p.t0) continue;
-                    for (int i = 0; i < (p.two ? 2 : 1) && ok; ++i) {
-                        if (nq[i] > 0 && !(ok = wait(bar(K::QEMPTY + i), (nq[i] - 1) & 1, ctl))) break;
-                        ++nq[i];
-                        mbar_arrive_expect_tx(bar(K::QFULL + i), K::SLABS * a.pb * a.group * 128);
-                        for (int s = 0; s < K::SLABS; ++s)
-                            tensor_g2s(sb + K::OFF_Q + i * K::TILE + s * K::SLAB, &a.q, s * 64, p.g * a.group,
-                                       (int)(p.s.q0 + p.q0 + i * a.pb), bar(K::QFULL + i));
-                    }
-                    for (int t = p.t0; t < p.t1 && ok; ++t) {
-                        const int key = (int)(p.s.k0 + (int64_t)t * kKeys);
-                        const int sk = nk % NSK, sv = nv % NSV;
-                        if (nk >= NSK && !(ok = wait(bar(K::KEMPTY + sk), ((nk - NSK) / NSK) & 1, ctl))) break;
-                        ++nk;
-                        mbar_arrive_expect_tx(bar(K::KFULL + sk), K::TILE);
-                        for (int s = 0; s < K::SLABS; ++s)
-                            tensor_g2s(sb + K::OFF_K + sk * K::TILE + s * K::SLAB, &a.k, s * 64, p.g, key, bar(K::KFULL + sk));
-                        if (nv >= NSV && !(ok = wait(bar(K::VEMPTY + sv), ((nv - NSV) / NSV) & 1, ctl))) break;
-                        ++nv;
-                        mbar_arrive_expect_tx(bar(K::VFULL + sv), K::TILE);
-                        for (int s = 0; s < K::SLABS; ++s)
-                            tensor_g2s(sb + K::OFF_V + sv * K::TILE + s * K::SLAB, &a.v, s * 64, p.g, key, bar(K::VFULL + sv));
-                    }
-                }
                 // drain: every copy in flight lands before the CTA exits
                 const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
                 for (int t = max(0, nk - NSK); t < nk; ++t) wait(bar(K::KFULL + t % NSK), (t / NSK) & 1, drain);
@@ -1108,45 +1190,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 // CTA c left in its slot 1, rows 32 y .. 32 y + 31; a warp's lanes are rows (the slots' layout makes
 // its loads contiguous) and warps share the dimensions.  Parts are added in the keys' order.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Arg a, int chunk, int grid) {
-    __shared__ int tab[3 * (kTable + 1)];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Table table{tab, chunk};
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Arg a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x;
     griddep_wait();
-    if (warp == 0) {
-        build_table(a, tab, chunk, lane, false);
-        __syncwarp();
-        sum_table(tab, lane);
-    }
-    __syncthreads();
-    const int total = tab[kTable], ctas = split_ctas(total, grid), c = blockIdx.x;
-    if (c >= ctas || total == 0) return;
-    const int u0 = split_start(total, ctas, c), u1 = split_start(total, ctas, c + 1);
-    if (u0 == u1) return;
-    // the CTA's last piece: does it start an item that goes on past the range?
-    Piece p;
-    int step;
-    if (!locate(a, table, u1 - 1, 1, p, &step)) return;
-    const int first = u1 - 1 - p.t0, end = first + p.T;   // the item's units
-    if (first < u0 || end <= u1) return;
+    const Join& join = a.joins[c];
+    const int parts = join.parts;
+    if (parts == 0) return;
+    const Piece p = join.p;
     const int R = blockIdx.y * 32 + lane, i = R / kRows, r = R % kRows;
     const int pos = r / a.group, hl = r - pos * a.group, qi = p.q0 + i * a.pb + pos;
     if (!(pos < a.pb && qi < p.q0 + p.nq) || (i == 1 && !p.two)) return;
     const float* slots = a.partials;
     auto slot = [&](int x) { return slots + ((size_t)x * 2 + (x == c ? 1 : 0)) * slot_floats(D); };
     float m = -INFINITY;
-    int last = c;
-    for (int x = c; x < ctas; ++x) {
-        m = fmaxf(m, slot(x)[(size_t)2 * kRows * D + R]);
-        last = x;
-        if (split_start(total, ctas, x + 1) >= end) break;
-    }
+    for (int x = c; x < c + parts; ++x) m = fmaxf(m, slot(x)[(size_t)2 * kRows * D + R]);
     const float mref = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     float o[D / 8];
 #pragma unroll
     for (int d = 0; d < D / 8; ++d) o[d] = 0.f;
-    for (int x = c; x <= last; ++x) {
+    for (int x = c; x < c + parts; ++x) {
         const float* s = slot(x);
         const float mx = s[(size_t)2 * kRows * D + R];
         const float f = mx == -INFINITY ? (s[(size_t)2 * kRows * (D + 1) + R] == 0.f ? 0.f : 1.f) : exp2f(mx - mref);
@@ -1209,18 +1272,17 @@ bool make_map(CUtensorMap* m, const pkv_rows* r, const void* fallback, int dtype
 }
 
 template <typename T, int D>
-cudaError_t launch(const Arg& a, int chunk, unsigned grid, cudaStream_t st) {
+cudaError_t launch(const Arg& a, unsigned grid, cudaStream_t st) {
     static std::atomic<uint64_t> set{0};
-    cudaError_t e = launch_pdl_bigsmem(set, prompt_kernel<T, D>, dim3(grid), dim3(kThreads), (size_t)Cfg<D>::SMEM, st, a,
-                                       chunk);
+    cudaError_t e = launch_pdl_bigsmem(set, prompt_kernel<T, D>, dim3(grid), dim3(kThreads), (size_t)Cfg<D>::SMEM, st, a);
     if (e == cudaSuccess && a.split)
-        e = launch_pdl(join_kernel<T, D>, dim3(grid, 2 * kRows / 32), dim3(256), (size_t)0, st, a, chunk, (int)grid);
+        e = launch_pdl(join_kernel<T, D>, dim3(grid, 2 * kRows / 32), dim3(256), (size_t)0, st, a);
     return e;
 }
 
 }  // namespace prompt
 
-size_t prompt_workspace_bytes() { return (size_t)prompt::kMaxSplit * 2 * prompt::slot_floats(128) * sizeof(float); }
+size_t prompt_workspace_bytes() { return (size_t)prompt::kMaxSplit * (2 * prompt::slot_floats(128) * sizeof(float) + sizeof(prompt::Join)); }
 
 cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* v, const pkv_rows* out, float* lse,
                           int dtype, int head_dim, int64_t num_q_rows, int64_t num_kv_rows, const int32_t* q_lens,
@@ -1247,7 +1309,8 @@ cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* 
     a.q_starts = q_starts;
     a.kv_starts = kv_starts;
     a.err = err;
-    a.partials = (float*)workspace;
+    a.joins = (Join*)workspace;                           // then the slots (kMaxSplit records: a multiple of 16 bytes)
+    a.partials = (float*)((uint8_t*)workspace + kMaxSplit * sizeof(Join));
     AttnParams dbg = {};
     fill_debug(dbg);
     a.wait_limit_ns = dbg.wait_limit_ns;
@@ -1266,12 +1329,13 @@ cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* 
     const int64_t items = Hkv * std::min<int64_t>((int64_t)num_seqs * ((max_q_len + per - 1) / per),
                                                   num_q_rows / per + num_seqs);
     if (items > 0x7fffffff) return cudaErrorInvalidValue;
-    a.split = workspace != nullptr && items < 2 * sms && items * ((num_kv_rows + kKeys - 1) / kKeys + 1) < 0x7fffffff;
+    // Splitting pays (a second launch, parts written and read) where the items do not come out even
+    // and some have several tiles; the units of the rest stay below 2^31.
+    a.split = workspace != nullptr && num_kv_rows > 4 * kKeys && num_kv_rows < (1 << 30);
     const unsigned grid = (unsigned)(a.split ? std::min(sms, kMaxSplit) : std::min<int64_t>(std::max<int64_t>(items, 1), sms));
-    const int chunk = (num_seqs + kTable - 1) / kTable;
     if (dtype == PKV_BF16)
-        return head_dim == 128 ? launch<__nv_bfloat16, 128>(a, chunk, grid, st) : launch<__nv_bfloat16, 64>(a, chunk, grid, st);
-    return head_dim == 128 ? launch<__half, 128>(a, chunk, grid, st) : launch<__half, 64>(a, chunk, grid, st);
+        return head_dim == 128 ? launch<__nv_bfloat16, 128>(a, grid, st) : launch<__nv_bfloat16, 64>(a, grid, st);
+    return head_dim == 128 ? launch<__half, 128>(a, grid, st) : launch<__half, 64>(a, grid, st);
 }
 
 }  // namespace pkv
