@@ -19,6 +19,15 @@ namespace cache_read {
 using rows::View;
 
 constexpr int kThreads = 256;
+constexpr int kLoads = 3;              // 16-byte loads a thread has in flight (with 6 resident CTAs an SM)
+
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 
 struct Arg {
     const uint8_t *k_cache, *v_cache;
@@ -28,19 +37,54 @@ struct Arg {
     int* err;
     int64_t num_blocks, num_rows;
     int num_seqs, max_blocks, Hkv;
+    bool wide;                         // the rows' 32-byte pieces are aligned
 };
 
+// n elements of T (a whole cache chunk), 32 bytes at a time where the rows allow it: two 16-byte
+// stores of a sector reach L2 as two partial writes.
 template <typename T>
-__device__ __forceinline__ void store_chunk(uint8_t* dst, const float* x, int n) {
-    // n elements of T, 16 bytes at a time
+__device__ __forceinline__ void store_chunk(uint8_t* dst, const float* x, int n, bool wide) {
 #pragma unroll
-    for (int e = 0; e < 16; e += rows::Chunk<T>::N)
-        if (e < n) *reinterpret_cast<uint4*>(dst + e * sizeof(T)) = rows::Chunk<T>::pack(x + e);
+    for (int e = 0; e < 16; e += 2 * rows::Chunk<T>::N) {
+        if (e >= n) continue;
+        const uint4 a = rows::Chunk<T>::pack(x + e);
+        if (e + rows::Chunk<T>::N >= n) {                  // (16 bytes in all)
+            *reinterpret_cast<uint4*>(dst + e * sizeof(T)) = a;
+            continue;
+        }
+        const uint4 b = rows::Chunk<T>::pack(x + e + rows::Chunk<T>::N);
+        if (wide) {
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            rows::store32(dst + e * sizeof(T), w);
+        } else {
+            *reinterpret_cast<uint4*>(dst + e * sizeof(T)) = a;
+            *reinterpret_cast<uint4*>(dst + e * sizeof(T) + 16) = b;
+        }
+    }
+}
+
+// Cache chunk x of a block: K's, then V's, head by head; within a page a warp
+// takes 8 chunks of the head dimension x 4 tokens (NCH = 4: 4 x 8).
+struct At {
+    int g, ch, off;
+    bool v;
+};
+template <int NCH>
+__device__ __forceinline__ At place(int x, int total) {
+    constexpr int CW = NCH < 8 ? NCH : 8, TW = 32 / CW;
+    At a;
+    a.v = x >= total;
+    x -= a.v ? total : 0;
+    a.g = x / (kBlock * NCH);
+    const int y = x % (kBlock * NCH), l = y % 32, w = y / 32;
+    a.ch = (w % (NCH / CW)) * CW + l % CW;
+    a.off = (w / (NCH / CW)) * TW + l / CW;
+    return a;
 }
 
 // E: bytes of a cache element (2: bf16, 1: e4m3)
 template <typename T, int E, int D>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Arg a) {
+__global__ void __launch_bounds__(kThreads, 6) read_kernel(const __grid_constant__ Arg a) {
     constexpr int C = 16 / E, NCH = D / C;                 // elements a chunk, chunks a row
     constexpr int PAGE = kBlock * D * E;
     __shared__ int s_seq, s_page;
@@ -101,59 +145,48 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     const int lo = max(st - pg * kBlock, 0), hi = min(st + n - pg * kBlock, kBlock);
     const int64_t row0 = s_row + (int64_t)pg * kBlock - st;
     if (row0 + hi > a.num_rows && threadIdx.x == 0) raise_error(a.err, PKV_DEVERR_LENGTH);
-    const int per_head = kBlock * NCH, total = a.Hkv * per_head;   // chunks
-    auto which = [&](const uint8_t* cache, const float* scales, const View& out) {
-        if (!out.data) return;
-        const uint8_t* src = cache + (size_t)blk * a.Hkv * PAGE;
-        constexpr int U = 4;
-        for (int x0 = threadIdx.x; x0 < total; x0 += U * kThreads) {
-            uint4 raw[U];
-            int off[U], ch[U], g[U];
-            bool ok[U];
+    // chunks of K, then of V (or of the one that is wanted)
+    const int total = a.Hkv * kBlock * NCH, first = a.k.data ? 0 : total,
+              last = a.v.data ? 2 * total : total;
+    const size_t block = (size_t)blk * a.Hkv;
+    for (int x0 = first + threadIdx.x; x0 < last; x0 += kLoads * kThreads) {
+        uint4 raw[kLoads];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                // 8 chunks of the head dimension x 4 tokens per warp (NCH = 4: 4 chunks x 8 tokens)
-                const int x = x0 + u * kThreads;
-                constexpr int CW = NCH < 8 ? NCH : 8, TW = 32 / CW;
-                g[u] = x / per_head;
-                const int y = x % per_head, l = y % 32, wv = y / 32;
-                ch[u] = (wv % (NCH / CW)) * CW + l % CW;
-                off[u] = (wv / (NCH / CW)) * TW + l / CW;
-                ok[u] = x < total && off[u] >= lo && off[u] < hi && row0 + off[u] < a.num_rows;
-                if (ok[u])
-                    raw[u] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)g[u] * PAGE +
-                                                                  ((off[u] >> 3) * NCH + ch[u]) * 128 + (off[u] & 7) * 16));
-            }
+        for (int u = 0; u < kLoads; ++u) {
+            const At at = place<NCH>(x0 + u * kThreads, total);
+            if (x0 + u * kThreads < last && at.off >= lo && at.off < hi)
+                raw[u] = ld_stream((at.v ? a.v_cache : a.k_cache) + (block + at.g) * PAGE + ((at.off >> 3) * NCH + at.ch) * 128 +
+                                   (at.off & 7) * 16);
+        }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!ok[u]) continue;
-                uint8_t* dst = out.row(row0 + off[u], g[u]) + ch[u] * C * sizeof(T);
-                float v[16];
-                if constexpr (E == 2) {
-                    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                        *reinterpret_cast<uint4*>(dst) = raw[u];
-                    } else {
-                        rows::Chunk<__nv_bfloat16>::unpack(raw[u], v);
-                        store_chunk<T>(dst, v, 8);
-                    }
+        for (int u = 0; u < kLoads; ++u) {
+            const At at = place<NCH>(x0 + u * kThreads, total);
+            if (x0 + u * kThreads >= last || at.off < lo || at.off >= hi || row0 + at.off >= a.num_rows) continue;
+            const View& out = at.v ? a.v : a.k;
+            uint8_t* dst = out.row(row0 + at.off, at.g) + at.ch * C * sizeof(T);
+            float v[16];
+            if constexpr (E == 2) {
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                    *reinterpret_cast<uint4*>(dst) = raw[u];
                 } else {
-                    const float sc = scales[(size_t)blk * a.Hkv + g[u]];
-                    const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 p = e4m3x2_to_float2(w[j]), q = e4m3x2_to_float2(w[j] >> 16);
-                        v[4 * j] = p.x * sc;
-                        v[4 * j + 1] = p.y * sc;
-                        v[4 * j + 2] = q.x * sc;
-                        v[4 * j + 3] = q.y * sc;
-                    }
-                    store_chunk<T>(dst, v, 16);
+                    rows::Chunk<__nv_bfloat16>::unpack(raw[u], v);
+                    store_chunk<T>(dst, v, 8, a.wide);
                 }
+            } else {
+                const float sc = (at.v ? a.v_scales : a.k_scales)[block + at.g];
+                const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 p = e4m3x2_to_float2(w[j]), q = e4m3x2_to_float2(w[j] >> 16);
+                    v[4 * j] = p.x * sc;
+                    v[4 * j + 1] = p.y * sc;
+                    v[4 * j + 2] = q.x * sc;
+                    v[4 * j + 3] = q.y * sc;
+                }
+                store_chunk<T>(dst, v, 16, a.wide);
             }
         }
-    };
-    which(a.k_cache, a.k_scales, a.k);
-    which(a.v_cache, a.v_scales, a.v);
+    }
 }
 
 }  // namespace cache_read
@@ -174,7 +207,8 @@ cudaError_t launch_cache_read(const pkv_cache& c, const int32_t* tables, int max
         return x;
     };
     Arg a = {(const uint8_t*)c.k_cache, (const uint8_t*)c.v_cache, c.k_scales, c.v_scales, view(k), view(v), tables,
-             lens, starts, err, c.num_blocks, num_rows, num_seqs, max_blocks, c.num_kv_heads};
+             lens, starts, err, c.num_blocks, num_rows, num_seqs, max_blocks, c.num_kv_heads, true};
+    a.wide = (!k || rows::wide(a.k)) && (!v || rows::wide(a.v));
     // every sequence's rows touch at most ceil(len / 16) pages, one more where it starts inside a page
     const int64_t units = num_rows / kBlock + (int64_t)num_seqs * (starts ? 2 : 1);
     if (units > 0x7fffffff) return cudaErrorInvalidValue;

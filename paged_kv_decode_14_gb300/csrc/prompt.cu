@@ -59,6 +59,7 @@ int num_sms_current();
 namespace prompt {
 
 using namespace ptx;
+using rows::store32;
 using rows::View;
 
 constexpr int kRows = 128;                 // rows of a row tile (MMA M)
@@ -539,13 +540,6 @@ struct Type<__half> {
 };
 
 // ------------------------------------------------------------------ kernel
-
-// 32 bytes to a 32-byte aligned address.
-__device__ __forceinline__ void store32(uint8_t* p, const uint32_t* v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
 
 // (split) where a part of an item goes: the part that starts the item is its CTA's last piece (slot
 // 1), any other its CTA's first (slot 0).
@@ -1323,7 +1317,7 @@ cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* 
     a.Hkv = Hkv;
     a.group = G;
     a.scale_log2 = scale * kLog2e;
-    a.wide = (((uintptr_t)a.out.data | (uintptr_t)a.out.ts | (uintptr_t)a.out.hs) & 31) == 0;
+    a.wide = rows::wide(a.out);
     // at most this many items (their number depends on the lengths, which the host does not see)
     const int64_t per = 2 * a.pb;
     const int64_t items = Hkv * std::min<int64_t>((int64_t)num_seqs * ((max_q_len + per - 1) / per),

@@ -20,6 +20,18 @@ struct View {
     __device__ __forceinline__ uint8_t* row(int64_t t, int h) const { return data + t * ts + h * hs; }
 };
 
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void store32(uint8_t* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Rows of which every 32-byte piece is 32-byte aligned.
+__host__ inline bool wide(const View& v) {
+    return (((uintptr_t)v.data | (uintptr_t)v.ts | (uintptr_t)v.hs) & 31) == 0;
+}
+
 // The rotation of a launch.  turn[i] is pair i's advance per position as a
 // fraction of a full turn in 64-bit fixed point, so position * turn wraps at
 // whole turns by itself: the angle of any 32-bit position keeps 32 fraction
