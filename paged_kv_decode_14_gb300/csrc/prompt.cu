@@ -26,11 +26,12 @@
 // Roles (512 threads): warps 0-3 the softmax of row tile 0, warps 4-7 of row
 // tile 1, warps 8-11 the epilogue of both, warp 12 the producer, warps 13 and
 // 14 the MMA issuers of row tiles 0 and 1, warp 15 the V guard.  Per tile
-// issuer i runs  PV_i(t), first 64 keys as soon as their P is written | PV_i(t)
-// rest, S_i(t + 1).  The second block runs in turns (0, 1, 0, 1, ...): left
-// alone, the MMAs of both interleave, both S finish together and the tensor
-// core idles through two simultaneous softmaxes; in turns the row tiles stay
-// half a period apart.  The last tile of an item is followed by the next
+// issuer i runs  PV_i(t), first 64 keys as soon as their P is written, PV_i(t)
+// rest, S_i(t + 1), as one block, in turns with the other (0, 1, 0, 1, ...):
+// left alone, the MMAs of both interleave, both S finish together and the
+// tensor core idles through two simultaneous softmaxes; in turns the row tiles
+// stay half a period apart (8k rows of 32 heads: 358 us; the first half's PV
+// ahead of the turn 395; no turns 440).  The last tile of an item is followed by the next
 // item's first S.  One thread's tcgen05 operations complete in order, so when
 // S_i(t + 1) signals, PV_i(t) is done and O_i may be rescaled, and S_i(t + 1)
 // overwrites P_i(t) only after PV_i(t) has read it.
@@ -85,7 +86,7 @@ struct Arg {
     const int64_t *q_starts, *kv_starts;
     int* err;
     float* partials;                       // split launches: [CTA][2] slots
-    Join* joins;                    // and [CTA]
+    Join* joins;                           // and [CTA]
     uint64_t wait_limit_ns;
     const int* hold;
     int64_t num_q_rows, num_kv_rows;
@@ -152,14 +153,13 @@ struct Cfg {
 
 // ------------------------------------------------------------------ work
 
-// The plan of a launch, made by one warp of every CTA alike (the CTA's producer;
-// the join's first warp).  Items are dealt in the order of their key tiles, most
+// The plan of a launch, made by one warp of every CTA alike (its producer).  Items are dealt in the order of their key tiles, most
 // first, whatever sequence they are of: the first `whole` of them as a whole,
 // every CTA the same number in serpentine rounds; and (split launches) the key
 // tiles of the rest, fewer items than CTAs, laid end to end and cut into equal
 // ranges.  So long and short sequences, a last round that is not full and few
 // rows over long contexts all leave the CTAs within a tile or so of each other.
-// (4 prompts of 2048: in the order of the sequences 172 us, by tiles 140.)
+// (4 prompts of 2048: in the order of the sequences 172 us, by tiles 152; 151 with the turns as they are now.)
 //
 // The items of a sequence with at least tau tiles are its last blocks, and
 // their number has a closed form, so no list is kept: a lane stands for `chunk`
@@ -473,11 +473,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 __device__ __forceinline__ uint64_t f2pack(uint32_t a, uint32_t b) {
     uint64_t r;
@@ -1077,14 +1072,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     // (what the turn needs is waited for before P, off the path from P to the next S)
                     if (follow && !(ok = wait_all(bar(K::QFULL + i), qcnt & 1))) break;
                     if ((!end || follow) && !(ok = wait_k())) break;
-                    if (!(ok = wait_all(bar(K::PFA + i), pcnt & 1))) break;
-                    tc_fence_after();
-                    pv(0);
-                    commit(lead, bar(K::PVA + i));
                     if (p.two) {
                         if ((i == 1 || turn > 0) && !(ok = wait_all(bar(K::TURN + i), (i == 1 ? turn : turn - 1) & 1))) break;
                         ++turn;
                     }
+                    if (!(ok = wait_all(bar(K::PFA + i), pcnt & 1))) break;
+                    tc_fence_after();
+                    pv(0);
+                    commit(lead, bar(K::PVA + i));
                     if (!(ok = wait_all(bar(K::PFB + i), pcnt & 1))) break;
                     tc_fence_after();
                     pv(4);
@@ -1095,7 +1090,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         ++qcnt;
                         issue_s(q.t1 - q.t0 == 1);
                     }
-                    if (p.two && lead) mbar_arrive(bar(K::TURN + 1 - i));
+                    // The turn passes when these MMAs are issued (D = 128: 358 us for 8k rows, 380 passed when they
+                    // complete) or, with products half as long, complete (D = 64: 304 us, 315 when issued)
+                    if (p.two) {
+                        if constexpr (D == 64) commit(lead, bar(K::TURN + 1 - i));
+                        else if (lead) mbar_arrive(bar(K::TURN + 1 - i));
+                    }
                 }
                 if (!ok) break;
                 ++ocnt;
