@@ -388,7 +388,10 @@ typedef enum pkv_dtype { PKV_BF16 = 0, PKV_FP16 = 1, PKV_FP32 = 2 } pkv_dtype;
  * t * token_stride + h * head_stride + d of `data` (device), so a view of a
  * fused projection's output needs no copy.  data and, where there is more
  * than one token or head, both strides in bytes must be multiples of 16 (else
- * PKV_ERR_INVALID_ARG).  An output's rows must not overlap each other. */
+ * PKV_ERR_INVALID_ARG).  An output's rows do not overlap: all heads of a token
+ * lie within |token_stride|, or all tokens of a head within |head_stride|
+ * (else PKV_ERR_INVALID_ARG).  In place means the same view; an output that
+ * overlaps an input in any other way is undefined. */
 typedef struct pkv_rows {
     void* data;
     int64_t token_stride;      /* elements */
@@ -449,9 +452,9 @@ PKV_API pkv_status pkv_rope_init(pkv_rope* rope, int32_t rotary_dim, int32_t int
  *   q_weight, k_weight  device [head_dim], 16-byte aligned, or NULL
  *   norm_eps       < 0: no norm (weights must be NULL)
  *
- * One launch; num_tokens <= 2^31 - 1.  It lets the next
- * kernel on the stream start only once it has completed (an attention reads
- * q before its own dependency wait).
+ * One launch; num_tokens <= 2^31 - 1.  It lets the next kernel on the stream
+ * start only once it has completed (an attention reads q before its own
+ * dependency wait).
  */
 PKV_API pkv_status pkv_qk_norm_rope(const pkv_rows* q_in, const pkv_rows* q_out, const pkv_rows* k_in,
                                     const pkv_rows* k_out, int32_t dtype, int32_t head_dim, int64_t num_tokens,
@@ -529,7 +532,7 @@ PKV_API pkv_status pkv_paged_kv_read(const pkv_cache* cache, const int32_t* bloc
  *                  than one head or token.
  *   lse            optional device fp32 [num_q_rows][Hq]
  *   dtype          PKV_BF16 or PKV_FP16 (q, k, v and out); head_dim 64 or 128
- *   num_q_rows, num_kv_rows   rows of the tensors (fewer than 2^31)
+ *   num_q_rows, num_kv_rows   rows of the tensors (at most 2^31 - 256)
  *   q_lens, kv_lens   device int32 [num_seqs]
  *   q_starts, kv_starts   device int64 [num_seqs], each sequence's first row, or
  *                  NULL: packed (padded batches and slices of larger tensors give
@@ -550,7 +553,9 @@ PKV_API pkv_status pkv_paged_kv_read(const pkv_cache* cache, const int32_t* bloc
  * type (bf16: 8 significant bits, fp16: 11), sums and statistics are fp32.
  * NaN or infinity in a key or value row reaches the queries that see it, and
  * no other.  Deterministic.  Reads nothing before the previous kernel on the
- * stream has completed.  The wait limit of pkv_debug_set_wait_limit applies.
+ * stream has completed.  The wait limit and hold flag of
+ * pkv_debug_set_wait_limit apply to it too (the join's rows are undefined after
+ * a wait that ran out, as all of the call's results are).
  */
 PKV_API size_t pkv_prompt_workspace_size(void);
 PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, const pkv_rows* v, const pkv_rows* out,
@@ -577,9 +582,9 @@ PKV_API pkv_status pkv_read_device_error(void* error_word, int32_t* code, void* 
  * down.  A non-NULL hold_flag (device int32) makes the kernel wait for
  * *hold_flag != 0 before its first K/V copy: a flag that nothing sets makes
  * that wait run out.  The settings are process-wide and apply to every
- * later pkv_paged_attention(_noalloc) and pkv_paged_prefill launch (not to
- * the CUDA-core kernel, which has no waits) until they are set again; not for
- * concurrent use.
+ * later pkv_paged_attention(_noalloc), pkv_paged_prefill and
+ * pkv_prompt_attention launch (not to the CUDA-core kernel, which has no
+ * waits) until they are set again; not for concurrent use.
  */
 PKV_API void pkv_debug_set_wait_limit(uint64_t limit_ns, const int32_t* hold_flag);
 

@@ -378,11 +378,20 @@ def _row_view(t, name, dtype, device, shape):
     return _ROWS.pack(t.data_ptr(), strides[0], strides[1], shape[1])
 
 
-def _row_output(t, name, like, dtype, device, shape):
+def _new(stream, make, *args, **kw):
+    """make(...), the memory belonging to the stream that will write it: memory of another stream
+    could be handed out while that stream's earlier work still reads it."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _row_output(t, name, like, dtype, device, shape, stream):
     """(output, its pkv_rows): t, or a new contiguous tensor of the shape."""
     if t is not None:
         return t, _row_view(t, name, dtype, device, shape)
-    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    t = _new(stream, torch.empty_like, like, memory_format=torch.contiguous_format)
     return t, _ROWS.pack(t.data_ptr(), shape[1] * shape[2], shape[2], shape[1])
 
 
@@ -448,12 +457,12 @@ def qk_norm_rope(q, k=None, positions=None, rope: Rope | None = None, q_weight=N
     T, _, D = shape
     _check_norm_rope(q_weight, k_weight, eps, rope, positions)
     qr = _row_view(q, "q", dtype, device, shape)
-    q_out, qo = _row_output(q_out, "q_out", q, dtype, device, shape)
+    q_out, qo = _row_output(q_out, "q_out", q, dtype, device, shape, stream)
     kr = ko = None
     if k is not None:
         kshape = (T, k.shape[1] if k.dim() == 3 else 0, D)
         kr = _row_view(k, "k", dtype, device, kshape)
-        k_out, ko = _row_output(k_out, "k_out", k, dtype, device, kshape)
+        k_out, ko = _row_output(k_out, "k_out", k, dtype, device, kshape, stream)
     elif k_out is not None:
         raise ValueError("k_out without k")
     _call("pkv_qk_norm_rope", device, stream, qr, qo, kr, ko, _ROW_DTYPES[dtype], D, T,
@@ -479,7 +488,7 @@ def append_norm_rope(cache: PagedKVCache, q, k, v, slot_mapping, positions=None,
     if q is not None:
         qshape = (T, q.shape[1] if q.dim() == 3 else 0, D)
         qr = _row_view(q, "q", bf16, device, qshape)
-        q_out, qo = _row_output(q_out, "q_out", q, bf16, device, qshape)
+        q_out, qo = _row_output(q_out, "q_out", q, bf16, device, qshape, stream)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _call("pkv_paged_kv_append_norm_rope", device, stream, ctypes.byref(cache.desc()), qr, qo,
@@ -501,11 +510,11 @@ def read_cache(cache: PagedKVCache, block_tables, lens, num_rows: int, starts=No
     device, n = _device_of(block_tables, "block_tables"), lens.numel()
     shape = (int(num_rows), cache.num_kv_heads, cache.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype if v_out is None else v_out.dtype, device=block_tables.device)
+        k_out = _new(stream, torch.empty, shape, dtype=dtype if v_out is None else v_out.dtype, device=block_tables.device)
     dtype = k_out.dtype
     if dtype not in _ROW_DTYPES:
         raise ValueError("rows must be bfloat16, float16 or float32")
-    v_out, vr = _row_output(v_out, "v_out", k_out, dtype, device, shape)
+    v_out, vr = _row_output(v_out, "v_out", k_out, dtype, device, shape, stream)
     _check_cache_device(cache, device)
     if block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
@@ -545,9 +554,9 @@ def prompt_attention(q, k, v, q_lens, kv_lens, max_q_len: int, scale: float, out
     kshape = (k.shape[0], k.shape[1] if k.dim() == 3 else 0, D)
     qr, kr = _row_view(q, "q", dtype, device, shape), _row_view(k, "k", dtype, device, kshape)
     vr = _row_view(v, "v", dtype, device, kshape)
-    out, orow = _row_output(out, "out", q, dtype, device, shape)
+    out, orow = _row_output(out, "out", q, dtype, device, shape, stream)
     if lse is None:
-        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+        lse = _new(stream, torch.empty, (Tq, Hq), dtype=torch.float32, device=q.device)
     if workspace is not None and (workspace.get_device() != device or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous on the same GPU")
     _call("pkv_prompt_attention", device, stream, qr, kr, vr, orow, _vector(lse, "lse", torch.float32, device, Tq * Hq),

@@ -28,14 +28,17 @@ namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-// Rows the kernels may touch in 16-byte pieces; out: no two of them the same memory.
+// Rows the kernels may touch in 16-byte pieces; out: no two of them share memory (all heads of a token lie
+// between two tokens' starts, or all tokens of a head between two heads').
 bool rows_ok(const pkv_rows* r, int64_t tokens, int elem_bytes, int head_dim, bool out) {
     if (!r || !r->data || r->num_heads < 1 || !aligned16(r->data)) return false;
     if (tokens > 1 && (r->token_stride * elem_bytes) % 16) return false;
     if (r->num_heads > 1 && (r->head_stride * elem_bytes) % 16) return false;
-    if (out && tokens > 1 && std::llabs(r->token_stride) < head_dim) return false;
-    if (out && r->num_heads > 1 && std::llabs(r->head_stride) < head_dim) return false;
-    return true;
+    if (!out || (tokens <= 1 && r->num_heads == 1)) return true;
+    const __int128 ts = tokens > 1 ? r->token_stride : 0, hs = r->num_heads > 1 ? r->head_stride : 0;
+    const __int128 t = ts < 0 ? -ts : ts, h = hs < 0 ? -hs : hs;
+    if ((tokens > 1 && t < head_dim) || (r->num_heads > 1 && h < head_dim)) return false;
+    return tokens == 1 || r->num_heads == 1 || t >= h * (r->num_heads - 1) + head_dim || h >= t * (tokens - 1) + head_dim;
 }
 
 bool rope_ok(const pkv_rope* r, int head_dim, const int32_t* positions) {
@@ -192,7 +195,7 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, co
     if (dtype < PKV_BF16 || dtype > PKV_FP32 || num_seqs < 0 || num_q_rows < 0 || num_kv_rows < 0)
         return PKV_ERR_INVALID_ARG;
     if (dtype == PKV_FP32 || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
-    if (num_q_rows > 0x7fffffff || num_kv_rows > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+    if (num_q_rows > 0x7fffff00 || num_kv_rows > 0x7fffff00) return PKV_ERR_UNSUPPORTED;
     if (!(scale > 0.f) || !std::isfinite(scale) || max_q_len < 1) return PKV_ERR_INVALID_ARG;
     if (num_seqs == 0 || num_q_rows == 0) return PKV_OK;
     if (!q_lens || !kv_lens) return PKV_ERR_INVALID_ARG;

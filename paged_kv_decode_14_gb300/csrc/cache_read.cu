@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 6) read_kernel(const __grid_constant
                 n = max(n, 0);                             // (its rows stay reserved, its pages are not read)
             }
             const bool bad = n > 0 && (st < 0 || ((int64_t)st + n + kBlock - 1) / kBlock > a.max_blocks);
-            int64_t pages = n > 0 && !bad ? (st + n - 1) / kBlock - st / kBlock + 1 : 0;
+            int64_t pages = n > 0 && !bad ? ((int64_t)st + n - 1) / kBlock - st / kBlock + 1 : 0;
             int64_t pu = pages, pr = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -134,16 +134,16 @@ __global__ void __launch_bounds__(kThreads, 6) read_kernel(const __grid_constant
     __syncthreads();
     const int b = s_seq;
     if (b < 0) return;
-    const int n = a.lens[b], st = a.starts ? a.starts[b] : 0;
-    const int pg = st / kBlock + s_page;                   // page of the sequence
+    const int64_t n = a.lens[b], st = a.starts ? a.starts[b] : 0;
+    const int64_t pg = st / kBlock + s_page;               // page of the sequence
     const int32_t blk = a.tables[(size_t)b * a.max_blocks + pg];
     if (blk < 0 || blk >= a.num_blocks) {
         if (threadIdx.x == 0) raise_error(a.err, PKV_DEVERR_BLOCK_ID);
         return;
     }
     // tokens [lo, hi) of the page are wanted; token off's row is row0 + off
-    const int lo = max(st - pg * kBlock, 0), hi = min(st + n - pg * kBlock, kBlock);
-    const int64_t row0 = s_row + (int64_t)pg * kBlock - st;
+    const int lo = (int)max(st - pg * kBlock, (int64_t)0), hi = (int)min(st + n - pg * kBlock, (int64_t)kBlock);
+    const int64_t row0 = s_row + pg * kBlock - st;
     if (row0 + hi > a.num_rows && threadIdx.x == 0) raise_error(a.err, PKV_DEVERR_LENGTH);
     // chunks of K, then of V (or of the one that is wanted)
     const int total = a.Hkv * kBlock * NCH, first = a.k.data ? 0 : total,

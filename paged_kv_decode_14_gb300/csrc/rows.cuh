@@ -303,14 +303,14 @@ struct Cursor {
     static constexpr int RPW = 32 / GS;
     const uint8_t* p;       // this lane's first 16 bytes of its row
     int64_t t;
-    int step;               // bytes to the next group's row (head strides below 2^31 / RPW)
+    int64_t step;           // bytes to the next group's row
     int rows;               // heads from this lane's row on (<= 0: none)
     int left;               // groups left of this tensor's heads
     bool k;                 // in k's heads
     __device__ __forceinline__ void open(const View& v, int64_t t_, int g, int l, int sub) {
         t = t_;
         p = v.row(t, g * RPW + sub) + l * 16;
-        step = (int)(v.hs * RPW);
+        step = v.hs * RPW;
         rows = v.heads - g * RPW - sub;
         left = (v.heads + RPW - 1) / RPW - g;
     }

@@ -1,0 +1,263 @@
+"""The row operators used together, and the calls around their edges: a prompt served from projections to
+decode, graphs and streams, timeouts, scales at the ends of fp32, addresses past 2^31."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_decode_14_gb300 import _native as nat
+from gpu_helpers import ATOL, RTOL
+from test_gpu_prompt import check, reference, run
+from test_gpu_rows import assert_rows, clone, make, new_cache, page_rows, ref_rows, same_cache
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 6, 3)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_prompt_chunk_decode(dtype, D, Hq, Hkv):
+    """Three prompts: the first chunk attends its own rows, the second the context read back from the
+    cache, then one decode step attends the cache; each against 64 bits from the rows it was given."""
+    first, second, nb = [40, 16, 129], [25, 3, 16], 64
+    B, fp8 = len(first), dtype == "fp8"
+    per = [-(-(a + b + 1) // 16) for a, b in zip(first, second)]
+    ids = np.random.default_rng(D).permutation(nb)
+    table = np.zeros((B, max(per)), np.int32)
+    at = 0
+    for b, n in enumerate(per):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    slot = lambda b, p: int(table[b, p // 16]) * 16 + p % 16
+    c = new_cache(nb, Hkv, D, dtype, seed=D)
+    tables = torch.from_numpy(table).cuda()
+    rope = nat.Rope(D, 10000.0, False, "bands", 4.0, 64, 1.0, 4.0)
+    qw, kw = ((1 + 0.2 * torch.randn(D, device="cuda")).bfloat16() for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws, scale = nat.make_prompt_workspace(), D ** -0.5
+
+    def step(new, have, seed):
+        T = sum(new)
+        q, k, v = make(T, (Hq, Hkv, Hkv), D, torch.bfloat16, seed)
+        pos = i32([have[b] + i for b in range(B) for i in range(new[b])])
+        slots = torch.tensor([slot(b, have[b] + i) for b in range(B) for i in range(new[b])], dtype=torch.int64, device="cuda")
+        ko = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device="cuda")
+        qo = nat.append_norm_rope(c, q, k, v, slots, pos, rope, qw, kw, 1e-6, k_out=ko, fp8_scales_from_values=fp8,
+                                  device_error=err)
+        assert_rows(qo, *ref_rows(q, qw, 1e-6, pos, rope), "q")
+        assert_rows(ko, *ref_rows(k, kw, 1e-6, pos, rope), "k")
+        return qo, ko, v
+
+    def context(lens, dt=torch.bfloat16):
+        k, v = nat.read_cache(c, tables, i32(lens), sum(lens), dtype=dt, device_error=err)
+        # what it reads is what the pages hold
+        pk, pv = page_rows(c.k, D, 1 if fp8 else 2), page_rows(c.v, D, 1 if fp8 else 2)
+        r = 0
+        for b, n in enumerate(lens):
+            for p in (0, n // 2, n - 1):
+                blk = int(table[b, p // 16])
+                for got, page, sc in ((k, pk, c.k_scales), (v, pv, c.v_scales)):
+                    want = page[blk, :, p % 16].float() * (sc[blk][:, None] if fp8 else 1.0)
+                    assert torch.equal(got[r + p], want.to(dt))
+            r += n
+        return k, v
+
+    q, k, v = step(first, [0] * B, 1)
+    out, lse = nat.prompt_attention(q, k, v, i32(first), i32(first), max(first), scale, workspace=ws, device_error=err)
+    check(out, lse, *reference(q, k, v, first, first, scale))
+
+    q, _, _ = step(second, first, 2)
+    lens = [a + b for a, b in zip(first, second)]
+    k, v = context(lens)
+    out, lse = nat.prompt_attention(q, k, v, i32(second), i32(lens), max(second), scale, workspace=ws, device_error=err)
+    check(out, lse, *reference(q, k, v, second, lens, scale))
+
+    q, _, _ = step([1] * B, lens, 3)
+    lens = [n + 1 for n in lens]
+    k, v = context(lens, torch.float32)
+    aw = nat.make_workspace(B, Hq, Hkv, D, 1)
+    out = nat.attention(c, q, tables, i32(lens), i32([1] * B), 1, scale, aw)
+    ref, _, _ = reference(q, k, v, [1] * B, lens, scale)
+    assert ((out.double() - ref).abs() <= ATOL + RTOL * ref.abs()).all()
+    assert nat.read_device_error(err) == 0
+
+
+def test_scales_at_the_ends_of_fp32():
+    """Continuing a block with any scale a cache may hold gives the IEEE quotient's code, as append does."""
+    tiny = [0.0, -0.0, 2.0 ** -149, 2.0 ** -127, 2.0 ** -126, 2.0 ** -101, 2.0 ** -100, 2.0 ** -99, 1e-20, 448.0 ** -1, 1.0,
+            2.0 ** 99, 2.0 ** 100, 2.0 ** 101, 2.0 ** 127, math.inf, math.nan, -1.0, -2.0 ** -126]
+    nb, Hkv, D = len(tiny), 2, 64
+    c = new_cache(nb, Hkv, D, "fp8")
+    c.k_scales[:] = torch.tensor(tiny, device="cuda")[:, None]
+    c.v_scales[:] = torch.tensor(tiny[::-1], device="cuda")[:, None]
+    T = 3 * nb
+    slots = torch.tensor([b * 16 + o for b in range(nb) for o in (1, 5, 15)], dtype=torch.int64, device="cuda")
+    _, k, v = make(T, (1, Hkv, Hkv), D, torch.bfloat16, 9)
+    k, v = k.clone(), v.clone()
+    k[::3] *= 2.0 ** -120                      # quotients near 1 for the smallest scales too
+    v[::3] *= 2.0 ** -120
+    k[1::3] *= 2.0 ** 110
+    v[1::3] *= 2.0 ** 110
+    k[0, 0, 0], k[1, 0, 1], v[2, 1, 2] = math.inf, math.nan, -math.inf
+    a, b = clone(c), clone(c)
+    nat.append(a, k, v, slots)
+    nat.append_norm_rope(b, None, k, v, slots)
+    for x, y in ((a.k, b.k), (a.v, b.v)):
+        nan = ((x & 127) == 127) & ((y & 127) == 127)       # (either sign of NaN)
+        assert bool(((x == y) | nan).all())
+
+
+def test_codes_next_to_rounding_boundaries():
+    """Values whose quotient by the scale falls on, or one fp32 step beside, the middle between two codes."""
+    codes = torch.arange(0, 127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).float()
+    mid = ((codes[1:] + codes[:-1]) / 2).double()
+    Hkv, D = 1, 64
+    nb = 64
+    c = new_cache(nb, Hkv, D, "fp8")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    # for a bf16 value x and a middle m, the scale x / m to fp32, a step up and a step down
+    x = torch.randn(nb, generator=g, device="cuda").abs().add(0.5).bfloat16()
+    m = mid[torch.randint(0, mid.numel(), (nb,), generator=g, device="cuda")]
+    s = (x.double() / m).float()
+    s = torch.stack([torch.nextafter(s, torch.zeros_like(s)), s, torch.nextafter(s, torch.full_like(s, 9e9))])[
+        torch.arange(nb, device="cuda") % 3, torch.arange(nb, device="cuda")]
+    c.k_scales[:, 0] = s
+    c.v_scales[:, 0] = s
+    slots = torch.arange(nb, device="cuda") * 16 + 3
+    k = x[:, None, None].expand(nb, Hkv, D).contiguous()
+    a, b = clone(c), clone(c)
+    nat.append(a, k, -k, slots)
+    nat.append_norm_rope(b, None, k, -k, slots)
+    assert same_cache(a, b)
+
+
+def test_captured_and_on_another_stream():
+    """One graph of rows, append, read and attention, replayed with other inputs in the same tensors."""
+    D, Hq, Hkv, T = 128, 8, 2, 50
+    rope = nat.Rope(D)
+    c = new_cache(8, Hkv, D, "fp8")
+    q, k, v = (x.clone() for x in make(T, (Hq, Hkv, Hkv), D, torch.bfloat16, 1))
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    slots = torch.arange(T, device="cuda", dtype=torch.int64) + 16
+    tables, lens = i32([[1, 2, 3, 4]]), i32([T])
+    qo, out, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(T, Hq, device="cuda")
+    kr, vr = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device="cuda"), torch.empty(T, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    kn = torch.empty_like(kr)
+    ws = nat.make_prompt_workspace()
+
+    def work():
+        nat.qk_norm_rope(q, k, pos, rope, eps=1e-5, q_out=qo, k_out=kn)
+        nat.append_norm_rope(c, None, kn, v, slots, fp8_scales_from_values=True)
+        nat.read_cache(c, tables, lens, T, k_out=kr, v_out=vr)
+        nat.prompt_attention(qo, kr, vr, lens, lens, T, 0.1, out=out, lse=lse, workspace=ws)
+
+    work()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            work()
+    torch.cuda.current_stream().wait_stream(s)
+    for seed in (1, 2, 3):
+        for x, y in zip((q, k, v), make(T, (Hq, Hkv, Hkv), D, torch.bfloat16, seed)):
+            x.copy_(y)
+        for x in (out, lse, kr, vr, kn, qo):
+            x.zero_()
+        g.replay()
+        got = [x.clone() for x in (qo, kn, kr, vr, out, lse)]
+        work()
+        for x, y in zip(got, (qo, kn, kr, vr, out, lse)):
+            assert torch.equal(x, y)
+        check(out, lse, *reference(qo, kr, vr, [T], [T], 0.1))
+    # a stream given by its handle, while the current one is another
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a, _ = nat.qk_norm_rope(q, None, pos, rope, eps=1e-5, stream=other)
+    other.synchronize()
+    assert torch.equal(a, qo)
+
+
+@pytest.mark.parametrize("L", [300, 5000])
+def test_wait_timeout_reports_and_recovers(L):
+    """The bounded waits, made to run out by a hold flag that nothing sets; the next call is right.  L = 5000:
+    the launch that is split along the keys, with its join."""
+    q = torch.randn(300, 4, 128, device="cuda").bfloat16()
+    k, v = (torch.randn(L, 2, 128, device="cuda").bfloat16() for _ in range(2))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hold = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = nat.make_prompt_workspace()
+    ws.fill_(0xFF)
+    ql, kl = i32([300]), i32([L])
+    try:
+        nat.debug_set_wait_limit(200_000, hold)
+        nat.prompt_attention(q, k, v, ql, kl, 300, 0.1, workspace=ws, device_error=err)
+        torch.cuda.synchronize()
+    finally:
+        nat.debug_set_wait_limit(0, None)
+    assert nat.read_device_error(err) == nat.DEVERR_TIMEOUT
+    out, lse = nat.prompt_attention(q, k, v, ql, kl, 300, 0.1, workspace=ws, device_error=err)
+    check(out, lse, *reference(q, k, v, [300], [L], 0.1))
+    assert nat.read_device_error(err) == 0
+
+
+@pytest.mark.parametrize("n", [33, 1500])
+def test_more_sequences_than_lanes(n):
+    """Ragged batches whose plan takes more than one sequence a lane, whole and cut along the keys."""
+    r = np.random.default_rng(n)
+    Q = [int(x) for x in r.integers(0, 5, n)]
+    L = [q + int(x) for q, x in zip(Q, r.integers(-3, 300, n))]
+    L = [max(x, 0) for x in L]
+    L[n // 2] += 4000
+    run(Q, L, 2, 1, 64, "fp16")
+    run(Q, Q, 4, 2, 128, "bf16", ws="no")
+
+
+def test_large_strides():
+    """Head strides of 256 MB (eight heads past 2^31 bytes) and token strides of 512 MB."""
+    D, T = 64, 3
+    buf = torch.empty(9 << 27, dtype=torch.bfloat16, device="cuda")
+    q = buf.as_strided((T, 9, D), (D, 1 << 27, 1))
+    src = torch.randn(T, 9, D, device="cuda").bfloat16()
+    q.copy_(src)
+    pos = i32([5, 70000, 3])
+    rope = nat.Rope(D)
+    out, _ = nat.qk_norm_rope(q, None, pos, rope, eps=1e-6)
+    assert_rows(out, *ref_rows(src, None, 1e-6, pos, rope))
+    nat.qk_norm_rope(q, None, pos, rope, eps=1e-6, q_out=q)
+    assert torch.equal(q, out)
+    kv = buf.as_strided((4, 2, D), (1 << 28, D, 1))
+    src = torch.randn(4, 2, D, device="cuda").bfloat16()
+    kv.copy_(src)
+    qs = torch.randn(4, 4, D, device="cuda").bfloat16()
+    a = nat.prompt_attention(qs, kv, kv, i32([4]), i32([4]), 4, 0.1)
+    b = nat.prompt_attention(qs, src, src, i32([4]), i32([4]), 4, 0.1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_cache_past_2_31_bytes():
+    """Blocks whose pages lie past 2^31 elements of the cache."""
+    Hkv, D = 8, 128
+    nb = (1 << 31) // (Hkv * 16 * D) + 8
+    k, v = (torch.empty(nb, Hkv, 16 * D, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones(nb, Hkv, device="cuda") for _ in range(2))
+    c = nat.PagedKVCache(nb, Hkv, D, "fp8", k=k, v=v, k_scales=ks, v_scales=vs)
+    blocks = [nb - 1, 0, nb - 8]
+    slots = torch.tensor([b * 16 + i for b in blocks for i in range(16)], dtype=torch.int64, device="cuda")
+    _, kr, vr = make(48, (1, Hkv, Hkv), D, torch.bfloat16, 2)
+    nat.append_norm_rope(c, None, kr, vr, slots, fp8_scales_from_values=True)
+    small = new_cache(3, Hkv, D, "fp8")
+    nat.append_norm_rope(small, None, kr, vr, torch.arange(48, device="cuda"), fp8_scales_from_values=True)
+    a = nat.read_cache(c, i32([blocks]), i32([48]), 48)
+    b = nat.read_cache(small, i32([[0, 1, 2]]), i32([48]), 48)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    # within half a code of what was written: e4m3's step is at most 2^-3 of the value, or 2^-9 of a scale
+    sc = kr.float().abs().view(3, 16, Hkv, D).amax((1, 3)) / 448
+    tol = kr.float().abs() * (2.0 ** -4 + 2.0 ** -8) + (sc * 2.0 ** -10).repeat_interleave(16, 0)[:, :, None]
+    assert ((a[0].float() - kr.float()).abs() <= tol).all()

@@ -163,3 +163,22 @@ def test_bindings_want_gpu_tensors():
         nat.qk_norm_rope(x)
     with pytest.raises(ValueError):
         nat.prompt_attention(x, x, x, torch.ones(1, dtype=torch.int32), torch.ones(1, dtype=torch.int32), 2, 0.1)
+
+
+def test_outputs_whose_rows_share_memory_are_refused(L):
+    """Both strides at least a row, yet two (token, head) pairs in one place; either order of nesting is fine."""
+    def call(ts, hs, T=4, H=4, D=128):
+        return L.pkv_qk_norm_rope(rows(H, D), rows(H, D, ts=ts, hs=hs), None, None, 0, D, T, None, None, 0, None, None,
+                                  -2.0, None)
+
+    assert call(128, 128) == INVALID
+    assert call(256, 128) == INVALID
+    assert call(3 * 128, 128) == INVALID
+    assert call(128, 3 * 128) == INVALID
+    assert call(-3 * 128, 128) == INVALID
+    assert call(64, 4 * 128) == INVALID
+    assert call(2 ** 61, 2 ** 61) == INVALID                # (the spans pass 64 bits)
+    # (these pass the checks of the rows: what refuses them is the missing device, or that no tokens are given)
+    for ts, hs, T, H in ((512, 128, 4, 4), (128, 512, 4, 4), (-512, 128, 4, 4), (128, -512, 4, 4), (0, 128, 1, 4),
+                         (128, 0, 4, 1), (0, 0, 1, 1), (640, 128, 4, 4)):
+        assert call(ts, hs, T, H) != INVALID
