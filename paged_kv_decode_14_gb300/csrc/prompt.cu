@@ -92,6 +92,7 @@ struct Arg {
     int64_t num_q_rows, num_kv_rows;
     int num_seqs, max_q_len, Hq, Hkv, group;
     int pb;                                // query positions of a row tile
+    uint32_t per_mul, per_shift;           // n / (2 pb) = (n * per_mul) >> per_shift for n < 2^31
     int split;                             // the items that do not come out even are cut along the keys
     int wide;                              // out's rows are 32-byte aligned
     float scale_log2;
@@ -153,7 +154,7 @@ struct Cfg {
 
 // ------------------------------------------------------------------ work
 
-// The plan of a launch, made by one warp of every CTA alike (its producer).  Items are dealt in the order of their key tiles, most
+// The plan of a launch, made by one warp of every CTA alike (its V guard).  Items are dealt in the order of their key tiles, most
 // first, whatever sequence they are of: the first `whole` of them as a whole,
 // every CTA the same number in serpentine rounds; and (split launches) the key
 // tiles of the rest, fewer items than CTAs, laid end to end and cut into equal
@@ -176,7 +177,8 @@ struct Plan {
 
     __device__ __forceinline__ Plan(const Arg& a_, int lane_, int grid_) : a(a_), lane(lane_), grid(grid_) {}
     __device__ __forceinline__ int per() const { return 2 * a.pb; }
-    __device__ __forceinline__ int blocks(const Seq& s) const { return (s.Q + per() - 1) / per(); }
+    __device__ __forceinline__ int div_per(uint32_t n) const { return (int)(((uint64_t)n * a.per_mul) >> a.per_shift); }
+    __device__ __forceinline__ int blocks(const Seq& s) const { return div_per(s.Q + per() - 1); }
     // key tiles of query block blk: up to its last row's limit
     __device__ __forceinline__ int tiles(const Seq& s, int blk) const {
         const int keys = s.L - s.Q + min((blk + 1) * per(), s.Q);
@@ -188,7 +190,7 @@ struct Plan {
         if (t <= 0) return n;
         if (t > (s.L + kKeys - 1) / kKeys) return 0;
         const int need = (t - 1) * kKeys + 1 - s.L + s.Q;    // queries up to the block's end, at least (<= Q)
-        return need <= 0 ? n : n - (int)((unsigned)(need - 1) / (unsigned)per());
+        return need <= 0 ? n : n - div_per(need - 1);
     }
     // f(sequence number, sequence) for this lane's sequences; bad lengths and rows outside the tensors: Q = 0
     template <typename F>
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(K::PCFULL + i), 1);
-            mbar_init(bar(K::PCEMPTY + i), 15);           // every warp but the producer
+            mbar_init(bar(K::PCEMPTY + i), 15);           // every warp but the guard, which writes them
         }
         mbar_init(bar(K::DRAIN), 2);
         *abort_flag = 0;
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // The pieces of work, found by the producer and read here by the other warps: the n-th piece
+    // The pieces of work, found by the V guard and read here by the other warps: the n-th piece
     // (nullptr: a wait gave up), until its release.  The search costs registers and instruction
     // cache, which 15 warps that each did their own paid for in their loops.
     const Piece* ring = reinterpret_cast<const Piece*>(smem + K::OFF_PIECE);
@@ -689,9 +691,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 };
                 if (!__all_sync(0xffffffffu, m > -INFINITY)) {
-                    // no reference yet (a piece's first tile): the row's maximum.  (O and l are 0 so far, or NaN)
-                    const float top = maximum(0, kKeys) * sc;
-                    if (m == -INFINITY) m = top + kHeadroom;
+                    // no reference yet (a piece's first tile): the largest of the first 32 keys, or where the row
+                    // sees none of them, of the tile.  (O and l are 0 so far, or NaN)
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) mx[x & 3] = fmaxf(mx[x & 3], x <= rem ? __uint_as_float(sa[x]) : -INFINITY);
+                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (!__all_sync(0xffffffffu, top > -INFINITY || rem < 32)) top = maximum(0, kKeys);
+                    if (m == -INFINITY) m = top * sc + kHeadroom;
                 }
                 // (rare) a P of 64 keys at column c reaches 2: m rises by a whole number of octaves, and the P
                 // written in this tile, O and l are scaled down by as many (exact but for what falls below
@@ -823,7 +830,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int G = a.group, pos = r / G, hl = r - pos * G;
         const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
         auto wait_all = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, wait(bb, parity, ctl)); };
-        int cnt[2] = {0, 0}, item = 0;                    // items of either row tile; the CTA's items with tiles
+        // (one copy of the code, in loops: it runs once an item, from an instruction cache that holds the
+        // softmax's by then; unrolled it took 5 thousand clocks a row tile)
+        uint32_t phase = 0;                               // of either row tile's items, as bits
+        int item = 0;                                     // the CTA's items with tiles
         bool ok = true;
         for (int n = 0; ok; ++n) {
             const Piece* at = piece_at(n);
@@ -832,73 +842,59 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             release(n);
             if (p.t1 == p.t0) continue;
             const int it = item++;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!ok || (i == 1 && !p.two)) break;
+#pragma unroll 1
+            for (int i = 0; i < (p.two ? 2 : 1); ++i) {
                 const uint32_t ocol = tmem + lbase + K::COL_O + i * D;
                 const int qi = p.q0 + i * a.pb + pos;
                 const bool row_ok = pos < a.pb && qi < p.q0 + p.nq;
                 const int lim = p.s.L - p.s.Q + qi;
-                if (!(ok = wait_all(bar(K::LREADY + i), cnt[i] & 1))) break;
-                const float inv = inv_l[i * kRows + r];
-                if (!(ok = wait_all(bar(K::ODONE + i), cnt[i] & 1))) break;
-                ++cnt[i];
+                if (!(ok = wait_all(bar(K::LREADY + i), (phase >> i) & 1))) break;
+                const float inv = lim >= 0 ? inv_l[i * kRows + r] : 0.f;
+                if (!(ok = wait_all(bar(K::ODONE + i), (phase >> i) & 1))) break;
+                phase ^= 1u << i;
                 tc_fence_after();
                 // infinities and NaN that the guard took out of V, for the rows that see them
                 const bool fix = nonfinite[it & (kFlags - 1)] != 0;
-                auto add_back = [&](float (&o)[32], int c) {
-                    const int first = max(p.s.L - p.s.Q + p.q0 + 1, p.t0 * kKeys);
-                    for (int j = first; j <= min(lim, p.t1 * kKeys - 1); ++j) {
-                        const uint8_t* v = a.vrows.row(p.s.k0 + j, p.g) + c * 2;
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            const float f = Type<T>::get(v + 2 * x);
-                            if (!(fabsf(f) < INFINITY)) o[x] += f;
-                        }
-                    }
-                };
-                auto free_o = [&] {                       // O_i read: the next item's first PV may overwrite it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(K::OFREE + i));
-                };
-                if (p.whole) {
-                    uint32_t v[D / 2];                    // the whole row, packed, so that O_i is free before the stores
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        tmem_ld32(ocol + c, o);
-                        if (fix && row_ok) add_back(o, c);
-#pragma unroll
-                        for (int x = 0; x < 32; x += 2)
-                            v[(c + x) >> 1] = lim >= 0 ? pack2<T>(o[x] * inv, o[x + 1] * inv) : 0u;
-                    }
-                    free_o();
-                    if (row_ok) {
-                        uint8_t* dst = a.out.row(p.s.q0 + qi, p.g * G + hl);
-                        if (a.wide) {
-#pragma unroll
-                            for (int c = 0; c < D / 2; c += 8) store32(dst + c * 4, v + c);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < D / 2; c += 4)
-                                *reinterpret_cast<uint4*>(dst + c * 4) = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-                        }
-                    }
-                } else {
-                    float* slot = part_slot<D>(a, p);
-                    const int R = i * kRows + r;
+                uint8_t* dst = a.out.row(p.s.q0 + qi, p.g * G + hl);
+                float* slot = part_slot<D>(a, p) + (i * kRows + r) * 4;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        tmem_ld32(ocol + c, o);
-                        if (fix && row_ok) add_back(o, c);
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(ocol + c, o);
+                    if (c + 32 == D) {                    // O_i read: the next item's first PV may overwrite it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(K::OFREE + i));
+                    }
+                    if (fix && row_ok) {
+                        const int first = max(p.s.L - p.s.Q + p.q0 + 1, p.t0 * kKeys);
+                        for (int j = first; j <= min(lim, p.t1 * kKeys - 1); ++j) {
+                            const uint8_t* v = a.vrows.row(p.s.k0 + j, p.g) + c * 2;
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) {
+                                const float f = Type<T>::get(v + 2 * x);
+                                if (!(fabsf(f) < INFINITY)) o[x] += f;
+                            }
+                        }
+                    }
+                    if (!p.whole) {
 #pragma unroll
                         for (int x = 0; x < 32; x += 4)
-                            *reinterpret_cast<float4*>(slot + ((size_t)((c + x) / 4) * 2 * kRows + R) * 4) =
+                            *reinterpret_cast<float4*>(slot + (size_t)((c + x) / 4) * 2 * kRows * 4) =
                                 make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                    } else if (row_ok) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int x = 0; x < 32; x += 2) v[x >> 1] = lim >= 0 ? pack2<T>(o[x] * inv, o[x + 1] * inv) : 0u;
+                        if (a.wide) {
+                            store32(dst + c * 2, v);
+                            store32(dst + c * 2 + 32, v + 8);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 16; x += 4)
+                                *reinterpret_cast<uint4*>(dst + c * 2 + x * 4) = make_uint4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+                        }
                     }
-                    free_o();
                 }
             }
         }
@@ -908,8 +904,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             // -------------------------------------------- tensor copies: Q tiles, K and V tiles in order
             bool ok = true;
             int nk = 0, nv = 0, nq[2] = {0, 0};           // copies issued: K, V and Q tiles
-            Plan plan(a, lane, gridDim.x);
-            plan.begin();
             if (a.hold != nullptr && lane == 0) {
                 // (tests of the timeout path only) wait, bounded, for a flag that nothing sets
                 const uint64_t h0 = globaltimer_ns();
@@ -922,12 +916,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     __nanosleep(256);
                 }
             }
-            // one lane: piece n to the other warps, and its tiles' copies
-            auto produce = [&](int n, const Piece& p) -> bool {
-                if (n >= kPieces && !wait(bar(K::PCEMPTY + n % kPieces), ((n - kPieces) / kPieces) & 1, ctl)) return false;
-                const_cast<Piece*>(ring)[n % kPieces] = p;
-                mbar_arrive(bar(K::PCFULL + n % kPieces));
-                if (p.end || p.t1 == p.t0) return true;
+            // one lane: the copies of a piece's tiles
+            auto produce = [&](const Piece& p) -> bool {
+                if (p.t1 == p.t0) return true;
                 for (int i = 0; i < (p.two ? 2 : 1); ++i) {
                     if (nq[i] > 0 && !wait(bar(K::QEMPTY + i), (nq[i] - 1) & 1, ctl)) return false;
                     ++nq[i];
@@ -952,21 +943,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
                 return true;
             };
-            Walk w;
-            w.start();
-            Join join = {};
             for (int n = 0; __all_sync(0xffffffffu, ok); ++n) {
-                Piece p = {};
-                const bool have = w.next(plan, p);        // (the whole warp; the same in every lane)
-                p.end = !have;
-                if (lane == 0) ok = produce(n, p);
-                __syncwarp();
-                if (!have) break;
-                join.p = p;
-            }
-            if (a.split && lane == 0) {
-                join.parts = w.parts;
-                a.joins[blockIdx.x] = join;
+                const Piece* p = piece_at(n);
+                if (!p || p->end) break;
+                if (lane == 0) ok = produce(*p);
+                release(n);
             }
             if (lane == 0) {
                 // drain: every copy in flight lands before the CTA exits
@@ -1109,16 +1090,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             wait(bar(K::DRAIN), 0, drain);
             __syncwarp();
         } else if (warp == kGuard) {
-            // -------------------------------------------- V guard
-            int n = 0, item = 0;
-            bool ok = true;
+            // -------------------------------------------- the plan, and the V guard
+            // A piece is planned while the one before it is worked on (planned by the producer between two
+            // pieces' copies it held up each item by 3 to 8 thousand clocks).
+            Plan plan(a, lane, gridDim.x);
+            plan.begin();
+            Walk w;
+            w.start();
+            int n = 0, item = 0, np = 0;                  // V tiles and items seen; pieces published
+            auto publish = [&]() -> bool {
+                Piece p = {};
+                p.end = !w.next(plan, p);                 // (the whole warp; the same in every lane)
+                if (np >= kPieces && !__all_sync(0xffffffffu, wait(bar(K::PCEMPTY + np % kPieces), ((np - kPieces) / kPieces) & 1, ctl)))
+                    return false;
+                if (lane == 0) {
+                    const_cast<Piece*>(ring)[np % kPieces] = p;
+                    mbar_arrive(bar(K::PCFULL + np % kPieces));
+                }
+                ++np;
+                __syncwarp();
+                return true;
+            };
+            bool ok = publish();
             for (int m = 0; ok; ++m) {
-                const Piece* at = piece_at(m);
-                if (!at || at->end) break;
-                const Piece p = *at;
-                release(m);
-                const int it = item;
-                item += p.t1 > p.t0;
+                const Piece& p = ring[m % kPieces];
+                if (p.end) break;
+                if (p.t1 == p.t0) {
+                    ok = publish();
+                    continue;
+                }
+                const int it = item++;
                 // keys past `all` are not seen by every row of the item; L and beyond by none
                 const int all = p.s.L - p.s.Q + p.q0;
                 bool found = false;
@@ -1129,40 +1130,51 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     if (t == p.t0 && lane == 0) nonfinite[it & (kFlags - 1)] = 0;
                     __syncwarp();
                     if (r0 < kKeys) {
-                        uint8_t* base = smem + K::OFF_V + sv * K::TILE;
-                        for (int s = 0; s < K::SLABS; ++s)
-                            for (int x = r0 * 8 + lane; x < kKeys * 8; x += 32) {
-                                uint4* e16 = reinterpret_cast<uint4*>(base + s * K::SLAB + x * 16);
-                                if (x / 8 >= r1) {
-                                    *e16 = make_uint4(0, 0, 0, 0);
-                                    continue;
-                                }
-                                uint4 v = *e16;
-                                uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-                                bool bad = false;
+                        // 8 loads in flight a lane, one test for all of them (a loop of single loads and tests took
+                        // 8 to 12 thousand clocks a tile, four times a tile's MMAs, at the end of every item)
+                        for (int s = 0; s < K::SLABS; ++s) {
+                            uint8_t* base = smem + K::OFF_V + sv * K::TILE + s * K::SLAB;
+                            for (int x = r1 * 8 + lane; x < kKeys * 8; x += 32)
+                                *reinterpret_cast<uint4*>(base + x * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                            for (int x = r0 * 8 + lane; x < r1 * 8; x += 8 * 32) {
+                                uint4 v[8];
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    constexpr uint32_t I = Type<T>::INF;
-                                    if ((e[j] & I) == I) {
-                                        e[j] &= 0xffff0000u;
-                                        bad = true;
+                                for (int j = 0; j < 8; ++j)
+                                    v[j] = x + j * 32 < r1 * 8 ? *reinterpret_cast<const uint4*>(base + (x + j * 32) * 16)
+                                                               : make_uint4(0, 0, 0, 0);
+                                // an exponent of all ones carries into the sign's place
+                                constexpr uint32_t I = Type<T>::INF * 0x10001u, A = 0x80008000u - I;
+                                uint32_t bad = 0;
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    bad |= ((v[j].x & I) + A) | ((v[j].y & I) + A) | ((v[j].z & I) + A) | ((v[j].w & I) + A);
+                                if (!(bad & 0x80008000u)) continue;
+                                found = true;
+                                for (int j = 0; j < 8 && x + j * 32 < r1 * 8; ++j) {
+                                    uint32_t* e = reinterpret_cast<uint32_t*>(base + (x + j * 32) * 16);
+                                    for (int y = 0; y < 4; ++y) {
+                                        const uint32_t hit = ((e[y] & I) + A) & 0x80008000u;
+                                        e[y] &= ~((hit >> 15) * 0xffffu);
                                     }
-                                    if ((e[j] & (I << 16)) == (I << 16)) {
-                                        e[j] &= 0xffffu;
-                                        bad = true;
-                                    }
-                                }
-                                if (bad) {
-                                    *e16 = v;
-                                    found = true;
                                 }
                             }
+                        }
                         if (__any_sync(0xffffffffu, found) && lane == 0) nonfinite[it & (kFlags - 1)] = 1;
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
+                    if (t == p.t0) ok = publish();
                 }
+            }
+            if (a.split && lane == 0) {
+                Join join = {};
+                if (ok && np > 1) {
+                    join.p = ring[(np - 2) % kPieces];    // the last piece (the one behind it says `end`)
+                    join.parts = w.parts;
+                }
+                a.joins[blockIdx.x] = join;
             }
         }
     }
@@ -1320,6 +1332,10 @@ cudaError_t launch_prompt(const pkv_rows* q, const pkv_rows* k, const pkv_rows* 
     a.wide = rows::wide(a.out);
     // at most this many items (their number depends on the lengths, which the host does not see)
     const int64_t per = 2 * a.pb;
+    // (d <= 2^l, M = floor(2^(31 + l) / d) + 1: n M / 2^(31 + l) exceeds n / d by less than 2^-l <= 1 / d)
+    a.per_shift = 31;
+    while ((1u << (a.per_shift - 31)) < (uint32_t)per) ++a.per_shift;
+    a.per_mul = (uint32_t)(((uint64_t)1 << a.per_shift) / per + 1);
     const int64_t items = Hkv * std::min<int64_t>((int64_t)num_seqs * ((max_q_len + per - 1) / per),
                                                   num_q_rows / per + num_seqs);
     if (items > 0x7fffffff) return cudaErrorInvalidValue;
