@@ -476,6 +476,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ uint64_t f2pack(uint32_t a, uint32_t b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(a), "r"(b));
@@ -691,13 +696,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 };
                 if (!__all_sync(0xffffffffu, m > -INFINITY)) {
-                    // no reference yet (a piece's first tile): the largest of the first 32 keys, or where the row
-                    // sees none of them, of the tile.  (O and l are 0 so far, or NaN)
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    // no reference yet (a piece's first tile): the largest of the first 32 keys where all are seen, else
+                    // of the tile.  (O and l are 0 so far, or NaN)
+                    float top = -INFINITY;
+                    if (!masked) {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) mx[x & 3] = fmaxf(mx[x & 3], x <= rem ? __uint_as_float(sa[x]) : -INFINITY);
-                    float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (!__all_sync(0xffffffffu, top > -INFINITY || rem < 32)) top = maximum(0, kKeys);
+                        for (int x = 0; x < 32; x += 2) top = max3(top, __uint_as_float(sa[x]), __uint_as_float(sa[x + 1]));
+                    }
+                    if (!__all_sync(0xffffffffu, top > -INFINITY)) top = maximum(0, kKeys);
                     if (m == -INFINITY) m = top * sc + kHeadroom;
                 }
                 // (rare) a P of 64 keys at column c reaches 2: m rises by a whole number of octaves, and the P
@@ -1130,42 +1136,44 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     if (t == p.t0 && lane == 0) nonfinite[it & (kFlags - 1)] = 0;
                     __syncwarp();
                     if (r0 < kKeys) {
-                        // 8 loads in flight a lane, one test for all of them (a loop of single loads and tests took
-                        // 8 to 12 thousand clocks a tile, four times a tile's MMAs, at the end of every item)
-                        for (int s = 0; s < K::SLABS; ++s) {
-                            uint8_t* base = smem + K::OFF_V + sv * K::TILE + s * K::SLAB;
-                            for (int x = r1 * 8 + lane; x < kKeys * 8; x += 32)
-                                *reinterpret_cast<uint4*>(base + x * 16) = make_uint4(0, 0, 0, 0);
+                        // A short loop with few branches: code that runs once an item comes from L2, line by line (a
+                        // loop with 8 loads in flight took 5 to 8 thousand clocks, single loads tested one by one 8
+                        // to 12; a tile's MMAs take 2).  An exponent of all ones carries into the sign's place.
+                        uint8_t* base = smem + K::OFF_V + sv * K::TILE;
+                        constexpr uint32_t I = Type<T>::INF * 0x10001u, A = 0x80008000u - I;
 #pragma unroll 1
-                            for (int x = r0 * 8 + lane; x < r1 * 8; x += 8 * 32) {
-                                uint4 v[8];
+                        for (int x = r0 * 8 + lane; x < r1 * 8; x += 2 * 32) {
+                            uint32_t bad = 0;
 #pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    v[j] = x + j * 32 < r1 * 8 ? *reinterpret_cast<const uint4*>(base + (x + j * 32) * 16)
-                                                               : make_uint4(0, 0, 0, 0);
-                                // an exponent of all ones carries into the sign's place
-                                constexpr uint32_t I = Type<T>::INF * 0x10001u, A = 0x80008000u - I;
-                                uint32_t bad = 0;
+                            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    bad |= ((v[j].x & I) + A) | ((v[j].y & I) + A) | ((v[j].z & I) + A) | ((v[j].w & I) + A);
-                                if (!(bad & 0x80008000u)) continue;
+                                for (int s = 0; s < K::SLABS; ++s) {
+                                    const uint4 v = *reinterpret_cast<const uint4*>(base + s * K::SLAB + min(x + j * 32, r1 * 8 - 1) * 16);
+                                    bad |= ((v.x & I) + A) | ((v.y & I) + A) | ((v.z & I) + A) | ((v.w & I) + A);
+                                }
+                            if (bad & 0x80008000u) {
                                 found = true;
-                                for (int j = 0; j < 8 && x + j * 32 < r1 * 8; ++j) {
-                                    uint32_t* e = reinterpret_cast<uint32_t*>(base + (x + j * 32) * 16);
-                                    for (int y = 0; y < 4; ++y) {
-                                        const uint32_t hit = ((e[y] & I) + A) & 0x80008000u;
-                                        e[y] &= ~((hit >> 15) * 0xffffu);
+#pragma unroll 1
+                                for (int j = 0; j < 2 * K::SLABS; ++j) {
+                                    const int y = x + (j / K::SLABS) * 32;
+                                    uint32_t* e = reinterpret_cast<uint32_t*>(base + (j % K::SLABS) * K::SLAB + y * 16);
+                                    for (int z = 0; z < 4 && y < r1 * 8; ++z) {
+                                        const uint32_t hit = ((e[z] & I) + A) & 0x80008000u;
+                                        e[z] &= ~((hit >> 15) * 0xffffu);
                                     }
                                 }
                             }
                         }
+#pragma unroll 1
+                        for (int x = r1 * 8 + lane; x < kKeys * 8; x += 32)
+                            for (int s = 0; s < K::SLABS; ++s)
+                                *reinterpret_cast<uint4*>(base + s * K::SLAB + x * 16) = make_uint4(0, 0, 0, 0);
                         if (__any_sync(0xffffffffu, found) && lane == 0) nonfinite[it & (kFlags - 1)] = 1;
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
-                    if (t == p.t0) ok = publish();
+                    if (t == min(p.t0 + 1, p.t1 - 1)) ok = publish();   // (the copies are up to three tiles ahead)
                 }
             }
             if (a.split && lane == 0) {
