@@ -5,7 +5,11 @@
 // One launch of two kinds of CTAs: some take the query rows, one warp's share
 // each, the others 16 tokens' key and value rows.  Every row is read and
 // written once, so the bound is HBM for many tokens and the launch's latency
-// for few.
+// for few.  Measured: 7.7k prompt tokens of 32/8 heads of 128 into an FP8 cache,
+// 51 us = 3.3 TB/s (a window's chain slots -> rows -> angles, which the 16
+// resident warps of an SM hide by half; the q CTAs first 61 us, both kinds mixed
+// 56, rows prefetched to L2 before the slots are known 55); a decode step of 32
+// tokens 8 us.
 #include "rows.cuh"
 
 namespace pkv {

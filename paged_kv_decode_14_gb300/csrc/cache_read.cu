@@ -8,7 +8,8 @@
 // chunk holds consecutive elements of one token, and the 8 chunks of 8 tokens
 // are adjacent; a warp takes 4 tokens x 8 chunks of the head dimension, so
 // its loads cover whole 64-byte pieces and its stores whole 128-byte (or
-// longer) pieces of rows.
+// longer) pieces of rows.  Measured: 64k FP8 tokens of 8 heads of 128 to bf16,
+// 430 MB, 74 us = 5.8 TB/s (K and V in CTAs of their own, 16-byte stores: 87 us).
 #include <type_traits>
 
 #include "rows.cuh"

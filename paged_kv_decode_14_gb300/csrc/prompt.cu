@@ -25,16 +25,17 @@
 //
 // Roles (512 threads): warps 0-3 the softmax of row tile 0, warps 4-7 of row
 // tile 1, warps 8-11 the epilogue of both, warp 12 the producer, warps 13 and
-// 14 the MMA issuers of row tiles 0 and 1, warp 15 the V guard.  Per tile
-// issuer i runs  PV_i(t), first 64 keys as soon as their P is written, PV_i(t)
-// rest, S_i(t + 1), as one block, in turns with the other (0, 1, 0, 1, ...):
-// left alone, the MMAs of both interleave, both S finish together and the
+// 14 the MMA issuers of row tiles 0 and 1, warp 15 the plan and the V guard.
+// Per tile issuer i runs  PV_i(t), first 64 keys as soon as their P is written,
+// PV_i(t) rest, S_i(t + 1), as one block, in turns with the other (0, 1, 0, 1,
+// ...): left alone, the MMAs of both interleave, both S finish together and the
 // tensor core idles through two simultaneous softmaxes; in turns the row tiles
-// stay half a period apart (8k rows of 32 heads: 358 us; the first half's PV
-// ahead of the turn 395; no turns 440).  The last tile of an item is followed by the next
-// item's first S.  One thread's tcgen05 operations complete in order, so when
-// S_i(t + 1) signals, PV_i(t) is done and O_i may be rescaled, and S_i(t + 1)
-// overwrites P_i(t) only after PV_i(t) has read it.
+// stay half a period apart (8192 tokens of 32 heads, when this was measured:
+// 361 us; the first half's PV ahead of the turn 395; no turns 440).  The last
+// tile of an item is followed by the next item's first S.  One thread's tcgen05
+// operations complete in order, so when S_i(t + 1) signals, PV_i(t) is done and
+// O_i may be rescaled, and S_i(t + 1) overwrites P_i(t) only after PV_i(t) has
+// read it.
 //
 // The V guard makes keys that some rows do not see harmless: a weight of 0
 // times NaN or infinity is NaN, so rows of V past the sequence's end are
@@ -42,10 +43,17 @@
 // part of the item's rows see are replaced by 0 there and added back, row by
 // row, when the result is written (from global memory: rare).
 //
-// Few rows over many keys (fewer items than the SMs can share): the key tiles
-// of all items are laid end to end and cut into equal ranges, one per CTA; a
-// cut item leaves partial (O, m, l) in the workspace, joined in order by a
-// second kernel.  Every wait is bounded.
+// The items that do not fill a round (few rows over many keys: all of them) have
+// their key tiles laid end to end and cut into equal ranges, one per CTA; a cut
+// item leaves partial (O, m, l) in the workspace, joined in order by a second
+// kernel.  Every wait is bounded.
+//
+// Bound: a key tile of both row tiles takes about 2830 clocks, of which the MMAs
+// are 2080 (the rest is the chain softmax -> PV -> next S of a row tile), and a
+// change of item about 5000.  Measured (32/8 heads of 128, bf16): 8192 tokens
+// 351 us = 1560 TFLOP/s over the visible pairs, 0.81 of the measured burst rate;
+// 4 x 2048 tokens 133 us; 512-token chunks over 3 to 4 thousand keys 174 us;
+// up to 33 rows over 32k keys (fp16) 73 us = 3.6 TB/s.
 #include <cuda.h>
 
 #include <algorithm>
@@ -71,7 +79,7 @@ constexpr int kRegsSoftmax = 160, kRegsEpilogue = 112, kRegsOther = 80;
 static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOther == 4 * 128, "register file");
 constexpr int kProducer = 12, kMma = 13, kGuard = 15;   // (0-7: softmax, 8-11: epilogue)
 constexpr int kMinTiles = 2;               // key tiles that a CTA of a split range has at least
-constexpr int kCutCost = 10;               // what cutting a round of items costs, in key tiles (about 20 us)
+constexpr int kCutCost = 10;               // what cutting a round of items costs, in key tiles (about 14 us)
 constexpr int kFlags = 8;                  // items whose "non-finite V" flags are kept
 constexpr int kMaxSplit = 160;             // CTAs of a split launch (two workspace slots each)
 constexpr float kHeadroom = 4.f;           // octaves of m above the largest logit it was set by
@@ -160,7 +168,7 @@ struct Cfg {
 // tiles of the rest, fewer items than CTAs, laid end to end and cut into equal
 // ranges.  So long and short sequences, a last round that is not full and few
 // rows over long contexts all leave the CTAs within a tile or so of each other.
-// (4 prompts of 2048: in the order of the sequences 172 us, by tiles 152; 151 with the turns as they are now.)
+// (4 prompts of 2048: in the order of the sequences 172 us, by tiles 152.)
 //
 // The items of a sequence with at least tau tiles are its last blocks, and
 // their number has a closed form, so no list is kept: a lane stands for `chunk`

@@ -5,7 +5,8 @@
 //   y = x / sqrt(mean(x^2) + eps) * w                       (where a norm is asked for)
 //   (y_a, y_b) <- (y_a c - y_b s, y_b c + y_a s)            for every pair (a, b) of the rotated part
 // A row is read and written once, so the bound is HBM for many tokens and the
-// launch's latency for few.
+// launch's latency for few (8192 tokens of 40 heads of 128 bf16: 33 us = 5.1
+// TB/s; 32 tokens: 6 us).
 #include "rows.cuh"
 
 namespace pkv {

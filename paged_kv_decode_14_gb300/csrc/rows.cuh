@@ -339,7 +339,7 @@ struct Cursor {
 // for each other.  What bounds it beside HBM is the instructions of a group, so
 // pointers step from head to head.  (8192 tokens of 40 heads of 128 bf16, 168
 // MB: direct loads, a CTA a token with its angles behind a barrier, 52 us; this
-// with the addresses computed from scratch, 39 us.)
+// with the addresses computed from scratch, 39 us; as it is, 33 us = 5.1 TB/s.)
 template <typename T, int GS, int KIND, bool NORM>
 __device__ __forceinline__ void warp_rows(const View& qi, const View& qo, const View& ki, const View& ko, const T* qw,
                                           const T* kw, float eps, int D, const Rope& rope,
