@@ -181,6 +181,7 @@ struct Plan {
     int items, whole;           // all items; those dealt as a whole
     int tau, base, upto;        // the level being dealt: its tiles, items with more, items with as many or more
     int units, ctas;            // the rest: key tiles, CTAs that share them
+    int each_cta, longer;       // a CTA's units, and how many CTAs have one more
     int mine, before;           // of them this lane's and earlier lanes'
 
     __device__ __forceinline__ Plan(const Arg& a_, int lane_, int grid_) : a(a_), lane(lane_), grid(grid_) {}
@@ -243,32 +244,32 @@ struct Plan {
     }
     // The level that holds this item: the most tiles t with more than `item` items of at least t, at
     // or below the present level (the next one, mostly; else a search -- stepping through 64 levels
-    // took a join of 8k rows 170 us).
+    // took a join of 8k rows 170 us).  One call of count: every copy of its code comes from L2.
     __device__ __forceinline__ void level(int item) {
         if (item < upto) return;
-        int hi = tau - 1, lo = 0;                            // (count(0) is all of them)
-        int n = hi >= 0 ? count(hi) : 0;
-        if (n > item) {
-            lo = hi;
-        } else {
-            --hi;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (count(mid) > item) lo = mid;
-                else hi = mid - 1;
+        int lo = 0, hi = tau - 1;                            // (count(0) is all of them, count(tau) is upto)
+        base = upto;
+        upto = items;
+        for (int t = hi; lo < hi; t = (lo + hi + 1) >> 1) {
+            const int n = count(t);
+            if (n > item) {
+                lo = t;
+                upto = n;
+            } else {
+                hi = t - 1;
+                base = n;
             }
-            n = count(lo);
         }
         tau = lo;
-        upto = n;
-        base = count(lo + 1);
     }
     // before the first level: above the most tiles of any item
     __device__ __forceinline__ void top() {
-        int m = -1;
+        int m = -1, n = 0;
         each([&](int, const Seq& s) {
             if (s.Q > 0) m = max(m, tiles(s, blocks(s) - 1));
+            n += blocks(s);
         });
+        items = __reduce_add_sync(0xffffffffu, n) * a.Hkv;
         tau = __reduce_max_sync(0xffffffffu, m) + 1;
         base = upto = 0;
     }
@@ -285,7 +286,6 @@ struct Plan {
         one = Seq{0, 0, 0, 0};
         each([&](int, const Seq& s) { one = s; }, true);     // (reads the lengths)
         top();
-        items = count(0);
         whole = a.split ? items / grid * grid : items;
         units = ctas = 0;
     }
@@ -299,6 +299,8 @@ struct Plan {
         mine = n;
         units = __reduce_add_sync(0xffffffffu, n);
         ctas = min(grid, max(units / kMinTiles, items - whole));
+        each_cta = units / ctas;                             // (every item has a unit: at least 1)
+        longer = units - each_cta * ctas;
         // a round of whole items takes as long as its first, the longest; cutting it takes an equal
         // share, and about kCutCost tiles more for the parts and their join
         if (tau <= units / grid + kCutCost) {
@@ -373,7 +375,12 @@ struct Plan {
         });
         share(p, here);
     }
-    __device__ __forceinline__ int range(int c) const { return (int)((int64_t)units * c / ctas); }
+    __device__ __forceinline__ int range(int c) const { return each_cta * c + min(c, longer); }
+    // the CTA whose range ends at or behind unit u, the first one
+    __device__ __forceinline__ int cta_of_end(int u) const {
+        const int head = (each_cta + 1) * longer;
+        return (u <= head ? (u + each_cta) / (each_cta + 1) : longer + (u - head + each_cta - 1) / each_cta) - 1;
+    }
 };
 
 // A CTA's pieces in order: its whole items, then its range of the rest (planned
@@ -402,9 +409,7 @@ struct Walk {
         if (u >= end) return false;
         plan.unit(u, end - u, p);
         if (p.t0 == 0 && p.t1 < p.T) {
-            int x = c + 1;
-            while (plan.range(x + 1) < u + p.T) ++x;
-            parts = x - c + 1;
+            parts = plan.cta_of_end(u + p.T) - c + 1;
         }
         u += max(p.t1 - p.t0, 1);
         return true;
