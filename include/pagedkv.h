@@ -550,7 +550,8 @@ PKV_API pkv_status pkv_paged_kv_read(const pkv_cache* cache, const int32_t* bloc
  *
  * Precision: q.k and weights times V on the tensor cores in the inputs' type
  * with fp32 accumulation; the weights 2^(s - m) are rounded to the inputs'
- * type (bf16: 8 significant bits, fp16: 11), sums and statistics are fp32.
+ * type (bf16: 8 significant bits; fp16: 11 down to 2^-23 of the weight of the
+ * largest early logit), sums and statistics are fp32.
  * NaN or infinity in a key or value row reaches the queries that see it, and
  * no other.  Deterministic.  Reads nothing before the previous kernel on the
  * stream has completed.  The wait limit and hold flag of

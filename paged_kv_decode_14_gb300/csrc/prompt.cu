@@ -10,14 +10,16 @@
 //   S_i[128 rows, 128 keys] = Q_i . K_t^T      (A and B K-major in shared memory)
 //   P_i = 2^(S_i scale log2(e) - m), l += sum P_i    (one thread per row = TMEM lane)
 //   O_i[128 rows, D] += P_i . V_t              (A = P from TMEM, B MN-major in shared memory)
-// and out = O / l at the end.  m is the maximum of the row's first tile plus
-// 2^4 of headroom; after that no maximum is taken.  P below 2 has a clear top
-// exponent bit in either type, so one OR over the packed P of 64 keys tells
-// whether any reaches 2; only then (a logit 5 octaves above the first tile's
-// largest) m rises, by whole octaves (O and l are rescaled by exact powers of
-// 2), and those P are computed again.  P is rounded to the inputs' type because
-// both operands of one MMA have the same type; the headroom costs bf16 nothing
-// and leaves fp16 11 bits down to 2^-10 of the largest weight.
+// and out = O / l at the end.  m is set by the maximum of the row's first 32 keys
+// (of its first tile where they are masked); after that no maximum is taken.  P
+// is rounded to the inputs' type because both operands of one MMA have the same
+// type.  bf16: m is four octaves above that maximum, and P below 2 has a clear
+// top exponent bit, so one OR over the packed P of 64 keys tells whether any
+// reaches 2.  fp16, whose range is short: m is nine octaves below it, and the
+// largest bit pattern of 64 P tells whether any reaches 2^13, so that weights
+// keep 11 bits down to 2^-23 of the one that set m.  Only then (a logit 5 or 4
+// octaves above that one) m rises, by whole octaves (O and l are rescaled by
+// exact powers of 2), and those P are computed again.
 //
 // Q, K and V tiles arrive by tensor copies (TMA) in the 128-byte swizzle,
 // straight from strided rows: K-major operands for Q and K, an MN-major one
@@ -82,7 +84,6 @@ constexpr int kMinTiles = 2;               // key tiles that a CTA of a split ra
 constexpr int kCutCost = 10;               // what cutting a round of items costs, in key tiles (about 14 us)
 constexpr int kFlags = 8;                  // items whose "non-finite V" flags are kept
 constexpr int kMaxSplit = 160;             // CTAs of a split launch (two workspace slots each)
-constexpr float kHeadroom = 4.f;           // octaves of m above the largest logit it was set by
 constexpr int kPieces = 4;                 // pieces of work the producer may be ahead
 
 struct Join;
@@ -544,12 +545,31 @@ struct Type;
 template <>
 struct Type<__nv_bfloat16> {
     static constexpr uint32_t INF = 0x7f80u;              // exponent bits of infinities and NaN
+    static constexpr float HEADROOM = 4.f;                // octaves of m above the logit it is set by
+    // any P of 64 (two a word) at 2 or above: the top exponent bit
+    static __device__ __forceinline__ bool high(const uint32_t (&v)[32]) {
+        uint32_t any[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int x = 4; x < 32; ++x) any[x & 3] |= v[x];
+        return ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
+    }
     static constexpr uint32_t id(int M, int N, bool b_mn) { return idesc_bf16_f32(M, N, false, b_mn); }
     static __device__ __forceinline__ float get(const uint8_t* p) { return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p)); }
 };
 template <>
 struct Type<__half> {
     static constexpr uint32_t INF = 0x7c00u;
+    static constexpr float HEADROOM = -9.f;               // (P = 2^9 there: 11 bits down to 2^-14)
+    // at 2^13 or above: the largest bit pattern (P has no sign), whose halves carry into the sign's place
+    static __device__ __forceinline__ bool high(const uint32_t (&v)[32]) {
+        uint32_t any[2] = {v[0], v[1]};
+#pragma unroll
+        for (int x = 2; x < 32; x += 4) {
+            any[0] = __vimax3_u16x2(any[0], v[x], v[x + 1]);
+            if (x + 2 < 32) any[1] = __vimax3_u16x2(any[1], v[x + 2], v[x + 3]);
+        }
+        return ((__vmaxu2(any[0], any[1]) + 0x10001000u) & 0x80008000u) != 0;
+    }
     static constexpr uint32_t id(int M, int N, bool b_mn) { return idesc_f16_f32(M, N, false, b_mn); }
     static __device__ __forceinline__ float get(const uint8_t* p) { return __half2float(*reinterpret_cast<const __half*>(p)); }
 };
@@ -717,13 +737,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                         for (int x = 0; x < 32; x += 2) top = max3(top, __uint_as_float(sa[x]), __uint_as_float(sa[x + 1]));
                     }
                     if (!__all_sync(0xffffffffu, top > -INFINITY)) top = maximum(0, kKeys);
-                    if (m == -INFINITY) m = top * sc + kHeadroom;
+                    if (m == -INFINITY) m = top * sc + Type<T>::HEADROOM;
                 }
-                // (rare) a P of 64 keys at column c reaches 2: m rises by a whole number of octaves, and the P
+                // (rare) a P of 64 keys at column c reaches the limit: m rises by a whole number of octaves, and the P
                 // written in this tile, O and l are scaled down by as many (exact but for what falls below
                 // the type's range, far below the new maximum)
                 auto raise_ref = [&](float target, int c) {
-                    const float inc = target + kHeadroom > m ? ceilf(target + kHeadroom - m) : 0.f;
+                    const float inc = target + Type<T>::HEADROOM > m ? ceilf(target + Type<T>::HEADROOM - m) : 0.f;
                     const int k = (int)fminf(inc, 127.f);
                     const float alpha = k < 127 ? __uint_as_float((uint32_t)(127 - k) << 23) : 0.f;
                     if (c > 0) {                          // the first half's P is being used: it ends in O
@@ -758,12 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                     acc = f2add(acc, f2add(ca, cb));
                 };
-                // The P of 64 keys is written once none is known to reach 2.  True: written.
+                // The P of 64 keys is written once none is known to reach the limit.  True: written.
                 auto write = [&](uint64_t acc, int c, const uint32_t (&v)[32], bool force) -> bool {
-                    uint32_t any[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                    for (int x = 4; x < 32; ++x) any[x & 3] |= v[x];
-                    const bool high = ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
+                    const bool high = Type<T>::high(v);
                     if (__any_sync(0xffffffffu, row_ok && high) && !force) return false;
                     tmem_st32u(scol + (c >> 1), v);
                     float a0, a1;

@@ -261,3 +261,58 @@ def test_cache_past_2_31_bytes():
     sc = kr.float().abs().view(3, 16, Hkv, D).amax((1, 3)) / 448
     tol = kr.float().abs() * (2.0 ** -4 + 2.0 ** -8) + (sc * 2.0 ** -10).repeat_interleave(16, 0)[:, :, None]
     assert ((a[0].float() - kr.float()).abs() <= tol).all()
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with a workspace of its own, as one after the other."""
+    Q, L, Hq, Hkv, D = [70, 3], [3000, 700], 8, 2, 128
+    sets, want = [], []
+    for seed in range(2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        q = torch.randn(sum(Q), Hq, D, generator=g, device="cuda").bfloat16()
+        k, v = (torch.randn(sum(L), Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+        out, lse = torch.empty_like(q), torch.empty(sum(Q), Hq, device="cuda")
+        sets.append((q, k, v, out, lse, nat.make_prompt_workspace()))
+    ql, kl, pos, rope = i32(Q), i32(L), i32(list(range(sum(L)))), nat.Rope(D, interleaved=True)
+
+    def work(s, stream=None):
+        q, k, v, out, lse, ws = s
+        kr, _ = nat.qk_norm_rope(k, None, pos, rope, eps=1e-6, stream=stream)
+        nat.prompt_attention(q, kr, v, ql, kl, max(Q), 0.1, out=out, lse=lse, workspace=ws, stream=stream)
+        return kr
+
+    for s in sets:
+        work(s)
+        want.append((s[3].clone(), s[4].clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        keep = [work(s, st) for _ in range(3) for s, st in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for s, (out, lse) in zip(sets, want):
+            assert torch.equal(s[3], out) and torch.equal(s[4], lse)
+        del keep
+
+
+def test_workspace_is_left_between_calls_of_any_size():
+    """One workspace for split and whole calls in turn: nothing of the last call is taken over."""
+    ws = nat.make_prompt_workspace()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for Q, L in (([40], [5000]), ([3, 3], [3, 3]), ([1] * 9, [1300] * 9), ([600], [700]), ([40], [5000])):
+        q = torch.randn(sum(Q), 6, 64, generator=g, device="cuda").half()
+        k, v = (torch.randn(sum(L), 3, 64, generator=g, device="cuda").half() for _ in range(2))
+        out, lse = nat.prompt_attention(q, k, v, i32(Q), i32(L), max(Q), 0.125, workspace=ws)
+        check(out, lse, *reference(q, k, v, Q, L, 0.125))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("octaves", [6, 12, 18])
+def test_one_early_key_above_many(dtype, octaves):
+    """A first key whose weight is 2^octaves of every other's: the small weights, together far more or less
+    than it, keep their bits (they are equal: a rounding that is off is off by as much in the sum)."""
+    def edit(q, k, v):
+        q[:] = 1.0
+        k[:] = 0.0
+        k[0] = octaves * math.log(2.0) / 16         # logit 64 x this x scale, rounded to the type
+        v[1:] = v[1:].abs()
+    run([3, 130], [9000, 1200], 4, 2, 64, dtype, scale=0.25, edit=edit)
