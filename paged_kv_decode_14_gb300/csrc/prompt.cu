@@ -53,9 +53,9 @@
 // Bound: a key tile of both row tiles takes about 2830 clocks, of which the MMAs
 // are 2080 (the rest is the chain softmax -> PV -> next S of a row tile), and a
 // change of item about 5000.  Measured (32/8 heads of 128, bf16): 8192 tokens
-// 351 us = 1560 TFLOP/s over the visible pairs, 0.81 of the measured burst rate;
-// 4 x 2048 tokens 133 us; 512-token chunks over 3 to 4 thousand keys 174 us;
-// up to 33 rows over 32k keys (fp16) 73 us = 3.6 TB/s.
+// 353 us = 1560 TFLOP/s over the visible pairs, 0.81 of the measured burst rate;
+// 4 x 2048 tokens 134 us; 512-token chunks over 3 to 4 thousand keys 176 us;
+// up to 33 rows over 32k keys (fp16) 75 us = 3.6 TB/s.
 #include <cuda.h>
 
 #include <algorithm>
