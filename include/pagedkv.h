@@ -553,7 +553,8 @@ PKV_API pkv_status pkv_paged_kv_read(const pkv_cache* cache, const int32_t* bloc
  * type (bf16: 8 significant bits; fp16: 11 down to 2^-23 of the weight of the
  * largest early logit), sums and statistics are fp32.
  * NaN or infinity in a key or value row reaches the queries that see it, and
- * no other.  Deterministic.  Reads nothing before the previous kernel on the
+ * no other (an infinite value as NaN where its weight is so small that it
+ * rounds to 0).  Deterministic.  Reads nothing before the previous kernel on the
  * stream has completed.  The wait limit and hold flag of
  * pkv_debug_set_wait_limit apply to it too (the join's rows are undefined after
  * a wait that ran out, as all of the call's results are).
