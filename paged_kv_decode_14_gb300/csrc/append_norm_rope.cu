@@ -277,7 +277,9 @@ __device__ __forceinline__ void append_window(const AppendArg& a, const Rope& ro
                 member[tid] = in ? t + tid : -1;
             }
             __syncthreads();
-            if (member[15] < 0) {
+            const bool partial = member[15] < 0;
+            __syncthreads();                                // (read by every thread before the scan writes it)
+            if (partial) {
                 // the run is short of the block: the block's other tokens may be anywhere in the call
                 scan_slots(a, tid, [&](int64_t y, int64_t z) {
                     z -= s;

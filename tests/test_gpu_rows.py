@@ -304,6 +304,34 @@ def test_append_norm_rope_fp8(D, Hkv, kind, values):
         assert torch.equal(torch.nan_to_num(got[keep], 1e9), torch.nan_to_num(before[keep], 1e9))
 
 
+@pytest.mark.parametrize("D,Hkv", [(128, 8), (64, 3)])
+@pytest.mark.parametrize("order", ["interleaved", "ends", "shuffled", "reversed"])
+def test_started_blocks_gathered_from_all_over_the_call(D, Hkv, order):
+    """Whole blocks whose tokens are not consecutive, offset 15 among the scattered ones: every block's owner
+    finds its last row by the scan, not in its run.  Many calls: every one as the first append's, bit for bit."""
+    nb = 96
+    blocks = np.random.default_rng(5).permutation(nb).tolist()
+    if order == "interleaved":                # token by token through the blocks in turn
+        lst = [b * 16 + o for o in range(16) for b in blocks]
+    elif order == "ends":                     # runs of 15, all the last rows behind them
+        lst = [b * 16 + o for b in blocks for o in range(15)] + [b * 16 + 15 for b in blocks]
+    else:
+        lst = [b * 16 + o for b in blocks for o in range(16)]
+        np.random.default_rng(6).shuffle(lst) if order == "shuffled" else lst.reverse()
+    slots = torch.tensor(lst, dtype=torch.int64, device="cuda")
+    T = slots.numel()
+    _, k, v = make(T, (1, Hkv, Hkv), D, torch.bfloat16, T)
+    base = new_cache(nb, Hkv, D, "fp8")
+    want = clone(base)
+    nat.append_rope(want, k.contiguous(), v.contiguous(), slots, fp8_scales_from_values=True)
+    k_out = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    for _ in range(50):
+        got = clone(base)
+        k_out.fill_(9.0)
+        nat.append_norm_rope(got, None, k, v, slots, k_out=k_out, fp8_scales_from_values=True)
+        assert same_cache(want, got) and torch.equal(k_out, k)
+
+
 def test_append_bad_slots_are_reported():
     D, Hkv, nb = 64, 2, 8
     slots = torch.tensor([3, nb * 16, 5, 1 << 40], dtype=torch.int64, device="cuda")
