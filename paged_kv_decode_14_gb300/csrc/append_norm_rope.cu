@@ -321,8 +321,11 @@ using namespace rows;
 template <int E, int D, bool FRESH, int KIND, bool NORM>
 static cudaError_t launch_one(unsigned grid, size_t smem, cudaStream_t st, const AppendArg& a, const Rope& r) {
     static std::atomic<uint64_t> set{0};
-    return launch_pdl_bigsmem(set, append_norm_rope_kernel<E, D, FRESH, KIND, NORM>, dim3(grid), dim3(kThreads), smem, st,
-                              a, r);
+    constexpr int GS = lanes_of<__nv_bfloat16>(D);
+    // (the K/V part's most: 16 tokens' (cos, sin), and the rows at once in fp32)
+    constexpr size_t kv = 16 * 8 * (D / 2) + kThreads / GS * D * 4, q = rows_smem_most<__nv_bfloat16, GS>();
+    return launch_pdl_bigsmem(set, append_norm_rope_kernel<E, D, FRESH, KIND, NORM>, dim3(grid), dim3(kThreads),
+                              DynSmem(smem, kv > q ? kv : q), st, a, r);
 }
 
 cudaError_t launch_append_norm_rope(const pkv_cache& c, const pkv_rows* q_in, const pkv_rows* q_out, const pkv_rows* k,

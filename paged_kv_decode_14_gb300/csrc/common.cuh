@@ -67,32 +67,43 @@ __host__ inline cudaError_t launch_pdl(void (*kern)(Args...), dim3 grid, dim3 bl
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// A launch's dynamic shared memory, and the most that any launch of its kernel asks for.
+struct DynSmem {
+    size_t bytes, most;
+    DynSmem(size_t n) : bytes(n), most(n) {}               // every launch asks for as much
+    DynSmem(size_t n, size_t m) : bytes(n), most(m) {}
+};
+
 // launch_pdl for a kernel with more than 48 KiB of dynamic shared memory.
 // The function attribute that allows it is set once per device (`done` holds
 // one bit per device, static in the caller, one per kernel): setting it on
-// every launch costs a driver call for nothing.  A launch refused after the
-// attribute was lost (a device reset) sets it again and retries once.
+// every launch costs a driver call for nothing.  It is set to the most that
+// the kernel can ask for, whatever this launch does: a launch that is refused
+// would end a stream capture, and host threads whose first launches differ
+// would lower each other's limit.  A launch refused after the attribute was
+// lost (a device reset) sets it again and retries once.
 template <typename... Args>
 __host__ inline cudaError_t launch_pdl_bigsmem(std::atomic<uint64_t>& done, void (*kern)(Args...), dim3 grid,
-                                               dim3 block, size_t smem, cudaStream_t st, Args... args) {
+                                               dim3 block, DynSmem smem, cudaStream_t st, Args... args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (smem.bytes > smem.most) return cudaErrorInvalidValue;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
     const bool set = bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0;
     if (!set) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem.most);
         if (e != cudaSuccess) return e;
         if (bit) done.fetch_or(bit, std::memory_order_release);
     }
-    e = launch_pdl(kern, grid, block, smem, st, args...);
+    e = launch_pdl(kern, grid, block, smem.bytes, st, args...);
     if (e != cudaSuccess && set) {
         (void)cudaGetLastError();
         done.fetch_and(~bit, std::memory_order_release);
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem.most);
         if (e != cudaSuccess) return e;
         done.fetch_or(bit, std::memory_order_release);
-        e = launch_pdl(kern, grid, block, smem, st, args...);
+        e = launch_pdl(kern, grid, block, smem.bytes, st, args...);
     }
     return e;
 }

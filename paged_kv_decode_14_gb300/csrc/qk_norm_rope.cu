@@ -41,8 +41,8 @@ static cudaError_t launch_rows(const View& qi, const View& qo, const View& ki, c
     return for_kind(rope_kind<T>(rope, GS), eps >= 0.f, [&](auto kind, auto norm) {
         static std::atomic<uint64_t> set{0};
         return launch_pdl_bigsmem(set, qk_norm_rope_kernel<T, GS, decltype(kind)::value, decltype(norm)::value>,
-                                  dim3(rows_ctas(units, num_sms)), dim3(kThreads), smem, st, qi, qo, ki, ko, (const T*)qw,
-                                  (const T*)kw, eps, D, rope, positions, T_, units, (int)(smem / kWarps));
+                                  dim3(rows_ctas(units, num_sms)), dim3(kThreads), DynSmem(smem, rows_smem_most<T, GS>()), st, qi,
+                                  qo, ki, ko, (const T*)qw, (const T*)kw, eps, D, rope, positions, T_, units, (int)(smem / kWarps));
     });
 }
 

@@ -295,6 +295,12 @@ __host__ inline size_t rows_smem(const Rope& r, int D) {
     const size_t stage = r.pairs > 0 && !r.interleaved && r.pairs % Chunk<T>::N ? (size_t)(32 / GS) * D * 4 : 0;
     return kWarps * (kRing + (((size_t)r.pairs * 8 + 15) / 16 * 16) + (stage + 15) / 16 * 16);
 }
+// The most of it: a row fills its lanes' chunks, all of it rotated.
+template <typename T, int GS>
+__host__ constexpr size_t rows_smem_most() {
+    constexpr size_t D = GS * kSets * Chunk<T>::N;
+    return kWarps * (kRing + D / 2 * 8 + 32 / GS * D * 4);
+}
 
 // Where a warp is in its share: a group of 32 / GS rows of one tensor's heads,
 // of one token.  A token's groups are q's, then k's.

@@ -2,6 +2,10 @@
 decode, graphs and streams, timeouts, scales at the ends of fp32, addresses past 2^31."""
 
 import math
+import os
+import subprocess
+import sys
+import textwrap
 
 import numpy as np
 import pytest
@@ -316,3 +320,76 @@ def test_one_early_key_above_many(dtype, octaves):
         k[0] = octaves * math.log(2.0) / 16         # logit 64 x this x scale, rounded to the type
         v[1:] = v[1:].abs()
     run([3, 130], [9000, 1200], 4, 2, 64, dtype, scale=0.25, edit=edit)
+
+
+def in_a_new_process(code):
+    """Runs code where no kernel has been launched before (what a first launch sets lasts as long as the process)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    head = "import sys, threading, torch\nfrom paged_kv_decode_14_gb300 import _native as nat\n"
+    r = subprocess.run([sys.executable, "-c", head + textwrap.dedent(code)], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stdout[-2000:] + r.stderr[-2000:]
+
+
+def test_a_larger_call_captured_after_a_smaller_first_one():
+    """One instance of a kernel wants shared memory by the rotation, the head size and whether there are query rows;
+    a call that wants more than the first did is captured like any other."""
+    in_a_new_process("""
+        bf16, dev = torch.bfloat16, "cuda"
+        pos = torch.arange(40, device=dev, dtype=torch.int32)
+        slots = torch.arange(40, device=dev)
+        q, k = torch.randn(40, 8, 128, device=dev).to(bf16), torch.randn(40, 2, 128, device=dev).to(bf16)
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
+        w = torch.randn(40, 2, 256, device=dev).to(bf16)
+        wo = torch.empty_like(w)
+        zero = lambda: torch.zeros(4, 2, 16 * 128, device=dev, dtype=bf16)
+        cache = nat.PagedKVCache(4, 2, 128, "bf16", k=zero(), v=zero())
+        rope = nat.Rope(128)
+        nat.append_norm_rope(cache, None, k, k, slots, pos, rope, eps=1e-6)             # no query rows
+        nat.qk_norm_rope(w[:, :, :136], None, pos, nat.Rope(2))
+        def work():
+            nat.append_norm_rope(cache, q, k, k, slots, pos, rope, eps=1e-6, q_out=qo, k_out=ko)
+            nat.qk_norm_rope(w, None, pos, nat.Rope(250), q_out=wo)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            work()
+        g.replay()
+        got = [x.clone() for x in (qo, ko, wo)]
+        for x in (qo, ko, wo):
+            x.zero_()
+        work()
+        assert all(torch.equal(x, y) for x, y in zip(got, (qo, ko, wo)))
+        print("ok")
+    """)
+
+
+def test_first_calls_of_several_sizes_from_host_threads():
+    """Four host threads, each with a stream of its own, whose calls of one kernel instance differ in what they want."""
+    in_a_new_process("""
+        failed = []
+        def many(n, wait):
+            try:
+                stream = torch.cuda.Stream()
+                x = torch.randn(16, 2, 256, device="cuda").to(torch.bfloat16)
+                pos = torch.arange(16, device="cuda", dtype=torch.int32)
+                rope, out = nat.Rope(2 + 84 * n), torch.empty_like(x)
+                torch.cuda.synchronize()
+                want = None
+                wait.wait()
+                for _ in range(2000):
+                    nat.qk_norm_rope(x, None, pos, rope, q_out=out, stream=stream)
+                stream.synchronize()
+                want, _ = nat.qk_norm_rope(x, None, pos, rope)
+                torch.cuda.synchronize()
+                assert torch.equal(want, out)
+            except Exception as e:
+                failed.append(repr(e))
+        wait = threading.Barrier(4)
+        threads = [threading.Thread(target=many, args=(n, wait)) for n in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not failed, failed
+        print("ok")
+    """)
