@@ -227,20 +227,47 @@ struct Rotator {
 };
 
 // x *= w / sqrt(mean(x^2) + eps) over the row held by a group of GS lanes
-// (lanes past the row hold zeros); sums and statistics in fp32.
+// (lanes past the row hold zeros); sums and statistics in fp32.  Squares leave
+// fp32's range long before the values do (from 2^64 up, from 2^-75 down): where
+// some row's mean is out of the range that is sure to be right, the warp takes
+// its rows times a power of two that brings the row's largest value, or
+// sqrt(eps), near 1 (1 for the rows that were in range: the same bits).
 template <typename T, int GS>
 __device__ __forceinline__ void rms_norm(float (&x)[kSets][Chunk<T>::N], const uint4 (&w)[kSets], bool weighted,
                                          float eps, float inv_dim) {
     constexpr int N = Chunk<T>::N;
-    float ss[kSets] = {0.f, 0.f};
+    auto mean_square = [&](float plus) {
+        float ss[kSets] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < N; ++e)
+        for (int e = 0; e < N; ++e)
 #pragma unroll
-        for (int j = 0; j < kSets; ++j) ss[j] = fmaf(x[j][e], x[j][e], ss[j]);
-    float sum = ss[0] + ss[1];
+            for (int j = 0; j < kSets; ++j) ss[j] = fmaf(x[j][e], x[j][e], ss[j]);
+        float sum = ss[0] + ss[1];
 #pragma unroll
-    for (int o = GS / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, GS);
-    const float inv = rsqrtf(fmaf(sum, inv_dim, eps));
+        for (int o = GS / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, GS);
+        return fmaf(sum, inv_dim, plus);
+    };
+    float mean = mean_square(eps);
+    const bool sure = mean >= 0x1p-100f && mean <= 0x1p120f;
+    if (!__all_sync(0xffffffffu, sure)) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+#pragma unroll
+            for (int j = 0; j < kSets; ++j) top = fmaxf(top, fabsf(x[j][e]));
+#pragma unroll
+        for (int o = GS / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, GS));
+        top = fmaxf(top, sqrtf(eps));
+        // (an infinite row, and one of zeros without eps, stay as the formula has them)
+        const bool plain = sure || !(top > 0.f) || !(top < INFINITY);
+        const float f = plain ? 1.f : __uint_as_float((uint32_t)max(254 - (int)(__float_as_uint(top) >> 23), 1) << 23);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+#pragma unroll
+            for (int j = 0; j < kSets; ++j) x[j][e] *= f;
+        mean = mean_square(eps * f * f);
+    }
+    const float inv = rsqrtf(mean);
 #pragma unroll
     for (int j = 0; j < kSets; ++j) {
         float g[N];

@@ -147,6 +147,62 @@ def test_rows_nan_and_inf_stay_in_their_rows():
     assert torch.isfinite(out[:3]).all() and torch.isfinite(out[4:6]).all() and torch.isfinite(out[3, :2]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-31, 1e-6, 1e37])
+def test_norm_of_rows_whose_squares_leave_fp32(dtype, D, eps):
+    """Rows from fp32's largest values to its subnormals, side by side in every token (a warp holds several): the
+    norm is the formula's, in rows and in the pass that writes the cache."""
+    dt, eps = TYPES[dtype], float(np.float32(eps))
+    scales = [1.0, 1e20, 2e37, 1e-12, 1e-25, 1e-37, 1e-3]
+    T, H = 5, len(scales)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    # (no element below 2^-7 of a row's unit: a result stays in fp32's normal range or is covered below)
+    x = torch.randn(T, H, D, generator=g, device="cuda")
+    x = torch.where(x.abs() < 2.0 ** -7, 2.0 ** -7, x)
+    x = (x * torch.tensor(scales, device="cuda")[:, None]).to(dt)
+    w = (1 + 0.3 * torch.randn(D, generator=g, device="cuda")).to(dt)
+
+    def check(got, ref, size):
+        # Results below the normal range (fp32's and bf16's alike): half a subnormal step of the type, and in fp32
+        # h = 2^-150 for each rounding of the chain there: two before the weight (at most 2.2 here), one after it, and
+        # one for either product of the rotation: (2 h 2.2 + h) sqrt(2) + 2 h < 10 h.
+        low = HALF[dt] * 2.0 ** -126 + 10 * 2.0 ** -150
+        bad = (got.double() - ref).abs() > HALF[dt] * ref.abs() + 2 * CHAIN * size + low
+        assert not bad.any(), (bad.nonzero()[0].tolist(), got[bad][0].item(), ref[bad][0].item())
+
+    for weight in (None, w):
+        out, _ = nat.qk_norm_rope(x, None, q_weight=weight, eps=eps)
+        check(out, *ref_rows(x, weight, eps, None, None))
+    pos = torch.arange(T, device="cuda", dtype=torch.int32) * 77
+    rope = nat.Rope(D // 2)
+    out, _ = nat.qk_norm_rope(x, None, pos, rope, w, eps=eps)
+    check(out, *ref_rows(x, w, eps, pos, rope))
+    if dtype == "bf16" and D in (64, 128):
+        c = new_cache(1, H, D, "bf16")
+        k_out, slots = torch.empty_like(x), torch.arange(T, device="cuda")
+        nat.append_norm_rope(c, None, x, x, slots, pos, rope, None, w, eps, k_out=k_out)
+        assert torch.equal(k_out, out) and torch.equal(page_rows(c.k, D, 2)[0, :, :T].transpose(0, 1), out)
+
+
+def test_norm_of_zero_infinite_and_nan_rows():
+    """As the formula has them: 0 / 0 is NaN, finite / infinite is 0, and the rows beside them are untouched."""
+    x = torch.randn(3, 8, 128, device="cuda")
+    want, _ = nat.qk_norm_rope(x, None, eps=0.0)
+    odd = x.clone()
+    odd[1, 2] = 0.0
+    odd[1, 4, 7] = math.inf
+    odd[2, 0, 9] = math.nan
+    out, _ = nat.qk_norm_rope(odd, None, eps=0.0)
+    assert torch.isnan(out[1, 2]).all() and torch.isnan(out[2, 0]).all()
+    assert torch.isnan(out[1, 4, 7]) and (out[1, 4, :7] == 0).all() and (out[1, 4, 8:] == 0).all()
+    same = torch.ones(3, 8, dtype=torch.bool, device="cuda")
+    same[1, 2] = same[1, 4] = same[2, 0] = False
+    assert torch.equal(out[same], want[same])
+    out, _ = nat.qk_norm_rope(odd, None, eps=1e-6)
+    assert (out[1, 2] == 0).all()
+
+
 # ------------------------------------------------------------------ append and read
 
 
