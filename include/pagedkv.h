@@ -439,7 +439,8 @@ PKV_API pkv_status pkv_rope_init(pkv_rope* rope, int32_t rotary_dim, int32_t int
  *   y = x / sqrt(mean(x^2) + eps) * w       (norm_eps >= 0; w = 1 where the weight is NULL)
  *   y = rotation of y at the token's position (rope not NULL and rotary_dim > 0)
  * in fp32 and rounded once (nearest even) to the rows' type.  The angle of
- * any 32-bit position is exact to 2^-32 of a turn.
+ * any 32-bit position, position * inv_freq[i] modulo a turn, is good to 2^-31
+ * of a turn before it is rounded to fp32 (at most 2^-26 of a turn more).
  *
  *   q_in, q_out    query rows and where they go (the same views: in place)
  *   k_in, k_out    key rows, both NULL if there are none; otherwise as q

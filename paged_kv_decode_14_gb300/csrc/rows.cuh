@@ -4,6 +4,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "common.cuh"
@@ -34,9 +35,10 @@ __host__ inline bool wide(const View& v) {
 
 // The rotation of a launch.  turn[i] is pair i's advance per position as a
 // fraction of a full turn in 64-bit fixed point, so position * turn wraps at
-// whole turns by itself: the angle of any 32-bit position keeps 32 fraction
-// bits with one integer multiply and no 64-bit floating point (whose rate on
-// this chip is a small fraction of the integer rate).
+// whole turns by itself: the angle of any 32-bit position is good to 2^-31 of a
+// turn (its top 32 bits are used; the advance is off by 2^-64, see turn_of) with
+// one integer multiply and no 64-bit floating point (whose rate on this chip is
+// a small fraction of the integer rate).  It is then rounded to fp32.
 struct Rope {
     uint64_t turn[PKV_ROPE_MAX_PAIRS];
     float magnitude;
@@ -277,6 +279,20 @@ __device__ __forceinline__ void rms_norm(float (&x)[kSets][Chunk<T>::N], const u
     }
 }
 
+// Host: radians per position -> the fraction of a turn, in units of 2^-64.  The
+// position multiplies its error, and 53 bits of the product f / 2 pi, or of 1 / 2 pi
+// itself, would leave 2^-25 of a turn at position 2^31 for f = 1 (a whole turn
+// for f near 1e9): the product and its rounding error are both kept.
+__host__ inline uint64_t turn_of(double f) {
+    constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;   // 1 / 2 pi
+    const double x = std::fabs(f);
+    const volatile double product = x * hi;                // (rounded here: not to be fused into what uses it)
+    const double p = product, e = std::fma(x, hi, -p) + x * lo;
+    const double part = (p - std::floor(p)) * 0x1p32, top = std::floor(part);  // (exact)
+    const uint64_t t = ((uint64_t)top << 32) + (uint64_t)(int64_t)std::nearbyint((part - top) * 0x1p32 + e * 0x1p64);
+    return f < 0 ? 0 - t : t;
+}
+
 // Host: the kernel's form of a rotation.
 __host__ inline Rope rope_arg(const pkv_rope* r, bool negate) {
     Rope a = {};
@@ -286,15 +302,7 @@ __host__ inline Rope rope_arg(const pkv_rope* r, bool negate) {
     a.interleaved = r->interleaved != 0;
     a.magnitude = r->magnitude;
     a.negate = negate;
-    for (int i = 0; i < a.pairs; ++i) {
-        // radians per position -> the fraction of a turn, in units of 2^-64
-        const double t = r->inv_freq[i] * 0.15915494309189533577;
-        double f = t - (double)(long long)t;
-        if (f < 0) f += 1.0;
-        // (scaled by 2^63, not 2^64: a conversion to a signed 64-bit value is defined there;
-        // a tiny negative fraction rounds up to a whole turn, which is none)
-        a.turn[i] = f >= 1.0 ? 0 : (uint64_t)(int64_t)(f * 0x1p63) << 1;
-    }
+    for (int i = 0; i < a.pairs; ++i) a.turn[i] = turn_of(r->inv_freq[i]);
     return a;
 }
 

@@ -147,6 +147,32 @@ def test_rows_nan_and_inf_stay_in_their_rows():
     assert torch.isfinite(out[:3]).all() and torch.isfinite(out[4:6]).all() and torch.isfinite(out[3, :2]).all()
 
 
+@pytest.mark.parametrize("first", [1.0, 0.3, 1000.1, 123456.789, 9.9e8, -1.0, -1e-17, -77777.7, 6.283185307179586])
+def test_angles_of_far_positions(first):
+    """A caller's own frequencies at positions up to the ends of 32 bits, against position * inv_freq modulo a turn in
+    60 digits."""
+    from decimal import Decimal, localcontext
+    pairs, far = 8, [2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, 2 ** 20, 1, -1, 0]
+    rope = nat.Rope(2 * pairs)
+    for i in range(pairs):
+        rope.desc.inv_freq[i] = first / (1 + 0.7 * i)
+    pos = torch.tensor(far, dtype=torch.int64).to(torch.int32).cuda()
+    x = torch.zeros(len(far), 1, 16, device="cuda")
+    x[..., :pairs] = 1.0                                    # (cos, sin) of every pair
+    out, _ = nat.qk_norm_rope(x, None, pos, rope)
+    with localcontext() as ctx:
+        ctx.prec = 60
+        turn = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+        for t, p in enumerate(far):
+            for i in range(pairs):
+                a = Decimal(p) * Decimal(rope.desc.inv_freq[i])
+                a = float(a - (a / turn).to_integral_value() * turn)
+                # the angle: 2 pi (2^-31 + 2^-26) = 2^-23.3; cos and sin: an ulp of results up to 1, 2^-24; the two
+                # roundings of the rotation: 2^-24.  Together below 2^-22.
+                for got, want in ((out[t, 0, i], math.cos(a)), (out[t, 0, pairs + i], math.sin(a))):
+                    assert abs(float(got) - want) <= 2.0 ** -22, (p, rope.desc.inv_freq[i], float(got), want)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("D", [64, 80, 128, 256])
 @pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-31, 1e-6, 1e37])
