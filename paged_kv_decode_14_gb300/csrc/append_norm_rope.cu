@@ -271,15 +271,13 @@ __device__ __forceinline__ void append_window(const AppendArg& a, const Rope& ro
             if (kind[x] != 1) continue;
             const int64_t t = t0 + x, s = wslot[x];
             __syncthreads();
+            bool in = true;
             if (tid < 16) {
-                bool in = true;
                 for (int y = 1; y <= tid; ++y) in = in && wslot[x + y] == s + y;
                 member[tid] = in ? t + tid : -1;
             }
-            __syncthreads();
-            const bool partial = member[15] < 0;
-            __syncthreads();                                // (read by every thread before the scan writes it)
-            if (partial) {
+            // (the barrier carries the answer: a read of member[15] behind it could meet the scan's write)
+            if (__syncthreads_or(!in)) {
                 // the run is short of the block: the block's other tokens may be anywhere in the call
                 scan_slots(a, tid, [&](int64_t y, int64_t z) {
                     z -= s;
