@@ -393,3 +393,106 @@ def test_first_calls_of_several_sizes_from_host_threads():
         assert not failed, failed
         print("ok")
     """)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("starts", [None, [3, 15, 0, 31]])
+def test_keys_or_values_alone_and_no_lse(dtype, starts):
+    """The optional outputs of the C entry points left out: the others are the same bits."""
+    lib, bf16, D, Hkv = nat.lib(), torch.bfloat16, 128, 2
+    c = new_cache(40, Hkv, D, dtype)
+    lens, wide = [33, 1, 160, 17], 12
+    tables = torch.randperm(40, device="cuda").to(torch.int32).repeat(2)[:4 * wide].view(4, wide).contiguous()
+    ln, st = i32(lens), None if starts is None else i32(starts)
+    T = sum(lens)
+    want = nat.read_cache(c, tables, ln, T, st)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    view = lambda t: nat._ROWS.pack(t.data_ptr(), t.stride(0), t.stride(1), t.shape[1])
+    stream = torch.cuda.current_stream().cuda_stream
+    for one in range(2):
+        out = torch.zeros(T, Hkv, D, dtype=bf16, device="cuda")
+        rows = [None, None]
+        rows[one] = view(out)
+        assert lib.pkv_paged_kv_read(nat.ctypes.byref(c.desc()), ptr(tables), wide, ptr(st), ptr(ln), 4, T, *rows, 0, None,
+                                     stream) == 0
+        assert torch.equal(out, want[one])
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn(40, 6, D, generator=g, device="cuda").to(bf16)
+    k, v = (torch.randn(3000, Hkv, D, generator=g, device="cuda").to(bf16) for _ in range(2))
+    ws = nat.make_prompt_workspace()
+    for w in (None, ws):                                   # whole; split along the keys and joined
+        want, _ = nat.prompt_attention(q, k, v, i32([40]), i32([3000]), 40, 0.1, workspace=w)
+        out, a, b = torch.zeros_like(q), i32([40]), i32([3000])
+        assert lib.pkv_prompt_attention(view(q), view(k), view(v), view(out), None, 0, D, 40, 3000, ptr(a), ptr(b), None,
+                                        None, 1, 40, 0.1, ptr(w), 0 if w is None else w.numel(), None, stream) == 0
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype,top", [("fp16", 25), ("bf16", 28)])
+@pytest.mark.parametrize("Q,L", [([300], [300]), ([20, 3], [6000, 500])])
+def test_logits_up_to_the_stated_limit(dtype, top, Q, L):
+    """Logits of either sign up to 2^top, where a logit's own fp32 step is several octaves: the weights are 0 or
+    those of equal keys, late maxima among them."""
+    D, Hq, Hkv = 128, 4, 2
+    g = torch.Generator(device="cuda").manual_seed(top)
+    dt = {"fp16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    # q . k / 8 = 128 * 2^(top - 14) k / 8 for |k| <= 2^10: steps of 2^(top - 10)
+    q = torch.full((sum(Q), Hq, D), 2.0 ** (top - 14), device="cuda").to(dt)
+    k = torch.randint(-256, 257, (sum(L), Hkv, 1), generator=g, device="cuda").float().mul(4).expand(-1, -1, D)
+    v = torch.randn(sum(L), Hkv, D, generator=g, device="cuda").to(dt)
+    k = k.to(dt).contiguous()
+    out, lse = nat.prompt_attention(q, k, v, i32(Q), i32(L), max(Q), 0.125, workspace=nat.make_prompt_workspace())
+    ref, rlse, size = reference(q, k, v, Q, L, 0.125)
+    half = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    # as check(), with weights that are equal but for their rounding
+    assert ((out.double() - ref).abs() <= half * ref.abs() + (half + 2.0 ** -13) * size * (1 + half) + 2.0 ** -24).all()
+    # scale log2(e), its product with the logit, m + log2(l) and the product with ln 2: four roundings of 2^-24
+    assert ((lse.double() - rlse).abs() <= 2.0 ** -22 * rlse.abs() + 2.0 ** -13).all()
+
+
+def test_attention_in_place_of_its_queries():
+    for Q, L, w in (([300, 40], [300, 700], None), ([40, 1], [3000, 2000], nat.make_prompt_workspace())):
+        q = torch.randn(sum(Q), 8, 64, device="cuda").half()
+        k, v = (torch.randn(sum(L), 2, 64, device="cuda").half() for _ in range(2))
+        want, lse = nat.prompt_attention(q, k, v, i32(Q), i32(L), max(Q), 0.125, workspace=w)
+        nat.prompt_attention(q, k, v, i32(Q), i32(L), max(Q), 0.125, out=q, workspace=w)
+        assert torch.equal(q, want)
+
+
+def test_calls_from_host_threads():
+    """Four host threads, each with a stream, a cache and a workspace of its own, as one after the other."""
+    import threading
+    D, Hq, Hkv, T = 128, 8, 2, 70
+    rope = nat.Rope(D, scaling="bands", factor=4.0, original_len=64)
+    lens, tables = i32([T]), i32([[0, 1, 2, 3, 4]])
+    pos, slots = torch.arange(T, device="cuda", dtype=torch.int32), torch.arange(T, device="cuda")
+    sets = [[x.clone() for x in make(T, (Hq, Hkv, Hkv), D, torch.bfloat16, seed)] for seed in range(4)]
+    caches = [[new_cache(5, Hkv, D, "fp8", seed) for _ in range(2)] for seed in range(4)]
+    spaces = [nat.make_prompt_workspace() for _ in range(4)]
+    failed = []
+
+    def work(n, cache, stream):
+        q, k, v = sets[n]
+        qo = nat.append_norm_rope(cache, q, k, v, slots, pos, rope, eps=1e-6, fp8_scales_from_values=True, stream=stream)
+        kr, vr = nat.read_cache(cache, tables, lens, T, stream=stream)
+        return (qo, kr, vr) + nat.prompt_attention(qo, kr, vr, lens, lens, T, 0.1, workspace=spaces[n], stream=stream)
+
+    want = [work(n, caches[n][0], None) for n in range(4)]
+    torch.cuda.synchronize()
+
+    def many(n):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(100):
+                got = work(n, caches[n][1], stream)
+            stream.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(got, want[n]))
+        except Exception as e:
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=many, args=(n,)) for n in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
