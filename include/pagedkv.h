@@ -88,7 +88,7 @@ typedef enum pkv_kv_dtype { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1 } pkv_kv_dtype;
 #define PKV_DEVERR_TIMEOUT 8    /* a bounded wait inside a kernel expired */
 #define PKV_DEVERR_RANGE 16     /* pkv_paged_prefill: a finite V value of magnitude >= 65536;
                                    pkv_paged_attention, FP8 cache on the tensor cores: a V scale
-                                   above 255 */
+                                   above 255; pkv_prompt_attention: finite logits past their limit */
 
 /* One paged cache ("startup policy": fixed for its lifetime). */
 typedef struct pkv_cache {
@@ -551,8 +551,12 @@ PKV_API pkv_status pkv_paged_kv_read(const pkv_cache* cache, const int32_t* bloc
  *
  * Precision: q.k and weights times V on the tensor cores in the inputs' type
  * with fp32 accumulation; the weights 2^(s - m) are rounded to the inputs'
- * type (bf16: 8 significant bits; fp16: 11 down to 2^-23 of the weight of the
- * largest early logit), sums and statistics are fp32.
+ * type (bf16: 8 significant bits; fp16: 11 down to 2^-22 of the weight of the
+ * logit that last set m, which is the largest of a row's first keys or a later
+ * one 4 octaves or more above it), sums and statistics are fp32.  Finite logits
+ * scale q.k may reach 2^28 (bf16) or 2^25 (fp16) in magnitude; from about 1.4
+ * times that on, fp32 cannot place the weights beside m: PKV_DEVERR_RANGE is
+ * set and the row's results are unspecified.
  * NaN or infinity in a key or value row reaches the queries that see it, and
  * no other (an infinite value as NaN where its weight is so small that it
  * rounds to 0).  Deterministic.  Reads nothing before the previous kernel on the

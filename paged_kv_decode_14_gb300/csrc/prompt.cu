@@ -17,7 +17,7 @@
 // top exponent bit, so one OR over the packed P of 64 keys tells whether any
 // reaches 2.  fp16, whose range is short: m is nine octaves below it, and the
 // largest bit pattern of 64 P tells whether any reaches 2^13, so that weights
-// keep 11 bits down to 2^-23 of the one that set m.  Only then (a logit 5 or 4
+// keep 11 bits down to 2^-22 of the one that set m.  Only then (a logit 5 or 4
 // octaves above that one) m rises, by whole octaves (O and l are rescaled by
 // exact powers of 2), and those P are computed again.
 //
@@ -546,6 +546,9 @@ template <>
 struct Type<__nv_bfloat16> {
     static constexpr uint32_t INF = 0x7f80u;              // exponent bits of infinities and NaN
     static constexpr float HEADROOM = 4.f;                // octaves of m above the logit it is set by
+    // |m| from which its roundings (half of fp32's step at m each, up to three of them) may leave P, l or O
+    // their range: 2^29, three times 16 octaves below it
+    static constexpr float LIMIT = 0x1p29f;
     // any P of 64 (two a word) at 2 or above: the top exponent bit
     static __device__ __forceinline__ bool high(const uint32_t (&v)[32]) {
         uint32_t any[4] = {v[0], v[1], v[2], v[3]};
@@ -560,6 +563,7 @@ template <>
 struct Type<__half> {
     static constexpr uint32_t INF = 0x7c00u;
     static constexpr float HEADROOM = -9.f;               // (P = 2^9 there: 11 bits down to 2^-14)
+    static constexpr float LIMIT = 0x1p26f;               // three times 2 octaves below it: P from 2^3 to 2^15
     // at 2^13 or above: the largest bit pattern (P has no sign), whose halves carry into the sign's place
     static __device__ __forceinline__ bool high(const uint32_t (&v)[32]) {
         uint32_t any[2] = {v[0], v[1]};
@@ -738,6 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                     if (!__all_sync(0xffffffffu, top > -INFINITY)) top = maximum(0, kKeys);
                     if (m == -INFINITY) m = top * sc + Type<T>::HEADROOM;
+                    // (too far below 0 is only seen here: m rises)
+                    if (row_ok && m <= -Type<T>::LIMIT && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
                 }
                 // (rare) a P of 64 keys at column c reaches the limit: m rises by a whole number of octaves, and the P
                 // written in this tile, O and l are scaled down by as many (exact but for what falls below
@@ -834,6 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                 }
             }
             if (!ok) break;
+            // (a reference so large that fp32 cannot place the weights beside it is reported)
+            const float size = fabsf(m);
+            if (row_ok && size >= Type<T>::LIMIT && size < INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
             // this piece's sums go to the epilogue (1 / l) and to memory (lse, or the part's m and l)
             const bool tiles = t1 > t0, sees = lim >= 0;
             // (an item of a single tile gets here before its PV: the epilogue may still hold the last item's)

@@ -441,13 +441,36 @@ def test_logits_up_to_the_stated_limit(dtype, top, Q, L):
     k = torch.randint(-256, 257, (sum(L), Hkv, 1), generator=g, device="cuda").float().mul(4).expand(-1, -1, D)
     v = torch.randn(sum(L), Hkv, D, generator=g, device="cuda").to(dt)
     k = k.to(dt).contiguous()
-    out, lse = nat.prompt_attention(q, k, v, i32(Q), i32(L), max(Q), 0.125, workspace=nat.make_prompt_workspace())
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = nat.make_prompt_workspace()
+    out, lse = nat.prompt_attention(q, k, v, i32(Q), i32(L), max(Q), 0.125, workspace=ws, device_error=err)
+    assert nat.read_device_error(err) == 0
     ref, rlse, size = reference(q, k, v, Q, L, 0.125)
     half = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
     # as check(), with weights that are equal but for their rounding
     assert ((out.double() - ref).abs() <= half * ref.abs() + (half + 2.0 ** -13) * size * (1 + half) + 2.0 ** -24).all()
     # scale log2(e), its product with the logit, m + log2(l) and the product with ln 2: four roundings of 2^-24
     assert ((lse.double() - rlse).abs() <= 2.0 ** -22 * rlse.abs() + 2.0 ** -13).all()
+
+
+@pytest.mark.parametrize("dtype,top", [("fp16", 25), ("bf16", 28)])
+@pytest.mark.parametrize("where", ["first", "late", "negative", "negative first"])
+def test_logits_past_the_stated_limit_are_reported(dtype, top, where):
+    """Twice the limit and more, at a row's first key, at its last, or with the other sign in all of them or the first
+    128; in rows of one head only.  Infinite logits are not reported: they have their own results."""
+    dt = {"fp16": torch.float16, "bf16": torch.bfloat16}[dtype]
+    q = torch.full((200, 4, 128), 2.0 ** (top - 14), device="cuda").to(dt)
+    k, v = torch.zeros(200, 2, 128, device="cuda").to(dt), torch.randn(200, 2, 128, device="cuda").to(dt)
+    err, n = torch.zeros(1, dtype=torch.int32, device="cuda"), i32([200])
+    nat.prompt_attention(q, k, v, n, n, 200, 0.125, device_error=err)
+    assert nat.read_device_error(err) == 0
+    at = {"first": slice(0, 1), "late": slice(199, 200), "negative": slice(0, 200), "negative first": slice(0, 128)}[where]
+    k[at, 1] = -2.0 ** 11 if "negative" in where else 2.0 ** 11
+    nat.prompt_attention(q, k, v, n, n, 200, 0.125, device_error=err)
+    assert nat.read_device_error(err) == nat.DEVERR_RANGE
+    k[at, 1] = -math.inf if "negative" in where else math.inf
+    nat.prompt_attention(q, k, v, n, n, 200, 0.125, device_error=err)
+    assert nat.read_device_error(err) == 0
 
 
 def test_attention_in_place_of_its_queries():
