@@ -546,7 +546,8 @@ def prompt_attention(q, k, v, q_lens, kv_lens, max_q_len: int, scale: float, out
     value rows (bf16 or fp16; q [Tq, Hq, D], k and v [Tk, Hkv, D], views are
     fine).  Returns (out, lse): new tensors unless given; lse fp32 [Tq, Hq],
     natural logarithm.  With starts, rows outside every sequence are not
-    written."""
+    written.  Without a workspace (make_prompt_workspace) a few rows over long
+    contexts run on a few SMs only."""
     device, dtype, shape = _device_of(q, "q"), q.dtype, q.shape
     if len(shape) != 3 or (dtype is not torch.bfloat16 and dtype is not torch.float16):
         raise ValueError("q must be [rows, heads, head_dim] in bfloat16 or float16")

@@ -6,10 +6,12 @@
 // each, the others 16 tokens' key and value rows.  Every row is read and
 // written once, so the bound is HBM for many tokens and the launch's latency
 // for few.  Measured: 7.7k prompt tokens of 32/8 heads of 128 into an FP8 cache,
-// 51 us = 3.3 TB/s (a window's chain slots -> rows -> angles, which the 16
-// resident warps of an SM hide by half; the q CTAs first 61 us, both kinds mixed
-// 56, rows prefetched to L2 before the slots are known 55); a decode step of 32
-// tokens 8 us.
+// 48.5 us = 3.6 TB/s, a bf16 one 44 us; a decode step of 32 tokens 5.0 us, and 16.7
+// us where FP8 scales come from the values (a scan of the slots for every token
+// whose block's first slot is not in its window).  Prompts are held up by a
+// window's chain slots -> rows -> angles, which the 16 resident warps of an SM hide
+// by half (with replays of one call 51 us; the q CTAs first 61, both kinds mixed
+// 56, rows prefetched to L2 before the slots are known 55).
 #include "rows.cuh"
 
 namespace pkv {

@@ -53,9 +53,14 @@
 // Bound: a key tile of both row tiles takes about 2830 clocks, of which the MMAs
 // are 2080 (the rest is the chain softmax -> PV -> next S of a row tile), and a
 // change of item about 5000.  Measured (32/8 heads of 128, bf16): 8192 tokens
-// 353 us = 1560 TFLOP/s over the visible pairs, 0.81 of the measured burst rate;
-// 4 x 2048 tokens 134 us; 512-token chunks over 3 to 4 thousand keys 176 us;
-// up to 33 rows over 32k keys (fp16) 75 us = 3.6 TB/s.
+// 366 us = 1500 TFLOP/s over the visible pairs, 0.78 of the measured burst rate
+// (354 to 374 over boxes: the power cap); 4 x 2048 tokens 130 us; 512-token chunks
+// over 3 to 4 thousand keys 173 us; up to 33 rows over 32k keys (fp16) 72 us = 3.7
+// TB/s.  All for logits of standard deviation 1: at 2, 3 and 5 a row of some warp
+// is past m in many steps, and 4 x 2048 tokens take 228, 273 and 303 us.  At the
+// clock that explains 8192 tokens, the tiles and changes of item of the busiest CTA
+// leave some 20 us of 4 x 2048 and of the chunks unexplained (among it the first
+// plan and chain, 8 us in a launch of one tile, and the join's launch).
 #include <cuda.h>
 
 #include <algorithm>

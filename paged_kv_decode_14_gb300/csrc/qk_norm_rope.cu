@@ -5,8 +5,10 @@
 //   y = x / sqrt(mean(x^2) + eps) * w                       (where a norm is asked for)
 //   (y_a, y_b) <- (y_a c - y_b s, y_b c + y_a s)            for every pair (a, b) of the rotated part
 // A row is read and written once, so the bound is HBM for many tokens and the
-// launch's latency for few (8192 tokens of 40 heads of 128 bf16: 33 us = 5.1
-// TB/s; 32 tokens: 6 us).
+// launch's latency for few (8192 tokens of 40 heads of 128 bf16: half of a head
+// rotated in the interleaved layout 29 us = 5.8 TB/s, with a norm and the whole
+// head rotated 32 us, with a norm and pairs across a part of a head 40 to 49 us;
+// 32 tokens: 3.5 us).
 #include "rows.cuh"
 
 namespace pkv {
