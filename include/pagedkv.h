@@ -526,9 +526,11 @@ PKV_API pkv_status pkv_paged_kv_read(const pkv_cache* cache, const int32_t* bloc
  * later chunks attend rows read back by pkv_paged_kv_read; fp16; any group
  * size).  With a bf16 cache either may be used: pkv_paged_prefill reads the
  * pages itself and holds its weights to 11 significant bits; this one needs the
- * rows, holds them to 8 in bf16, and takes 130 us for four prompts of 2048
- * tokens (32/8 heads of 128) whose logits spread by about 1 where that one takes
- * 191, but 273 us where they spread by 3.  Query i (0 <= i < Q_b) of sequence b and head h sees keys
+ * rows and holds them to 8 in bf16.  Four prompts of 2048 tokens (32/8 heads of
+ * 128): here 130 us where their logits have a standard deviation of 1, and 228
+ * or 273 where it is 2 or 3; there 190 to 192 us.
+ *
+ * Query i (0 <= i < Q_b) of sequence b and head h sees keys
  * j = 0 .. L_b - Q_b + i of kv-head h / G:
  *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j).
  * A query that sees no key (L_b - Q_b + i < 0) gets out = 0 and lse = -inf.
