@@ -88,7 +88,9 @@ typedef enum pkv_kv_dtype { PKV_KV_BF16 = 0, PKV_KV_FP8_E4M3 = 1 } pkv_kv_dtype;
 #define PKV_DEVERR_TIMEOUT 8    /* a bounded wait inside a kernel expired */
 #define PKV_DEVERR_RANGE 16     /* pkv_paged_prefill: a finite V value of magnitude >= 65536;
                                    pkv_paged_attention, FP8 cache on the tensor cores: a V scale
-                                   above 255; pkv_prompt_attention: finite logits past their limit */
+                                   above 255; pkv_prompt_attention, pkv_paged_attention_window and
+                                   _tree: finite logits past their limit */
+#define PKV_DEVERR_NO_BLOCKS 32 /* pkv_block_tables_update: not enough free blocks for a request */
 
 /* One paged cache ("startup policy": fixed for its lifetime). */
 typedef struct pkv_cache {
@@ -582,6 +584,124 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, co
                                         int32_t max_q_len, float scale, void* workspace, size_t workspace_bytes,
                                         int32_t* device_error, void* stream);
 
+/* ------------------------------------------------------------------ a step on the GPU
+ *
+ * Entry points for serving loops whose state stays on the GPU from step to step (in a CUDA graph, for
+ * instance): masked attention over the cache, block tables and slots from request lengths, and the accepted path of
+ * a tree of drafted tokens.
+ */
+
+/*
+ * Attention over the paged cache with a sliding window, in which the first `sinks` tokens stay visible: query i
+ * (0 <= i < Q_b) of sequence b stands at position p = L_b - Q_b + i and sees position j of kv-head h / G iff
+ *     j <= p  and  (j > p - window  or  j < sinks):
+ *     out = sum_j softmax_j(scale * q . k_j) v_j,   lse = ln sum_j exp(scale * q . k_j).
+ * From single tokens (decode) over verify windows to prompts and prompt chunks, bf16 and FP8 caches.  A window of at
+ * least L_b is plain causal attention.
+ *
+ *   q, out         bf16 rows of num_q_rows queries, num_heads = Hq = G * Hkv, G <= 128; q's strides positive.  out
+ *                  may be q (the same view)
+ *   lse            optional device fp32 [num_q_rows][Hq]
+ *   block_tables   as for pkv_paged_attention; entries of blocks that no query sees are never read, so blocks
+ *                  behind the window may have been given back
+ *   context_lens, q_lens   device int32 [num_seqs], 0 <= q_lens[b] <= context_lens[b]
+ *   q_starts       device int64 [num_seqs], each sequence's first row of q and out, or NULL: packed.  Rows
+ *                  outside every sequence are left as they were
+ *   max_q_len      host upper bound of q_lens, >= 1
+ *   window         >= 1;  sinks >= 0
+ *   scale          finite, > 0
+ *   workspace      >= pkv_masked_workspace_size() bytes, 16-byte aligned, zeroed once (pkv_workspace_init), not
+ *                  shared by concurrent calls (or by graphs that may run at the same time).  Its first 4 bytes are
+ *                  the device error word.  After PKV_DEVERR_TIMEOUT zero it again before reusing it.
+ * A sequence with a bad length, a table row that is too short, or rows outside num_q_rows sets PKV_DEVERR_LENGTH
+ * and its rows are left as they were; a bad block id sets PKV_DEVERR_BLOCK_ID and the results that see it are
+ * unspecified.
+ *
+ * Precision: q . k in bf16 (FP8 codes widened exactly, the page's scale applied in fp32) with fp32 accumulation;
+ * weights rounded to bf16 for the product with V (8 significant bits; FP8: after the page's scale has been applied in
+ * fp32), their sum in fp32 before that.  Finite logits scale * q . k may reach 2^28 in magnitude; from about 1.4 times
+ * that on PKV_DEVERR_RANGE is set and the row's results are unspecified.  NaN or infinity in a key or value row
+ * reaches the queries that see it, and no other (an infinite value as NaN where its weight rounds to 0).
+ * Deterministic.  One launch; it reads nothing before the previous kernel on the stream has completed, and lets the
+ * next start once it has.  The wait limit and hold flag of pkv_debug_set_wait_limit apply.
+ */
+PKV_API size_t pkv_masked_workspace_size(void);
+PKV_API pkv_status pkv_paged_attention_window(const pkv_cache* cache, const pkv_rows* q, const pkv_rows* out, float* lse,
+                                              int64_t num_q_rows, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                              const int32_t* context_lens, const int32_t* q_lens, const int64_t* q_starts,
+                                              int32_t num_seqs, int32_t max_q_len, int32_t window, int32_t sinks,
+                                              float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same for a tree of drafted tokens: the Q_b queries of sequence b are the nodes of its tree, whose keys and
+ * values lie in the last Q_b positions of its context, in the same order.  Node i sees every position below
+ * L_b - Q_b, and node j (at L_b - Q_b + j) iff bit j of its mask is set: usually its ancestors and itself.  A
+ * node that sees nothing gets out = 0 and lse = -inf.
+ *
+ *   tree_mask      device int32 [num_q_rows][mask_words], a row for each row of q: bit j % 32 of word j / 32;
+ *                  bits at and past Q_b are ignored.  32 * mask_words >= max_q_len
+ * Everything else as above, but that every block of a sequence's context is read (the positions that a rotation of the
+ * nodes needs are the caller's: the depth in the tree).
+ */
+PKV_API pkv_status pkv_paged_attention_tree(const pkv_cache* cache, const pkv_rows* q, const pkv_rows* out, float* lse,
+                                            int64_t num_q_rows, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                            const int32_t* context_lens, const int32_t* q_lens, const int64_t* q_starts,
+                                            int32_t num_seqs, int32_t max_q_len, const int32_t* tree_mask,
+                                            int32_t mask_words, float scale, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/*
+ * Block tables, slots and positions from request lengths: the device-side counterpart of a block manager's step,
+ * for requests that share no blocks.  Request b grows by grow[b] tokens, or, where grow[b] < 0, drops its last
+ * -grow[b] ones; blocks that are no longer needed go back to the pool, and blocks that are come from it.
+ *
+ *   block_tables   device int32 [num_seqs][max_blocks_per_seq], updated: entries of new blocks, and -1 for dropped ones
+ *   context_lens   device int32 [num_seqs], tokens before the call, updated to those after it
+ *   grow           device int32 [num_seqs]
+ *   free_blocks, free_count   the pool: a stack of block ids, device int32 [num_blocks], of which the first
+ *                  *free_count are free.  Updated.
+ *   slots          device int64 [num_rows]: the slots of the new tokens, packed by request (max(grow, 0) rows
+ *                  each), as the appends take them
+ *   positions      optional device int32 [num_rows]: their positions
+ *   granted        optional device int32 [num_seqs]: tokens that a request has got (grow, or 0): the q_lens of
+ *                  the step's attention
+ *   row_starts     optional device int64 [num_seqs]: its first row, granted or not: the q_starts of it
+ *
+ * Dropped blocks are pushed first, the last request's last block first; then new ones are popped, the first
+ * request's first block first: a call with the negated changes restores pool and tables exactly.  Dropped entries
+ * that are negative (given back earlier, behind a window) are skipped.
+ * A request is refused, and stays as it was, if the blocks it and the requests before it need are more than are
+ * free (PKV_DEVERR_NO_BLOCKS; requests that need none are not), if its rows do not fit in num_rows, or if its
+ * length would leave 0 .. 16 * max_blocks_per_seq (PKV_DEVERR_LENGTH).  Its rows get slot -1 (which the appends
+ * skip).  Rows behind the last request's are left as they were.  A block id outside [0, num_blocks) that is taken
+ * from the pool or given back sets PKV_DEVERR_BLOCK_ID: the former's entry becomes -1, the latter is not pushed.
+ * A count outside [0, num_blocks] sets PKV_DEVERR_LENGTH and every change is refused.
+ * num_seqs <= 8192.  One launch; deterministic.
+ */
+PKV_API pkv_status pkv_block_tables_update(int32_t* block_tables, int32_t max_blocks_per_seq, int32_t* context_lens,
+                                           const int32_t* grow, int32_t num_seqs, int32_t* free_blocks,
+                                           int32_t* free_count, int64_t num_blocks, int64_t* slots, int32_t* positions,
+                                           int32_t* granted, int64_t* row_starts, int64_t num_rows,
+                                           int32_t* device_error, void* stream);
+
+/*
+ * The accepted path of a verified tree, moved into place: the K and V of node path[i] of sequence b (at position
+ * L_b - Q_b + path[i]) go to position L_b - Q_b + i, for i < path_lens[b].  The other nodes' positions are left as
+ * they are; pkv_block_tables_update drops them (grow = path_lens - q_lens).
+ *
+ *   path           device int32 [num_seqs][max_path], strictly ascending nodes (a parent stands before its
+ *                  children), 0 <= path[i] < Q_b; path_lens[b] <= min(Q_b, max_path)
+ *   context_lens, q_lens   as for pkv_paged_attention_tree (before the drop)
+ * FP8: codes that stay in their block move unchanged; between blocks a code becomes e4m3_rne_satfinite(code *
+ * scale of its block / scale of the new one), in IEEE fp32.  Page scales are not changed.
+ * A sequence with a bad length or path sets PKV_DEVERR_LENGTH and is left as it was; a bad block id sets
+ * PKV_DEVERR_BLOCK_ID and its rows are not moved.  One launch.
+ */
+PKV_API pkv_status pkv_paged_kv_keep_path(const pkv_cache* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* context_lens, const int32_t* q_lens, const int32_t* path,
+                                          int32_t max_path, const int32_t* path_lens, int32_t num_seqs,
+                                          int32_t* device_error, void* stream);
+
 /*
  * Read and clear a device error word: either the first 4 bytes of an
  * attention workspace or an append's device_error.  Synchronises `stream`.
@@ -599,7 +719,7 @@ PKV_API pkv_status pkv_read_device_error(void* error_word, int32_t* code, void* 
  * down.  A non-NULL hold_flag (device int32) makes the kernel wait for
  * *hold_flag != 0 before its first K/V copy: a flag that nothing sets makes
  * that wait run out.  The settings are process-wide and apply to every
- * later pkv_paged_attention(_noalloc), pkv_paged_prefill and
+ * later pkv_paged_attention(_noalloc, _window, _tree), pkv_paged_prefill and
  * pkv_prompt_attention launch (not to the CUDA-core kernel, which has no
  * waits) until they are set again; not for concurrent use.
  */

@@ -24,6 +24,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "wo
           4: "CUDA error", 5: "device-side index or length error", 6: "device-side wait timed out",
           7: "no free cache block and none evictable", 8: "unknown (or already registered) sequence id"}
 DEVERR_BLOCK_ID, DEVERR_LENGTH, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_RANGE = 1, 2, 4, 8, 16
+DEVERR_NO_BLOCKS = 32
 
 _lock = threading.Lock()
 _lib = None
@@ -121,6 +122,17 @@ def lib():
             L.pkv_prompt_attention.restype = c.c_int
             L.pkv_prompt_attention.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, i32, i32,
                                                c.c_float, vp, c.c_size_t, vp, vp]
+            L.pkv_masked_workspace_size.restype = c.c_size_t
+            L.pkv_masked_workspace_size.argtypes = []
+            masked = [pc, vp, vp, vp, i64, vp, i32, vp, vp, vp, i32, i32]
+            L.pkv_paged_attention_window.restype = c.c_int
+            L.pkv_paged_attention_window.argtypes = masked + [i32, i32, c.c_float, vp, c.c_size_t, vp]
+            L.pkv_paged_attention_tree.restype = c.c_int
+            L.pkv_paged_attention_tree.argtypes = masked + [vp, i32, c.c_float, vp, c.c_size_t, vp]
+            L.pkv_block_tables_update.restype = c.c_int
+            L.pkv_block_tables_update.argtypes = [vp, i32, vp, vp, i32, vp, vp, i64, vp, vp, vp, vp, i64, vp, vp]
+            L.pkv_paged_kv_keep_path.restype = c.c_int
+            L.pkv_paged_kv_keep_path.argtypes = [pc, vp, i32, vp, vp, vp, i32, vp, i32, vp, vp]
             L.pkv_copy_blocks.restype = c.c_int
             L.pkv_copy_blocks.argtypes = [c.POINTER(CacheDesc), vp, i32, vp, vp, vp]
             L.pkv_debug_set_wait_limit.restype = None
@@ -568,6 +580,128 @@ def prompt_attention(q, k, v, q_lens, kv_lens, max_q_len: int, scale: float, out
           None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.numel() * workspace.element_size(), _error_word(device_error, device))
     return out, lse
+
+
+# ------------------------------------------------------------------ a step on the GPU
+
+
+def make_masked_workspace(device="cuda", stream=None):
+    """A workspace for attention_window and attention_tree on the given device, zeroed on its current stream (or
+    `stream`): calls on other streams wait for that."""
+    with torch.cuda.device(device):
+        ws = torch.empty(int(lib().pkv_masked_workspace_size()), dtype=torch.uint8, device=device)
+        workspace_init(ws, stream)
+    return ws
+
+
+def _masked(cache, q, block_tables, context_lens, q_lens, workspace, out, lse, q_starts, stream):
+    """(device, out, lse, the arguments that both masked attentions begin with, the workspace's)."""
+    device, bf16, shape = _device_of(q, "q"), torch.bfloat16, q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError("q must be [rows, heads, head_dim of the cache]")
+    n = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    _check_cache_device(cache, device)
+    qr = _row_view(q, "q", bf16, device, shape)
+    out, orow = _row_output(out, "out", q, bf16, device, shape, stream)
+    if lse is None:
+        lse = _new(stream, torch.empty, shape[:2], dtype=torch.float32, device=q.device)
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the same GPU")
+    args = (ctypes.byref(cache.desc()), qr, orow, _vector(lse, "lse", torch.float32, device, shape[0] * shape[1]),
+            shape[0], _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()),
+            block_tables.shape[1], _vector(context_lens, "context_lens", torch.int32, device, n),
+            _vector(q_lens, "q_lens", torch.int32, device, n),
+            None if q_starts is None else _vector(q_starts, "q_starts", torch.int64, device, n), n)
+    return device, out, lse, args, (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def attention_window(cache: PagedKVCache, q, block_tables, context_lens, q_lens, max_q_len: int, window: int,
+                     sinks: int, scale: float, workspace, out=None, lse=None, q_starts=None, stream=None):
+    """pkv_paged_attention_window: attention over the cache in which a query sees the last `window` positions up to
+    its own and the first `sinks`; q bf16 [rows, Hq, D] (views are fine), single tokens to prompts.  Returns
+    (out, lse): new tensors unless given; lse fp32 [rows, Hq], natural logarithm.  With q_starts (int64
+    [num_seqs]), rows outside every sequence are not written.  workspace: make_masked_workspace."""
+    device, out, lse, args, ws = _masked(cache, q, block_tables, context_lens, q_lens, workspace, out, lse, q_starts,
+                                         stream)
+    _call("pkv_paged_attention_window", device, stream, *args, max_q_len, window, sinks, scale, *ws)
+    return out, lse
+
+
+def attention_tree(cache: PagedKVCache, q, block_tables, context_lens, q_lens, max_q_len: int, tree_mask,
+                   scale: float, workspace, out=None, lse=None, q_starts=None, stream=None):
+    """pkv_paged_attention_tree: attention of a tree of drafted tokens, whose keys and values are the last q_lens
+    positions of each context: a row sees the context before them and the nodes whose bits are set in its row of
+    tree_mask (int32 [rows, words], bit j % 32 of word j / 32).  Otherwise as attention_window."""
+    device, out, lse, args, ws = _masked(cache, q, block_tables, context_lens, q_lens, workspace, out, lse, q_starts,
+                                         stream)
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0]:
+        raise ValueError("tree_mask must be [rows, words]")
+    _call("pkv_paged_attention_tree", device, stream, *args, max_q_len,
+          _vector(tree_mask, "tree_mask", torch.int32, device, tree_mask.numel()), tree_mask.shape[1], scale, *ws)
+    return out, lse
+
+
+class BlockPool:
+    """The free blocks of a cache as a stack on the GPU (update_tables): `free` int32 [num_blocks], of which the first
+    `count` (int32 [1]) are free.  Without them: all are, and 0 is taken first."""
+
+    def __init__(self, num_blocks: int, device="cuda", free=None, count=None):
+        if (free is None) != (count is None):
+            raise ValueError("free and count go together")
+        self.num_blocks = int(num_blocks)
+        if free is None:
+            free = torch.arange(self.num_blocks - 1, -1, -1, dtype=torch.int32, device=device)
+            count = torch.full((1,), self.num_blocks, dtype=torch.int32, device=device)
+        self.free, self.count = free, count
+        at = _device_of(free, "free")
+        _vector(free, "free", torch.int32, at, self.num_blocks)
+        _vector(count, "count", torch.int32, at, 1)
+
+
+def update_tables(pool: BlockPool, block_tables, context_lens, grow, num_rows: int, slots=None, positions=None,
+                  granted=None, row_starts=None, device_error=None, stream=None):
+    """pkv_block_tables_update: requests grow by (or, negative, drop) grow tokens: block_tables, context_lens and the
+    pool are updated in place.  num_rows >= sum(max(grow, 0)).  Returns (slots int64, positions int32 [num_rows],
+    granted int32, row_starts int64 [num_seqs]), new tensors unless given: what an append and the attention of
+    the new tokens take as slot_mapping, positions, q_lens and q_starts."""
+    device, n, num_rows = _device_of(block_tables, "block_tables"), context_lens.numel(), int(num_rows)
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+
+    def output(t, name, dtype, numel):
+        if t is None:
+            t = _new(stream, torch.empty, numel, dtype=dtype, device=block_tables.device)
+        return t, _vector(t, name, dtype, device, numel)
+
+    slots, sp = output(slots, "slots", torch.int64, num_rows)
+    positions, pp = output(positions, "positions", torch.int32, num_rows)
+    granted, gp = output(granted, "granted", torch.int32, n)
+    row_starts, rp = output(row_starts, "row_starts", torch.int64, n)
+    _call("pkv_block_tables_update", device, stream,
+          _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()), block_tables.shape[1],
+          _vector(context_lens, "context_lens", torch.int32, device, n), _vector(grow, "grow", torch.int32, device, n),
+          n, _vector(pool.free, "pool.free", torch.int32, device, pool.num_blocks),
+          _vector(pool.count, "pool.count", torch.int32, device, 1), pool.num_blocks, sp, pp, gp, rp, num_rows,
+          _error_word(device_error, device))
+    return slots, positions, granted, row_starts
+
+
+def keep_path(cache: PagedKVCache, block_tables, context_lens, q_lens, path, path_lens, device_error=None, stream=None):
+    """pkv_paged_kv_keep_path: the accepted nodes of each sequence's tree (path int32 [num_seqs, max_path], strictly
+    ascending, path_lens int32 [num_seqs] of them) moved to the places behind the context, in the cache."""
+    device, n = _device_of(block_tables, "block_tables"), context_lens.numel()
+    _check_cache_device(cache, device)
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    if path.dim() != 2 or path.shape[0] != n:
+        raise ValueError("path must be [num_seqs, max_path]")
+    _call("pkv_paged_kv_keep_path", device, stream, ctypes.byref(cache.desc()),
+          _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()), block_tables.shape[1],
+          _vector(context_lens, "context_lens", torch.int32, device, n),
+          _vector(q_lens, "q_lens", torch.int32, device, n), _vector(path, "path", torch.int32, device, path.numel()),
+          path.shape[1], _vector(path_lens, "path_lens", torch.int32, device, n), n, _error_word(device_error, device))
 
 
 def read_device_error(error_word, stream=None) -> int:

@@ -1,0 +1,1394 @@
+// Attention over the paged cache with a mask: a sliding window with first tokens that stay visible, or a tree of
+// drafted tokens.  Contracts: include/pagedkv.h, pkv_paged_attention_window and pkv_paged_attention_tree.
+//
+// For query i of sequence b at position p = L - Q + i and query head h (kv-head h / G):
+//   out = sum_j w_j v_j,  w = softmax over the visible j of scale * q . k_j,  lse = ln sum_j exp(scale * q . k_j)
+//   window: j is visible iff j <= p and (j > p - window or j < sinks)
+//   tree:   j is visible iff j < L - Q, or bit j - (L - Q) of row i of the mask is set
+//
+// A work item is up to 256 query rows of one (sequence, kv-head): 2 x PB consecutive queries, PB = floor(128 / G),
+// times the G heads of the group.  Its keys are a list of pages: those of the sinks that lie before the window, then
+// those from the first query's window to the last query.  A key's place v in that list and its position differ by one
+// jump behind the sinks, so what a row sees is at most two intervals of v, or one and the tree's bits, and pages
+// that no row sees are never touched (their table entries may be anything).
+//
+// Per key tile (8 pages, 128 keys) and chain:
+//   S[128 rows, 128 keys] = Q . K^T           (A: Q in the 128-byte swizzle; B: pages as they lie in the cache)
+//   P = 2^(S scale log2(e) - m), l += sum P   (one thread per row = TMEM lane)
+//   O[128 rows, D] += P . V                   (A = P in TMEM, bf16; B MN-major: pages as they lie)
+// There are two chains, each with its own S, O, m and l in tensor memory and four softmax warps.  An item with more
+// than PB queries has two row tiles, one a chain, and every key tile serves both.  One with fewer (decode) has one row
+// tile, and the chains take the key tiles in turns: while one's softmax runs the other's products do; their O, m and
+// l are joined at the end of the piece.  m is set by a row's first visible keys, four octaves above their maximum; P is
+// computed against it without a maximum, and only where some P reaches 2 (a logit 5 octaves above) m rises.
+//
+// P is rounded to bf16 (8 significant bits; l is summed from the fp32 P): the error it leaves in out is of the size
+// of out's own rounding to bf16.  fp16 would hold 11 bits, but not V's range.  FP8 caches: K and V are widened
+// to bf16 in shared memory (exact), a page's k scale multiplies its S and its v scale its P, in fp32.
+//
+// Work is cut into equal ranges of key tiles over all items, one range per CTA; an item that a range's end cuts leaves
+// partial (O, m, l) in the workspace, and whichever CTA finishes its part last joins them, in the keys' order.
+//
+// Roles (512 threads): warps 0-3 and 4-7 the softmax of chains 0 and 1; warps 8-11 make V (and, FP8, K) ready and run the
+// epilogue; warp 12 the producer; warps 13 and 14 the MMA issuers of the chains; warp 15 the plan.  Every wait is bounded.
+#include <cuda.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "rows.cuh"
+#include "tc_rows.cuh"
+
+namespace pkv {
+int num_sms_current();
+
+namespace masked {
+
+using namespace tcrow;
+using rows::store32;
+using rows::View;
+
+constexpr int kRows = 128;                 // rows of a row tile (MMA M)
+constexpr int kTP = 8;                     // pages of a key tile
+constexpr int kKeys = kTP * kBlock;        // keys of a key tile
+constexpr int kThreads = 512;
+// Registers a thread: the launch gives every thread 128, and the roles' shares add up to as many.
+constexpr int kRegsSoftmax = 160, kRegsReady = 112, kRegsOther = 80;
+static_assert(2 * kRegsSoftmax + kRegsReady + kRegsOther == 4 * 128, "register file");
+constexpr int kReady = 8, kProducer = 12, kMma = 13, kPlan = 15;
+constexpr int kPieces = 4;                 // pieces of work planned ahead
+constexpr int kFlags = 8;                  // pieces whose "non-finite V" flags are kept
+constexpr int kMaxCtas = 160;              // CTAs of a launch (two workspace slots each)
+constexpr int kItemUnits = 2;              // what an item costs beside its key tiles, in key tiles of one row tile
+constexpr int kMinUnits = 4;               // units that a CTA has at least
+
+struct Arg {
+    CUtensorMap q;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scales, *v_scales;
+    const int32_t *tables, *ctx_lens, *q_lens;
+    const int64_t* q_starts;
+    const uint32_t* tree;                  // nullptr: a window
+    View out;
+    float* lse;
+    int* err;
+    int* tickets;                          // [CTA][4]
+    float* partials;                       // [CTA][2] slots
+    uint64_t wait_limit_ns;
+    const int* hold;
+    int64_t num_blocks, num_q_rows;
+    int max_blocks, num_seqs, max_q_len, Hq, Hkv, group;
+    int pb;                                // queries of a row tile
+    int tree_words, window, sinks;
+    int wide;                              // out's rows are 32-byte aligned
+    float scale_log2;
+};
+
+// A partial slot: O as [D / 4][256 rows][4] fp32, then m and l, [256] each.
+__host__ __device__ constexpr int slot_floats(int D) { return 2 * kRows * (D + 2); }
+
+// A piece of work: key tiles [t0, t1) of queries q0 .. q0 + nq - 1 of a sequence, kv-head g.
+struct Piece {
+    int64_t row;            // q's row of query 0
+    int b, g, q0, nq, t0, t1;
+    int first;              // position of query q0
+    int L, Q;
+    int sp, np, jump;       // the list: sp first pages, then (from position sp * 16 + jump on) the others, np in all
+    int c0, parts;          // the CTAs that hold parts of the item: c0 .. c0 + parts - 1
+    int two;                // two row tiles
+    int end;                // no more work (the other fields are unset)
+    __device__ __forceinline__ int tiles() const { return t1 - t0; }
+    // tiles of chain i, the first of them, and the step from one to the next
+    __device__ __forceinline__ int count(int i) const { return two ? t1 - t0 : (t1 - t0 + 1 - i) >> 1; }
+    __device__ __forceinline__ int begin(int i) const { return two ? 0 : i; }
+    __device__ __forceinline__ int step() const { return two ? 1 : 2; }
+    __device__ __forceinline__ int page(int idx) const { return idx < sp ? idx : idx + jump / kBlock; }
+    // one past the last v that any query of [a, z) of the piece's queries sees
+    __device__ __forceinline__ int seen_end(const Arg& p, int z) const { return p.tree ? L : first + z - jump; }
+};
+static_assert(sizeof(Piece) % 8 == 0, "aligned ring entries");
+
+// What one query sees, in places of the list: [0, ns), [wl, wh], and (tree) bits from place `base` on.
+struct Sight {
+    int ns, wl, wh;
+    __device__ __forceinline__ void window(const Arg& a, const Piece& p, int pos) {
+        ns = min(a.sinks, pos + 1);
+        wl = max(0, pos - a.window + 1) - p.jump;
+        wh = pos - p.jump;
+    }
+    __device__ __forceinline__ void tree(const Piece& p) {
+        ns = wl = 0;
+        wh = p.L - p.Q - 1;
+    }
+    __device__ __forceinline__ bool has(int v) const { return v < ns || (v >= wl && v <= wh); }
+};
+
+// Bits j .. j + 31 of a row of `words` mask words (j from -31 up); bits at and past n are clear.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int j, int n) {
+    const int w = j >> 5, s = j & 31;
+    const uint32_t lo = w >= 0 && w < words ? row[w] : 0u, hi = w + 1 >= 0 && w + 1 < words ? row[w + 1] : 0u;
+    const uint32_t x = __funnelshift_r(lo, hi, s);
+    return n - j >= 32 ? x : n - j <= 0 ? 0u : x & ((1u << (n - j)) - 1u);
+}
+
+template <int D, bool FP8>
+struct Cfg {
+    static constexpr int SLAB = kRows * 128;              // Q: bytes of a 64-dimension slab
+    static constexpr int SLABS = D / 64;
+    static constexpr int QTILE = SLABS * SLAB;
+    static constexpr int NCH = D / 8;                     // 16-byte chunks of a bf16 row
+    static constexpr int PAGE = kBlock * D * 2;           // a page as bf16 operand
+    static constexpr int TILE = kTP * PAGE;
+    static constexpr int LAND = FP8 ? PAGE / 2 : PAGE;    // a page of the cache; FP8: it lands in the upper half
+    static constexpr int NSK = D == 128 ? 2 : 5;          // K ring depth
+    static constexpr int NSV = D == 128 ? 3 : 5;          // V ring depth
+    static constexpr int NSC = D == 128 ? 4 : 8;          // scale ring: a tile's are read until its V slot is free
+    static_assert(NSC > NSV, "scale ring");
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + 2 * QTILE;
+    static constexpr int OFF_V = OFF_K + NSK * TILE;
+    static constexpr int OFF_BAR = OFF_V + NSV * TILE;
+    static constexpr int KFULL = 0, KREADY = NSK, KEMPTY = 2 * NSK, VFULL = 3 * NSK, VREADY = VFULL + NSV,
+                         VEMPTY = VREADY + NSV, SFULL = VEMPTY + NSV, PFA = SFULL + 2, PFB = SFULL + 4, QFULL = SFULL + 6,
+                         QEMPTY = SFULL + 8, ODONE = SFULL + 10, OFREE = SFULL + 12, LREADY = SFULL + 14, PVA = SFULL + 16,
+                         TURN = SFULL + 18, PCFULL = SFULL + 20, PCEMPTY = PCFULL + kPieces, DRAIN = PCEMPTY + kPieces;
+    static constexpr int NBAR = DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
+    static constexpr int OFF_FLAG = OFF_MISC + 16;        // int[kFlags]
+    static constexpr int OFF_ML = OFF_FLAG + 4 * kFlags;  // float[chain][m, l][kRows]
+    static constexpr int OFF_SC = OFF_ML + 4 * 4 * kRows; // float[NSC][k scales 8, v scales 8]
+    static constexpr int OFF_PIECE = (OFF_SC + (FP8 ? NSC * 64 : 0) + 7) / 8 * 8;
+    static constexpr int SMEM = OFF_PIECE + kPieces * (int)sizeof(Piece);
+    static constexpr int COL_O = 2 * kKeys;
+    static constexpr int TMEM_COLS = 512;
+    static_assert(COL_O + 2 * D <= TMEM_COLS, "tensor memory budget");
+    static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// ------------------------------------------------------------------ plan
+
+struct Seq {
+    int64_t row;
+    int Q, L;               // 0 queries where the lengths are bad
+};
+
+// The plan of a launch, made by one warp of every CTA alike.  An item's units are its key tiles times its row tiles
+// and kItemUnits; all items' units, in the order sequence, query block, kv-head, are cut into equal ranges, one per
+// CTA, and a CTA has the tiles whose first unit lies in its range.
+struct Plan {
+    const Arg& a;
+    const int lane;
+    int chunk;
+    int64_t total, u, u1;   // all units; the CTA's place and end
+    int ctas;
+    int b, blk, g;          // the item at u, its first unit
+    int64_t start;
+    Seq s;
+    int64_t packed;         // rows before sequence b
+
+    __device__ __forceinline__ Plan(const Arg& a_, int lane_) : a(a_), lane(lane_) {}
+    __device__ __forceinline__ int per() const { return 2 * a.pb; }
+    __device__ __forceinline__ Seq load(int i, int64_t rows, bool report) const {
+        Seq x{a.q_starts ? a.q_starts[i] : rows, a.q_lens[i], a.ctx_lens[i]};
+        if (x.Q < 0 || x.Q > a.max_q_len || x.L < x.Q || x.row < 0 || x.row > a.num_q_rows - x.Q ||
+            (x.Q > 0 && (x.L - 1) / kBlock >= a.max_blocks)) {
+            if (report && (x.Q != 0 || x.L < 0)) raise_error(a.err, PKV_DEVERR_LENGTH);
+            x.Q = 0;
+        }
+        return x;
+    }
+    __device__ __forceinline__ void span(const Seq& x, int block, int& first, int& nq, int& sp, int& np, int& jump) const {
+        const int q0 = block * per();
+        nq = min(per(), x.Q - q0);
+        first = x.L - x.Q + q0;
+        if (a.tree) {
+            sp = jump = 0;
+            np = (x.L + kBlock - 1) / kBlock;
+            return;
+        }
+        const int wp = max(0, first - a.window + 1) / kBlock;
+        sp = min((min(a.sinks, x.L) + kBlock - 1) / kBlock, wp);
+        jump = (wp - sp) * kBlock;
+        np = (first + nq - 1) / kBlock + 1 - (wp - sp);
+    }
+    __device__ __forceinline__ int units(const Seq& x, int block, int& tiles, int& each) const {
+        int first, nq, sp, np, jump;
+        span(x, block, first, nq, sp, np, jump);
+        tiles = (np + kTP - 1) / kTP;
+        each = nq > a.pb ? 2 : 1;
+        return tiles * each + kItemUnits;
+    }
+    template <typename V>
+    __device__ __forceinline__ V scan(V x) const {        // the sum over earlier lanes
+        V y = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const V z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        return y - x;
+    }
+    __device__ __forceinline__ void begin() {
+        chunk = (a.num_seqs + 31) / 32;
+        const int b0 = min(lane * chunk, a.num_seqs), b1 = min(b0 + chunk, a.num_seqs);
+        int64_t rows = 0;
+        if (!a.q_starts) {
+            for (int i = b0; i < b1; ++i) rows += max(a.q_lens[i], 0);
+            rows = scan(rows);
+        }
+        int64_t mine = 0, at = rows;
+        int tiles, each;
+        for (int i = b0; i < b1; ++i) {
+            const Seq x = load(i, at, true);
+            at += max(a.q_lens[i], 0);
+            for (int k = 0; k * per() < x.Q; ++k) mine += (int64_t)units(x, k, tiles, each) * a.Hkv;
+        }
+        const int64_t before = scan(mine);
+        total = __shfl_sync(0xffffffffu, before + mine, 31);
+        ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
+        u = u1 = 0;
+        if ((int)blockIdx.x >= ctas || total == 0) return;
+        u = total * blockIdx.x / ctas;
+        u1 = total * (blockIdx.x + 1) / ctas;
+        // the lane that has the item at u, and where it lies
+        const bool here = u >= before && u < before + mine;
+        int fb = 0, fblk = 0, fg = 0;
+        int64_t fs = 0, fp = 0;
+        if (here) {
+            int64_t r = before;
+            at = rows;
+            bool found = false;
+            for (int i = b0; i < b1 && !found; ++i) {
+                const Seq x = load(i, at, false);
+                for (int k = 0; k * per() < x.Q; ++k) {
+                    const int w = units(x, k, tiles, each);
+                    if (u < r + (int64_t)w * a.Hkv) {
+                        fb = i;
+                        fblk = k;
+                        fg = (int)((u - r) / w);
+                        fs = r + (int64_t)fg * w;
+                        fp = at;
+                        found = true;
+                        break;
+                    }
+                    r += (int64_t)w * a.Hkv;
+                }
+                at += max(a.q_lens[i], 0);
+            }
+        }
+        const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        b = __shfl_sync(0xffffffffu, fb, from);
+        blk = __shfl_sync(0xffffffffu, fblk, from);
+        g = __shfl_sync(0xffffffffu, fg, from);
+        start = __shfl_sync(0xffffffffu, fs, from);
+        packed = __shfl_sync(0xffffffffu, fp, from);
+        s = load(b, packed, false);
+    }
+    __device__ __forceinline__ int cta_of(int64_t unit) const { return (int)(((unit + 1) * ctas - 1) / total); }
+    // The next piece with tiles; the same in every lane.
+    __device__ __forceinline__ bool next(Piece& p) {
+        while (u < u1) {
+            int tiles, each;
+            const int w = units(s, blk, tiles, each);
+            const int64_t keys = start + kItemUnits;      // the first tile's first unit
+            auto tile_at = [&](int64_t x) { return (int)min((int64_t)tiles, max((int64_t)0, (x - keys + each - 1) / each)); };
+            p.t0 = u <= keys ? 0 : tile_at(u);
+            p.t1 = u1 <= keys ? 0 : tile_at(u1);
+            const bool some = p.t1 > p.t0;
+            if (some) {
+                p.row = s.row;
+                p.b = b;
+                p.g = g;
+                p.q0 = blk * per();
+                span(s, blk, p.first, p.nq, p.sp, p.np, p.jump);
+                p.L = s.L;
+                p.Q = s.Q;
+                p.two = p.nq > a.pb;
+                p.end = 0;
+                p.c0 = blockIdx.x;
+                p.parts = 1;
+                if (p.t0 > 0 || p.t1 < tiles) {
+                    p.c0 = cta_of(keys);
+                    p.parts = cta_of(keys + (int64_t)(tiles - 1) * each) - p.c0 + 1;
+                }
+            }
+            // on to the next item
+            start += w;
+            u = start;
+            if (++g == a.Hkv) {
+                g = 0;
+                if (++blk * per() >= s.Q) {
+                    blk = 0;
+                    do {
+                        packed += max(a.q_lens[b], 0);
+                        if (++b >= a.num_seqs) {
+                            u = u1;
+                            break;
+                        }
+                        s = load(b, packed, false);
+                    } while (s.Q == 0);
+                }
+            }
+            if (some) return true;
+        }
+        return false;
+    }
+};
+
+// ------------------------------------------------------------------ numbers
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+constexpr float kHeadroom = 4.f;           // octaves of m above the logit it is set by
+// |m| from which its roundings (half of fp32's step at m each, up to three of them) may leave P, l or O their range:
+// 2^29, three times 16 octaves below it
+constexpr float kLimit = 0x1p29f;
+
+// Four e4m3 codes as bf16, exactly: the code's exponent and mantissa moved to bf16's places mean the value times
+// 2^-120 (subnormals too).  NaN codes become 480 here: the caller looks for them.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+    uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), y = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+    const uint32_t f = 0x7b807b80u;        // 2^120
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(lo) : "r"(x), "r"(f));
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(hi) : "r"(y), "r"(f));
+}
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// ------------------------------------------------------------------ kernel
+
+template <int D>
+__device__ __forceinline__ float* part_slot(const Arg& a, int cta, bool starts) {
+    return a.partials + ((size_t)cta * 2 + (starts ? 1 : 0)) * slot_floats(D);
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_constant__ Arg a) {
+    using K = Cfg<D, FP8>;
+    extern __shared__ __align__(1024) uint8_t smem[];     // (the swizzle needs it; checked below)
+    const uint32_t sb = smem_u32(smem);
+    // (the warp's number by a shuffle: known to be uniform, and with it the roles' control flow)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    auto bar = [&](int i) -> uint32_t { return sb + K::OFF_BAR + 8 * i; };
+    constexpr int NSK = K::NSK, NSV = K::NSV;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 4);
+    volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 8);   // (drain waits at the end)
+    volatile int* nonfinite = reinterpret_cast<volatile int*>(smem + K::OFF_FLAG);
+    float* ml = reinterpret_cast<float*>(smem + K::OFF_ML);
+    float* scales = reinterpret_cast<float*>(smem + K::OFF_SC);
+    const Ctl ctl{abort_flag, a.err, a.wait_limit_ns};
+
+    if (tid == 0) {
+        for (int i = 0; i < NSK; ++i) {
+            mbar_init(bar(K::KFULL + i), 1);
+            mbar_init(bar(K::KREADY + i), 4);             // (FP8) one arrival a warp that widens
+            mbar_init(bar(K::KEMPTY + i), 2);             // one of each chain
+        }
+        for (int i = 0; i < NSV; ++i) {
+            mbar_init(bar(K::VFULL + i), 1);
+            mbar_init(bar(K::VREADY + i), 4);             // one arrival a warp that makes it ready
+            mbar_init(bar(K::VEMPTY + i), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(K::SFULL + i), 1);
+            mbar_init(bar(K::PFA + i), 4);                // one arrival a softmax warp
+            mbar_init(bar(K::PFB + i), 4);
+            mbar_init(bar(K::QFULL + i), 1);
+            mbar_init(bar(K::QEMPTY + i), 2);
+            mbar_init(bar(K::ODONE + i), 1);
+            mbar_init(bar(K::OFREE + i), 4);
+            mbar_init(bar(K::LREADY + i), 4);
+            mbar_init(bar(K::PVA + i), 1);
+            mbar_init(bar(K::TURN + i), 1);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bar(K::PCFULL + i), 1);
+            mbar_init(bar(K::PCEMPTY + i), 15);           // every warp but the plan's, which writes them
+        }
+        mbar_init(bar(K::DRAIN), 2);
+        *abort_flag = 0;
+        *drain_flag = 0;
+        for (int i = 0; i < kFlags; ++i) nonfinite[i] = 0;
+        mbar_fence_init();
+    }
+    if (warp == kProducer && lane == 0) asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.q) : "memory");
+    if (warp == kPlan) {
+        tmem_alloc(smem_u32(tmem_slot), K::TMEM_COLS);
+        tmem_relinquish();
+    }
+    griddep_wait();
+    if ((sb & 1023) != 0 && tid == 0) {
+        raise_error(a.err, PKV_DEVERR_TIMEOUT);           // (never: the declaration above aligns it)
+        *abort_flag = 1;
+    }
+    tc_fence_before();
+    cta_bar_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // The pieces of work: the n-th (nullptr: a wait gave up), until its release by every warp.
+    const Piece* ring = reinterpret_cast<const Piece*>(smem + K::OFF_PIECE);
+    auto piece_at = [&](int n) -> const Piece* {
+        return __all_sync(0xffffffffu, wait(bar(K::PCFULL + n % kPieces), (n / kPieces) & 1, ctl)) ? ring + n % kPieces
+                                                                                                  : nullptr;
+    };
+    auto release = [&](int n) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(K::PCEMPTY + n % kPieces));
+    };
+    // every wait and every TMEM access is warp-uniform (tcgen05.ld / st are .aligned)
+    auto wait_all = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, wait(bb, parity, ctl)); };
+
+    if (warp < kReady) {
+        // ------------------------------------------------ softmax of chain i, thread r = row r
+        regs_inc<kRegsSoftmax>();
+        const int i = warp >> 2, r = tid & (kRows - 1);
+        const int G = a.group, pos = r / G;
+        const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t scol = tmem + lbase + i * kKeys;   // S / P
+        const uint32_t ocol = tmem + lbase + K::COL_O + i * D;
+        const float sc = a.scale_log2;
+        auto signal = [&](uint32_t bb) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bb);
+        };
+        bool ok = true;
+        int scnt = 0, ocnt = 0, tbase = 0;                // this chain's tiles and pieces; the CTA's tiles
+        for (int n = 0; ok; ++n) {
+            const Piece* p = piece_at(n);
+            if (!p || p->end) break;
+            const int cnt = p->count(i), x0 = p->begin(i), step = p->step(), t0 = p->t0;
+            const int base = tbase;
+            tbase += p->tiles();
+            if (cnt == 0) {
+                release(n);
+                continue;
+            }
+            const int qi = (p->two ? i * a.pb : 0) + pos;  // the row's query, from the piece's first on
+            const bool row_ok = pos < a.pb && qi < p->nq;
+            const bool live = __any_sync(0xffffffffu, row_ok);
+            // (rows of no query see everything, so that they ask for no mask)
+            Sight see{0, -0x40000000, 0x3fffffff};
+            const uint32_t* tree = nullptr;
+            if (row_ok) {
+                if (a.tree) {
+                    see.tree(*p);
+                    tree = a.tree + (p->row + p->q0 + qi) * (int64_t)a.tree_words;
+                } else {
+                    see.window(a, *p, p->first + qi);
+                }
+            }
+            const int tree0 = p->L - p->Q, tree_n = p->Q;
+            const int ends = p->seen_end(a, min(p->nq, p->two ? (i + 1) * a.pb : a.pb));
+            // m: the reference maximum (exp2 units), l: the sum of P
+            float m = row_ok ? -INFINITY : 0.f, l = 0.f;
+            for (int j = 0; j < cnt; ++j, ++scnt) {
+                const int x = x0 + j * step, v0 = (t0 + x) * kKeys;
+                if (!(ok = wait_all(bar(K::SFULL + i), scnt & 1))) break;
+                if (!live) {
+                    if (lane == 0) {
+                        mbar_arrive(bar(K::PFA + i));
+                        mbar_arrive(bar(K::PFB + i));
+                    }
+                    continue;
+                }
+                tc_fence_after();
+                const float* ks = scales + ((base + x) % K::NSC) * 16;
+                const bool masked = !__all_sync(0xffffffffu, (v0 >= see.wl && v0 + kKeys - 1 <= see.wh) || v0 + kKeys <= see.ns);
+                // the visible ones of columns c .. c + 31
+                auto bits = [&](int c) -> uint32_t {
+                    const int v = v0 + c, n_s = see.ns - v, lo = max(see.wl - v, 0), hi = min(see.wh - v, 31);
+                    uint32_t w = n_s >= 32 ? 0xffffffffu : n_s > 0 ? (1u << n_s) - 1u : 0u;
+                    if (lo <= hi) w |= (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+                    if (tree && v + 31 >= tree0) w |= tree_bits(tree, a.tree_words, v - tree0, tree_n);
+                    return w;
+                };
+                uint32_t sa[32], sb_[32];
+                tmem_ld32_async(scol, sa);
+                // O *= alpha (exact powers of 2, or 1)
+                auto rescale_o = [&](float alpha) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        tmem_ld16(ocol + c, o);
+                        uint32_t v[16];
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(o[y] * alpha);
+                        tmem_st16u(ocol + c, v);
+                    }
+                    tmem_wait_st();
+                };
+                tmem_wait_ld_into(sa);
+                // the largest visible S (FP8: times its page's scale) of columns [c0, c1)
+                auto maximum = [&](int c0, int c1) -> float {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 32) {
+                        uint32_t s[32];
+                        tmem_ld32_async(scol + c, s);
+                        const uint32_t w = bits(c);
+                        tmem_wait_ld_into(s);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            const float f = __uint_as_float(s[y]) * (FP8 ? ks[(c + y) / kBlock] : 1.f);
+                            mx[y & 3] = fmaxf(mx[y & 3], w >> y & 1 ? f : -INFINITY);
+                        }
+                        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    }
+                    return top;
+                };
+                if (!__all_sync(0xffffffffu, m > -INFINITY)) {
+                    // no reference yet (a piece's first tile): the largest of the first 32 keys where all are seen, else
+                    // of the tile.  (O and l are 0 so far, or NaN)
+                    float top = -INFINITY;
+                    if (!masked) {
+                        float t1 = -INFINITY;
+#pragma unroll
+                        for (int y = 0; y < 16; y += 2) {
+                            top = max3(top, __uint_as_float(sa[y]), __uint_as_float(sa[y + 1]));
+                            t1 = max3(t1, __uint_as_float(sa[y + 16]), __uint_as_float(sa[y + 17]));
+                        }
+                        // (a scale has any sign; a smaller reference than the maximum is as good)
+                        if (FP8) top = fmaxf(top * ks[0], t1 * ks[1]);
+                        else top = fmaxf(top, t1);
+                    }
+                    if (!__all_sync(0xffffffffu, top > -INFINITY)) top = maximum(0, kKeys);
+                    if (m == -INFINITY) m = top * sc + kHeadroom;
+                    // (too far below 0 is only seen here: m rises)
+                    if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
+                }
+                // (rare) a P of 64 keys at column c reaches 2: m rises by a whole number of octaves, and the P written in
+                // this tile, O and l are scaled down by as many (exact but for what falls below fp32's range)
+                auto raise_ref = [&](float target, int c) {
+                    const float inc = target + kHeadroom > m ? ceilf(target + kHeadroom - m) : 0.f;
+                    const int k = (int)fminf(inc, 127.f);
+                    const float alpha = k < 127 ? __uint_as_float((uint32_t)(127 - k) << 23) : 0.f;
+                    if (c > 0) {                          // the first half's P is being used: it ends in O
+                        wait_all(bar(K::PVA + i), scnt & 1);
+                        tc_fence_after();
+                    }
+                    if (j > 0 || c > 0) rescale_o(alpha);
+                    l *= alpha;
+                    m += inc;
+                };
+                // P of 32 keys at column c, two per packed fp32 operation (the even key in the low half); adds them to
+                // acc.  (Rows with nothing visible so far keep m = -inf: all their P are masked.)
+                auto neg_m = [&] {
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    return f2pack(__float_as_uint(nm), __float_as_uint(nm));
+                };
+                uint32_t over = 0;                        // (FP8) the OR of the P of 64 keys
+                auto emit = [&](const uint32_t (&s)[32], int c, uint32_t* v, uint64_t& acc, uint64_t nm2, auto mask, uint32_t w) {
+                    uint64_t ca = 0, cb = 0;
+#pragma unroll
+                    for (int h = 0; h < 32; h += 16) {
+                        const float f = FP8 ? sc * ks[(c + h) / kBlock] : sc;
+                        const uint64_t sc2 = f2pack(__float_as_uint(f), __float_as_uint(f));
+#pragma unroll
+                        for (int y = h; y < h + 16; y += 2) {
+                            float q0, q1;
+                            f2unpack(f2fma(f2pack(s[y], s[y + 1]), sc2, nm2), q0, q1);
+                            float p0 = exp2_fast(q0), p1 = exp2_fast(q1);
+                            if constexpr (decltype(mask)::value) {
+                                p0 = w >> y & 1 ? p0 : 0.f;
+                                p1 = w >> (y + 1) & 1 ? p1 : 0.f;
+                            }
+                            if ((y >> 1) & 1) cb = f2add(cb, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
+                            else ca = f2add(ca, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
+                            if constexpr (FP8) {
+                                over |= __float_as_uint(p0) | __float_as_uint(p1);
+                                const float vs = ks[8 + (c + h) / kBlock];
+                                float w0 = p0 * vs, w1 = p1 * vs;
+                                if constexpr (decltype(mask)::value) {   // (a scale may be infinite or NaN)
+                                    w0 = w >> y & 1 ? w0 : 0.f;
+                                    w1 = w >> (y + 1) & 1 ? w1 : 0.f;
+                                }
+                                v[y >> 1] = pack_bf16(w0, w1);
+                            } else {
+                                v[y >> 1] = pack_bf16(p0, p1);
+                            }
+                        }
+                    }
+                    acc = f2add(acc, f2add(ca, cb));
+                };
+                // The P of 64 keys is written once none is known to reach 2 (the top exponent bit is clear below).
+                // True: written.
+                auto write = [&](uint64_t acc, int c, const uint32_t (&v)[32], bool force) -> bool {
+                    bool high;
+                    if constexpr (FP8) {
+                        high = (over & 0x40000000u) != 0;
+                    } else {
+                        uint32_t any[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                        for (int y = 4; y < 32; ++y) any[y & 3] |= v[y];
+                        high = ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
+                    }
+                    if (__any_sync(0xffffffffu, row_ok && high) && !force) return false;
+                    tmem_st32u(scol + (c >> 1), v);
+                    float a0, a1;
+                    f2unpack(acc, a0, a1);
+                    l += a0 + a1;                         // (behind the store)
+                    tmem_wait_st();
+                    return true;
+                };
+                // 64 keys at column c, masked; a second time, with m raised, where the first is too large (NaN logits pass
+                // then).  A second half that no row sees is not read by the PV.
+                auto careful = [&](int c) {
+                    if (c > 0 && c >= ends - v0) return;
+                    for (bool force = false;; force = true) {
+                        uint32_t v[32];
+                        uint64_t acc = 0;
+                        const uint64_t nm2 = neg_m();
+                        over = 0;
+                        tmem_ld32_async(scol + c, sa);
+                        tmem_wait_ld_into(sa);
+                        tmem_ld32_async(scol + c + 32, sb_);
+                        emit(sa, c, v, acc, nm2, std::true_type{}, bits(c));
+                        tmem_wait_ld_into(sb_);
+                        emit(sb_, c + 32, v + 16, acc, nm2, std::true_type{}, bits(c + 32));
+                        if (write(acc, c, v, force)) break;
+                        const float top = maximum(c, c + 64);
+                        raise_ref(row_ok ? top * sc : -INFINITY, c);
+                    }
+                };
+                // (one copy of either path: the instruction cache holds little more than a tile's code)
+#pragma unroll 1
+                for (int c = 0; c < kKeys; c += 64) {
+                    bool done = false;
+                    if (!masked) {                        // loads in flight behind the arithmetic
+                        uint32_t v[32];
+                        uint64_t acc = 0;
+                        const uint64_t nm2 = neg_m();
+                        over = 0;
+                        tmem_ld32_async(scol + c + 32, sb_);
+                        emit(sa, c, v, acc, nm2, std::false_type{}, 0u);
+                        tmem_wait_ld_into(sb_);
+                        tmem_ld32_async(scol + 64, sa);   // (for the second half; after it, for nothing)
+                        emit(sb_, c + 32, v + 16, acc, nm2, std::false_type{}, 0u);
+                        tmem_wait_ld_into(sa);
+                        done = write(acc, c, v, false);
+                    }
+                    if (!done) {
+                        careful(c);
+                        tmem_ld32_async(scol + 64, sa);
+                        tmem_wait_ld_into(sa);
+                    }
+                    // P of the first 64 keys: their PV may run while the rest is computed
+                    signal(bar(K::PFA + i) + (c ? 8 * (K::PFB - K::PFA) : 0));
+                }
+            }
+            if (!ok) break;
+            // (a reference so large that fp32 cannot place the weights beside it is reported)
+            const float size = fabsf(m);
+            if (row_ok && size >= kLimit && size < INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
+            // m and l go to the epilogue, once it has taken the last piece's
+            if (ocnt++ > 0 && !(ok = wait_all(bar(K::OFREE + i), ocnt & 1))) break;
+            ml[(2 * i) * kRows + r] = m;
+            ml[(2 * i + 1) * kRows + r] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(K::LREADY + i));
+            release(n);
+        }
+    } else if (warp < kProducer) {
+        // ------------------------------------------------ V (FP8: K too) made ready; epilogue, thread r = row r
+        regs_dec<kRegsReady>();
+        const int w = warp - kReady, r = tid & (kRows - 1);
+        const int G = a.group, pos = r / G, hl = r - pos * G;
+        const uint32_t lbase = (uint32_t)(w * 32) << 16;
+
+        // Keys of a tile that not every row of the item sees: a weight of 0 times NaN or infinity is NaN, so V rows that no
+        // row sees are cleared, and non-finite values among those that some see become 0 here and are added back, row
+        // by row, in the epilogue (from global memory: rare).
+        struct Guard {
+            int ns_all, wl_all, wh_all, ns_any, wl_any, wh_any;
+            __device__ __forceinline__ bool all(int v) const { return v < ns_all || (v >= wl_all && v <= wh_all); }
+            __device__ __forceinline__ bool any(int v) const { return v < ns_any || (v >= wl_any && v <= wh_any); }
+            __device__ __forceinline__ bool all8(int v) const {
+                return v + 7 < ns_all || (v >= wl_all && v + 7 <= wh_all);
+            }
+        };
+        auto guard_of = [&](const Piece& p) {
+            Guard x;
+            if (a.tree) {
+                x = Guard{0, 0, p.L - p.Q - 1, 0, 0, p.L - 1};
+            } else {
+                Sight f, l;
+                f.window(a, p, p.first);
+                l.window(a, p, p.first + p.nq - 1);
+                x = Guard{f.ns, l.wl, f.wh, l.ns, f.wl, l.wh};
+            }
+            return x;
+        };
+        // One warp's share of tile x of a piece, the CTA's gt-th: its pages 2 w and 2 w + 1.  (FP8: a page lies in the upper
+        // half of its place and is widened over it.)
+        auto widen_page = [&](uint8_t* at, const Guard* gd, int v) -> bool {
+            constexpr int N = D / 32;                     // 16-byte chunks of codes a lane
+            uint4 raw[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) raw[j] = *reinterpret_cast<const uint4*>(at + K::LAND + (lane + 32 * j) * 16);
+            __syncwarp();
+            bool found = false;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int q = lane + 32 * j, k8 = q & 7, ch = (q >> 3) % (D / 16), grp = (q >> 3) / (D / 16);
+                uint32_t o[8];
+                widen4(raw[j].x, o[0], o[1]);
+                widen4(raw[j].y, o[2], o[3]);
+                widen4(raw[j].z, o[4], o[5]);
+                widen4(raw[j].w, o[6], o[7]);
+                const uint32_t nan[4] = {nan_codes(raw[j].x), nan_codes(raw[j].y), nan_codes(raw[j].z), nan_codes(raw[j].w)};
+                const int key = v + grp * 8 + k8;
+                const bool partial = gd && !gd->all(key);
+                if (nan[0] | nan[1] | nan[2] | nan[3]) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (nan[e / 4] >> (8 * (e % 4) + 7) & 1) {
+                            const uint32_t mask = 0xffffu << (16 * (e & 1));
+                            o[e / 2] = (o[e / 2] & ~mask) | (partial ? 0u : 0x7fc07fc0u & mask);
+                        }
+                    found |= partial;
+                }
+                if (partial && !gd->any(key)) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = 0;
+                }
+                uint8_t* dst = at + grp * (K::NCH * 128) + 2 * ch * 128 + k8 * 16;
+                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            return found;
+        };
+        auto guard_group = [&](uint8_t* at, const Guard& gd, int v) -> bool {     // 8 keys of bf16 V
+            bool found = false;
+            const int key = v + (lane & 7);
+            const bool any = gd.any(key), all = gd.all(key);
+#pragma unroll
+            for (int j = 0; j < K::NCH / 4; ++j) {
+                uint4* e = reinterpret_cast<uint4*>(at + (lane + 32 * j) * 16);
+                if (!any) {
+                    *e = make_uint4(0, 0, 0, 0);
+                } else if (!all) {
+                    uint32_t* y = reinterpret_cast<uint32_t*>(e);
+                    constexpr uint32_t I = 0x7f807f80u, A = 0x80008000u - I;     // an exponent of all ones carries
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t hit = ((y[z] & I) + A) & 0x80008000u;
+                        if (hit) {
+                            y[z] &= ~((hit >> 15) * 0xffffu);
+                            found = true;
+                        }
+                    }
+                }
+            }
+            return found;
+        };
+        auto ready = [&](const Piece& p, int n, int x, int gt, bool k_part) {
+            const int sk = gt % NSK, sv = gt % NSV, v0 = (p.t0 + x) * kKeys, pages = min(kTP, p.np - (p.t0 + x) * kTP);
+            if (k_part) {
+#pragma unroll 1
+                for (int u = 2 * w; u < min(2 * w + 2, pages); ++u)
+                    widen_page(smem + K::OFF_K + sk * K::TILE + u * K::PAGE, nullptr, 0);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(K::KREADY + sk));
+                return;
+            }
+            uint8_t* base = smem + K::OFF_V + sv * K::TILE;
+            const Guard gd = guard_of(p);
+            bool found = false;
+            if constexpr (FP8) {
+#pragma unroll 1
+                for (int u = 2 * w; u < min(2 * w + 2, pages); ++u)
+                    found |= widen_page(base + u * K::PAGE, &gd, v0 + u * kBlock);
+                fence_proxy_async_smem();
+            } else {
+                bool touched = false;
+#pragma unroll 1
+                for (int y = 4 * w; y < min(4 * w + 4, 2 * pages); ++y)
+                    if (!gd.all8(v0 + 8 * y)) {
+                        touched = true;
+                        found |= guard_group(base + y * (K::NCH * 128), gd, v0 + 8 * y);
+                    }
+                if (touched) fence_proxy_async_smem();
+            }
+            if (__any_sync(0xffffffffu, found) && lane == 0) nonfinite[n % kFlags] = n + 1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
+        };
+
+        // What the guard took out of the V of partially seen keys, for columns c .. c + 15 of a row.
+        auto add_back = [&](const Piece& p, int qi, int c, float (&o)[16]) {
+            const Guard gd = guard_of(p);
+            Sight see;
+            const uint32_t* tree = nullptr;
+            if (a.tree) {
+                see.tree(p);
+                tree = a.tree + (p.row + p.q0 + qi) * (int64_t)a.tree_words;
+            } else {
+                see.window(a, p, p.first + qi);
+            }
+            auto span = [&](int v, int z) {
+                v = max(v, p.t0 * kKeys);
+                z = min(z, min(p.t1 * kKeys, p.np * kBlock) - 1);
+                for (; v <= z; ++v) {
+                    const bool has = see.has(v) || (tree && v >= p.L - p.Q &&
+                                                    (tree_bits(tree, a.tree_words, v - (p.L - p.Q), p.Q) & 1u));
+                    if (!has) continue;
+                    const int id = a.tables[(int64_t)p.b * a.max_blocks + p.page(v / kBlock)];
+                    if (id < 0 || id >= a.num_blocks) continue;
+                    const uint8_t* page = a.v_cache + ((int64_t)id * a.Hkv + p.g) * K::LAND;
+                    const int off = v % kBlock;
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        const int d = c + y;
+                        float f;
+                        if constexpr (FP8) {
+                            const uint8_t code = page[((off / 8) * (D / 16) + d / 16) * 128 + (off % 8) * 16 + d % 16];
+                            f = (code & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
+                        } else {
+                            f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                                page + ((off / 8) * (D / 8) + d / 8) * 128 + (off % 8) * 16 + (d % 8) * 2));
+                        }
+                        if (!(fabsf(f) < INFINITY)) o[y] += f;
+                    }
+                }
+            };
+            span(gd.wl_any, gd.wl_all - 1);
+            span(gd.wh_all + 1, gd.wh_any);
+        };
+        auto put = [&](int64_t row, int h, int c, const float (&o)[16]) {
+            uint8_t* dst = a.out.row(row, h) + c * 2;
+            uint32_t v[8];
+#pragma unroll
+            for (int y = 0; y < 16; y += 2) v[y >> 1] = pack_bf16(o[y], o[y + 1]);
+            if (a.wide) {
+                store32(dst, v);
+            } else {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint4*>(dst + 16) = make_uint4(v[4], v[5], v[6], v[7]);
+            }
+        };
+        // the weight of a part with reference m and sum l beside the largest reference `top` of the parts.  (A part
+        // that saw nothing holds zeros, or NaN)
+        auto weight = [](float m, float l, float top) {
+            return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - top);
+        };
+        auto finish_lse = [](float m, float l) {
+            return m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+        };
+        uint32_t phase = 0;                               // of either chain's pieces, as bits
+        auto epilogue = [&](const Piece& p, int n) {
+            const bool whole = p.parts == 1, fix = nonfinite[n % kFlags] == n + 1;
+            float* slot = part_slot<D>(a, blockIdx.x, p.t0 == 0);
+            const int tiles_r = p.two ? 2 : 1;
+#pragma unroll 1
+            for (int i = 0; i < tiles_r; ++i) {
+                const int qi = i * a.pb + pos;
+                const bool row_ok = pos < a.pb && qi < p.nq;
+                const bool both = !p.two && p.count(1) > 0;            // this row tile's keys are shared by the chains
+                const uint32_t oa = tmem + lbase + K::COL_O + (p.two ? i * D : 0), ob = tmem + lbase + K::COL_O + D;
+                const float* mla = ml + (p.two ? 2 * i : 0) * kRows;
+                tc_fence_after();
+                float m = mla[r], l = mla[kRows + r], fa = 1.f, fb = 0.f;
+                if (both) {
+                    const float m1 = ml[2 * kRows + r], l1 = ml[3 * kRows + r], top = fmaxf(m, m1);
+                    fa = weight(m, l, top);
+                    fb = weight(m1, l1, top);
+                    l = l * fa + l1 * fb;
+                    if (m == -INFINITY) fa = 1.f;
+                    if (m1 == -INFINITY) fb = 1.f;
+                    m = top;
+                }
+                const bool none = m == -INFINITY && l == 0.f;
+                const float inv = none ? 0.f : 1.f / l;
+                const int64_t row = p.row + p.q0 + qi;
+                const int h = p.g * G + hl;
+                if (row_ok) {
+                    if (!whole) {
+                        slot[(size_t)2 * kRows * D + i * kRows + r] = m;
+                        slot[(size_t)2 * kRows * (D + 1) + i * kRows + r] = l;
+                    } else if (a.lse) {
+                        a.lse[row * a.Hq + h] = finish_lse(m, l);
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    tmem_ld16(oa + c, o);
+                    if (both) {
+                        float o1[16];
+                        tmem_ld16(ob + c, o1);
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] = o[y] * fa + o1[y] * fb;
+                    }
+                    if (c + 16 == D) {                    // O read: the next piece's first PV may overwrite it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar(K::OFREE + (p.two ? i : 0)));
+                            if (both) mbar_arrive(bar(K::OFREE + 1));
+                        }
+                    }
+                    if (row_ok && fix) add_back(p, qi, c, o);
+                    if (row_ok && whole) {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] = none ? 0.f : o[y] * inv;
+                        put(row, h, c, o);
+                    } else if (row_ok) {
+#pragma unroll
+                        for (int y = 0; y < 16; y += 4)
+                            __stcg(reinterpret_cast<float4*>(slot + (size_t)((c + y) / 4) * 2 * kRows * 4 + (i * kRows + r) * 4),
+                                   make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (whole) return;
+            // The part is in memory: the last of the item's CTAs to get here (for these 32 lanes' rows) joins them, in order.
+            __threadfence();
+            __syncwarp();
+            int old = 0;
+            int* ticket = a.tickets + p.c0 * 4 + w;
+            if (lane == 0) old = atom_add_acq_rel_gpu(ticket, 1);
+            if (__shfl_sync(0xffffffffu, old, 0) != p.parts - 1) return;
+            if (lane == 0) *ticket = 0;
+            fence_acquire_gpu();
+#pragma unroll 1
+            for (int i = 0; i < tiles_r; ++i) {
+                const int rows_i = min(a.pb, p.nq - i * a.pb) * G, mine = min(32, rows_i - w * 32);
+                if (mine <= 0) continue;
+#pragma unroll 1
+                for (int y = lane; y < mine * (D / 8); y += 32) {
+                    const int R = w * 32 + y % mine, c = y / mine * 8;
+                    const int rp = R / G;
+                    auto at = [&](int x) { return part_slot<D>(a, p.c0 + x, x == 0); };
+                    float top = -INFINITY;
+                    for (int x = 0; x < p.parts; ++x) top = fmaxf(top, __ldcg(at(x) + (size_t)2 * kRows * D + i * kRows + R));
+                    float l = 0.f, o[8] = {};
+#pragma unroll 2
+                    for (int x = 0; x < p.parts; ++x) {
+                        const float* s = at(x);
+                        const float mx = __ldcg(s + (size_t)2 * kRows * D + i * kRows + R);
+                        const float lx = __ldcg(s + (size_t)2 * kRows * (D + 1) + i * kRows + R);
+                        const float4 u0 = __ldcg(reinterpret_cast<const float4*>(s + ((size_t)(c / 4) * 2 * kRows + i * kRows + R) * 4));
+                        const float4 u1 = __ldcg(reinterpret_cast<const float4*>(s + ((size_t)(c / 4 + 1) * 2 * kRows + i * kRows + R) * 4));
+                        float f = weight(mx, lx, top);
+                        l += f * lx;
+                        if (mx == -INFINITY) f = 1.f;
+                        o[0] = fmaf(u0.x, f, o[0]);
+                        o[1] = fmaf(u0.y, f, o[1]);
+                        o[2] = fmaf(u0.z, f, o[2]);
+                        o[3] = fmaf(u0.w, f, o[3]);
+                        o[4] = fmaf(u1.x, f, o[4]);
+                        o[5] = fmaf(u1.y, f, o[5]);
+                        o[6] = fmaf(u1.z, f, o[6]);
+                        o[7] = fmaf(u1.w, f, o[7]);
+                    }
+                    const bool none = top == -INFINITY && l == 0.f;
+                    const float inv = none ? 0.f : 1.f / l;
+                    const int64_t row = p.row + p.q0 + i * a.pb + rp;
+                    const int h = p.g * G + R - rp * G;
+                    uint32_t v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = none ? 0u : pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+                    *reinterpret_cast<uint4*>(a.out.row(row, h) + c * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (c == 0 && a.lse) a.lse[row * a.Hq + h] = finish_lse(top, l);
+                }
+            }
+        };
+
+        // Either job when its input is there, none waited for while the other may run: the next piece's tiles are made
+        // ready while the last piece's results are awaited, and its products wait for that epilogue.
+        int rp = 0, rx = 0, rg = 0;                       // the piece, its tile, and the CTA's tile to make ready
+        int ep = 0;                                       // the piece to finish
+        bool rk = FP8, last = false;                      // (FP8) K is next, else V; no more pieces
+        bool known = false;                               // piece rp is there
+        uint64_t since = 0;
+        uint32_t spins = 0;
+        auto there = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bb, parity)); };
+        for (;;) {
+            bool moved = false;
+            if (ep < rp) {
+                const Piece& p = ring[ep % kPieces];
+                const bool c1 = p.count(1) > 0;           // (chain 0 always has tiles)
+                if (there(bar(K::ODONE), phase & 1) && there(bar(K::LREADY), phase & 1) &&
+                    (!c1 || (there(bar(K::ODONE + 1), phase >> 1 & 1) && there(bar(K::LREADY + 1), phase >> 1 & 1)))) {
+                    epilogue(p, ep);
+                    phase ^= c1 ? 3u : 1u;
+                    release(ep);
+                    ++ep;
+                    moved = true;
+                }
+            } else if (last) {
+                break;
+            }
+            if (!last) {
+                if (!known && there(bar(K::PCFULL + rp % kPieces), (rp / kPieces) & 1)) {
+                    known = true;
+                    if (ring[rp % kPieces].end) last = true;
+                    moved = true;
+                }
+                if (known && !last) {
+                    const Piece& p = ring[rp % kPieces];
+                    if (there(rk ? bar(K::KFULL + rg % NSK) : bar(K::VFULL + rg % NSV), (rg / (rk ? NSK : NSV)) & 1)) {
+                        ready(p, rp, rx, rg, rk);
+                        moved = true;
+                        if (rk) {
+                            rk = false;
+                        } else {
+                            rk = FP8;
+                            ++rg;
+                            if (++rx == p.tiles()) {
+                                rx = 0;
+                                ++rp;
+                                known = false;
+                            }
+                        }
+                    }
+                }
+            }
+            if (moved) {
+                since = 0;
+                spins = 0;
+                continue;
+            }
+            if ((++spins & 63) == 0) {
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+                const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+                if (since == 0) since = now;
+                if (now - since > a.wait_limit_ns) {
+                    if (lane == 0) {
+                        raise_error(a.err, PKV_DEVERR_TIMEOUT);
+                        *abort_flag = 1;
+                    }
+                    break;
+                }
+            }
+            __nanosleep(20);
+        }
+    } else {
+        regs_dec<kRegsOther>();
+        if (warp == kProducer) {
+            // -------------------------------------------- Q tiles, K and V pages in order
+            bool ok = true;
+            int nt = 0, nq = 0;                           // key tiles and Q tiles
+            int nk = 0, nv = 0;                           // copies issued: K and V tiles
+            if (a.hold != nullptr && lane == 0) {
+                // (tests of the timeout path only) wait, bounded, for a flag that nothing sets
+                const uint64_t h0 = globaltimer_ns();
+                while (ok && *reinterpret_cast<const volatile int*>(a.hold) == 0) {
+                    if (*abort_flag || globaltimer_ns() - h0 > a.wait_limit_ns) {
+                        if (!*abort_flag) raise_error(a.err, PKV_DEVERR_TIMEOUT);
+                        *abort_flag = 1;
+                        ok = false;
+                    }
+                    __nanosleep(256);
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            const int u8 = lane & 7;
+            const bool is_v = lane >= 8;
+            for (int n = 0; ok; ++n) {
+                const Piece* p = piece_at(n);
+                if (!p || p->end) break;
+                for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
+                    const int slot = nq & 1;
+                    if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(K::QFULL + slot), K::SLABS * a.pb * a.group * 128);
+                        for (int s = 0; s < K::SLABS; ++s)
+                            tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + s * K::SLAB, &a.q, s * 64, p->g * a.group,
+                                       (int)(p->row + p->q0 + i * a.pb), bar(K::QFULL + slot));
+                    }
+                }
+                const int32_t* table = a.tables + (int64_t)p->b * a.max_blocks;
+                const int np = p->np, g = p->g;
+                // the block of this lane's page of tile t (a bad id is reported, and block 0 read in its place)
+                auto block = [&](int t) -> int {
+                    const int idx = t * kTP + u8;
+                    return lane < 16 && idx < np ? table[p->page(idx)] : 0;
+                };
+                auto checked = [&](int id) -> int {
+                    if (id >= 0 && id < a.num_blocks) return id;
+                    raise_error(a.err, PKV_DEVERR_BLOCK_ID);
+                    return 0;
+                };
+                auto scale_of = [&](int id) -> float {
+                    return FP8 && lane < 16 ? (is_v ? a.v_scales : a.k_scales)[(int64_t)id * a.Hkv + g] : 0.f;
+                };
+                int id = checked(block(p->t0));
+                float s = scale_of(id);
+                for (int t = p->t0; t < p->t1 && ok; ++t, ++nt) {
+                    const int sk = nt % NSK, sv = nt % NSV, pages = min(kTP, np - t * kTP);
+                    int after = t + 1 < p->t1 ? block(t + 1) : 0;
+                    const int64_t src = ((int64_t)id * a.Hkv + g) * K::LAND;
+                    if (nt >= NSK && !(ok = wait_all(bar(K::KEMPTY + sk), ((nt - NSK) / NSK) & 1))) break;
+                    if (FP8 && lane < 16) scales[(nt % K::NSC) * 16 + lane] = s;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(bar(K::KFULL + sk), pages * K::LAND);
+                    __syncwarp();
+                    if (lane < pages)
+                        bulk_g2s(sb + K::OFF_K + sk * K::TILE + u8 * K::PAGE + (FP8 ? K::LAND : 0), a.k_cache + src, K::LAND,
+                                 bar(K::KFULL + sk));
+                    ++nk;
+                    if (nt >= NSV && !(ok = wait_all(bar(K::VEMPTY + sv), ((nt - NSV) / NSV) & 1))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(K::VFULL + sv), pages * K::LAND);
+                    __syncwarp();
+                    if (is_v && lane < 8 + pages)
+                        bulk_g2s(sb + K::OFF_V + sv * K::TILE + u8 * K::PAGE + (FP8 ? K::LAND : 0), a.v_cache + src, K::LAND,
+                                 bar(K::VFULL + sv));
+                    ++nv;
+                    id = checked(after);
+                    s = scale_of(id);
+                }
+                release(n);
+            }
+            if (lane == 0) {
+                // drain: every copy in flight lands before the CTA exits
+                const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
+                for (int t = max(0, nk - NSK); t < nk; ++t) wait(bar(K::KFULL + t % NSK), (t / NSK) & 1, drain);
+                for (int t = max(0, nv - NSV); t < nv; ++t) wait(bar(K::VFULL + t % NSV), (t / NSV) & 1, drain);
+                for (int t = max(0, nq - 2); t < nq; ++t) wait(bar(K::QFULL + (t & 1)), (t >> 1) & 1, drain);
+            }
+            __syncwarp();
+        } else if (warp == kMma || warp == kMma + 1) {
+            // -------------------------------------------- MMA issuer of chain i
+            const int i = warp - kMma;
+            const bool lead = elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);       // (known to be uniform)
+            const uint32_t s_i = tm + __shfl_sync(0xffffffffu, i, 0) * kKeys;
+            const uint32_t o_i = tm + K::COL_O + __shfl_sync(0xffffffffu, i, 0) * D;
+            constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys, false, false);
+            constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true);
+            int pcnt = 0, ocnt = 0, turn = 0;             // this chain's tiles and pieces; turns
+            int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
+            int kn = 0, vn = 0, qn = 0;                   // K, V and Q tiles seen: every one, in order, by both chains (a
+                                                          // barrier's parity tells neighbouring phases apart, no more)
+            bool ok = true;
+            struct Work {
+                int cnt, x0, step, t0, two, ends;
+                int base, q;                              // the CTA's numbers of its first tile and of the chain's Q tile
+            };
+            // up to tile `upto`: what the other chain alone uses is given back as soon as it has landed
+            auto skip = [&](int& at, int upto, int ring_n, int full, int empty) -> bool {
+                for (; at < upto; ++at) {
+                    if (!wait_all(bar(full + at % ring_n), (at / ring_n) & 1)) return false;
+                    if (lead) mbar_arrive(bar(empty + at % ring_n));
+                }
+                return true;
+            };
+            auto see = [&](int& at, int target, int ring_n, int full, int empty) -> bool {
+                if (!skip(at, target, ring_n, full, empty)) return false;
+                at = target + 1;
+                return wait_all(bar(full + target % ring_n), (target / ring_n) & 1);
+            };
+            constexpr int KRDY = FP8 ? K::KREADY : K::KFULL;
+            auto see_k = [&](int t) { return see(kn, t, NSK, KRDY, K::KEMPTY); };
+            auto see_v = [&](int t) { return see(vn, t, NSV, K::VREADY, K::VEMPTY); };
+            auto see_q = [&](int t) { return see(qn, t, 2, K::QFULL, K::QEMPTY); };
+            int n = 0;
+            // The next piece, if there is one and (or else, with `any`, the next that does) it has tiles of this chain.
+            auto next = [&](Work& x, bool any) -> bool {
+                for (;; ++n) {
+                    const Piece* at = piece_at(n);
+                    if (!at || at->end) return false;
+                    x.cnt = at->count(i);
+                    if (x.cnt == 0 && !any) return false;
+                    x.x0 = at->begin(i);
+                    x.step = at->step();
+                    x.t0 = at->t0;
+                    x.two = at->two;
+                    x.ends = at->seen_end(a, min(at->nq, at->two ? (i + 1) * a.pb : a.pb));
+                    x.base = tbase;
+                    x.q = qbase + (at->two ? i : 0);
+                    tbase += at->tiles();
+                    qbase += at->two ? 2 : 1;
+                    release(n);
+                    if (x.cnt > 0) break;
+                    if (!skip(qn, qbase, 2, K::QFULL, K::QEMPTY) || !skip(kn, tbase, NSK, KRDY, K::KEMPTY) ||
+                        !skip(vn, tbase, NSV, K::VREADY, K::VEMPTY))
+                        return false;
+                }
+                ++n;
+                return true;
+            };
+            // S of tile j of this chain's in a piece (its K and Q seen)
+            auto issue_s = [&](const Work& x, int j) {
+                const int sk = (x.base + x.x0 + j * x.step) % NSK;
+                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::TILE, 0);
+                const uint32_t q_s = __shfl_sync(0xffffffffu, sb + K::OFF_Q + (x.q & 1) * K::QTILE, 0);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(lead, s_i, desc_sw128(q_s + (k / 4) * K::SLAB + (k % 4) * 32, 16, 1024),
+                           smem_desc(kbase + k * 256, 128, K::NCH * 128), idS, k > 0 ? 1u : 0u);
+                commit(lead, bar(K::SFULL + i));
+                commit(lead, bar(K::KEMPTY + sk));
+                if (j + 1 == x.cnt) commit(lead, bar(K::QEMPTY + (x.q & 1)));
+            };
+            Work p;
+            bool more = next(p, true), begun = false;     // begun: this piece's first S is issued
+            while (more && ok) {
+                if (!begun) {
+                    if (!(ok = see_q(p.q)) || !(ok = see_k(p.base + p.x0))) break;
+                    tc_fence_after();
+                    issue_s(p, 0);
+                }
+                Work q;
+                bool after = false;                       // the piece behind this has tiles of this chain
+                for (int j = 0; j < p.cnt; ++j, ++pcnt) {
+                    const bool end = j + 1 == p.cnt;
+                    const int x = p.x0 + j * p.step, gt = p.base + x;
+                    if (end) after = next(q, false);
+                    const int sv = gt % NSV;
+                    const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::TILE, 0);
+                    const int steps = min(max((p.ends - (p.t0 + x) * kKeys + kBlock - 1) / kBlock, 1), kTP);   // pages
+                    auto pv = [&](int k0) {               // 4 pages
+                        if (steps == kTP) {
+#pragma unroll
+                            for (int k = k0; k < k0 + 4; ++k)
+                                mma_ts(lead, o_i, s_i + k * 8, smem_desc(vbase + k * K::PAGE, K::NCH * 128, 128), idPV,
+                                       j > 0 || k > 0 ? 1u : 0u);
+                        } else {
+#pragma unroll 1
+                            for (int k = k0; k < min(k0 + 4, steps); ++k)
+                                mma_ts(lead, o_i, s_i + k * 8, smem_desc(vbase + k * K::PAGE, K::NCH * 128, 128), idPV,
+                                       j > 0 || k > 0 ? 1u : 0u);
+                        }
+                    };
+                    if (!(ok = see_v(gt))) break;
+                    // a piece's first PV starts O afresh: the last one's result has been read
+                    if (j == 0 && ocnt > 0 && !(ok = wait_all(bar(K::OFREE + i), (ocnt - 1) & 1))) break;
+                    // (what the next S needs is waited for before P, off the path from P to it)
+                    if (end && after && (!(ok = see_q(q.q)) || !(ok = see_k(q.base + q.x0)))) break;
+                    if (!end && !(ok = see_k(gt + p.step))) break;
+                    if (p.two) {
+                        if ((i == 1 || turn > 0) && !(ok = wait_all(bar(K::TURN + i), (i == 1 ? turn : turn - 1) & 1))) break;
+                        ++turn;
+                    }
+                    if (!(ok = wait_all(bar(K::PFA + i), pcnt & 1))) break;
+                    tc_fence_after();
+                    pv(0);
+                    commit(lead, bar(K::PVA + i));
+                    if (!(ok = wait_all(bar(K::PFB + i), pcnt & 1))) break;
+                    tc_fence_after();
+                    pv(4);
+                    if (end) commit(lead, bar(K::ODONE + i));
+                    commit(lead, bar(K::VEMPTY + sv));
+                    if (!end) issue_s(p, j + 1);
+                    else if (after) issue_s(q, 0);
+                    if (p.two) {
+                        if constexpr (D == 64) commit(lead, bar(K::TURN + 1 - i));
+                        else if (lead) mbar_arrive(bar(K::TURN + 1 - i));
+                    }
+                }
+                if (!ok) break;
+                ++ocnt;
+                begun = after;
+                if (after) p = q;
+                else more = next(p, true);
+            }
+            commit(lead, bar(K::DRAIN));
+            // every MMA issued has completed before TMEM is freed
+            const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
+            wait(bar(K::DRAIN), 0, drain);
+            __syncwarp();
+        } else if (warp == kPlan) {
+            // -------------------------------------------- the plan
+            Plan plan(a, lane);
+            plan.begin();
+            for (int n = 0;; ++n) {
+                Piece p = {};
+                p.end = !plan.next(p);
+                if (n >= kPieces && !wait_all(bar(K::PCEMPTY + n % kPieces), ((n - kPieces) / kPieces) & 1)) break;
+                if (lane == 0) {
+                    const_cast<Piece*>(ring)[n % kPieces] = p;
+                    mbar_arrive(bar(K::PCFULL + n % kPieces));
+                }
+                __syncwarp();
+                if (p.end) break;
+            }
+        }
+    }
+
+    // teardown: every role arrives from its own code path (non-.aligned barrier)
+    __syncwarp();
+    tc_fence_before();
+    cta_bar_sync();
+    if (warp == kPlan) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, K::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr size_t kTicketOff = 256;         // behind the error word
+constexpr size_t kPartOff = kTicketOff + (size_t)kMaxCtas * 4 * sizeof(int);
+
+template <int D, bool FP8>
+cudaError_t launch(const Arg& a, unsigned grid, cudaStream_t st) {
+    static std::atomic<uint64_t> set{0};
+    return launch_pdl_bigsmem(set, masked_kernel<D, FP8>, dim3(grid), dim3(kThreads), (size_t)Cfg<D, FP8>::SMEM, st, a);
+}
+
+}  // namespace masked
+
+size_t masked_workspace_bytes() {
+    return masked::kPartOff + (size_t)masked::kMaxCtas * 2 * masked::slot_floats(128) * sizeof(float);
+}
+
+cudaError_t launch_masked(const pkv_cache& c, const pkv_rows* q, const pkv_rows* out, float* lse, int64_t num_q_rows,
+                          const int32_t* tables, int max_blocks, const int32_t* ctx_lens, const int32_t* q_lens,
+                          const int64_t* q_starts, int num_seqs, int max_q_len, int window, int sinks, const int32_t* tree,
+                          int tree_words, float scale, void* workspace, cudaStream_t st) {
+    using namespace masked;
+    const int sms = num_sms_current();
+    if (sms <= 0 || !encoder()) return cudaErrorUnknown;
+    const int G = q->num_heads / c.num_kv_heads;
+    Arg a = {};
+    a.pb = kRows / G;
+    if (!make_map(&a.q, q, q->data, PKV_BF16, c.head_dim, num_q_rows, G, a.pb)) return cudaErrorInvalidValue;
+    a.k_cache = (const uint8_t*)c.k_cache;
+    a.v_cache = (const uint8_t*)c.v_cache;
+    a.k_scales = c.k_scales;
+    a.v_scales = c.v_scales;
+    a.tables = tables;
+    a.ctx_lens = ctx_lens;
+    a.q_lens = q_lens;
+    a.q_starts = q_starts;
+    a.tree = (const uint32_t*)tree;
+    a.out = View{(uint8_t*)out->data, out->token_stride * 2, out->head_stride * 2, out->num_heads};
+    a.lse = lse;
+    a.err = (int*)workspace;
+    a.tickets = (int*)((uint8_t*)workspace + kTicketOff);
+    a.partials = (float*)((uint8_t*)workspace + kPartOff);
+    AttnParams dbg = {};
+    fill_debug(dbg);
+    a.wait_limit_ns = dbg.wait_limit_ns;
+    a.hold = dbg.hold;
+    a.num_blocks = c.num_blocks;
+    a.num_q_rows = num_q_rows;
+    a.max_blocks = max_blocks;
+    a.num_seqs = num_seqs;
+    a.max_q_len = max_q_len;
+    a.Hq = q->num_heads;
+    a.Hkv = c.num_kv_heads;
+    a.group = G;
+    a.tree_words = tree_words;
+    a.window = window;
+    a.sinks = sinks;
+    a.wide = rows::wide(a.out);
+    a.scale_log2 = scale * kLog2e;
+    const unsigned grid = (unsigned)std::min(sms, kMaxCtas);
+    if (c.kv_dtype == PKV_KV_FP8_E4M3)
+        return c.head_dim == 128 ? launch<128, true>(a, grid, st) : launch<64, true>(a, grid, st);
+    return c.head_dim == 128 ? launch<128, false>(a, grid, st) : launch<64, false>(a, grid, st);
+}
+
+}  // namespace pkv

@@ -1,0 +1,292 @@
+// Block tables, slots and positions from request lengths, and the pool of free blocks behind them.  Contract:
+// include/pagedkv.h, pkv_block_tables_update.
+//
+// With had_b and has_b the blocks of request b before and after, D the blocks that all dropping requests give back
+// and N_b = sum over b' <= b of max(has - had, 0):
+//   the i-th block given back (last request first, its last block first) goes to stack[count + i]
+//   the k-th block needed (first request first, its first block first) is stack[count + D - 1 - k]
+// so everything follows from three sums over the requests, and a call with the negated changes puts the pool back
+// exactly.  No data to speak of moves: the time is a chain of dependent reads (lengths, table entries or the
+// stack, then the writes) and one launch.  One cluster does it, of one CTA or, where there are many rows to write, eight:
+// every CTA forms the sums for itself, and the cluster's barrier stands between the reads of the old state, the
+// blocks given back and the blocks taken.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+
+namespace pkv {
+namespace tables {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024;
+constexpr int kMaxSeqs = 8192;             // requests a call takes: their state is held in shared memory
+constexpr int kCluster = 8;
+constexpr int kManyRows = 4096;            // rows from which the cluster has kCluster CTAs
+
+struct Arg {
+    int32_t* table;
+    int32_t* lens;
+    const int32_t* grow;
+    int32_t* free_blocks;
+    int32_t* free_count;
+    int64_t* slots;
+    int32_t* positions;
+    int32_t* granted;
+    int64_t* row_starts;
+    int* err;
+    int64_t num_blocks, num_rows;
+    int num_seqs, max_blocks;
+};
+
+// Shared memory, by request: tokens before; change (0: refused or none); blocks given back by later
+// requests; blocks needed by earlier ones; first row; rows (of a refused request too).
+struct Shared {
+    int *len, *change, *back, *need, *row, *rows;
+    __device__ explicit Shared(int* p, int n) : len(p), change(p + n), back(p + 2 * n), need(p + 3 * n), row(p + 4 * n), rows(p + 5 * n) {}
+};
+constexpr int kArrays = 6;
+
+__device__ __forceinline__ int blocks(int tokens) { return (int)(((unsigned)tokens + kBlock - 1) / kBlock); }
+
+// Exclusive sums over the CTA's threads of two values; *total_a, *total_b their sums.
+__device__ void scan2(int64_t& a, int64_t& b, int64_t* total_a, int64_t* total_b, int64_t (*part)[2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = a, y = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) {
+            x += p;
+            y += q;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) {
+        part[warp][0] = x;
+        part[warp][1] = y;
+    }
+    __syncthreads();
+    int64_t u = part[lane][0], v = part[lane][1];         // (32 warps; every warp sums them for itself)
+    const int64_t u0 = u, v0 = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t p = __shfl_up_sync(0xffffffffu, u, o), q = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) {
+            u += p;
+            v += q;
+        }
+    }
+    *total_a = __shfl_sync(0xffffffffu, u, 31);
+    *total_b = __shfl_sync(0xffffffffu, v, 31);
+    a = x - a + __shfl_sync(0xffffffffu, u - u0, warp);
+    b = y - b + __shfl_sync(0xffffffffu, v - v0, warp);
+}
+
+// The last i of [0, n) with at[i] <= x (at ascending, at[0] <= x).
+__device__ __forceinline__ int find(const int* at, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (at[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
+    extern __shared__ int smem[];
+    __shared__ int64_t part[32][2];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_seqs;
+    const Shared s(smem, n);
+    griddep_wait();
+    int errors = 0;
+    int count = *a.free_count;
+    if (count < 0 || count > a.num_blocks) {              // nothing can be given or taken back
+        errors |= PKV_DEVERR_LENGTH;
+        count = -1;
+    }
+
+    // lengths and changes; a change that cannot be is none
+    for (int b = tid; b < n; b += kThreads) {
+        const int len = a.lens[b], g = a.grow[b];
+        int change = g;
+        const int64_t after = (int64_t)len + g;
+        if (len < 0 || after < 0 || blocks(len) > a.max_blocks || after > (int64_t)a.max_blocks * kBlock || count < 0) {
+            if (g != 0 || len < 0) errors |= PKV_DEVERR_LENGTH;
+            change = 0;
+        }
+        s.len[b] = max(len, 0);
+        s.change[b] = change;
+        s.rows[b] = max(g, 0);
+        s.back[b] = 0;
+    }
+    __syncthreads();
+    // blocks that come back: a warp a request counts the table's entries that are blocks
+    bool drops = false;
+    for (int b = tid; b < n; b += kThreads) drops |= s.change[b] < 0;
+    const bool any_drop = __syncthreads_or(drops);
+    auto is_block = [&](int id) { return id >= 0 && id < a.num_blocks; };
+    if (any_drop) {
+        for (int b = warp; b < n; b += kThreads / 32) {
+            if (s.change[b] >= 0) continue;
+            const int j1 = blocks(s.len[b]);
+            int c = 0;
+            for (int j = blocks(s.len[b] + s.change[b]) + lane; j < j1; j += 32) {
+                const int id = a.table[(int64_t)b * a.max_blocks + j];
+                c += is_block(id);
+                if (id >= a.num_blocks) errors |= PKV_DEVERR_BLOCK_ID;
+            }
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (lane == 0) s.back[b] = c;
+        }
+        __syncthreads();
+    }
+    // sums, each thread over consecutive requests
+    const int each = (n + kThreads - 1) / kThreads, b0 = min(tid * each, n), b1 = min(b0 + each, n);
+    int64_t rows = 0, back = 0, all_rows, all_back;
+    for (int b = b0; b < b1; ++b) {
+        rows += s.rows[b];
+        back += s.back[b];
+    }
+    scan2(rows, back, &all_rows, &all_back, part);
+    int64_t need = 0, none = 0, all_need, all_none;
+    for (int b = b0; b < b1; ++b) {
+        const int mine = s.back[b];
+        back += mine;
+        s.back[b] = (int)(all_back - back);               // of later requests
+        s.row[b] = (int)min(rows, (int64_t)0x7fffffff);
+        rows += s.rows[b];
+        if (s.change[b] > 0 && rows > a.num_rows) {       // its rows do not fit
+            errors |= PKV_DEVERR_LENGTH;
+            s.change[b] = 0;
+        }
+        if (s.change[b] > 0) need += blocks(s.len[b] + s.change[b]) - blocks(s.len[b]);
+    }
+    if (all_rows > a.num_rows) errors |= PKV_DEVERR_LENGTH;
+    scan2(need, none, &all_need, &all_none, part);
+    const int64_t room = count < 0 ? 0 : a.num_blocks - count;
+    if (all_back > room) errors |= PKV_DEVERR_BLOCK_ID;   // (a block was given back twice)
+    const int top = count < 0 ? 0 : (int)(count + min(all_back, room));
+    int taken = 0;                                        // blocks needed by the requests that get theirs, up to here
+    for (int b = b0; b < b1; ++b) {
+        s.need[b] = (int)min(need, (int64_t)0x7fffffff);
+        if (s.change[b] <= 0) continue;
+        const int c = blocks(s.len[b] + s.change[b]) - blocks(s.len[b]);
+        need += c;
+        if (c > 0 && need > top) {                        // not enough are free
+            errors |= PKV_DEVERR_NO_BLOCKS;
+            s.change[b] = 0;
+        } else if (c > 0) {
+            taken = (int)need;
+        }
+    }
+    taken = __reduce_max_sync(0xffffffffu, taken);
+    __syncthreads();
+    if (lane == 0) part[warp][0] = taken;
+    __syncthreads();
+    taken = __reduce_max_sync(0xffffffffu, (int)part[lane][0]);
+
+    cluster.sync();                                       // every CTA has read the old state
+    if (any_drop) {
+        // last block first: a request's entries are taken from its end
+        for (int b = warp * ctas + rank; b < n; b += kThreads / 32 * ctas) {
+            if (s.change[b] >= 0) continue;
+            const int j0 = blocks(s.len[b] + s.change[b]);
+            int at = s.back[b];
+            for (int j = blocks(s.len[b]) - 1 - lane; __any_sync(0xffffffffu, j >= j0); j -= 32) {
+                int32_t* e = a.table + (int64_t)b * a.max_blocks + j;
+                const int id = j >= j0 ? *e : -1;
+                const bool give = is_block(id);
+                const unsigned m = __ballot_sync(0xffffffffu, give);
+                const int place = at + __popc(m & ((1u << lane) - 1u));
+                if (give && place < room) a.free_blocks[count + place] = id;
+                if (j >= j0) *e = -1;
+                at += __popc(m);
+            }
+        }
+        __threadfence();
+        cluster.sync();                                   // the stack is whole
+    }
+    const int64_t first = (int64_t)rank * kThreads + tid, stride = (int64_t)ctas * kThreads;
+    auto block_of = [&](int b, int j) -> int {            // request b's block j, which is new
+        const int id = __ldcg(a.free_blocks + top - 1 - (s.need[b] + j - blocks(s.len[b])));
+        if (is_block(id)) return id;
+        errors |= PKV_DEVERR_BLOCK_ID;
+        return -1;
+    };
+    for (int64_t k = first; k < taken; k += stride) {
+        // (requests without new blocks share their place with the next that has some: the last with it)
+        const int b = find(s.need, n, (int)k);
+        const int j = blocks(s.len[b]) + (int)k - s.need[b];
+        if (s.change[b] > 0 && j < blocks(s.len[b] + s.change[b])) a.table[(int64_t)b * a.max_blocks + j] = block_of(b, j);
+    }
+    const int64_t shown = min(all_rows, a.num_rows);
+    for (int64_t r = first; r < shown; r += stride) {
+        const int b = find(s.row, n, (int)r);
+        const int64_t at = (int64_t)s.len[b] + (r - s.row[b]);
+        int64_t slot = -1;
+        if (s.change[b] > 0) {
+            const int j = (int)(at / kBlock), had = blocks(s.len[b]);
+            int id = j < had ? a.table[(int64_t)b * a.max_blocks + j] : block_of(b, j);
+            if (!is_block(id)) {
+                errors |= PKV_DEVERR_BLOCK_ID;
+                id = -1;
+            }
+            if (id >= 0) slot = (int64_t)id * kBlock + at % kBlock;
+        }
+        a.slots[r] = slot;
+        if (a.positions) a.positions[r] = (int)at;
+    }
+    for (int64_t b = first; b < n; b += stride) {
+        if (s.change[b] != 0) a.lens[b] = s.len[b] + s.change[b];
+        if (a.granted) a.granted[b] = max(s.change[b], 0);
+        if (a.row_starts) a.row_starts[b] = s.row[b];
+    }
+    if (first == 0 && count >= 0) *a.free_count = top - taken;
+    errors = (int)__reduce_or_sync(0xffffffffu, (unsigned)errors);
+    if (errors && lane == 0) raise_error(a.err, errors);
+}
+
+}  // namespace tables
+
+bool block_tables_fit(int num_seqs) { return num_seqs <= tables::kMaxSeqs; }
+
+cudaError_t launch_block_tables(int32_t* table, int max_blocks, int32_t* lens, const int32_t* grow, int num_seqs,
+                                int32_t* free_blocks, int32_t* free_count, int64_t num_blocks, int64_t* slots,
+                                int32_t* positions, int32_t* granted, int64_t* row_starts, int64_t num_rows, int* err,
+                                cudaStream_t st) {
+    using namespace tables;
+    static std::atomic<uint64_t> set{0};
+    const Arg a{table, lens, grow, free_blocks, free_count, slots, positions, granted, row_starts, err, num_blocks,
+                num_rows, num_seqs, max_blocks};
+    const size_t bytes = (size_t)num_seqs * kArrays * sizeof(int), most = (size_t)kMaxSeqs * kArrays * sizeof(int);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!bit || !(set.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    const unsigned ctas = num_rows > kManyRows ? kCluster : 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, update_kernel, a);
+}
+
+}  // namespace pkv

@@ -67,14 +67,14 @@
 #include <type_traits>
 
 #include "rows.cuh"
-#include "tc_ptx.cuh"
+#include "tc_rows.cuh"
 
 namespace pkv {
 int num_sms_current();
 
 namespace prompt {
 
-using namespace ptx;
+using namespace tcrow;
 using rows::store32;
 using rows::View;
 
@@ -422,116 +422,7 @@ struct Walk {
     }
 };
 
-// ------------------------------------------------------------------ PTX pieces of this kernel
-
-struct Ctl {
-    volatile int* abort;
-    int* err;
-    uint64_t limit;
-};
-// (inlined: a call would keep ptxas from giving the roles registers of their own)
-__device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, volatile int* abort, int* err, uint64_t limit) {
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63) == 0) {
-            if (*abort) return false;
-            if (globaltimer_ns() - t0 > limit) {
-                raise_error(err, PKV_DEVERR_TIMEOUT);
-                *abort = 1;
-                return false;
-            }
-        }
-    }
-}
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return wait_spin(bar, parity, c.abort, c.err, c.limit);
-}
-
-// A box of a 3-D tensor (dim, head, token) -> shared memory.
-__device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap* map, int d, int h, int t, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
-            dst),
-        "l"(map), "r"(d), "r"(h), "r"(t), "r"(bar)
-        : "memory");
-}
-
-// Shared-memory matrix descriptor of a 128-byte-swizzled operand.  K-major: sbo = bytes between
-// groups of 8 rows (lbo unused).  MN-major: lbo = bytes between 64-element slabs, sbo between groups of 8 k.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-
-// The issuer's operations run in warp-uniform code with one lane's predicate: in code that one lane
-// runs alone, every descriptor is moved to a uniform register first, which cost ~107 clocks a MMA
-// against the 64 that the tensor core needs for it.
-__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)lead)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)lead)
-        : "memory");
-}
-__device__ __forceinline__ void commit(bool lead, uint32_t bar) {
-    asm volatile(
-        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
-        "r"((uint32_t)lead)
-        : "memory");
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t f2pack(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ void f2unpack(uint64_t r, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t f2fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t f2add(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n.reg .pred P;\nelect.sync _|P, 0xffffffff;\nselp.b32 %0, 1, 0, P;\n}\n" : "=r"(p));
-    return p != 0;
-}
+// ------------------------------------------------------------------ types
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);
@@ -1299,35 +1190,6 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Arg a
 }
 
 // ------------------------------------------------------------------ host
-
-using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-Encode encoder() {
-    static const Encode fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult st;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
-            st != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return (Encode)p;
-    }();
-    return fn;
-}
-
-// Map of rows [tokens][heads][D] in boxes of 64 dims x `bh` heads x `bt` tokens.
-bool make_map(CUtensorMap* m, const pkv_rows* r, const void* fallback, int dtype, int D, int64_t tokens, int bh, int bt) {
-    const bool none = tokens < 1;                         // (nothing is ever copied: any valid map)
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)r->num_heads, (cuuint64_t)(none ? 1 : tokens)};
-    // strides of dimensions of extent 1 are never used, but are checked
-    const cuuint64_t strides[2] = {none || r->num_heads == 1 ? (cuuint64_t)D * 2 : (cuuint64_t)r->head_stride * 2,
-                                   none || tokens == 1 ? (cuuint64_t)D * 2 : (cuuint64_t)r->token_stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)bh, (cuuint32_t)bt}, one[3] = {1, 1, 1};
-    return encoder()(m, dtype == PKV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                     none ? const_cast<void*>(fallback) : r->data, dims, strides, box, one,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <typename T, int D>
 cudaError_t launch(const Arg& a, unsigned grid, cudaStream_t st) {
