@@ -6,30 +6,36 @@
 //   window: j is visible iff j <= p and (j > p - window or j < sinks)
 //   tree:   j is visible iff j < L - Q, or bit j - (L - Q) of row i of the mask is set
 //
-// A work item is up to 256 query rows of one (sequence, kv-head): 2 x PB consecutive queries, PB = floor(128 / G),
-// times the G heads of the group.  Its keys are a list of pages: those of the sinks that lie before the window, then
-// those from the first query's window to the last query.  A key's place v in that list and its position differ by one
-// jump behind the sinks, so what a row sees is at most two intervals of v, or one and the tree's bits, and pages
-// that no row sees are never touched (their table entries may be anything).
+// A work item is some queries of one sequence times the heads of HG adjacent kv-heads (HG = 4, 2 or 1).  A row tile has 128
+// rows, 128 / HG for each kv-head: PB = floor(128 / (HG G)) queries times its G heads.  The item's keys are a list of
+// pages: those of the sinks that lie before the window, then those from the first query's window to the last query.  A
+// key's place v in that list and its position differ by one jump behind the sinks, so what a row sees is at most two
+// intervals of v, or one and the tree's bits, and pages that no row sees are never touched (their table entries may
+// be anything).
 //
-// Per key tile (8 pages, 128 keys) and chain:
-//   S[128 rows, 128 keys] = Q . K^T           (A: Q in the 128-byte swizzle; B: pages as they lie in the cache)
-//   P = 2^(S scale log2(e) - m), l += sum P   (one thread per row = TMEM lane)
+// Per key tile (8 / HG pages of each kv-head, 128 columns: page after page, the heads of a page side by side, which is
+// how they lie in the cache) and chain:
+//   S[128 rows, 128 columns] = Q . K^T        (B: pages as they lie in the cache)
+//   P = 2^(S scale log2(e) - m), l += sum P   (one thread per row = TMEM lane; P = 0 in other heads' columns)
 //   O[128 rows, D] += P . V                   (A = P in TMEM, bf16; B MN-major: pages as they lie)
-// There are two chains, each with its own S, O, m and l in tensor memory and four softmax warps.  An item with more
-// than PB queries has two row tiles, one a chain, and every key tile serves both.  One with fewer (decode) has one row
-// tile, and the chains take the key tiles in turns: while one's softmax runs the other's products do; their O, m and
-// l are joined at the end of the piece.  m is set by a row's first visible keys, four octaves above their maximum; P is
-// computed against it without a maximum, and only where some P reaches 2 (a logit 5 octaves above) m rises.
+// With HG = 4 a decode step's few rows are spread over all four quarters of the lanes, and a row has 32 columns of a
+// tile to work on instead of 128.
+// There are two chains, each with its own S, O, m and l in tensor memory and four softmax warps.  With HG = 1 an item may
+// have two row tiles, one a chain, and every key tile serves both.  Otherwise the chains take the key tiles in turns:
+// while one's softmax runs the other's products do; their O, m and l are joined at the end of the piece.  m is set by a
+// row's first visible keys, four octaves above their maximum; P is computed against it without a maximum, and only where
+// some P reaches 2 (a logit 5 octaves above) m rises.
 //
 // P is rounded to bf16 (8 significant bits; l is summed from the fp32 P): the error it leaves in out is of the size
-// of out's own rounding to bf16.  fp16 would hold 11 bits, but not V's range.  FP8 caches: K and V are widened
-// to bf16 in shared memory (exact), a page's k scale multiplies its S and its v scale its P, in fp32.
+// of out's own rounding to bf16.  fp16 would hold 11 bits, but not V's range.
+// FP8 caches: S on e4m3 MMAs, the K pages as they are; a row of q is scaled by a power of two to a maximum in [128,
+// 256) and split into two e4m3 terms (exact but for elements below 2^-10 of the row's largest, which are good to 2^-17 of
+// it).  V is widened to bf16 in shared memory (exact).  A page's k scale multiplies its S and its v scale its P, in fp32.
 //
 // Work is cut into equal ranges of key tiles over all items, one range per CTA; an item that a range's end cuts leaves
 // partial (O, m, l) in the workspace, and whichever CTA finishes its part last joins them, in the keys' order.
 //
-// Roles (512 threads): warps 0-3 and 4-7 the softmax of chains 0 and 1; warps 8-11 make V (and, FP8, K) ready and run the
+// Roles (512 threads): warps 0-3 and 4-7 the softmax of chains 0 and 1; warps 8-11 make V (and, FP8, Q) ready and run the
 // epilogue; warp 12 the producer; warps 13 and 14 the MMA issuers of the chains; warp 15 the plan.  Every wait is bounded.
 #include <cuda.h>
 
@@ -49,8 +55,8 @@ using rows::store32;
 using rows::View;
 
 constexpr int kRows = 128;                 // rows of a row tile (MMA M)
-constexpr int kTP = 8;                     // pages of a key tile
-constexpr int kKeys = kTP * kBlock;        // keys of a key tile
+constexpr int kUnits = 8;                  // pages of one kv-head in a key tile
+constexpr int kCols = kUnits * kBlock;     // columns of a key tile
 constexpr int kThreads = 512;
 // Registers a thread: the launch gives every thread 128, and the roles' shares add up to as many.
 constexpr int kRegsSoftmax = 160, kRegsReady = 112, kRegsOther = 80;
@@ -87,7 +93,7 @@ struct Arg {
 // A partial slot: O as [D / 4][256 rows][4] fp32, then m and l, [256] each.
 __host__ __device__ constexpr int slot_floats(int D) { return 2 * kRows * (D + 2); }
 
-// A piece of work: key tiles [t0, t1) of queries q0 .. q0 + nq - 1 of a sequence, kv-head g.
+// A piece of work: key tiles [t0, t1) of queries q0 .. q0 + nq - 1 of a sequence, kv-heads from g on.
 struct Piece {
     int64_t row;            // q's row of query 0
     int b, g, q0, nq, t0, t1;
@@ -131,36 +137,44 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, in
     return n - j >= 32 ? x : n - j <= 0 ? 0u : x & ((1u << (n - j)) - 1u);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int HG>
 struct Cfg {
+    static constexpr int TP = kUnits / HG;                // pages of a tile (of each head)
+    static constexpr int KEYS = TP * kBlock;              // keys of a tile
+    static constexpr int RQ = kRows / HG;                 // rows of a row tile that a head has
     static constexpr int SLAB = kRows * 128;              // Q: bytes of a 64-dimension slab
     static constexpr int SLABS = D / 64;
     static constexpr int QTILE = SLABS * SLAB;
     static constexpr int NCH = D / 8;                     // 16-byte chunks of a bf16 row
     static constexpr int PAGE = kBlock * D * 2;           // a page as bf16 operand
-    static constexpr int TILE = kTP * PAGE;
-    static constexpr int LAND = FP8 ? PAGE / 2 : PAGE;    // a page of the cache; FP8: it lands in the upper half
-    static constexpr int NSK = D == 128 ? 2 : 5;          // K ring depth
-    static constexpr int NSV = D == 128 ? 3 : 5;          // V ring depth
-    static constexpr int NSC = D == 128 ? 4 : 8;          // scale ring: a tile's are read until its V slot is free
+    static constexpr int LAND = FP8 ? PAGE / 2 : PAGE;    // a page of the cache
+    static constexpr int KTILE = kUnits * LAND;
+    static constexpr int VTILE = kUnits * PAGE;           // (FP8: a page lands in the upper half of its place)
+    static constexpr int NSK = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 5);     // K ring depth
+    static constexpr int NSV = D == 128 ? 3 : FP8 ? 6 : 5;                        // V ring depth
+    static constexpr int NSC = 8;                         // scale ring: a tile's are read until its V slot is free
     static_assert(NSC > NSV, "scale ring");
+    static constexpr int NQS = 4;                         // ring of the rows' powers of two (FP8)
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + 2 * QTILE;
-    static constexpr int OFF_V = OFF_K + NSK * TILE;
-    static constexpr int OFF_BAR = OFF_V + NSV * TILE;
-    static constexpr int KFULL = 0, KREADY = NSK, KEMPTY = 2 * NSK, VFULL = 3 * NSK, VREADY = VFULL + NSV,
-                         VEMPTY = VREADY + NSV, SFULL = VEMPTY + NSV, PFA = SFULL + 2, PFB = SFULL + 4, QFULL = SFULL + 6,
-                         QEMPTY = SFULL + 8, ODONE = SFULL + 10, OFREE = SFULL + 12, LREADY = SFULL + 14, PVA = SFULL + 16,
-                         TURN = SFULL + 18, PCFULL = SFULL + 20, PCEMPTY = PCFULL + kPieces, DRAIN = PCEMPTY + kPieces;
+    static constexpr int OFF_V = OFF_K + NSK * KTILE;
+    static constexpr int OFF_BAR = OFF_V + NSV * VTILE;
+    static constexpr int KFULL = 0, KEMPTY = NSK, VFULL = 2 * NSK, VREADY = VFULL + NSV, VEMPTY = VREADY + NSV,
+                         SFULL = VEMPTY + NSV, PFA = SFULL + 2, PFB = SFULL + 4, QFULL = SFULL + 6, QREADY = SFULL + 8,
+                         QEMPTY = SFULL + 10, ODONE = SFULL + 12, OFREE = SFULL + 14, LREADY = SFULL + 16,
+                         PVA = SFULL + 18, TURN = SFULL + 20, PCFULL = SFULL + 22, PCEMPTY = PCFULL + kPieces,
+                         DRAIN = PCEMPTY + kPieces;
     static constexpr int NBAR = DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
     static constexpr int OFF_FLAG = OFF_MISC + 16;        // int[kFlags]
     static constexpr int OFF_ML = OFF_FLAG + 4 * kFlags;  // float[chain][m, l][kRows]
-    static constexpr int OFF_SC = OFF_ML + 4 * 4 * kRows; // float[NSC][k scales 8, v scales 8]
-    static constexpr int OFF_PIECE = (OFF_SC + (FP8 ? NSC * 64 : 0) + 7) / 8 * 8;
-    static constexpr int SMEM = OFF_PIECE + kPieces * (int)sizeof(Piece);
-    static constexpr int COL_O = 2 * kKeys;
+    static constexpr int OFF_PIECE = OFF_ML + 4 * 4 * kRows;
+    static constexpr int OFF_SC = OFF_PIECE + kPieces * (int)sizeof(Piece);       // FP8: float[NSC][k scales 8, v scales 8]
+    static constexpr int OFF_QS = OFF_SC + (FP8 ? NSC * 64 : 0);                  // FP8: float[NQS][kRows]
+    static constexpr int SMEM = OFF_QS + (FP8 ? NQS * 4 * kRows : 0);
+    static constexpr int COL_O = 2 * kCols;
     static constexpr int TMEM_COLS = 512;
+    static_assert(OFF_PIECE % 8 == 0, "alignment");
     static_assert(COL_O + 2 * D <= TMEM_COLS, "tensor memory budget");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -172,22 +186,31 @@ struct Seq {
     int Q, L;               // 0 queries where the lengths are bad
 };
 
+// a / b, by 32-bit arithmetic where that is enough (the 64-bit division is a long routine)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((uint64_t)(a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
 // The plan of a launch, made by one warp of every CTA alike.  An item's units are its key tiles times its row tiles
-// and kItemUnits; all items' units, in the order sequence, query block, kv-head, are cut into equal ranges, one per
+// and kItemUnits; all items' units, in the order sequence, query block, kv-heads, are cut into equal ranges, one per
 // CTA, and a CTA has the tiles whose first unit lies in its range.
+template <int HG>
 struct Plan {
+    static constexpr int TP = kUnits / HG;
     const Arg& a;
     const int lane;
-    int chunk;
+    int chunk, groups;      // sequences a lane; groups of HG kv-heads
     int64_t total, u, u1;   // all units; the CTA's place and end
-    int ctas;
+    int64_t share;          // units of a CTA, and how many CTAs have one more
+    int ctas, longer;
     int b, blk, g;          // the item at u, its first unit
     int64_t start;
     Seq s;
     int64_t packed;         // rows before sequence b
 
-    __device__ __forceinline__ Plan(const Arg& a_, int lane_) : a(a_), lane(lane_) {}
-    __device__ __forceinline__ int per() const { return 2 * a.pb; }
+    __device__ __forceinline__ Plan(const Arg& a_, int lane_) : a(a_), lane(lane_), groups(a_.Hkv / HG) {}
+    __device__ __forceinline__ int per() const { return HG == 1 ? 2 * a.pb : a.pb; }
     __device__ __forceinline__ Seq load(int i, int64_t rows, bool report) const {
         Seq x{a.q_starts ? a.q_starts[i] : rows, a.q_lens[i], a.ctx_lens[i]};
         if (x.Q < 0 || x.Q > a.max_q_len || x.L < x.Q || x.row < 0 || x.row > a.num_q_rows - x.Q ||
@@ -214,8 +237,8 @@ struct Plan {
     __device__ __forceinline__ int units(const Seq& x, int block, int& tiles, int& each) const {
         int first, nq, sp, np, jump;
         span(x, block, first, nq, sp, np, jump);
-        tiles = (np + kTP - 1) / kTP;
-        each = nq > a.pb ? 2 : 1;
+        tiles = (np + TP - 1) / TP;
+        each = HG == 1 && nq > a.pb ? 2 : 1;
         return tiles * each + kItemUnits;
     }
     template <typename V>
@@ -227,6 +250,11 @@ struct Plan {
             if (lane >= o) y += z;
         }
         return y - x;
+    }
+    __device__ __forceinline__ int64_t range(int c) const { return share * c + min(c, longer); }
+    __device__ __forceinline__ int cta_of(int64_t unit) const {
+        const int64_t head = (share + 1) * longer;
+        return unit < head ? (int)quotient(unit, share + 1) : longer + (int)quotient(unit - head, share);
     }
     __device__ __forceinline__ void begin() {
         chunk = (a.num_seqs + 31) / 32;
@@ -241,15 +269,17 @@ struct Plan {
         for (int i = b0; i < b1; ++i) {
             const Seq x = load(i, at, true);
             at += max(a.q_lens[i], 0);
-            for (int k = 0; k * per() < x.Q; ++k) mine += (int64_t)units(x, k, tiles, each) * a.Hkv;
+            for (int k = 0; k * per() < x.Q; ++k) mine += (int64_t)units(x, k, tiles, each) * groups;
         }
         const int64_t before = scan(mine);
         total = __shfl_sync(0xffffffffu, before + mine, 31);
         ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
+        share = quotient(total, ctas);
+        longer = (int)(total - share * ctas);
         u = u1 = 0;
         if ((int)blockIdx.x >= ctas || total == 0) return;
-        u = total * blockIdx.x / ctas;
-        u1 = total * (blockIdx.x + 1) / ctas;
+        u = range(blockIdx.x);
+        u1 = range(blockIdx.x + 1);
         // the lane that has the item at u, and where it lies
         const bool here = u >= before && u < before + mine;
         int fb = 0, fblk = 0, fg = 0;
@@ -262,16 +292,16 @@ struct Plan {
                 const Seq x = load(i, at, false);
                 for (int k = 0; k * per() < x.Q; ++k) {
                     const int w = units(x, k, tiles, each);
-                    if (u < r + (int64_t)w * a.Hkv) {
+                    if (u < r + (int64_t)w * groups) {
                         fb = i;
                         fblk = k;
-                        fg = (int)((u - r) / w);
+                        fg = (int)quotient(u - r, w);
                         fs = r + (int64_t)fg * w;
                         fp = at;
                         found = true;
                         break;
                     }
-                    r += (int64_t)w * a.Hkv;
+                    r += (int64_t)w * groups;
                 }
                 at += max(a.q_lens[i], 0);
             }
@@ -284,26 +314,25 @@ struct Plan {
         packed = __shfl_sync(0xffffffffu, fp, from);
         s = load(b, packed, false);
     }
-    __device__ __forceinline__ int cta_of(int64_t unit) const { return (int)(((unit + 1) * ctas - 1) / total); }
     // The next piece with tiles; the same in every lane.
     __device__ __forceinline__ bool next(Piece& p) {
         while (u < u1) {
             int tiles, each;
             const int w = units(s, blk, tiles, each);
             const int64_t keys = start + kItemUnits;      // the first tile's first unit
-            auto tile_at = [&](int64_t x) { return (int)min((int64_t)tiles, max((int64_t)0, (x - keys + each - 1) / each)); };
-            p.t0 = u <= keys ? 0 : tile_at(u);
-            p.t1 = u1 <= keys ? 0 : tile_at(u1);
+            auto tile_at = [&](int64_t x) { return x <= keys ? 0 : (int)min((int64_t)tiles, (x - keys + each - 1) >> (each - 1)); };
+            p.t0 = tile_at(u);
+            p.t1 = tile_at(u1);
             const bool some = p.t1 > p.t0;
             if (some) {
                 p.row = s.row;
                 p.b = b;
-                p.g = g;
+                p.g = g * HG;
                 p.q0 = blk * per();
                 span(s, blk, p.first, p.nq, p.sp, p.np, p.jump);
                 p.L = s.L;
                 p.Q = s.Q;
-                p.two = p.nq > a.pb;
+                p.two = each == 2;
                 p.end = 0;
                 p.c0 = blockIdx.x;
                 p.parts = 1;
@@ -315,7 +344,7 @@ struct Plan {
             // on to the next item
             start += w;
             u = start;
-            if (++g == a.Hkv) {
+            if (++g == groups) {
                 g = 0;
                 if (++blk * per() >= s.Q) {
                     blk = 0;
@@ -350,12 +379,20 @@ constexpr float kLimit = 0x1p29f;
 // 2^-120 (subnormals too).  NaN codes become 480 here: the caller looks for them.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-    uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), y = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+    const uint32_t x = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), y = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
     const uint32_t f = 0x7b807b80u;        // 2^120
     asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(lo) : "r"(x), "r"(f));
     asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(hi) : "r"(y), "r"(f));
 }
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// Two bf16 (of a word) times f as e4m3 codes, and what they leave as e4m3 codes.
+__device__ __forceinline__ void split2(uint32_t w, float f, uint32_t& hi, uint32_t& lo) {
+    const float2 x = make_float2(bf16_lo(w) * f, bf16_hi(w) * f);
+    hi = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    const float2 y = e4m3x2_to_float2(hi);
+    lo = __nv_cvt_float2_to_fp8x2(make_float2(x.x - y.x, x.y - y.y), __NV_SATFINITE, __NV_E4M3);
+}
 
 // ------------------------------------------------------------------ kernel
 
@@ -364,27 +401,30 @@ __device__ __forceinline__ float* part_slot(const Arg& a, int cta, bool starts) 
     return a.partials + ((size_t)cta * 2 + (starts ? 1 : 0)) * slot_floats(D);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int HG>
 __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_constant__ Arg a) {
-    using K = Cfg<D, FP8>;
+    using K = Cfg<D, FP8, HG>;
     extern __shared__ __align__(1024) uint8_t smem[];     // (the swizzle needs it; checked below)
     const uint32_t sb = smem_u32(smem);
     // (the warp's number by a shuffle: known to be uniform, and with it the roles' control flow)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     auto bar = [&](int i) -> uint32_t { return sb + K::OFF_BAR + 8 * i; };
-    constexpr int NSK = K::NSK, NSV = K::NSV;
+    constexpr int NSK = K::NSK, NSV = K::NSV, RQ = K::RQ;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 4);
     volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 8);   // (drain waits at the end)
     volatile int* nonfinite = reinterpret_cast<volatile int*>(smem + K::OFF_FLAG);
     float* ml = reinterpret_cast<float*>(smem + K::OFF_ML);
     float* scales = reinterpret_cast<float*>(smem + K::OFF_SC);
+    float* q_scale = reinterpret_cast<float*>(smem + K::OFF_QS);
+    Piece* ring = reinterpret_cast<Piece*>(smem + K::OFF_PIECE);
     const Ctl ctl{abort_flag, a.err, a.wait_limit_ns};
+    // every wait and every TMEM access is warp-uniform (tcgen05.ld / st are .aligned)
+    auto wait_all = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, wait(bb, parity, ctl)); };
 
     if (tid == 0) {
         for (int i = 0; i < NSK; ++i) {
             mbar_init(bar(K::KFULL + i), 1);
-            mbar_init(bar(K::KREADY + i), 4);             // (FP8) one arrival a warp that widens
             mbar_init(bar(K::KEMPTY + i), 2);             // one of each chain
         }
         for (int i = 0; i < NSV; ++i) {
@@ -397,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             mbar_init(bar(K::PFA + i), 4);                // one arrival a softmax warp
             mbar_init(bar(K::PFB + i), 4);
             mbar_init(bar(K::QFULL + i), 1);
+            mbar_init(bar(K::QREADY + i), 4);
             mbar_init(bar(K::QEMPTY + i), 2);
             mbar_init(bar(K::ODONE + i), 1);
             mbar_init(bar(K::OFREE + i), 4);
@@ -415,55 +456,66 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         mbar_fence_init();
     }
     if (warp == kProducer && lane == 0) asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.q) : "memory");
-    if (warp == kPlan) {
+    if (warp == kMma) {
         tmem_alloc(smem_u32(tmem_slot), K::TMEM_COLS);
         tmem_relinquish();
     }
-    griddep_wait();
     if ((sb & 1023) != 0 && tid == 0) {
         raise_error(a.err, PKV_DEVERR_TIMEOUT);           // (never: the declaration above aligns it)
         *abort_flag = 1;
     }
-    tc_fence_before();
-    cta_bar_sync();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    // every role goes through here, from its own code path (non-.aligned barrier); the tensor memory's address
+    auto enter = [&]() -> uint32_t {
+        griddep_wait();
+        tc_fence_before();
+        cta_bar_sync();
+        tc_fence_after();
+        return *tmem_slot;
+    };
 
     // The pieces of work: the n-th (nullptr: a wait gave up), until its release by every warp.
-    const Piece* ring = reinterpret_cast<const Piece*>(smem + K::OFF_PIECE);
     auto piece_at = [&](int n) -> const Piece* {
-        return __all_sync(0xffffffffu, wait(bar(K::PCFULL + n % kPieces), (n / kPieces) & 1, ctl)) ? ring + n % kPieces
-                                                                                                  : nullptr;
+        return wait_all(bar(K::PCFULL + n % kPieces), (n / kPieces) & 1) ? ring + n % kPieces : nullptr;
     };
     auto release = [&](int n) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(K::PCEMPTY + n % kPieces));
     };
-    // every wait and every TMEM access is warp-uniform (tcgen05.ld / st are .aligned)
-    auto wait_all = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, wait(bb, parity, ctl)); };
 
     if (warp < kReady) {
         // ------------------------------------------------ softmax of chain i, thread r = row r
         regs_inc<kRegsSoftmax>();
-        const int i = warp >> 2, r = tid & (kRows - 1);
-        const int G = a.group, pos = r / G;
+        const uint32_t tmem = enter();
+        const int i = warp >> 2, r = tid & (kRows - 1), hw = (warp & 3) * HG / 4;      // hw: the row's head of the HG
+        const int G = a.group, pos = r % RQ / G;
         const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t scol = tmem + lbase + i * kKeys;   // S / P
+        const uint32_t scol = tmem + lbase + i * kCols;   // S / P
         const uint32_t ocol = tmem + lbase + K::COL_O + i * D;
-        const float sc = a.scale_log2;
         auto signal = [&](uint32_t bb) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bb);
         };
+        // S of 32 of the row's keys of the tile, from key k on (a multiple of 32)
+        auto load_s = [&](int k, uint32_t (&s)[32]) {
+            if constexpr (HG == 1) {
+                tmem_ld32_async(scol + k, s);
+            } else {
+                tmem_ld16_at<0>(scol + (k * HG + hw * kBlock), s);
+                tmem_ld16_at<16>(scol + ((k + kBlock) * HG + hw * kBlock), s);
+            }
+        };
+        constexpr int STEP = K::KEYS < 64 ? K::KEYS : 64; // keys whose P is written at once
+        constexpr bool PAIR = STEP == 64;
         bool ok = true;
-        int scnt = 0, ocnt = 0, tbase = 0;                // this chain's tiles and pieces; the CTA's tiles
+        int scnt = 0, ocnt = 0, tbase = 0, qbase = 0;     // this chain's tiles and pieces; the CTA's tiles and Q tiles
         for (int n = 0; ok; ++n) {
             const Piece* p = piece_at(n);
             if (!p || p->end) break;
             const int cnt = p->count(i), x0 = p->begin(i), step = p->step(), t0 = p->t0;
-            const int base = tbase;
+            const int base = tbase, qt = qbase + (p->two ? i : 0);
             tbase += p->tiles();
+            qbase += p->two ? 2 : 1;
             if (cnt == 0) {
                 release(n);
                 continue;
@@ -485,109 +537,77 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             const int tree0 = p->L - p->Q, tree_n = p->Q;
             const int ends = p->seen_end(a, min(p->nq, p->two ? (i + 1) * a.pb : a.pb));
             // m: the reference maximum (exp2 units), l: the sum of P
-            float m = row_ok ? -INFINITY : 0.f, l = 0.f;
+            float m = row_ok ? -INFINITY : 0.f, l = 0.f, sc = a.scale_log2;
             for (int j = 0; j < cnt; ++j, ++scnt) {
-                const int x = x0 + j * step, v0 = (t0 + x) * kKeys;
+                const int x = x0 + j * step, v0 = (t0 + x) * K::KEYS;
                 if (!(ok = wait_all(bar(K::SFULL + i), scnt & 1))) break;
                 if (!live) {
                     if (lane == 0) {
-                        mbar_arrive(bar(K::PFA + i));
+                        if (HG == 1) mbar_arrive(bar(K::PFA + i));
                         mbar_arrive(bar(K::PFB + i));
                     }
                     continue;
                 }
                 tc_fence_after();
-                const float* ks = scales + ((base + x) % K::NSC) * 16;
-                const bool masked = !__all_sync(0xffffffffu, (v0 >= see.wl && v0 + kKeys - 1 <= see.wh) || v0 + kKeys <= see.ns);
-                // the visible ones of columns c .. c + 31
-                auto bits = [&](int c) -> uint32_t {
-                    const int v = v0 + c, n_s = see.ns - v, lo = max(see.wl - v, 0), hi = min(see.wh - v, 31);
+                uint32_t sa[32], sb_[32];
+                load_s(0, sa);
+                if (FP8 && j == 0) sc = a.scale_log2 * q_scale[qt % K::NQS * kRows + r];
+                const float* ks = scales + ((base + x) % K::NSC) * 16 + hw;     // (of unit u: ks[u * HG])
+                const bool masked = !__all_sync(0xffffffffu, (v0 >= see.wl && v0 + K::KEYS - 1 <= see.wh) || v0 + K::KEYS <= see.ns);
+                // the visible ones of keys k .. k + 31 of the tile
+                auto bits = [&](int k) -> uint32_t {
+                    const int v = v0 + k, n_s = see.ns - v, lo = max(see.wl - v, 0), hi = min(see.wh - v, 31);
                     uint32_t w = n_s >= 32 ? 0xffffffffu : n_s > 0 ? (1u << n_s) - 1u : 0u;
                     if (lo <= hi) w |= (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
                     if (tree && v + 31 >= tree0) w |= tree_bits(tree, a.tree_words, v - tree0, tree_n);
                     return w;
                 };
-                uint32_t sa[32], sb_[32];
-                tmem_ld32_async(scol, sa);
-                // O *= alpha (exact powers of 2, or 1)
-                auto rescale_o = [&](float alpha) {
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        float o[16];
-                        tmem_ld16(ocol + c, o);
-                        uint32_t v[16];
+                // the largest visible S (FP8: times its page's scale) of 32 keys from k on
+                auto largest = [&](const uint32_t (&s)[32], int k, uint32_t w) -> float {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(o[y] * alpha);
-                        tmem_st16u(ocol + c, v);
+                    for (int y = 0; y < 32; ++y) {
+                        const float f = FP8 ? __uint_as_float(s[y]) * ks[(k + y) / kBlock * HG] : __uint_as_float(s[y]);
+                        mx[y & 3] = fmaxf(mx[y & 3], w >> y & 1 ? f : -INFINITY);
                     }
-                    tmem_wait_st();
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 };
-                tmem_wait_ld_into(sa);
-                // the largest visible S (FP8: times its page's scale) of columns [c0, c1)
-                auto maximum = [&](int c0, int c1) -> float {
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int c = c0; c < c1; c += 32) {
-                        uint32_t s[32];
-                        tmem_ld32_async(scol + c, s);
-                        const uint32_t w = bits(c);
-                        tmem_wait_ld_into(s);
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) {
-                            const float f = __uint_as_float(s[y]) * (FP8 ? ks[(c + y) / kBlock] : 1.f);
-                            mx[y & 3] = fmaxf(mx[y & 3], w >> y & 1 ? f : -INFINITY);
-                        }
-                        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                    }
-                    return top;
-                };
-                if (!__all_sync(0xffffffffu, m > -INFINITY)) {
-                    // no reference yet (a piece's first tile): the largest of the first 32 keys where all are seen, else
-                    // of the tile.  (O and l are 0 so far, or NaN)
-                    float top = -INFINITY;
-                    if (!masked) {
-                        float t1 = -INFINITY;
-#pragma unroll
-                        for (int y = 0; y < 16; y += 2) {
-                            top = max3(top, __uint_as_float(sa[y]), __uint_as_float(sa[y + 1]));
-                            t1 = max3(t1, __uint_as_float(sa[y + 16]), __uint_as_float(sa[y + 17]));
-                        }
-                        // (a scale has any sign; a smaller reference than the maximum is as good)
-                        if (FP8) top = fmaxf(top * ks[0], t1 * ks[1]);
-                        else top = fmaxf(top, t1);
-                    }
-                    if (!__all_sync(0xffffffffu, top > -INFINITY)) top = maximum(0, kKeys);
-                    if (m == -INFINITY) m = top * sc + kHeadroom;
-                    // (too far below 0 is only seen here: m rises)
-                    if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
-                }
-                // (rare) a P of 64 keys at column c reaches 2: m rises by a whole number of octaves, and the P written in
+                // (rare) a P of the keys from k on reaches 2: m rises by a whole number of octaves, and the P written in
                 // this tile, O and l are scaled down by as many (exact but for what falls below fp32's range)
-                auto raise_ref = [&](float target, int c) {
+                auto raise_ref = [&](float target, int k) {
                     const float inc = target + kHeadroom > m ? ceilf(target + kHeadroom - m) : 0.f;
-                    const int k = (int)fminf(inc, 127.f);
-                    const float alpha = k < 127 ? __uint_as_float((uint32_t)(127 - k) << 23) : 0.f;
-                    if (c > 0) {                          // the first half's P is being used: it ends in O
+                    const int e = (int)fminf(inc, 127.f);
+                    const float alpha = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+                    if (k > 0) {                          // the first half's P is being used: it ends in O
                         wait_all(bar(K::PVA + i), scnt & 1);
                         tc_fence_after();
                     }
-                    if (j > 0 || c > 0) rescale_o(alpha);
+                    if (j > 0 || k > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float o[16];
+                            tmem_ld16(ocol + c, o);
+                            uint32_t v[16];
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(o[y] * alpha);
+                            tmem_st16u(ocol + c, v);
+                        }
+                        tmem_wait_st();
+                    }
                     l *= alpha;
                     m += inc;
                 };
-                // P of 32 keys at column c, two per packed fp32 operation (the even key in the low half); adds them to
+                uint32_t over = 0;                        // (FP8) the OR of the P to be written
+                // P of 32 keys from k on, two per packed fp32 operation (the even key in the low half); adds them to
                 // acc.  (Rows with nothing visible so far keep m = -inf: all their P are masked.)
-                auto neg_m = [&] {
-                    const float nm = m == -INFINITY ? 0.f : -m;
-                    return f2pack(__float_as_uint(nm), __float_as_uint(nm));
-                };
-                uint32_t over = 0;                        // (FP8) the OR of the P of 64 keys
-                auto emit = [&](const uint32_t (&s)[32], int c, uint32_t* v, uint64_t& acc, uint64_t nm2, auto mask, uint32_t w) {
+                auto emit = [&](const uint32_t (&s)[32], int k, uint32_t* v, uint64_t& acc, auto mask, uint32_t w) {
                     uint64_t ca = 0, cb = 0;
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    const uint64_t nm2 = f2pack(__float_as_uint(nm), __float_as_uint(nm));
 #pragma unroll
                     for (int h = 0; h < 32; h += 16) {
-                        const float f = FP8 ? sc * ks[(c + h) / kBlock] : sc;
+                        const int u = (k + h) / kBlock * HG;
+                        const float f = FP8 ? sc * ks[u] : sc;
                         const uint64_t sc2 = f2pack(__float_as_uint(f), __float_as_uint(f));
 #pragma unroll
                         for (int y = h; y < h + 16; y += 2) {
@@ -601,85 +621,93 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                             if ((y >> 1) & 1) cb = f2add(cb, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
                             else ca = f2add(ca, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
                             if constexpr (FP8) {
+                                const float vs = ks[8 + u];
                                 over |= __float_as_uint(p0) | __float_as_uint(p1);
-                                const float vs = ks[8 + (c + h) / kBlock];
-                                float w0 = p0 * vs, w1 = p1 * vs;
+                                p0 *= vs;
+                                p1 *= vs;
                                 if constexpr (decltype(mask)::value) {   // (a scale may be infinite or NaN)
-                                    w0 = w >> y & 1 ? w0 : 0.f;
-                                    w1 = w >> (y + 1) & 1 ? w1 : 0.f;
+                                    p0 = w >> y & 1 ? p0 : 0.f;
+                                    p1 = w >> (y + 1) & 1 ? p1 : 0.f;
                                 }
-                                v[y >> 1] = pack_bf16(w0, w1);
-                            } else {
-                                v[y >> 1] = pack_bf16(p0, p1);
                             }
+                            v[y >> 1] = pack_bf16(p0, p1);
                         }
                     }
                     acc = f2add(acc, f2add(ca, cb));
                 };
-                // The P of 64 keys is written once none is known to reach 2 (the top exponent bit is clear below).
-                // True: written.
-                auto write = [&](uint64_t acc, int c, const uint32_t (&v)[32], bool force) -> bool {
-                    bool high;
-                    if constexpr (FP8) {
-                        high = (over & 0x40000000u) != 0;
-                    } else {
-                        uint32_t any[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                        for (int y = 4; y < 32; ++y) any[y & 3] |= v[y];
-                        high = ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
-                    }
-                    if (__any_sync(0xffffffffu, row_ok && high) && !force) return false;
-                    tmem_st32u(scol + (c >> 1), v);
-                    float a0, a1;
-                    f2unpack(acc, a0, a1);
-                    l += a0 + a1;                         // (behind the store)
-                    tmem_wait_st();
-                    return true;
-                };
-                // 64 keys at column c, masked; a second time, with m raised, where the first is too large (NaN logits pass
-                // then).  A second half that no row sees is not read by the PV.
-                auto careful = [&](int c) {
-                    if (c > 0 && c >= ends - v0) return;
-                    for (bool force = false;; force = true) {
-                        uint32_t v[32];
-                        uint64_t acc = 0;
-                        const uint64_t nm2 = neg_m();
-                        over = 0;
-                        tmem_ld32_async(scol + c, sa);
-                        tmem_wait_ld_into(sa);
-                        tmem_ld32_async(scol + c + 32, sb_);
-                        emit(sa, c, v, acc, nm2, std::true_type{}, bits(c));
-                        tmem_wait_ld_into(sb_);
-                        emit(sb_, c + 32, v + 16, acc, nm2, std::true_type{}, bits(c + 32));
-                        if (write(acc, c, v, force)) break;
-                        const float top = maximum(c, c + 64);
-                        raise_ref(row_ok ? top * sc : -INFINITY, c);
-                    }
-                };
+                tmem_wait_ld_into(sa);
                 // (one copy of either path: the instruction cache holds little more than a tile's code)
 #pragma unroll 1
-                for (int c = 0; c < kKeys; c += 64) {
-                    bool done = false;
-                    if (!masked) {                        // loads in flight behind the arithmetic
-                        uint32_t v[32];
+                for (int k = 0; k < K::KEYS; k += STEP) {
+                    uint32_t v[STEP / 2];
+                    // a second half that no row sees is not read by the PV
+                    const bool none = k > 0 && k >= ends - v0;
+                    for (bool again = false; !none; again = true) {
                         uint64_t acc = 0;
-                        const uint64_t nm2 = neg_m();
                         over = 0;
-                        tmem_ld32_async(scol + c + 32, sb_);
-                        emit(sa, c, v, acc, nm2, std::false_type{}, 0u);
-                        tmem_wait_ld_into(sb_);
-                        tmem_ld32_async(scol + 64, sa);   // (for the second half; after it, for nothing)
-                        emit(sb_, c + 32, v + 16, acc, nm2, std::false_type{}, 0u);
-                        tmem_wait_ld_into(sa);
-                        done = write(acc, c, v, false);
-                    }
-                    if (!done) {
-                        careful(c);
-                        tmem_ld32_async(scol + 64, sa);
-                        tmem_wait_ld_into(sa);
+                        if (PAIR) load_s(k + 32, sb_);
+                        if (!__all_sync(0xffffffffu, m > -INFINITY)) {
+                            // no reference yet (a piece's first tile): the largest that is visible.  (O and l are 0 so far)
+                            if (PAIR) tmem_wait_ld_into(sb_);
+                            float top = largest(sa, k, masked ? bits(k) : ~0u);
+                            if (PAIR) top = fmaxf(top, largest(sb_, k + 32, masked ? bits(k + 32) : ~0u));
+                            if (m == -INFINITY) m = top * sc + kHeadroom;
+                            // (too far below 0 is only seen here: m rises)
+                            if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
+                        }
+                        if (!masked) emit(sa, k, v, acc, std::false_type{}, 0u);
+                        else emit(sa, k, v, acc, std::true_type{}, bits(k));
+                        if constexpr (PAIR) {
+                            tmem_wait_ld_into(sb_);
+                            if (HG == 1) load_s(64, sa);  // (for the second half; after it, for nothing)
+                            if (!masked) emit(sb_, k + 32, v + 16, acc, std::false_type{}, 0u);
+                            else emit(sb_, k + 32, v + 16, acc, std::true_type{}, bits(k + 32));
+                            if (HG == 1) tmem_wait_ld_into(sa);
+                        }
+                        // P is written once none is known to reach 2 (the top exponent bit is clear below)
+                        bool high;
+                        if constexpr (FP8) {
+                            high = (over & 0x40000000u) != 0;
+                        } else {
+                            uint32_t any[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                            for (int y = 4; y < STEP / 2; ++y) any[y & 3] |= v[y];
+                            high = ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
+                        }
+                        if (__any_sync(0xffffffffu, row_ok && high) && !again) {
+                            // once more with m raised (NaN logits pass then)
+                            load_s(k, sa);
+                            tmem_wait_ld_into(sa);
+                            float top = largest(sa, k, masked ? bits(k) : ~0u);
+                            if (PAIR) {
+                                load_s(k + 32, sb_);
+                                tmem_wait_ld_into(sb_);
+                                top = fmaxf(top, largest(sb_, k + 32, masked ? bits(k + 32) : ~0u));
+                            }
+                            raise_ref(row_ok ? top * sc : -INFINITY, k);
+                            continue;
+                        }
+                        if constexpr (HG == 1) {
+                            tmem_st32u(scol + (k >> 1), v);
+                        } else {
+#pragma unroll
+                            for (int pg = 0; pg < K::TP; ++pg) {
+                                uint32_t w[8], z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) w[y] = v[pg * 8 + y];
+                                tmem_st8(scol + (pg * HG + hw) * 8, w);
+#pragma unroll
+                                for (int y = 1; y < HG; ++y) tmem_st8(scol + (pg * HG + (hw + y) % HG) * 8, z);
+                            }
+                        }
+                        float a0, a1;
+                        f2unpack(acc, a0, a1);
+                        l += a0 + a1;                     // (behind the store)
+                        tmem_wait_st();
+                        break;
                     }
                     // P of the first 64 keys: their PV may run while the rest is computed
-                    signal(bar(K::PFA + i) + (c ? 8 * (K::PFB - K::PFA) : 0));
+                    signal(bar(HG == 1 && k == 0 ? K::PFA + i : K::PFB + i));
                 }
             }
             if (!ok) break;
@@ -695,21 +723,27 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             release(n);
         }
     } else if (warp < kProducer) {
-        // ------------------------------------------------ V (FP8: K too) made ready; epilogue, thread r = row r
+        // ------------------------------------------------ V (FP8: Q too) made ready; epilogue, thread r = row r
         regs_dec<kRegsReady>();
-        const int w = warp - kReady, r = tid & (kRows - 1);
-        const int G = a.group, pos = r / G, hl = r - pos * G;
+        const uint32_t tmem = enter();
+        const int w = warp - kReady, r = tid & (kRows - 1), hw = w * HG / 4;
+        const int G = a.group, rr = r % RQ, pos = rr / G, hl = rr - pos * G;
         const uint32_t lbase = (uint32_t)(w * 32) << 16;
 
-        // Keys of a tile that not every row of the item sees: a weight of 0 times NaN or infinity is NaN, so V rows that no
-        // row sees are cleared, and non-finite values among those that some see become 0 here and are added back, row
-        // by row, in the epilogue (from global memory: rare).
+        // V is made harmless to rows that do not see it: a weight of 0 times NaN or infinity is NaN.  Keys that no row sees
+        // are cleared, and non-finite values become 0 where some rows do not see them (HG > 1: everywhere, for other
+        // heads' rows have weight 0 for them) and are added back, row by row, in the epilogue (from global memory:
+        // rare).
         struct Guard {
             int ns_all, wl_all, wh_all, ns_any, wl_any, wh_any;
-            __device__ __forceinline__ bool all(int v) const { return v < ns_all || (v >= wl_all && v <= wh_all); }
             __device__ __forceinline__ bool any(int v) const { return v < ns_any || (v >= wl_any && v <= wh_any); }
-            __device__ __forceinline__ bool all8(int v) const {
-                return v + 7 < ns_all || (v >= wl_all && v + 7 <= wh_all);
+            __device__ __forceinline__ bool all(int v) const { return HG == 1 && (v < ns_all || (v >= wl_all && v <= wh_all)); }
+            // all of v .. v + n - 1 are seen by some row (whole: by every row of the tile)
+            __device__ __forceinline__ bool any_of(int v, int n) const {
+                return v + n <= ns_any || (v >= wl_any && v + n - 1 <= wh_any);
+            }
+            __device__ __forceinline__ bool all_of(int v, int n) const {
+                return HG == 1 && (v + n <= ns_all || (v >= wl_all && v + n - 1 <= wh_all));
             }
         };
         auto guard_of = [&](const Piece& p) {
@@ -724,15 +758,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             }
             return x;
         };
-        // One warp's share of tile x of a piece, the CTA's gt-th: its pages 2 w and 2 w + 1.  (FP8: a page lies in the upper
-        // half of its place and is widened over it.)
-        auto widen_page = [&](uint8_t* at, const Guard* gd, int v) -> bool {
+        // (FP8) a page of V in the upper half of its place, widened over it; its first key at v
+        auto widen_page = [&](uint8_t* at, const Guard& gd, int v) -> bool {
             constexpr int N = D / 32;                     // 16-byte chunks of codes a lane
             uint4 raw[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) raw[j] = *reinterpret_cast<const uint4*>(at + K::LAND + (lane + 32 * j) * 16);
             __syncwarp();
-            bool found = false;
+            uint32_t nan = 0;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int q = lane + 32 * j, k8 = q & 7, ch = (q >> 3) % (D / 16), grp = (q >> 3) / (D / 16);
@@ -741,88 +774,148 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 widen4(raw[j].y, o[2], o[3]);
                 widen4(raw[j].z, o[4], o[5]);
                 widen4(raw[j].w, o[6], o[7]);
-                const uint32_t nan[4] = {nan_codes(raw[j].x), nan_codes(raw[j].y), nan_codes(raw[j].z), nan_codes(raw[j].w)};
-                const int key = v + grp * 8 + k8;
-                const bool partial = gd && !gd->all(key);
-                if (nan[0] | nan[1] | nan[2] | nan[3]) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (nan[e / 4] >> (8 * (e % 4) + 7) & 1) {
-                            const uint32_t mask = 0xffffu << (16 * (e & 1));
-                            o[e / 2] = (o[e / 2] & ~mask) | (partial ? 0u : 0x7fc07fc0u & mask);
-                        }
-                    found |= partial;
-                }
-                if (partial && !gd->any(key)) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = 0;
-                }
+                nan |= nan_codes(raw[j].x) | nan_codes(raw[j].y) | nan_codes(raw[j].z) | nan_codes(raw[j].w);
                 uint8_t* dst = at + grp * (K::NCH * 128) + 2 * ch * 128 + k8 * 16;
                 *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
             }
-            return found;
-        };
-        auto guard_group = [&](uint8_t* at, const Guard& gd, int v) -> bool {     // 8 keys of bf16 V
             bool found = false;
-            const int key = v + (lane & 7);
-            const bool any = gd.any(key), all = gd.all(key);
+            if (nan != 0 || !gd.any_of(v, kBlock)) {      // (a lane's own chunks again)
 #pragma unroll
-            for (int j = 0; j < K::NCH / 4; ++j) {
-                uint4* e = reinterpret_cast<uint4*>(at + (lane + 32 * j) * 16);
-                if (!any) {
-                    *e = make_uint4(0, 0, 0, 0);
-                } else if (!all) {
-                    uint32_t* y = reinterpret_cast<uint32_t*>(e);
-                    constexpr uint32_t I = 0x7f807f80u, A = 0x80008000u - I;     // an exponent of all ones carries
+                for (int j = 0; j < N; ++j) {
+                    const int q = lane + 32 * j, k8 = q & 7, ch = (q >> 3) % (D / 16), grp = (q >> 3) / (D / 16);
+                    const int key = v + grp * 8 + k8;
+                    const bool all = gd.all(key), any = gd.any(key);
+                    uint16_t* e = reinterpret_cast<uint16_t*>(at + grp * (K::NCH * 128) + 2 * ch * 128 + k8 * 16);
+                    const uint32_t words[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const uint32_t hit = ((y[z] & I) + A) & 0x80008000u;
-                        if (hit) {
-                            y[z] &= ~((hit >> 15) * 0xffffu);
-                            found = true;
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t bad = nan_codes(words[x]);
+                        if (bad == 0 && any) continue;
+#pragma unroll 1
+                        for (int y = 0; y < 4; ++y) {
+                            uint16_t* at16 = e + (x / 2) * 64 + (x & 1) * 4 + y;
+                            if (!any) {
+                                *at16 = 0;
+                            } else if (bad >> (8 * y + 7) & 1) {
+                                *at16 = all ? 0x7fc0 : 0;
+                                found |= !all;
+                            }
                         }
                     }
                 }
             }
             return found;
         };
-        auto ready = [&](const Piece& p, int n, int x, int gt, bool k_part) {
-            const int sk = gt % NSK, sv = gt % NSV, v0 = (p.t0 + x) * kKeys, pages = min(kTP, p.np - (p.t0 + x) * kTP);
-            if (k_part) {
-#pragma unroll 1
-                for (int u = 2 * w; u < min(2 * w + 2, pages); ++u)
-                    widen_page(smem + K::OFF_K + sk * K::TILE + u * K::PAGE, nullptr, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(K::KREADY + sk));
-                return;
+        auto guard_group = [&](uint8_t* at, const Guard& gd, int v) -> bool {     // 8 keys of bf16 V
+            constexpr uint32_t I = 0x7f807f80u, A = 0x80008000u - I;              // an exponent of all ones carries
+            constexpr int N = K::NCH / 4;
+            uint4* e = reinterpret_cast<uint4*>(at + lane * 16);
+            const int key = v + (lane & 7);
+            if (!gd.any(key)) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) e[32 * j] = make_uint4(0, 0, 0, 0);
+                return false;
             }
-            uint8_t* base = smem + K::OFF_V + sv * K::TILE;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint4 x = e[32 * j];
+                bad |= ((x.x & I) + A) | ((x.y & I) + A) | ((x.z & I) + A) | ((x.w & I) + A);
+            }
+            if ((bad & 0x80008000u) == 0 || gd.all(key)) return false;
+#pragma unroll 1
+            for (int j = 0; j < 4 * N; ++j) {
+                uint32_t* y = reinterpret_cast<uint32_t*>(e + 32 * (j / 4)) + j % 4;
+                const uint32_t hit = ((*y & I) + A) & 0x80008000u;
+                *y &= ~((hit >> 15) * 0xffffu);
+            }
+            return true;
+        };
+        // One warp's share of tile x of piece n, the CTA's gt-th: its units 2 w and 2 w + 1.
+        auto ready_v = [&](const Piece& p, int n, int x, int gt) {
+            const int sv = gt % NSV, v0 = (p.t0 + x) * K::KEYS, pages = min(K::TP, p.np - (p.t0 + x) * K::TP);
+            uint8_t* base = smem + K::OFF_V + sv * K::VTILE;
             const Guard gd = guard_of(p);
             bool found = false;
             if constexpr (FP8) {
 #pragma unroll 1
-                for (int u = 2 * w; u < min(2 * w + 2, pages); ++u)
-                    found |= widen_page(base + u * K::PAGE, &gd, v0 + u * kBlock);
+                for (int u = 2 * w; u < 2 * w + 2; ++u)
+                    if (u / HG < pages) found |= widen_page(base + u * K::PAGE, gd, v0 + u / HG * kBlock);
                 fence_proxy_async_smem();
             } else {
                 bool touched = false;
 #pragma unroll 1
-                for (int y = 4 * w; y < min(4 * w + 4, 2 * pages); ++y)
-                    if (!gd.all8(v0 + 8 * y)) {
-                        touched = true;
-                        found |= guard_group(base + y * (K::NCH * 128), gd, v0 + 8 * y);
-                    }
-                if (touched) fence_proxy_async_smem();
+                for (int y = 4 * w; y < 4 * w + 4; ++y) {
+                    const int pg = y / 2 / HG, v = v0 + pg * kBlock + (y & 1) * 8;
+                    if (pg >= pages || gd.all_of(v, 8)) continue;
+                    const bool f = guard_group(base + y * (K::NCH * 128), gd, v);
+                    found |= f;
+                    touched |= f || !gd.any_of(v, 8);
+                }
+                if (__any_sync(0xffffffffu, touched)) fence_proxy_async_smem();
             }
             if (__any_sync(0xffffffffu, found) && lane == 0) nonfinite[n % kFlags] = n + 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
         };
+        // (FP8) this warp's rows of Q tile qt, in place, 16 at a time, half a row a lane: groups of 8 rows are 1024 bytes of a
+        // slab; the first term's codes go where the first slab was (D = 64: to the first half of each 1024 bytes), the
+        // second's to the other.
+        auto ready_q = [&](int qt) {
+            uint8_t* tile = smem + K::OFF_Q + (qt & 1) * K::QTILE;
+            constexpr int N = D / 16;                     // 16-byte chunks of half a row
+            constexpr int LO = D == 128 ? K::SLAB : 512;
+            const int half = lane >> 4;
+#pragma unroll 1
+            for (int row = w * 32 + (lane & 15); row < w * 32 + 32; row += 16) {
+                uint32_t top = 0;
+                uint4 x[N];
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    const int ch = half * N + c;          // (dimensions 8 ch .. 8 ch + 7)
+                    x[c] = *reinterpret_cast<const uint4*>(tile + (ch / 8) * K::SLAB + row * 128 + (((ch & 7) ^ (row & 7)) * 16));
+                    const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, y[e] >> 16 & 0x7fffu));
+                }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                // 2^(134 - exponent) takes the largest element to [128, 256); kept inside fp32's normal range (a row below
+                // 2^-113 counts as smaller beside any scale); infinities and NaN make the row NaN
+                const int ex = min(max((int)(top >> 7), 14), 254);
+                const float f = __uint_as_float((uint32_t)(261 - ex) << 23);
+                const float inv = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ex - 7) << 23);
+                uint8_t* dst = tile + (row / 8) * 1024 + (row & 7) * 16 + half * (N / 2) * 128;
+#pragma unroll
+                for (int c = 0; c < N / 2; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 y = x[2 * c + e / 2];
+                        uint32_t h0, h1, l0, l1;
+                        split2(e & 1 ? y.z : y.x, f, h0, l0);
+                        split2(e & 1 ? y.w : y.y, f, h1, l1);
+                        hi[e] = h0 | h1 << 16;
+                        lo[e] = l0 | l1 << 16;
+                    }
+                    x[2 * c] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    x[2 * c + 1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < N / 2; ++c) {
+                    *reinterpret_cast<uint4*>(dst + c * 128) = x[2 * c];
+                    *reinterpret_cast<uint4*>(dst + LO + c * 128) = x[2 * c + 1];
+                }
+                if (half == 0) q_scale[qt % K::NQS * kRows + row] = inv;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(K::QREADY + (qt & 1)));
+        };
 
-        // What the guard took out of the V of partially seen keys, for columns c .. c + 15 of a row.
-        auto add_back = [&](const Piece& p, int qi, int c, float (&o)[16]) {
+        // What the guard took out of V, added to a row's results where this lane has just written them (rare).
+        auto add_back = [&](const Piece& p, int qi, uint8_t* out, float* part) {
             const Guard gd = guard_of(p);
             Sight see;
             const uint32_t* tree = nullptr;
@@ -833,19 +926,19 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 see.window(a, p, p.first + qi);
             }
             auto span = [&](int v, int z) {
-                v = max(v, p.t0 * kKeys);
-                z = min(z, min(p.t1 * kKeys, p.np * kBlock) - 1);
+                v = max(v, p.t0 * K::KEYS);
+                z = min(z, min(p.t1 * K::KEYS, p.np * kBlock) - 1);
+#pragma unroll 1
                 for (; v <= z; ++v) {
                     const bool has = see.has(v) || (tree && v >= p.L - p.Q &&
                                                     (tree_bits(tree, a.tree_words, v - (p.L - p.Q), p.Q) & 1u));
                     if (!has) continue;
                     const int id = a.tables[(int64_t)p.b * a.max_blocks + p.page(v / kBlock)];
                     if (id < 0 || id >= a.num_blocks) continue;
-                    const uint8_t* page = a.v_cache + ((int64_t)id * a.Hkv + p.g) * K::LAND;
+                    const uint8_t* page = a.v_cache + ((int64_t)id * a.Hkv + p.g + hw) * K::LAND;
                     const int off = v % kBlock;
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        const int d = c + y;
+#pragma unroll 1
+                    for (int d = 0; d < D; ++d) {
                         float f;
                         if constexpr (FP8) {
                             const uint8_t code = page[((off / 8) * (D / 16) + d / 16) * 128 + (off % 8) * 16 + d % 16];
@@ -854,23 +947,21 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                             f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
                                 page + ((off / 8) * (D / 8) + d / 8) * 128 + (off % 8) * 16 + (d % 8) * 2));
                         }
-                        if (!(fabsf(f) < INFINITY)) o[y] += f;
+                        if (fabsf(f) < INFINITY) continue;
+                        if (part) {
+                            part[(size_t)(d / 4) * 2 * kRows * 4 + d % 4] += f;
+                        } else {
+                            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out) + d;
+                            *o = __float2bfloat16_rn(__bfloat162float(*o) + f);
+                        }
                     }
                 }
             };
-            span(gd.wl_any, gd.wl_all - 1);
-            span(gd.wh_all + 1, gd.wh_any);
-        };
-        auto put = [&](int64_t row, int h, int c, const float (&o)[16]) {
-            uint8_t* dst = a.out.row(row, h) + c * 2;
-            uint32_t v[8];
-#pragma unroll
-            for (int y = 0; y < 16; y += 2) v[y >> 1] = pack_bf16(o[y], o[y + 1]);
-            if (a.wide) {
-                store32(dst, v);
+            if (HG > 1) {
+                span(0, p.np * kBlock);
             } else {
-                *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<uint4*>(dst + 16) = make_uint4(v[4], v[5], v[6], v[7]);
+                span(gd.wl_any, gd.wl_all - 1);
+                span(gd.wh_all + 1, gd.wh_any);
             }
         };
         // the weight of a part with reference m and sum l beside the largest reference `top` of the parts.  (A part
@@ -881,20 +972,23 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         auto finish_lse = [](float m, float l) {
             return m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
         };
-        uint32_t phase = 0;                               // of either chain's pieces, as bits
-        auto epilogue = [&](const Piece& p, int n) {
-            const bool whole = p.parts == 1, fix = nonfinite[n % kFlags] == n + 1;
+        // The epilogue of piece ep, 32 columns at a time (the jobs above come between them).  True: done.
+        int ep = 0, ei = 0, ec = 0;                       // the piece, its row tile and column
+        float fa = 1.f, fb = 0.f, inv = 0.f;              // factors of the chains' O, and of the sum
+        auto epilogue = [&]() -> bool {
+            const Piece& p = ring[ep % kPieces];
+            const bool whole = p.parts == 1, both = !p.two && p.count(1) > 0;          // both: the chains share a row
+            const int qi = ei * a.pb + pos;
+            const bool row_ok = pos < a.pb && qi < p.nq;
+            const int64_t row = p.row + p.q0 + qi;
+            const int h = (p.g + hw) * G + hl;
             float* slot = part_slot<D>(a, blockIdx.x, p.t0 == 0);
-            const int tiles_r = p.two ? 2 : 1;
-#pragma unroll 1
-            for (int i = 0; i < tiles_r; ++i) {
-                const int qi = i * a.pb + pos;
-                const bool row_ok = pos < a.pb && qi < p.nq;
-                const bool both = !p.two && p.count(1) > 0;            // this row tile's keys are shared by the chains
-                const uint32_t oa = tmem + lbase + K::COL_O + (p.two ? i * D : 0), ob = tmem + lbase + K::COL_O + D;
-                const float* mla = ml + (p.two ? 2 * i : 0) * kRows;
-                tc_fence_after();
-                float m = mla[r], l = mla[kRows + r], fa = 1.f, fb = 0.f;
+            const bool live = __any_sync(0xffffffffu, row_ok);
+            if (ec == 0 && live) {
+                const float* mla = ml + (p.two ? 2 * ei : 0) * kRows;
+                float m = mla[r], l = mla[kRows + r];
+                fa = 1.f;
+                fb = 0.f;
                 if (both) {
                     const float m1 = ml[2 * kRows + r], l1 = ml[3 * kRows + r], top = fmaxf(m, m1);
                     fa = weight(m, l, top);
@@ -904,70 +998,88 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     if (m1 == -INFINITY) fb = 1.f;
                     m = top;
                 }
-                const bool none = m == -INFINITY && l == 0.f;
-                const float inv = none ? 0.f : 1.f / l;
-                const int64_t row = p.row + p.q0 + qi;
-                const int h = p.g * G + hl;
+                inv = m == -INFINITY && l == 0.f ? -1.f : 1.f / l;         // (-1: a row that saw nothing)
                 if (row_ok) {
                     if (!whole) {
-                        slot[(size_t)2 * kRows * D + i * kRows + r] = m;
-                        slot[(size_t)2 * kRows * (D + 1) + i * kRows + r] = l;
+                        slot[(size_t)2 * kRows * D + ei * kRows + r] = m;
+                        slot[(size_t)2 * kRows * (D + 1) + ei * kRows + r] = l;
                     } else if (a.lse) {
                         a.lse[row * a.Hq + h] = finish_lse(m, l);
                     }
                 }
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float o[16];
-                    tmem_ld16(oa + c, o);
-                    if (both) {
-                        float o1[16];
-                        tmem_ld16(ob + c, o1);
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) o[y] = o[y] * fa + o1[y] * fb;
-                    }
-                    if (c + 16 == D) {                    // O read: the next piece's first PV may overwrite it
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(bar(K::OFREE + (p.two ? i : 0)));
-                            if (both) mbar_arrive(bar(K::OFREE + 1));
-                        }
-                    }
-                    if (row_ok && fix) add_back(p, qi, c, o);
-                    if (row_ok && whole) {
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) o[y] = none ? 0.f : o[y] * inv;
-                        put(row, h, c, o);
-                    } else if (row_ok) {
-#pragma unroll
-                        for (int y = 0; y < 16; y += 4)
-                            __stcg(reinterpret_cast<float4*>(slot + (size_t)((c + y) / 4) * 2 * kRows * 4 + (i * kRows + r) * 4),
-                                   make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]));
-                    }
-                    __syncwarp();
-                }
             }
-            if (whole) return;
+            if (live) {
+                tc_fence_after();
+                const uint32_t oa = tmem + lbase + K::COL_O + (p.two ? ei * D : 0) + ec, ob = tmem + lbase + K::COL_O + D + ec;
+                uint32_t x[32], y[32];
+                tmem_ld32_async(oa, x);
+                if (both) tmem_ld32_async(ob, y);
+                tmem_wait_ld_into(x);
+                if (both) {
+                    tmem_wait_ld_into(y);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        x[e] = __float_as_uint(__uint_as_float(x[e]) * fa + __uint_as_float(y[e]) * fb);
+                }
+                if (row_ok) {
+                    uint8_t* dst = a.out.row(row, h);
+                    float* part = slot + (ei * kRows + r) * 4;
+                    if (whole) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            v[e] = inv == -1.f ? 0u : pack_bf16(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+                        if (a.wide) {
+                            store32(dst + ec * 2, v);
+                            store32(dst + ec * 2 + 32, v + 8);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<uint4*>(dst + ec * 2 + e * 4) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(part + (size_t)((ec + e) / 4) * 2 * kRows * 4) =
+                                make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    }
+                    if (ec + 32 == D && nonfinite[ep % kFlags] == ep + 1) add_back(p, qi, dst, whole ? nullptr : part);
+                }
+                __syncwarp();
+            }
+            ec += 32;
+            if (live && ec < D) return false;
+            // O read: the next piece's first PV may overwrite it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(K::OFREE + (p.two ? ei : 0)));
+                if (both) mbar_arrive(bar(K::OFREE + 1));
+            }
+            ec = 0;
+            if (++ei < (p.two ? 2 : 1)) return false;
+            ei = 0;
+            if (whole) return true;
             // The part is in memory: the last of the item's CTAs to get here (for these 32 lanes' rows) joins them, in order.
             __threadfence();
             __syncwarp();
             int old = 0;
             int* ticket = a.tickets + p.c0 * 4 + w;
             if (lane == 0) old = atom_add_acq_rel_gpu(ticket, 1);
-            if (__shfl_sync(0xffffffffu, old, 0) != p.parts - 1) return;
+            if (__shfl_sync(0xffffffffu, old, 0) != p.parts - 1) return true;
             if (lane == 0) *ticket = 0;
             fence_acquire_gpu();
 #pragma unroll 1
-            for (int i = 0; i < tiles_r; ++i) {
-                const int rows_i = min(a.pb, p.nq - i * a.pb) * G, mine = min(32, rows_i - w * 32);
+            for (int i = 0; i < (p.two ? 2 : 1); ++i) {
+                const int mine = min(32, min(a.pb, p.nq - i * a.pb) * G - (w * 32) % RQ);      // valid rows among the lanes
                 if (mine <= 0) continue;
 #pragma unroll 1
                 for (int y = lane; y < mine * (D / 8); y += 32) {
                     const int R = w * 32 + y % mine, c = y / mine * 8;
-                    const int rp = R / G;
+                    const int rp = R % RQ / G;
                     auto at = [&](int x) { return part_slot<D>(a, p.c0 + x, x == 0); };
                     float top = -INFINITY;
+#pragma unroll 4
                     for (int x = 0; x < p.parts; ++x) top = fmaxf(top, __ldcg(at(x) + (size_t)2 * kRows * D + i * kRows + R));
                     float l = 0.f, o[8] = {};
 #pragma unroll 2
@@ -990,67 +1102,71 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                         o[7] = fmaf(u1.w, f, o[7]);
                     }
                     const bool none = top == -INFINITY && l == 0.f;
-                    const float inv = none ? 0.f : 1.f / l;
-                    const int64_t row = p.row + p.q0 + i * a.pb + rp;
-                    const int h = p.g * G + R - rp * G;
+                    const float il = none ? 0.f : 1.f / l;
+                    const int64_t orow = p.row + p.q0 + i * a.pb + rp;
+                    const int oh = (p.g + hw) * G + R % RQ - rp * G;
                     uint32_t v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = none ? 0u : pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-                    *reinterpret_cast<uint4*>(a.out.row(row, h) + c * 2) = make_uint4(v[0], v[1], v[2], v[3]);
-                    if (c == 0 && a.lse) a.lse[row * a.Hq + h] = finish_lse(top, l);
+                    for (int e = 0; e < 4; ++e) v[e] = none ? 0u : pack_bf16(o[2 * e] * il, o[2 * e + 1] * il);
+                    *reinterpret_cast<uint4*>(a.out.row(orow, oh) + c * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (c == 0 && a.lse) a.lse[orow * a.Hq + oh] = finish_lse(top, l);
                 }
             }
+            return true;
         };
 
-        // Either job when its input is there, none waited for while the other may run: the next piece's tiles are made
-        // ready while the last piece's results are awaited, and its products wait for that epilogue.
+        // Each job when its input is there, none waited for while another may run: the next piece's tiles are made ready
+        // while the last piece's results are awaited, and its products wait for that epilogue.
         int rp = 0, rx = 0, rg = 0;                       // the piece, its tile, and the CTA's tile to make ready
-        int ep = 0;                                       // the piece to finish
-        bool rk = FP8, last = false;                      // (FP8) K is next, else V; no more pieces
-        bool known = false;                               // piece rp is there
+        int qp = 0, qn = 0, qi = 0;                       // (FP8) the piece, the CTA's Q tile and the piece's to make ready
+        bool last = false, known = false;                 // no piece behind rp; piece rp is there
+        bool busy = false;                                // in piece ep's epilogue
+        uint32_t phase = 0;                               // of either chain's pieces, as bits
         uint64_t since = 0;
         uint32_t spins = 0;
         auto there = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bb, parity)); };
         for (;;) {
             bool moved = false;
-            if (ep < rp) {
-                const Piece& p = ring[ep % kPieces];
-                const bool c1 = p.count(1) > 0;           // (chain 0 always has tiles)
-                if (there(bar(K::ODONE), phase & 1) && there(bar(K::LREADY), phase & 1) &&
-                    (!c1 || (there(bar(K::ODONE + 1), phase >> 1 & 1) && there(bar(K::LREADY + 1), phase >> 1 & 1)))) {
-                    epilogue(p, ep);
-                    phase ^= c1 ? 3u : 1u;
-                    release(ep);
-                    ++ep;
-                    moved = true;
+            if (FP8 && qp <= rp + 1 && there(bar(K::PCFULL + qp % kPieces), (qp / kPieces) & 1) && !ring[qp % kPieces].end &&
+                there(bar(K::QFULL + (qn & 1)), (qn >> 1) & 1)) {
+                ready_q(qn++);
+                if (++qi == (ring[qp % kPieces].two ? 2 : 1)) {
+                    qi = 0;
+                    ++qp;
                 }
-            } else if (last) {
-                break;
+                moved = true;
             }
             if (!last) {
                 if (!known && there(bar(K::PCFULL + rp % kPieces), (rp / kPieces) & 1)) {
                     known = true;
                     if (ring[rp % kPieces].end) last = true;
+                }
+                if (known && !last && there(bar(K::VFULL + rg % NSV), (rg / NSV) & 1)) {
+                    const Piece& p = ring[rp % kPieces];
+                    ready_v(p, rp, rx, rg++);
+                    if (++rx == p.tiles()) {
+                        rx = 0;
+                        ++rp;
+                        known = false;
+                    }
                     moved = true;
                 }
-                if (known && !last) {
-                    const Piece& p = ring[rp % kPieces];
-                    if (there(rk ? bar(K::KFULL + rg % NSK) : bar(K::VFULL + rg % NSV), (rg / (rk ? NSK : NSV)) & 1)) {
-                        ready(p, rp, rx, rg, rk);
-                        moved = true;
-                        if (rk) {
-                            rk = false;
-                        } else {
-                            rk = FP8;
-                            ++rg;
-                            if (++rx == p.tiles()) {
-                                rx = 0;
-                                ++rp;
-                                known = false;
-                            }
-                        }
+            }
+            if (ep < rp) {
+                const bool c1 = ring[ep % kPieces].count(1) > 0;               // (chain 0 always has tiles)
+                if (!busy && there(bar(K::ODONE), phase & 1) && there(bar(K::LREADY), phase & 1) &&
+                    (!c1 || (there(bar(K::ODONE + 1), phase >> 1 & 1) && there(bar(K::LREADY + 1), phase >> 1 & 1))))
+                    busy = true;
+                if (busy) {
+                    if (epilogue()) {
+                        phase ^= c1 ? 3u : 1u;
+                        release(ep++);
+                        busy = false;
                     }
+                    moved = true;
                 }
+            } else if (last) {
+                break;
             }
             if (moved) {
                 since = 0;
@@ -1073,7 +1189,26 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         }
     } else {
         regs_dec<kRegsOther>();
-        if (warp == kProducer) {
+        if (warp == kPlan) {
+            // -------------------------------------------- the plan (begun while the others set up)
+            griddep_wait();
+            Plan<HG> plan(a, lane);
+            plan.begin();
+            Piece p = {};
+            p.end = !plan.next(p);
+            enter();
+            for (int n = 0;; ++n) {
+                if (n >= kPieces && !wait_all(bar(K::PCEMPTY + n % kPieces), ((n - kPieces) / kPieces) & 1)) break;
+                if (lane == 0) {
+                    ring[n % kPieces] = p;
+                    mbar_arrive(bar(K::PCFULL + n % kPieces));
+                }
+                __syncwarp();
+                if (p.end) break;
+                p.end = !plan.next(p);
+            }
+        } else if (warp == kProducer) {
+            enter();
             // -------------------------------------------- Q tiles, K and V pages in order
             bool ok = true;
             int nt = 0, nq = 0;                           // key tiles and Q tiles
@@ -1091,26 +1226,17 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
-            const int u8 = lane & 7;
+            // lanes 0-7 stand for a tile's units of K, 8-15 for those of V
+            const int u8 = lane & 7, upg = u8 / HG, uh = u8 % HG;
             const bool is_v = lane >= 8;
             for (int n = 0; ok; ++n) {
                 const Piece* p = piece_at(n);
                 if (!p || p->end) break;
-                for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
-                    const int slot = nq & 1;
-                    if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(K::QFULL + slot), K::SLABS * a.pb * a.group * 128);
-                        for (int s = 0; s < K::SLABS; ++s)
-                            tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + s * K::SLAB, &a.q, s * 64, p->g * a.group,
-                                       (int)(p->row + p->q0 + i * a.pb), bar(K::QFULL + slot));
-                    }
-                }
                 const int32_t* table = a.tables + (int64_t)p->b * a.max_blocks;
-                const int np = p->np, g = p->g;
-                // the block of this lane's page of tile t (a bad id is reported, and block 0 read in its place)
+                const int np = p->np, g = p->g + uh;
+                // the block of this lane's unit of tile t (a bad id is reported, and block 0 read in its place)
                 auto block = [&](int t) -> int {
-                    const int idx = t * kTP + u8;
+                    const int idx = t * K::TP + upg;
                     return lane < 16 && idx < np ? table[p->page(idx)] : 0;
                 };
                 auto checked = [&](int id) -> int {
@@ -1121,27 +1247,44 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 auto scale_of = [&](int id) -> float {
                     return FP8 && lane < 16 ? (is_v ? a.v_scales : a.k_scales)[(int64_t)id * a.Hkv + g] : 0.f;
                 };
-                int id = checked(block(p->t0));
+                int id = block(p->t0);
+                for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
+                    const int slot = nq & 1;
+                    if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(K::QFULL + slot), HG * K::SLABS * a.pb * a.group * 128);
+                        for (int x = 0; x < HG * K::SLABS; ++x)
+                            tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + (x % K::SLABS) * K::SLAB + (x / K::SLABS) * RQ * 128, &a.q,
+                                       (x % K::SLABS) * 64, (p->g + x / K::SLABS) * a.group, (int)(p->row + p->q0 + i * a.pb),
+                                       bar(K::QFULL + slot));
+                    }
+                }
+                id = checked(id);
                 float s = scale_of(id);
                 for (int t = p->t0; t < p->t1 && ok; ++t, ++nt) {
-                    const int sk = nt % NSK, sv = nt % NSV, pages = min(kTP, np - t * kTP);
-                    int after = t + 1 < p->t1 ? block(t + 1) : 0;
+                    const int sk = nt % NSK, sv = nt % NSV, pages = min(K::TP, np - t * K::TP);
+                    const int after = t + 1 < p->t1 ? block(t + 1) : 0;
                     const int64_t src = ((int64_t)id * a.Hkv + g) * K::LAND;
                     if (nt >= NSK && !(ok = wait_all(bar(K::KEMPTY + sk), ((nt - NSK) / NSK) & 1))) break;
                     if (FP8 && lane < 16) scales[(nt % K::NSC) * 16 + lane] = s;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(bar(K::KFULL + sk), pages * K::LAND);
+                    if (lane == 0) mbar_arrive_expect_tx(bar(K::KFULL + sk), pages * HG * K::LAND);
                     __syncwarp();
-                    if (lane < pages)
-                        bulk_g2s(sb + K::OFF_K + sk * K::TILE + u8 * K::PAGE + (FP8 ? K::LAND : 0), a.k_cache + src, K::LAND,
-                                 bar(K::KFULL + sk));
+                    // (a page's HG heads lie side by side)
+                    if (!is_v && uh == 0 && upg < pages)
+                        bulk_g2s(sb + K::OFF_K + sk * K::KTILE + u8 * K::LAND, a.k_cache + src, HG * K::LAND, bar(K::KFULL + sk));
                     ++nk;
                     if (nt >= NSV && !(ok = wait_all(bar(K::VEMPTY + sv), ((nt - NSV) / NSV) & 1))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(K::VFULL + sv), pages * K::LAND);
+                    if (lane == 0) mbar_arrive_expect_tx(bar(K::VFULL + sv), pages * HG * K::LAND);
                     __syncwarp();
-                    if (is_v && lane < 8 + pages)
-                        bulk_g2s(sb + K::OFF_V + sv * K::TILE + u8 * K::PAGE + (FP8 ? K::LAND : 0), a.v_cache + src, K::LAND,
-                                 bar(K::VFULL + sv));
+                    if (is_v && lane < 16 && upg < pages) {
+                        if (FP8)
+                            bulk_g2s(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE + K::LAND, a.v_cache + src, K::LAND,
+                                     bar(K::VFULL + sv));
+                        else if (uh == 0)
+                            bulk_g2s(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE, a.v_cache + src, HG * K::PAGE,
+                                     bar(K::VFULL + sv));
+                    }
                     ++nv;
                     id = checked(after);
                     s = scale_of(id);
@@ -1158,12 +1301,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             __syncwarp();
         } else if (warp == kMma || warp == kMma + 1) {
             // -------------------------------------------- MMA issuer of chain i
+            const uint32_t tmem = enter();
             const int i = warp - kMma;
             const bool lead = elect_one();
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);       // (known to be uniform)
-            const uint32_t s_i = tm + __shfl_sync(0xffffffffu, i, 0) * kKeys;
+            const uint32_t s_i = tm + __shfl_sync(0xffffffffu, i, 0) * kCols;
             const uint32_t o_i = tm + K::COL_O + __shfl_sync(0xffffffffu, i, 0) * D;
-            constexpr uint32_t idS = idesc_bf16_f32(kRows, kKeys, false, false);
+            constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(kRows, kCols) : idesc_bf16_f32(kRows, kCols, false, false);
             constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true);
             int pcnt = 0, ocnt = 0, turn = 0;             // this chain's tiles and pieces; turns
             int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
@@ -1174,7 +1318,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 int cnt, x0, step, t0, two, ends;
                 int base, q;                              // the CTA's numbers of its first tile and of the chain's Q tile
             };
-            // up to tile `upto`: what the other chain alone uses is given back as soon as it has landed
+            // up to tile `upto`: what the other chain alone uses is given back as soon as it is there
             auto skip = [&](int& at, int upto, int ring_n, int full, int empty) -> bool {
                 for (; at < upto; ++at) {
                     if (!wait_all(bar(full + at % ring_n), (at / ring_n) & 1)) return false;
@@ -1187,10 +1331,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 at = target + 1;
                 return wait_all(bar(full + target % ring_n), (target / ring_n) & 1);
             };
-            constexpr int KRDY = FP8 ? K::KREADY : K::KFULL;
-            auto see_k = [&](int t) { return see(kn, t, NSK, KRDY, K::KEMPTY); };
+            constexpr int QRDY = FP8 ? K::QREADY : K::QFULL;
+            auto see_k = [&](int t) { return see(kn, t, NSK, K::KFULL, K::KEMPTY); };
             auto see_v = [&](int t) { return see(vn, t, NSV, K::VREADY, K::VEMPTY); };
-            auto see_q = [&](int t) { return see(qn, t, 2, K::QFULL, K::QEMPTY); };
+            auto see_q = [&](int t) { return see(qn, t, 2, QRDY, K::QEMPTY); };
             int n = 0;
             // The next piece, if there is one and (or else, with `any`, the next that does) it has tiles of this chain.
             auto next = [&](Work& x, bool any) -> bool {
@@ -1210,7 +1354,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     qbase += at->two ? 2 : 1;
                     release(n);
                     if (x.cnt > 0) break;
-                    if (!skip(qn, qbase, 2, K::QFULL, K::QEMPTY) || !skip(kn, tbase, NSK, KRDY, K::KEMPTY) ||
+                    if (!skip(qn, qbase, 2, QRDY, K::QEMPTY) || !skip(kn, tbase, NSK, K::KFULL, K::KEMPTY) ||
                         !skip(vn, tbase, NSV, K::VREADY, K::VEMPTY))
                         return false;
                 }
@@ -1220,12 +1364,20 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             // S of tile j of this chain's in a piece (its K and Q seen)
             auto issue_s = [&](const Work& x, int j) {
                 const int sk = (x.base + x.x0 + j * x.step) % NSK;
-                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::TILE, 0);
+                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::KTILE, 0);
                 const uint32_t q_s = __shfl_sync(0xffffffffu, sb + K::OFF_Q + (x.q & 1) * K::QTILE, 0);
+                if constexpr (FP8) {
+                    constexpr uint32_t LO = D == 128 ? K::SLAB : 512;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ss(lead, s_i, desc_sw128(q_s + (k / 4) * K::SLAB + (k % 4) * 32, 16, 1024),
-                           smem_desc(kbase + k * 256, 128, K::NCH * 128), idS, k > 0 ? 1u : 0u);
+                    for (int k = 0; k < D / 16; ++k)      // the first term's, then the second's
+                        mma_ss_f8(lead, s_i, smem_desc(q_s + (k / (D / 32)) * LO + (k % (D / 32)) * 256, 128, 1024),
+                                  smem_desc(kbase + (k % (D / 32)) * 256, 128, D * 8), idS, k > 0 ? 1u : 0u);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(lead, s_i, desc_sw128(q_s + (k / 4) * K::SLAB + (k % 4) * 32, 16, 1024),
+                               smem_desc(kbase + k * 256, 128, K::NCH * 128), idS, k > 0 ? 1u : 0u);
+                }
                 commit(lead, bar(K::SFULL + i));
                 commit(lead, bar(K::KEMPTY + sk));
                 if (j + 1 == x.cnt) commit(lead, bar(K::QEMPTY + (x.q & 1)));
@@ -1245,17 +1397,18 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     const int x = p.x0 + j * p.step, gt = p.base + x;
                     if (end) after = next(q, false);
                     const int sv = gt % NSV;
-                    const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::TILE, 0);
-                    const int steps = min(max((p.ends - (p.t0 + x) * kKeys + kBlock - 1) / kBlock, 1), kTP);   // pages
-                    auto pv = [&](int k0) {               // 4 pages
-                        if (steps == kTP) {
+                    const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
+                    // units up to the last page that a row sees
+                    const int steps = HG * min(max((p.ends - (p.t0 + x) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
+                    auto pv = [&](int k0, int k1) {
+                        if (steps == kUnits) {
 #pragma unroll
-                            for (int k = k0; k < k0 + 4; ++k)
+                            for (int k = k0; k < k1; ++k)
                                 mma_ts(lead, o_i, s_i + k * 8, smem_desc(vbase + k * K::PAGE, K::NCH * 128, 128), idPV,
                                        j > 0 || k > 0 ? 1u : 0u);
                         } else {
 #pragma unroll 1
-                            for (int k = k0; k < min(k0 + 4, steps); ++k)
+                            for (int k = k0; k < min(k1, steps); ++k)
                                 mma_ts(lead, o_i, s_i + k * 8, smem_desc(vbase + k * K::PAGE, K::NCH * 128, 128), idPV,
                                        j > 0 || k > 0 ? 1u : 0u);
                         }
@@ -1266,22 +1419,28 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     // (what the next S needs is waited for before P, off the path from P to it)
                     if (end && after && (!(ok = see_q(q.q)) || !(ok = see_k(q.base + q.x0)))) break;
                     if (!end && !(ok = see_k(gt + p.step))) break;
-                    if (p.two) {
+                    if (HG == 1 && p.two) {
                         if ((i == 1 || turn > 0) && !(ok = wait_all(bar(K::TURN + i), (i == 1 ? turn : turn - 1) & 1))) break;
                         ++turn;
                     }
-                    if (!(ok = wait_all(bar(K::PFA + i), pcnt & 1))) break;
-                    tc_fence_after();
-                    pv(0);
-                    commit(lead, bar(K::PVA + i));
-                    if (!(ok = wait_all(bar(K::PFB + i), pcnt & 1))) break;
-                    tc_fence_after();
-                    pv(4);
+                    if constexpr (HG == 1) {
+                        if (!(ok = wait_all(bar(K::PFA + i), pcnt & 1))) break;
+                        tc_fence_after();
+                        pv(0, 4);
+                        commit(lead, bar(K::PVA + i));
+                        if (!(ok = wait_all(bar(K::PFB + i), pcnt & 1))) break;
+                        tc_fence_after();
+                        pv(4, 8);
+                    } else {
+                        if (!(ok = wait_all(bar(K::PFB + i), pcnt & 1))) break;
+                        tc_fence_after();
+                        pv(0, 8);
+                    }
                     if (end) commit(lead, bar(K::ODONE + i));
                     commit(lead, bar(K::VEMPTY + sv));
                     if (!end) issue_s(p, j + 1);
                     else if (after) issue_s(q, 0);
-                    if (p.two) {
+                    if (HG == 1 && p.two) {
                         if constexpr (D == 64) commit(lead, bar(K::TURN + 1 - i));
                         else if (lead) mbar_arrive(bar(K::TURN + 1 - i));
                     }
@@ -1297,21 +1456,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
             wait(bar(K::DRAIN), 0, drain);
             __syncwarp();
-        } else if (warp == kPlan) {
-            // -------------------------------------------- the plan
-            Plan plan(a, lane);
-            plan.begin();
-            for (int n = 0;; ++n) {
-                Piece p = {};
-                p.end = !plan.next(p);
-                if (n >= kPieces && !wait_all(bar(K::PCEMPTY + n % kPieces), ((n - kPieces) / kPieces) & 1)) break;
-                if (lane == 0) {
-                    const_cast<Piece*>(ring)[n % kPieces] = p;
-                    mbar_arrive(bar(K::PCFULL + n % kPieces));
-                }
-                __syncwarp();
-                if (p.end) break;
-            }
         }
     }
 
@@ -1319,10 +1463,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
     __syncwarp();
     tc_fence_before();
     cta_bar_sync();
-    if (warp == kPlan) {
+    if (warp == kMma) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, K::TMEM_COLS);
+        tmem_dealloc(*tmem_slot, K::TMEM_COLS);
     }
 }
 
@@ -1331,10 +1475,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
 constexpr size_t kTicketOff = 256;         // behind the error word
 constexpr size_t kPartOff = kTicketOff + (size_t)kMaxCtas * 4 * sizeof(int);
 
-template <int D, bool FP8>
+template <int D, bool FP8, int HG>
 cudaError_t launch(const Arg& a, unsigned grid, cudaStream_t st) {
     static std::atomic<uint64_t> set{0};
-    return launch_pdl_bigsmem(set, masked_kernel<D, FP8>, dim3(grid), dim3(kThreads), (size_t)Cfg<D, FP8>::SMEM, st, a);
+    return launch_pdl_bigsmem(set, masked_kernel<D, FP8, HG>, dim3(grid), dim3(kThreads), (size_t)Cfg<D, FP8, HG>::SMEM, st,
+                              a);
+}
+template <int D, bool FP8>
+cudaError_t launch_hg(const Arg& a, int hg, unsigned grid, cudaStream_t st) {
+    return hg == 4 ? launch<D, FP8, 4>(a, grid, st) : hg == 2 ? launch<D, FP8, 2>(a, grid, st) : launch<D, FP8, 1>(a, grid, st);
 }
 
 }  // namespace masked
@@ -1352,7 +1501,10 @@ cudaError_t launch_masked(const pkv_cache& c, const pkv_rows* q, const pkv_rows*
     if (sms <= 0 || !encoder()) return cudaErrorUnknown;
     const int G = q->num_heads / c.num_kv_heads;
     Arg a = {};
-    a.pb = kRows / G;
+    // as many kv-heads an item as their rows fit in a row tile
+    const int rows = std::min<int64_t>((int64_t)max_q_len * G, kRows);
+    const int hg = rows <= kRows / 4 && c.num_kv_heads % 4 == 0 ? 4 : rows <= kRows / 2 && c.num_kv_heads % 2 == 0 ? 2 : 1;
+    a.pb = kRows / hg / G;
     if (!make_map(&a.q, q, q->data, PKV_BF16, c.head_dim, num_q_rows, G, a.pb)) return cudaErrorInvalidValue;
     a.k_cache = (const uint8_t*)c.k_cache;
     a.v_cache = (const uint8_t*)c.v_cache;
@@ -1387,8 +1539,8 @@ cudaError_t launch_masked(const pkv_cache& c, const pkv_rows* q, const pkv_rows*
     a.scale_log2 = scale * kLog2e;
     const unsigned grid = (unsigned)std::min(sms, kMaxCtas);
     if (c.kv_dtype == PKV_KV_FP8_E4M3)
-        return c.head_dim == 128 ? launch<128, true>(a, grid, st) : launch<64, true>(a, grid, st);
-    return c.head_dim == 128 ? launch<128, false>(a, grid, st) : launch<64, false>(a, grid, st);
+        return c.head_dim == 128 ? launch_hg<128, true>(a, hg, grid, st) : launch_hg<64, true>(a, hg, grid, st);
+    return c.head_dim == 128 ? launch_hg<128, false>(a, hg, grid, st) : launch_hg<64, false>(a, hg, grid, st);
 }
 
 }  // namespace pkv

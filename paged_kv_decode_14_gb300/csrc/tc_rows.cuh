@@ -78,6 +78,27 @@ __device__ __forceinline__ void commit(bool lead, uint32_t bar) {
         : "memory");
 }
 
+// The same with e4m3 operands in shared memory (32 elements of K an instruction).
+__device__ __forceinline__ void mma_ss_f8(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)lead)
+        : "memory");
+}
+
+// 16 consecutive 32-bit columns of this thread's TMEM lane into r[O .. O + 15], not waited for (tmem_wait_ld_into).
+template <int O>
+__device__ __forceinline__ void tmem_ld16_at(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[O + 0]), "=r"(r[O + 1]), "=r"(r[O + 2]), "=r"(r[O + 3]), "=r"(r[O + 4]), "=r"(r[O + 5]), "=r"(r[O + 6]),
+          "=r"(r[O + 7]), "=r"(r[O + 8]), "=r"(r[O + 9]), "=r"(r[O + 10]), "=r"(r[O + 11]), "=r"(r[O + 12]),
+          "=r"(r[O + 13]), "=r"(r[O + 14]), "=r"(r[O + 15])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
