@@ -51,7 +51,6 @@ int num_sms_current();
 namespace masked {
 
 using namespace tcrow;
-using rows::store32;
 using rows::View;
 
 constexpr int kRows = 128;                 // rows of a row tile (MMA M)
@@ -86,7 +85,6 @@ struct Arg {
     int max_blocks, num_seqs, max_q_len, Hq, Hkv, group;
     int pb;                                // queries of a row tile
     int tree_words, window, sinks;
-    int wide;                              // out's rows are 32-byte aligned
     float scale_log2;
 };
 
@@ -186,26 +184,20 @@ struct Seq {
     int Q, L;               // 0 queries where the lengths are bad
 };
 
-// a / b, by 32-bit arithmetic where that is enough (the 64-bit division is a long routine)
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((uint64_t)(a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
-
 // The plan of a launch, made by one warp of every CTA alike.  An item's units are its key tiles times its row tiles
 // and kItemUnits; all items' units, in the order sequence, query block, kv-heads, are cut into equal ranges, one per
-// CTA, and a CTA has the tiles whose first unit lies in its range.
+// CTA, and a CTA has the tiles whose first unit lies in its range.  (Loops are kept rolled: this code runs once, from a
+// cold instruction cache.)
 template <int HG>
 struct Plan {
     static constexpr int TP = kUnits / HG;
     const Arg& a;
     const int lane;
-    int chunk, groups;      // sequences a lane; groups of HG kv-heads
-    int64_t total, u, u1;   // all units; the CTA's place and end
-    int64_t share;          // units of a CTA, and how many CTAs have one more
-    int ctas, longer;
+    int groups;             // of HG kv-heads
+    int total, u, u1;       // all units; the CTA's place and end
+    int share, longer;      // units of a CTA, and how many CTAs have one more
     int b, blk, g;          // the item at u, its first unit
-    int64_t start;
+    int start;
     Seq s;
     int64_t packed;         // rows before sequence b
 
@@ -220,25 +212,21 @@ struct Plan {
         }
         return x;
     }
-    __device__ __forceinline__ void span(const Seq& x, int block, int& first, int& nq, int& sp, int& np, int& jump) const {
-        const int q0 = block * per();
-        nq = min(per(), x.Q - q0);
-        first = x.L - x.Q + q0;
-        if (a.tree) {
-            sp = jump = 0;
-            np = (x.L + kBlock - 1) / kBlock;
-            return;
+    // the geometry of query block `block` of a sequence; its key tiles, and the units of one
+    __device__ __forceinline__ int span(const Seq& x, int block, Piece& p, int& tiles, int& each) const {
+        p.q0 = block * per();
+        p.nq = min(per(), x.Q - p.q0);
+        p.first = x.L - x.Q + p.q0;
+        p.sp = p.jump = 0;
+        p.np = (x.L + kBlock - 1) / kBlock;
+        if (!a.tree) {
+            const int wp = max(0, p.first - a.window + 1) / kBlock;
+            p.sp = min((min(a.sinks, x.L) + kBlock - 1) / kBlock, wp);
+            p.jump = (wp - p.sp) * kBlock;
+            p.np = (p.first + p.nq - 1) / kBlock + 1 - (wp - p.sp);
         }
-        const int wp = max(0, first - a.window + 1) / kBlock;
-        sp = min((min(a.sinks, x.L) + kBlock - 1) / kBlock, wp);
-        jump = (wp - sp) * kBlock;
-        np = (first + nq - 1) / kBlock + 1 - (wp - sp);
-    }
-    __device__ __forceinline__ int units(const Seq& x, int block, int& tiles, int& each) const {
-        int first, nq, sp, np, jump;
-        span(x, block, first, nq, sp, np, jump);
-        tiles = (np + TP - 1) / TP;
-        each = HG == 1 && nq > a.pb ? 2 : 1;
+        tiles = (p.np + TP - 1) / TP;
+        each = HG == 1 && p.nq > a.pb ? 2 : 1;
         return tiles * each + kItemUnits;
     }
     template <typename V>
@@ -251,95 +239,103 @@ struct Plan {
         }
         return y - x;
     }
-    __device__ __forceinline__ int64_t range(int c) const { return share * c + min(c, longer); }
-    __device__ __forceinline__ int cta_of(int64_t unit) const {
-        const int64_t head = (share + 1) * longer;
-        return unit < head ? (int)quotient(unit, share + 1) : longer + (int)quotient(unit - head, share);
+    __device__ __forceinline__ int range(int c) const { return share * c + min(c, longer); }
+    __device__ __forceinline__ int cta_of(int unit) const {
+        const int head = (share + 1) * longer;
+        const bool in = unit < head;
+        return (in ? 0 : longer) + (int)((uint32_t)(in ? unit : unit - head) / (uint32_t)(in ? share + 1 : share));
     }
     __device__ __forceinline__ void begin() {
-        chunk = (a.num_seqs + 31) / 32;
-        const int b0 = min(lane * chunk, a.num_seqs), b1 = min(b0 + chunk, a.num_seqs);
+        const int chunk = (a.num_seqs + 31) / 32, b0 = min(lane * chunk, a.num_seqs), b1 = min(b0 + chunk, a.num_seqs);
         int64_t rows = 0;
         if (!a.q_starts) {
+#pragma unroll 1
             for (int i = b0; i < b1; ++i) rows += max(a.q_lens[i], 0);
             rows = scan(rows);
         }
-        int64_t mine = 0, at = rows;
-        int tiles, each;
-        for (int i = b0; i < b1; ++i) {
-            const Seq x = load(i, at, true);
-            at += max(a.q_lens[i], 0);
-            for (int k = 0; k * per() < x.Q; ++k) mine += (int64_t)units(x, k, tiles, each) * groups;
-        }
-        const int64_t before = scan(mine);
-        total = __shfl_sync(0xffffffffu, before + mine, 31);
-        ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
-        share = quotient(total, ctas);
-        longer = (int)(total - share * ctas);
-        u = u1 = 0;
-        if ((int)blockIdx.x >= ctas || total == 0) return;
-        u = range(blockIdx.x);
-        u1 = range(blockIdx.x + 1);
-        // the lane that has the item at u, and where it lies
-        const bool here = u >= before && u < before + mine;
-        int fb = 0, fblk = 0, fg = 0;
-        int64_t fs = 0, fp = 0;
-        if (here) {
-            int64_t r = before;
-            at = rows;
-            bool found = false;
-            for (int i = b0; i < b1 && !found; ++i) {
-                const Seq x = load(i, at, false);
-                for (int k = 0; k * per() < x.Q; ++k) {
-                    const int w = units(x, k, tiles, each);
-                    if (u < r + (int64_t)w * groups) {
-                        fb = i;
-                        fblk = k;
-                        fg = (int)quotient(u - r, w);
-                        fs = r + (int64_t)fg * w;
-                        fp = at;
-                        found = true;
-                        break;
+        // units of this lane's sequences; the second time, the item of them that holds unit `u`
+        int64_t mine = 0, before = 0;
+        int fb = 0, fblk = 0, fg = 0, fs = 0;
+        int64_t fp = 0;
+        total = u = u1 = 0;
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+            const bool here = turn == 1 && u >= before && u < before + mine;
+            if (turn == 0 || here) {
+                int64_t at = rows, r = before;
+                bool found = false;
+#pragma unroll 1
+                for (int i = b0; i < b1 && !found; ++i) {
+                    const Seq x = load(i, at, turn == 0);
+#pragma unroll 1
+                    for (int k = 0; k * per() < x.Q && !found; ++k) {
+                        Piece p;
+                        int tiles, each;
+                        const int w = span(x, k, p, tiles, each);
+                        const int64_t all = (int64_t)w * groups;
+                        if (turn == 1 && u < r + all) {
+                            fb = i;
+                            fblk = k;
+                            fg = (int)((uint32_t)(u - (int)r) / (uint32_t)w);
+                            fs = (int)r + fg * w;
+                            fp = at;
+                            found = true;
+                        }
+                        r += all;
                     }
-                    r += (int64_t)w * groups;
+                    at += max(a.q_lens[i], 0);
                 }
-                at += max(a.q_lens[i], 0);
+                if (turn == 0) mine = r;
+            }
+            if (turn == 0) {
+                before = scan(mine);
+                const int64_t sum = __shfl_sync(0xffffffffu, before + mine, 31);
+                if (sum > 0x7ffffff0) {                   // (more than a month's work)
+                    raise_error(a.err, PKV_DEVERR_LENGTH);
+                    return;
+                }
+                total = (int)sum;
+                const int ctas = max(1, min((int)gridDim.x, total / kMinUnits));
+                if ((int)blockIdx.x >= ctas || total == 0) return;
+                share = (int)((uint32_t)total / (uint32_t)ctas);
+                longer = total - share * ctas;
+                u = range(blockIdx.x);
+                u1 = range(blockIdx.x + 1);
+            } else {
+                const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+                b = __shfl_sync(0xffffffffu, fb, from);
+                blk = __shfl_sync(0xffffffffu, fblk, from);
+                g = __shfl_sync(0xffffffffu, fg, from);
+                start = __shfl_sync(0xffffffffu, fs, from);
+                packed = __shfl_sync(0xffffffffu, fp, from);
             }
         }
-        const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-        b = __shfl_sync(0xffffffffu, fb, from);
-        blk = __shfl_sync(0xffffffffu, fblk, from);
-        g = __shfl_sync(0xffffffffu, fg, from);
-        start = __shfl_sync(0xffffffffu, fs, from);
-        packed = __shfl_sync(0xffffffffu, fp, from);
         s = load(b, packed, false);
     }
     // The next piece with tiles; the same in every lane.
     __device__ __forceinline__ bool next(Piece& p) {
-        while (u < u1) {
+        bool some = false;
+#pragma unroll 1
+        while (u < u1 && !some) {
             int tiles, each;
-            const int w = units(s, blk, tiles, each);
-            const int64_t keys = start + kItemUnits;      // the first tile's first unit
-            auto tile_at = [&](int64_t x) { return x <= keys ? 0 : (int)min((int64_t)tiles, (x - keys + each - 1) >> (each - 1)); };
+            const int w = span(s, blk, p, tiles, each);
+            const int keys = start + kItemUnits;          // the first tile's first unit
+            auto tile_at = [&](int x) { return x <= keys ? 0 : min(tiles, (x - keys + each - 1) >> (each - 1)); };
             p.t0 = tile_at(u);
             p.t1 = tile_at(u1);
-            const bool some = p.t1 > p.t0;
-            if (some) {
-                p.row = s.row;
-                p.b = b;
-                p.g = g * HG;
-                p.q0 = blk * per();
-                span(s, blk, p.first, p.nq, p.sp, p.np, p.jump);
-                p.L = s.L;
-                p.Q = s.Q;
-                p.two = each == 2;
-                p.end = 0;
-                p.c0 = blockIdx.x;
-                p.parts = 1;
-                if (p.t0 > 0 || p.t1 < tiles) {
-                    p.c0 = cta_of(keys);
-                    p.parts = cta_of(keys + (int64_t)(tiles - 1) * each) - p.c0 + 1;
-                }
+            some = p.t1 > p.t0;
+            p.row = s.row;
+            p.b = b;
+            p.g = g * HG;
+            p.L = s.L;
+            p.Q = s.Q;
+            p.two = each == 2;
+            p.end = 0;
+            p.c0 = blockIdx.x;
+            p.parts = 1;
+            if (some && (p.t0 > 0 || p.t1 < tiles)) {
+                if (p.t0 > 0) p.c0 = cta_of(keys);
+                p.parts = (p.t1 < tiles ? cta_of(keys + (tiles - 1) * each) : (int)blockIdx.x) - p.c0 + 1;
             }
             // on to the next item
             start += w;
@@ -348,6 +344,7 @@ struct Plan {
                 g = 0;
                 if (++blk * per() >= s.Q) {
                     blk = 0;
+#pragma unroll 1
                     do {
                         packed += max(a.q_lens[b], 0);
                         if (++b >= a.num_seqs) {
@@ -358,9 +355,8 @@ struct Plan {
                     } while (s.Q == 0);
                 }
             }
-            if (some) return true;
         }
-        return false;
+        return some;
     }
 };
 
@@ -418,9 +414,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
     float* scales = reinterpret_cast<float*>(smem + K::OFF_SC);
     float* q_scale = reinterpret_cast<float*>(smem + K::OFF_QS);
     Piece* ring = reinterpret_cast<Piece*>(smem + K::OFF_PIECE);
-    const Ctl ctl{abort_flag, a.err, a.wait_limit_ns};
     // every wait and every TMEM access is warp-uniform (tcgen05.ld / st are .aligned)
-    auto wait_all = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, wait(bb, parity, ctl)); };
+    // (Their limit is kept by warps 8-11, which see every tile: where none of their jobs moves on for so long, they set
+    // the abort flag.  A clock in each of the sixty waits made the code a fifth longer, and it hardly fits the
+    // instruction cache.)
+    auto wait_all = [&](uint32_t bb, uint32_t parity) {
+        bool there = mbar_try_wait(bb, parity);
+        while (!there && !*abort_flag) there = mbar_try_wait(bb, parity);
+        return (bool)__all_sync(0xffffffffu, there);
+    };
 
     if (tid == 0) {
         for (int i = 0; i < NSK; ++i) {
@@ -467,6 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
     // every role goes through here, from its own code path (non-.aligned barrier); the tensor memory's address
     auto enter = [&]() -> uint32_t {
         griddep_wait();
+        griddep_launch();
         tc_fence_before();
         cta_bar_sync();
         tc_fence_after();
@@ -505,8 +508,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 tmem_ld16_at<16>(scol + ((k + kBlock) * HG + hw * kBlock), s);
             }
         };
-        constexpr int STEP = K::KEYS < 64 ? K::KEYS : 64; // keys whose P is written at once
-        constexpr bool PAIR = STEP == 64;
         bool ok = true;
         int scnt = 0, ocnt = 0, tbase = 0, qbase = 0;     // this chain's tiles and pieces; the CTA's tiles and Q tiles
         for (int n = 0; ok; ++n) {
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     continue;
                 }
                 tc_fence_after();
-                uint32_t sa[32], sb_[32];
+                uint32_t sa[32];
                 load_s(0, sa);
                 if (FP8 && j == 0) sc = a.scale_log2 * q_scale[qt % K::NQS * kRows + r];
                 const float* ks = scales + ((base + x) % K::NSC) * 16 + hw;     // (of unit u: ks[u * HG])
@@ -572,17 +573,20 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     }
                     return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 };
+                // columns of this row's P of page pg of the tile (8: two P a column)
+                auto p_col = [&](int pg) { return scol + (pg * HG + hw) * 8; };
                 // (rare) a P of the keys from k on reaches 2: m rises by a whole number of octaves, and the P written in
-                // this tile, O and l are scaled down by as many (exact but for what falls below fp32's range)
+                // this tile, O and l are scaled down by as many (exact but for what falls below the types' range)
                 auto raise_ref = [&](float target, int k) {
                     const float inc = target + kHeadroom > m ? ceilf(target + kHeadroom - m) : 0.f;
                     const int e = (int)fminf(inc, 127.f);
                     const float alpha = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
-                    if (k > 0) {                          // the first half's P is being used: it ends in O
+                    const bool half = HG == 1 && k >= 64; // the first half's P is being used: it ends in O
+                    if (half) {
                         wait_all(bar(K::PVA + i), scnt & 1);
                         tc_fence_after();
                     }
-                    if (j > 0 || k > 0) {
+                    if (j > 0 || half) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float o[16];
@@ -592,8 +596,17 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                             for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(o[y] * alpha);
                             tmem_st16u(ocol + c, v);
                         }
-                        tmem_wait_st();
                     }
+                    // (P that are written and not used yet)
+#pragma unroll 1
+                    for (int pg = (half ? 64 : 0) / kBlock; pg < k / kBlock; ++pg) {
+                        uint32_t v[8];
+                        tmem_ld8(p_col(pg), v);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) v[y] = pack_bf16(bf16_lo(v[y]) * alpha, bf16_hi(v[y]) * alpha);
+                        tmem_st8(p_col(pg), v);
+                    }
+                    tmem_wait_st();
                     l *= alpha;
                     m += inc;
                 };
@@ -636,66 +649,55 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     acc = f2add(acc, f2add(ca, cb));
                 };
                 tmem_wait_ld_into(sa);
-                // (one copy of either path: the instruction cache holds little more than a tile's code)
+                // (rolled, one copy of either path: the instruction cache holds little more than the roles' inner loops)
 #pragma unroll 1
-                for (int k = 0; k < K::KEYS; k += STEP) {
-                    uint32_t v[STEP / 2];
-                    // a second half that no row sees is not read by the PV
-                    const bool none = k > 0 && k >= ends - v0;
-                    for (bool again = false; !none; again = true) {
-                        uint64_t acc = 0;
-                        over = 0;
-                        if (PAIR) load_s(k + 32, sb_);
-                        if (!__all_sync(0xffffffffu, m > -INFINITY)) {
-                            // no reference yet (a piece's first tile): the largest that is visible.  (O and l are 0 so far)
-                            if (PAIR) tmem_wait_ld_into(sb_);
-                            float top = largest(sa, k, masked ? bits(k) : ~0u);
-                            if (PAIR) top = fmaxf(top, largest(sb_, k + 32, masked ? bits(k + 32) : ~0u));
-                            if (m == -INFINITY) m = top * sc + kHeadroom;
+                for (int k = 0; k < K::KEYS; k += 32) {
+                    uint32_t next_s[32];
+                    if (K::KEYS > 32) load_s(min(k + 32, K::KEYS - 32), next_s);
+                    // what no row sees behind the first half is not read by the PV
+                    const bool none = HG == 1 && k >= 64 && v0 + 64 >= ends;
+                    bool again = false;
+#pragma unroll 1
+                    while (!none) {
+                        const uint32_t w = masked ? bits(k) : ~0u;
+                        if (again || !__all_sync(0xffffffffu, m > -INFINITY)) {
+                            // no reference yet (a piece's first tile): the largest that is visible (O and l are 0 so far); or
+                            // one that is too small
+                            const float top = largest(sa, k, w);
+                            if (again) raise_ref(row_ok ? top * sc : -INFINITY, k);
+                            else if (m == -INFINITY) m = top * sc + kHeadroom;
                             // (too far below 0 is only seen here: m rises)
                             if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
                         }
-                        if (!masked) emit(sa, k, v, acc, std::false_type{}, 0u);
-                        else emit(sa, k, v, acc, std::true_type{}, bits(k));
-                        if constexpr (PAIR) {
-                            tmem_wait_ld_into(sb_);
-                            if (HG == 1) load_s(64, sa);  // (for the second half; after it, for nothing)
-                            if (!masked) emit(sb_, k + 32, v + 16, acc, std::false_type{}, 0u);
-                            else emit(sb_, k + 32, v + 16, acc, std::true_type{}, bits(k + 32));
-                            if (HG == 1) tmem_wait_ld_into(sa);
-                        }
+                        uint64_t acc = 0;
+                        uint32_t v[16];
+                        over = 0;
+                        if (!masked) emit(sa, k, v, acc, std::false_type{}, w);
+                        else emit(sa, k, v, acc, std::true_type{}, w);
                         // P is written once none is known to reach 2 (the top exponent bit is clear below)
                         bool high;
                         if constexpr (FP8) {
                             high = (over & 0x40000000u) != 0;
                         } else {
-                            uint32_t any[4] = {v[0], v[1], v[2], v[3]};
+                            uint32_t any[2] = {v[0], v[1]};
 #pragma unroll
-                            for (int y = 4; y < STEP / 2; ++y) any[y & 3] |= v[y];
-                            high = ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
+                            for (int y = 2; y < 16; ++y) any[y & 1] |= v[y];
+                            high = ((any[0] | any[1]) & 0x40004000u) != 0;
                         }
                         if (__any_sync(0xffffffffu, row_ok && high) && !again) {
-                            // once more with m raised (NaN logits pass then)
-                            load_s(k, sa);
-                            tmem_wait_ld_into(sa);
-                            float top = largest(sa, k, masked ? bits(k) : ~0u);
-                            if (PAIR) {
-                                load_s(k + 32, sb_);
-                                tmem_wait_ld_into(sb_);
-                                top = fmaxf(top, largest(sb_, k + 32, masked ? bits(k + 32) : ~0u));
-                            }
-                            raise_ref(row_ok ? top * sc : -INFINITY, k);
+                            again = true;                 // once more with m raised (NaN logits pass then)
                             continue;
                         }
                         if constexpr (HG == 1) {
-                            tmem_st32u(scol + (k >> 1), v);
+                            tmem_st16u(scol + (k >> 1), v);
                         } else {
 #pragma unroll
-                            for (int pg = 0; pg < K::TP; ++pg) {
-                                uint32_t w[8], z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                            for (int x2 = 0; x2 < 2; ++x2) {
+                                uint32_t d8[8], z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                                for (int y = 0; y < 8; ++y) w[y] = v[pg * 8 + y];
-                                tmem_st8(scol + (pg * HG + hw) * 8, w);
+                                for (int y = 0; y < 8; ++y) d8[y] = v[x2 * 8 + y];
+                                const int pg = k / kBlock + x2;
+                                tmem_st8(p_col(pg), d8);
 #pragma unroll
                                 for (int y = 1; y < HG; ++y) tmem_st8(scol + (pg * HG + (hw + y) % HG) * 8, z);
                             }
@@ -706,9 +708,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                         tmem_wait_st();
                         break;
                     }
+                    if (K::KEYS > 32) {
+                        tmem_wait_ld_into(next_s);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) sa[y] = next_s[y];
+                    }
                     // P of the first 64 keys: their PV may run while the rest is computed
-                    signal(bar(HG == 1 && k == 0 ? K::PFA + i : K::PFB + i));
+                    if (HG == 1 && k == 32) signal(bar(K::PFA + i));
                 }
+                signal(bar(K::PFB + i));
             }
             if (!ok) break;
             // (a reference so large that fp32 cannot place the weights beside it is reported)
@@ -758,50 +766,49 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             }
             return x;
         };
-        // (FP8) a page of V in the upper half of its place, widened over it; its first key at v
-        auto widen_page = [&](uint8_t* at, const Guard& gd, int v) -> bool {
-            constexpr int N = D / 32;                     // 16-byte chunks of codes a lane
-            uint4 raw[N];
+        // (FP8) `pages` of the two pages of V from `at` on, each in the upper half of its place and widened over it; their
+        // first keys at v and v1
+        auto widen_pages = [&](uint8_t* at, const Guard& gd, int v, int v1, int pages) -> bool {
+            constexpr int N = D / 32;                     // 16-byte chunks of codes a lane and page
+            uint4 raw[2 * N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) raw[j] = *reinterpret_cast<const uint4*>(at + K::LAND + (lane + 32 * j) * 16);
+            for (int j = 0; j < 2 * N; ++j)
+                raw[j] = *reinterpret_cast<const uint4*>(at + j / N * K::PAGE + K::LAND + (lane + 32 * (j % N)) * 16);
             __syncwarp();
+            // (a lane's chunk j % N of page j / N: its key of the page, and where it goes)
+            auto key_of = [&](int j) { return (lane & 7) + ((lane + 32 * (j % N)) >> 3) / (D / 16) * 8; };
+            auto place = [&](int j) {
+                const int q = (lane + 32 * (j % N)) >> 3;
+                return at + j / N * K::PAGE + q / (D / 16) * (K::NCH * 128) + 2 * (q % (D / 16)) * 128 + (lane & 7) * 16;
+            };
             uint32_t nan = 0;
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int q = lane + 32 * j, k8 = q & 7, ch = (q >> 3) % (D / 16), grp = (q >> 3) / (D / 16);
+            for (int j = 0; j < 2 * N; ++j) {
+                if (j >= N && pages < 2) break;
                 uint32_t o[8];
                 widen4(raw[j].x, o[0], o[1]);
                 widen4(raw[j].y, o[2], o[3]);
                 widen4(raw[j].z, o[4], o[5]);
                 widen4(raw[j].w, o[6], o[7]);
                 nan |= nan_codes(raw[j].x) | nan_codes(raw[j].y) | nan_codes(raw[j].z) | nan_codes(raw[j].w);
-                uint8_t* dst = at + grp * (K::NCH * 128) + 2 * ch * 128 + k8 * 16;
-                *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                *reinterpret_cast<uint4*>(place(j)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(place(j) + 128) = make_uint4(o[4], o[5], o[6], o[7]);
             }
             bool found = false;
-            if (nan != 0 || !gd.any_of(v, kBlock)) {      // (a lane's own chunks again)
+            if (nan != 0 || !gd.any_of(v, kBlock) || (pages > 1 && !gd.any_of(v1, kBlock))) {      // (a lane's own chunks again)
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int q = lane + 32 * j, k8 = q & 7, ch = (q >> 3) % (D / 16), grp = (q >> 3) / (D / 16);
-                    const int key = v + grp * 8 + k8;
+                for (int j = 0; j < 2 * N; ++j) {
+                    if (j >= N && pages < 2) break;
+                    const int key = (j < N ? v : v1) + key_of(j);
                     const bool all = gd.all(key), any = gd.any(key);
-                    uint16_t* e = reinterpret_cast<uint16_t*>(at + grp * (K::NCH * 128) + 2 * ch * 128 + k8 * 16);
-                    const uint32_t words[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+                    uint16_t* e = reinterpret_cast<uint16_t*>(place(j));
+                    const uint32_t bad[4] = {nan_codes(raw[j].x), nan_codes(raw[j].y), nan_codes(raw[j].z), nan_codes(raw[j].w)};
+                    if (any && (bad[0] | bad[1] | bad[2] | bad[3]) == 0) continue;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t bad = nan_codes(words[x]);
-                        if (bad == 0 && any) continue;
-#pragma unroll 1
-                        for (int y = 0; y < 4; ++y) {
-                            uint16_t* at16 = e + (x / 2) * 64 + (x & 1) * 4 + y;
-                            if (!any) {
-                                *at16 = 0;
-                            } else if (bad >> (8 * y + 7) & 1) {
-                                *at16 = all ? 0x7fc0 : 0;
-                                found |= !all;
-                            }
-                        }
+                    for (int y = 0; y < 16; ++y) {        // code y
+                        const bool is_nan = bad[y / 4] >> (8 * (y % 4) + 7) & 1;
+                        if (!any || is_nan) e[y / 8 * 64 + y % 8] = any && all ? 0x7fc0 : 0;
+                        found |= any && is_nan && !all;
                     }
                 }
             }
@@ -839,9 +846,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             const Guard gd = guard_of(p);
             bool found = false;
             if constexpr (FP8) {
-#pragma unroll 1
-                for (int u = 2 * w; u < 2 * w + 2; ++u)
-                    if (u / HG < pages) found |= widen_page(base + u * K::PAGE, gd, v0 + u / HG * kBlock);
+                const int pg = 2 * w / HG, pg1 = (2 * w + 1) / HG;
+                if (pg < pages)
+                    found = widen_pages(base + 2 * w * K::PAGE, gd, v0 + pg * kBlock, v0 + pg1 * kBlock, pg1 < pages ? 2 : 1);
                 fence_proxy_async_smem();
             } else {
                 bool touched = false;
@@ -1029,14 +1036,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             v[e] = inv == -1.f ? 0u : pack_bf16(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
-                        if (a.wide) {
-                            store32(dst + ec * 2, v);
-                            store32(dst + ec * 2 + 32, v + 8);
-                        } else {
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4)
-                                *reinterpret_cast<uint4*>(dst + ec * 2 + e * 4) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                        }
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<uint4*>(dst + ec * 2 + e * 4) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
@@ -1247,12 +1249,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 auto scale_of = [&](int id) -> float {
                     return FP8 && lane < 16 ? (is_v ? a.v_scales : a.k_scales)[(int64_t)id * a.Hkv + g] : 0.f;
                 };
-                int id = block(p->t0);
+                // (a tile's block is read two tiles ahead and its scale one, so that neither is waited for)
+                int id = block(p->t0), id1 = p->t0 + 1 < p->t1 ? block(p->t0 + 1) : 0;
                 for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
                     const int slot = nq & 1;
                     if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar(K::QFULL + slot), HG * K::SLABS * a.pb * a.group * 128);
+#pragma unroll 1
                         for (int x = 0; x < HG * K::SLABS; ++x)
                             tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + (x % K::SLABS) * K::SLAB + (x / K::SLABS) * RQ * 128, &a.q,
                                        (x % K::SLABS) * 64, (p->g + x / K::SLABS) * a.group, (int)(p->row + p->q0 + i * a.pb),
@@ -1261,9 +1265,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 }
                 id = checked(id);
                 float s = scale_of(id);
+#pragma unroll 1
                 for (int t = p->t0; t < p->t1 && ok; ++t, ++nt) {
                     const int sk = nt % NSK, sv = nt % NSV, pages = min(K::TP, np - t * K::TP);
-                    const int after = t + 1 < p->t1 ? block(t + 1) : 0;
+                    const int id2 = t + 2 < p->t1 ? block(t + 2) : 0;
+                    id1 = checked(id1);
+                    const float s1 = scale_of(id1);
                     const int64_t src = ((int64_t)id * a.Hkv + g) * K::LAND;
                     if (nt >= NSK && !(ok = wait_all(bar(K::KEMPTY + sk), ((nt - NSK) / NSK) & 1))) break;
                     if (FP8 && lane < 16) scales[(nt % K::NSC) * 16 + lane] = s;
@@ -1286,8 +1293,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                                      bar(K::VFULL + sv));
                     }
                     ++nv;
-                    id = checked(after);
-                    s = scale_of(id);
+                    id = id1;
+                    id1 = id2;
+                    s = s1;
                 }
                 release(n);
             }
@@ -1313,7 +1321,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
             int kn = 0, vn = 0, qn = 0;                   // K, V and Q tiles seen: every one, in order, by both chains (a
                                                           // barrier's parity tells neighbouring phases apart, no more)
-            bool ok = true;
             struct Work {
                 int cnt, x0, step, t0, two, ends;
                 int base, q;                              // the CTA's numbers of its first tile and of the chain's Q tile
@@ -1382,74 +1389,69 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 commit(lead, bar(K::KEMPTY + sk));
                 if (j + 1 == x.cnt) commit(lead, bar(K::QEMPTY + (x.q & 1)));
             };
-            Work p;
-            bool more = next(p, true), begun = false;     // begun: this piece's first S is issued
-            while (more && ok) {
-                if (!begun) {
-                    if (!(ok = see_q(p.q)) || !(ok = see_k(p.base + p.x0))) break;
-                    tc_fence_after();
-                    issue_s(p, 0);
-                }
-                Work q;
-                bool after = false;                       // the piece behind this has tiles of this chain
-                for (int j = 0; j < p.cnt; ++j, ++pcnt) {
-                    const bool end = j + 1 == p.cnt;
-                    const int x = p.x0 + j * p.step, gt = p.base + x;
-                    if (end) after = next(q, false);
-                    const int sv = gt % NSV;
-                    const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
-                    // units up to the last page that a row sees
-                    const int steps = HG * min(max((p.ends - (p.t0 + x) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
-                    auto pv = [&](int k0, int k1) {
-                        if (steps == kUnits) {
-#pragma unroll
-                            for (int k = k0; k < k1; ++k)
-                                mma_ts(lead, o_i, s_i + k * 8, smem_desc(vbase + k * K::PAGE, K::NCH * 128, 128), idPV,
-                                       j > 0 || k > 0 ? 1u : 0u);
-                        } else {
+            // One loop: P . V of the chain's present tile, if there is one, then S of the next, if there is one.
+            Work p, q;
+            int j = 0, jq = 0;
+            bool now = false;                             // S of tile j of piece p has been issued
 #pragma unroll 1
-                            for (int k = k0; k < min(k1, steps); ++k)
-                                mma_ts(lead, o_i, s_i + k * 8, smem_desc(vbase + k * K::PAGE, K::NCH * 128, 128), idPV,
-                                       j > 0 || k > 0 ? 1u : 0u);
-                        }
-                    };
-                    if (!(ok = see_v(gt))) break;
+            for (;;) {
+                bool then, fresh = false;
+                if (now && j + 1 < p.cnt) {
+                    q = p;
+                    jq = j + 1;
+                    then = true;
+                } else {
+                    then = next(q, !now);                 // (in time for the present piece's last tile, if it is there)
+                    jq = 0;
+                    fresh = true;
+                    if (!then && !now) break;
+                }
+                const int gt = p.base + p.x0 + j * p.step, sv = gt % NSV;
+                if (now) {
+                    if (!see_v(gt)) break;
                     // a piece's first PV starts O afresh: the last one's result has been read
-                    if (j == 0 && ocnt > 0 && !(ok = wait_all(bar(K::OFREE + i), (ocnt - 1) & 1))) break;
-                    // (what the next S needs is waited for before P, off the path from P to it)
-                    if (end && after && (!(ok = see_q(q.q)) || !(ok = see_k(q.base + q.x0)))) break;
-                    if (!end && !(ok = see_k(gt + p.step))) break;
+                    if (j == 0 && ocnt > 0 && !wait_all(bar(K::OFREE + i), (ocnt - 1) & 1)) break;
+                }
+                // (what the next S needs is waited for before P, off the path from P to it)
+                if (then && ((fresh && !see_q(q.q)) || !see_k(q.base + q.x0 + jq * q.step))) break;
+                if (now) {
                     if (HG == 1 && p.two) {
-                        if ((i == 1 || turn > 0) && !(ok = wait_all(bar(K::TURN + i), (i == 1 ? turn : turn - 1) & 1))) break;
+                        if ((i == 1 || turn > 0) && !wait_all(bar(K::TURN + i), (i == 1 ? turn : turn - 1) & 1)) break;
                         ++turn;
                     }
-                    if constexpr (HG == 1) {
-                        if (!(ok = wait_all(bar(K::PFA + i), pcnt & 1))) break;
+                    const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
+                    // units up to the last page that a row sees
+                    const int steps = HG * min(max((p.ends - (p.t0 + p.x0 + j * p.step) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
+                    constexpr int HALVES = HG == 1 ? 2 : 1, EACH = kUnits / HALVES;
+                    bool ok = true;
+#pragma unroll
+                    for (int half = 0; half < HALVES; ++half) {
+                        if (!(ok = wait_all(bar((HG == 1 && half == 0 ? K::PFA : K::PFB) + i), pcnt & 1))) break;
                         tc_fence_after();
-                        pv(0, 4);
-                        commit(lead, bar(K::PVA + i));
-                        if (!(ok = wait_all(bar(K::PFB + i), pcnt & 1))) break;
-                        tc_fence_after();
-                        pv(4, 8);
-                    } else {
-                        if (!(ok = wait_all(bar(K::PFB + i), pcnt & 1))) break;
-                        tc_fence_after();
-                        pv(0, 8);
+#pragma unroll
+                        for (int k = half * EACH; k < half * EACH + EACH; ++k)
+                            mma_ts(lead && k < steps, o_i, s_i + k * 8, smem_desc(vbase + k * K::PAGE, K::NCH * 128, 128), idPV,
+                                   j > 0 || k > 0 ? 1u : 0u);
+                        if (HG == 1 && half == 0) commit(lead, bar(K::PVA + i));
                     }
-                    if (end) commit(lead, bar(K::ODONE + i));
+                    if (!ok) break;
+                    if (j + 1 == p.cnt) {
+                        commit(lead, bar(K::ODONE + i));
+                        ++ocnt;
+                    }
                     commit(lead, bar(K::VEMPTY + sv));
-                    if (!end) issue_s(p, j + 1);
-                    else if (after) issue_s(q, 0);
-                    if (HG == 1 && p.two) {
-                        if constexpr (D == 64) commit(lead, bar(K::TURN + 1 - i));
-                        else if (lead) mbar_arrive(bar(K::TURN + 1 - i));
-                    }
+                    ++pcnt;
+                } else {
+                    tc_fence_after();
                 }
-                if (!ok) break;
-                ++ocnt;
-                begun = after;
-                if (after) p = q;
-                else more = next(p, true);
+                if (then) issue_s(q, jq);
+                if (HG == 1 && now && p.two) {
+                    if constexpr (D == 64) commit(lead, bar(K::TURN + 1 - i));
+                    else if (lead) mbar_arrive(bar(K::TURN + 1 - i));
+                }
+                now = then;
+                p = q;
+                j = jq;
             }
             commit(lead, bar(K::DRAIN));
             // every MMA issued has completed before TMEM is freed
@@ -1535,7 +1537,6 @@ cudaError_t launch_masked(const pkv_cache& c, const pkv_rows* q, const pkv_rows*
     a.tree_words = tree_words;
     a.window = window;
     a.sinks = sinks;
-    a.wide = rows::wide(a.out);
     a.scale_log2 = scale * kLog2e;
     const unsigned grid = (unsigned)std::min(sms, kMaxCtas);
     if (c.kv_dtype == PKV_KV_FP8_E4M3)
