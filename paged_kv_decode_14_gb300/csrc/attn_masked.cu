@@ -508,6 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 tmem_ld16_at<16>(scol + ((k + kBlock) * HG + hw * kBlock), s);
             }
         };
+        constexpr int STEP = K::KEYS < 64 ? K::KEYS : 64; // keys whose P is written at once
+        constexpr bool PAIR = STEP == 64;
         bool ok = true;
         int scnt = 0, ocnt = 0, tbase = 0, qbase = 0;     // this chain's tiles and pieces; the CTA's tiles and Q tiles
         for (int n = 0; ok; ++n) {
@@ -573,20 +575,17 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     }
                     return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 };
-                // columns of this row's P of page pg of the tile (8: two P a column)
-                auto p_col = [&](int pg) { return scol + (pg * HG + hw) * 8; };
                 // (rare) a P of the keys from k on reaches 2: m rises by a whole number of octaves, and the P written in
-                // this tile, O and l are scaled down by as many (exact but for what falls below the types' range)
+                // this tile, O and l are scaled down by as many (exact but for what falls below fp32's range)
                 auto raise_ref = [&](float target, int k) {
                     const float inc = target + kHeadroom > m ? ceilf(target + kHeadroom - m) : 0.f;
                     const int e = (int)fminf(inc, 127.f);
                     const float alpha = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
-                    const bool half = HG == 1 && k >= 64; // the first half's P is being used: it ends in O
-                    if (half) {
+                    if (k > 0) {                          // the first half's P is being used: it ends in O
                         wait_all(bar(K::PVA + i), scnt & 1);
                         tc_fence_after();
                     }
-                    if (j > 0 || half) {
+                    if (j > 0 || k > 0) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float o[16];
@@ -596,17 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                             for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(o[y] * alpha);
                             tmem_st16u(ocol + c, v);
                         }
+                        tmem_wait_st();
                     }
-                    // (P that are written and not used yet)
-#pragma unroll 1
-                    for (int pg = (half ? 64 : 0) / kBlock; pg < k / kBlock; ++pg) {
-                        uint32_t v[8];
-                        tmem_ld8(p_col(pg), v);
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) v[y] = pack_bf16(bf16_lo(v[y]) * alpha, bf16_hi(v[y]) * alpha);
-                        tmem_st8(p_col(pg), v);
-                    }
-                    tmem_wait_st();
                     l *= alpha;
                     m += inc;
                 };
@@ -649,55 +639,83 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     acc = f2add(acc, f2add(ca, cb));
                 };
                 tmem_wait_ld_into(sa);
-                // (rolled, one copy of either path: the instruction cache holds little more than the roles' inner loops)
+                // (one copy of either path: the instruction cache holds little more than the roles' inner loops)
 #pragma unroll 1
-                for (int k = 0; k < K::KEYS; k += 32) {
-                    uint32_t next_s[32];
-                    if (K::KEYS > 32) load_s(min(k + 32, K::KEYS - 32), next_s);
+                for (int k = 0; k < K::KEYS; k += STEP) {
                     // what no row sees behind the first half is not read by the PV
-                    const bool none = HG == 1 && k >= 64 && v0 + 64 >= ends;
+                    const bool none = k > 0 && v0 + k >= ends;
                     bool again = false;
 #pragma unroll 1
                     while (!none) {
-                        const uint32_t w = masked ? bits(k) : ~0u;
+                        uint32_t w0 = ~0u, w1 = ~0u;
+                        if (masked) {
+                            w0 = bits(k);
+                            if (PAIR) w1 = bits(k + 32);
+                        }
                         if (again || !__all_sync(0xffffffffu, m > -INFINITY)) {
                             // no reference yet (a piece's first tile): the largest that is visible (O and l are 0 so far); or
                             // one that is too small
-                            const float top = largest(sa, k, w);
+                            float top = -INFINITY;
+#pragma unroll 1
+                            for (int h = 0; h < STEP; h += 32) {
+                                load_s(k + h, sa);
+                                tmem_wait_ld_into(sa);
+                                top = fmaxf(top, largest(sa, k + h, h ? w1 : w0));
+                            }
+                            if (PAIR) {
+                                load_s(k, sa);
+                                tmem_wait_ld_into(sa);
+                            }
                             if (again) raise_ref(row_ok ? top * sc : -INFINITY, k);
                             else if (m == -INFINITY) m = top * sc + kHeadroom;
                             // (too far below 0 is only seen here: m rises)
                             if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
                         }
                         uint64_t acc = 0;
-                        uint32_t v[16];
+                        uint32_t v[STEP / 2];
                         over = 0;
-                        if (!masked) emit(sa, k, v, acc, std::false_type{}, w);
-                        else emit(sa, k, v, acc, std::true_type{}, w);
+                        if constexpr (PAIR) {             // loads in flight behind the arithmetic
+                            uint32_t s1[32];
+                            load_s(k + 32, s1);
+                            if (!masked) {
+                                emit(sa, k, v, acc, std::false_type{}, w0);
+                                tmem_wait_ld_into(s1);
+                                if (HG == 1) load_s(64, sa);      // (for the second half; after it, for nothing)
+                                emit(s1, k + 32, v + 16, acc, std::false_type{}, w1);
+                            } else {
+                                emit(sa, k, v, acc, std::true_type{}, w0);
+                                tmem_wait_ld_into(s1);
+                                if (HG == 1) load_s(64, sa);
+                                emit(s1, k + 32, v + 16, acc, std::true_type{}, w1);
+                            }
+                            if (HG == 1) tmem_wait_ld_into(sa);
+                        } else {
+                            if (!masked) emit(sa, k, v, acc, std::false_type{}, w0);
+                            else emit(sa, k, v, acc, std::true_type{}, w0);
+                        }
                         // P is written once none is known to reach 2 (the top exponent bit is clear below)
                         bool high;
                         if constexpr (FP8) {
                             high = (over & 0x40000000u) != 0;
                         } else {
-                            uint32_t any[2] = {v[0], v[1]};
+                            uint32_t any[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                            for (int y = 2; y < 16; ++y) any[y & 1] |= v[y];
-                            high = ((any[0] | any[1]) & 0x40004000u) != 0;
+                            for (int y = 4; y < STEP / 2; ++y) any[y & 3] |= v[y];
+                            high = ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
                         }
                         if (__any_sync(0xffffffffu, row_ok && high) && !again) {
                             again = true;                 // once more with m raised (NaN logits pass then)
                             continue;
                         }
                         if constexpr (HG == 1) {
-                            tmem_st16u(scol + (k >> 1), v);
+                            tmem_st32u(scol + (k >> 1), v);
                         } else {
 #pragma unroll
-                            for (int x2 = 0; x2 < 2; ++x2) {
+                            for (int pg = 0; pg < K::TP; ++pg) {
                                 uint32_t d8[8], z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                                for (int y = 0; y < 8; ++y) d8[y] = v[x2 * 8 + y];
-                                const int pg = k / kBlock + x2;
-                                tmem_st8(p_col(pg), d8);
+                                for (int y = 0; y < 8; ++y) d8[y] = v[pg * 8 + y];
+                                tmem_st8(scol + (pg * HG + hw) * 8, d8);
 #pragma unroll
                                 for (int y = 1; y < HG; ++y) tmem_st8(scol + (pg * HG + (hw + y) % HG) * 8, z);
                             }
@@ -708,15 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                         tmem_wait_st();
                         break;
                     }
-                    if (K::KEYS > 32) {
-                        tmem_wait_ld_into(next_s);
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) sa[y] = next_s[y];
-                    }
                     // P of the first 64 keys: their PV may run while the rest is computed
-                    if (HG == 1 && k == 32) signal(bar(K::PFA + i));
+                    signal(bar(HG == 1 && k == 0 ? K::PFA + i : K::PFB + i));
                 }
-                signal(bar(K::PFB + i));
             }
             if (!ok) break;
             // (a reference so large that fp32 cannot place the weights beside it is reported)
@@ -979,96 +991,97 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         auto finish_lse = [](float m, float l) {
             return m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
         };
-        // The epilogue of piece ep, 32 columns at a time (the jobs above come between them).  True: done.
-        int ep = 0, ei = 0, ec = 0;                       // the piece, its row tile and column
-        float fa = 1.f, fb = 0.f, inv = 0.f;              // factors of the chains' O, and of the sum
-        auto epilogue = [&]() -> bool {
-            const Piece& p = ring[ep % kPieces];
+        // The epilogue of piece n.  (In loops, one copy: it runs once a piece, from an instruction cache that holds the
+        // inner loops by then.)
+        auto epilogue = [&](const Piece& p, int n) {
             const bool whole = p.parts == 1, both = !p.two && p.count(1) > 0;          // both: the chains share a row
-            const int qi = ei * a.pb + pos;
-            const bool row_ok = pos < a.pb && qi < p.nq;
-            const int64_t row = p.row + p.q0 + qi;
-            const int h = (p.g + hw) * G + hl;
             float* slot = part_slot<D>(a, blockIdx.x, p.t0 == 0);
-            const bool live = __any_sync(0xffffffffu, row_ok);
-            if (ec == 0 && live) {
-                const float* mla = ml + (p.two ? 2 * ei : 0) * kRows;
-                float m = mla[r], l = mla[kRows + r];
-                fa = 1.f;
-                fb = 0.f;
-                if (both) {
-                    const float m1 = ml[2 * kRows + r], l1 = ml[3 * kRows + r], top = fmaxf(m, m1);
-                    fa = weight(m, l, top);
-                    fb = weight(m1, l1, top);
-                    l = l * fa + l1 * fb;
-                    if (m == -INFINITY) fa = 1.f;
-                    if (m1 == -INFINITY) fb = 1.f;
-                    m = top;
-                }
-                inv = m == -INFINITY && l == 0.f ? -1.f : 1.f / l;         // (-1: a row that saw nothing)
-                if (row_ok) {
-                    if (!whole) {
-                        slot[(size_t)2 * kRows * D + ei * kRows + r] = m;
-                        slot[(size_t)2 * kRows * (D + 1) + ei * kRows + r] = l;
-                    } else if (a.lse) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < (p.two ? 2 : 1); ++i) {
+                const int qi = i * a.pb + pos;
+                const bool row_ok = pos < a.pb && qi < p.nq;
+                if (__any_sync(0xffffffffu, row_ok)) {
+                    const uint32_t oa = tmem + lbase + K::COL_O + (p.two ? i * D : 0), ob = tmem + lbase + K::COL_O + D;
+                    uint32_t x[32];
+                    tmem_ld32_async(oa, x);
+                    const float* mla = ml + (p.two ? 2 * i : 0) * kRows;
+                    float m = mla[r], l = mla[kRows + r], fa = 1.f, fb = 0.f;
+                    if (both) {
+                        const float m1 = ml[2 * kRows + r], l1 = ml[3 * kRows + r], top = fmaxf(m, m1);
+                        fa = weight(m, l, top);
+                        fb = weight(m1, l1, top);
+                        l = l * fa + l1 * fb;
+                        if (m == -INFINITY) fa = 1.f;
+                        if (m1 == -INFINITY) fb = 1.f;
+                        m = top;
+                    }
+                    const bool none = m == -INFINITY && l == 0.f;          // a row that saw nothing
+                    const int64_t row = p.row + p.q0 + qi;
+                    const int h = (p.g + hw) * G + hl;
+                    uint8_t* dst = row_ok ? a.out.row(row, h) : nullptr;
+                    float* part = slot + (i * kRows + r) * 4;
+                    if (row_ok && !whole) {
+                        slot[(size_t)2 * kRows * D + i * kRows + r] = m;
+                        slot[(size_t)2 * kRows * (D + 1) + i * kRows + r] = l;
+                    } else if (row_ok && a.lse) {
                         a.lse[row * a.Hq + h] = finish_lse(m, l);
                     }
-                }
-            }
-            if (live) {
-                tc_fence_after();
-                const uint32_t oa = tmem + lbase + K::COL_O + (p.two ? ei * D : 0) + ec, ob = tmem + lbase + K::COL_O + D + ec;
-                uint32_t x[32], y[32];
-                tmem_ld32_async(oa, x);
-                if (both) tmem_ld32_async(ob, y);
-                tmem_wait_ld_into(x);
-                if (both) {
-                    tmem_wait_ld_into(y);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        x[e] = __float_as_uint(__uint_as_float(x[e]) * fa + __uint_as_float(y[e]) * fb);
-                }
-                if (row_ok) {
-                    uint8_t* dst = a.out.row(row, h);
-                    float* part = slot + (ei * kRows + r) * 4;
+                    const float inv = none ? 0.f : 1.f / l;
                     if (whole) {
-                        uint32_t v[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            v[e] = inv == -1.f ? 0u : pack_bf16(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<uint4*>(dst + ec * 2 + e * 4) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(part + (size_t)((ec + e) / 4) * 2 * kRows * 4) =
-                                make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        fa *= inv;
+                        fb *= inv;
                     }
-                    if (ec + 32 == D && nonfinite[ep % kFlags] == ep + 1) add_back(p, qi, dst, whole ? nullptr : part);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_wait_ld_into(x);
+                        if (both) {
+                            uint32_t y[32];
+                            tmem_ld32_async(ob + c, y);
+                            tmem_wait_ld_into(y);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa + __uint_as_float(y[e]) * fb;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa;
+                        }
+                        tmem_ld32_async(oa + min(c + 32, D - 32), x);      // (behind the last, for nothing)
+                        if (row_ok && whole) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                uint32_t v[4];
+#pragma unroll
+                                for (int f = 0; f < 4; ++f) v[f] = none ? 0u : pack_bf16(o[e + 2 * f], o[e + 2 * f + 1]);
+                                *reinterpret_cast<uint4*>(dst + (c + e) * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+                            }
+                        } else if (row_ok) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4*>(part + (size_t)((c + e) / 4) * 2 * kRows * 4) =
+                                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    tmem_wait_ld_into(x);
+                    if (row_ok && nonfinite[n % kFlags] == n + 1) add_back(p, qi, dst, whole ? nullptr : part);
                 }
+                // O read: the next piece's first PV may overwrite it
+                tc_fence_before();
                 __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(K::OFREE + (p.two ? i : 0)));
+                    if (both) mbar_arrive(bar(K::OFREE + 1));
+                }
             }
-            ec += 32;
-            if (live && ec < D) return false;
-            // O read: the next piece's first PV may overwrite it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(K::OFREE + (p.two ? ei : 0)));
-                if (both) mbar_arrive(bar(K::OFREE + 1));
-            }
-            ec = 0;
-            if (++ei < (p.two ? 2 : 1)) return false;
-            ei = 0;
-            if (whole) return true;
+            if (whole) return;
             // The part is in memory: the last of the item's CTAs to get here (for these 32 lanes' rows) joins them, in order.
             __threadfence();
             __syncwarp();
             int old = 0;
             int* ticket = a.tickets + p.c0 * 4 + w;
             if (lane == 0) old = atom_add_acq_rel_gpu(ticket, 1);
-            if (__shfl_sync(0xffffffffu, old, 0) != p.parts - 1) return true;
+            if (__shfl_sync(0xffffffffu, old, 0) != p.parts - 1) return;
             if (lane == 0) *ticket = 0;
             fence_acquire_gpu();
 #pragma unroll 1
@@ -1114,7 +1127,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     if (c == 0 && a.lse) a.lse[orow * a.Hq + oh] = finish_lse(top, l);
                 }
             }
-            return true;
         };
 
         // Each job when its input is there, none waited for while another may run: the next piece's tiles are made ready
@@ -1122,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         int rp = 0, rx = 0, rg = 0;                       // the piece, its tile, and the CTA's tile to make ready
         int qp = 0, qn = 0, qi = 0;                       // (FP8) the piece, the CTA's Q tile and the piece's to make ready
         bool last = false, known = false;                 // no piece behind rp; piece rp is there
-        bool busy = false;                                // in piece ep's epilogue
+        int ep = 0;                                       // the piece to finish
         uint32_t phase = 0;                               // of either chain's pieces, as bits
         uint64_t since = 0;
         uint32_t spins = 0;
@@ -1155,16 +1167,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 }
             }
             if (ep < rp) {
-                const bool c1 = ring[ep % kPieces].count(1) > 0;               // (chain 0 always has tiles)
-                if (!busy && there(bar(K::ODONE), phase & 1) && there(bar(K::LREADY), phase & 1) &&
-                    (!c1 || (there(bar(K::ODONE + 1), phase >> 1 & 1) && there(bar(K::LREADY + 1), phase >> 1 & 1))))
-                    busy = true;
-                if (busy) {
-                    if (epilogue()) {
-                        phase ^= c1 ? 3u : 1u;
-                        release(ep++);
-                        busy = false;
-                    }
+                const Piece& p = ring[ep % kPieces];
+                const bool c1 = p.count(1) > 0;           // (chain 0 always has tiles)
+                if (there(bar(K::ODONE), phase & 1) && there(bar(K::LREADY), phase & 1) &&
+                    (!c1 || (there(bar(K::ODONE + 1), phase >> 1 & 1) && there(bar(K::LREADY + 1), phase >> 1 & 1)))) {
+                    epilogue(p, ep);
+                    phase ^= c1 ? 3u : 1u;
+                    release(ep++);
                     moved = true;
                 }
             } else if (last) {
@@ -1254,13 +1263,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
                     const int slot = nq & 1;
                     if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(K::QFULL + slot), HG * K::SLABS * a.pb * a.group * 128);
-#pragma unroll 1
-                        for (int x = 0; x < HG * K::SLABS; ++x)
-                            tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + (x % K::SLABS) * K::SLAB + (x / K::SLABS) * RQ * 128, &a.q,
-                                       (x % K::SLABS) * 64, (p->g + x / K::SLABS) * a.group, (int)(p->row + p->q0 + i * a.pb),
-                                       bar(K::QFULL + slot));
+                    if (lane == 0) mbar_arrive_expect_tx(bar(K::QFULL + slot), HG * K::SLABS * a.pb * a.group * 128);
+                    __syncwarp();
+                    if (lane < HG * K::SLABS) {           // (a lane for each head's slab)
+                        const int sl = lane % K::SLABS, hq = lane / K::SLABS;
+                        tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + sl * K::SLAB + hq * RQ * 128, &a.q, sl * 64,
+                                   (p->g + hq) * a.group, (int)(p->row + p->q0 + i * a.pb), bar(K::QFULL + slot));
                     }
                 }
                 id = checked(id);
