@@ -35,8 +35,8 @@
 // Work is cut into equal ranges of key tiles over all items, one range per CTA; an item that a range's end cuts leaves
 // partial (O, m, l) in the workspace, and whichever CTA finishes its part last joins them, in the keys' order.
 //
-// Roles (512 threads): warps 0-3 and 4-7 the softmax of chains 0 and 1; warps 8-11 make V (and, FP8, Q) ready and run the
-// epilogue; warp 12 the producer; warps 13 and 14 the MMA issuers of the chains; warp 15 the plan.  Every wait is bounded.
+// Roles (512 threads): warps 0-3 and 4-7 the softmax of chains 0 and 1, and the results; warps 8-11 make V (and, FP8, Q)
+// ready; warp 12 the producer; warps 13 and 14 the MMA issuers of the chains; warp 15 the plan.  Every wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>
@@ -65,6 +65,7 @@ constexpr int kPieces = 4;                 // pieces of work planned ahead
 constexpr int kFlags = 8;                  // pieces whose "non-finite V" flags are kept
 constexpr int kMaxCtas = 160;              // CTAs of a launch (two workspace slots each)
 constexpr int kItemUnits = 2;              // what an item costs beside its key tiles, in key tiles of one row tile
+constexpr uint32_t kWaitHint = 20000;     // ns that a wait may sleep before it looks at the abort flag
 constexpr int kMinUnits = 4;               // units that a CTA has at least
 
 struct Arg {
@@ -77,7 +78,7 @@ struct Arg {
     View out;
     float* lse;
     int* err;
-    int* tickets;                          // [CTA][4]
+    int* tickets;                          // [CTA][8]
     float* partials;                       // [CTA][2] slots
     uint64_t wait_limit_ns;
     const int* hold;
@@ -135,6 +136,30 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, in
     return n - j >= 32 ? x : n - j <= 0 ? 0u : x & ((1u << (n - j)) - 1u);
 }
 
+// What all rows of an item see, and what any does.
+template <int HG>
+struct Guard {
+    int ns_all, wl_all, wh_all, ns_any, wl_any, wh_any;
+    __device__ __forceinline__ bool any(int v) const { return v < ns_any || (v >= wl_any && v <= wh_any); }
+    __device__ __forceinline__ bool all(int v) const { return HG == 1 && (v < ns_all || (v >= wl_all && v <= wh_all)); }
+    // all of v .. v + n - 1 are seen by some row (whole: by every row of the tile)
+    __device__ __forceinline__ bool any_of(int v, int n) const {
+        return v + n <= ns_any || (v >= wl_any && v + n - 1 <= wh_any);
+    }
+    __device__ __forceinline__ bool all_of(int v, int n) const {
+        return HG == 1 && (v + n <= ns_all || (v >= wl_all && v + n - 1 <= wh_all));
+    }
+};
+
+template <int HG>
+__device__ __forceinline__ Guard<HG> guard_of(const Arg& a, const Piece& p) {
+    if (a.tree) return Guard<HG>{0, 0, p.L - p.Q - 1, 0, 0, p.L - 1};
+    Sight f, l;
+    f.window(a, p, p.first);
+    l.window(a, p, p.first + p.nq - 1);
+    return Guard<HG>{f.ns, l.wl, f.wh, l.ns, f.wl, l.wh};
+}
+
 template <int D, bool FP8, int HG>
 struct Cfg {
     static constexpr int TP = kUnits / HG;                // pages of a tile (of each head)
@@ -169,7 +194,8 @@ struct Cfg {
     static constexpr int OFF_PIECE = OFF_ML + 4 * 4 * kRows;
     static constexpr int OFF_SC = OFF_PIECE + kPieces * (int)sizeof(Piece);       // FP8: float[NSC][k scales 8, v scales 8]
     static constexpr int OFF_QS = OFF_SC + (FP8 ? NSC * 64 : 0);                  // FP8: float[NQS][kRows]
-    static constexpr int SMEM = OFF_QS + (FP8 ? NQS * 4 * kRows : 0);
+    static constexpr int OFF_VF = OFF_QS + (FP8 ? NQS * 4 * kRows : 0);           // FP8: bool[NSC][8], a unit's v scale is finite
+    static constexpr int SMEM = OFF_VF + (FP8 ? NSC * 8 : 0);
     static constexpr int COL_O = 2 * kCols;
     static constexpr int TMEM_COLS = 512;
     static_assert(OFF_PIECE % 8 == 0, "alignment");
@@ -413,14 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
     float* ml = reinterpret_cast<float*>(smem + K::OFF_ML);
     float* scales = reinterpret_cast<float*>(smem + K::OFF_SC);
     float* q_scale = reinterpret_cast<float*>(smem + K::OFF_QS);
+    uint8_t* v_finite = smem + K::OFF_VF;
     Piece* ring = reinterpret_cast<Piece*>(smem + K::OFF_PIECE);
     // every wait and every TMEM access is warp-uniform (tcgen05.ld / st are .aligned)
-    // (Their limit is kept by warps 8-11, which see every tile: where none of their jobs moves on for so long, they set
-    // the abort flag.  A clock in each of the sixty waits made the code a fifth longer, and it hardly fits the
-    // instruction cache.)
+    // (Their limit is kept by the plan's warp, which waits for every piece's end: where one takes that long it sets the abort
+    // flag.  A clock in each of the sixty waits made the code a fifth longer.)
     auto wait_all = [&](uint32_t bb, uint32_t parity) {
         bool there = mbar_try_wait(bb, parity);
-        while (!there && !*abort_flag) there = mbar_try_wait(bb, parity);
+        while (!there && !*abort_flag) there = mbar_try_wait_hint(bb, parity, kWaitHint);
         return (bool)__all_sync(0xffffffffu, there);
     };
 
@@ -442,8 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             mbar_init(bar(K::QREADY + i), 4);
             mbar_init(bar(K::QEMPTY + i), 2);
             mbar_init(bar(K::ODONE + i), 1);
-            mbar_init(bar(K::OFREE + i), 4);
-            mbar_init(bar(K::LREADY + i), 4);
             mbar_init(bar(K::PVA + i), 1);
             mbar_init(bar(K::TURN + i), 1);
         }
@@ -451,6 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             mbar_init(bar(K::PCFULL + i), 1);
             mbar_init(bar(K::PCEMPTY + i), 15);           // every warp but the plan's, which writes them
         }
+        mbar_init(bar(K::OFREE), 8);                      // every softmax warp, after a piece of both chains
+        mbar_init(bar(K::LREADY), 8);
         mbar_init(bar(K::DRAIN), 2);
         *abort_flag = 0;
         *drain_flag = 0;
@@ -490,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         regs_inc<kRegsSoftmax>();
         const uint32_t tmem = enter();
         const int i = warp >> 2, r = tid & (kRows - 1), hw = (warp & 3) * HG / 4;      // hw: the row's head of the HG
-        const int G = a.group, pos = r % RQ / G;
+        const int G = a.group, rr = r % RQ, pos = rr / G, hl = rr - pos * G;
         const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t scol = tmem + lbase + i * kCols;   // S / P
         const uint32_t ocol = tmem + lbase + K::COL_O + i * D;
@@ -508,10 +534,195 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 tmem_ld16_at<16>(scol + ((k + kBlock) * HG + hw * kBlock), s);
             }
         };
+        // What the guard took out of V, added to a row's results where this lane has just written them (rare).
+        auto add_back = [&](const Piece& p, int qi, int d0, int d1, uint8_t* out, float* part) {
+            const Guard<HG> gd = guard_of<HG>(a, p);
+            Sight see;
+            const uint32_t* tree = nullptr;
+            if (a.tree) {
+                see.tree(p);
+                tree = a.tree + (p.row + p.q0 + qi) * (int64_t)a.tree_words;
+            } else {
+                see.window(a, p, p.first + qi);
+            }
+            auto span = [&](int v, int z) {
+                v = max(v, p.t0 * K::KEYS);
+                z = min(z, min(p.t1 * K::KEYS, p.np * kBlock) - 1);
+#pragma unroll 1
+                for (; v <= z; ++v) {
+                    const bool has = see.has(v) || (tree && v >= p.L - p.Q &&
+                                                    (tree_bits(tree, a.tree_words, v - (p.L - p.Q), p.Q) & 1u));
+                    if (!has) continue;
+                    const int id = a.tables[(int64_t)p.b * a.max_blocks + p.page(v / kBlock)];
+                    if (id < 0 || id >= a.num_blocks) continue;
+                    const uint8_t* page = a.v_cache + ((int64_t)id * a.Hkv + p.g + hw) * K::LAND;
+                    const int off = v % kBlock;
+#pragma unroll 1
+                    for (int d = d0; d < d1; ++d) {
+                        float f;
+                        if constexpr (FP8) {
+                            const uint8_t code = page[((off / 8) * (D / 16) + d / 16) * 128 + (off % 8) * 16 + d % 16];
+                            f = e4m3x2_to_float2(code).x * a.v_scales[(int64_t)id * a.Hkv + p.g + hw];
+                        } else {
+                            f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                                page + ((off / 8) * (D / 8) + d / 8) * 128 + (off % 8) * 16 + (d % 8) * 2));
+                        }
+                        if (fabsf(f) < INFINITY) continue;
+                        if (part) {
+                            part[(size_t)(d / 4) * 2 * kRows * 4 + d % 4] += f;
+                        } else {
+                            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out) + d;
+                            *o = __float2bfloat16_rn(__bfloat162float(*o) + f);
+                        }
+                    }
+                }
+            };
+            if (HG > 1 || FP8) {                          // (FP8: a page whose scale is not finite, wherever it lies)
+                span(0, p.np * kBlock);
+            } else {
+                span(gd.wl_any, gd.wl_all - 1);
+                span(gd.wh_all + 1, gd.wh_any);
+            }
+        };
+        // the weight of a part with reference m and sum l beside the largest reference `top` of the parts.  (A part
+        // that saw nothing holds zeros, or NaN)
+        auto weight = [](float m, float l, float top) {
+            return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - top);
+        };
+        auto finish_lse = [](float m, float l) {
+            return m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+        };
+        // The results of piece n: part ct of its rows' results (two row tiles: row tile ct; one: columns from ct * D / 2 on), from
+        // this chain's O or (both) from both.  (In loops, one copy: it runs once a piece, from an instruction cache
+        // that holds the inner loops by then.)
+        auto finish = [&](const Piece& p, int n, int ct, bool both, float m, float l) {
+            const bool whole = p.parts == 1;
+            float* slot = part_slot<D>(a, blockIdx.x, p.t0 == 0);
+            const int qi = (p.two ? ct * a.pb : 0) + pos;
+            const bool row_ok = pos < a.pb && qi < p.nq;
+            if (!__any_sync(0xffffffffu, row_ok)) return;
+            const int d0 = p.two ? 0 : ct * (D / 2), d1 = p.two ? D : d0 + D / 2;
+            const uint32_t oa = tmem + lbase + K::COL_O + (both ? 0 : i * D), ob = tmem + lbase + K::COL_O + D;
+            uint32_t x[32];
+            tmem_ld32_async(oa + d0, x);
+            float fa = 1.f, fb = 0.f;
+            if (both) {
+                const float m0 = ml[r], l0 = ml[kRows + r], m1 = ml[2 * kRows + r], l1 = ml[3 * kRows + r];
+                m = fmaxf(m0, m1);
+                fa = weight(m0, l0, m);
+                fb = weight(m1, l1, m);
+                l = l0 * fa + l1 * fb;
+                if (m0 == -INFINITY) fa = 1.f;
+                if (m1 == -INFINITY) fb = 1.f;
+            }
+            const bool none = m == -INFINITY && l == 0.f;          // a row that saw nothing
+            const int64_t row = p.row + p.q0 + qi;
+            const int h = (p.g + hw) * G + hl;
+            uint8_t* dst = row_ok ? a.out.row(row, h) : nullptr;
+            float* part = slot + ((p.two ? ct * kRows : 0) + r) * 4;
+            if (row_ok && !whole) {
+                slot[(size_t)2 * kRows * D + ct * kRows + r] = m;
+                slot[(size_t)2 * kRows * (D + 1) + ct * kRows + r] = l;
+            } else if (row_ok && a.lse && (p.two || ct == 0)) {
+                a.lse[row * a.Hq + h] = finish_lse(m, l);
+            }
+            const float inv = none ? 0.f : 1.f / l;
+            if (whole) {
+                fa *= inv;
+                fb *= inv;
+            }
+#pragma unroll 1
+            for (int c = d0; c < d1; c += 32) {
+                float o[32];
+                tmem_wait_ld_into(x);
+                if (both) {
+                    uint32_t y[32];
+                    tmem_ld32_async(ob + c, y);
+                    tmem_wait_ld_into(y);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa + __uint_as_float(y[e]) * fb;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa;
+                }
+                tmem_ld32_async(oa + min(c + 32, D - 32), x);      // (behind the last, for nothing)
+                if (row_ok && whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) v[f] = none ? 0u : pack_bf16(o[e + 2 * f], o[e + 2 * f + 1]);
+                        *reinterpret_cast<uint4*>(dst + (c + e) * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                } else if (row_ok) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(part + (size_t)((c + e) / 4) * 2 * kRows * 4) =
+                            make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+                __syncwarp();
+            }
+            tmem_wait_ld_into(x);
+            if (row_ok && nonfinite[n % kFlags] == n + 1) add_back(p, qi, d0, d1, dst, whole ? nullptr : part);
+        };
+        // A cut piece's part ct is in memory: the last of the item's CTAs to get here (with these lanes' rows) joins
+        // them, in order.
+        auto join = [&](const Piece& p, int ct) {
+            const int w = warp & 3;
+            const int mine = min(32, min(a.pb, p.nq - (p.two ? ct * a.pb : 0)) * G - (w * 32) % RQ);     // valid rows among the lanes
+            if (mine <= 0) return;
+            __threadfence();
+            __syncwarp();
+            int old = 0;
+            int* ticket = a.tickets + p.c0 * 8 + ct * 4 + w;
+            if (lane == 0) old = atom_add_acq_rel_gpu(ticket, 1);
+            if (__shfl_sync(0xffffffffu, old, 0) != p.parts - 1) return;
+            if (lane == 0) *ticket = 0;
+            fence_acquire_gpu();
+            const int d0 = p.two ? 0 : ct * (D / 2), n8 = (p.two ? D : D / 2) / 8, rt = p.two ? ct * kRows : 0;
+#pragma unroll 1
+            for (int y = lane; y < mine * n8; y += 32) {
+                const int R = w * 32 + y % mine, c = d0 + y / mine * 8, rp = R % RQ / G;
+                auto at = [&](int x) { return part_slot<D>(a, p.c0 + x, x == 0); };
+                float top = -INFINITY;
+#pragma unroll 4
+                for (int x = 0; x < p.parts; ++x) top = fmaxf(top, __ldcg(at(x) + (size_t)2 * kRows * D + ct * kRows + R));
+                float l = 0.f, o[8] = {};
+#pragma unroll 2
+                for (int x = 0; x < p.parts; ++x) {
+                    const float* s = at(x);
+                    const float mx = __ldcg(s + (size_t)2 * kRows * D + ct * kRows + R);
+                    const float lx = __ldcg(s + (size_t)2 * kRows * (D + 1) + ct * kRows + R);
+                    const float4 u0 = __ldcg(reinterpret_cast<const float4*>(s + ((size_t)(c / 4) * 2 * kRows + rt + R) * 4));
+                    const float4 u1 = __ldcg(reinterpret_cast<const float4*>(s + ((size_t)(c / 4 + 1) * 2 * kRows + rt + R) * 4));
+                    float f = weight(mx, lx, top);
+                    l += f * lx;
+                    if (mx == -INFINITY) f = 1.f;
+                    o[0] = fmaf(u0.x, f, o[0]);
+                    o[1] = fmaf(u0.y, f, o[1]);
+                    o[2] = fmaf(u0.z, f, o[2]);
+                    o[3] = fmaf(u0.w, f, o[3]);
+                    o[4] = fmaf(u1.x, f, o[4]);
+                    o[5] = fmaf(u1.y, f, o[5]);
+                    o[6] = fmaf(u1.z, f, o[6]);
+                    o[7] = fmaf(u1.w, f, o[7]);
+                }
+                const bool none = top == -INFINITY && l == 0.f;
+                const float il = none ? 0.f : 1.f / l;
+                const int64_t orow = p.row + p.q0 + (p.two ? ct * a.pb : 0) + rp;
+                const int oh = (p.g + hw) * G + R % RQ - rp * G;
+                uint32_t v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = none ? 0u : pack_bf16(o[2 * e] * il, o[2 * e + 1] * il);
+                *reinterpret_cast<uint4*>(a.out.row(orow, oh) + c * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+                if (c == 0 && a.lse) a.lse[orow * a.Hq + oh] = finish_lse(top, l);
+            }
+        };
         constexpr int STEP = K::KEYS < 64 ? K::KEYS : 64; // keys whose P is written at once
         constexpr bool PAIR = STEP == 64;
         bool ok = true;
-        int scnt = 0, ocnt = 0, tbase = 0, qbase = 0;     // this chain's tiles and pieces; the CTA's tiles and Q tiles
+        int scnt = 0, tbase = 0, qbase = 0;               // this chain's tiles; the CTA's tiles and Q tiles
+        int pieces = 0, pieces1 = 0, bcnt = 0;            // the CTA's pieces; those of chain 1; those of both chains
         for (int n = 0; ok; ++n) {
             const Piece* p = piece_at(n);
             if (!p || p->end) break;
@@ -520,6 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             tbase += p->tiles();
             qbase += p->two ? 2 : 1;
             if (cnt == 0) {
+                ++pieces;
                 release(n);
                 continue;
             }
@@ -552,28 +764,48 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     continue;
                 }
                 tc_fence_after();
-                uint32_t sa[32];
-                load_s(0, sa);
                 if (FP8 && j == 0) sc = a.scale_log2 * q_scale[qt % K::NQS * kRows + r];
                 const float* ks = scales + ((base + x) % K::NSC) * 16 + hw;     // (of unit u: ks[u * HG])
                 const bool masked = !__all_sync(0xffffffffu, (v0 >= see.wl && v0 + K::KEYS - 1 <= see.wh) || v0 + K::KEYS <= see.ns);
-                // the visible ones of keys k .. k + 31 of the tile
-                auto bits = [&](int k) -> uint32_t {
-                    const int v = v0 + k, n_s = see.ns - v, lo = max(see.wl - v, 0), hi = min(see.wh - v, 31);
-                    uint32_t w = n_s >= 32 ? 0xffffffffu : n_s > 0 ? (1u << n_s) - 1u : 0u;
-                    if (lo <= hi) w |= (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
-                    if (tree && v + 31 >= tree0) w |= tree_bits(tree, a.tree_words, v - tree0, tree_n);
-                    return w;
-                };
-                // the largest visible S (FP8: times its page's scale) of 32 keys from k on
-                auto largest = [&](const uint32_t (&s)[32], int k, uint32_t w) -> float {
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // A tile that some row does not see all of: its S becomes -inf there, in tensor memory (FP8: the page's scale is
+                // multiplied in on the way), and what follows knows no masks.  (A second copy of it with masks, though
+                // hardly ever run, made every tile a third slower: the inner loops no longer fit the instruction cache.)
+                if (masked) {
+#pragma unroll 1
+                    for (int pg = 0; pg < K::TP; ++pg) {
+                        // the visible ones of the page's 16 keys
+                        const int v = v0 + pg * kBlock, n_s = see.ns - v, lo = max(see.wl - v, 0), hi = min(see.wh - v, 31);
+                        uint32_t w = n_s >= 16 ? 0xffffu : n_s > 0 ? (1u << n_s) - 1u : 0u;
+                        if (lo <= hi) w |= (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+                        if (tree && v + 31 >= tree0) w |= tree_bits(tree, a.tree_words, v - tree0, tree_n);
+                        if (!FP8 && __all_sync(0xffffffffu, (w & 0xffffu) == 0xffffu)) continue;
+                        const uint32_t col = scol + (pg * HG + hw) * kBlock;
+                        float f[16];
+                        tmem_ld16(col, f);
+                        uint32_t t[16];
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) {
-                        const float f = FP8 ? __uint_as_float(s[y]) * ks[(k + y) / kBlock * HG] : __uint_as_float(s[y]);
-                        mx[y & 3] = fmaxf(mx[y & 3], w >> y & 1 ? f : -INFINITY);
+                        for (int y = 0; y < 16; ++y)
+                            t[y] = w >> y & 1 ? __float_as_uint(FP8 ? f[y] * ks[pg * HG] : f[y]) : 0xff800000u;
+                        tmem_st16u(col, t);
                     }
-                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    tmem_wait_st();
+                }
+                // the factor of S of page pg
+                auto k_scale = [&](int pg) { return masked ? 1.f : ks[pg * HG]; };
+                uint32_t sa[32];
+                load_s(0, sa);
+                // the largest S (FP8: times its page's scale) of keys k .. k + STEP - 1
+                auto largest = [&](int k) -> float {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int pg = k / kBlock; pg < (k + STEP) / kBlock; ++pg) {
+                        float f[16], t = -INFINITY;
+                        tmem_ld16(scol + (pg * HG + hw) * kBlock, f);
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) t = fmaxf(t, FP8 ? f[y] * k_scale(pg) : f[y]);
+                        top = fmaxf(top, t);
+                    }
+                    return top;
                 };
                 // (rare) a P of the keys from k on reaches 2: m rises by a whole number of octaves, and the P written in
                 // this tile, O and l are scaled down by as many (exact but for what falls below fp32's range)
@@ -602,36 +834,28 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 };
                 uint32_t over = 0;                        // (FP8) the OR of the P to be written
                 // P of 32 keys from k on, two per packed fp32 operation (the even key in the low half); adds them to
-                // acc.  (Rows with nothing visible so far keep m = -inf: all their P are masked.)
-                auto emit = [&](const uint32_t (&s)[32], int k, uint32_t* v, uint64_t& acc, auto mask, uint32_t w) {
+                // acc.  (Rows with nothing visible so far keep m = -inf: all their S are.)
+                auto emit = [&](const uint32_t (&s)[32], int k, uint32_t* v, uint64_t& acc) {
                     uint64_t ca = 0, cb = 0;
                     const float nm = m == -INFINITY ? 0.f : -m;
                     const uint64_t nm2 = f2pack(__float_as_uint(nm), __float_as_uint(nm));
 #pragma unroll
                     for (int h = 0; h < 32; h += 16) {
-                        const int u = (k + h) / kBlock * HG;
-                        const float f = FP8 ? sc * ks[u] : sc;
+                        const int pg = (k + h) / kBlock;
+                        const float f = FP8 ? sc * k_scale(pg) : sc;
                         const uint64_t sc2 = f2pack(__float_as_uint(f), __float_as_uint(f));
 #pragma unroll
                         for (int y = h; y < h + 16; y += 2) {
                             float q0, q1;
                             f2unpack(f2fma(f2pack(s[y], s[y + 1]), sc2, nm2), q0, q1);
                             float p0 = exp2_fast(q0), p1 = exp2_fast(q1);
-                            if constexpr (decltype(mask)::value) {
-                                p0 = w >> y & 1 ? p0 : 0.f;
-                                p1 = w >> (y + 1) & 1 ? p1 : 0.f;
-                            }
                             if ((y >> 1) & 1) cb = f2add(cb, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
                             else ca = f2add(ca, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
                             if constexpr (FP8) {
-                                const float vs = ks[8 + u];
+                                const float vs = ks[8 + pg * HG];
                                 over |= __float_as_uint(p0) | __float_as_uint(p1);
                                 p0 *= vs;
                                 p1 *= vs;
-                                if constexpr (decltype(mask)::value) {   // (a scale may be infinite or NaN)
-                                    p0 = w >> y & 1 ? p0 : 0.f;
-                                    p1 = w >> (y + 1) & 1 ? p1 : 0.f;
-                                }
                             }
                             v[y >> 1] = pack_bf16(p0, p1);
                         }
@@ -647,29 +871,18 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     bool again = false;
 #pragma unroll 1
                     while (!none) {
-                        uint32_t w0 = ~0u, w1 = ~0u;
-                        if (masked) {
-                            w0 = bits(k);
-                            if (PAIR) w1 = bits(k + 32);
-                        }
                         if (again || !__all_sync(0xffffffffu, m > -INFINITY)) {
                             // no reference yet (a piece's first tile): the largest that is visible (O and l are 0 so far); or
                             // one that is too small
-                            float top = -INFINITY;
-#pragma unroll 1
-                            for (int h = 0; h < STEP; h += 32) {
-                                load_s(k + h, sa);
-                                tmem_wait_ld_into(sa);
-                                top = fmaxf(top, largest(sa, k + h, h ? w1 : w0));
-                            }
-                            if (PAIR) {
-                                load_s(k, sa);
-                                tmem_wait_ld_into(sa);
-                            }
+                            const float top = largest(k);
                             if (again) raise_ref(row_ok ? top * sc : -INFINITY, k);
                             else if (m == -INFINITY) m = top * sc + kHeadroom;
                             // (too far below 0 is only seen here: m rises)
                             if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
+                            if (HG == 1) {
+                                load_s(k, sa);
+                                tmem_wait_ld_into(sa);
+                            }
                         }
                         uint64_t acc = 0;
                         uint32_t v[STEP / 2];
@@ -677,21 +890,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                         if constexpr (PAIR) {             // loads in flight behind the arithmetic
                             uint32_t s1[32];
                             load_s(k + 32, s1);
-                            if (!masked) {
-                                emit(sa, k, v, acc, std::false_type{}, w0);
-                                tmem_wait_ld_into(s1);
-                                if (HG == 1) load_s(64, sa);      // (for the second half; after it, for nothing)
-                                emit(s1, k + 32, v + 16, acc, std::false_type{}, w1);
-                            } else {
-                                emit(sa, k, v, acc, std::true_type{}, w0);
-                                tmem_wait_ld_into(s1);
-                                if (HG == 1) load_s(64, sa);
-                                emit(s1, k + 32, v + 16, acc, std::true_type{}, w1);
-                            }
+                            emit(sa, k, v, acc);
+                            tmem_wait_ld_into(s1);
+                            if (HG == 1) load_s(64, sa);  // (for the second half; after it, for nothing)
+                            emit(s1, k + 32, v + 16, acc);
                             if (HG == 1) tmem_wait_ld_into(sa);
                         } else {
-                            if (!masked) emit(sa, k, v, acc, std::false_type{}, w0);
-                            else emit(sa, k, v, acc, std::true_type{}, w0);
+                            emit(sa, k, v, acc);
                         }
                         // P is written once none is known to reach 2 (the top exponent bit is clear below)
                         bool high;
@@ -734,53 +939,49 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             // (a reference so large that fp32 cannot place the weights beside it is reported)
             const float size = fabsf(m);
             if (row_ok && size >= kLimit && size < INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
-            // m and l go to the epilogue, once it has taken the last piece's
-            if (ocnt++ > 0 && !(ok = wait_all(bar(K::OFREE + i), ocnt & 1))) break;
-            ml[(2 * i) * kRows + r] = m;
-            ml[(2 * i + 1) * kRows + r] = l;
+            // the results; with both chains, half the columns each, from both O, m and l
+            const bool both = !p->two && p->count(1) > 0;
+            if (both) {
+                // (m and l lie in shared memory until both chains have read the last ones)
+                if (bcnt > 0 && !(ok = wait_all(bar(K::OFREE), (bcnt - 1) & 1))) break;
+                ml[(2 * i) * kRows + r] = m;
+                ml[(2 * i + 1) * kRows + r] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(K::LREADY));
+                if (!(ok = wait_all(bar(K::LREADY), bcnt & 1))) break;
+                ++bcnt;
+            }
+            if ((both || i == 0) && !(ok = wait_all(bar(K::ODONE), pieces & 1))) break;
+            if ((both || i == 1) && !(ok = wait_all(bar(K::ODONE + 1), pieces1 & 1))) break;
+            tc_fence_after();
+            const int ct0 = p->two || both ? i : 0, ct1 = p->two || both ? i + 1 : 2;
+#pragma unroll 1
+            for (int ct = ct0; ct < ct1; ++ct) finish(*p, n, ct, both, m, l);
+            // O read: the next piece's first PV may overwrite it (in the chain itself, its P come after this)
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(K::LREADY + i));
+            if (both && lane == 0) mbar_arrive(bar(K::OFREE));
+            if (p->parts > 1) {
+#pragma unroll 1
+                for (int ct = ct0; ct < ct1; ++ct) join(*p, ct);
+            }
+            ++pieces;
+            pieces1 += p->two || both;
             release(n);
         }
     } else if (warp < kProducer) {
-        // ------------------------------------------------ V (FP8: Q too) made ready; epilogue, thread r = row r
+        // ------------------------------------------------ V (FP8: Q too) made ready
         regs_dec<kRegsReady>();
-        const uint32_t tmem = enter();
-        const int w = warp - kReady, r = tid & (kRows - 1), hw = w * HG / 4;
-        const int G = a.group, rr = r % RQ, pos = rr / G, hl = rr - pos * G;
-        const uint32_t lbase = (uint32_t)(w * 32) << 16;
+        enter();
+        const int w = warp - kReady;
 
         // V is made harmless to rows that do not see it: a weight of 0 times NaN or infinity is NaN.  Keys that no row sees
         // are cleared, and non-finite values become 0 where some rows do not see them (HG > 1: everywhere, for other
         // heads' rows have weight 0 for them) and are added back, row by row, in the epilogue (from global memory:
         // rare).
-        struct Guard {
-            int ns_all, wl_all, wh_all, ns_any, wl_any, wh_any;
-            __device__ __forceinline__ bool any(int v) const { return v < ns_any || (v >= wl_any && v <= wh_any); }
-            __device__ __forceinline__ bool all(int v) const { return HG == 1 && (v < ns_all || (v >= wl_all && v <= wh_all)); }
-            // all of v .. v + n - 1 are seen by some row (whole: by every row of the tile)
-            __device__ __forceinline__ bool any_of(int v, int n) const {
-                return v + n <= ns_any || (v >= wl_any && v + n - 1 <= wh_any);
-            }
-            __device__ __forceinline__ bool all_of(int v, int n) const {
-                return HG == 1 && (v + n <= ns_all || (v >= wl_all && v + n - 1 <= wh_all));
-            }
-        };
-        auto guard_of = [&](const Piece& p) {
-            Guard x;
-            if (a.tree) {
-                x = Guard{0, 0, p.L - p.Q - 1, 0, 0, p.L - 1};
-            } else {
-                Sight f, l;
-                f.window(a, p, p.first);
-                l.window(a, p, p.first + p.nq - 1);
-                x = Guard{f.ns, l.wl, f.wh, l.ns, f.wl, l.wh};
-            }
-            return x;
-        };
         // (FP8) `pages` of the two pages of V from `at` on, each in the upper half of its place and widened over it; their
-        // first keys at v and v1
-        auto widen_pages = [&](uint8_t* at, const Guard& gd, int v, int v1, int pages) -> bool {
+        // first keys at v and v1.  finite: of either page's scale; where it is not, all its codes count as NaN (its scale, as 1)
+        auto widen_pages = [&](uint8_t* at, const Guard<HG>& gd, int v, int v1, int pages, const uint8_t* finite) -> bool {
             constexpr int N = D / 32;                     // 16-byte chunks of codes a lane and page
             uint4 raw[2 * N];
 #pragma unroll
@@ -793,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 const int q = (lane + 32 * (j % N)) >> 3;
                 return at + j / N * K::PAGE + q / (D / 16) * (K::NCH * 128) + 2 * (q % (D / 16)) * 128 + (lane & 7) * 16;
             };
-            uint32_t nan = 0;
+            uint32_t nan = finite[0] == 0 || (pages > 1 && finite[1] == 0);
 #pragma unroll
             for (int j = 0; j < 2 * N; ++j) {
                 if (j >= N && pages < 2) break;
@@ -807,26 +1008,25 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 *reinterpret_cast<uint4*>(place(j) + 128) = make_uint4(o[4], o[5], o[6], o[7]);
             }
             bool found = false;
-            if (nan != 0 || !gd.any_of(v, kBlock) || (pages > 1 && !gd.any_of(v1, kBlock))) {      // (a lane's own chunks again)
-#pragma unroll
-                for (int j = 0; j < 2 * N; ++j) {
-                    if (j >= N && pages < 2) break;
+            if (nan != 0 || !gd.any_of(v, kBlock) || (pages > 1 && !gd.any_of(v1, kBlock))) {
+                // (rare) a lane's own chunks again: a NaN code is the only one that has become +-480
+#pragma unroll 1
+                for (int j = 0; j < pages * N; ++j) {
                     const int key = (j < N ? v : v1) + key_of(j);
-                    const bool all = gd.all(key), any = gd.any(key);
+                    const bool any = gd.any(key), leave = gd.all(key) && finite[j / N];
                     uint16_t* e = reinterpret_cast<uint16_t*>(place(j));
-                    const uint32_t bad[4] = {nan_codes(raw[j].x), nan_codes(raw[j].y), nan_codes(raw[j].z), nan_codes(raw[j].w)};
-                    if (any && (bad[0] | bad[1] | bad[2] | bad[3]) == 0) continue;
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) {        // code y
-                        const bool is_nan = bad[y / 4] >> (8 * (y % 4) + 7) & 1;
-                        if (!any || is_nan) e[y / 8 * 64 + y % 8] = any && all ? 0x7fc0 : 0;
-                        found |= any && is_nan && !all;
+#pragma unroll 1
+                    for (int y = 0; y < 16; ++y) {
+                        uint16_t& x = e[y / 8 * 64 + y % 8];
+                        const bool is_nan = (x & 0x7fff) == 0x43f0 || !finite[j / N];
+                        if (!any || is_nan) x = any && leave ? 0x7fc0 : 0;
+                        found |= any && is_nan && !leave;
                     }
                 }
             }
             return found;
         };
-        auto guard_group = [&](uint8_t* at, const Guard& gd, int v) -> bool {     // 8 keys of bf16 V
+        auto guard_group = [&](uint8_t* at, const Guard<HG>& gd, int v) -> bool {     // 8 keys of bf16 V
             constexpr uint32_t I = 0x7f807f80u, A = 0x80008000u - I;              // an exponent of all ones carries
             constexpr int N = K::NCH / 4;
             uint4* e = reinterpret_cast<uint4*>(at + lane * 16);
@@ -855,12 +1055,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         auto ready_v = [&](const Piece& p, int n, int x, int gt) {
             const int sv = gt % NSV, v0 = (p.t0 + x) * K::KEYS, pages = min(K::TP, p.np - (p.t0 + x) * K::TP);
             uint8_t* base = smem + K::OFF_V + sv * K::VTILE;
-            const Guard gd = guard_of(p);
+            const Guard<HG> gd = guard_of<HG>(a, p);
             bool found = false;
             if constexpr (FP8) {
                 const int pg = 2 * w / HG, pg1 = (2 * w + 1) / HG;
                 if (pg < pages)
-                    found = widen_pages(base + 2 * w * K::PAGE, gd, v0 + pg * kBlock, v0 + pg1 * kBlock, pg1 < pages ? 2 : 1);
+                    found = widen_pages(base + 2 * w * K::PAGE, gd, v0 + pg * kBlock, v0 + pg1 * kBlock, pg1 < pages ? 2 : 1,
+                                        v_finite + gt % K::NSC * 8 + 2 * w);
                 fence_proxy_async_smem();
             } else {
                 bool touched = false;
@@ -933,270 +1134,24 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             if (lane == 0) mbar_arrive(bar(K::QREADY + (qt & 1)));
         };
 
-        // What the guard took out of V, added to a row's results where this lane has just written them (rare).
-        auto add_back = [&](const Piece& p, int qi, uint8_t* out, float* part) {
-            const Guard gd = guard_of(p);
-            Sight see;
-            const uint32_t* tree = nullptr;
-            if (a.tree) {
-                see.tree(p);
-                tree = a.tree + (p.row + p.q0 + qi) * (int64_t)a.tree_words;
-            } else {
-                see.window(a, p, p.first + qi);
-            }
-            auto span = [&](int v, int z) {
-                v = max(v, p.t0 * K::KEYS);
-                z = min(z, min(p.t1 * K::KEYS, p.np * kBlock) - 1);
+        bool ok = true;
+        int gt = 0, qn = 0;                               // key tiles and Q tiles
+        for (int n = 0; ok; ++n) {
+            const Piece* p = piece_at(n);
+            if (!p || p->end) break;
+            // (not before the last piece's last V: the other row tile's old Q is given back only behind that)
 #pragma unroll 1
-                for (; v <= z; ++v) {
-                    const bool has = see.has(v) || (tree && v >= p.L - p.Q &&
-                                                    (tree_bits(tree, a.tree_words, v - (p.L - p.Q), p.Q) & 1u));
-                    if (!has) continue;
-                    const int id = a.tables[(int64_t)p.b * a.max_blocks + p.page(v / kBlock)];
-                    if (id < 0 || id >= a.num_blocks) continue;
-                    const uint8_t* page = a.v_cache + ((int64_t)id * a.Hkv + p.g + hw) * K::LAND;
-                    const int off = v % kBlock;
+            for (int i = 0; FP8 && i < (p->two ? 2 : 1) && ok; ++i, ++qn) {
+                ok = wait_all(bar(K::QFULL + (qn & 1)), (qn >> 1) & 1);
+                if (ok) ready_q(qn);
+            }
+            const int tiles = p->tiles();
 #pragma unroll 1
-                    for (int d = 0; d < D; ++d) {
-                        float f;
-                        if constexpr (FP8) {
-                            const uint8_t code = page[((off / 8) * (D / 16) + d / 16) * 128 + (off % 8) * 16 + d % 16];
-                            f = (code & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
-                        } else {
-                            f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-                                page + ((off / 8) * (D / 8) + d / 8) * 128 + (off % 8) * 16 + (d % 8) * 2));
-                        }
-                        if (fabsf(f) < INFINITY) continue;
-                        if (part) {
-                            part[(size_t)(d / 4) * 2 * kRows * 4 + d % 4] += f;
-                        } else {
-                            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out) + d;
-                            *o = __float2bfloat16_rn(__bfloat162float(*o) + f);
-                        }
-                    }
-                }
-            };
-            if (HG > 1) {
-                span(0, p.np * kBlock);
-            } else {
-                span(gd.wl_any, gd.wl_all - 1);
-                span(gd.wh_all + 1, gd.wh_any);
+            for (int x = 0; x < tiles && ok; ++x, ++gt) {
+                if (!(ok = wait_all(bar(K::VFULL + gt % NSV), (gt / NSV) & 1))) break;
+                ready_v(*p, n, x, gt);
             }
-        };
-        // the weight of a part with reference m and sum l beside the largest reference `top` of the parts.  (A part
-        // that saw nothing holds zeros, or NaN)
-        auto weight = [](float m, float l, float top) {
-            return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - top);
-        };
-        auto finish_lse = [](float m, float l) {
-            return m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
-        };
-        // The epilogue of piece n.  (In loops, one copy: it runs once a piece, from an instruction cache that holds the
-        // inner loops by then.)
-        auto epilogue = [&](const Piece& p, int n) {
-            const bool whole = p.parts == 1, both = !p.two && p.count(1) > 0;          // both: the chains share a row
-            float* slot = part_slot<D>(a, blockIdx.x, p.t0 == 0);
-            tc_fence_after();
-#pragma unroll 1
-            for (int i = 0; i < (p.two ? 2 : 1); ++i) {
-                const int qi = i * a.pb + pos;
-                const bool row_ok = pos < a.pb && qi < p.nq;
-                if (__any_sync(0xffffffffu, row_ok)) {
-                    const uint32_t oa = tmem + lbase + K::COL_O + (p.two ? i * D : 0), ob = tmem + lbase + K::COL_O + D;
-                    uint32_t x[32];
-                    tmem_ld32_async(oa, x);
-                    const float* mla = ml + (p.two ? 2 * i : 0) * kRows;
-                    float m = mla[r], l = mla[kRows + r], fa = 1.f, fb = 0.f;
-                    if (both) {
-                        const float m1 = ml[2 * kRows + r], l1 = ml[3 * kRows + r], top = fmaxf(m, m1);
-                        fa = weight(m, l, top);
-                        fb = weight(m1, l1, top);
-                        l = l * fa + l1 * fb;
-                        if (m == -INFINITY) fa = 1.f;
-                        if (m1 == -INFINITY) fb = 1.f;
-                        m = top;
-                    }
-                    const bool none = m == -INFINITY && l == 0.f;          // a row that saw nothing
-                    const int64_t row = p.row + p.q0 + qi;
-                    const int h = (p.g + hw) * G + hl;
-                    uint8_t* dst = row_ok ? a.out.row(row, h) : nullptr;
-                    float* part = slot + (i * kRows + r) * 4;
-                    if (row_ok && !whole) {
-                        slot[(size_t)2 * kRows * D + i * kRows + r] = m;
-                        slot[(size_t)2 * kRows * (D + 1) + i * kRows + r] = l;
-                    } else if (row_ok && a.lse) {
-                        a.lse[row * a.Hq + h] = finish_lse(m, l);
-                    }
-                    const float inv = none ? 0.f : 1.f / l;
-                    if (whole) {
-                        fa *= inv;
-                        fb *= inv;
-                    }
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        tmem_wait_ld_into(x);
-                        if (both) {
-                            uint32_t y[32];
-                            tmem_ld32_async(ob + c, y);
-                            tmem_wait_ld_into(y);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa + __uint_as_float(y[e]) * fb;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa;
-                        }
-                        tmem_ld32_async(oa + min(c + 32, D - 32), x);      // (behind the last, for nothing)
-                        if (row_ok && whole) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint32_t v[4];
-#pragma unroll
-                                for (int f = 0; f < 4; ++f) v[f] = none ? 0u : pack_bf16(o[e + 2 * f], o[e + 2 * f + 1]);
-                                *reinterpret_cast<uint4*>(dst + (c + e) * 2) = make_uint4(v[0], v[1], v[2], v[3]);
-                            }
-                        } else if (row_ok) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4*>(part + (size_t)((c + e) / 4) * 2 * kRows * 4) =
-                                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                        }
-                        __syncwarp();
-                    }
-                    tmem_wait_ld_into(x);
-                    if (row_ok && nonfinite[n % kFlags] == n + 1) add_back(p, qi, dst, whole ? nullptr : part);
-                }
-                // O read: the next piece's first PV may overwrite it
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(K::OFREE + (p.two ? i : 0)));
-                    if (both) mbar_arrive(bar(K::OFREE + 1));
-                }
-            }
-            if (whole) return;
-            // The part is in memory: the last of the item's CTAs to get here (for these 32 lanes' rows) joins them, in order.
-            __threadfence();
-            __syncwarp();
-            int old = 0;
-            int* ticket = a.tickets + p.c0 * 4 + w;
-            if (lane == 0) old = atom_add_acq_rel_gpu(ticket, 1);
-            if (__shfl_sync(0xffffffffu, old, 0) != p.parts - 1) return;
-            if (lane == 0) *ticket = 0;
-            fence_acquire_gpu();
-#pragma unroll 1
-            for (int i = 0; i < (p.two ? 2 : 1); ++i) {
-                const int mine = min(32, min(a.pb, p.nq - i * a.pb) * G - (w * 32) % RQ);      // valid rows among the lanes
-                if (mine <= 0) continue;
-#pragma unroll 1
-                for (int y = lane; y < mine * (D / 8); y += 32) {
-                    const int R = w * 32 + y % mine, c = y / mine * 8;
-                    const int rp = R % RQ / G;
-                    auto at = [&](int x) { return part_slot<D>(a, p.c0 + x, x == 0); };
-                    float top = -INFINITY;
-#pragma unroll 4
-                    for (int x = 0; x < p.parts; ++x) top = fmaxf(top, __ldcg(at(x) + (size_t)2 * kRows * D + i * kRows + R));
-                    float l = 0.f, o[8] = {};
-#pragma unroll 2
-                    for (int x = 0; x < p.parts; ++x) {
-                        const float* s = at(x);
-                        const float mx = __ldcg(s + (size_t)2 * kRows * D + i * kRows + R);
-                        const float lx = __ldcg(s + (size_t)2 * kRows * (D + 1) + i * kRows + R);
-                        const float4 u0 = __ldcg(reinterpret_cast<const float4*>(s + ((size_t)(c / 4) * 2 * kRows + i * kRows + R) * 4));
-                        const float4 u1 = __ldcg(reinterpret_cast<const float4*>(s + ((size_t)(c / 4 + 1) * 2 * kRows + i * kRows + R) * 4));
-                        float f = weight(mx, lx, top);
-                        l += f * lx;
-                        if (mx == -INFINITY) f = 1.f;
-                        o[0] = fmaf(u0.x, f, o[0]);
-                        o[1] = fmaf(u0.y, f, o[1]);
-                        o[2] = fmaf(u0.z, f, o[2]);
-                        o[3] = fmaf(u0.w, f, o[3]);
-                        o[4] = fmaf(u1.x, f, o[4]);
-                        o[5] = fmaf(u1.y, f, o[5]);
-                        o[6] = fmaf(u1.z, f, o[6]);
-                        o[7] = fmaf(u1.w, f, o[7]);
-                    }
-                    const bool none = top == -INFINITY && l == 0.f;
-                    const float il = none ? 0.f : 1.f / l;
-                    const int64_t orow = p.row + p.q0 + i * a.pb + rp;
-                    const int oh = (p.g + hw) * G + R % RQ - rp * G;
-                    uint32_t v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = none ? 0u : pack_bf16(o[2 * e] * il, o[2 * e + 1] * il);
-                    *reinterpret_cast<uint4*>(a.out.row(orow, oh) + c * 2) = make_uint4(v[0], v[1], v[2], v[3]);
-                    if (c == 0 && a.lse) a.lse[orow * a.Hq + oh] = finish_lse(top, l);
-                }
-            }
-        };
-
-        // Each job when its input is there, none waited for while another may run: the next piece's tiles are made ready
-        // while the last piece's results are awaited, and its products wait for that epilogue.
-        int rp = 0, rx = 0, rg = 0;                       // the piece, its tile, and the CTA's tile to make ready
-        int qp = 0, qn = 0, qi = 0;                       // (FP8) the piece, the CTA's Q tile and the piece's to make ready
-        bool last = false, known = false;                 // no piece behind rp; piece rp is there
-        int ep = 0;                                       // the piece to finish
-        uint32_t phase = 0;                               // of either chain's pieces, as bits
-        uint64_t since = 0;
-        uint32_t spins = 0;
-        auto there = [&](uint32_t bb, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bb, parity)); };
-        for (;;) {
-            bool moved = false;
-            if (FP8 && qp <= rp + 1 && there(bar(K::PCFULL + qp % kPieces), (qp / kPieces) & 1) && !ring[qp % kPieces].end &&
-                there(bar(K::QFULL + (qn & 1)), (qn >> 1) & 1)) {
-                ready_q(qn++);
-                if (++qi == (ring[qp % kPieces].two ? 2 : 1)) {
-                    qi = 0;
-                    ++qp;
-                }
-                moved = true;
-            }
-            if (!last) {
-                if (!known && there(bar(K::PCFULL + rp % kPieces), (rp / kPieces) & 1)) {
-                    known = true;
-                    if (ring[rp % kPieces].end) last = true;
-                }
-                if (known && !last && there(bar(K::VFULL + rg % NSV), (rg / NSV) & 1)) {
-                    const Piece& p = ring[rp % kPieces];
-                    ready_v(p, rp, rx, rg++);
-                    if (++rx == p.tiles()) {
-                        rx = 0;
-                        ++rp;
-                        known = false;
-                    }
-                    moved = true;
-                }
-            }
-            if (ep < rp) {
-                const Piece& p = ring[ep % kPieces];
-                const bool c1 = p.count(1) > 0;           // (chain 0 always has tiles)
-                if (there(bar(K::ODONE), phase & 1) && there(bar(K::LREADY), phase & 1) &&
-                    (!c1 || (there(bar(K::ODONE + 1), phase >> 1 & 1) && there(bar(K::LREADY + 1), phase >> 1 & 1)))) {
-                    epilogue(p, ep);
-                    phase ^= c1 ? 3u : 1u;
-                    release(ep++);
-                    moved = true;
-                }
-            } else if (last) {
-                break;
-            }
-            if (moved) {
-                since = 0;
-                spins = 0;
-                continue;
-            }
-            if ((++spins & 63) == 0) {
-                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-                const uint64_t now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
-                if (since == 0) since = now;
-                if (now - since > a.wait_limit_ns) {
-                    if (lane == 0) {
-                        raise_error(a.err, PKV_DEVERR_TIMEOUT);
-                        *abort_flag = 1;
-                    }
-                    break;
-                }
-            }
-            __nanosleep(20);
+            release(n);
         }
     } else {
         regs_dec<kRegsOther>();
@@ -1208,14 +1163,22 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             Piece p = {};
             p.end = !plan.next(p);
             enter();
+            // every warp is done with piece x: the only wait that keeps the time
+            const Ctl clock{abort_flag, a.err, a.wait_limit_ns};
+            auto done = [&](int x) -> bool {
+                return __all_sync(0xffffffffu, wait(bar(K::PCEMPTY + x % kPieces), (x / kPieces) & 1, clock));
+            };
             for (int n = 0;; ++n) {
-                if (n >= kPieces && !wait_all(bar(K::PCEMPTY + n % kPieces), ((n - kPieces) / kPieces) & 1)) break;
+                if (n >= kPieces && !done(n - kPieces)) break;
                 if (lane == 0) {
                     ring[n % kPieces] = p;
                     mbar_arrive(bar(K::PCFULL + n % kPieces));
                 }
                 __syncwarp();
-                if (p.end) break;
+                if (p.end) {
+                    for (int x = max(n - kPieces, 0); x < n && done(x); ++x) {}
+                    break;
+                }
                 p.end = !plan.next(p);
             }
         } else if (warp == kProducer) {
@@ -1281,7 +1244,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     const float s1 = scale_of(id1);
                     const int64_t src = ((int64_t)id * a.Hkv + g) * K::LAND;
                     if (nt >= NSK && !(ok = wait_all(bar(K::KEMPTY + sk), ((nt - NSK) / NSK) & 1))) break;
-                    if (FP8 && lane < 16) scales[(nt % K::NSC) * 16 + lane] = s;
+                    if (FP8 && lane < 16) scales[(nt % K::NSC) * 16 + lane] = is_v && !(fabsf(s) < INFINITY) ? 1.f : s;
+                    if (FP8 && lane < 16 && is_v) v_finite[(nt % K::NSC) * 8 + u8] = fabsf(s) < INFINITY;
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(bar(K::KFULL + sk), pages * HG * K::LAND);
                     __syncwarp();
@@ -1325,12 +1289,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             const uint32_t o_i = tm + K::COL_O + __shfl_sync(0xffffffffu, i, 0) * D;
             constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(kRows, kCols) : idesc_bf16_f32(kRows, kCols, false, false);
             constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true);
-            int pcnt = 0, ocnt = 0, turn = 0;             // this chain's tiles and pieces; turns
+            int pcnt = 0, bcnt = 0, turn = 0;             // this chain's tiles; pieces of both chains; turns
             int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
             int kn = 0, vn = 0, qn = 0;                   // K, V and Q tiles seen: every one, in order, by both chains (a
                                                           // barrier's parity tells neighbouring phases apart, no more)
             struct Work {
-                int cnt, x0, step, t0, two, ends;
+                int cnt, x0, step, t0, two, both, ends;
                 int base, q;                              // the CTA's numbers of its first tile and of the chain's Q tile
             };
             // up to tile `upto`: what the other chain alone uses is given back as soon as it is there
@@ -1362,6 +1326,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     x.step = at->step();
                     x.t0 = at->t0;
                     x.two = at->two;
+                    x.both = !at->two && at->count(1) > 0;
                     x.ends = at->seen_end(a, min(at->nq, at->two ? (i + 1) * a.pb : a.pb));
                     x.base = tbase;
                     x.q = qbase + (at->two ? i : 0);
@@ -1417,8 +1382,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 const int gt = p.base + p.x0 + j * p.step, sv = gt % NSV;
                 if (now) {
                     if (!see_v(gt)) break;
-                    // a piece's first PV starts O afresh: the last one's result has been read
-                    if (j == 0 && ocnt > 0 && !wait_all(bar(K::OFREE + i), (ocnt - 1) & 1)) break;
+                    // a piece's first PV starts O afresh: the other chain too has read the last result that they shared
+                    if (j == 0 && bcnt > 0 && !wait_all(bar(K::OFREE), (bcnt - 1) & 1)) break;
                 }
                 // (what the next S needs is waited for before P, off the path from P to it)
                 if (then && ((fresh && !see_q(q.q)) || !see_k(q.base + q.x0 + jq * q.step))) break;
@@ -1445,7 +1410,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     if (!ok) break;
                     if (j + 1 == p.cnt) {
                         commit(lead, bar(K::ODONE + i));
-                        ++ocnt;
+                        bcnt += p.both;
                     }
                     commit(lead, bar(K::VEMPTY + sv));
                     ++pcnt;
@@ -1483,7 +1448,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
 // ------------------------------------------------------------------ host
 
 constexpr size_t kTicketOff = 256;         // behind the error word
-constexpr size_t kPartOff = kTicketOff + (size_t)kMaxCtas * 4 * sizeof(int);
+constexpr size_t kPartOff = kTicketOff + (size_t)kMaxCtas * 8 * sizeof(int);
 
 template <int D, bool FP8, int HG>
 cudaError_t launch(const Arg& a, unsigned grid, cudaStream_t st) {

@@ -37,6 +37,19 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c
     return wait_spin(bar, parity, c.abort, c.err, c.limit);
 }
 
+// mbar_try_wait that may sleep for so many nanoseconds.
+__device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred P1;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n"
+        "selp.b32 %0, 1, 0, P1;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+
 // A box of a 3-D tensor (dim, head, token) -> shared memory.
 __device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap* map, int d, int h, int t, uint32_t bar) {
     asm volatile(

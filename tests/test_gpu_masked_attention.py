@@ -109,6 +109,20 @@ def test_tree(case, dtype, workspace):
     check(out, lse, s.reference())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("q_lens,ctx,heads", [([120, 77, 1, 64, 65] * 8, 300, 16), ([3, 1, 8, 2] * 20, 600, 16),
+                                              ([1] * 300, 90, 32), ([40, 7] * 30, 100, 56)])
+def test_many_items_a_cta(q_lens, ctx, heads, dtype, workspace):
+    """Several items in a row on every CTA, of one and two row tiles, of one key tile and of many."""
+    rnd = random.Random(len(q_lens))
+    lens = [q + rnd.randint(0, ctx) for q in q_lens]
+    s = windowed(lens, q_lens, 150, 4, heads=heads, kv_heads=8, dim=64, dtype=dtype, seed=3)
+    out, lse = run_window(s, 150, 4, workspace)
+    check(out, lse, s.reference())
+    again = run_window(s, 150, 4, workspace)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random(seed, workspace):
     rnd = random.Random(seed)
