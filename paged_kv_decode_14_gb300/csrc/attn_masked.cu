@@ -64,8 +64,11 @@ constexpr int kReady = 8, kProducer = 12, kMma = 13, kPlan = 15;
 constexpr int kPieces = 4;                 // pieces of work planned ahead
 constexpr int kFlags = 8;                  // pieces whose "non-finite V" flags are kept
 constexpr int kMaxCtas = 160;              // CTAs of a launch (two workspace slots each)
-constexpr int kItemUnits = 2;              // what an item costs beside its key tiles, in key tiles of one row tile
+// what an item costs beside its key tiles, in key tiles of one row tile
+template <int HG>
+constexpr int kItemUnits = HG == 1 ? 4 : 2;
 constexpr uint32_t kWaitHint = 20000;     // ns that a wait may sleep before it looks at the abort flag
+constexpr int kAhead = 3;                  // tiles that an FP8 page's scales are fetched ahead
 constexpr int kMinUnits = 4;               // units that a CTA has at least
 
 struct Arg {
@@ -175,8 +178,8 @@ struct Cfg {
     static constexpr int VTILE = kUnits * PAGE;           // (FP8: a page lands in the upper half of its place)
     static constexpr int NSK = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 5);     // K ring depth
     static constexpr int NSV = D == 128 ? 3 : FP8 ? 6 : 5;                        // V ring depth
-    static constexpr int NSC = 8;                         // scale ring: a tile's are read until its V slot is free
-    static_assert(NSC > NSV, "scale ring");
+    static constexpr int NSC = D == 128 ? 8 : 16;         // scale ring: a tile's are read until its V slot is free
+    static_assert(NSC > NSV + kAhead, "scale ring");
     static constexpr int NQS = 4;                         // ring of the rows' powers of two (FP8)
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + 2 * QTILE;
@@ -194,8 +197,7 @@ struct Cfg {
     static constexpr int OFF_PIECE = OFF_ML + 4 * 4 * kRows;
     static constexpr int OFF_SC = OFF_PIECE + kPieces * (int)sizeof(Piece);       // FP8: float[NSC][k scales 8, v scales 8]
     static constexpr int OFF_QS = OFF_SC + (FP8 ? NSC * 64 : 0);                  // FP8: float[NQS][kRows]
-    static constexpr int OFF_VF = OFF_QS + (FP8 ? NQS * 4 * kRows : 0);           // FP8: bool[NSC][8], a unit's v scale is finite
-    static constexpr int SMEM = OFF_VF + (FP8 ? NSC * 8 : 0);
+    static constexpr int SMEM = OFF_QS + (FP8 ? NQS * 4 * kRows : 0);
     static constexpr int COL_O = 2 * kCols;
     static constexpr int TMEM_COLS = 512;
     static_assert(OFF_PIECE % 8 == 0, "alignment");
@@ -253,7 +255,7 @@ struct Plan {
         }
         tiles = (p.np + TP - 1) / TP;
         each = HG == 1 && p.nq > a.pb ? 2 : 1;
-        return tiles * each + kItemUnits;
+        return tiles * each + kItemUnits<HG>;
     }
     template <typename V>
     __device__ __forceinline__ V scan(V x) const {        // the sum over earlier lanes
@@ -272,12 +274,16 @@ struct Plan {
         return (in ? 0 : longer) + (int)((uint32_t)(in ? unit : unit - head) / (uint32_t)(in ? share + 1 : share));
     }
     __device__ __forceinline__ void begin() {
-        const int chunk = (a.num_seqs + 31) / 32, b0 = min(lane * chunk, a.num_seqs), b1 = min(b0 + chunk, a.num_seqs);
+        // a lane stands for some sequences, or where there are few, `each_seq` lanes for one, with equal shares of its blocks
+        const int chunk = (a.num_seqs + 31) / 32;
+        const int lg = a.num_seqs > 16 ? 0 : 5 - (32 - __clz(a.num_seqs - 1)), each_seq = 1 << lg, seg = lane & (each_seq - 1);
+        const int b0 = min((lane >> lg) * chunk, a.num_seqs), b1 = min(b0 + chunk, a.num_seqs);
         int64_t rows = 0;
         if (!a.q_starts) {
 #pragma unroll 1
             for (int i = b0; i < b1; ++i) rows += max(a.q_lens[i], 0);
-            rows = scan(rows);
+            rows = scan(seg == 0 ? rows : (int64_t)0);
+            rows = __shfl_sync(0xffffffffu, rows, lane - seg);
         }
         // units of this lane's sequences; the second time, the item of them that holds unit `u`
         int64_t mine = 0, before = 0;
@@ -293,8 +299,9 @@ struct Plan {
 #pragma unroll 1
                 for (int i = b0; i < b1 && !found; ++i) {
                     const Seq x = load(i, at, turn == 0);
+                    const int n = (x.Q + per() - 1) / per(), some = (n + each_seq - 1) >> lg;
 #pragma unroll 1
-                    for (int k = 0; k * per() < x.Q && !found; ++k) {
+                    for (int k = seg * some; k < min((seg + 1) * some, n) && !found; ++k) {
                         Piece p;
                         int tiles, each;
                         const int w = span(x, k, p, tiles, each);
@@ -345,7 +352,7 @@ struct Plan {
         while (u < u1 && !some) {
             int tiles, each;
             const int w = span(s, blk, p, tiles, each);
-            const int keys = start + kItemUnits;          // the first tile's first unit
+            const int keys = start + kItemUnits<HG>;          // the first tile's first unit
             auto tile_at = [&](int x) { return x <= keys ? 0 : min(tiles, (x - keys + each - 1) >> (each - 1)); };
             p.t0 = tile_at(u);
             p.t1 = tile_at(u1);
@@ -439,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
     float* ml = reinterpret_cast<float*>(smem + K::OFF_ML);
     float* scales = reinterpret_cast<float*>(smem + K::OFF_SC);
     float* q_scale = reinterpret_cast<float*>(smem + K::OFF_QS);
-    uint8_t* v_finite = smem + K::OFF_VF;
     Piece* ring = reinterpret_cast<Piece*>(smem + K::OFF_PIECE);
     // every wait and every TMEM access is warp-uniform (tcgen05.ld / st are .aligned)
     // (Their limit is kept by the plan's warp, which waits for every piece's end: where one takes that long it sets the abort
@@ -587,10 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         // the weight of a part with reference m and sum l beside the largest reference `top` of the parts.  (A part
         // that saw nothing holds zeros, or NaN)
         auto weight = [](float m, float l, float top) {
-            return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - top);
+            return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2_fast(m - top);
         };
         auto finish_lse = [](float m, float l) {
-            return m == -INFINITY && l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945f;
+            return m == -INFINITY && l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.693147180559945f;
         };
         // The results of piece n: part ct of its rows' results (two row tiles: row tile ct; one: columns from ct * D / 2 on), from
         // this chain's O or (both) from both.  (In loops, one copy: it runs once a piece, from an instruction cache
@@ -603,8 +609,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             if (!__any_sync(0xffffffffu, row_ok)) return;
             const int d0 = p.two ? 0 : ct * (D / 2), d1 = p.two ? D : d0 + D / 2;
             const uint32_t oa = tmem + lbase + K::COL_O + (both ? 0 : i * D), ob = tmem + lbase + K::COL_O + D;
-            uint32_t x[32];
-            tmem_ld32_async(oa + d0, x);
             float fa = 1.f, fb = 0.f;
             if (both) {
                 const float m0 = ml[r], l0 = ml[kRows + r], m1 = ml[2 * kRows + r], l1 = ml[3 * kRows + r];
@@ -626,33 +630,33 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             } else if (row_ok && a.lse && (p.two || ct == 0)) {
                 a.lse[row * a.Hq + h] = finish_lse(m, l);
             }
-            const float inv = none ? 0.f : 1.f / l;
+            const float inv = none ? 0.f : __fdividef(1.f, l);
             if (whole) {
                 fa *= inv;
                 fb *= inv;
             }
+            uint32_t x[32], y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) y[e] = 0;
+            tmem_ld32_async(oa + d0, x);
 #pragma unroll 1
             for (int c = d0; c < d1; c += 32) {
-                float o[32];
-                tmem_wait_ld_into(x);
                 if (both) {
-                    uint32_t y[32];
                     tmem_ld32_async(ob + c, y);
                     tmem_wait_ld_into(y);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa + __uint_as_float(y[e]) * fb;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa;
                 }
+                tmem_wait_ld_into(x);
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(x[e]) * fa + __uint_as_float(y[e]) * fb;
                 tmem_ld32_async(oa + min(c + 32, D - 32), x);      // (behind the last, for nothing)
                 if (row_ok && whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t v[4];
 #pragma unroll
-                        for (int f = 0; f < 4; ++f) v[f] = none ? 0u : pack_bf16(o[e + 2 * f], o[e + 2 * f + 1]);
-                        *reinterpret_cast<uint4*>(dst + (c + e) * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+                        for (int f = 0; f < 4; ++f) v[f] = pack_bf16(o[e + 2 * f], o[e + 2 * f + 1]);
+                        *reinterpret_cast<uint4*>(dst + (c + e) * 2) = none ? make_uint4(0, 0, 0, 0) : make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 } else if (row_ok) {
 #pragma unroll
@@ -679,43 +683,54 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             if (__shfl_sync(0xffffffffu, old, 0) != p.parts - 1) return;
             if (lane == 0) *ticket = 0;
             fence_acquire_gpu();
-            const int d0 = p.two ? 0 : ct * (D / 2), n8 = (p.two ? D : D / 2) / 8, rt = p.two ? ct * kRows : 0;
-#pragma unroll 1
-            for (int y = lane; y < mine * n8; y += 32) {
-                const int R = w * 32 + y % mine, c = d0 + y / mine * 8, rp = R % RQ / G;
-                auto at = [&](int x) { return part_slot<D>(a, p.c0 + x, x == 0); };
-                float top = -INFINITY;
-#pragma unroll 4
-                for (int x = 0; x < p.parts; ++x) top = fmaxf(top, __ldcg(at(x) + (size_t)2 * kRows * D + ct * kRows + R));
-                float l = 0.f, o[8] = {};
+            // Lanes are rows, or where there are few, rows times groups of columns; eight 16-byte pieces of a part in flight.
+            const int d0 = p.two ? 0 : ct * (D / 2), n4 = (p.two ? D : D / 2) / 4, rt = p.two ? ct * kRows : 0;
+            const int lg = 32 - __clz(mine - 1), R = w * 32 + (lane & ((1 << lg) - 1)), rp = R % RQ / G;
+            if (R >= w * 32 + mine) return;
+            auto at = [&](int x) { return part_slot<D>(a, p.c0 + x, x == 0); };
+            auto m_of = [&](int x) { return __ldcg(at(x) + (size_t)2 * kRows * D + ct * kRows + R); };
+            auto l_of = [&](int x) { return __ldcg(at(x) + (size_t)2 * kRows * (D + 1) + ct * kRows + R); };
+            float top = -INFINITY, l = 0.f;
 #pragma unroll 2
+            for (int x = 0; x < p.parts; ++x) top = fmaxf(top, m_of(x));
+#pragma unroll 2
+            for (int x = 0; x < p.parts; ++x) {
+                const float lx = l_of(x);
+                l += weight(m_of(x), lx, top) * lx;
+            }
+            const bool none = top == -INFINITY && l == 0.f;
+            const float il = none ? 0.f : __fdividef(1.f, l);
+            const int64_t orow = p.row + p.q0 + (p.two ? ct * a.pb : 0) + rp;
+            const int oh = (p.g + hw) * G + R % RQ - rp * G, step = 32 >> lg;
+            uint8_t* dst = a.out.row(orow, oh);
+            if (lane >> lg == 0 && a.lse && (p.two || ct == 0)) a.lse[orow * a.Hq + oh] = finish_lse(top, l);
+#pragma unroll 1
+            for (int q0 = lane >> lg; q0 < n4; q0 += 8 * step) {
+                float o[32] = {};
+#pragma unroll 1
                 for (int x = 0; x < p.parts; ++x) {
-                    const float* s = at(x);
-                    const float mx = __ldcg(s + (size_t)2 * kRows * D + ct * kRows + R);
-                    const float lx = __ldcg(s + (size_t)2 * kRows * (D + 1) + ct * kRows + R);
-                    const float4 u0 = __ldcg(reinterpret_cast<const float4*>(s + ((size_t)(c / 4) * 2 * kRows + rt + R) * 4));
-                    const float4 u1 = __ldcg(reinterpret_cast<const float4*>(s + ((size_t)(c / 4 + 1) * 2 * kRows + rt + R) * 4));
-                    float f = weight(mx, lx, top);
-                    l += f * lx;
-                    if (mx == -INFINITY) f = 1.f;
-                    o[0] = fmaf(u0.x, f, o[0]);
-                    o[1] = fmaf(u0.y, f, o[1]);
-                    o[2] = fmaf(u0.z, f, o[2]);
-                    o[3] = fmaf(u0.w, f, o[3]);
-                    o[4] = fmaf(u1.x, f, o[4]);
-                    o[5] = fmaf(u1.y, f, o[5]);
-                    o[6] = fmaf(u1.z, f, o[6]);
-                    o[7] = fmaf(u1.w, f, o[7]);
-                }
-                const bool none = top == -INFINITY && l == 0.f;
-                const float il = none ? 0.f : 1.f / l;
-                const int64_t orow = p.row + p.q0 + (p.two ? ct * a.pb : 0) + rp;
-                const int oh = (p.g + hw) * G + R % RQ - rp * G;
-                uint32_t v[4];
+                    const float mx = m_of(x), f = mx == -INFINITY ? 1.f : weight(mx, 0.f, top);
+                    const float4* s = reinterpret_cast<const float4*>(at(x)) + (size_t)(d0 / 4) * 2 * kRows + rt + R;
+                    float4 u[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = none ? 0u : pack_bf16(o[2 * e] * il, o[2 * e + 1] * il);
-                *reinterpret_cast<uint4*>(a.out.row(orow, oh) + c * 2) = make_uint4(v[0], v[1], v[2], v[3]);
-                if (c == 0 && a.lse) a.lse[orow * a.Hq + oh] = finish_lse(top, l);
+                    for (int e = 0; e < 8; ++e)
+                        if (q0 + e * step < n4) u[e] = __ldcg(s + (size_t)(q0 + e * step) * 2 * kRows);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (q0 + e * step < n4) {
+                            o[4 * e] = fmaf(u[e].x, f, o[4 * e]);
+                            o[4 * e + 1] = fmaf(u[e].y, f, o[4 * e + 1]);
+                            o[4 * e + 2] = fmaf(u[e].z, f, o[4 * e + 2]);
+                            o[4 * e + 3] = fmaf(u[e].w, f, o[4 * e + 3]);
+                        }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (q0 + e * step < n4) {
+                        uint2 v = make_uint2(0, 0);
+                        if (!none) v = make_uint2(pack_bf16(o[4 * e] * il, o[4 * e + 1] * il), pack_bf16(o[4 * e + 2] * il, o[4 * e + 3] * il));
+                        *reinterpret_cast<uint2*>(dst + (d0 + (q0 + e * step) * 4) * 2) = v;
+                    }
             }
         };
         constexpr int STEP = K::KEYS < 64 ? K::KEYS : 64; // keys whose P is written at once
@@ -852,7 +867,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                             if ((y >> 1) & 1) cb = f2add(cb, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
                             else ca = f2add(ca, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
                             if constexpr (FP8) {
-                                const float vs = ks[8 + pg * HG];
+                                float vs = ks[8 + pg * HG];
+                                vs = fabsf(vs) < INFINITY ? vs : 1.f;       // (V has no finite values then)
                                 over |= __float_as_uint(p0) | __float_as_uint(p1);
                                 p0 *= vs;
                                 p1 *= vs;
@@ -980,8 +996,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         // heads' rows have weight 0 for them) and are added back, row by row, in the epilogue (from global memory:
         // rare).
         // (FP8) `pages` of the two pages of V from `at` on, each in the upper half of its place and widened over it; their
-        // first keys at v and v1.  finite: of either page's scale; where it is not, all its codes count as NaN (its scale, as 1)
-        auto widen_pages = [&](uint8_t* at, const Guard<HG>& gd, int v, int v1, int pages, const uint8_t* finite) -> bool {
+        // first keys at v and v1.  vs: their scales; where one is not finite, all its page's codes count as NaN (and it, as 1)
+        auto widen_pages = [&](uint8_t* at, const Guard<HG>& gd, int v, int v1, int pages, const float* vs) -> bool {
             constexpr int N = D / 32;                     // 16-byte chunks of codes a lane and page
             uint4 raw[2 * N];
 #pragma unroll
@@ -994,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 const int q = (lane + 32 * (j % N)) >> 3;
                 return at + j / N * K::PAGE + q / (D / 16) * (K::NCH * 128) + 2 * (q % (D / 16)) * 128 + (lane & 7) * 16;
             };
-            uint32_t nan = finite[0] == 0 || (pages > 1 && finite[1] == 0);
+            uint32_t nan = 0;                             // a lane's chunks that hold NaN codes
 #pragma unroll
             for (int j = 0; j < 2 * N; ++j) {
                 if (j >= N && pages < 2) break;
@@ -1003,25 +1019,35 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 widen4(raw[j].y, o[2], o[3]);
                 widen4(raw[j].z, o[4], o[5]);
                 widen4(raw[j].w, o[6], o[7]);
-                nan |= nan_codes(raw[j].x) | nan_codes(raw[j].y) | nan_codes(raw[j].z) | nan_codes(raw[j].w);
+                if (nan_codes(raw[j].x) | nan_codes(raw[j].y) | nan_codes(raw[j].z) | nan_codes(raw[j].w)) nan |= 1u << j;
                 *reinterpret_cast<uint4*>(place(j)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(place(j) + 128) = make_uint4(o[4], o[5], o[6], o[7]);
             }
+            const bool fin0 = fabsf(vs[0]) < INFINITY, fin1 = pages < 2 || fabsf(vs[1]) < INFINITY;
+            if (!gd.any_of(v, kBlock) || (pages > 1 && !gd.any_of(v1, kBlock))) {
+#pragma unroll 1
+                for (int j = 0; j < pages * N; ++j) {
+                    if (gd.any((j < N ? v : v1) + key_of(j))) continue;
+                    *reinterpret_cast<uint4*>(place(j)) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(place(j) + 128) = make_uint4(0, 0, 0, 0);
+                    nan &= ~(1u << j);
+                }
+            }
             bool found = false;
-            if (nan != 0 || !gd.any_of(v, kBlock) || (pages > 1 && !gd.any_of(v1, kBlock))) {
+            if (nan != 0 || !fin0 || !fin1) {
                 // (rare) a lane's own chunks again: a NaN code is the only one that has become +-480
 #pragma unroll 1
                 for (int j = 0; j < pages * N; ++j) {
                     const int key = (j < N ? v : v1) + key_of(j);
-                    const bool any = gd.any(key), leave = gd.all(key) && finite[j / N];
+                    const bool fin = j < N ? fin0 : fin1, leave = gd.all(key) && fin;
+                    if (!gd.any(key) || ((nan >> j & 1) == 0 && fin)) continue;
                     uint16_t* e = reinterpret_cast<uint16_t*>(place(j));
 #pragma unroll 1
                     for (int y = 0; y < 16; ++y) {
                         uint16_t& x = e[y / 8 * 64 + y % 8];
-                        const bool is_nan = (x & 0x7fff) == 0x43f0 || !finite[j / N];
-                        if (!any || is_nan) x = any && leave ? 0x7fc0 : 0;
-                        found |= any && is_nan && !leave;
+                        if ((x & 0x7fff) == 0x43f0 || !fin) x = leave ? 0x7fc0 : 0;
                     }
+                    found |= !leave;
                 }
             }
             return found;
@@ -1061,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 const int pg = 2 * w / HG, pg1 = (2 * w + 1) / HG;
                 if (pg < pages)
                     found = widen_pages(base + 2 * w * K::PAGE, gd, v0 + pg * kBlock, v0 + pg1 * kBlock, pg1 < pages ? 2 : 1,
-                                        v_finite + gt % K::NSC * 8 + 2 * w);
+                                        scales + gt % K::NSC * 16 + 8 + 2 * w);
                 fence_proxy_async_smem();
             } else {
                 bool touched = false;
@@ -1201,6 +1227,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             }
             ok = __all_sync(0xffffffffu, ok);
             // lanes 0-7 stand for a tile's units of K, 8-15 for those of V
+            // (pages leave L2 first: with them in its way the kernel's own code came from DRAM, 41 us for a decode step against 38)
+            const uint64_t evict = policy_evict_first();
             const int u8 = lane & 7, upg = u8 / HG, uh = u8 % HG;
             const bool is_v = lane >= 8;
             for (int n = 0; ok; ++n) {
@@ -1208,21 +1236,35 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 if (!p || p->end) break;
                 const int32_t* table = a.tables + (int64_t)p->b * a.max_blocks;
                 const int np = p->np, g = p->g + uh;
-                // the block of this lane's unit of tile t (a bad id is reported, and block 0 read in its place)
-                auto block = [&](int t) -> int {
-                    const int idx = t * K::TP + upg;
-                    return lane < 16 && idx < np ? table[p->page(idx)] : 0;
-                };
-                auto checked = [&](int id) -> int {
+                // 32 entries of the list at a time, a lane each (a bad id is reported, and block 0 read in its place)
+                auto blocks = [&](int first) -> int {
+                    const int idx = first + lane;
+                    const int id = idx < min(np, p->t1 * K::TP) ? table[p->page(idx)] : 0;
                     if (id >= 0 && id < a.num_blocks) return id;
                     raise_error(a.err, PKV_DEVERR_BLOCK_ID);
                     return 0;
                 };
-                auto scale_of = [&](int id) -> float {
-                    return FP8 && lane < 16 ? (is_v ? a.v_scales : a.k_scales)[(int64_t)id * a.Hkv + g] : 0.f;
+                const int first = p->t0 * K::TP;
+                int held = first, ids = blocks(first), ids1 = blocks(first + 32);       // entries from `held` on, and the next 32
+                // the block of this lane's unit of tile t, which lies among them
+                auto block = [&](int t) -> int {
+                    const int at = t * K::TP + upg - held;
+                    int id = __shfl_sync(0xffffffffu, ids, at & 31);
+                    if (__any_sync(0xffffffffu, at >= 32)) {
+                        const int x = __shfl_sync(0xffffffffu, ids1, at & 31);
+                        id = at < 32 ? id : x;
+                    }
+                    return id;
                 };
-                // (a tile's block is read two tiles ahead and its scale one, so that neither is waited for)
-                int id = block(p->t0), id1 = p->t0 + 1 < p->t1 ? block(p->t0 + 1) : 0;
+                // (FP8) scales on their way into the ring, kAhead tiles before they are needed
+                auto fetch = [&](int t, int slot) {
+                    if (!FP8) return;
+                    const int id = block(t);
+                    if (lane < 16 && t < p->t1 && t * K::TP + upg < np)
+                        cp_async_4(sb + K::OFF_SC + ((slot % K::NSC) * 16 + lane) * 4,
+                                   (is_v ? a.v_scales : a.k_scales) + (int64_t)id * a.Hkv + g);
+                    asm volatile("cp.async.commit_group;\n" ::: "memory");
+                };
                 for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
                     const int slot = nq & 1;
                     if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
@@ -1234,41 +1276,43 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                                    (p->g + hq) * a.group, (int)(p->row + p->q0 + i * a.pb), bar(K::QFULL + slot));
                     }
                 }
-                id = checked(id);
-                float s = scale_of(id);
+#pragma unroll 1
+                for (int x = 0; x < kAhead; ++x) fetch(p->t0 + x, nt + x);
 #pragma unroll 1
                 for (int t = p->t0; t < p->t1 && ok; ++t, ++nt) {
                     const int sk = nt % NSK, sv = nt % NSV, pages = min(K::TP, np - t * K::TP);
-                    const int id2 = t + 2 < p->t1 ? block(t + 2) : 0;
-                    id1 = checked(id1);
-                    const float s1 = scale_of(id1);
-                    const int64_t src = ((int64_t)id * a.Hkv + g) * K::LAND;
+                    if (t * K::TP - held >= 32) {
+                        held += 32;
+                        ids = ids1;
+                        ids1 = blocks(held + 32);
+                    }
+                    const int64_t src = ((int64_t)block(t) * a.Hkv + g) * K::LAND;
                     if (nt >= NSK && !(ok = wait_all(bar(K::KEMPTY + sk), ((nt - NSK) / NSK) & 1))) break;
-                    if (FP8 && lane < 16) scales[(nt % K::NSC) * 16 + lane] = is_v && !(fabsf(s) < INFINITY) ? 1.f : s;
-                    if (FP8 && lane < 16 && is_v) v_finite[(nt % K::NSC) * 8 + u8] = fabsf(s) < INFINITY;
+                    fetch(t + kAhead, nt + kAhead);
+                    if (FP8) asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead) : "memory");
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(bar(K::KFULL + sk), pages * HG * K::LAND);
                     __syncwarp();
                     // (a page's HG heads lie side by side)
                     if (!is_v && uh == 0 && upg < pages)
-                        bulk_g2s(sb + K::OFF_K + sk * K::KTILE + u8 * K::LAND, a.k_cache + src, HG * K::LAND, bar(K::KFULL + sk));
+                        bulk_g2s_hint(sb + K::OFF_K + sk * K::KTILE + u8 * K::LAND, a.k_cache + src, HG * K::LAND, bar(K::KFULL + sk),
+                                      evict);
                     ++nk;
                     if (nt >= NSV && !(ok = wait_all(bar(K::VEMPTY + sv), ((nt - NSV) / NSV) & 1))) break;
                     if (lane == 0) mbar_arrive_expect_tx(bar(K::VFULL + sv), pages * HG * K::LAND);
                     __syncwarp();
                     if (is_v && lane < 16 && upg < pages) {
                         if (FP8)
-                            bulk_g2s(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE + K::LAND, a.v_cache + src, K::LAND,
-                                     bar(K::VFULL + sv));
+                            bulk_g2s_hint(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE + K::LAND, a.v_cache + src, K::LAND,
+                                          bar(K::VFULL + sv), evict);
                         else if (uh == 0)
-                            bulk_g2s(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE, a.v_cache + src, HG * K::PAGE,
-                                     bar(K::VFULL + sv));
+                            bulk_g2s_hint(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE, a.v_cache + src, HG * K::PAGE,
+                                          bar(K::VFULL + sv), evict);
                     }
                     ++nv;
-                    id = id1;
-                    id1 = id2;
-                    s = s1;
                 }
+                // (what a piece fetched past its end is not read: its slots are the next piece's, fetched again)
+                if (FP8) cp_async_wait_all();
                 release(n);
             }
             if (lane == 0) {
