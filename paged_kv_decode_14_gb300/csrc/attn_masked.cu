@@ -22,9 +22,9 @@
 // tile to work on instead of 128.
 // There are two chains, each with its own S, O, m and l in tensor memory and four softmax warps.  With HG = 1 an item may
 // have two row tiles, one a chain, and every key tile serves both.  Otherwise the chains take the key tiles in turns:
-// while one's softmax runs the other's products do; their O, m and l are joined at the end of the piece.  m is set by a
-// row's first visible keys, four octaves above their maximum; P is computed against it without a maximum, and only where
-// some P reaches 2 (a logit 5 octaves above) m rises.
+// while one's softmax runs the other's products do; their O, m and l are joined at the end of the piece.  m is set by the
+// maximum of a row's first visible keys; P is computed against it without a maximum, and only where the P of 64 keys add
+// up to 2^14 (bf16 has fp32's range) m rises.
 //
 // P is rounded to bf16 (8 significant bits; l is summed from the fp32 P): the error it leaves in out is of the size
 // of out's own rounding to bf16.  fp16 would hold 11 bits, but not V's range.
@@ -35,7 +35,7 @@
 // Work is cut into equal ranges of key tiles over all items, one range per CTA; an item that a range's end cuts leaves
 // partial (O, m, l) in the workspace, and whichever CTA finishes its part last joins them, in the keys' order.
 //
-// Roles (512 threads): warps 0-3 and 4-7 the softmax of chains 0 and 1, and the results; warps 8-11 make V (and, FP8, Q)
+// Roles (512 threads): warps 0-3 and 4-7 the softmax of chains 0 and 1, and the results; warps 8-11 make V
 // ready; warp 12 the producer; warps 13 and 14 the MMA issuers of the chains; warp 15 the plan.  Every wait is bounded.
 #include <cuda.h>
 
@@ -189,7 +189,7 @@ struct Cfg {
                          SFULL = VEMPTY + NSV, PFA = SFULL + 2, PFB = SFULL + 4, QFULL = SFULL + 6, QREADY = SFULL + 8,
                          QEMPTY = SFULL + 10, ODONE = SFULL + 12, OFREE = SFULL + 14, LREADY = SFULL + 16,
                          PVA = SFULL + 18, TURN = SFULL + 20, PCFULL = SFULL + 22, PCEMPTY = PCFULL + kPieces,
-                         DRAIN = PCEMPTY + kPieces;
+                         Q1FULL = PCEMPTY + kPieces, DRAIN = Q1FULL + 1;
     static constexpr int NBAR = DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
     static constexpr int OFF_FLAG = OFF_MISC + 16;        // int[kFlags]
@@ -399,9 +399,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-constexpr float kHeadroom = 4.f;           // octaves of m above the logit it is set by
+constexpr float kHigh = 0x1p14f;           // sum of 64 P at which m rises
 // |m| from which its roundings (half of fp32's step at m each, up to three of them) may leave P, l or O their range:
-// 2^29, three times 16 octaves below it
+// 2^29, three times 16 octaves above kHigh or below 1
 constexpr float kLimit = 0x1p29f;
 
 // Four e4m3 codes as bf16, exactly: the code's exponent and mantissa moved to bf16's places mean the value times
@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         }
         mbar_init(bar(K::OFREE), 8);                      // every softmax warp, after a piece of both chains
         mbar_init(bar(K::LREADY), 8);
+        mbar_init(bar(K::Q1FULL), 1);
         mbar_init(bar(K::DRAIN), 2);
         *abort_flag = 0;
         *drain_flag = 0;
@@ -690,40 +691,50 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             auto at = [&](int x) { return part_slot<D>(a, p.c0 + x, x == 0); };
             auto m_of = [&](int x) { return __ldcg(at(x) + (size_t)2 * kRows * D + ct * kRows + R); };
             auto l_of = [&](int x) { return __ldcg(at(x) + (size_t)2 * kRows * (D + 1) + ct * kRows + R); };
-            float top = -INFINITY, l = 0.f;
-#pragma unroll 2
-            for (int x = 0; x < p.parts; ++x) top = fmaxf(top, m_of(x));
-#pragma unroll 2
-            for (int x = 0; x < p.parts; ++x) {
-                const float lx = l_of(x);
-                l += weight(m_of(x), lx, top) * lx;
-            }
-            const bool none = top == -INFINITY && l == 0.f;
-            const float il = none ? 0.f : __fdividef(1.f, l);
             const int64_t orow = p.row + p.q0 + (p.two ? ct * a.pb : 0) + rp;
             const int oh = (p.g + hw) * G + R % RQ - rp * G, step = 32 >> lg;
             uint8_t* dst = a.out.row(orow, oh);
-            if (lane >> lg == 0 && a.lse && (p.two || ct == 0)) a.lse[orow * a.Hq + oh] = finish_lse(top, l);
 #pragma unroll 1
             for (int q0 = lane >> lg; q0 < n4; q0 += 8 * step) {
-                float o[32] = {};
+                float o[32] = {}, top = -INFINITY, l = 0.f;
 #pragma unroll 1
-                for (int x = 0; x < p.parts; ++x) {
-                    const float mx = m_of(x), f = mx == -INFINITY ? 1.f : weight(mx, 0.f, top);
-                    const float4* s = reinterpret_cast<const float4*>(at(x)) + (size_t)(d0 / 4) * 2 * kRows + rt + R;
-                    float4 u[8];
+                for (int x = 0; x < p.parts; x += 2) {    // two parts' loads in flight
+                    float mx[2], lx[2];
+                    float4 u[2][8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (q0 + e * step < n4) u[e] = __ldcg(s + (size_t)(q0 + e * step) * 2 * kRows);
+                    for (int y = 0; y < 2; ++y) {
+                        const bool is = x + y < p.parts;
+                        const int z = is ? x + y : x;
+                        mx[y] = is ? m_of(z) : -INFINITY;
+                        lx[y] = is ? l_of(z) : 0.f;
+                        const float4* s = reinterpret_cast<const float4*>(at(z)) + (size_t)(d0 / 4) * 2 * kRows + rt + R;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (q0 + e * step < n4) {
-                            o[4 * e] = fmaf(u[e].x, f, o[4 * e]);
-                            o[4 * e + 1] = fmaf(u[e].y, f, o[4 * e + 1]);
-                            o[4 * e + 2] = fmaf(u[e].z, f, o[4 * e + 2]);
-                            o[4 * e + 3] = fmaf(u[e].w, f, o[4 * e + 3]);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            u[y][e] = is && q0 + e * step < n4 ? __ldcg(s + (size_t)(q0 + e * step) * 2 * kRows)
+                                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    const float was = top;
+                    top = fmaxf(top, fmaxf(mx[0], mx[1]));
+                    const float fo = was == -INFINITY ? 1.f : exp2_fast(was - top);
+                    float f[2];
+                    l *= fo;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        f[y] = weight(mx[y], lx[y], top);
+                        l += f[y] * lx[y];
+                        if (mx[y] == -INFINITY) f[y] = 1.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        o[4 * e] = o[4 * e] * fo + u[0][e].x * f[0] + u[1][e].x * f[1];
+                        o[4 * e + 1] = o[4 * e + 1] * fo + u[0][e].y * f[0] + u[1][e].y * f[1];
+                        o[4 * e + 2] = o[4 * e + 2] * fo + u[0][e].z * f[0] + u[1][e].z * f[1];
+                        o[4 * e + 3] = o[4 * e + 3] * fo + u[0][e].w * f[0] + u[1][e].w * f[1];
+                    }
                 }
+                const bool none = top == -INFINITY && l == 0.f;
+                const float il = none ? 0.f : __fdividef(1.f, l);
+                if (q0 == 0 && a.lse && (p.two || ct == 0)) a.lse[orow * a.Hq + oh] = finish_lse(top, l);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (q0 + e * step < n4) {
@@ -733,23 +744,75 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     }
             }
         };
+        // (FP8) this lane's row of Q tile qt, in place: groups of 8 rows are 1024 bytes of a slab; the first term's codes go
+        // where the first slab was (D = 64: to the first half of each 1024 bytes), the second's to the other.
+        auto split_q = [&](int qt) {
+            uint8_t* tile = smem + K::OFF_Q + (qt & 1) * K::QTILE;
+            constexpr int N = D / 8, LO = D == 128 ? K::SLAB : 512;
+            uint32_t top = 0;
+            uint4 x[N];
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                x[c] = *reinterpret_cast<const uint4*>(tile + (c / 8) * K::SLAB + r * 128 + (((c & 7) ^ (r & 7)) * 16));
+                const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, y[e] >> 16 & 0x7fffu));
+            }
+            __syncwarp();
+            // 2^(134 - exponent) takes the largest element to [128, 256); kept inside fp32's normal range (a row below
+            // 2^-113 counts as smaller beside any scale); infinities and NaN make the row NaN
+            const int ex = min(max((int)(top >> 7), 14), 254);
+            const float f = __uint_as_float((uint32_t)(261 - ex) << 23);
+            q_scale[qt % K::NQS * kRows + r] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ex - 7) << 23);
+            uint8_t* dst = tile + (r / 8) * 1024 + (r & 7) * 16;
+#pragma unroll
+            for (int c = 0; c < N / 2; ++c) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 y = x[2 * c + e / 2];
+                    uint32_t h0, h1, l0, l1;
+                    split2(e & 1 ? y.z : y.x, f, h0, l0);
+                    split2(e & 1 ? y.w : y.y, f, h1, l1);
+                    hi[e] = h0 | h1 << 16;
+                    lo[e] = l0 | l1 << 16;
+                }
+                *reinterpret_cast<uint4*>(dst + c * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(dst + LO + c * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            fence_proxy_async_smem();
+        };
         constexpr int STEP = K::KEYS < 64 ? K::KEYS : 64; // keys whose P is written at once
         constexpr bool PAIR = STEP == 64;
         bool ok = true;
         int scnt = 0, tbase = 0, qbase = 0;               // this chain's tiles; the CTA's tiles and Q tiles
         int pieces = 0, pieces1 = 0, bcnt = 0;            // the CTA's pieces; those of chain 1; those of both chains
-        for (int n = 0; ok; ++n) {
+        int q1 = 0;                                       // chain 1: its Q tiles
+        // (FP8) piece n's Q, whose first tile is the CTA's qt-th: chain 0's row tile by its warps, and chain 1's
+        auto ready_q = [&](int n, int qt) {
             const Piece* p = piece_at(n);
-            if (!p || p->end) break;
-            const int cnt = p->count(i), x0 = p->begin(i), step = p->step(), t0 = p->t0;
-            const int base = tbase, qt = qbase + (p->two ? i : 0);
-            tbase += p->tiles();
-            qbase += p->two ? 2 : 1;
-            if (cnt == 0) {
-                ++pieces;
-                release(n);
-                continue;
+            if (!p || p->end || (i == 1 && !p->two)) return;
+            qt += i;
+            ok = i == 0 ? wait_all(bar(K::QFULL + (n & 1)), (n >> 1) & 1) : wait_all(bar(K::Q1FULL), q1 & 1);
+            if (!ok) return;
+            ++q1;
+            if (__any_sync(0xffffffffu, pos < a.pb && (p->two ? i * a.pb : 0) + pos < p->nq)) split_q(qt);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(K::QREADY + (qt & 1)));
+        };
+#pragma unroll 1
+        for (int n = FP8 ? -1 : 0; ok; ++n) {             // (from -1: the first piece's Q, by the one copy of that code)
+            const Piece* p = n < 0 ? nullptr : piece_at(n);
+            if (n >= 0 && (!p || p->end)) break;
+            const int cnt = p ? p->count(i) : 0;
+            const int base = tbase, qt = qbase + (p && p->two ? i : 0);
+            if (p) {
+                tbase += p->tiles();
+                qbase += p->two ? 2 : 1;
             }
+            float m = 0.f, l = 0.f;                       // the reference maximum (exp2 units); the sum of P
+            if (cnt > 0) {
+            const int x0 = p->begin(i), step = p->step(), t0 = p->t0;
             const int qi = (p->two ? i * a.pb : 0) + pos;  // the row's query, from the piece's first on
             const bool row_ok = pos < a.pb && qi < p->nq;
             const bool live = __any_sync(0xffffffffu, row_ok);
@@ -766,8 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             }
             const int tree0 = p->L - p->Q, tree_n = p->Q;
             const int ends = p->seen_end(a, min(p->nq, p->two ? (i + 1) * a.pb : a.pb));
-            // m: the reference maximum (exp2 units), l: the sum of P
-            float m = row_ok ? -INFINITY : 0.f, l = 0.f, sc = a.scale_log2;
+            m = row_ok ? -INFINITY : 0.f;
+            float sc = a.scale_log2;
             for (int j = 0; j < cnt; ++j, ++scnt) {
                 const int x = x0 + j * step, v0 = (t0 + x) * K::KEYS;
                 if (!(ok = wait_all(bar(K::SFULL + i), scnt & 1))) break;
@@ -822,10 +885,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     }
                     return top;
                 };
-                // (rare) a P of the keys from k on reaches 2: m rises by a whole number of octaves, and the P written in
+                // (rare) the P of the keys from k on reach kHigh: m rises by a whole number of octaves, and the P written in
                 // this tile, O and l are scaled down by as many (exact but for what falls below fp32's range)
                 auto raise_ref = [&](float target, int k) {
-                    const float inc = target + kHeadroom > m ? ceilf(target + kHeadroom - m) : 0.f;
+                    const float inc = target > m ? ceilf(target - m) : 0.f;
                     const int e = (int)fminf(inc, 127.f);
                     const float alpha = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
                     if (k > 0) {                          // the first half's P is being used: it ends in O
@@ -847,7 +910,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     l *= alpha;
                     m += inc;
                 };
-                uint32_t over = 0;                        // (FP8) the OR of the P to be written
                 // P of 32 keys from k on, two per packed fp32 operation (the even key in the low half); adds them to
                 // acc.  (Rows with nothing visible so far keep m = -inf: all their S are.)
                 auto emit = [&](const uint32_t (&s)[32], int k, uint32_t* v, uint64_t& acc) {
@@ -859,6 +921,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                         const int pg = (k + h) / kBlock;
                         const float f = FP8 ? sc * k_scale(pg) : sc;
                         const uint64_t sc2 = f2pack(__float_as_uint(f), __float_as_uint(f));
+                        float vs = FP8 ? ks[8 + pg * HG] : 1.f;
+                        vs = fabsf(vs) < INFINITY ? vs : 1.f;               // (V has no finite values then)
+                        const uint64_t vs2 = f2pack(__float_as_uint(vs), __float_as_uint(vs));
 #pragma unroll
                         for (int y = h; y < h + 16; y += 2) {
                             float q0, q1;
@@ -867,11 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                             if ((y >> 1) & 1) cb = f2add(cb, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
                             else ca = f2add(ca, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
                             if constexpr (FP8) {
-                                float vs = ks[8 + pg * HG];
-                                vs = fabsf(vs) < INFINITY ? vs : 1.f;       // (V has no finite values then)
-                                over |= __float_as_uint(p0) | __float_as_uint(p1);
-                                p0 *= vs;
-                                p1 *= vs;
+                                f2unpack(f2mul(f2pack(__float_as_uint(p0), __float_as_uint(p1)), vs2), p0, p1);
                             }
                             v[y >> 1] = pack_bf16(p0, p1);
                         }
@@ -892,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                             // one that is too small
                             const float top = largest(k);
                             if (again) raise_ref(row_ok ? top * sc : -INFINITY, k);
-                            else if (m == -INFINITY) m = top * sc + kHeadroom;
+                            else if (m == -INFINITY) m = top * sc;
                             // (too far below 0 is only seen here: m rises)
                             if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
                             if (HG == 1) {
@@ -902,7 +963,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                         }
                         uint64_t acc = 0;
                         uint32_t v[STEP / 2];
-                        over = 0;
                         if constexpr (PAIR) {             // loads in flight behind the arithmetic
                             uint32_t s1[32];
                             load_s(k + 32, s1);
@@ -914,16 +974,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                         } else {
                             emit(sa, k, v, acc);
                         }
-                        // P is written once none is known to reach 2 (the top exponent bit is clear below)
-                        bool high;
-                        if constexpr (FP8) {
-                            high = (over & 0x40000000u) != 0;
-                        } else {
-                            uint32_t any[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                            for (int y = 4; y < STEP / 2; ++y) any[y & 3] |= v[y];
-                            high = ((any[0] | any[1] | any[2] | any[3]) & 0x40004000u) != 0;
-                        }
+                        float a0, a1;
+                        f2unpack(acc, a0, a1);
+                        const bool high = !(a0 + a1 < kHigh);
                         if (__any_sync(0xffffffffu, row_ok && high) && !again) {
                             again = true;                 // once more with m raised (NaN logits pass then)
                             continue;
@@ -941,8 +994,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                                 for (int y = 1; y < HG; ++y) tmem_st8(scol + (pg * HG + (hw + y) % HG) * 8, z);
                             }
                         }
-                        float a0, a1;
-                        f2unpack(acc, a0, a1);
                         l += a0 + a1;                     // (behind the store)
                         tmem_wait_st();
                         break;
@@ -955,6 +1006,17 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             // (a reference so large that fp32 cannot place the weights beside it is reported)
             const float size = fabsf(m);
             if (row_ok && size >= kLimit && size < INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
+            }
+            // (while the last P . V runs)
+            if (FP8) ready_q(n + 1, qbase);
+            if (!ok) break;
+            if (cnt == 0) {
+                if (n >= 0) {
+                    ++pieces;
+                    release(n);
+                }
+                continue;
+            }
             // the results; with both chains, half the columns each, from both O, m and l
             const bool both = !p->two && p->count(1) > 0;
             if (both) {
@@ -986,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             release(n);
         }
     } else if (warp < kProducer) {
-        // ------------------------------------------------ V (FP8: Q too) made ready
+        // ------------------------------------------------ V made ready
         regs_dec<kRegsReady>();
         enter();
         const int w = warp - kReady;
@@ -1105,72 +1167,11 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
         };
-        // (FP8) this warp's rows of Q tile qt, in place, 16 at a time, half a row a lane: groups of 8 rows are 1024 bytes of a
-        // slab; the first term's codes go where the first slab was (D = 64: to the first half of each 1024 bytes), the
-        // second's to the other.
-        auto ready_q = [&](int qt) {
-            uint8_t* tile = smem + K::OFF_Q + (qt & 1) * K::QTILE;
-            constexpr int N = D / 16;                     // 16-byte chunks of half a row
-            constexpr int LO = D == 128 ? K::SLAB : 512;
-            const int half = lane >> 4;
-#pragma unroll 1
-            for (int row = w * 32 + (lane & 15); row < w * 32 + 32; row += 16) {
-                uint32_t top = 0;
-                uint4 x[N];
-#pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    const int ch = half * N + c;          // (dimensions 8 ch .. 8 ch + 7)
-                    x[c] = *reinterpret_cast<const uint4*>(tile + (ch / 8) * K::SLAB + row * 128 + (((ch & 7) ^ (row & 7)) * 16));
-                    const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, y[e] >> 16 & 0x7fffu));
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                // 2^(134 - exponent) takes the largest element to [128, 256); kept inside fp32's normal range (a row below
-                // 2^-113 counts as smaller beside any scale); infinities and NaN make the row NaN
-                const int ex = min(max((int)(top >> 7), 14), 254);
-                const float f = __uint_as_float((uint32_t)(261 - ex) << 23);
-                const float inv = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ex - 7) << 23);
-                uint8_t* dst = tile + (row / 8) * 1024 + (row & 7) * 16 + half * (N / 2) * 128;
-#pragma unroll
-                for (int c = 0; c < N / 2; ++c) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint4 y = x[2 * c + e / 2];
-                        uint32_t h0, h1, l0, l1;
-                        split2(e & 1 ? y.z : y.x, f, h0, l0);
-                        split2(e & 1 ? y.w : y.y, f, h1, l1);
-                        hi[e] = h0 | h1 << 16;
-                        lo[e] = l0 | l1 << 16;
-                    }
-                    x[2 * c] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    x[2 * c + 1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int c = 0; c < N / 2; ++c) {
-                    *reinterpret_cast<uint4*>(dst + c * 128) = x[2 * c];
-                    *reinterpret_cast<uint4*>(dst + LO + c * 128) = x[2 * c + 1];
-                }
-                if (half == 0) q_scale[qt % K::NQS * kRows + row] = inv;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(K::QREADY + (qt & 1)));
-        };
-
         bool ok = true;
-        int gt = 0, qn = 0;                               // key tiles and Q tiles
+        int gt = 0;                                       // key tiles
         for (int n = 0; ok; ++n) {
             const Piece* p = piece_at(n);
             if (!p || p->end) break;
-            // (not before the last piece's last V: the other row tile's old Q is given back only behind that)
-#pragma unroll 1
-            for (int i = 0; FP8 && i < (p->two ? 2 : 1) && ok; ++i, ++qn) {
-                ok = wait_all(bar(K::QFULL + (qn & 1)), (qn >> 1) & 1);
-                if (ok) ready_q(qn);
-            }
             const int tiles = p->tiles();
 #pragma unroll 1
             for (int x = 0; x < tiles && ok; ++x, ++gt) {
@@ -1211,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             enter();
             // -------------------------------------------- Q tiles, K and V pages in order
             bool ok = true;
-            int nt = 0, nq = 0;                           // key tiles and Q tiles
+            int nt = 0, nq = 0, nq1 = 0, npc = 0;         // key tiles; Q tiles, those of chain 1; pieces
             int nk = 0, nv = 0;                           // copies issued: K and V tiles
             if (a.hold != nullptr && lane == 0) {
                 // (tests of the timeout path only) wait, bounded, for a flag that nothing sets
@@ -1268,12 +1269,17 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
                     const int slot = nq & 1;
                     if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(K::QFULL + slot), HG * K::SLABS * a.pb * a.group * 128);
+                    // (bf16: a barrier each slot, for the issuers, who see every tile.  FP8: those of chain 0's, by turns, and one of
+                    // chain 1's, for the warps that split them, who see no others: no barrier's phases run ahead unseen)
+                    const uint32_t full = bar(!FP8 ? K::QFULL + slot : i == 0 ? K::QFULL + (n & 1) : K::Q1FULL);
+                    if (lane == 0) mbar_arrive_expect_tx(full, HG * K::SLABS * a.pb * a.group * 128);
+                    nq1 += i;
+                    npc += i == 0;
                     __syncwarp();
                     if (lane < HG * K::SLABS) {           // (a lane for each head's slab)
                         const int sl = lane % K::SLABS, hq = lane / K::SLABS;
                         tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + sl * K::SLAB + hq * RQ * 128, &a.q, sl * 64,
-                                   (p->g + hq) * a.group, (int)(p->row + p->q0 + i * a.pb), bar(K::QFULL + slot));
+                                   (p->g + hq) * a.group, (int)(p->row + p->q0 + i * a.pb), full);
                     }
                 }
 #pragma unroll 1
@@ -1320,7 +1326,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
                 for (int t = max(0, nk - NSK); t < nk; ++t) wait(bar(K::KFULL + t % NSK), (t / NSK) & 1, drain);
                 for (int t = max(0, nv - NSV); t < nv; ++t) wait(bar(K::VFULL + t % NSV), (t / NSV) & 1, drain);
-                for (int t = max(0, nq - 2); t < nq; ++t) wait(bar(K::QFULL + (t & 1)), (t >> 1) & 1, drain);
+                for (int t = max(0, (FP8 ? npc : nq) - 2); t < (FP8 ? npc : nq); ++t)
+                    wait(bar(K::QFULL + (t & 1)), (t >> 1) & 1, drain);
+                if (FP8 && nq1 > 0) wait(bar(K::Q1FULL), (nq1 - 1) & 1, drain);
             }
             __syncwarp();
         } else if (warp == kMma || warp == kMma + 1) {
@@ -1429,8 +1437,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     // a piece's first PV starts O afresh: the other chain too has read the last result that they shared
                     if (j == 0 && bcnt > 0 && !wait_all(bar(K::OFREE), (bcnt - 1) & 1)) break;
                 }
-                // (what the next S needs is waited for before P, off the path from P to it)
-                if (then && ((fresh && !see_q(q.q)) || !see_k(q.base + q.x0 + jq * q.step))) break;
+                // (the next S's K is waited for before P, off the path from P to it; a new piece's Q comes only behind P)
+                if (then && !fresh && !see_k(q.base + q.x0 + jq * q.step)) break;
                 if (now) {
                     if (HG == 1 && p.two) {
                         if ((i == 1 || turn > 0) && !wait_all(bar(K::TURN + i), (i == 1 ? turn : turn - 1) & 1)) break;
@@ -1461,8 +1469,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 } else {
                     tc_fence_after();
                 }
+                const bool pass = HG == 1 && now && p.two;
+                if (pass && (fresh || !then)) commit(lead, bar(K::TURN + 1 - i));
+                if (then && fresh && (!see_q(q.q) || !see_k(q.base + q.x0))) break;
+                if (then && fresh) tc_fence_after();
                 if (then) issue_s(q, jq);
-                if (HG == 1 && now && p.two) {
+                if (pass && !fresh && then) {
                     if constexpr (D == 64) commit(lead, bar(K::TURN + 1 - i));
                     else if (lead) mbar_arrive(bar(K::TURN + 1 - i));
                 }
