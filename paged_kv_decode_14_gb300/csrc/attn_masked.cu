@@ -69,6 +69,7 @@ template <int HG>
 constexpr int kItemUnits = HG == 1 ? 4 : 2;
 constexpr uint32_t kWaitHint = 20000;     // ns that a wait may sleep before it looks at the abort flag
 constexpr int kAhead = 3;                  // tiles that an FP8 page's scales are fetched ahead
+constexpr int kCutUnits = 8;               // what cutting an item costs, in units
 constexpr int kMinUnits = 4;               // units that a CTA has at least
 
 struct Arg {
@@ -188,7 +189,7 @@ struct Cfg {
     static constexpr int KFULL = 0, KEMPTY = NSK, VFULL = 2 * NSK, VREADY = VFULL + NSV, VEMPTY = VREADY + NSV,
                          SFULL = VEMPTY + NSV, PFA = SFULL + 2, PFB = SFULL + 4, QFULL = SFULL + 6, QREADY = SFULL + 8,
                          QEMPTY = SFULL + 10, ODONE = SFULL + 12, OFREE = SFULL + 14, LREADY = SFULL + 16,
-                         PVA = SFULL + 18, TURN = SFULL + 20, PCFULL = SFULL + 22, PCEMPTY = PCFULL + kPieces,
+                         PVA = SFULL + 18, PCFULL = SFULL + 20, PCEMPTY = PCFULL + kPieces,
                          Q1FULL = PCEMPTY + kPieces, DRAIN = Q1FULL + 1;
     static constexpr int NBAR = DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
@@ -224,6 +225,7 @@ struct Plan {
     int groups;             // of HG kv-heads
     int total, u, u1;       // all units; the CTA's place and end
     int share, longer;      // units of a CTA, and how many CTAs have one more
+    bool flat;              // a CTA has one item or none: an item counts one unit
     int b, blk, g;          // the item at u, its first unit
     int start;
     Seq s;
@@ -255,7 +257,7 @@ struct Plan {
         }
         tiles = (p.np + TP - 1) / TP;
         each = HG == 1 && p.nq > a.pb ? 2 : 1;
-        return tiles * each + kItemUnits<HG>;
+        return flat ? 1 : tiles * each + kItemUnits<HG>;
     }
     template <typename V>
     __device__ __forceinline__ V scan(V x) const {        // the sum over earlier lanes
@@ -287,9 +289,11 @@ struct Plan {
         }
         // units of this lane's sequences; the second time, the item of them that holds unit `u`
         int64_t mine = 0, before = 0;
-        int fb = 0, fblk = 0, fg = 0, fs = 0;
-        int64_t fp = 0;
+        int fb = 0, fblk = 0, fg = 0, fs = 0, most = 0;
+        int64_t fp = 0, items = 0;
         total = u = u1 = 0;
+        flat = false;
+        // (a third turn, between the two, where the items turn out to be dealt whole)
 #pragma unroll 1
         for (int turn = 0; turn < 2; ++turn) {
             const bool here = turn == 1 && u >= before && u < before + mine;
@@ -306,6 +310,8 @@ struct Plan {
                         int tiles, each;
                         const int w = span(x, k, p, tiles, each);
                         const int64_t all = (int64_t)w * groups;
+                        most = max(most, w);
+                        items += groups;
                         if (turn == 1 && u < r + all) {
                             fb = i;
                             fblk = k;
@@ -328,7 +334,19 @@ struct Plan {
                     return;
                 }
                 total = (int)sum;
-                const int ctas = max(1, min((int)gridDim.x, total / kMinUnits));
+                int ctas = max(1, min((int)gridDim.x, total / kMinUnits));
+                // few and short items: a join would cost more than it spreads
+                if (!flat) {
+                    const int n = (int)__reduce_add_sync(0xffffffffu, (unsigned)min(items, (int64_t)1 << 16));
+                    most = __reduce_max_sync(0xffffffffu, most);
+                    if (n <= (int)gridDim.x && most <= total / ctas + kCutUnits) {
+                        flat = true;
+                        before = 0;
+                        turn = -1;
+                        continue;
+                    }
+                }
+                if (flat) ctas = total;
                 if ((int)blockIdx.x >= ctas || total == 0) return;
                 share = (int)((uint32_t)total / (uint32_t)ctas);
                 longer = total - share * ctas;
@@ -353,7 +371,7 @@ struct Plan {
             int tiles, each;
             const int w = span(s, blk, p, tiles, each);
             const int keys = start + kItemUnits<HG>;          // the first tile's first unit
-            auto tile_at = [&](int x) { return x <= keys ? 0 : min(tiles, (x - keys + each - 1) >> (each - 1)); };
+            auto tile_at = [&](int x) { return flat ? (x > start ? tiles : 0) : x <= keys ? 0 : min(tiles, (x - keys + each - 1) >> (each - 1)); };
             p.t0 = tile_at(u);
             p.t1 = tile_at(u1);
             some = p.t1 > p.t0;
@@ -366,7 +384,7 @@ struct Plan {
             p.end = 0;
             p.c0 = blockIdx.x;
             p.parts = 1;
-            if (some && (p.t0 > 0 || p.t1 < tiles)) {
+            if (some && !flat && (p.t0 > 0 || p.t1 < tiles)) {
                 if (p.t0 > 0) p.c0 = cta_of(keys);
                 p.parts = (p.t1 < tiles ? cta_of(keys + (tiles - 1) * each) : (int)blockIdx.x) - p.c0 + 1;
             }
@@ -475,7 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             mbar_init(bar(K::QEMPTY + i), 2);
             mbar_init(bar(K::ODONE + i), 1);
             mbar_init(bar(K::PVA + i), 1);
-            mbar_init(bar(K::TURN + i), 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(K::PCFULL + i), 1);
@@ -1341,7 +1358,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             const uint32_t o_i = tm + K::COL_O + __shfl_sync(0xffffffffu, i, 0) * D;
             constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(kRows, kCols) : idesc_bf16_f32(kRows, kCols, false, false);
             constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true);
-            int pcnt = 0, bcnt = 0, turn = 0;             // this chain's tiles; pieces of both chains; turns
+            int pcnt = 0, bcnt = 0;                       // this chain's tiles; pieces of both chains
             int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
             int kn = 0, vn = 0, qn = 0;                   // K, V and Q tiles seen: every one, in order, by both chains (a
                                                           // barrier's parity tells neighbouring phases apart, no more)
@@ -1437,13 +1454,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     // a piece's first PV starts O afresh: the other chain too has read the last result that they shared
                     if (j == 0 && bcnt > 0 && !wait_all(bar(K::OFREE), (bcnt - 1) & 1)) break;
                 }
-                // (the next S's K is waited for before P, off the path from P to it; a new piece's Q comes only behind P)
-                if (then && !fresh && !see_k(q.base + q.x0 + jq * q.step)) break;
+                // (what the next S needs is waited for before P, off the path from P to it; but a new piece's split Q comes only
+                // behind P)
+                if (then && (!fresh || (!FP8 && now)) && ((fresh && !see_q(q.q)) || !see_k(q.base + q.x0 + jq * q.step))) break;
                 if (now) {
-                    if (HG == 1 && p.two) {
-                        if ((i == 1 || turn > 0) && !wait_all(bar(K::TURN + i), (i == 1 ? turn : turn - 1) & 1)) break;
-                        ++turn;
-                    }
                     const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
                     // units up to the last page that a row sees
                     const int steps = HG * min(max((p.ends - (p.t0 + p.x0 + j * p.step) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
@@ -1469,15 +1483,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 } else {
                     tc_fence_after();
                 }
-                const bool pass = HG == 1 && now && p.two;
-                if (pass && (fresh || !then)) commit(lead, bar(K::TURN + 1 - i));
-                if (then && fresh && (!see_q(q.q) || !see_k(q.base + q.x0))) break;
+                if (then && fresh && (FP8 || !now) && (!see_q(q.q) || !see_k(q.base + q.x0))) break;
                 if (then && fresh) tc_fence_after();
                 if (then) issue_s(q, jq);
-                if (pass && !fresh && then) {
-                    if constexpr (D == 64) commit(lead, bar(K::TURN + 1 - i));
-                    else if (lead) mbar_arrive(bar(K::TURN + 1 - i));
-                }
                 now = then;
                 p = q;
                 j = jq;
