@@ -169,6 +169,8 @@ struct Cfg {
     static constexpr int TP = kUnits / HG;                // pages of a tile (of each head)
     static constexpr int KEYS = TP * kBlock;              // keys of a tile
     static constexpr int RQ = kRows / HG;                 // rows of a row tile that a head has
+    // A tile's products and softmax go by halves of its columns where a row works on all of them; else whole.
+    static constexpr int HALVES = HG == 1 ? 2 : 1, HCOLS = kCols / HALVES;
     static constexpr int SLAB = kRows * 128;              // Q: bytes of a 64-dimension slab
     static constexpr int SLABS = D / 64;
     static constexpr int QTILE = SLABS * SLAB;
@@ -187,9 +189,9 @@ struct Cfg {
     static constexpr int OFF_V = OFF_K + NSK * KTILE;
     static constexpr int OFF_BAR = OFF_V + NSV * VTILE;
     static constexpr int KFULL = 0, KEMPTY = NSK, VFULL = 2 * NSK, VREADY = VFULL + NSV, VEMPTY = VREADY + NSV,
-                         SFULL = VEMPTY + NSV, PFA = SFULL + 2, PFB = SFULL + 4, QFULL = SFULL + 6, QREADY = SFULL + 8,
-                         QEMPTY = SFULL + 10, ODONE = SFULL + 12, OFREE = SFULL + 14, LREADY = SFULL + 16,
-                         PVA = SFULL + 18, PCFULL = SFULL + 20, PCEMPTY = PCFULL + kPieces,
+                         SFULL = VEMPTY + NSV, PFULL = SFULL + 4, PVDONE = SFULL + 8, QFULL = SFULL + 12, QREADY = SFULL + 14,
+                         QEMPTY = SFULL + 16, ODONE = SFULL + 18, OFREE = SFULL + 20, LREADY = SFULL + 21,
+                         PCFULL = SFULL + 22, PCEMPTY = PCFULL + kPieces,
                          Q1FULL = PCEMPTY + kPieces, DRAIN = Q1FULL + 1;
     static constexpr int NBAR = DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
@@ -485,14 +487,15 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             mbar_init(bar(K::VEMPTY + i), 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(K::SFULL + i), 1);
-            mbar_init(bar(K::PFA + i), 4);                // one arrival a softmax warp
-            mbar_init(bar(K::PFB + i), 4);
+            for (int h = 0; h < 2; ++h) {                 // by chain and half of a tile's columns
+                mbar_init(bar(K::SFULL + 2 * i + h), 1);
+                mbar_init(bar(K::PFULL + 2 * i + h), 4);  // one arrival a softmax warp
+                mbar_init(bar(K::PVDONE + 2 * i + h), 1);
+            }
             mbar_init(bar(K::QFULL + i), 1);
             mbar_init(bar(K::QREADY + i), 4);
             mbar_init(bar(K::QEMPTY + i), 2);
             mbar_init(bar(K::ODONE + i), 1);
-            mbar_init(bar(K::PVA + i), 1);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(K::PCFULL + i), 1);
@@ -544,20 +547,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t scol = tmem + lbase + i * kCols;   // S / P
         const uint32_t ocol = tmem + lbase + K::COL_O + i * D;
-        auto signal = [&](uint32_t bb) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bb);
-        };
-        // S of 32 of the row's keys of the tile, from key k on (a multiple of 32)
-        auto load_s = [&](int k, uint32_t (&s)[32]) {
-            if constexpr (HG == 1) {
-                tmem_ld32_async(scol + k, s);
-            } else {
-                tmem_ld16_at<0>(scol + (k * HG + hw * kBlock), s);
-                tmem_ld16_at<16>(scol + ((k + kBlock) * HG + hw * kBlock), s);
-            }
-        };
         // What the guard took out of V, added to a row's results where this lane has just written them (rare).
         auto add_back = [&](const Piece& p, int qi, int d0, int d1, uint8_t* out, float* part) {
             const Guard<HG> gd = guard_of<HG>(a, p);
@@ -799,8 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             }
             fence_proxy_async_smem();
         };
-        constexpr int STEP = K::KEYS < 64 ? K::KEYS : 64; // keys whose P is written at once
-        constexpr bool PAIR = STEP == 64;
+        constexpr int HALVES = K::HALVES, STEP = K::KEYS / HALVES, PAGES = STEP / kBlock;      // keys and pages (of each head)
         bool ok = true;
         int scnt = 0, tbase = 0, qbase = 0;               // this chain's tiles; the CTA's tiles and Q tiles
         int pieces = 0, pieces1 = 0, bcnt = 0;            // the CTA's pieces; those of chain 1; those of both chains
@@ -829,200 +817,194 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             }
             float m = 0.f, l = 0.f;                       // the reference maximum (exp2 units); the sum of P
             if (cnt > 0) {
-            const int x0 = p->begin(i), step = p->step(), t0 = p->t0;
-            const int qi = (p->two ? i * a.pb : 0) + pos;  // the row's query, from the piece's first on
-            const bool row_ok = pos < a.pb && qi < p->nq;
-            const bool live = __any_sync(0xffffffffu, row_ok);
-            // (rows of no query see everything, so that they ask for no mask)
-            Sight see{0, -0x40000000, 0x3fffffff};
-            const uint32_t* tree = nullptr;
-            if (row_ok) {
-                if (a.tree) {
-                    see.tree(*p);
-                    tree = a.tree + (p->row + p->q0 + qi) * (int64_t)a.tree_words;
-                } else {
-                    see.window(a, *p, p->first + qi);
-                }
-            }
-            const int tree0 = p->L - p->Q, tree_n = p->Q;
-            const int ends = p->seen_end(a, min(p->nq, p->two ? (i + 1) * a.pb : a.pb));
-            m = row_ok ? -INFINITY : 0.f;
-            float sc = a.scale_log2;
-            for (int j = 0; j < cnt; ++j, ++scnt) {
-                const int x = x0 + j * step, v0 = (t0 + x) * K::KEYS;
-                if (!(ok = wait_all(bar(K::SFULL + i), scnt & 1))) break;
-                if (!live) {
-                    if (lane == 0) {
-                        if (HG == 1) mbar_arrive(bar(K::PFA + i));
-                        mbar_arrive(bar(K::PFB + i));
+                const int x0 = p->begin(i), step = p->step(), t0 = p->t0;
+                const int qi = (p->two ? i * a.pb : 0) + pos;  // the row's query, from the piece's first on
+                const bool row_ok = pos < a.pb && qi < p->nq;
+                const bool live = __any_sync(0xffffffffu, row_ok);
+                // (rows of no query see everything, so that they ask for no mask)
+                Sight see{0, -0x40000000, 0x3fffffff};
+                const uint32_t* tree = nullptr;
+                if (row_ok) {
+                    if (a.tree) {
+                        see.tree(*p);
+                        tree = a.tree + (p->row + p->q0 + qi) * (int64_t)a.tree_words;
+                    } else {
+                        see.window(a, *p, p->first + qi);
                     }
-                    continue;
                 }
-                tc_fence_after();
-                if (FP8 && j == 0) sc = a.scale_log2 * q_scale[qt % K::NQS * kRows + r];
-                const float* ks = scales + ((base + x) % K::NSC) * 16 + hw;     // (of unit u: ks[u * HG])
-                const bool masked = !__all_sync(0xffffffffu, (v0 >= see.wl && v0 + K::KEYS - 1 <= see.wh) || v0 + K::KEYS <= see.ns);
-                // A tile that some row does not see all of: its S becomes -inf there, in tensor memory (FP8: the page's scale is
-                // multiplied in on the way), and what follows knows no masks.  (A second copy of it with masks, though
-                // hardly ever run, made every tile a third slower: the inner loops no longer fit the instruction cache.)
-                if (masked) {
+                const int tree0 = p->L - p->Q, tree_n = p->Q;
+                const int ends = p->seen_end(a, min(p->nq, p->two ? (i + 1) * a.pb : a.pb));
+                m = row_ok ? -INFINITY : 0.f;
+                float sc = a.scale_log2;
+                // (by halves: while P of one is made, the other's P . V and next S run)
 #pragma unroll 1
-                    for (int pg = 0; pg < K::TP; ++pg) {
-                        // the visible ones of the page's 16 keys
-                        const int v = v0 + pg * kBlock, n_s = see.ns - v, lo = max(see.wl - v, 0), hi = min(see.wh - v, 31);
-                        uint32_t w = n_s >= 16 ? 0xffffu : n_s > 0 ? (1u << n_s) - 1u : 0u;
-                        if (lo <= hi) w |= (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
-                        if (tree && v + 31 >= tree0) w |= tree_bits(tree, a.tree_words, v - tree0, tree_n);
-                        if (!FP8 && __all_sync(0xffffffffu, (w & 0xffffu) == 0xffffu)) continue;
-                        const uint32_t col = scol + (pg * HG + hw) * kBlock;
-                        float f[16];
-                        tmem_ld16(col, f);
-                        uint32_t t[16];
-#pragma unroll
-                        for (int y = 0; y < 16; ++y)
-                            t[y] = w >> y & 1 ? __float_as_uint(FP8 ? f[y] * ks[pg * HG] : f[y]) : 0xff800000u;
-                        tmem_st16u(col, t);
-                    }
-                    tmem_wait_st();
-                }
-                // the factor of S of page pg
-                auto k_scale = [&](int pg) { return masked ? 1.f : ks[pg * HG]; };
-                uint32_t sa[32];
-                load_s(0, sa);
-                // the largest S (FP8: times its page's scale) of keys k .. k + STEP - 1
-                auto largest = [&](int k) -> float {
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int pg = k / kBlock; pg < (k + STEP) / kBlock; ++pg) {
-                        float f[16], t = -INFINITY;
-                        tmem_ld16(scol + (pg * HG + hw) * kBlock, f);
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) t = fmaxf(t, FP8 ? f[y] * k_scale(pg) : f[y]);
-                        top = fmaxf(top, t);
-                    }
-                    return top;
-                };
-                // (rare) the P of the keys from k on reach kHigh: m rises by a whole number of octaves, and the P written in
-                // this tile, O and l are scaled down by as many (exact but for what falls below fp32's range)
-                auto raise_ref = [&](float target, int k) {
-                    const float inc = target > m ? ceilf(target - m) : 0.f;
-                    const int e = (int)fminf(inc, 127.f);
-                    const float alpha = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
-                    if (k > 0) {                          // the first half's P is being used: it ends in O
-                        wait_all(bar(K::PVA + i), scnt & 1);
+                for (int hh = 0; hh < HALVES * cnt; ++hh) {
+                    const int j = hh / HALVES, h = hh % HALVES, x = x0 + j * step;
+                    const int v0 = (t0 + x) * K::KEYS + h * STEP;          // the half's first key
+                    if (!(ok = wait_all(bar(K::SFULL + 2 * i + h), scnt & 1))) break;
+                    // (what no row sees behind the first half is not read by the PV)
+                    if (live && !(h > 0 && v0 >= ends)) {
                         tc_fence_after();
-                    }
-                    if (j > 0 || k > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            float o[16];
-                            tmem_ld16(ocol + c, o);
-                            uint32_t v[16];
+                        if (FP8 && hh == 0) sc = a.scale_log2 * q_scale[qt % K::NQS * kRows + r];
+                        const bool masked =
+                            !__all_sync(0xffffffffu, (v0 >= see.wl && v0 + STEP - 1 <= see.wh) || v0 + STEP <= see.ns);
+                        // S and P of page pg of the half: columns of this row's head
+                        auto s_col = [&](int pg) { return scol + h * K::HCOLS + (pg * HG + hw) * kBlock; };
+                        auto p_col = [&](int pg, int head) { return scol + h * K::HCOLS + (pg * HG + head) * 8; };
+                        // FP8: factors of S and of P, a page each
+                        float ks[PAGES], vs[PAGES];
+                        const float* ks_at = scales + ((base + x) % K::NSC) * 16 + h * PAGES * HG + hw;
+                        if constexpr (FP8) {
 #pragma unroll
-                            for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(o[y] * alpha);
-                            tmem_st16u(ocol + c, v);
-                        }
-                        tmem_wait_st();
-                    }
-                    l *= alpha;
-                    m += inc;
-                };
-                // P of 32 keys from k on, two per packed fp32 operation (the even key in the low half); adds them to
-                // acc.  (Rows with nothing visible so far keep m = -inf: all their S are.)
-                auto emit = [&](const uint32_t (&s)[32], int k, uint32_t* v, uint64_t& acc) {
-                    uint64_t ca = 0, cb = 0;
-                    const float nm = m == -INFINITY ? 0.f : -m;
-                    const uint64_t nm2 = f2pack(__float_as_uint(nm), __float_as_uint(nm));
-#pragma unroll
-                    for (int h = 0; h < 32; h += 16) {
-                        const int pg = (k + h) / kBlock;
-                        const float f = FP8 ? sc * k_scale(pg) : sc;
-                        const uint64_t sc2 = f2pack(__float_as_uint(f), __float_as_uint(f));
-                        float vs = FP8 ? ks[8 + pg * HG] : 1.f;
-                        vs = fabsf(vs) < INFINITY ? vs : 1.f;               // (V has no finite values then)
-                        const uint64_t vs2 = f2pack(__float_as_uint(vs), __float_as_uint(vs));
-#pragma unroll
-                        for (int y = h; y < h + 16; y += 2) {
-                            float q0, q1;
-                            f2unpack(f2fma(f2pack(s[y], s[y + 1]), sc2, nm2), q0, q1);
-                            float p0 = exp2_fast(q0), p1 = exp2_fast(q1);
-                            if ((y >> 1) & 1) cb = f2add(cb, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
-                            else ca = f2add(ca, f2pack(__float_as_uint(p0), __float_as_uint(p1)));
-                            if constexpr (FP8) {
-                                f2unpack(f2mul(f2pack(__float_as_uint(p0), __float_as_uint(p1)), vs2), p0, p1);
-                            }
-                            v[y >> 1] = pack_bf16(p0, p1);
-                        }
-                    }
-                    acc = f2add(acc, f2add(ca, cb));
-                };
-                tmem_wait_ld_into(sa);
-                // (one copy of either path: the instruction cache holds little more than the roles' inner loops)
-#pragma unroll 1
-                for (int k = 0; k < K::KEYS; k += STEP) {
-                    // what no row sees behind the first half is not read by the PV
-                    const bool none = k > 0 && v0 + k >= ends;
-                    bool again = false;
-#pragma unroll 1
-                    while (!none) {
-                        if (again || !__all_sync(0xffffffffu, m > -INFINITY)) {
-                            // no reference yet (a piece's first tile): the largest that is visible (O and l are 0 so far); or
-                            // one that is too small
-                            const float top = largest(k);
-                            if (again) raise_ref(row_ok ? top * sc : -INFINITY, k);
-                            else if (m == -INFINITY) m = top * sc;
-                            // (too far below 0 is only seen here: m rises)
-                            if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
-                            if (HG == 1) {
-                                load_s(k, sa);
-                                tmem_wait_ld_into(sa);
+                            for (int pg = 0; pg < PAGES; ++pg) {
+                                ks[pg] = masked ? 1.f : ks_at[pg * HG];
+                                vs[pg] = ks_at[8 + pg * HG];
+                                vs[pg] = fabsf(vs[pg]) < INFINITY ? vs[pg] : 1.f;          // (V has no finite values then)
                             }
                         }
-                        uint64_t acc = 0;
-                        uint32_t v[STEP / 2];
-                        if constexpr (PAIR) {             // loads in flight behind the arithmetic
-                            uint32_t s1[32];
-                            load_s(k + 32, s1);
-                            emit(sa, k, v, acc);
-                            tmem_wait_ld_into(s1);
-                            if (HG == 1) load_s(64, sa);  // (for the second half; after it, for nothing)
-                            emit(s1, k + 32, v + 16, acc);
-                            if (HG == 1) tmem_wait_ld_into(sa);
-                        } else {
-                            emit(sa, k, v, acc);
-                        }
-                        float a0, a1;
-                        f2unpack(acc, a0, a1);
-                        const bool high = !(a0 + a1 < kHigh);
-                        if (__any_sync(0xffffffffu, row_ok && high) && !again) {
-                            again = true;                 // once more with m raised (NaN logits pass then)
-                            continue;
-                        }
-                        if constexpr (HG == 1) {
-                            tmem_st32u(scol + (k >> 1), v);
-                        } else {
+                        // Keys that some row does not see: their S becomes -inf there, in tensor memory (FP8: the page's scale
+                        // is multiplied in on the way), and what follows knows no masks.  (A second copy of it with masks,
+                        // though hardly ever run, made every tile a third slower: the inner loops no longer fit the
+                        // instruction cache.)
+                        if (masked) {
+#pragma unroll 1
+                            for (int pg = 0; pg < PAGES; ++pg) {
+                                // the visible ones of the page's 16 keys
+                                const int v = v0 + pg * kBlock, n_s = see.ns - v, lo = max(see.wl - v, 0), hi = min(see.wh - v, 31);
+                                uint32_t w = n_s >= 16 ? 0xffffu : n_s > 0 ? (1u << n_s) - 1u : 0u;
+                                if (lo <= hi) w |= (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+                                if (tree && v + 31 >= tree0) w |= tree_bits(tree, a.tree_words, v - tree0, tree_n);
+                                if (!FP8 && __all_sync(0xffffffffu, (w & 0xffffu) == 0xffffu)) continue;
+                                float f[16];
+                                tmem_ld16(s_col(pg), f);
+                                uint32_t t[16];
 #pragma unroll
-                            for (int pg = 0; pg < K::TP; ++pg) {
-                                uint32_t d8[8], z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-                                for (int y = 0; y < 8; ++y) d8[y] = v[pg * 8 + y];
-                                tmem_st8(scol + (pg * HG + hw) * 8, d8);
-#pragma unroll
-                                for (int y = 1; y < HG; ++y) tmem_st8(scol + (pg * HG + (hw + y) % HG) * 8, z);
+                                for (int y = 0; y < 16; ++y)
+                                    t[y] = w >> y & 1 ? __float_as_uint(FP8 ? f[y] * ks_at[pg * HG] : f[y]) : 0xff800000u;
+                                tmem_st16u(s_col(pg), t);
                             }
+                            tmem_wait_st();
                         }
-                        l += a0 + a1;                     // (behind the store)
-                        tmem_wait_st();
-                        break;
+                        bool again = false;
+#pragma unroll 1
+                        for (;;) {
+                            if (again || !__all_sync(0xffffffffu, m > -INFINITY)) {
+                                // no reference yet (a piece's first tile): the largest that is visible (O and l are 0 so far);
+                                // or (rare) one that is too small: m rises by a whole number of octaves, and O and l are
+                                // scaled down by as many (exact but for what falls below fp32's range)
+                                float top = -INFINITY;
+#pragma unroll 1
+                                for (int pg = 0; pg < PAGES; ++pg) {
+                                    float f[16], t = -INFINITY;
+                                    tmem_ld16(s_col(pg), f);
+#pragma unroll
+                                    for (int y = 0; y < 16; ++y) t = fmaxf(t, FP8 && !masked ? f[y] * ks_at[pg * HG] : f[y]);
+                                    top = fmaxf(top, t);
+                                }
+                                const float target = row_ok ? top * sc : -INFINITY;
+                                if (!again) {
+                                    if (m == -INFINITY) m = target;
+                                } else {
+                                    const float inc = target > m ? ceilf(target - m) : 0.f;
+                                    const int e = (int)fminf(inc, 127.f);
+                                    const float alpha = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+                                    if (hh > 0) {         // the last P . V may still add to O
+                                        if (HALVES > 1) wait_all(bar(K::PVDONE + 2 * i + 1 - h), (h ? scnt : scnt - 1) & 1);
+                                        tc_fence_after();
+#pragma unroll 1
+                                        for (int c = 0; c < D; c += 16) {
+                                            float o[16];
+                                            tmem_ld16(ocol + c, o);
+                                            uint32_t v[16];
+#pragma unroll
+                                            for (int y = 0; y < 16; ++y) v[y] = __float_as_uint(o[y] * alpha);
+                                            tmem_st16u(ocol + c, v);
+                                        }
+                                        tmem_wait_st();
+                                    }
+                                    l *= alpha;
+                                    m += inc;
+                                }
+                                // (too far below 0 is only seen here: m rises)
+                                if (row_ok && m <= -kLimit && m > -INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
+                            }
+                            // P, two per packed fp32 operation (the even key in the low half), and their sum.  (Rows with
+                            // nothing visible so far keep m = -inf: all their S are.)
+                            uint32_t v[STEP / 2];
+                            uint64_t ca = 0, cb = 0;
+                            const float nm = m == -INFINITY ? 0.f : -m;
+                            const uint64_t nm2 = f2pack(__float_as_uint(nm), __float_as_uint(nm));
+                            // 16 keys in s[o .. o + 15]: page pg
+                            auto emit16 = [&](const uint32_t* s, int pg) {
+                                const float f = FP8 ? sc * ks[pg] : sc;
+                                const uint64_t sc2 = f2pack(__float_as_uint(f), __float_as_uint(f));
+                                const uint64_t vs2 = FP8 ? f2pack(__float_as_uint(vs[pg]), __float_as_uint(vs[pg])) : 0;
+#pragma unroll
+                                for (int y = 0; y < 16; y += 2) {
+                                    float p0, p1;
+                                    f2unpack(f2fma(f2pack(s[y], s[y + 1]), sc2, nm2), p0, p1);
+                                    p0 = exp2_fast(p0);
+                                    p1 = exp2_fast(p1);
+                                    uint64_t p2 = f2pack(__float_as_uint(p0), __float_as_uint(p1));
+                                    if ((y >> 1) & 1) cb = f2add(cb, p2);
+                                    else ca = f2add(ca, p2);
+                                    if constexpr (FP8) f2unpack(f2mul(p2, vs2), p0, p1);
+                                    v[pg * 8 + (y >> 1)] = pack_bf16(p0, p1);
+                                }
+                            };
+                            uint32_t s0[32], s1[32];
+                            if constexpr (HG == 1) {
+                                tmem_ld32_async(s_col(0), s0);
+                                tmem_ld32_async(s_col(2), s1);
+                            } else {
+                                tmem_ld16_at<0>(s_col(0), s0);
+                                tmem_ld16_at<16>(s_col(1), s0);
+                                if constexpr (PAGES > 2) {
+                                    tmem_ld16_at<0>(s_col(2), s1);
+                                    tmem_ld16_at<16>(s_col(3), s1);
+                                }
+                            }
+                            tmem_wait_ld_into(s0);
+                            emit16(s0, 0);
+                            emit16(s0 + 16, 1);
+                            if constexpr (PAGES > 2) {
+                                tmem_wait_ld_into(s1);
+                                emit16(s1, 2);
+                                emit16(s1 + 16, 3);
+                            }
+                            float a0, a1;
+                            f2unpack(f2add(ca, cb), a0, a1);
+                            if (__any_sync(0xffffffffu, row_ok && !(a0 + a1 < kHigh)) && !again) {
+                                again = true;             // once more with m raised (NaN logits pass then)
+                                continue;
+                            }
+                            if constexpr (HG == 1) {
+                                tmem_st32u(p_col(0, 0), v);
+                            } else {
+#pragma unroll
+                                for (int pg = 0; pg < PAGES; ++pg) {
+                                    uint32_t d8[8], z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                                    for (int y = 0; y < 8; ++y) d8[y] = v[pg * 8 + y];
+                                    tmem_st8(p_col(pg, hw), d8);
+#pragma unroll
+                                    for (int y = 1; y < HG; ++y) tmem_st8(p_col(pg, (hw + y) % HG), z);
+                                }
+                            }
+                            l += a0 + a1;                 // (behind the store)
+                            tmem_wait_st();
+                            break;
+                        }
+                        tc_fence_before();
                     }
-                    // P of the first 64 keys: their PV may run while the rest is computed
-                    signal(bar(HG == 1 && k == 0 ? K::PFA + i : K::PFB + i));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(K::PFULL + 2 * i + h));
+                    scnt += h == HALVES - 1;
                 }
-            }
-            if (!ok) break;
-            // (a reference so large that fp32 cannot place the weights beside it is reported)
-            const float size = fabsf(m);
-            if (row_ok && size >= kLimit && size < INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
+                if (!ok) break;
+                // (a reference so large that fp32 cannot place the weights beside it is reported)
+                const float size = fabsf(m);
+                if (row_ok && size >= kLimit && size < INFINITY) raise_error(a.err, PKV_DEVERR_RANGE);
             }
             // (while the last P . V runs)
             if (FP8) ready_q(n + 1, qbase);
@@ -1356,7 +1338,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);       // (known to be uniform)
             const uint32_t s_i = tm + __shfl_sync(0xffffffffu, i, 0) * kCols;
             const uint32_t o_i = tm + K::COL_O + __shfl_sync(0xffffffffu, i, 0) * D;
-            constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(kRows, kCols) : idesc_bf16_f32(kRows, kCols, false, false);
+            constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(kRows, K::HCOLS) : idesc_bf16_f32(kRows, K::HCOLS, false, false);
             constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true);
             int pcnt = 0, bcnt = 0;                       // this chain's tiles; pieces of both chains
             int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
@@ -1410,33 +1392,38 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 ++n;
                 return true;
             };
-            // S of tile j of this chain's in a piece (its K and Q seen)
-            auto issue_s = [&](const Work& x, int j) {
+            // half h of S of tile j of this chain's in a piece (its K and Q seen)
+            auto issue_s = [&](const Work& x, int j, int h) {
                 const int sk = (x.base + x.x0 + j * x.step) % NSK;
-                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::KTILE, 0);
+                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::KTILE + h * (K::KTILE / K::HALVES), 0);
                 const uint32_t q_s = __shfl_sync(0xffffffffu, sb + K::OFF_Q + (x.q & 1) * K::QTILE, 0);
+                const uint32_t dst = s_i + __shfl_sync(0xffffffffu, h, 0) * K::HCOLS;
                 if constexpr (FP8) {
                     constexpr uint32_t LO = D == 128 ? K::SLAB : 512;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)      // the first term's, then the second's
-                        mma_ss_f8(lead, s_i, smem_desc(q_s + (k / (D / 32)) * LO + (k % (D / 32)) * 256, 128, 1024),
+                        mma_ss_f8(lead, dst, smem_desc(q_s + (k / (D / 32)) * LO + (k % (D / 32)) * 256, 128, 1024),
                                   smem_desc(kbase + (k % (D / 32)) * 256, 128, D * 8), idS, k > 0 ? 1u : 0u);
                 } else {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(lead, s_i, desc_sw128(q_s + (k / 4) * K::SLAB + (k % 4) * 32, 16, 1024),
+                        mma_ss(lead, dst, desc_sw128(q_s + (k / 4) * K::SLAB + (k % 4) * 32, 16, 1024),
                                smem_desc(kbase + k * 256, 128, K::NCH * 128), idS, k > 0 ? 1u : 0u);
                 }
-                commit(lead, bar(K::SFULL + i));
-                commit(lead, bar(K::KEMPTY + sk));
-                if (j + 1 == x.cnt) commit(lead, bar(K::QEMPTY + (x.q & 1)));
+                commit(lead, bar(K::SFULL + 2 * i + h));
+                if (h == K::HALVES - 1) {
+                    commit(lead, bar(K::KEMPTY + sk));
+                    if (j + 1 == x.cnt) commit(lead, bar(K::QEMPTY + (x.q & 1)));
+                }
             };
-            // One loop: P . V of the chain's present tile, if there is one, then S of the next, if there is one.
-            Work p, q;
+            // One loop: by halves, P . V of the chain's present tile, if there is one, each with the same half of S of the next
+            // tile behind it, if there is one in the piece; then both halves of S of a new piece's first.  One thread's
+            // products are done in order: S of a half may overwrite the P there.
+            Work p = {}, q = {};
             int j = 0, jq = 0;
-            bool now = false;                             // S of tile j of piece p has been issued
+            bool now = false, ok = true;                  // now: S of tile j of piece p has been issued
 #pragma unroll 1
-            for (;;) {
+            while (ok) {
                 bool then, fresh = false;
                 if (now && j + 1 < p.cnt) {
                     q = p;
@@ -1454,38 +1441,40 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     // a piece's first PV starts O afresh: the other chain too has read the last result that they shared
                     if (j == 0 && bcnt > 0 && !wait_all(bar(K::OFREE), (bcnt - 1) & 1)) break;
                 }
-                // (what the next S needs is waited for before P, off the path from P to it; but a new piece's split Q comes only
-                // behind P)
-                if (then && (!fresh || (!FP8 && now)) && ((fresh && !see_q(q.q)) || !see_k(q.base + q.x0 + jq * q.step))) break;
-                if (now) {
-                    const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
-                    // units up to the last page that a row sees
-                    const int steps = HG * min(max((p.ends - (p.t0 + p.x0 + j * p.step) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
-                    constexpr int HALVES = HG == 1 ? 2 : 1, EACH = kUnits / HALVES;
-                    bool ok = true;
-#pragma unroll
-                    for (int half = 0; half < HALVES; ++half) {
-                        if (!(ok = wait_all(bar((HG == 1 && half == 0 ? K::PFA : K::PFB) + i), pcnt & 1))) break;
+                // (what the next S needs is waited for before P, off the path from P to it)
+                if (then && !fresh && !see_k(q.base + q.x0 + jq * q.step)) break;
+                const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
+                // units up to the last page that a row sees
+                const int steps = HG * min(max((p.ends - (p.t0 + p.x0 + j * p.step) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
+                constexpr int HALVES = K::HALVES, EACH = kUnits / HALVES;
+#pragma unroll 1
+                for (int st = now ? 0 : HALVES; st < (then && fresh ? 2 * HALVES : HALVES); ++st) {
+                    const int h = st % HALVES;
+                    if (st < HALVES) {
+                        if (!(ok = wait_all(bar(K::PFULL + 2 * i + h), pcnt & 1))) break;
                         tc_fence_after();
+                        const int hu = __shfl_sync(0xffffffffu, h, 0);
 #pragma unroll
-                        for (int k = half * EACH; k < half * EACH + EACH; ++k)
-                            mma_ts(lead && k < steps, o_i, s_i + k * 8, smem_desc(vbase + k * K::PAGE, K::NCH * 128, 128), idPV,
-                                   j > 0 || k > 0 ? 1u : 0u);
-                        if (HG == 1 && half == 0) commit(lead, bar(K::PVA + i));
+                        for (int k = 0; k < EACH; ++k)
+                            mma_ts(lead && EACH * h + k < steps, o_i, s_i + hu * K::HCOLS + k * 8,
+                                   smem_desc(vbase + (EACH * hu + k) * K::PAGE, K::NCH * 128, 128), idPV, j > 0 || h > 0 || k > 0 ? 1u : 0u);
+                        if (HALVES > 1) commit(lead, bar(K::PVDONE + 2 * i + h));
+                        if (h == HALVES - 1) {
+                            if (j + 1 == p.cnt) commit(lead, bar(K::ODONE + i));
+                            commit(lead, bar(K::VEMPTY + sv));
+                        }
                     }
-                    if (!ok) break;
-                    if (j + 1 == p.cnt) {
-                        commit(lead, bar(K::ODONE + i));
-                        bcnt += p.both;
+                    // (a new piece's Q and K: bf16, before the last P; FP8, whose Q the softmax warps split behind it, after)
+                    if (then && fresh && (FP8 || HALVES == 1 || !now ? st == HALVES : st == 0)) {
+                        if (!(ok = see_q(q.q) && see_k(q.base + q.x0))) break;
+                        tc_fence_after();
                     }
-                    commit(lead, bar(K::VEMPTY + sv));
-                    ++pcnt;
-                } else {
-                    tc_fence_after();
+                    if (then && (!fresh || st >= HALVES)) issue_s(q, jq, h);
                 }
-                if (then && fresh && (FP8 || !now) && (!see_q(q.q) || !see_k(q.base + q.x0))) break;
-                if (then && fresh) tc_fence_after();
-                if (then) issue_s(q, jq);
+                if (now) {
+                    bcnt += j + 1 == p.cnt && p.both;
+                    ++pcnt;
+                }
                 now = then;
                 p = q;
                 j = jq;
