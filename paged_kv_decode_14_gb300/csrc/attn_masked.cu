@@ -1392,23 +1392,27 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 ++n;
                 return true;
             };
-            // half h of S of tile j of this chain's in a piece (its K and Q seen)
-            auto issue_s = [&](const Work& x, int j, int h) {
+            // Half h of S of tile j of this chain's in a piece (its K and Q seen).  (A descriptor is the first one's with a
+            // constant added: made anew for each, the issue of a product took longer than the product.)
+            auto issue_s = [&](const Work& x, int j, auto half) {
+                constexpr int h = decltype(half)::value;
                 const int sk = (x.base + x.x0 + j * x.step) % NSK;
-                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::KTILE + h * (K::KTILE / K::HALVES), 0);
+                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::KTILE, 0) + h * (K::KTILE / K::HALVES);
                 const uint32_t q_s = __shfl_sync(0xffffffffu, sb + K::OFF_Q + (x.q & 1) * K::QTILE, 0);
-                const uint32_t dst = s_i + __shfl_sync(0xffffffffu, h, 0) * K::HCOLS;
+                constexpr uint32_t dst = h * K::HCOLS;
                 if constexpr (FP8) {
                     constexpr uint32_t LO = D == 128 ? K::SLAB : 512;
+                    const uint64_t dq = smem_desc(q_s, 128, 1024), dk = smem_desc(kbase, 128, D * 8);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)      // the first term's, then the second's
-                        mma_ss_f8(lead, dst, smem_desc(q_s + (k / (D / 32)) * LO + (k % (D / 32)) * 256, 128, 1024),
-                                  smem_desc(kbase + (k % (D / 32)) * 256, 128, D * 8), idS, k > 0 ? 1u : 0u);
+                        mma_ss_f8(lead, s_i + dst, dq + (((k / (D / 32)) * LO + (k % (D / 32)) * 256) >> 4),
+                                  dk + (((k % (D / 32)) * 256) >> 4), idS, k > 0 ? 1u : 0u);
                 } else {
+                    const uint64_t dq = desc_sw128(q_s, 16, 1024), dk = smem_desc(kbase, 128, K::NCH * 128);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ss(lead, dst, desc_sw128(q_s + (k / 4) * K::SLAB + (k % 4) * 32, 16, 1024),
-                               smem_desc(kbase + k * 256, 128, K::NCH * 128), idS, k > 0 ? 1u : 0u);
+                        mma_ss(lead, s_i + dst, dq + (((k / 4) * K::SLAB + (k % 4) * 32) >> 4), dk + ((k * 256) >> 4), idS,
+                               k > 0 ? 1u : 0u);
                 }
                 commit(lead, bar(K::SFULL + 2 * i + h));
                 if (h == K::HALVES - 1) {
@@ -1447,30 +1451,47 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 // units up to the last page that a row sees
                 const int steps = HG * min(max((p.ends - (p.t0 + p.x0 + j * p.step) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
                 constexpr int HALVES = K::HALVES, EACH = kUnits / HALVES;
-#pragma unroll 1
-                for (int st = now ? 0 : HALVES; st < (then && fresh ? 2 * HALVES : HALVES); ++st) {
-                    const int h = st % HALVES;
-                    if (st < HALVES) {
-                        if (!(ok = wait_all(bar(K::PFULL + 2 * i + h), pcnt & 1))) break;
+                // a turn: P . V of half h, if there is a present tile, and S of it, if it belongs to the same piece; the second
+                // time (a new piece), S of both
+                auto turn = [&](auto half) -> bool {
+                    constexpr int h = decltype(half)::value;
+                    if (now) {
+                        if (!wait_all(bar(K::PFULL + 2 * i + h), pcnt & 1)) return false;
                         tc_fence_after();
-                        const int hu = __shfl_sync(0xffffffffu, h, 0);
+                        const uint64_t dv = smem_desc(vbase, K::NCH * 128, 128);
+                        if (steps == kUnits) {
 #pragma unroll
-                        for (int k = 0; k < EACH; ++k)
-                            mma_ts(lead && EACH * h + k < steps, o_i, s_i + hu * K::HCOLS + k * 8,
-                                   smem_desc(vbase + (EACH * hu + k) * K::PAGE, K::NCH * 128, 128), idPV, j > 0 || h > 0 || k > 0 ? 1u : 0u);
+                            for (int k = 0; k < EACH; ++k)
+                                mma_ts(lead, o_i, s_i + h * K::HCOLS + k * 8, dv + (((EACH * h + k) * K::PAGE) >> 4), idPV,
+                                       h > 0 || k > 0 ? 1u : j > 0 ? 1u : 0u);
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; k < min(EACH, steps - EACH * h); ++k)
+                                mma_ts(lead, o_i, s_i + h * K::HCOLS + k * 8, dv + (((EACH * h + k) * K::PAGE) >> 4), idPV,
+                                       j > 0 || h > 0 || k > 0 ? 1u : 0u);
+                        }
                         if (HALVES > 1) commit(lead, bar(K::PVDONE + 2 * i + h));
                         if (h == HALVES - 1) {
                             if (j + 1 == p.cnt) commit(lead, bar(K::ODONE + i));
                             commit(lead, bar(K::VEMPTY + sv));
                         }
                     }
-                    // (a new piece's Q and K: bf16, before the last P; FP8, whose Q the softmax warps split behind it, after)
-                    if (then && fresh && (FP8 || HALVES == 1 || !now ? st == HALVES : st == 0)) {
-                        if (!(ok = see_q(q.q) && see_k(q.base + q.x0))) break;
-                        tc_fence_after();
-                    }
-                    if (then && (!fresh || st >= HALVES)) issue_s(q, jq, h);
+                    return true;
+                };
+                using H0 = std::integral_constant<int, 0>;
+                using H1 = std::integral_constant<int, HALVES - 1>;
+                if (!(ok = turn(H0{}))) break;
+                // (a new piece's Q and K: bf16 by halves, before the last P; else, as FP8's softmax warps split Q behind it, after)
+                constexpr bool EARLY = !FP8 && HALVES > 1;
+                if (EARLY && then && fresh && !(ok = see_q(q.q) && see_k(q.base + q.x0))) break;
+                if (HALVES > 1) {
+                    if (then && !fresh) issue_s(q, jq, H0{});
+                    if (!(ok = turn(H1{}))) break;
                 }
+                if (!EARLY && then && fresh && !(ok = see_q(q.q) && see_k(q.base + q.x0))) break;
+                if (then && fresh) tc_fence_after();
+                if (then && (fresh && HALVES > 1)) issue_s(q, jq, H0{});
+                if (then) issue_s(q, jq, H1{});
                 if (now) {
                     bcnt += j + 1 == p.cnt && p.both;
                     ++pcnt;
