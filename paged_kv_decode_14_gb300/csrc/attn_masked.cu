@@ -750,41 +750,55 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     }
             }
         };
-        // (FP8) this lane's row of Q tile qt, in place: groups of 8 rows are 1024 bytes of a slab; the first term's codes go
-        // where the first slab was (D = 64: to the first half of each 1024 bytes), the second's to the other.
+        // (FP8) this warp's rows of Q tile qt, in place, 16 at a time, half a row a lane: groups of 8 rows are 1024 bytes of a
+        // slab; the first term's codes go where the first slab was (D = 64: to the first half of each 1024 bytes), the
+        // second's to the other.
         auto split_q = [&](int qt) {
             uint8_t* tile = smem + K::OFF_Q + (qt & 1) * K::QTILE;
-            constexpr int N = D / 8, LO = D == 128 ? K::SLAB : 512;
-            uint32_t top = 0;
-            uint4 x[N];
+            constexpr int N = D / 16;                     // 16-byte chunks of half a row
+            constexpr int LO = D == 128 ? K::SLAB : 512;
+            const int half = lane >> 4, w32 = (warp & 3) * 32;
+#pragma unroll 1
+            for (int row = w32 + (lane & 15); row < w32 + 32; row += 16) {
+                uint32_t top = 0;
+                uint4 x[N];
 #pragma unroll
-            for (int c = 0; c < N; ++c) {
-                x[c] = *reinterpret_cast<const uint4*>(tile + (c / 8) * K::SLAB + r * 128 + (((c & 7) ^ (r & 7)) * 16));
-                const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max(y[e] & 0x7fffu, y[e] >> 16 & 0x7fffu));
-            }
-            __syncwarp();
-            // 2^(134 - exponent) takes the largest element to [128, 256); kept inside fp32's normal range (a row below
-            // 2^-113 counts as smaller beside any scale); infinities and NaN make the row NaN
-            const int ex = min(max((int)(top >> 7), 14), 254);
-            const float f = __uint_as_float((uint32_t)(261 - ex) << 23);
-            q_scale[qt % K::NQS * kRows + r] = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ex - 7) << 23);
-            uint8_t* dst = tile + (r / 8) * 1024 + (r & 7) * 16;
-#pragma unroll
-            for (int c = 0; c < N / 2; ++c) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint4 y = x[2 * c + e / 2];
-                    uint32_t h0, h1, l0, l1;
-                    split2(e & 1 ? y.z : y.x, f, h0, l0);
-                    split2(e & 1 ? y.w : y.y, f, h1, l1);
-                    hi[e] = h0 | h1 << 16;
-                    lo[e] = l0 | l1 << 16;
+                for (int c = 0; c < N; ++c) {
+                    const int ch = half * N + c;          // (dimensions 8 ch .. 8 ch + 7)
+                    x[c] = *reinterpret_cast<const uint4*>(tile + (ch / 8) * K::SLAB + row * 128 + (((ch & 7) ^ (row & 7)) * 16));
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu),
+                                                 __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu)));
                 }
-                *reinterpret_cast<uint4*>(dst + c * 128) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(dst + LO + c * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                // 2^(134 - exponent) takes the largest element to [128, 256); kept inside fp32's normal range (a row below
+                // 2^-113 counts as smaller beside any scale); infinities and NaN make the row NaN
+                const int ex = min(max((int)(top >> 7), 14), 254);
+                const float f = __uint_as_float((uint32_t)(261 - ex) << 23);
+                const float inv = top >= 0x7f80u ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(ex - 7) << 23);
+                uint8_t* dst = tile + (row / 8) * 1024 + (row & 7) * 16 + half * (N / 2) * 128;
+#pragma unroll
+                for (int c = 0; c < N / 2; ++c) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 y = x[2 * c + e / 2];
+                        uint32_t h0, h1, l0, l1;
+                        split2(e & 1 ? y.z : y.x, f, h0, l0);
+                        split2(e & 1 ? y.w : y.y, f, h1, l1);
+                        hi[e] = h0 | h1 << 16;
+                        lo[e] = l0 | l1 << 16;
+                    }
+                    x[2 * c] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    x[2 * c + 1] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < N / 2; ++c) {
+                    *reinterpret_cast<uint4*>(dst + c * 128) = x[2 * c];
+                    *reinterpret_cast<uint4*>(dst + LO + c * 128) = x[2 * c + 1];
+                }
+                if (half == 0) q_scale[qt % K::NQS * kRows + row] = inv;
             }
             fence_proxy_async_smem();
         };
@@ -1060,11 +1074,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         // first keys at v and v1.  vs: their scales; where one is not finite, all its page's codes count as NaN (and it, as 1)
         auto widen_pages = [&](uint8_t* at, const Guard<HG>& gd, int v, int v1, int pages, const float* vs) -> bool {
             constexpr int N = D / 32;                     // 16-byte chunks of codes a lane and page
-            uint4 raw[2 * N];
-#pragma unroll
-            for (int j = 0; j < 2 * N; ++j)
-                raw[j] = *reinterpret_cast<const uint4*>(at + j / N * K::PAGE + K::LAND + (lane + 32 * (j % N)) * 16);
-            __syncwarp();
             // (a lane's chunk j % N of page j / N: its key of the page, and where it goes)
             auto key_of = [&](int j) { return (lane & 7) + ((lane + 32 * (j % N)) >> 3) / (D / 16) * 8; };
             auto place = [&](int j) {
@@ -1072,17 +1081,25 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 return at + j / N * K::PAGE + q / (D / 16) * (K::NCH * 128) + 2 * (q % (D / 16)) * 128 + (lane & 7) * 16;
             };
             uint32_t nan = 0;                             // a lane's chunks that hold NaN codes
+#pragma unroll 1
+            for (int pg = 0; pg < pages; ++pg) {          // (rolled, for the instruction cache)
+                uint4 raw[N];
 #pragma unroll
-            for (int j = 0; j < 2 * N; ++j) {
-                if (j >= N && pages < 2) break;
-                uint32_t o[8];
-                widen4(raw[j].x, o[0], o[1]);
-                widen4(raw[j].y, o[2], o[3]);
-                widen4(raw[j].z, o[4], o[5]);
-                widen4(raw[j].w, o[6], o[7]);
-                if (nan_codes(raw[j].x) | nan_codes(raw[j].y) | nan_codes(raw[j].z) | nan_codes(raw[j].w)) nan |= 1u << j;
-                *reinterpret_cast<uint4*>(place(j)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(place(j) + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                for (int j = 0; j < N; ++j)
+                    raw[j] = *reinterpret_cast<const uint4*>(at + pg * K::PAGE + K::LAND + (lane + 32 * j) * 16);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    uint32_t o[8];
+                    widen4(raw[j].x, o[0], o[1]);
+                    widen4(raw[j].y, o[2], o[3]);
+                    widen4(raw[j].z, o[4], o[5]);
+                    widen4(raw[j].w, o[6], o[7]);
+                    if (nan_codes(raw[j].x) | nan_codes(raw[j].y) | nan_codes(raw[j].z) | nan_codes(raw[j].w)) nan |= 1u << (pg * N + j);
+                    uint8_t* dst = place(j) + pg * K::PAGE;
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
             }
             const bool fin0 = fabsf(vs[0]) < INFINITY, fin1 = pages < 2 || fabsf(vs[1]) < INFINITY;
             if (!gd.any_of(v, kBlock) || (pages > 1 && !gd.any_of(v1, kBlock))) {
