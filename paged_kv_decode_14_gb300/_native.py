@@ -124,7 +124,7 @@ def lib():
                                                c.c_float, vp, c.c_size_t, vp, vp]
             L.pkv_masked_workspace_size.restype = c.c_size_t
             L.pkv_masked_workspace_size.argtypes = []
-            masked = [pc, vp, vp, vp, i64, vp, i32, vp, vp, vp, i32, i32]
+            masked = [vp, vp, vp, vp, i64, vp, i32, vp, vp, vp, i32, i32]
             L.pkv_paged_attention_window.restype = c.c_int
             L.pkv_paged_attention_window.argtypes = masked + [i32, i32, c.c_float, vp, c.c_size_t, vp]
             L.pkv_paged_attention_tree.restype = c.c_int
@@ -132,7 +132,7 @@ def lib():
             L.pkv_block_tables_update.restype = c.c_int
             L.pkv_block_tables_update.argtypes = [vp, i32, vp, vp, i32, vp, vp, i64, vp, vp, vp, vp, i64, vp, vp]
             L.pkv_paged_kv_keep_path.restype = c.c_int
-            L.pkv_paged_kv_keep_path.argtypes = [pc, vp, i32, vp, vp, vp, i32, vp, i32, vp, vp]
+            L.pkv_paged_kv_keep_path.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, i32, vp, vp]
             L.pkv_copy_blocks.restype = c.c_int
             L.pkv_copy_blocks.argtypes = [c.POINTER(CacheDesc), vp, i32, vp, vp, vp]
             L.pkv_debug_set_wait_limit.restype = None
@@ -348,6 +348,7 @@ def prefill(cache: PagedKVCache, q, block_tables, context_lens, q_lens, max_q_le
 # ------------------------------------------------------------------ rows
 
 _ROWS = struct.Struct("@Pqqi4x")            # pkv_rows
+_CACHE = struct.Struct("@qiiiiPPPP")        # pkv_cache
 _ROW_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "ramp": 4}
 
@@ -589,9 +590,31 @@ def make_masked_workspace(device="cuda", stream=None):
     """A workspace for attention_window and attention_tree on the given device, zeroed on its current stream (or
     `stream`): calls on other streams wait for that."""
     with torch.cuda.device(device):
-        ws = torch.empty(int(lib().pkv_masked_workspace_size()), dtype=torch.uint8, device=device)
+        ws = _new(stream, torch.empty, int(lib().pkv_masked_workspace_size()), dtype=torch.uint8, device=device)
         workspace_init(ws, stream)
     return ws
+
+
+def _cache_pack(cache, device):
+    """pkv_cache of a cache on the given GPU."""
+    k, v, ks, vs = cache.k, cache.v, cache.k_scales, cache.v_scales
+    if k.get_device() != device or v.get_device() != device:
+        raise ValueError("the cache must be on the same GPU as the other tensors")
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("cache buffers must be contiguous")
+    for t in (ks, vs):
+        if t is not None and (t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != device):
+            raise ValueError("scales must be contiguous float32 on the same GPU")
+    return _CACHE.pack(cache.num_blocks, 16, cache.num_kv_heads, cache.head_dim,
+                       KV_FP8_E4M3 if cache.kv_dtype == "fp8" else KV_BF16, k.data_ptr(), v.data_ptr(),
+                       0 if ks is None else ks.data_ptr(), 0 if vs is None else vs.data_ptr())
+
+
+def _tables_of(block_tables, device, n):
+    """Pointer and width of block_tables [n, width]."""
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    return _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()), block_tables.shape[1]
 
 
 def _masked(cache, q, block_tables, context_lens, q_lens, workspace, out, lse, q_starts, stream):
@@ -599,20 +622,16 @@ def _masked(cache, q, block_tables, context_lens, q_lens, workspace, out, lse, q
     device, bf16, shape = _device_of(q, "q"), torch.bfloat16, q.shape
     if len(shape) != 3 or shape[2] != cache.head_dim:
         raise ValueError("q must be [rows, heads, head_dim of the cache]")
-    n = context_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != n:
-        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    _check_cache_device(cache, device)
+    n, rows, i32 = context_lens.numel(), shape[0], torch.int32
     qr = _row_view(q, "q", bf16, device, shape)
     out, orow = _row_output(out, "out", q, bf16, device, shape, stream)
     if lse is None:
-        lse = _new(stream, torch.empty, shape[:2], dtype=torch.float32, device=q.device)
+        lse = _new(stream, torch.empty, (rows, shape[1]), dtype=torch.float32, device=q.device)
     if workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the same GPU")
-    args = (ctypes.byref(cache.desc()), qr, orow, _vector(lse, "lse", torch.float32, device, shape[0] * shape[1]),
-            shape[0], _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()),
-            block_tables.shape[1], _vector(context_lens, "context_lens", torch.int32, device, n),
-            _vector(q_lens, "q_lens", torch.int32, device, n),
+    args = (_cache_pack(cache, device), qr, orow, _vector(lse, "lse", torch.float32, device, rows * shape[1]), rows,
+            *_tables_of(block_tables, device, n), _vector(context_lens, "context_lens", i32, device, n),
+            _vector(q_lens, "q_lens", i32, device, n),
             None if q_starts is None else _vector(q_starts, "q_starts", torch.int64, device, n), n)
     return device, out, lse, args, (workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
@@ -667,41 +686,37 @@ def update_tables(pool: BlockPool, block_tables, context_lens, grow, num_rows: i
     granted int32, row_starts int64 [num_seqs]), new tensors unless given: what an append and the attention of
     the new tokens take as slot_mapping, positions, q_lens and q_starts."""
     device, n, num_rows = _device_of(block_tables, "block_tables"), context_lens.numel(), int(num_rows)
-    if block_tables.dim() != 2 or block_tables.shape[0] != n:
-        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    i32, i64 = torch.int32, torch.int64
+    if num_rows < 0:
+        raise ValueError("num_rows must not be negative")
 
     def output(t, name, dtype, numel):
         if t is None:
             t = _new(stream, torch.empty, numel, dtype=dtype, device=block_tables.device)
+            return t, t.data_ptr()
         return t, _vector(t, name, dtype, device, numel)
 
-    slots, sp = output(slots, "slots", torch.int64, num_rows)
-    positions, pp = output(positions, "positions", torch.int32, num_rows)
-    granted, gp = output(granted, "granted", torch.int32, n)
-    row_starts, rp = output(row_starts, "row_starts", torch.int64, n)
-    _call("pkv_block_tables_update", device, stream,
-          _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()), block_tables.shape[1],
-          _vector(context_lens, "context_lens", torch.int32, device, n), _vector(grow, "grow", torch.int32, device, n),
-          n, _vector(pool.free, "pool.free", torch.int32, device, pool.num_blocks),
-          _vector(pool.count, "pool.count", torch.int32, device, 1), pool.num_blocks, sp, pp, gp, rp, num_rows,
-          _error_word(device_error, device))
+    slots, sp = output(slots, "slots", i64, num_rows)
+    positions, pp = output(positions, "positions", i32, num_rows)
+    granted, gp = output(granted, "granted", i32, n)
+    row_starts, rp = output(row_starts, "row_starts", i64, n)
+    _call("pkv_block_tables_update", device, stream, *_tables_of(block_tables, device, n),
+          _vector(context_lens, "context_lens", i32, device, n), _vector(grow, "grow", i32, device, n), n,
+          _vector(pool.free, "pool.free", i32, device, pool.num_blocks), _vector(pool.count, "pool.count", i32, device, 1),
+          pool.num_blocks, sp, pp, gp, rp, num_rows, _error_word(device_error, device))
     return slots, positions, granted, row_starts
 
 
 def keep_path(cache: PagedKVCache, block_tables, context_lens, q_lens, path, path_lens, device_error=None, stream=None):
     """pkv_paged_kv_keep_path: the accepted nodes of each sequence's tree (path int32 [num_seqs, max_path], strictly
     ascending, path_lens int32 [num_seqs] of them) moved to the places behind the context, in the cache."""
-    device, n = _device_of(block_tables, "block_tables"), context_lens.numel()
-    _check_cache_device(cache, device)
-    if block_tables.dim() != 2 or block_tables.shape[0] != n:
-        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    device, n, i32 = _device_of(block_tables, "block_tables"), context_lens.numel(), torch.int32
     if path.dim() != 2 or path.shape[0] != n:
         raise ValueError("path must be [num_seqs, max_path]")
-    _call("pkv_paged_kv_keep_path", device, stream, ctypes.byref(cache.desc()),
-          _vector(block_tables, "block_tables", torch.int32, device, block_tables.numel()), block_tables.shape[1],
-          _vector(context_lens, "context_lens", torch.int32, device, n),
-          _vector(q_lens, "q_lens", torch.int32, device, n), _vector(path, "path", torch.int32, device, path.numel()),
-          path.shape[1], _vector(path_lens, "path_lens", torch.int32, device, n), n, _error_word(device_error, device))
+    _call("pkv_paged_kv_keep_path", device, stream, _cache_pack(cache, device), *_tables_of(block_tables, device, n),
+          _vector(context_lens, "context_lens", i32, device, n), _vector(q_lens, "q_lens", i32, device, n),
+          _vector(path, "path", i32, device, path.numel()), path.shape[1],
+          _vector(path_lens, "path_lens", i32, device, n), n, _error_word(device_error, device))
 
 
 def read_device_error(error_word, stream=None) -> int:

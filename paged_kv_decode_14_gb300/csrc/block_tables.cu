@@ -49,38 +49,35 @@ constexpr int kArrays = 6;
 
 __device__ __forceinline__ int blocks(int tokens) { return (int)(((unsigned)tokens + kBlock - 1) / kBlock); }
 
-// Exclusive sums over the CTA's threads of two values; *total_a, *total_b their sums.
-__device__ void scan2(int64_t& a, int64_t& b, int64_t* total_a, int64_t* total_b, int64_t (*part)[2]) {
+// Exclusive sums over the CTA's threads of N values, and their sums.
+template <int N>
+__device__ __forceinline__ void scan(int64_t (&v)[N], int64_t (&total)[N], int64_t (*part)[3]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = a, y = b;
+    int64_t x[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) {
-            x += p;
-            y += q;
+    for (int i = 0; i < N; ++i) {
+        x[i] = v[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t p = __shfl_up_sync(0xffffffffu, x[i], o);
+            if (lane >= o) x[i] += p;
         }
+        if (lane == 31) part[warp][i] = x[i];
     }
     __syncthreads();
-    if (lane == 31) {
-        part[warp][0] = x;
-        part[warp][1] = y;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int64_t mine = part[lane][i];                // (32 warps; every warp sums them for itself)
+        int64_t u = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t p = __shfl_up_sync(0xffffffffu, u, o);
+            if (lane >= o) u += p;
+        }
+        total[i] = __shfl_sync(0xffffffffu, u, 31);
+        v[i] = x[i] - v[i] + __shfl_sync(0xffffffffu, u - mine, warp);
     }
     __syncthreads();
-    int64_t u = part[lane][0], v = part[lane][1];         // (32 warps; every warp sums them for itself)
-    const int64_t u0 = u, v0 = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t p = __shfl_up_sync(0xffffffffu, u, o), q = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) {
-            u += p;
-            v += q;
-        }
-    }
-    *total_a = __shfl_sync(0xffffffffu, u, 31);
-    *total_b = __shfl_sync(0xffffffffu, v, 31);
-    a = x - a + __shfl_sync(0xffffffffu, u - u0, warp);
-    b = y - b + __shfl_sync(0xffffffffu, v - v0, warp);
 }
 
 // The last i of [0, n) with at[i] <= x (at ascending, at[0] <= x).
@@ -96,7 +93,7 @@ __device__ __forceinline__ int find(const int* at, int n, int x) {
 
 __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
     extern __shared__ int smem[];
-    __shared__ int64_t part[32][2];
+    __shared__ int64_t part[32][3];
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_seqs;
@@ -144,52 +141,60 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
         }
         __syncthreads();
     }
-    // sums, each thread over consecutive requests
+    // sums, each thread over consecutive requests: rows, blocks that come back, blocks needed
     const int each = (n + kThreads - 1) / kThreads, b0 = min(tid * each, n), b1 = min(b0 + each, n);
-    int64_t rows = 0, back = 0, all_rows, all_back;
+    auto need_of = [&](int b) { return s.change[b] > 0 ? blocks(s.len[b] + s.change[b]) - blocks(s.len[b]) : 0; };
+    int64_t at[3] = {0, 0, 0}, all[3];
     for (int b = b0; b < b1; ++b) {
-        rows += s.rows[b];
-        back += s.back[b];
+        at[0] += s.rows[b];
+        at[1] += s.back[b];
+        at[2] += need_of(b);
     }
-    scan2(rows, back, &all_rows, &all_back, part);
-    int64_t need = 0, none = 0, all_need, all_none;
-    for (int b = b0; b < b1; ++b) {
-        const int mine = s.back[b];
-        back += mine;
-        s.back[b] = (int)(all_back - back);               // of later requests
-        s.row[b] = (int)min(rows, (int64_t)0x7fffffff);
-        rows += s.rows[b];
-        if (s.change[b] > 0 && rows > a.num_rows) {       // its rows do not fit
-            errors |= PKV_DEVERR_LENGTH;
-            s.change[b] = 0;
+    scan(at, all, part);
+    const int64_t all_rows = all[0], all_back = all[1];
+    int64_t all_need = all[2];
+    if (all_rows > a.num_rows) {                          // the requests whose rows do not fit get nothing
+        errors |= PKV_DEVERR_LENGTH;
+        int64_t rows = at[0], need[1] = {0}, sum[1];
+        for (int b = b0; b < b1; ++b) {
+            rows += s.rows[b];
+            if (s.change[b] > 0 && rows > a.num_rows) s.change[b] = 0;
+            need[0] += need_of(b);
         }
-        if (s.change[b] > 0) need += blocks(s.len[b] + s.change[b]) - blocks(s.len[b]);
+        scan(need, sum, part);
+        at[2] = need[0];
+        all_need = sum[0];
     }
-    if (all_rows > a.num_rows) errors |= PKV_DEVERR_LENGTH;
-    scan2(need, none, &all_need, &all_none, part);
     const int64_t room = count < 0 ? 0 : a.num_blocks - count;
     if (all_back > room) errors |= PKV_DEVERR_BLOCK_ID;   // (a block was given back twice)
     const int top = count < 0 ? 0 : (int)(count + min(all_back, room));
     int taken = 0;                                        // blocks needed by the requests that get theirs, up to here
     for (int b = b0; b < b1; ++b) {
-        s.need[b] = (int)min(need, (int64_t)0x7fffffff);
-        if (s.change[b] <= 0) continue;
-        const int c = blocks(s.len[b] + s.change[b]) - blocks(s.len[b]);
-        need += c;
-        if (c > 0 && need > top) {                        // not enough are free
+        s.row[b] = (int)min(at[0], (int64_t)0x7fffffff);
+        at[0] += s.rows[b];
+        at[1] += s.back[b];
+        s.back[b] = (int)(all_back - at[1]);              // of later requests
+        s.need[b] = (int)min(at[2], (int64_t)0x7fffffff);
+        const int c = need_of(b);
+        at[2] += c;
+        if (c > 0 && at[2] > top) {                       // not enough are free
             errors |= PKV_DEVERR_NO_BLOCKS;
             s.change[b] = 0;
         } else if (c > 0) {
-            taken = (int)need;
+            taken = (int)at[2];
         }
     }
-    taken = __reduce_max_sync(0xffffffffu, taken);
+    if (all_need <= top) {
+        taken = (int)all_need;
+    } else {
+        taken = __reduce_max_sync(0xffffffffu, taken);
+        if (lane == 0) part[warp][0] = taken;
+        __syncthreads();
+        taken = __reduce_max_sync(0xffffffffu, (int)part[lane][0]);
+    }
     __syncthreads();
-    if (lane == 0) part[warp][0] = taken;
-    __syncthreads();
-    taken = __reduce_max_sync(0xffffffffu, (int)part[lane][0]);
 
-    cluster.sync();                                       // every CTA has read the old state
+    if (ctas > 1) cluster.sync();                         // every CTA has read the old state
     if (any_drop) {
         // last block first: a request's entries are taken from its end
         for (int b = warp * ctas + rank; b < n; b += kThreads / 32 * ctas) {
@@ -208,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
             }
         }
         __threadfence();
-        cluster.sync();                                   // the stack is whole
+        if (ctas > 1) cluster.sync();                     // the stack is whole
+        else __syncthreads();
     }
     const int64_t first = (int64_t)rank * kThreads + tid, stride = (int64_t)ctas * kThreads;
     auto block_of = [&](int b, int j) -> int {            // request b's block j, which is new
@@ -224,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
         if (s.change[b] > 0 && j < blocks(s.len[b] + s.change[b])) a.table[(int64_t)b * a.max_blocks + j] = block_of(b, j);
     }
     const int64_t shown = min(all_rows, a.num_rows);
+#pragma unroll 4
     for (int64_t r = first; r < shown; r += stride) {
         const int b = find(s.row, n, (int)r);
         const int64_t at = (int64_t)s.len[b] + (r - s.row[b]);
@@ -285,7 +292,7 @@ cudaError_t launch_block_tables(int32_t* table, int max_blocks, int32_t* lens, c
     attr[1].val.clusterDim.x = ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, update_kernel, a);
 }
 
