@@ -604,26 +604,37 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, co
  *   lse            optional device fp32 [num_q_rows][Hq]
  *   block_tables   as for pkv_paged_attention; entries of blocks that no query sees are never read, so blocks
  *                  behind the window may have been given back
- *   context_lens, q_lens   device int32 [num_seqs], 0 <= q_lens[b] <= context_lens[b]
+ *   context_lens, q_lens   device int32 [num_seqs], 0 <= q_lens[b] <= context_lens[b] <= 2^31 - 512
  *   q_starts       device int64 [num_seqs], each sequence's first row of q and out, or NULL: packed.  Rows
  *                  outside every sequence are left as they were
- *   max_q_len      host upper bound of q_lens, >= 1
+ *   num_q_rows     rows of q and out; 0: nothing is launched, so nothing is reported
+ *   max_q_len      host upper bound of q_lens, >= 1.  It chooses the kernel (how many kv-heads share a row tile): a
+ *                  bound far above the lengths costs speed
  *   window         >= 1;  sinks >= 0
  *   scale          finite, > 0
  *   workspace      >= pkv_masked_workspace_size() bytes, 16-byte aligned, zeroed once (pkv_workspace_init), not
  *                  shared by concurrent calls (or by graphs that may run at the same time).  Its first 4 bytes are
- *                  the device error word.  After PKV_DEVERR_TIMEOUT zero it again before reusing it.
+ *                  the device error word.  After PKV_DEVERR_TIMEOUT zero it again before reusing it.  (About 42 MB
+ *                  whatever the call; head dimension, lengths and masks may change from call to call.)
  * A sequence with a bad length, a table row that is too short, or rows outside num_q_rows sets PKV_DEVERR_LENGTH
  * and its rows are left as they were; a bad block id sets PKV_DEVERR_BLOCK_ID and the results that see it are
- * unspecified.
+ * unspecified.  A call of more than 2^31 units of work (a unit: 128 rows times 128 keys) sets PKV_DEVERR_LENGTH and
+ * writes nothing.
  *
- * Precision: q . k in bf16 (FP8 codes widened exactly, the page's scale applied in fp32) with fp32 accumulation;
- * weights rounded to bf16 for the product with V (8 significant bits; FP8: after the page's scale has been applied in
- * fp32), their sum in fp32 before that.  Finite logits scale * q . k may reach 2^28 in magnitude; from about 1.4 times
- * that on PKV_DEVERR_RANGE is set and the row's results are unspecified.  NaN or infinity in a key or value row
- * reaches the queries that see it, and no other (an infinite value as NaN where its weight rounds to 0).
- * Deterministic.  One launch; it reads nothing before the previous kernel on the stream has completed, and lets the
- * next start once it has.  The wait limit and hold flag of pkv_debug_set_wait_limit apply.
+ * Precision: fp32 accumulation throughout.  bf16 cache: q . k in bf16.  FP8 cache: a row of q, times a power of two, is
+ * split into two e4m3 terms (exact but for elements below 2^-10 of the row's largest, which are good to 2^-17 of it) and
+ * multiplied with the codes as they are; the page's scale is applied to the sum in fp32; values are widened exactly.
+ * Weights 2^(s - m) are rounded to bf16 for the product with V (8 significant bits; FP8: after the page's scale has been
+ * applied in fp32), their sum is formed in fp32 before that.  m is the largest logit of a row's first keys, or a
+ * later one: 64 weights may add up to 2^14 before it rises, so O may reach 2^14 times the largest value times the keys
+ * (values of 2^96 and more may overflow).  Finite logits scale * q . k may reach 2^28 in magnitude; from about 1.4
+ * times that on PKV_DEVERR_RANGE is set and the row's results are unspecified.  NaN or infinity in a key or value row
+ * or an FP8 page's scale reaches the queries that see it, and no other (an infinite value as NaN where its weight
+ * rounds to 0).  Deterministic: the same call gives the same bits.
+ *
+ * One launch.  It reads and writes nothing before the previous kernel on the stream has completed, and does not let the
+ * next start early (out may be the q of a pkv_paged_attention behind it).  A wait inside it that runs out (pkv_debug_set_wait_limit; no piece of a call's work
+ * comes near the limit) sets PKV_DEVERR_TIMEOUT, and all of the call's results are unspecified.
  */
 PKV_API size_t pkv_masked_workspace_size(void);
 PKV_API pkv_status pkv_paged_attention_window(const pkv_cache* cache, const pkv_rows* q, const pkv_rows* out, float* lse,
@@ -690,7 +701,7 @@ PKV_API pkv_status pkv_block_tables_update(int32_t* block_tables, int32_t max_bl
  * they are; pkv_block_tables_update drops them (grow = path_lens - q_lens).
  *
  *   path           device int32 [num_seqs][max_path], strictly ascending nodes (a parent stands before its
- *                  children), 0 <= path[i] < Q_b; path_lens[b] <= min(Q_b, max_path)
+ *                  children), 0 <= path[i] < Q_b; path_lens[b] <= min(Q_b, max_path); max_path < 2^27 - 128
  *   context_lens, q_lens   as for pkv_paged_attention_tree (before the drop)
  * FP8: codes that stay in their block move unchanged; between blocks a code becomes e4m3_rne_satfinite(code *
  * scale of its block / scale of the new one), in IEEE fp32.  Page scales are not changed.

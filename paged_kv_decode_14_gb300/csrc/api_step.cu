@@ -123,7 +123,7 @@ PKV_API pkv_status pkv_paged_kv_keep_path(const pkv_cache* cache, const int32_t*
     if (num_seqs == 0) return PKV_OK;
     if (!block_tables || !context_lens || !q_lens || !path_lens || (max_path > 0 && !path) || max_blocks_per_seq <= 0)
         return PKV_ERR_INVALID_ARG;
-    if ((int64_t)num_seqs * cache->num_kv_heads > 0x7fffffff / 2) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)num_seqs * cache->num_kv_heads > 0x7fffffff / 2 || max_path > 0x7fffffff / 16 - 128) return PKV_ERR_UNSUPPORTED;
     return launch_keep_path(*cache, block_tables, max_blocks_per_seq, context_lens, q_lens, path, max_path, path_lens,
                             num_seqs, device_error, (cudaStream_t)stream) == cudaSuccess
                ? PKV_OK

@@ -64,13 +64,17 @@ constexpr int kReady = 8, kProducer = 12, kMma = 13, kPlan = 15;
 constexpr int kPieces = 4;                 // pieces of work planned ahead
 constexpr int kFlags = 8;                  // pieces whose "non-finite V" flags are kept
 constexpr int kMaxCtas = 160;              // CTAs of a launch (two workspace slots each)
-// what an item costs beside its key tiles, in key tiles of one row tile
-template <int HG>
-constexpr int kItemUnits = HG == 1 ? 4 : 2;
+// what an item costs beside its key tiles, in units (key tiles of one row tile): four 2k prompts take 117 us with 4, 149 with
+// 2 and 119 with 8
+constexpr int kItemUnits = 4;
 constexpr uint32_t kWaitHint = 20000;     // ns that a wait may sleep before it looks at the abort flag
 constexpr int kAhead = 3;                  // tiles that an FP8 page's scales are fetched ahead
-constexpr int kCutUnits = 8;               // what cutting an item costs, in units
+// What cutting an item costs, in units.  Where there is a CTA for every item and none is longer than its share by more than
+// this, each is dealt whole: 32 requests of 256 keys, two kv-heads an item, 14.8 us against 24.0 with their items cut.
+constexpr int kCutUnits = 8;
 constexpr int kMinUnits = 4;               // units that a CTA has at least
+constexpr int kFp8Tiles = 16;              // key tiles a CTA (of one kv-head) that count as much FP8 work
+constexpr int kMaxLen = 0x7ffffe00;        // of a context: places of its last tile stay below 2^31
 
 struct Arg {
     CUtensorMap q;
@@ -237,7 +241,7 @@ struct Plan {
     __device__ __forceinline__ int per() const { return HG == 1 ? 2 * a.pb : a.pb; }
     __device__ __forceinline__ Seq load(int i, int64_t rows, bool report) const {
         Seq x{a.q_starts ? a.q_starts[i] : rows, a.q_lens[i], a.ctx_lens[i]};
-        if (x.Q < 0 || x.Q > a.max_q_len || x.L < x.Q || x.row < 0 || x.row > a.num_q_rows - x.Q ||
+        if (x.Q < 0 || x.Q > a.max_q_len || x.L < x.Q || x.L > kMaxLen || x.row < 0 || x.row > a.num_q_rows - x.Q ||
             (x.Q > 0 && (x.L - 1) / kBlock >= a.max_blocks)) {
             if (report && (x.Q != 0 || x.L < 0)) raise_error(a.err, PKV_DEVERR_LENGTH);
             x.Q = 0;
@@ -259,7 +263,7 @@ struct Plan {
         }
         tiles = (p.np + TP - 1) / TP;
         each = HG == 1 && p.nq > a.pb ? 2 : 1;
-        return flat ? 1 : tiles * each + kItemUnits<HG>;
+        return flat ? 1 : tiles * each + kItemUnits;
     }
     template <typename V>
     __device__ __forceinline__ V scan(V x) const {        // the sum over earlier lanes
@@ -295,7 +299,6 @@ struct Plan {
         int64_t fp = 0, items = 0;
         total = u = u1 = 0;
         flat = false;
-        // (a third turn, between the two, where the items turn out to be dealt whole)
 #pragma unroll 1
         for (int turn = 0; turn < 2; ++turn) {
             const bool here = turn == 1 && u >= before && u < before + mine;
@@ -337,18 +340,14 @@ struct Plan {
                 }
                 total = (int)sum;
                 int ctas = max(1, min((int)gridDim.x, total / kMinUnits));
-                // few and short items: a join would cost more than it spreads
-                if (!flat) {
-                    const int n = (int)__reduce_add_sync(0xffffffffu, (unsigned)min(items, (int64_t)1 << 16));
-                    most = __reduce_max_sync(0xffffffffu, most);
-                    if (n <= (int)gridDim.x && most <= total / ctas + kCutUnits) {
-                        flat = true;
-                        before = 0;
-                        turn = -1;
-                        continue;
-                    }
+                const int n = (int)__reduce_add_sync(0xffffffffu, (unsigned)min(items, (int64_t)1 << 16));
+                most = __reduce_max_sync(0xffffffffu, most);
+                flat = n <= (int)gridDim.x && most <= total / ctas + kCutUnits;
+                if (flat) {
+                    mine = items;
+                    before = scan(mine);
+                    total = ctas = n;
                 }
-                if (flat) ctas = total;
                 if ((int)blockIdx.x >= ctas || total == 0) return;
                 share = (int)((uint32_t)total / (uint32_t)ctas);
                 longer = total - share * ctas;
@@ -372,7 +371,7 @@ struct Plan {
         while (u < u1 && !some) {
             int tiles, each;
             const int w = span(s, blk, p, tiles, each);
-            const int keys = start + kItemUnits<HG>;          // the first tile's first unit
+            const int keys = start + kItemUnits;          // the first tile's first unit
             auto tile_at = [&](int x) { return flat ? (x > start ? tiles : 0) : x <= keys ? 0 : min(tiles, (x - keys + each - 1) >> (each - 1)); };
             p.t0 = tile_at(u);
             p.t1 = tile_at(u1);
@@ -521,8 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
     }
     // every role goes through here, from its own code path (non-.aligned barrier); the tensor memory's address
     auto enter = [&]() -> uint32_t {
-        griddep_wait();
-        griddep_launch();
+        griddep_wait();                                   // (no early trigger: pkv_paged_attention reads its q before its own wait)
         tc_fence_before();
         cta_bar_sync();
         tc_fence_after();
@@ -859,7 +857,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     // (what no row sees behind the first half is not read by the PV)
                     if (live && !(h > 0 && v0 >= ends)) {
                         tc_fence_after();
-                        if (FP8 && hh == 0) sc = a.scale_log2 * q_scale[qt % K::NQS * kRows + r];
+                        if (FP8 && hh == 0) {
+                            sc = a.scale_log2 * q_scale[qt % K::NQS * kRows + r];
+                            if (sc == 0.f) sc = 0x1p-149f;         // (a row of zeros, a tiny scale: -inf * 0 would be NaN)
+                        }
                         const bool masked =
                             !__all_sync(0xffffffffu, (v0 >= see.wl && v0 + STEP - 1 <= see.wh) || v0 + STEP <= see.ns);
                         // S and P of page pg of the half: columns of this row's head
@@ -1567,9 +1568,21 @@ cudaError_t launch_masked(const pkv_cache& c, const pkv_rows* q, const pkv_rows*
     if (sms <= 0 || !encoder()) return cudaErrorUnknown;
     const int G = q->num_heads / c.num_kv_heads;
     Arg a = {};
-    // as many kv-heads an item as their rows fit in a row tile
+    const unsigned grid = (unsigned)std::min(sms, kMaxCtas);
+    // As many kv-heads an item as their rows fit in a row tile (96 requests of 1024 keys, one query each, 32/8 heads of 128:
+    // 70 us with 4, 82 with 1; FP8 66 and 93) ...
+    const bool fp8 = c.kv_dtype == PKV_KV_FP8_E4M3;
     const int rows = std::min<int64_t>((int64_t)max_q_len * G, kRows);
-    const int hg = rows <= kRows / 4 && c.num_kv_heads % 4 == 0 ? 4 : rows <= kRows / 2 && c.num_kv_heads % 2 == 0 ? 2 : 1;
+    int hg = rows <= kRows / 4 && c.num_kv_heads % 4 == 0 ? 4 : rows <= kRows / 2 && c.num_kv_heads % 2 == 0 ? 2 : 1;
+    // ... but fewer while there is still a CTA for every item (there are no more queries than a row tile has), as uncut items
+    // need no join and cut ones a smaller: 1 request of 256, 4096 or 32k keys 11, 18 or 39 us with 1 against 16, 28 or 62
+    // with 4; 32 of 1024 keys 29 with 2, 35 with 4.  Not for much FP8 work in 8 items and more, by the longest context that
+    // there can be: there HG = 4's quicker tiles count for more (4 of 32k keys 77 us with 4, 91 with 1; below the limit, 16 of
+    // 1024 keys 32 and 23).
+    const int64_t keys = std::min<int64_t>((int64_t)max_blocks * kBlock, tree ? INT32_MAX : (int64_t)window + sinks + max_q_len);
+    const int64_t heads = (int64_t)num_seqs * c.num_kv_heads;
+    if (!(fp8 && heads / hg >= 8 && heads * keys > (int64_t)grid * kFp8Tiles * kCols))
+        while (hg > 1 && heads * 2 / hg <= grid) hg /= 2;
     a.pb = kRows / hg / G;
     if (!make_map(&a.q, q, q->data, PKV_BF16, c.head_dim, num_q_rows, G, a.pb)) return cudaErrorInvalidValue;
     a.k_cache = (const uint8_t*)c.k_cache;
@@ -1602,8 +1615,7 @@ cudaError_t launch_masked(const pkv_cache& c, const pkv_rows* q, const pkv_rows*
     a.window = window;
     a.sinks = sinks;
     a.scale_log2 = scale * kLog2e;
-    const unsigned grid = (unsigned)std::min(sms, kMaxCtas);
-    if (c.kv_dtype == PKV_KV_FP8_E4M3)
+    if (fp8)
         return c.head_dim == 128 ? launch_hg<128, true>(a, hg, grid, st) : launch_hg<64, true>(a, hg, grid, st);
     return c.head_dim == 128 ? launch_hg<128, false>(a, hg, grid, st) : launch_hg<64, false>(a, hg, grid, st);
 }

@@ -244,6 +244,24 @@ def test_bad_lengths_leave_their_rows(workspace):
     assert (out[s.starts[3]] == 7.0).all()
 
 
+@pytest.mark.parametrize("length", [(1 << 31) - 1, (1 << 31) - 512, (1 << 31) - 511])
+def test_a_context_near_2_to_31_is_refused(length, workspace):
+    """(At most 2^31 - 512 positions; the longest that is taken reads a window's pages at the table's end.)"""
+    s = windowed([40, 30], [1, 1], 1000, 0, heads=4, kv_heads=2, dim=64, dtype="bf16", seed=6)
+    table = torch.zeros(2, 1 << 27, dtype=torch.int32, device="cuda")
+    table[:, :2] = s.table[:, :2]
+    table[1, :2] = s.table[0, 0]
+    table[1, -40:] = s.table[0, 0]
+    out = torch.full_like(s.q, 7.0)
+    nat.attention_window(s.cache, s.q, table, ints([16, length]), s.t_q, 1, 16, 0, s.scale, workspace, out=out)
+    fits = length <= (1 << 31) - 512
+    assert nat.read_device_error(workspace) == (0 if fits else nat.DEVERR_LENGTH)
+    assert not (out[0] == 7.0).any() and bool((out[1] == 7.0).all()) != fits
+    if fits:                                                     # a window that is one whole page: the same keys as sequence 0's
+        one = nat.attention_window(s.cache, s.q[1:], table[:1], ints([16]), ints([1]), 1, 16, 0, s.scale, workspace)[0]
+        assert torch.equal(out[1], one[0])
+
+
 def test_a_bad_block_is_reported(workspace):
     s = windowed([100], [1], 1000, 0, heads=4, kv_heads=2, dim=64, dtype="bf16", seed=6)
     for bad in (-1, s.cache.num_blocks):
@@ -319,6 +337,17 @@ def test_queries_of_any_size(size, dtype, workspace):
     if size > 1:
         s.scale /= size
     out, lse = nat.attention_window(s.cache, s.q, s.table, s.t_lens, s.t_q, s.max_q, 100, 3, s.scale, workspace)
+    assert nat.read_device_error(workspace) == 0
+    check(out, lse, s.reference())
+
+
+@pytest.mark.parametrize("q_len", [1, 80])
+def test_rows_of_zeros_with_a_tiny_scale(q_len, workspace):
+    """A scale whose product with an FP8 row's power of two leaves fp32: still the mean of what is visible."""
+    s = windowed([200, 90], [q_len, q_len], 50, 3, heads=8, kv_heads=2, dim=64, dtype="fp8", seed=8)
+    s.q.zero_()
+    s.scale = 1e-30
+    out, lse = nat.attention_window(s.cache, s.q, s.table, s.t_lens, s.t_q, s.max_q, 50, 3, s.scale, workspace)
     assert nat.read_device_error(workspace) == 0
     check(out, lse, s.reference())
 

@@ -105,3 +105,4 @@ def test_keep_path_refusals(L):
     for what in ("bt", "cl", "ql", "path", "lens"):
         assert call(**{what: None}) == INVALID
     assert call(seqs=1 << 30) == UNSUPPORTED
+    assert call(most=1 << 27) == UNSUPPORTED
