@@ -27,6 +27,7 @@ constexpr int kCluster = 8;
 constexpr int kManyRows = 2048;
 // Blocks up to which a request's dropped blocks are one thread's work, not a warp's: a token's or a tree's worth.
 constexpr int kFew = 4;
+constexpr int kLoads = 4;                  // entries a lane has in flight where a warp gives a request's blocks back
 
 struct Arg {
     int32_t* table;
@@ -153,10 +154,15 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
         warps(warp, kThreads / 32, [&](int b) {
             const int j1 = blocks(s.len[b]);
             int c = 0;
-            for (int j = blocks(s.len[b] + s.change[b]) + lane; j < j1; j += 32) {
-                const int id = a.table[(int64_t)b * a.max_blocks + j];
-                c += is_block(id);
-                if (id >= a.num_blocks) errors |= PKV_DEVERR_BLOCK_ID;
+            for (int j = blocks(s.len[b] + s.change[b]) + lane; j < j1; j += 32 * kLoads) {
+                int id[kLoads];
+#pragma unroll
+                for (int y = 0; y < kLoads; ++y) id[y] = j + 32 * y < j1 ? a.table[(int64_t)b * a.max_blocks + j + 32 * y] : -1;
+#pragma unroll
+                for (int y = 0; y < kLoads; ++y) {
+                    c += is_block(id[y]);
+                    if (id[y] >= a.num_blocks) errors |= PKV_DEVERR_BLOCK_ID;
+                }
             }
             c = __reduce_add_sync(0xffffffffu, c);
             if (lane == 0) s.back[b] = c;
@@ -236,15 +242,20 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
         warps(warp * ctas + rank, kThreads / 32 * ctas, [&](int b) {
             const int j0 = blocks(s.len[b] + s.change[b]);
             int at = s.back[b];
-            for (int j = blocks(s.len[b]) - 1 - lane; __any_sync(0xffffffffu, j >= j0); j -= 32) {
+            for (int j = blocks(s.len[b]) - 1 - lane; __any_sync(0xffffffffu, j >= j0); j -= 32 * kLoads) {
                 int32_t* e = a.table + (int64_t)b * a.max_blocks + j;
-                const int id = j >= j0 ? *e : -1;
-                const bool give = is_block(id);
-                const unsigned m = __ballot_sync(0xffffffffu, give);
-                const int place = at + __popc(m & ((1u << lane) - 1u));
-                if (give && place < room) a.free_blocks[count + place] = id;
-                if (j >= j0) *e = -1;
-                at += __popc(m);
+                int id[kLoads];
+#pragma unroll
+                for (int y = 0; y < kLoads; ++y) id[y] = j - 32 * y >= j0 ? e[-32 * y] : -1;
+#pragma unroll
+                for (int y = 0; y < kLoads; ++y) {
+                    const bool give = is_block(id[y]);
+                    const unsigned m = __ballot_sync(0xffffffffu, give);
+                    const int place = at + __popc(m & ((1u << lane) - 1u));
+                    if (give && place < room) a.free_blocks[count + place] = id[y];
+                    if (j - 32 * y >= j0) e[-32 * y] = -1;
+                    at += __popc(m);
+                }
             }
         });
         __threadfence();
