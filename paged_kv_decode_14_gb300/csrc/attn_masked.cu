@@ -1373,29 +1373,36 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true);
             int pcnt = 0, bcnt = 0;                       // this chain's tiles; pieces of both chains
             int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
-            int kn = 0, vn = 0, qn = 0;                   // K, V and Q tiles seen: every one, in order, by both chains (a
-                                                          // barrier's parity tells neighbouring phases apart, no more)
+            // K, V and Q tiles seen: every one, in order, by both chains (a barrier's parity tells neighbouring phases apart, no
+            // more).  (Slots and parities are counted, not divided: this warp's own instructions are on the chain's path.)
+            struct Ring {
+                int at, slot, used;                       // tiles seen; the next one's slot; that of the last one seen
+                uint32_t parity;
+            };
+            Ring rk = {}, rv = {}, rq = {};
             struct Work {
                 int cnt, x0, step, t0, two, both, ends;
+                int whole;                                // tiles of the piece of which some row sees the last page
                 int base, q;                              // the CTA's numbers of its first tile and of the chain's Q tile
             };
-            // up to tile `upto`: what the other chain alone uses is given back as soon as it is there
-            auto skip = [&](int& at, int upto, int ring_n, int full, int empty) -> bool {
-                for (; at < upto; ++at) {
-                    if (!wait_all(bar(full + at % ring_n), (at / ring_n) & 1)) return false;
-                    if (lead) mbar_arrive(bar(empty + at % ring_n));
+            // the tiles up to `target`; what the other chain alone uses is given back as soon as it is there
+            auto see = [&](Ring& r, int target, bool mine, int ring_n, int full, int empty) -> bool {
+                while (r.at <= target) {
+                    if (!wait_all(bar(full + r.slot), r.parity)) return false;
+                    if (lead && !(mine && r.at == target)) mbar_arrive(bar(empty + r.slot));
+                    r.used = r.slot;
+                    ++r.at;
+                    if (++r.slot == ring_n) {
+                        r.slot = 0;
+                        r.parity ^= 1;
+                    }
                 }
                 return true;
             };
-            auto see = [&](int& at, int target, int ring_n, int full, int empty) -> bool {
-                if (!skip(at, target, ring_n, full, empty)) return false;
-                at = target + 1;
-                return wait_all(bar(full + target % ring_n), (target / ring_n) & 1);
-            };
             constexpr int QRDY = FP8 ? K::QREADY : K::QFULL;
-            auto see_k = [&](int t) { return see(kn, t, NSK, K::KFULL, K::KEMPTY); };
-            auto see_v = [&](int t) { return see(vn, t, NSV, K::VREADY, K::VEMPTY); };
-            auto see_q = [&](int t) { return see(qn, t, 2, QRDY, K::QEMPTY); };
+            auto see_k = [&](int t, bool mine) { return see(rk, t, mine, NSK, K::KFULL, K::KEMPTY); };
+            auto see_v = [&](int t, bool mine) { return see(rv, t, mine, NSV, K::VREADY, K::VEMPTY); };
+            auto see_q = [&](int t, bool mine) { return see(rq, t, mine, 2, QRDY, K::QEMPTY); };
             int n = 0;
             // The next piece, if there is one and (or else, with `any`, the next that does) it has tiles of this chain.
             auto next = [&](Work& x, bool any) -> bool {
@@ -1410,15 +1417,14 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     x.two = at->two;
                     x.both = !at->two && at->count(1) > 0;
                     x.ends = at->seen_end(a, min(at->nq, at->two ? (i + 1) * a.pb : a.pb));
+                    x.whole = (x.ends - x.t0 * K::KEYS + kBlock - 1) / kBlock / K::TP;
                     x.base = tbase;
                     x.q = qbase + (at->two ? i : 0);
                     tbase += at->tiles();
                     qbase += at->two ? 2 : 1;
                     release(n);
                     if (x.cnt > 0) break;
-                    if (!skip(qn, qbase, 2, QRDY, K::QEMPTY) || !skip(kn, tbase, NSK, K::KFULL, K::KEMPTY) ||
-                        !skip(vn, tbase, NSV, K::VREADY, K::VEMPTY))
-                        return false;
+                    if (!see_q(qbase - 1, false) || !see_k(tbase - 1, false) || !see_v(tbase - 1, false)) return false;
                 }
                 ++n;
                 return true;
@@ -1427,7 +1433,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             // constant added: made anew for each, the issue of a product took longer than the product.)
             auto issue_s = [&](const Work& x, int j, auto half) {
                 constexpr int h = decltype(half)::value;
-                const int sk = (x.base + x.x0 + j * x.step) % NSK;
+                const int sk = rk.used;                   // (no tile behind it has been seen yet)
                 const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::KTILE, 0) + h * (K::KTILE / K::HALVES);
                 const uint32_t q_s = __shfl_sync(0xffffffffu, sb + K::OFF_Q + (x.q & 1) * K::QTILE, 0);
                 constexpr uint32_t dst = h * K::HCOLS;
@@ -1470,17 +1476,18 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     fresh = true;
                     if (!then && !now) break;
                 }
-                const int gt = p.base + p.x0 + j * p.step, sv = gt % NSV;
+                const int x = p.x0 + j * p.step;
                 if (now) {
-                    if (!see_v(gt)) break;
+                    if (!see_v(p.base + x, true)) break;
                     // a piece's first PV starts O afresh: the other chain too has read the last result that they shared
                     if (j == 0 && bcnt > 0 && !wait_all(bar(K::OFREE), (bcnt - 1) & 1)) break;
                 }
                 // (what the next S needs is waited for before P, off the path from P to it)
-                if (then && !fresh && !see_k(q.base + q.x0 + jq * q.step)) break;
+                if (then && !fresh && !see_k(q.base + q.x0 + jq * q.step, true)) break;
+                const int sv = rv.used;
                 const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
                 // units up to the last page that a row sees
-                const int steps = HG * min(max((p.ends - (p.t0 + p.x0 + j * p.step) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
+                const int steps = x < p.whole ? kUnits : HG * min(max((p.ends - (p.t0 + x) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
                 constexpr int HALVES = K::HALVES, EACH = kUnits / HALVES;
                 // a turn: P . V of half h, if there is a present tile, and S of it, if it belongs to the same piece; the second
                 // time (a new piece), S of both
@@ -1514,12 +1521,12 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 if (!(ok = turn(H0{}))) break;
                 // (a new piece's Q and K: bf16 by halves, before the last P; else, as FP8's softmax warps split Q behind it, after)
                 constexpr bool EARLY = !FP8 && HALVES > 1;
-                if (EARLY && then && fresh && !(ok = see_q(q.q) && see_k(q.base + q.x0))) break;
+                if (EARLY && then && fresh && !(ok = see_q(q.q, true) && see_k(q.base + q.x0, true))) break;
                 if (HALVES > 1) {
                     if (then && !fresh) issue_s(q, jq, H0{});
                     if (!(ok = turn(H1{}))) break;
                 }
-                if (!EARLY && then && fresh && !(ok = see_q(q.q) && see_k(q.base + q.x0))) break;
+                if (!EARLY && then && fresh && !(ok = see_q(q.q, true) && see_k(q.base + q.x0, true))) break;
                 if (then && fresh) tc_fence_after();
                 if (then && (fresh && HALVES > 1)) issue_s(q, jq, H0{});
                 if (then) issue_s(q, jq, H1{});
