@@ -123,6 +123,47 @@ def test_many_items_a_cta(q_lens, ctx, heads, dtype, workspace):
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+# (sequences, longest query, heads, kv_heads, dim, longest context, kind): more items than CTAs, or much FP8 work, so that several
+# kv-heads stay in an item
+SHARED = [
+    (45, 1, 32, 8, 128, 300, "window"),                              # four: rows of 4 in quarters of the lanes
+    (45, 6, 32, 8, 128, 200, "tree"),
+    (40, 9, 24, 8, 64, 260, "window"),                               # G = 3
+    (45, 11, 20, 4, 128, 150, "window"),                             # two: 55 rows of 64
+    (80, 16, 12, 4, 64, 120, "tree"),                                # two: 48 rows
+    (45, 2, 28, 4, 128, 200, "window"),                              # four, G = 7: 28 rows of 32
+    (5, 3, 16, 8, 128, 12000, "window"),                             # few and long
+]
+
+
+@pytest.mark.parametrize("spread", [1.0, 12.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_items_of_several_heads(case, dtype, spread, workspace):
+    """One long sequence among short ones (cut between CTAs), NaN and infinities planted, references that rise."""
+    n, most, heads, kv, dim, longest, kind = SHARED[case]
+    rnd = random.Random(case)
+    q_lens = [most] + [rnd.choice((0, 1, most, rnd.randint(1, most))) for _ in range(n - 1)]
+    ctx = [rnd.randint(0, longest) for _ in range(n)]
+    ctx[n // 2] = max(3000, longest)
+    lens = [q + c for q, c in zip(q_lens, ctx)]
+    nan, big = math.nan, math.nan if dtype == "fp8" else math.inf
+    plant = [(b, 1, rnd.randrange(lens[b]), rnd.randrange(kv), rnd.randrange(dim), v)
+             for b, v in ((0, nan), (n // 2, big), (n - 1, -big), (1, nan)) if lens[b]]
+    kw = dict(heads=heads, kv_heads=kv, dim=dim, dtype=dtype, seed=case, plant=plant, spread=spread)
+    if kind == "window":
+        window = 100 if longest < 5000 else 1 << 30
+        s = windowed(lens, q_lens, window, 5, **kw)
+        run = lambda: run_window(s, window, 5, workspace)  # noqa: E731
+    else:
+        s, words = treed(lens, q_lens, True, **kw)
+        run = lambda: run_tree(s, words, workspace)  # noqa: E731
+    out, lse = run()
+    check(out, lse, s.reference())
+    again = run()
+    assert torch.equal(again[0].view(torch.int16), out.view(torch.int16)) and torch.equal(again[1].view(torch.int32), lse.view(torch.int32))
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random(seed, workspace):
     rnd = random.Random(seed)
