@@ -1482,8 +1482,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     // a piece's first PV starts O afresh: the other chain too has read the last result that they shared
                     if (j == 0 && bcnt > 0 && !wait_all(bar(K::OFREE), (bcnt - 1) & 1)) break;
                 }
-                // (what the next S needs is waited for before P, off the path from P to it)
-                if (then && !fresh && !see_k(q.base + q.x0 + jq * q.step, true)) break;
                 const int sv = rv.used;
                 const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
                 // units up to the last page that a row sees
@@ -1519,6 +1517,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 using H0 = std::integral_constant<int, 0>;
                 using H1 = std::integral_constant<int, HALVES - 1>;
                 if (!(ok = turn(H0{}))) break;
+                // (the next S's K is waited for while P . V runs: before it, a late K kept V from being given back)
+                if (then && !fresh && !(ok = see_k(q.base + q.x0 + jq * q.step, true))) break;
                 // (a new piece's Q and K: bf16 by halves, before the last P; else, as FP8's softmax warps split Q behind it, after)
                 constexpr bool EARLY = !FP8 && HALVES > 1;
                 if (EARLY && then && fresh && !(ok = see_q(q.q, true) && see_k(q.base + q.x0, true))) break;
