@@ -39,13 +39,14 @@
 // ready; warp 12 the producer; warps 13 and 14 the MMA issuers of the chains; warp 15 the plan.  Every wait is bounded.
 //
 // Measured (32/8 heads of 128, inputs past L2, back to back in a graph; copies run at 6786 GB/s, bf16 products at 1965
-// TFLOP/s): a decode step of 32 sequences, window 1024: 31 us for 133 MB (0.63 of the copy rate); 2048 sequences of 300
-// keys: 389 us (0.86).  128 FP8 streams, window 4096: 240 us (0.63).  Trees of 9 to 24 nodes over 32 contexts of 512 to
-// 4072: 66 us (0.72); of 64 nodes over 16 FP8 contexts of 8k to 16k: 195 us (0.58 of the product rate).  Four 2k prompts,
-// window 512: 116 us, FP8 chunks, window 2048: 177 us (0.27 and 0.34 of the product rate, by the visible pairs; the tiles at
+// TFLOP/s): a decode step of 32 sequences, window 1024: 30 us for 133 MB (0.65 of the copy rate); 2048 sequences of 300
+// keys: 389 us (0.86).  128 FP8 streams, window 4096: 226 us (0.67).  Trees of 9 to 24 nodes over 32 contexts of 512 to
+// 4072: 64 us (0.75); of 64 nodes over 16 FP8 contexts of 8k to 16k: 193 us (0.58 of the product rate).  Four 2k prompts,
+// window 512: 116 us, FP8 chunks, window 2048: 175 us (0.27 and 0.35 of the product rate, by the visible pairs; the tiles at
 // a window's two ends are computed whole).
-// What bounds it: with few rows the copies and, FP8, the widening; with many the chain S -> P -> P . V of a row tile, 3600
-// clocks for a key tile of both chains against 2500 of products, and 9000 at a change of item.  Beneath both lies the
+// What bounds it: with few rows the copies and, FP8, the widening (1600 of a tile's 2050 clocks); with many the chain S ->
+// P -> P . V of a row tile, 3600 clocks for a key tile of both chains, of which 2560 are reads and writes of shared memory (128
+// bytes a clock; Q is read once for each half of S), and 9000 at a change of item.  Beneath both lies the
 // instruction cache: five roles' code side by side misses it in 18 % of its requests, so that whatever was unrolled or doubled
 // (a masked copy of the softmax, 64 columns an epilogue step) made it slower, and loops outside the inner ones are
 // kept rolled.
