@@ -360,6 +360,80 @@ def test_a_wide_window_is_plain_causal_attention(workspace):
     assert ((a - b).abs() <= 2e-3 + 1e-2 * a.abs()).all()
 
 
+def test_results_as_the_next_attentions_queries(workspace):
+    """pkv_paged_attention reads its q while the kernel before it may still run: not before this one's results are there."""
+    s = windowed([900] * 24, [1] * 24, 1 << 20, 0, heads=16, kv_heads=4, dim=128, dtype="bf16", seed=5)
+    ws = nat.make_workspace(24, 16, 4, 128, 1)
+    mid, lse, last = (torch.empty_like(s.q), torch.empty(s.q.shape[:2], device="cuda"), torch.empty_like(s.q))
+
+    def first():
+        nat.attention_window(s.cache, s.q, s.table, s.t_lens, s.t_q, 1, 1 << 20, 0, s.scale, workspace, out=mid, lse=lse)
+
+    def second():
+        nat.attention(s.cache, mid, s.table, s.t_lens, s.t_q, 1, s.scale, ws, out=last)
+
+    first()
+    torch.cuda.synchronize()
+    second()
+    torch.cuda.synchronize()
+    want = last.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first()
+        second()
+    for call in (lambda: (first(), second()), graph.replay):
+        for _ in range(20):
+            mid.zero_()
+            last.zero_()
+            call()
+            torch.cuda.synchronize()
+            assert torch.equal(last, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_thousands_of_sequences(dtype, workspace):
+    """A hundred for each of the plan's lanes; with starts given, the same bits."""
+    rnd = random.Random(3)
+    n, heads, kv, dim, most = 3001, 8, 4, 64, 48
+    lens = [rnd.choice((0, 1, 16, 17, rnd.randint(0, most))) for _ in range(n)]
+    q_lens = [min(x, rnd.choice((0, 1, 1, 2))) for x in lens]
+    blocks = 700
+    g = torch.Generator(device="cuda").manual_seed(1)
+    if dtype == "fp8":
+        pools = [torch.randn(blocks, kv, 16 * dim, generator=g, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8) for _ in range(2)]
+        scales = [0.5 + torch.rand(blocks, kv, generator=g, device="cuda") for _ in range(2)]
+    else:
+        pools = [torch.randn(blocks, kv, 16 * dim, generator=g, device="cuda").bfloat16() for _ in range(2)]
+        scales = [None, None]
+    cache = nat.PagedKVCache(blocks, kv, dim, dtype, k=pools[0], v=pools[1], k_scales=scales[0], v_scales=scales[1])
+    table = torch.randint(blocks, (n, 4), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn(sum(q_lens), heads, dim, generator=g, device="cuda").bfloat16()
+    b, lse = nat.attention_window(cache, q, table, ints(lens), ints(q_lens), 2, 1 << 20, 0, dim ** -0.5, workspace)
+    assert nat.read_device_error(workspace) == 0
+    # K and V [sequence, kv head, token, dim] in 64 bits, and the rows' sequences and what they see
+    k, v = ((page_view(x, kv, dim) if sc is None else page_view(x, kv, dim).view(torch.float8_e4m3fn)).double() *
+            (1.0 if sc is None else sc.double()[:, :, None, None, None, None]) for x, sc in zip(pools, scales))
+    k, v = (x.permute(0, 1, 2, 4, 3, 5).reshape(blocks, kv, 16, dim)[table.long()].transpose(1, 2).reshape(n, kv, 64, dim)
+            for x in (k, v))
+    seq = torch.tensor([i for i, x in enumerate(q_lens) for _ in range(x)], device="cuda")
+    end = ints([lens[i] - x + 1 + j for i, x in enumerate(q_lens) for j in range(x)])
+    hidden = torch.arange(64, device="cuda")[None, None, :] >= end[:, None, None]
+    k, v = (x[seq].repeat_interleave(heads // kv, 1) for x in (k, v))
+    x = torch.einsum("rhd,rhtd->rht", q.double(), k) * dim ** -0.5
+    z = torch.logsumexp(x.masked_fill(hidden, -math.inf), -1)
+    w = (x - z[..., None]).exp().masked_fill(hidden, 0.0)
+    want, size = torch.einsum("rht,rhtd->rhd", w, v), torch.einsum("rht,rhtd->rhd", w, v.abs())
+    # the bound of Sequences.reference, by its arithmetic
+    top = (torch.einsum("rhd,rhtd->rht", q.double().abs(), k.abs()) * dim ** -0.5).masked_fill(hidden, 0.0).amax(-1)
+    delta, total = 2.0 ** -24 * (dim + 8) * (top + 8) + 2.0 ** -21, 2.0 ** -24 * (64 + 64)
+    bound = (2.0 ** -8 + 2 * delta + 2 * total)[..., None] * size * 1.01 + 2.0 ** -8 * want.abs() * 1.01 + 2.0 ** -133
+    assert ((b.double() - want).abs() <= bound).all()
+    assert ((lse.double() - z).abs() <= delta + total + 2.0 ** -22 * (z.abs() + 1)).all()
+    starts = torch.tensor([0] + q_lens[:-1], device="cuda").cumsum(0)
+    again = nat.attention_window(cache, q, table, ints(lens), ints(q_lens), 2, 1 << 20, 0, dim ** -0.5, workspace, q_starts=starts)
+    assert torch.equal(again[0], b) and torch.equal(again[1], lse)
+
+
 def test_python_refusals(workspace):
     s = windowed([40], [2], 16, 0, heads=4, kv_heads=2, dim=64, dtype="bf16", seed=6)
     call = lambda **k: nat.attention_window(*[k.get(x, y) for x, y in (  # noqa: E731
