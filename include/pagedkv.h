@@ -684,7 +684,9 @@ PKV_API pkv_status pkv_paged_attention_tree(const pkv_cache* cache, const pkv_ro
  * A request is refused, and stays as it was, if the blocks it and the requests before it need are more than are
  * free (PKV_DEVERR_NO_BLOCKS; requests that need none are not), if its rows do not fit in num_rows, or if its
  * length would leave 0 .. 16 * max_blocks_per_seq (PKV_DEVERR_LENGTH).  Its rows get slot -1 (which the appends
- * skip).  Rows behind the last request's are left as they were.  A block id outside [0, num_blocks) that is taken
+ * skip).  Rows behind the last request's are left as they were: an append of all num_rows rows must not follow where
+ * the changes may add up to less (in a captured step they hold an earlier step's slots, whose blocks may be another
+ * request's by then); pkv_block_tables_update_padded is for that.  A block id outside [0, num_blocks) that is taken
  * from the pool or given back sets PKV_DEVERR_BLOCK_ID: the former's entry becomes -1, the latter is not pushed.
  * A count outside [0, num_blocks] sets PKV_DEVERR_LENGTH and every change is refused.
  * num_seqs <= 8192.  One launch; deterministic.
@@ -694,6 +696,18 @@ PKV_API pkv_status pkv_block_tables_update(int32_t* block_tables, int32_t max_bl
                                            int32_t* free_count, int64_t num_blocks, int64_t* slots, int32_t* positions,
                                            int32_t* granted, int64_t* row_starts, int64_t num_rows,
                                            int32_t* device_error, void* stream);
+
+/*
+ * The same where num_rows is a bound, as in a captured step whose changes only the GPU knows: rows behind the last
+ * request's get slot -1, which the appends skip, and position 0, so that all num_rows rows may be appended.  (With
+ * num_seqs = 0 too, where the other arrays may be NULL.)
+ */
+PKV_API pkv_status pkv_block_tables_update_padded(int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                  int32_t* context_lens, const int32_t* grow, int32_t num_seqs,
+                                                  int32_t* free_blocks, int32_t* free_count, int64_t num_blocks,
+                                                  int64_t* slots, int32_t* positions, int32_t* granted,
+                                                  int64_t* row_starts, int64_t num_rows, int32_t* device_error,
+                                                  void* stream);
 
 /*
  * The accepted path of a verified tree, moved into place: the K and V of node path[i] of sequence b (at position

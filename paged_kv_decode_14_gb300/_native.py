@@ -129,8 +129,8 @@ def lib():
             L.pkv_paged_attention_window.argtypes = masked + [i32, i32, c.c_float, vp, c.c_size_t, vp]
             L.pkv_paged_attention_tree.restype = c.c_int
             L.pkv_paged_attention_tree.argtypes = masked + [vp, i32, c.c_float, vp, c.c_size_t, vp]
-            L.pkv_block_tables_update.restype = c.c_int
-            L.pkv_block_tables_update.argtypes = [vp, i32, vp, vp, i32, vp, vp, i64, vp, vp, vp, vp, i64, vp, vp]
+            L.pkv_block_tables_update.restype = L.pkv_block_tables_update_padded.restype = c.c_int
+            L.pkv_block_tables_update.argtypes = L.pkv_block_tables_update_padded.argtypes = [vp, i32, vp, vp, i32, vp, vp, i64, vp, vp, vp, vp, i64, vp, vp]
             L.pkv_paged_kv_keep_path.restype = c.c_int
             L.pkv_paged_kv_keep_path.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, i32, vp, vp]
             L.pkv_copy_blocks.restype = c.c_int
@@ -680,15 +680,20 @@ class BlockPool:
 
 
 def update_tables(pool: BlockPool, block_tables, context_lens, grow, num_rows: int, slots=None, positions=None,
-                  granted=None, row_starts=None, device_error=None, stream=None):
+                  granted=None, row_starts=None, device_error=None, stream=None, pad=None):
     """pkv_block_tables_update: requests grow by (or, negative, drop) grow tokens: block_tables, context_lens and the
     pool are updated in place.  num_rows >= sum(max(grow, 0)).  Returns (slots int64, positions int32 [num_rows],
     granted int32, row_starts int64 [num_seqs]), new tensors unless given: what an append and the attention of
-    the new tokens take as slot_mapping, positions, q_lens and q_starts."""
+    the new tokens take as slot_mapping, positions, q_lens and q_starts.
+    pad (pkv_block_tables_update_padded): rows behind the last request's get slot -1, which appends skip, and
+    position 0; else they are left as they were.  By default so where slots are new.  With slots given, say pad=True
+    where num_rows is more than the rows there are and an append of all of them follows."""
     device, n, num_rows = _device_of(block_tables, "block_tables"), context_lens.numel(), int(num_rows)
     i32, i64 = torch.int32, torch.int64
     if num_rows < 0:
         raise ValueError("num_rows must not be negative")
+
+    pad = slots is None if pad is None else pad
 
     def output(t, name, dtype, numel):
         if t is None:
@@ -700,7 +705,7 @@ def update_tables(pool: BlockPool, block_tables, context_lens, grow, num_rows: i
     positions, pp = output(positions, "positions", i32, num_rows)
     granted, gp = output(granted, "granted", i32, n)
     row_starts, rp = output(row_starts, "row_starts", i64, n)
-    _call("pkv_block_tables_update", device, stream, *_tables_of(block_tables, device, n),
+    _call("pkv_block_tables_update_padded" if pad else "pkv_block_tables_update", device, stream, *_tables_of(block_tables, device, n),
           _vector(context_lens, "context_lens", i32, device, n), _vector(grow, "grow", i32, device, n), n,
           _vector(pool.free, "pool.free", i32, device, pool.num_blocks), _vector(pool.count, "pool.count", i32, device, 1),
           pool.num_blocks, sp, pp, gp, rp, num_rows, _error_word(device_error, device))

@@ -13,8 +13,8 @@ size_t masked_workspace_bytes();
 bool block_tables_fit(int num_seqs);
 cudaError_t launch_block_tables(int32_t* table, int max_blocks, int32_t* lens, const int32_t* grow, int num_seqs,
                                 int32_t* free_blocks, int32_t* free_count, int64_t num_blocks, int64_t* slots,
-                                int32_t* positions, int32_t* granted, int64_t* row_starts, int64_t num_rows, int* err,
-                                cudaStream_t st);
+                                int32_t* positions, int32_t* granted, int64_t* row_starts, int64_t num_rows, bool pad,
+                                int* err, cudaStream_t st);
 cudaError_t launch_keep_path(const pkv_cache& c, const int32_t* tables, int max_blocks, const int32_t* ctx_lens,
                              const int32_t* q_lens, const int32_t* path, int max_path, const int32_t* path_lens,
                              int num_seqs, int* err, cudaStream_t st);
@@ -47,6 +47,30 @@ pkv_status check_masked(const pkv_cache* cache, const pkv_rows* q, const pkv_row
     if (!workspace || workspace_bytes < pkv_masked_workspace_size()) return PKV_ERR_WORKSPACE;
     if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
     return PKV_OK;
+}
+
+pkv_status update_tables(int32_t* block_tables, int32_t max_blocks_per_seq, int32_t* context_lens, const int32_t* grow,
+                         int32_t num_seqs, int32_t* free_blocks, int32_t* free_count, int64_t num_blocks, int64_t* slots,
+                         int32_t* positions, int32_t* granted, int64_t* row_starts, int64_t num_rows, bool pad,
+                         int32_t* device_error, cudaStream_t st) {
+    if (num_seqs < 0 || num_rows < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
+    if (!block_tables_fit(num_seqs) || num_rows > 0x7fffff00 || num_blocks > 0x7fffffff ||
+        (int64_t)max_blocks_per_seq * kBlock > 0x7fffffff)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) {
+        if (!pad || num_rows == 0) return PKV_OK;
+        if (!slots) return PKV_ERR_INVALID_ARG;
+        cudaError_t e = cudaMemsetAsync(slots, 0xff, (size_t)num_rows * sizeof(*slots), st);
+        if (e == cudaSuccess && positions) e = cudaMemsetAsync(positions, 0, (size_t)num_rows * sizeof(*positions), st);
+        return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    }
+    if (!block_tables || !context_lens || !grow || !free_blocks || !free_count || (num_rows > 0 && !slots))
+        return PKV_ERR_INVALID_ARG;
+    return launch_block_tables(block_tables, max_blocks_per_seq, context_lens, grow, num_seqs, free_blocks, free_count,
+                               num_blocks, slots, positions, granted, row_starts, num_rows, pad, device_error,
+                               st) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -99,18 +123,18 @@ PKV_API pkv_status pkv_block_tables_update(int32_t* block_tables, int32_t max_bl
                                            int32_t* free_count, int64_t num_blocks, int64_t* slots, int32_t* positions,
                                            int32_t* granted, int64_t* row_starts, int64_t num_rows,
                                            int32_t* device_error, void* stream) {
-    if (num_seqs < 0 || num_rows < 0 || num_blocks <= 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID_ARG;
-    if (!block_tables_fit(num_seqs) || num_rows > 0x7fffff00 || num_blocks > 0x7fffffff ||
-        (int64_t)max_blocks_per_seq * kBlock > 0x7fffffff)
-        return PKV_ERR_UNSUPPORTED;
-    if (num_seqs == 0) return PKV_OK;
-    if (!block_tables || !context_lens || !grow || !free_blocks || !free_count || (num_rows > 0 && !slots))
-        return PKV_ERR_INVALID_ARG;
-    return launch_block_tables(block_tables, max_blocks_per_seq, context_lens, grow, num_seqs, free_blocks, free_count,
-                               num_blocks, slots, positions, granted, row_starts, num_rows, device_error,
-                               (cudaStream_t)stream) == cudaSuccess
-               ? PKV_OK
-               : PKV_ERR_CUDA;
+    return update_tables(block_tables, max_blocks_per_seq, context_lens, grow, num_seqs, free_blocks, free_count, num_blocks,
+                         slots, positions, granted, row_starts, num_rows, false, device_error, (cudaStream_t)stream);
+}
+
+PKV_API pkv_status pkv_block_tables_update_padded(int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                  int32_t* context_lens, const int32_t* grow, int32_t num_seqs,
+                                                  int32_t* free_blocks, int32_t* free_count, int64_t num_blocks,
+                                                  int64_t* slots, int32_t* positions, int32_t* granted,
+                                                  int64_t* row_starts, int64_t num_rows, int32_t* device_error,
+                                                  void* stream) {
+    return update_tables(block_tables, max_blocks_per_seq, context_lens, grow, num_seqs, free_blocks, free_count, num_blocks,
+                         slots, positions, granted, row_starts, num_rows, true, device_error, (cudaStream_t)stream);
 }
 
 PKV_API pkv_status pkv_paged_kv_keep_path(const pkv_cache* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,

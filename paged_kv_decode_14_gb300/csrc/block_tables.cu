@@ -47,6 +47,7 @@ struct Arg {
     int* err;
     int64_t num_blocks, num_rows;
     int num_seqs, max_blocks;
+    bool pad;                              // rows behind the last request's: slot -1, position 0 (else left alone)
 };
 
 // Shared memory, by request: tokens before; change (0: refused or none); blocks given back by later
@@ -299,6 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
         a.slots[r] = slot;
         if (a.positions) a.positions[r] = (int)at;
     }
+    if (a.pad)
+        for (int64_t r = shown + first; r < a.num_rows; r += stride) {
+            a.slots[r] = -1;
+            if (a.positions) a.positions[r] = 0;
+        }
     for (int64_t b = first; b < n; b += stride) {
         if (s.change[b] != 0) a.lens[b] = s.len[b] + s.change[b];
         if (a.granted) a.granted[b] = max(s.change[b], 0);
@@ -315,12 +321,12 @@ bool block_tables_fit(int num_seqs) { return num_seqs <= tables::kMaxSeqs; }
 
 cudaError_t launch_block_tables(int32_t* table, int max_blocks, int32_t* lens, const int32_t* grow, int num_seqs,
                                 int32_t* free_blocks, int32_t* free_count, int64_t num_blocks, int64_t* slots,
-                                int32_t* positions, int32_t* granted, int64_t* row_starts, int64_t num_rows, int* err,
-                                cudaStream_t st) {
+                                int32_t* positions, int32_t* granted, int64_t* row_starts, int64_t num_rows, bool pad,
+                                int* err, cudaStream_t st) {
     using namespace tables;
     static std::atomic<uint64_t> set{0};
     const Arg a{table, lens, grow, free_blocks, free_count, slots, positions, granted, row_starts, err, num_blocks,
-                num_rows, num_seqs, max_blocks};
+                num_rows, num_seqs, max_blocks, pad};
     const size_t bytes = (size_t)num_seqs * kArrays * sizeof(int), most = (size_t)kMaxSeqs * kArrays * sizeof(int);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
