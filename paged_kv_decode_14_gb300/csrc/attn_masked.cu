@@ -75,7 +75,6 @@ constexpr int kRegsSoftmax = 160, kRegsReady = 112, kRegsOther = 80;
 static_assert(2 * kRegsSoftmax + kRegsReady + kRegsOther == 4 * 128, "register file");
 constexpr int kReady = 8, kProducer = 12, kMma = 13, kPlan = 15;
 constexpr int kPieces = 4;                 // pieces of work planned ahead
-constexpr int kFlags = 8;                  // pieces whose "non-finite V" flags are kept
 constexpr int kMaxCtas = 160;              // CTAs of a launch (two workspace slots each)
 // what an item costs beside its key tiles, in units (key tiles of one row tile): four 2k prompts take 117 us with 4, 149 with
 // 2 and 119 with 8
@@ -123,6 +122,9 @@ struct Piece {
     int c0, parts;          // the CTAs that hold parts of the item: c0 .. c0 + parts - 1
     int two;                // two row tiles
     int end;                // no more work (the other fields are unset)
+    unsigned bad;           // bit i: tiles [i << shift, (i + 1) << shift) hold values that the guard of V took out
+    // the shift: as many marks as there are tiles, up to 32
+    __device__ __forceinline__ int mark_shift() const { return max(0, 27 - __clz(max(tiles() - 1, 1))); }
     __device__ __forceinline__ int tiles() const { return t1 - t0; }
     // tiles of chain i, the first of them, and the step from one to the next
     __device__ __forceinline__ int count(int i) const { return two ? t1 - t0 : (t1 - t0 + 1 - i) >> 1; }
@@ -213,8 +215,7 @@ struct Cfg {
                          Q1FULL = PCEMPTY + kPieces, DRAIN = Q1FULL + 1;
     static constexpr int NBAR = DRAIN + 1;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;   // tmem address, abort flags
-    static constexpr int OFF_FLAG = OFF_MISC + 16;        // int[kFlags]
-    static constexpr int OFF_ML = OFF_FLAG + 4 * kFlags;  // float[chain][m, l][kRows]
+    static constexpr int OFF_ML = OFF_MISC + 16;          // float[chain][m, l][kRows]
     static constexpr int OFF_PIECE = OFF_ML + 4 * 4 * kRows;
     static constexpr int OFF_SC = OFF_PIECE + kPieces * (int)sizeof(Piece);       // FP8: float[NSC][k scales 8, v scales 8]
     static constexpr int OFF_QS = OFF_SC + (FP8 ? NSC * 64 : 0);                  // FP8: float[NQS][kRows]
@@ -446,6 +447,8 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(lo) : "r"(x), "r"(f));
     asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(hi) : "r"(y), "r"(f));
 }
+// A bit set where one of two bf16 is infinite or NaN: an exponent of all ones carries.
+__device__ __forceinline__ uint32_t inf_words(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 // Two bf16 (of a word) times f as e4m3 codes, and what they leave as e4m3 codes.
@@ -475,7 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + K::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 4);
     volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + K::OFF_MISC + 8);   // (drain waits at the end)
-    volatile int* nonfinite = reinterpret_cast<volatile int*>(smem + K::OFF_FLAG);
     float* ml = reinterpret_cast<float*>(smem + K::OFF_ML);
     float* scales = reinterpret_cast<float*>(smem + K::OFF_SC);
     float* q_scale = reinterpret_cast<float*>(smem + K::OFF_QS);
@@ -520,7 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         mbar_init(bar(K::DRAIN), 2);
         *abort_flag = 0;
         *drain_flag = 0;
-        for (int i = 0; i < kFlags; ++i) nonfinite[i] = 0;
         mbar_fence_init();
     }
     if (warp == kProducer && lane == 0) asm volatile("prefetch.tensormap [%0];\n" ::"l"(&a.q) : "memory");
@@ -559,9 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         const uint32_t lbase = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t scol = tmem + lbase + i * kCols;   // S / P
         const uint32_t ocol = tmem + lbase + K::COL_O + i * D;
-        // What the guard took out of V, added to a row's results where this lane has just written them (rare).
-        auto add_back = [&](const Piece& p, int qi, int d0, int d1, uint8_t* out, float* part) {
-            const Guard<HG> gd = guard_of<HG>(a, p);
+        // What the guard took out of V, added to a row's results where its lane has just written them (rare): the keys
+        // of the piece's marked parts are looked through, for 8 dimensions after the other, 8 keys' loads in flight.  (A value
+        // at a time over all keys took 20 ms for one NaN in each of 64 streams of 4096 keys, a call of 0.16 to 0.19 ms; now it
+        // takes 0.19 to 0.26.  No shuffles or votes: with them in this code every call took 0.8 us longer.)
+        auto add_back = [&](const Piece& p, unsigned bad, int qi, int d0, int d1, uint8_t* out, float* part) {
+            using Eight = std::conditional_t<FP8, uint2, uint4>;
+            constexpr int E = 8, C = FP8 ? 16 : 8;        // elements at a time, and of a 16-byte chunk
             Sight see;
             const uint32_t* tree = nullptr;
             if (a.tree) {
@@ -570,43 +575,60 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             } else {
                 see.window(a, p, p.first + qi);
             }
-            auto span = [&](int v, int z) {
-                v = max(v, p.t0 * K::KEYS);
-                z = min(z, min(p.t1 * K::KEYS, p.np * kBlock) - 1);
+            const int shift = p.mark_shift();
 #pragma unroll 1
-                for (; v <= z; ++v) {
-                    const bool has = see.has(v) || (tree && v >= p.L - p.Q &&
-                                                    (tree_bits(tree, a.tree_words, v - (p.L - p.Q), p.Q) & 1u));
-                    if (!has) continue;
-                    const int id = a.tables[(int64_t)p.b * a.max_blocks + p.page(v / kBlock)];
-                    if (id < 0 || id >= a.num_blocks) continue;
-                    const uint8_t* page = a.v_cache + ((int64_t)id * a.Hkv + p.g + hw) * K::LAND;
-                    const int off = v % kBlock;
+            for (int d = d0; d < d1; d += E) {
+                float add[E] = {};
 #pragma unroll 1
-                    for (int d = d0; d < d1; ++d) {
-                        float f;
-                        if constexpr (FP8) {
-                            const uint8_t code = page[((off / 8) * (D / 16) + d / 16) * 128 + (off % 8) * 16 + d % 16];
-                            f = e4m3x2_to_float2(code).x * a.v_scales[(int64_t)id * a.Hkv + p.g + hw];
-                        } else {
-                            f = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-                                page + ((off / 8) * (D / 8) + d / 8) * 128 + (off % 8) * 16 + (d % 8) * 2));
-                        }
-                        if (fabsf(f) < INFINITY) continue;
-                        if (part) {
-                            part[(size_t)(d / 4) * 2 * kRows * 4 + d % 4] += f;
-                        } else {
-                            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out) + d;
-                            *o = __float2bfloat16_rn(__bfloat162float(*o) + f);
+                for (unsigned marks = bad; marks; marks &= marks - 1) {
+                    const int x = (__ffs(marks) - 1) << shift;
+                    const int end = min((p.t0 + min(x + (1 << shift), p.tiles())) * K::TP, p.np) * kBlock;
+#pragma unroll 1
+                    for (int v = (p.t0 + x) * K::KEYS; v < end; v += 8) {
+                        const int id = a.tables[(int64_t)p.b * a.max_blocks + p.page(v / kBlock)];
+                        if (id < 0 || id >= a.num_blocks) continue;
+                        const int64_t page = (int64_t)id * a.Hkv + p.g + hw;
+                        const uint8_t* at = a.v_cache + page * K::LAND + (v % kBlock / 8 * (D / C) + d / C) * 128 + d % C;
+                        auto load = [&](int y) { return *reinterpret_cast<const Eight*>(at + y * 16); };
+                        const float sc = FP8 ? a.v_scales[page] : 1.f;
+                        auto hit = [](const Eight& w) {
+                            if constexpr (FP8) return nan_codes(w.x) | nan_codes(w.y);
+                            else return inf_words(w.x) | inf_words(w.y) | inf_words(w.z) | inf_words(w.w);
+                        };
+                        Eight w[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) w[y] = load(y);
+                        uint32_t any = fabsf(sc) < INFINITY ? 0u : 1u;
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) any |= hit(w[y]);
+                        if (any == 0) continue;
+#pragma unroll 1
+                        for (int y = 0; y < 8; ++y) {
+                            const bool has = see.has(v + y) || (tree && v + y >= p.L - p.Q &&
+                                                                (tree_bits(tree, a.tree_words, v + y - (p.L - p.Q), p.Q) & 1u));
+                            if (!has) continue;
+                            const Eight z = load(y);
+                            const uint32_t* c = &z.x;
+#pragma unroll
+                            for (int e = 0; e < E; e += 2) {
+                                const float2 f = FP8 ? e4m3x2_to_float2(c[e / 4] >> (e % 4 * 8))
+                                                     : make_float2(bf16_lo(c[FP8 ? 0 : e / 2]), bf16_hi(c[FP8 ? 0 : e / 2]));
+                                if (!(fabsf(f.x) < INFINITY && fabsf(sc) < INFINITY)) add[e] += f.x * sc;
+                                if (!(fabsf(f.y) < INFINITY && fabsf(sc) < INFINITY)) add[e + 1] += f.y * sc;
+                            }
                         }
                     }
                 }
-            };
-            if (HG > 1 || FP8) {                          // (FP8: a page whose scale is not finite, wherever it lies)
-                span(0, p.np * kBlock);
-            } else {
-                span(gd.wl_any, gd.wl_all - 1);
-                span(gd.wh_all + 1, gd.wh_any);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (add[e] == 0.f) continue;
+                    if (part) {
+                        part[(size_t)((d + e) / 4) * 2 * kRows * 4 + e % 4] += add[e];
+                    } else {
+                        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(out) + d + e;
+                        *o = __float2bfloat16_rn(__bfloat162float(*o) + add[e]);
+                    }
+                }
             }
         };
         // the weight of a part with reference m and sum l beside the largest reference `top` of the parts.  (A part
@@ -617,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         auto finish_lse = [](float m, float l) {
             return m == -INFINITY && l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.693147180559945f;
         };
-        // The results of piece n: part ct of its rows' results (two row tiles: row tile ct; one: columns from ct * D / 2 on), from
+        // The results of a piece: part ct of its rows' results (two row tiles: row tile ct; one: columns from ct * D / 2 on), from
         // this chain's O or (both) from both.  (In loops, one copy: it runs once a piece, from an instruction cache
         // that holds the inner loops by then.)
-        auto finish = [&](const Piece& p, int n, int ct, bool both, float m, float l) {
+        auto finish = [&](const Piece& p, int ct, bool both, float m, float l) {
             const bool whole = p.parts == 1;
             float* slot = part_slot<D>(a, blockIdx.x, p.t0 == 0);
             const int qi = (p.two ? ct * a.pb : 0) + pos;
@@ -686,7 +708,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 __syncwarp();
             }
             tmem_wait_ld_into(x);
-            if (row_ok && nonfinite[n % kFlags] == n + 1) add_back(p, qi, d0, d1, dst, whole ? nullptr : part);
         };
         // A cut piece's part ct is in memory: the last of the item's CTAs to get here (with these lanes' rows) joins
         // them, in order.
@@ -1062,11 +1083,24 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             tc_fence_after();
             const int ct0 = p->two || both ? i : 0, ct1 = p->two || both ? i + 1 : 2;
 #pragma unroll 1
-            for (int ct = ct0; ct < ct1; ++ct) finish(*p, n, ct, both, m, l);
+            for (int ct = ct0; ct < ct1; ++ct) finish(*p, ct, both, m, l);
             // O read: the next piece's first PV may overwrite it (in the chain itself, its P come after this)
             tc_fence_before();
             __syncwarp();
             if (both && lane == 0) mbar_arrive(bar(K::OFREE));
+            const unsigned bad = *const_cast<const volatile unsigned*>(&p->bad);
+            if (bad != 0) {
+#pragma unroll 1
+                for (int ct = ct0; ct < ct1; ++ct) {
+                    const int qi = (p->two ? ct * a.pb : 0) + pos;
+                    const int d0 = p->two ? 0 : ct * (D / 2), d1 = p->two ? D : d0 + D / 2;
+                    float* part = part_slot<D>(a, blockIdx.x, p->t0 == 0) + ((p->two ? ct * kRows : 0) + r) * 4;
+                    if (pos < a.pb && qi < p->nq)
+                        add_back(*p, bad, qi, d0, d1, a.out.row(p->row + p->q0 + qi, (p->g + hw) * G + hl),
+                                 p->parts == 1 ? nullptr : part);
+                }
+                __syncwarp();
+            }
             if (p->parts > 1) {
 #pragma unroll 1
                 for (int ct = ct0; ct < ct1; ++ct) join(*p, ct);
@@ -1146,7 +1180,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             return found;
         };
         auto guard_group = [&](uint8_t* at, const Guard<HG>& gd, int v) -> bool {     // 8 keys of bf16 V
-            constexpr uint32_t I = 0x7f807f80u, A = 0x80008000u - I;              // an exponent of all ones carries
             constexpr int N = K::NCH / 4;
             uint4* e = reinterpret_cast<uint4*>(at + lane * 16);
             const int key = v + (lane & 7);
@@ -1159,13 +1192,13 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const uint4 x = e[32 * j];
-                bad |= ((x.x & I) + A) | ((x.y & I) + A) | ((x.z & I) + A) | ((x.w & I) + A);
+                bad |= inf_words(x.x) | inf_words(x.y) | inf_words(x.z) | inf_words(x.w);
             }
-            if ((bad & 0x80008000u) == 0 || gd.all(key)) return false;
+            if (bad == 0 || gd.all(key)) return false;
 #pragma unroll 1
             for (int j = 0; j < 4 * N; ++j) {
                 uint32_t* y = reinterpret_cast<uint32_t*>(e + 32 * (j / 4)) + j % 4;
-                const uint32_t hit = ((*y & I) + A) & 0x80008000u;
+                const uint32_t hit = inf_words(*y);
                 *y &= ~((hit >> 15) * 0xffffu);
             }
             return true;
@@ -1194,7 +1227,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                 }
                 if (__any_sync(0xffffffffu, touched)) fence_proxy_async_smem();
             }
-            if (__any_sync(0xffffffffu, found) && lane == 0) nonfinite[n % kFlags] = n + 1;
+            if (__any_sync(0xffffffffu, found) && lane == 0) atomicOr(&ring[n % kPieces].bad, 1u << (x >> p.mark_shift()));
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
         };
