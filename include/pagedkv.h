@@ -632,9 +632,10 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, co
  * or an FP8 page's scale reaches the queries that see it, and no other (an infinite value as NaN where its weight
  * rounds to 0).  Deterministic: the same call gives the same bits.
  *
- * One launch.  It reads and writes nothing before the previous kernel on the stream has completed, and does not let the
- * next start early (out may be the q of a pkv_paged_attention behind it).  A wait inside it that runs out (pkv_debug_set_wait_limit; no piece of a call's work
- * comes near the limit) sets PKV_DEVERR_TIMEOUT, and all of the call's results are unspecified.
+ * One launch.  It reads and writes nothing before the previous kernel on the stream has completed, and does not let
+ * the next start early (out may be the q of a pkv_paged_attention behind it).  A wait inside it that runs out
+ * (pkv_debug_set_wait_limit's limit, and 100 us for each key tile of the piece of work that is waited for: 50 times what
+ * one takes) sets PKV_DEVERR_TIMEOUT, and all of the call's results are unspecified.
  */
 PKV_API size_t pkv_masked_workspace_size(void);
 PKV_API pkv_status pkv_paged_attention_window(const pkv_cache* cache, const pkv_rows* q, const pkv_rows* out, float* lse,

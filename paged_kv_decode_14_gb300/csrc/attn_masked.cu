@@ -79,6 +79,9 @@ constexpr int kMaxCtas = 160;              // CTAs of a launch (two workspace sl
 // what an item costs beside its key tiles, in units (key tiles of one row tile): four 2k prompts take 117 us with 4, 149 with
 // 2 and 119 with 8
 constexpr int kItemUnits = 4;
+// What a piece's wait limit grows by for each of its key tiles, in ns: they take 1 to 2 us, and with values that are not finite
+// alone some 50.
+constexpr uint64_t kTileLimit = 100000;
 constexpr uint32_t kWaitHint = 20000;     // ns that a wait may sleep before it looks at the abort flag
 constexpr int kAhead = 3;                  // tiles that an FP8 page's scales are fetched ahead
 // What cutting an item costs, in units.  Where there is a CTA for every item and none is longer than its share by more than
@@ -1255,8 +1258,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             p.end = !plan.next(p);
             enter();
             // every warp is done with piece x: the only wait that keeps the time
-            const Ctl clock{abort_flag, a.err, a.wait_limit_ns};
             auto done = [&](int x) -> bool {
+                const Ctl clock{abort_flag, a.err, a.wait_limit_ns + ring[x % kPieces].tiles() * kTileLimit};
                 return __all_sync(0xffffffffu, wait(bar(K::PCEMPTY + x % kPieces), (x / kPieces) & 1, clock));
             };
             for (int n = 0;; ++n) {
