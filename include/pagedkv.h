@@ -618,8 +618,9 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, co
  *                  whatever the call; head dimension, lengths and masks may change from call to call.)
  * A sequence with a bad length, a table row that is too short, or rows outside num_q_rows sets PKV_DEVERR_LENGTH
  * and its rows are left as they were; a bad block id sets PKV_DEVERR_BLOCK_ID and the results that see it are
- * unspecified.  A call of more than 2^31 units of work (a unit: 128 rows times 128 keys) sets PKV_DEVERR_LENGTH and
- * writes nothing.
+ * unspecified.  A call of more than 2^31 units of work (a unit: 128 rows times 128 keys, counted for each 1, 2 or 4 kv-heads
+ * whose rows share a row tile: some 15 s, two prompts of 2^20 tokens with 32/8 heads and no window) sets PKV_DEVERR_LENGTH
+ * and writes nothing.
  *
  * Precision: fp32 accumulation throughout.  bf16 cache: q . k in bf16.  FP8 cache: a row of q, times a power of two, is
  * split into two e4m3 terms (exact but for elements below 2^-10 of the row's largest, which are good to 2^-17 of it) and

@@ -352,7 +352,7 @@ struct Plan {
             if (turn == 0) {
                 before = scan(mine);
                 const int64_t sum = __shfl_sync(0xffffffffu, before + mine, 31);
-                if (sum > 0x7ffffff0) {                   // (more than a month's work)
+                if (sum > 0x7ffffff0) {                   // (some 15 s of a GPU's work; units are counted in 32 bits)
                     raise_error(a.err, PKV_DEVERR_LENGTH);
                     return;
                 }

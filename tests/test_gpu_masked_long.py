@@ -40,3 +40,26 @@ def test_long_pieces_do_not_run_out_of_time():
     assert ((out[:, 0].double() - want).abs() <= (2.0 ** -8 + 3 * 2.0 ** -9) * size + 2.0 ** -8 * want.abs()).all()
     z = torch.logsumexp(x, -1) + math.log(length / (16 * blocks))
     assert ((lse[:, 0].double() - z).abs() <= 2 * 2.0 ** -9).all()
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_more_work_than_a_call_takes_is_refused(tree):
+    """5 sequences of 2^26 keys and 1024 kv-heads, four of them an item: more than 2^31 units.  No table entry is read
+    (they are out of range), nothing is written."""
+    seqs, length, heads, dim = 5, 1 << 26, 1024, 64
+    cache = nat.PagedKVCache(2, heads, dim, "bf16")
+    cache.k.zero_()
+    cache.v.zero_()
+    table = torch.full((seqs, length // 16), 1 << 30, dtype=torch.int32, device="cuda")
+    q = torch.ones(seqs, heads, dim, device="cuda").bfloat16()
+    ws = nat.make_masked_workspace()
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    args = (cache, q, table, ints([length] * seqs), ints([1] * seqs), 1)
+    if tree:
+        nat.attention_tree(*args, torch.ones(seqs, 1, dtype=torch.int32, device="cuda"), 0.125, ws, out=out, lse=lse)
+    else:
+        nat.attention_window(*args, 1 << 30, 0, 0.125, ws, out=out, lse=lse)
+    assert nat.read_device_error(ws) == nat.DEVERR_LENGTH
+    assert (out == 7.0).all() and (lse == 7.0).all()
+    one = nat.attention_window(cache, q[:1], table[:1].zero_(), ints([20]), ints([1]), 1, 1 << 30, 0, 0.125, ws)
+    assert nat.read_device_error(ws) == 0 and torch.isfinite(one[1]).all()
