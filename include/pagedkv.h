@@ -690,6 +690,8 @@ PKV_API pkv_status pkv_paged_attention_tree(const pkv_cache* cache, const pkv_ro
  * the changes may add up to less (in a captured step they hold an earlier step's slots, whose blocks may be another
  * request's by then); pkv_block_tables_update_padded is for that.  A block id outside [0, num_blocks) that is taken
  * from the pool or given back sets PKV_DEVERR_BLOCK_ID: the former's entry becomes -1, the latter is not pushed.
+ * Where more blocks come back than the pool has room for (a block that two table entries hold, or that is free already),
+ * every request's drop is refused, and PKV_DEVERR_BLOCK_ID set; growth is not.  (Fewer of them go unseen.)
  * A count outside [0, num_blocks] sets PKV_DEVERR_LENGTH and every change is refused.
  * num_seqs <= 8192.  One launch; deterministic.
  */

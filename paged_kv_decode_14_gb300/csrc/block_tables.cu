@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
         at[2] += need_of(b);
     }
     scan(at, all, part);
-    const int64_t all_rows = all[0], all_back = all[1];
+    const int64_t all_rows = all[0];
     int64_t all_need = all[2];
     if (all_rows > a.num_rows) {                          // the requests whose rows do not fit get nothing
         errors |= PKV_DEVERR_LENGTH;
@@ -200,14 +200,21 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
         at[2] = need[0];
         all_need = sum[0];
     }
-    const int64_t room = count < 0 ? 0 : a.num_blocks - count;
-    if (all_back > room) errors |= PKV_DEVERR_BLOCK_ID;   // (a block was given back twice)
-    const int top = count < 0 ? 0 : (int)(count + min(all_back, room));
+    // More come back than the stack has room for: some block is in the tables or on the stack twice.  Which of them can not be
+    // told here, so that no request drops any.
+    const bool keep = count >= 0 && all[1] > a.num_blocks - count;
+    if (keep) {
+        errors |= PKV_DEVERR_BLOCK_ID;
+        at[1] = 0;
+    }
+    const int64_t all_back = keep ? 0 : all[1];
+    const int top = count < 0 ? 0 : (int)(count + all_back);
     int taken = 0;                                        // blocks needed by the requests that get theirs, up to here
     for (int b = b0; b < b1; ++b) {
         s.row[b] = (int)min(at[0], (int64_t)0x7fffffff);
         at[0] += s.rows[b];
-        at[1] += s.back[b];
+        if (!keep) at[1] += s.back[b];
+        else if (s.change[b] < 0) s.change[b] = 0;
         s.back[b] = (int)(all_back - at[1]);              // of later requests
         s.need[b] = (int)min(at[2], (int64_t)0x7fffffff);
         const int c = need_of(b);
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
     __syncthreads();
 
     if (ctas > 1) cluster.sync();                         // every CTA has read the old state
-    if (any_drop) {
+    if (any_drop && !keep) {
         // last block first: a request's entries are taken from its end
         for (int b = rank * kThreads + tid; b < n; b += kThreads * ctas) {
             const int few = dropped(b);
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
                 int32_t* e = a.table + (int64_t)b * a.max_blocks + j;
                 const int id = *e;
                 if (is_block(id)) {
-                    if (at < room) a.free_blocks[count + at] = id;
+                    a.free_blocks[count + at] = id;
                     ++at;
                 }
                 *e = -1;
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
                     const bool give = is_block(id[y]);
                     const unsigned m = __ballot_sync(0xffffffffu, give);
                     const int place = at + __popc(m & ((1u << lane) - 1u));
-                    if (give && place < room) a.free_blocks[count + place] = id[y];
+                    if (give) a.free_blocks[count + place] = id[y];
                     if (j - 32 * y >= j0) e[-32 * y] = -1;
                     at += __popc(m);
                 }
