@@ -122,11 +122,12 @@ typedef struct pkv_cache {
  * num_tokens = 0 is a no-op.
  *
  * Launch (programmatic dependent launch): the kernel lets the next kernel on
- * the stream launch at once, and reads slot_mapping, k_new and v_new (its
- * threads' first chunks) before waiting for the previous kernel on the
- * stream; the cache and the scales are touched only after that wait.  So a
- * kernel that lets its dependents start early must not write those three
- * inputs (none of this library's kernels writes them).
+ * the stream launch at once, and reads k_new and v_new (its threads' first
+ * chunks) before waiting for the previous kernel on the stream; slot_mapping,
+ * the cache and the scales are touched only after that wait.  So a kernel that
+ * lets its dependents start early must not write k_new or v_new.  (Of this
+ * library's, pkv_paged_kv_read may have written them, and
+ * pkv_block_tables_update slot_mapping: neither lets its dependents start early.)
  */
 PKV_API pkv_status pkv_paged_kv_append(const pkv_cache* cache, const void* k_new, const void* v_new,
                                        const int64_t* slot_mapping, int64_t num_tokens,
@@ -249,7 +250,8 @@ PKV_API pkv_status pkv_workspace_init(void* workspace, size_t workspace_bytes, v
  * kernel's set-up, which reads context_lens, q_lens, block_tables and q,
  * overlaps that kernel; its K/V reads and its workspace accesses wait until
  * that kernel has completed.  So a kernel that lets its dependents start
- * early must not write those four inputs.  This kernel lets the next kernel
+ * early must not write those four inputs (this library's that write them --
+ * pkv_block_tables_update, the row operators, the masked attentions -- do not).  This kernel lets the next kernel
  * on the stream launch at once; a kernel launched for programmatic
  * dependence must wait for its prerequisites (griddepcontrol.wait) before
  * reading `out` or the workspace.  Kernels launched the ordinary way see

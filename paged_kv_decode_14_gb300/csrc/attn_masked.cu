@@ -1583,6 +1583,8 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         }
     }
 
+    // (results are in L2 when the CTA ends: pkv_paged_attention reads its q before its dependency wait)
+    if (warp < kReady) __threadfence();
     // teardown: every role arrives from its own code path (non-.aligned barrier)
     __syncwarp();
     tc_fence_before();

@@ -318,6 +318,9 @@ __global__ void __launch_bounds__(kThreads, 1) update_kernel(const Arg a) {
         if (a.row_starts) a.row_starts[b] = s.row[b];
     }
     if (first == 0 && count >= 0) *a.free_count = top - taken;
+    // The append and the attention behind this kernel read slots, lengths and tables before their dependency wait: they
+    // start when every CTA here has ended (there is no early trigger), and what it wrote is in L2 by then.
+    __threadfence();
     errors = (int)__reduce_or_sync(0xffffffffu, (unsigned)errors);
     if (errors && lane == 0) raise_error(a.err, errors);
 }
