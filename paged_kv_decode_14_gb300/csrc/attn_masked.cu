@@ -53,6 +53,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "rows.cuh"
@@ -1673,7 +1674,7 @@ cudaError_t launch_masked(const pkv_cache& c, const pkv_rows* q, const pkv_rows*
     a.tree_words = tree_words;
     a.window = window;
     a.sinks = sinks;
-    a.scale_log2 = scale * kLog2e;
+    a.scale_log2 = std::min(scale * kLog2e, FLT_MAX);     // (not infinite, so that a logit of 0 stays 0)
     if (fp8)
         return c.head_dim == 128 ? launch_hg<128, true>(a, hg, grid, st) : launch_hg<64, true>(a, hg, grid, st);
     return c.head_dim == 128 ? launch_hg<128, false>(a, hg, grid, st) : launch_hg<64, false>(a, hg, grid, st);

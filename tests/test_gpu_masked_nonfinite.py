@@ -1,4 +1,4 @@
-"""Values that are not finite: what they cost a call, and where they lie in its pieces of work."""
+"""Values that are not finite: what they cost a call, where they lie in its pieces of work, and what must not become one."""
 
 import math
 import random
@@ -85,5 +85,17 @@ def test_values_anywhere_in_long_pieces(heads, kv, q_len, dtype, workspace):
     s = Sequences([tree_mask(n, q, m) for n, q, m in zip(lens, q_lens, bits)], whole=True, **kw)
     words = tree_words(bits, s.rows, s.starts, 3)
     out, lse = nat.attention_tree(s.cache, s.q, s.table, s.t_lens, s.t_q, s.max_q, words, s.scale, workspace)
+    assert nat.read_device_error(workspace) == 0
+    check(out, lse, s.reference())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("q_len", [1, 80])
+def test_logits_of_zero_with_the_largest_scale(q_len, dtype, workspace):
+    """scale times log2 e leaves fp32's range: queries of 0 see the mean of their keys' values all the same."""
+    s = Sequences([window_mask(n, q_len, 50, 3) for n in (200, 90)], 8, 2, 64, dtype, 8)
+    s.q.zero_()
+    s.scale = 3.4e38
+    out, lse = nat.attention_window(s.cache, s.q, s.table, s.t_lens, s.t_q, s.max_q, 50, 3, s.scale, workspace)
     assert nat.read_device_error(workspace) == 0
     check(out, lse, s.reference())
