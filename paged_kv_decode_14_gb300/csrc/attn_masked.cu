@@ -1419,7 +1419,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             };
             Ring rk = {}, rv = {}, rq = {};
             struct Work {
-                int cnt, x0, step, t0, two, both, ends;
+                int cnt, x0, step, t0, both, ends;
                 int whole;                                // tiles of the piece of which some row sees the last page
                 int base, q;                              // the CTA's numbers of its first tile and of the chain's Q tile
             };
@@ -1452,7 +1452,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
                     x.x0 = at->begin(i);
                     x.step = at->step();
                     x.t0 = at->t0;
-                    x.two = at->two;
                     x.both = !at->two && at->count(1) > 0;
                     x.ends = at->seen_end(a, min(at->nq, at->two ? (i + 1) * a.pb : a.pb));
                     x.whole = (x.ends - x.t0 * K::KEYS + kBlock - 1) / kBlock / K::TP;
