@@ -555,7 +555,477 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(bar(K::PCEMPTY + n % kPieces));
     };
 
-    if (warp < kReady) {
+    // (The softmax's code comes last: it is the longest, with all that runs rarely in it.  With it before the other roles',
+    // FP8 chunks took 180 us, not 176, and 128 FP8 streams 225.5, not 224.)
+    if (warp >= kProducer) {
+        regs_dec<kRegsOther>();
+        if (warp == kPlan) {
+            // -------------------------------------------- the plan (begun while the others set up)
+            griddep_wait();
+            Plan<HG> plan(a, lane);
+            plan.begin();
+            Piece p = {};
+            p.end = !plan.next(p);
+            enter();
+            // every warp is done with piece x: the only wait that keeps the time
+            auto done = [&](int x) -> bool {
+                const Ctl clock{abort_flag, a.err, a.wait_limit_ns + ring[x % kPieces].tiles() * kTileLimit};
+                return __all_sync(0xffffffffu, wait(bar(K::PCEMPTY + x % kPieces), (x / kPieces) & 1, clock));
+            };
+            for (int n = 0;; ++n) {
+                if (n >= kPieces && !done(n - kPieces)) break;
+                if (lane == 0) {
+                    ring[n % kPieces] = p;
+                    mbar_arrive(bar(K::PCFULL + n % kPieces));
+                }
+                __syncwarp();
+                if (p.end) {
+                    for (int x = max(n - kPieces, 0); x < n && done(x); ++x) {}
+                    break;
+                }
+                p.end = !plan.next(p);
+            }
+        } else if (warp == kProducer) {
+            enter();
+            // -------------------------------------------- Q tiles, K and V pages in order
+            bool ok = true;
+            int nt = 0, nq = 0, nq1 = 0, npc = 0;         // key tiles; Q tiles, those of chain 1; pieces
+            int nk = 0, nv = 0;                           // copies issued: K and V tiles
+            if (a.hold != nullptr && lane == 0) {
+                // (tests of the timeout path only) wait, bounded, for a flag that nothing sets
+                const uint64_t h0 = globaltimer_ns();
+                while (ok && *reinterpret_cast<const volatile int*>(a.hold) == 0) {
+                    if (*abort_flag || globaltimer_ns() - h0 > a.wait_limit_ns) {
+                        if (!*abort_flag) raise_error(a.err, PKV_DEVERR_TIMEOUT);
+                        *abort_flag = 1;
+                        ok = false;
+                    }
+                    __nanosleep(256);
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            // lanes 0-7 stand for a tile's units of K, 8-15 for those of V
+            // (pages leave L2 first: with them in its way the kernel's own code came from DRAM, 41 us for a decode step against 38)
+            const uint64_t evict = policy_evict_first();
+            const int u8 = lane & 7, upg = u8 / HG, uh = u8 % HG;
+            const bool is_v = lane >= 8;
+            for (int n = 0; ok; ++n) {
+                const Piece* p = piece_at(n);
+                if (!p || p->end) break;
+                const int32_t* table = a.tables + (int64_t)p->b * a.max_blocks;
+                const int np = p->np, g = p->g + uh;
+                // 32 entries of the list at a time, a lane each (a bad id is reported, and block 0 read in its place)
+                auto blocks = [&](int first) -> int {
+                    const int idx = first + lane;
+                    const int id = idx < min(np, p->t1 * K::TP) ? table[p->page(idx)] : 0;
+                    if (id >= 0 && id < a.num_blocks) return id;
+                    raise_error(a.err, PKV_DEVERR_BLOCK_ID);
+                    return 0;
+                };
+                const int first = p->t0 * K::TP;
+                int held = first, ids = blocks(first), ids1 = blocks(first + 32);       // entries from `held` on, and the next 32
+                // the block of this lane's unit of tile t, which lies among them
+                auto block = [&](int t) -> int {
+                    const int at = t * K::TP + upg - held;
+                    int id = __shfl_sync(0xffffffffu, ids, at & 31);
+                    if (__any_sync(0xffffffffu, at >= 32)) {
+                        const int x = __shfl_sync(0xffffffffu, ids1, at & 31);
+                        id = at < 32 ? id : x;
+                    }
+                    return id;
+                };
+                // (FP8) scales on their way into the ring, kAhead tiles before they are needed
+                auto fetch = [&](int t, int slot) {
+                    if (!FP8) return;
+                    const int id = block(t);
+                    if (lane < 16 && t < p->t1 && t * K::TP + upg < np)
+                        cp_async_4(sb + K::OFF_SC + ((slot % K::NSC) * 16 + lane) * 4,
+                                   (is_v ? a.v_scales : a.k_scales) + (int64_t)id * a.Hkv + g);
+                    asm volatile("cp.async.commit_group;\n" ::: "memory");
+                };
+                for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
+                    const int slot = nq & 1;
+                    if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
+                    // (bf16: a barrier each slot, for the issuers, who see every tile.  FP8: those of chain 0's, by turns, and one of
+                    // chain 1's, for the warps that split them, who see no others: no barrier's phases run ahead unseen)
+                    const uint32_t full = bar(!FP8 ? K::QFULL + slot : i == 0 ? K::QFULL + (n & 1) : K::Q1FULL);
+                    if (lane == 0) mbar_arrive_expect_tx(full, HG * K::SLABS * a.pb * a.group * 128);
+                    nq1 += i;
+                    npc += i == 0;
+                    __syncwarp();
+                    if (lane < HG * K::SLABS) {           // (a lane for each head's slab)
+                        const int sl = lane % K::SLABS, hq = lane / K::SLABS;
+                        tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + sl * K::SLAB + hq * RQ * 128, &a.q, sl * 64,
+                                   (p->g + hq) * a.group, (int)(p->row + p->q0 + i * a.pb), full);
+                    }
+                }
+#pragma unroll 1
+                for (int x = 0; x < kAhead; ++x) fetch(p->t0 + x, nt + x);
+#pragma unroll 1
+                for (int t = p->t0; t < p->t1 && ok; ++t, ++nt) {
+                    const int sk = nt % NSK, sv = nt % NSV, pages = min(K::TP, np - t * K::TP);
+                    if (t * K::TP - held >= 32) {
+                        held += 32;
+                        ids = ids1;
+                        ids1 = blocks(held + 32);
+                    }
+                    const int64_t src = ((int64_t)block(t) * a.Hkv + g) * K::LAND;
+                    if (nt >= NSK && !(ok = wait_all(bar(K::KEMPTY + sk), ((nt - NSK) / NSK) & 1))) break;
+                    fetch(t + kAhead, nt + kAhead);
+                    if (FP8) asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead) : "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(bar(K::KFULL + sk), pages * HG * K::LAND);
+                    __syncwarp();
+                    // (a page's HG heads lie side by side)
+                    if (!is_v && uh == 0 && upg < pages)
+                        bulk_g2s_hint(sb + K::OFF_K + sk * K::KTILE + u8 * K::LAND, a.k_cache + src, HG * K::LAND, bar(K::KFULL + sk),
+                                      evict);
+                    ++nk;
+                    if (nt >= NSV && !(ok = wait_all(bar(K::VEMPTY + sv), ((nt - NSV) / NSV) & 1))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(K::VFULL + sv), pages * HG * K::LAND);
+                    __syncwarp();
+                    if (is_v && lane < 16 && upg < pages) {
+                        if (FP8)
+                            bulk_g2s_hint(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE + K::LAND, a.v_cache + src, K::LAND,
+                                          bar(K::VFULL + sv), evict);
+                        else if (uh == 0)
+                            bulk_g2s_hint(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE, a.v_cache + src, HG * K::PAGE,
+                                          bar(K::VFULL + sv), evict);
+                    }
+                    ++nv;
+                }
+                // (what a piece fetched past its end is not read: its slots are the next piece's, fetched again)
+                if (FP8) cp_async_wait_all();
+                release(n);
+            }
+            if (lane == 0) {
+                // drain: every copy in flight lands before the CTA exits
+                const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
+                for (int t = max(0, nk - NSK); t < nk; ++t) wait(bar(K::KFULL + t % NSK), (t / NSK) & 1, drain);
+                for (int t = max(0, nv - NSV); t < nv; ++t) wait(bar(K::VFULL + t % NSV), (t / NSV) & 1, drain);
+                for (int t = max(0, (FP8 ? npc : nq) - 2); t < (FP8 ? npc : nq); ++t)
+                    wait(bar(K::QFULL + (t & 1)), (t >> 1) & 1, drain);
+                if (FP8 && nq1 > 0) wait(bar(K::Q1FULL), (nq1 - 1) & 1, drain);
+            }
+            __syncwarp();
+        } else if (warp == kMma || warp == kMma + 1) {
+            // -------------------------------------------- MMA issuer of chain i
+            const uint32_t tmem = enter();
+            const int i = warp - kMma;
+            const bool lead = elect_one();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);       // (known to be uniform)
+            const uint32_t s_i = tm + __shfl_sync(0xffffffffu, i, 0) * kCols;
+            const uint32_t o_i = tm + K::COL_O + __shfl_sync(0xffffffffu, i, 0) * D;
+            constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(kRows, K::HCOLS) : idesc_bf16_f32(kRows, K::HCOLS, false, false);
+            constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true);
+            int pcnt = 0, bcnt = 0;                       // this chain's tiles; pieces of both chains
+            int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
+            // K, V and Q tiles seen: every one, in order, by both chains (a barrier's parity tells neighbouring phases apart, no
+            // more).  (Slots and parities are counted, not divided: this warp's own instructions are on the chain's path.)
+            struct Ring {
+                int at, slot, used;                       // tiles seen; the next one's slot; that of the last one seen
+                uint32_t parity;
+            };
+            Ring rk = {}, rv = {}, rq = {};
+            struct Work {
+                int cnt, x0, step, t0, both, ends;
+                int whole;                                // tiles of the piece of which some row sees the last page
+                int base, q;                              // the CTA's numbers of its first tile and of the chain's Q tile
+            };
+            // the tiles up to `target`; what the other chain alone uses is given back as soon as it is there
+            auto see = [&](Ring& r, int target, bool mine, int ring_n, int full, int empty) -> bool {
+                while (r.at <= target) {
+                    if (!wait_all(bar(full + r.slot), r.parity)) return false;
+                    if (lead && !(mine && r.at == target)) mbar_arrive(bar(empty + r.slot));
+                    r.used = r.slot;
+                    ++r.at;
+                    if (++r.slot == ring_n) {
+                        r.slot = 0;
+                        r.parity ^= 1;
+                    }
+                }
+                return true;
+            };
+            constexpr int QRDY = FP8 ? K::QREADY : K::QFULL;
+            auto see_k = [&](int t, bool mine) { return see(rk, t, mine, NSK, K::KFULL, K::KEMPTY); };
+            auto see_v = [&](int t, bool mine) { return see(rv, t, mine, NSV, K::VREADY, K::VEMPTY); };
+            auto see_q = [&](int t, bool mine) { return see(rq, t, mine, 2, QRDY, K::QEMPTY); };
+            int n = 0;
+            // The next piece, if there is one and (or else, with `any`, the next that does) it has tiles of this chain.
+            auto next = [&](Work& x, bool any) -> bool {
+                for (;; ++n) {
+                    const Piece* at = piece_at(n);
+                    if (!at || at->end) return false;
+                    x.cnt = at->count(i);
+                    if (x.cnt == 0 && !any) return false;
+                    x.x0 = at->begin(i);
+                    x.step = at->step();
+                    x.t0 = at->t0;
+                    x.both = !at->two && at->count(1) > 0;
+                    x.ends = at->seen_end(a, min(at->nq, at->two ? (i + 1) * a.pb : a.pb));
+                    x.whole = (x.ends - x.t0 * K::KEYS + kBlock - 1) / kBlock / K::TP;
+                    x.base = tbase;
+                    x.q = qbase + (at->two ? i : 0);
+                    tbase += at->tiles();
+                    qbase += at->two ? 2 : 1;
+                    release(n);
+                    if (x.cnt > 0) break;
+                    if (!see_q(qbase - 1, false) || !see_k(tbase - 1, false) || !see_v(tbase - 1, false)) return false;
+                }
+                ++n;
+                return true;
+            };
+            // Half h of S of tile j of this chain's in a piece (its K and Q seen).  (A descriptor is the first one's with a
+            // constant added: made anew for each, the issue of a product took longer than the product.)
+            auto issue_s = [&](const Work& x, int j, auto half) {
+                constexpr int h = decltype(half)::value;
+                const int sk = rk.used;                   // (no tile behind it has been seen yet)
+                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::KTILE, 0) + h * (K::KTILE / K::HALVES);
+                const uint32_t q_s = __shfl_sync(0xffffffffu, sb + K::OFF_Q + (x.q & 1) * K::QTILE, 0);
+                constexpr uint32_t dst = h * K::HCOLS;
+                if constexpr (FP8) {
+                    constexpr uint32_t LO = D == 128 ? K::SLAB : 512;
+                    const uint64_t dq = smem_desc(q_s, 128, 1024), dk = smem_desc(kbase, 128, D * 8);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)      // the first term's, then the second's
+                        mma_ss_f8(lead, s_i + dst, dq + (((k / (D / 32)) * LO + (k % (D / 32)) * 256) >> 4),
+                                  dk + (((k % (D / 32)) * 256) >> 4), idS, k > 0 ? 1u : 0u);
+                } else {
+                    const uint64_t dq = desc_sw128(q_s, 16, 1024), dk = smem_desc(kbase, 128, K::NCH * 128);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(lead, s_i + dst, dq + (((k / 4) * K::SLAB + (k % 4) * 32) >> 4), dk + ((k * 256) >> 4), idS,
+                               k > 0 ? 1u : 0u);
+                }
+                commit(lead, bar(K::SFULL + 2 * i + h));
+                if (h == K::HALVES - 1) {
+                    commit(lead, bar(K::KEMPTY + sk));
+                    if (j + 1 == x.cnt) commit(lead, bar(K::QEMPTY + (x.q & 1)));
+                }
+            };
+            // One loop: by halves, P . V of the chain's present tile, if there is one, each with the same half of S of the next
+            // tile behind it, if there is one in the piece; then both halves of S of a new piece's first.  One thread's
+            // products are done in order: S of a half may overwrite the P there.
+            Work p = {}, q = {};
+            int j = 0, jq = 0;
+            bool now = false, ok = true;                  // now: S of tile j of piece p has been issued
+#pragma unroll 1
+            while (ok) {
+                bool then, fresh = false;
+                if (now && j + 1 < p.cnt) {
+                    q = p;
+                    jq = j + 1;
+                    then = true;
+                } else {
+                    then = next(q, !now);                 // (in time for the present piece's last tile, if it is there)
+                    jq = 0;
+                    fresh = true;
+                    if (!then && !now) break;
+                }
+                const int x = p.x0 + j * p.step;
+                if (now) {
+                    if (!see_v(p.base + x, true)) break;
+                    // a piece's first PV starts O afresh: the other chain too has read the last result that they shared
+                    if (j == 0 && bcnt > 0 && !wait_all(bar(K::OFREE), (bcnt - 1) & 1)) break;
+                }
+                const int sv = rv.used;
+                const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
+                // units up to the last page that a row sees
+                const int steps = x < p.whole ? kUnits : HG * min(max((p.ends - (p.t0 + x) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
+                constexpr int HALVES = K::HALVES, EACH = kUnits / HALVES;
+                // a turn: P . V of half h, if there is a present tile, and S of it, if it belongs to the same piece; the second
+                // time (a new piece), S of both
+                auto turn = [&](auto half) -> bool {
+                    constexpr int h = decltype(half)::value;
+                    if (now) {
+                        if (!wait_all(bar(K::PFULL + 2 * i + h), pcnt & 1)) return false;
+                        tc_fence_after();
+                        const uint64_t dv = smem_desc(vbase, K::NCH * 128, 128);
+                        if (steps == kUnits) {
+#pragma unroll
+                            for (int k = 0; k < EACH; ++k)
+                                mma_ts(lead, o_i, s_i + h * K::HCOLS + k * 8, dv + (((EACH * h + k) * K::PAGE) >> 4), idPV,
+                                       h > 0 || k > 0 ? 1u : j > 0 ? 1u : 0u);
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; k < min(EACH, steps - EACH * h); ++k)
+                                mma_ts(lead, o_i, s_i + h * K::HCOLS + k * 8, dv + (((EACH * h + k) * K::PAGE) >> 4), idPV,
+                                       j > 0 || h > 0 || k > 0 ? 1u : 0u);
+                        }
+                        if (HALVES > 1) commit(lead, bar(K::PVDONE + 2 * i + h));
+                        if (h == HALVES - 1) {
+                            if (j + 1 == p.cnt) commit(lead, bar(K::ODONE + i));
+                            commit(lead, bar(K::VEMPTY + sv));
+                        }
+                    }
+                    return true;
+                };
+                using H0 = std::integral_constant<int, 0>;
+                using H1 = std::integral_constant<int, HALVES - 1>;
+                if (!(ok = turn(H0{}))) break;
+                // (the next S's K is waited for while P . V runs: before it, a late K kept V from being given back)
+                if (then && !fresh && !(ok = see_k(q.base + q.x0 + jq * q.step, true))) break;
+                // (a new piece's Q and K: bf16 by halves, before the last P; else, as FP8's softmax warps split Q behind it, after)
+                constexpr bool EARLY = !FP8 && HALVES > 1;
+                if (EARLY && then && fresh && !(ok = see_q(q.q, true) && see_k(q.base + q.x0, true))) break;
+                if (HALVES > 1) {
+                    if (then && !fresh) issue_s(q, jq, H0{});
+                    if (!(ok = turn(H1{}))) break;
+                }
+                if (!EARLY && then && fresh && !(ok = see_q(q.q, true) && see_k(q.base + q.x0, true))) break;
+                if (then && fresh) tc_fence_after();
+                if (then && (fresh && HALVES > 1)) issue_s(q, jq, H0{});
+                if (then) issue_s(q, jq, H1{});
+                if (now) {
+                    bcnt += j + 1 == p.cnt && p.both;
+                    ++pcnt;
+                }
+                now = then;
+                p = q;
+                j = jq;
+            }
+            commit(lead, bar(K::DRAIN));
+            // every MMA issued has completed before TMEM is freed
+            const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
+            wait(bar(K::DRAIN), 0, drain);
+            __syncwarp();
+        }
+    } else if (warp >= kReady) {
+        // ------------------------------------------------ V made ready
+        regs_dec<kRegsReady>();
+        enter();
+        const int w = warp - kReady;
+
+        // V is made harmless to rows that do not see it: a weight of 0 times NaN or infinity is NaN.  Keys that no row sees
+        // are cleared, and non-finite values become 0 where some rows do not see them (HG > 1: everywhere, for other
+        // heads' rows have weight 0 for them) and are added back, row by row, in the epilogue (from global memory:
+        // rare).
+        // (FP8) `pages` of the two pages of V from `at` on, each in the upper half of its place and widened over it; their
+        // first keys at v and v1.  vs: their scales; where one is not finite, all its page's codes count as NaN (and it, as 1)
+        auto widen_pages = [&](uint8_t* at, const Guard<HG>& gd, int v, int v1, int pages, const float* vs) -> bool {
+            constexpr int N = D / 32;                     // 16-byte chunks of codes a lane and page
+            // (a lane's chunk j % N of page j / N: its key of the page, and where it goes)
+            auto key_of = [&](int j) { return (lane & 7) + ((lane + 32 * (j % N)) >> 3) / (D / 16) * 8; };
+            auto place = [&](int j) {
+                const int q = (lane + 32 * (j % N)) >> 3;
+                return at + j / N * K::PAGE + q / (D / 16) * (K::NCH * 128) + 2 * (q % (D / 16)) * 128 + (lane & 7) * 16;
+            };
+            uint32_t nan = 0;                             // a lane's chunks that hold NaN codes
+#pragma unroll 1
+            for (int pg = 0; pg < pages; ++pg) {          // (rolled, for the instruction cache)
+                uint4 raw[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    raw[j] = *reinterpret_cast<const uint4*>(at + pg * K::PAGE + K::LAND + (lane + 32 * j) * 16);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    uint32_t o[8];
+                    widen4(raw[j].x, o[0], o[1]);
+                    widen4(raw[j].y, o[2], o[3]);
+                    widen4(raw[j].z, o[4], o[5]);
+                    widen4(raw[j].w, o[6], o[7]);
+                    if (nan_codes(raw[j].x) | nan_codes(raw[j].y) | nan_codes(raw[j].z) | nan_codes(raw[j].w)) nan |= 1u << (pg * N + j);
+                    uint8_t* dst = place(j) + pg * K::PAGE;
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+            }
+            const bool fin0 = fabsf(vs[0]) < INFINITY, fin1 = pages < 2 || fabsf(vs[1]) < INFINITY;
+            if (!gd.any_of(v, kBlock) || (pages > 1 && !gd.any_of(v1, kBlock))) {
+#pragma unroll 1
+                for (int j = 0; j < pages * N; ++j) {
+                    if (gd.any((j < N ? v : v1) + key_of(j))) continue;
+                    *reinterpret_cast<uint4*>(place(j)) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(place(j) + 128) = make_uint4(0, 0, 0, 0);
+                    nan &= ~(1u << j);
+                }
+            }
+            bool found = false;
+            if (nan != 0 || !fin0 || !fin1) {
+                // (rare) a lane's own chunks again: a NaN code is the only one that has become +-480
+#pragma unroll 1
+                for (int j = 0; j < pages * N; ++j) {
+                    const int key = (j < N ? v : v1) + key_of(j);
+                    const bool fin = j < N ? fin0 : fin1, leave = gd.all(key) && fin;
+                    if (!gd.any(key) || ((nan >> j & 1) == 0 && fin)) continue;
+                    uint16_t* e = reinterpret_cast<uint16_t*>(place(j));
+#pragma unroll 1
+                    for (int y = 0; y < 16; ++y) {
+                        uint16_t& x = e[y / 8 * 64 + y % 8];
+                        if ((x & 0x7fff) == 0x43f0 || !fin) x = leave ? 0x7fc0 : 0;
+                    }
+                    found |= !leave;
+                }
+            }
+            return found;
+        };
+        auto guard_group = [&](uint8_t* at, const Guard<HG>& gd, int v) -> bool {     // 8 keys of bf16 V
+            constexpr int N = K::NCH / 4;
+            uint4* e = reinterpret_cast<uint4*>(at + lane * 16);
+            const int key = v + (lane & 7);
+            if (!gd.any(key)) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) e[32 * j] = make_uint4(0, 0, 0, 0);
+                return false;
+            }
+            uint32_t bad = 0;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint4 x = e[32 * j];
+                bad |= inf_words(x.x) | inf_words(x.y) | inf_words(x.z) | inf_words(x.w);
+            }
+            if (bad == 0 || gd.all(key)) return false;
+#pragma unroll 1
+            for (int j = 0; j < 4 * N; ++j) {
+                uint32_t* y = reinterpret_cast<uint32_t*>(e + 32 * (j / 4)) + j % 4;
+                const uint32_t hit = inf_words(*y);
+                *y &= ~((hit >> 15) * 0xffffu);
+            }
+            return true;
+        };
+        // One warp's share of tile x of piece n, the CTA's gt-th: its units 2 w and 2 w + 1.
+        auto ready_v = [&](const Piece& p, int n, int x, int gt) {
+            const int sv = gt % NSV, v0 = (p.t0 + x) * K::KEYS, pages = min(K::TP, p.np - (p.t0 + x) * K::TP);
+            uint8_t* base = smem + K::OFF_V + sv * K::VTILE;
+            const Guard<HG> gd = guard_of<HG>(a, p);
+            bool found = false;
+            if constexpr (FP8) {
+                const int pg = 2 * w / HG, pg1 = (2 * w + 1) / HG;
+                if (pg < pages)
+                    found = widen_pages(base + 2 * w * K::PAGE, gd, v0 + pg * kBlock, v0 + pg1 * kBlock, pg1 < pages ? 2 : 1,
+                                        scales + gt % K::NSC * 16 + 8 + 2 * w);
+                fence_proxy_async_smem();
+            } else {
+                bool touched = false;
+#pragma unroll 1
+                for (int y = 4 * w; y < 4 * w + 4; ++y) {
+                    const int pg = y / 2 / HG, v = v0 + pg * kBlock + (y & 1) * 8;
+                    if (pg >= pages || gd.all_of(v, 8)) continue;
+                    const bool f = guard_group(base + y * (K::NCH * 128), gd, v);
+                    found |= f;
+                    touched |= f || !gd.any_of(v, 8);
+                }
+                if (__any_sync(0xffffffffu, touched)) fence_proxy_async_smem();
+            }
+            if (__any_sync(0xffffffffu, found) && lane == 0) atomicOr(&ring[n % kPieces].bad, 1u << (x >> p.mark_shift()));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
+        };
+        bool ok = true;
+        int gt = 0;                                       // key tiles
+        for (int n = 0; ok; ++n) {
+            const Piece* p = piece_at(n);
+            if (!p || p->end) break;
+            const int tiles = p->tiles();
+#pragma unroll 1
+            for (int x = 0; x < tiles && ok; ++x, ++gt) {
+                if (!(ok = wait_all(bar(K::VFULL + gt % NSV), (gt / NSV) & 1))) break;
+                ready_v(*p, n, x, gt);
+            }
+            release(n);
+        }
+    } else {
         // ------------------------------------------------ softmax of chain i, thread r = row r
         regs_inc<kRegsSoftmax>();
         const uint32_t tmem = enter();
@@ -1112,474 +1582,6 @@ __global__ void __launch_bounds__(kThreads, 1) masked_kernel(const __grid_consta
             ++pieces;
             pieces1 += p->two || both;
             release(n);
-        }
-    } else if (warp < kProducer) {
-        // ------------------------------------------------ V made ready
-        regs_dec<kRegsReady>();
-        enter();
-        const int w = warp - kReady;
-
-        // V is made harmless to rows that do not see it: a weight of 0 times NaN or infinity is NaN.  Keys that no row sees
-        // are cleared, and non-finite values become 0 where some rows do not see them (HG > 1: everywhere, for other
-        // heads' rows have weight 0 for them) and are added back, row by row, in the epilogue (from global memory:
-        // rare).
-        // (FP8) `pages` of the two pages of V from `at` on, each in the upper half of its place and widened over it; their
-        // first keys at v and v1.  vs: their scales; where one is not finite, all its page's codes count as NaN (and it, as 1)
-        auto widen_pages = [&](uint8_t* at, const Guard<HG>& gd, int v, int v1, int pages, const float* vs) -> bool {
-            constexpr int N = D / 32;                     // 16-byte chunks of codes a lane and page
-            // (a lane's chunk j % N of page j / N: its key of the page, and where it goes)
-            auto key_of = [&](int j) { return (lane & 7) + ((lane + 32 * (j % N)) >> 3) / (D / 16) * 8; };
-            auto place = [&](int j) {
-                const int q = (lane + 32 * (j % N)) >> 3;
-                return at + j / N * K::PAGE + q / (D / 16) * (K::NCH * 128) + 2 * (q % (D / 16)) * 128 + (lane & 7) * 16;
-            };
-            uint32_t nan = 0;                             // a lane's chunks that hold NaN codes
-#pragma unroll 1
-            for (int pg = 0; pg < pages; ++pg) {          // (rolled, for the instruction cache)
-                uint4 raw[N];
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    raw[j] = *reinterpret_cast<const uint4*>(at + pg * K::PAGE + K::LAND + (lane + 32 * j) * 16);
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    uint32_t o[8];
-                    widen4(raw[j].x, o[0], o[1]);
-                    widen4(raw[j].y, o[2], o[3]);
-                    widen4(raw[j].z, o[4], o[5]);
-                    widen4(raw[j].w, o[6], o[7]);
-                    if (nan_codes(raw[j].x) | nan_codes(raw[j].y) | nan_codes(raw[j].z) | nan_codes(raw[j].w)) nan |= 1u << (pg * N + j);
-                    uint8_t* dst = place(j) + pg * K::PAGE;
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(dst + 128) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-            }
-            const bool fin0 = fabsf(vs[0]) < INFINITY, fin1 = pages < 2 || fabsf(vs[1]) < INFINITY;
-            if (!gd.any_of(v, kBlock) || (pages > 1 && !gd.any_of(v1, kBlock))) {
-#pragma unroll 1
-                for (int j = 0; j < pages * N; ++j) {
-                    if (gd.any((j < N ? v : v1) + key_of(j))) continue;
-                    *reinterpret_cast<uint4*>(place(j)) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(place(j) + 128) = make_uint4(0, 0, 0, 0);
-                    nan &= ~(1u << j);
-                }
-            }
-            bool found = false;
-            if (nan != 0 || !fin0 || !fin1) {
-                // (rare) a lane's own chunks again: a NaN code is the only one that has become +-480
-#pragma unroll 1
-                for (int j = 0; j < pages * N; ++j) {
-                    const int key = (j < N ? v : v1) + key_of(j);
-                    const bool fin = j < N ? fin0 : fin1, leave = gd.all(key) && fin;
-                    if (!gd.any(key) || ((nan >> j & 1) == 0 && fin)) continue;
-                    uint16_t* e = reinterpret_cast<uint16_t*>(place(j));
-#pragma unroll 1
-                    for (int y = 0; y < 16; ++y) {
-                        uint16_t& x = e[y / 8 * 64 + y % 8];
-                        if ((x & 0x7fff) == 0x43f0 || !fin) x = leave ? 0x7fc0 : 0;
-                    }
-                    found |= !leave;
-                }
-            }
-            return found;
-        };
-        auto guard_group = [&](uint8_t* at, const Guard<HG>& gd, int v) -> bool {     // 8 keys of bf16 V
-            constexpr int N = K::NCH / 4;
-            uint4* e = reinterpret_cast<uint4*>(at + lane * 16);
-            const int key = v + (lane & 7);
-            if (!gd.any(key)) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) e[32 * j] = make_uint4(0, 0, 0, 0);
-                return false;
-            }
-            uint32_t bad = 0;
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const uint4 x = e[32 * j];
-                bad |= inf_words(x.x) | inf_words(x.y) | inf_words(x.z) | inf_words(x.w);
-            }
-            if (bad == 0 || gd.all(key)) return false;
-#pragma unroll 1
-            for (int j = 0; j < 4 * N; ++j) {
-                uint32_t* y = reinterpret_cast<uint32_t*>(e + 32 * (j / 4)) + j % 4;
-                const uint32_t hit = inf_words(*y);
-                *y &= ~((hit >> 15) * 0xffffu);
-            }
-            return true;
-        };
-        // One warp's share of tile x of piece n, the CTA's gt-th: its units 2 w and 2 w + 1.
-        auto ready_v = [&](const Piece& p, int n, int x, int gt) {
-            const int sv = gt % NSV, v0 = (p.t0 + x) * K::KEYS, pages = min(K::TP, p.np - (p.t0 + x) * K::TP);
-            uint8_t* base = smem + K::OFF_V + sv * K::VTILE;
-            const Guard<HG> gd = guard_of<HG>(a, p);
-            bool found = false;
-            if constexpr (FP8) {
-                const int pg = 2 * w / HG, pg1 = (2 * w + 1) / HG;
-                if (pg < pages)
-                    found = widen_pages(base + 2 * w * K::PAGE, gd, v0 + pg * kBlock, v0 + pg1 * kBlock, pg1 < pages ? 2 : 1,
-                                        scales + gt % K::NSC * 16 + 8 + 2 * w);
-                fence_proxy_async_smem();
-            } else {
-                bool touched = false;
-#pragma unroll 1
-                for (int y = 4 * w; y < 4 * w + 4; ++y) {
-                    const int pg = y / 2 / HG, v = v0 + pg * kBlock + (y & 1) * 8;
-                    if (pg >= pages || gd.all_of(v, 8)) continue;
-                    const bool f = guard_group(base + y * (K::NCH * 128), gd, v);
-                    found |= f;
-                    touched |= f || !gd.any_of(v, 8);
-                }
-                if (__any_sync(0xffffffffu, touched)) fence_proxy_async_smem();
-            }
-            if (__any_sync(0xffffffffu, found) && lane == 0) atomicOr(&ring[n % kPieces].bad, 1u << (x >> p.mark_shift()));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(K::VREADY + sv));
-        };
-        bool ok = true;
-        int gt = 0;                                       // key tiles
-        for (int n = 0; ok; ++n) {
-            const Piece* p = piece_at(n);
-            if (!p || p->end) break;
-            const int tiles = p->tiles();
-#pragma unroll 1
-            for (int x = 0; x < tiles && ok; ++x, ++gt) {
-                if (!(ok = wait_all(bar(K::VFULL + gt % NSV), (gt / NSV) & 1))) break;
-                ready_v(*p, n, x, gt);
-            }
-            release(n);
-        }
-    } else {
-        regs_dec<kRegsOther>();
-        if (warp == kPlan) {
-            // -------------------------------------------- the plan (begun while the others set up)
-            griddep_wait();
-            Plan<HG> plan(a, lane);
-            plan.begin();
-            Piece p = {};
-            p.end = !plan.next(p);
-            enter();
-            // every warp is done with piece x: the only wait that keeps the time
-            auto done = [&](int x) -> bool {
-                const Ctl clock{abort_flag, a.err, a.wait_limit_ns + ring[x % kPieces].tiles() * kTileLimit};
-                return __all_sync(0xffffffffu, wait(bar(K::PCEMPTY + x % kPieces), (x / kPieces) & 1, clock));
-            };
-            for (int n = 0;; ++n) {
-                if (n >= kPieces && !done(n - kPieces)) break;
-                if (lane == 0) {
-                    ring[n % kPieces] = p;
-                    mbar_arrive(bar(K::PCFULL + n % kPieces));
-                }
-                __syncwarp();
-                if (p.end) {
-                    for (int x = max(n - kPieces, 0); x < n && done(x); ++x) {}
-                    break;
-                }
-                p.end = !plan.next(p);
-            }
-        } else if (warp == kProducer) {
-            enter();
-            // -------------------------------------------- Q tiles, K and V pages in order
-            bool ok = true;
-            int nt = 0, nq = 0, nq1 = 0, npc = 0;         // key tiles; Q tiles, those of chain 1; pieces
-            int nk = 0, nv = 0;                           // copies issued: K and V tiles
-            if (a.hold != nullptr && lane == 0) {
-                // (tests of the timeout path only) wait, bounded, for a flag that nothing sets
-                const uint64_t h0 = globaltimer_ns();
-                while (ok && *reinterpret_cast<const volatile int*>(a.hold) == 0) {
-                    if (*abort_flag || globaltimer_ns() - h0 > a.wait_limit_ns) {
-                        if (!*abort_flag) raise_error(a.err, PKV_DEVERR_TIMEOUT);
-                        *abort_flag = 1;
-                        ok = false;
-                    }
-                    __nanosleep(256);
-                }
-            }
-            ok = __all_sync(0xffffffffu, ok);
-            // lanes 0-7 stand for a tile's units of K, 8-15 for those of V
-            // (pages leave L2 first: with them in its way the kernel's own code came from DRAM, 41 us for a decode step against 38)
-            const uint64_t evict = policy_evict_first();
-            const int u8 = lane & 7, upg = u8 / HG, uh = u8 % HG;
-            const bool is_v = lane >= 8;
-            for (int n = 0; ok; ++n) {
-                const Piece* p = piece_at(n);
-                if (!p || p->end) break;
-                const int32_t* table = a.tables + (int64_t)p->b * a.max_blocks;
-                const int np = p->np, g = p->g + uh;
-                // 32 entries of the list at a time, a lane each (a bad id is reported, and block 0 read in its place)
-                auto blocks = [&](int first) -> int {
-                    const int idx = first + lane;
-                    const int id = idx < min(np, p->t1 * K::TP) ? table[p->page(idx)] : 0;
-                    if (id >= 0 && id < a.num_blocks) return id;
-                    raise_error(a.err, PKV_DEVERR_BLOCK_ID);
-                    return 0;
-                };
-                const int first = p->t0 * K::TP;
-                int held = first, ids = blocks(first), ids1 = blocks(first + 32);       // entries from `held` on, and the next 32
-                // the block of this lane's unit of tile t, which lies among them
-                auto block = [&](int t) -> int {
-                    const int at = t * K::TP + upg - held;
-                    int id = __shfl_sync(0xffffffffu, ids, at & 31);
-                    if (__any_sync(0xffffffffu, at >= 32)) {
-                        const int x = __shfl_sync(0xffffffffu, ids1, at & 31);
-                        id = at < 32 ? id : x;
-                    }
-                    return id;
-                };
-                // (FP8) scales on their way into the ring, kAhead tiles before they are needed
-                auto fetch = [&](int t, int slot) {
-                    if (!FP8) return;
-                    const int id = block(t);
-                    if (lane < 16 && t < p->t1 && t * K::TP + upg < np)
-                        cp_async_4(sb + K::OFF_SC + ((slot % K::NSC) * 16 + lane) * 4,
-                                   (is_v ? a.v_scales : a.k_scales) + (int64_t)id * a.Hkv + g);
-                    asm volatile("cp.async.commit_group;\n" ::: "memory");
-                };
-                for (int i = 0; i < (p->two ? 2 : 1) && ok; ++i, ++nq) {
-                    const int slot = nq & 1;
-                    if (nq >= 2 && !(ok = wait_all(bar(K::QEMPTY + slot), ((nq - 2) >> 1) & 1))) break;
-                    // (bf16: a barrier each slot, for the issuers, who see every tile.  FP8: those of chain 0's, by turns, and one of
-                    // chain 1's, for the warps that split them, who see no others: no barrier's phases run ahead unseen)
-                    const uint32_t full = bar(!FP8 ? K::QFULL + slot : i == 0 ? K::QFULL + (n & 1) : K::Q1FULL);
-                    if (lane == 0) mbar_arrive_expect_tx(full, HG * K::SLABS * a.pb * a.group * 128);
-                    nq1 += i;
-                    npc += i == 0;
-                    __syncwarp();
-                    if (lane < HG * K::SLABS) {           // (a lane for each head's slab)
-                        const int sl = lane % K::SLABS, hq = lane / K::SLABS;
-                        tensor_g2s(sb + K::OFF_Q + slot * K::QTILE + sl * K::SLAB + hq * RQ * 128, &a.q, sl * 64,
-                                   (p->g + hq) * a.group, (int)(p->row + p->q0 + i * a.pb), full);
-                    }
-                }
-#pragma unroll 1
-                for (int x = 0; x < kAhead; ++x) fetch(p->t0 + x, nt + x);
-#pragma unroll 1
-                for (int t = p->t0; t < p->t1 && ok; ++t, ++nt) {
-                    const int sk = nt % NSK, sv = nt % NSV, pages = min(K::TP, np - t * K::TP);
-                    if (t * K::TP - held >= 32) {
-                        held += 32;
-                        ids = ids1;
-                        ids1 = blocks(held + 32);
-                    }
-                    const int64_t src = ((int64_t)block(t) * a.Hkv + g) * K::LAND;
-                    if (nt >= NSK && !(ok = wait_all(bar(K::KEMPTY + sk), ((nt - NSK) / NSK) & 1))) break;
-                    fetch(t + kAhead, nt + kAhead);
-                    if (FP8) asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead) : "memory");
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(bar(K::KFULL + sk), pages * HG * K::LAND);
-                    __syncwarp();
-                    // (a page's HG heads lie side by side)
-                    if (!is_v && uh == 0 && upg < pages)
-                        bulk_g2s_hint(sb + K::OFF_K + sk * K::KTILE + u8 * K::LAND, a.k_cache + src, HG * K::LAND, bar(K::KFULL + sk),
-                                      evict);
-                    ++nk;
-                    if (nt >= NSV && !(ok = wait_all(bar(K::VEMPTY + sv), ((nt - NSV) / NSV) & 1))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(K::VFULL + sv), pages * HG * K::LAND);
-                    __syncwarp();
-                    if (is_v && lane < 16 && upg < pages) {
-                        if (FP8)
-                            bulk_g2s_hint(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE + K::LAND, a.v_cache + src, K::LAND,
-                                          bar(K::VFULL + sv), evict);
-                        else if (uh == 0)
-                            bulk_g2s_hint(sb + K::OFF_V + sv * K::VTILE + u8 * K::PAGE, a.v_cache + src, HG * K::PAGE,
-                                          bar(K::VFULL + sv), evict);
-                    }
-                    ++nv;
-                }
-                // (what a piece fetched past its end is not read: its slots are the next piece's, fetched again)
-                if (FP8) cp_async_wait_all();
-                release(n);
-            }
-            if (lane == 0) {
-                // drain: every copy in flight lands before the CTA exits
-                const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
-                for (int t = max(0, nk - NSK); t < nk; ++t) wait(bar(K::KFULL + t % NSK), (t / NSK) & 1, drain);
-                for (int t = max(0, nv - NSV); t < nv; ++t) wait(bar(K::VFULL + t % NSV), (t / NSV) & 1, drain);
-                for (int t = max(0, (FP8 ? npc : nq) - 2); t < (FP8 ? npc : nq); ++t)
-                    wait(bar(K::QFULL + (t & 1)), (t >> 1) & 1, drain);
-                if (FP8 && nq1 > 0) wait(bar(K::Q1FULL), (nq1 - 1) & 1, drain);
-            }
-            __syncwarp();
-        } else if (warp == kMma || warp == kMma + 1) {
-            // -------------------------------------------- MMA issuer of chain i
-            const uint32_t tmem = enter();
-            const int i = warp - kMma;
-            const bool lead = elect_one();
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);       // (known to be uniform)
-            const uint32_t s_i = tm + __shfl_sync(0xffffffffu, i, 0) * kCols;
-            const uint32_t o_i = tm + K::COL_O + __shfl_sync(0xffffffffu, i, 0) * D;
-            constexpr uint32_t idS = FP8 ? idesc_e4m3_f32(kRows, K::HCOLS) : idesc_bf16_f32(kRows, K::HCOLS, false, false);
-            constexpr uint32_t idPV = idesc_bf16_f32(kRows, D, false, true);
-            int pcnt = 0, bcnt = 0;                       // this chain's tiles; pieces of both chains
-            int tbase = 0, qbase = 0;                     // the CTA's key tiles and Q tiles up to the next piece
-            // K, V and Q tiles seen: every one, in order, by both chains (a barrier's parity tells neighbouring phases apart, no
-            // more).  (Slots and parities are counted, not divided: this warp's own instructions are on the chain's path.)
-            struct Ring {
-                int at, slot, used;                       // tiles seen; the next one's slot; that of the last one seen
-                uint32_t parity;
-            };
-            Ring rk = {}, rv = {}, rq = {};
-            struct Work {
-                int cnt, x0, step, t0, both, ends;
-                int whole;                                // tiles of the piece of which some row sees the last page
-                int base, q;                              // the CTA's numbers of its first tile and of the chain's Q tile
-            };
-            // the tiles up to `target`; what the other chain alone uses is given back as soon as it is there
-            auto see = [&](Ring& r, int target, bool mine, int ring_n, int full, int empty) -> bool {
-                while (r.at <= target) {
-                    if (!wait_all(bar(full + r.slot), r.parity)) return false;
-                    if (lead && !(mine && r.at == target)) mbar_arrive(bar(empty + r.slot));
-                    r.used = r.slot;
-                    ++r.at;
-                    if (++r.slot == ring_n) {
-                        r.slot = 0;
-                        r.parity ^= 1;
-                    }
-                }
-                return true;
-            };
-            constexpr int QRDY = FP8 ? K::QREADY : K::QFULL;
-            auto see_k = [&](int t, bool mine) { return see(rk, t, mine, NSK, K::KFULL, K::KEMPTY); };
-            auto see_v = [&](int t, bool mine) { return see(rv, t, mine, NSV, K::VREADY, K::VEMPTY); };
-            auto see_q = [&](int t, bool mine) { return see(rq, t, mine, 2, QRDY, K::QEMPTY); };
-            int n = 0;
-            // The next piece, if there is one and (or else, with `any`, the next that does) it has tiles of this chain.
-            auto next = [&](Work& x, bool any) -> bool {
-                for (;; ++n) {
-                    const Piece* at = piece_at(n);
-                    if (!at || at->end) return false;
-                    x.cnt = at->count(i);
-                    if (x.cnt == 0 && !any) return false;
-                    x.x0 = at->begin(i);
-                    x.step = at->step();
-                    x.t0 = at->t0;
-                    x.both = !at->two && at->count(1) > 0;
-                    x.ends = at->seen_end(a, min(at->nq, at->two ? (i + 1) * a.pb : a.pb));
-                    x.whole = (x.ends - x.t0 * K::KEYS + kBlock - 1) / kBlock / K::TP;
-                    x.base = tbase;
-                    x.q = qbase + (at->two ? i : 0);
-                    tbase += at->tiles();
-                    qbase += at->two ? 2 : 1;
-                    release(n);
-                    if (x.cnt > 0) break;
-                    if (!see_q(qbase - 1, false) || !see_k(tbase - 1, false) || !see_v(tbase - 1, false)) return false;
-                }
-                ++n;
-                return true;
-            };
-            // Half h of S of tile j of this chain's in a piece (its K and Q seen).  (A descriptor is the first one's with a
-            // constant added: made anew for each, the issue of a product took longer than the product.)
-            auto issue_s = [&](const Work& x, int j, auto half) {
-                constexpr int h = decltype(half)::value;
-                const int sk = rk.used;                   // (no tile behind it has been seen yet)
-                const uint32_t kbase = __shfl_sync(0xffffffffu, sb + K::OFF_K + sk * K::KTILE, 0) + h * (K::KTILE / K::HALVES);
-                const uint32_t q_s = __shfl_sync(0xffffffffu, sb + K::OFF_Q + (x.q & 1) * K::QTILE, 0);
-                constexpr uint32_t dst = h * K::HCOLS;
-                if constexpr (FP8) {
-                    constexpr uint32_t LO = D == 128 ? K::SLAB : 512;
-                    const uint64_t dq = smem_desc(q_s, 128, 1024), dk = smem_desc(kbase, 128, D * 8);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)      // the first term's, then the second's
-                        mma_ss_f8(lead, s_i + dst, dq + (((k / (D / 32)) * LO + (k % (D / 32)) * 256) >> 4),
-                                  dk + (((k % (D / 32)) * 256) >> 4), idS, k > 0 ? 1u : 0u);
-                } else {
-                    const uint64_t dq = desc_sw128(q_s, 16, 1024), dk = smem_desc(kbase, 128, K::NCH * 128);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ss(lead, s_i + dst, dq + (((k / 4) * K::SLAB + (k % 4) * 32) >> 4), dk + ((k * 256) >> 4), idS,
-                               k > 0 ? 1u : 0u);
-                }
-                commit(lead, bar(K::SFULL + 2 * i + h));
-                if (h == K::HALVES - 1) {
-                    commit(lead, bar(K::KEMPTY + sk));
-                    if (j + 1 == x.cnt) commit(lead, bar(K::QEMPTY + (x.q & 1)));
-                }
-            };
-            // One loop: by halves, P . V of the chain's present tile, if there is one, each with the same half of S of the next
-            // tile behind it, if there is one in the piece; then both halves of S of a new piece's first.  One thread's
-            // products are done in order: S of a half may overwrite the P there.
-            Work p = {}, q = {};
-            int j = 0, jq = 0;
-            bool now = false, ok = true;                  // now: S of tile j of piece p has been issued
-#pragma unroll 1
-            while (ok) {
-                bool then, fresh = false;
-                if (now && j + 1 < p.cnt) {
-                    q = p;
-                    jq = j + 1;
-                    then = true;
-                } else {
-                    then = next(q, !now);                 // (in time for the present piece's last tile, if it is there)
-                    jq = 0;
-                    fresh = true;
-                    if (!then && !now) break;
-                }
-                const int x = p.x0 + j * p.step;
-                if (now) {
-                    if (!see_v(p.base + x, true)) break;
-                    // a piece's first PV starts O afresh: the other chain too has read the last result that they shared
-                    if (j == 0 && bcnt > 0 && !wait_all(bar(K::OFREE), (bcnt - 1) & 1)) break;
-                }
-                const int sv = rv.used;
-                const uint32_t vbase = __shfl_sync(0xffffffffu, sb + K::OFF_V + sv * K::VTILE, 0);
-                // units up to the last page that a row sees
-                const int steps = x < p.whole ? kUnits : HG * min(max((p.ends - (p.t0 + x) * K::KEYS + kBlock - 1) / kBlock, 1), K::TP);
-                constexpr int HALVES = K::HALVES, EACH = kUnits / HALVES;
-                // a turn: P . V of half h, if there is a present tile, and S of it, if it belongs to the same piece; the second
-                // time (a new piece), S of both
-                auto turn = [&](auto half) -> bool {
-                    constexpr int h = decltype(half)::value;
-                    if (now) {
-                        if (!wait_all(bar(K::PFULL + 2 * i + h), pcnt & 1)) return false;
-                        tc_fence_after();
-                        const uint64_t dv = smem_desc(vbase, K::NCH * 128, 128);
-                        if (steps == kUnits) {
-#pragma unroll
-                            for (int k = 0; k < EACH; ++k)
-                                mma_ts(lead, o_i, s_i + h * K::HCOLS + k * 8, dv + (((EACH * h + k) * K::PAGE) >> 4), idPV,
-                                       h > 0 || k > 0 ? 1u : j > 0 ? 1u : 0u);
-                        } else {
-#pragma unroll 1
-                            for (int k = 0; k < min(EACH, steps - EACH * h); ++k)
-                                mma_ts(lead, o_i, s_i + h * K::HCOLS + k * 8, dv + (((EACH * h + k) * K::PAGE) >> 4), idPV,
-                                       j > 0 || h > 0 || k > 0 ? 1u : 0u);
-                        }
-                        if (HALVES > 1) commit(lead, bar(K::PVDONE + 2 * i + h));
-                        if (h == HALVES - 1) {
-                            if (j + 1 == p.cnt) commit(lead, bar(K::ODONE + i));
-                            commit(lead, bar(K::VEMPTY + sv));
-                        }
-                    }
-                    return true;
-                };
-                using H0 = std::integral_constant<int, 0>;
-                using H1 = std::integral_constant<int, HALVES - 1>;
-                if (!(ok = turn(H0{}))) break;
-                // (the next S's K is waited for while P . V runs: before it, a late K kept V from being given back)
-                if (then && !fresh && !(ok = see_k(q.base + q.x0 + jq * q.step, true))) break;
-                // (a new piece's Q and K: bf16 by halves, before the last P; else, as FP8's softmax warps split Q behind it, after)
-                constexpr bool EARLY = !FP8 && HALVES > 1;
-                if (EARLY && then && fresh && !(ok = see_q(q.q, true) && see_k(q.base + q.x0, true))) break;
-                if (HALVES > 1) {
-                    if (then && !fresh) issue_s(q, jq, H0{});
-                    if (!(ok = turn(H1{}))) break;
-                }
-                if (!EARLY && then && fresh && !(ok = see_q(q.q, true) && see_k(q.base + q.x0, true))) break;
-                if (then && fresh) tc_fence_after();
-                if (then && (fresh && HALVES > 1)) issue_s(q, jq, H0{});
-                if (then) issue_s(q, jq, H1{});
-                if (now) {
-                    bcnt += j + 1 == p.cnt && p.both;
-                    ++pcnt;
-                }
-                now = then;
-                p = q;
-                j = jq;
-            }
-            commit(lead, bar(K::DRAIN));
-            // every MMA issued has completed before TMEM is freed
-            const Ctl drain{drain_flag, a.err, a.wait_limit_ns};
-            wait(bar(K::DRAIN), 0, drain);
-            __syncwarp();
         }
     }
 
