@@ -605,13 +605,17 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, co
  *                  may be q (the same view)
  *   lse            optional device fp32 [num_q_rows][Hq]
  *   block_tables   as for pkv_paged_attention; entries of blocks that no query sees are never read, so blocks
- *                  behind the window may have been given back
+ *                  behind the window may have been given back (by the caller: no entry point pushes them onto the pool)
  *   context_lens, q_lens   device int32 [num_seqs], 0 <= q_lens[b] <= context_lens[b] <= 2^31 - 512
  *   q_starts       device int64 [num_seqs], each sequence's first row of q and out, or NULL: packed.  Rows
  *                  outside every sequence are left as they were
  *   num_q_rows     rows of q and out; 0: nothing is launched, so nothing is reported
  *   max_q_len      host upper bound of q_lens, >= 1.  It chooses the kernel (how many kv-heads share a row tile): a
- *                  bound far above the lengths costs speed
+ *                  bound far above the lengths costs speed, as do single tokens beside a prompt chunk in an FP8 call (64 and
+ *                  4 x 512, window 1024: 148 us, in two calls 123; bf16 104 and 107).  For FP8 caches
+ *                  max_blocks_per_seq (with a window, window + sinks + max_q_len too, if they are less) stands for the
+ *                  contexts' length in that choice: a table far wider than its contexts costs a few short ones up to a
+ *                  third (16 requests of 1024 keys 22 us, with a table of 8192 blocks 27.5)
  *   window         >= 1;  sinks >= 0
  *   scale          finite, > 0
  *   workspace      >= pkv_masked_workspace_size() bytes, 16-byte aligned, zeroed once (pkv_workspace_init), not
@@ -628,12 +632,14 @@ PKV_API pkv_status pkv_prompt_attention(const pkv_rows* q, const pkv_rows* k, co
  * split into two e4m3 terms (exact but for elements below 2^-10 of the row's largest, which are good to 2^-17 of it) and
  * multiplied with the codes as they are; the page's scale is applied to the sum in fp32; values are widened exactly.
  * Weights 2^(s - m) are rounded to bf16 for the product with V (8 significant bits; FP8: after the page's scale has been
- * applied in fp32), their sum is formed in fp32 before that.  m is the largest logit of a row's first keys, or a
+ * applied in fp32), their sum is formed in fp32 before that: an error of 0.0023 of out's norm, of which its own rounding is
+ * 0.0017.  (pkv_paged_attention, for few queries without a window, keeps weights in two parts: 0.0017 in all.)  m is the largest logit of a row's first keys, or a
  * later one: 64 weights may add up to 2^14 before it rises, so O may reach 2^14 times the largest value times the keys
  * (values of 2^96 and more may overflow).  Finite logits scale * q . k may reach 2^28 in magnitude; from about 1.4
  * times that on PKV_DEVERR_RANGE is set and the row's results are unspecified.  NaN or infinity in a key or value row
  * or an FP8 page's scale reaches the queries that see it, and no other (an infinite value as NaN where its weight
- * rounds to 0).  Deterministic: the same call gives the same bits.
+ * rounds to 0).  A query whose logits are all -infinity gets what one that sees nothing does: out = 0, lse = -inf.
+ * Deterministic: the same call gives the same bits.
  *
  * One launch.  It reads and writes nothing before the previous kernel on the stream has completed, and does not let
  * the next start early (out may be the q of a pkv_paged_attention behind it).  A wait inside it that runs out

@@ -27,7 +27,10 @@
 // up to 2^14 (bf16 has fp32's range) m rises.
 //
 // P is rounded to bf16 (8 significant bits; l is summed from the fp32 P): the error it leaves in out is of the size
-// of out's own rounding to bf16.  fp16 would hold 11 bits, but not V's range.
+// of out's own rounding to bf16, so that out's error (relative to its norm) is 0.0023 where P in fp32 gives 0.0017.  P in two
+// bf16 parts, as pkv_paged_attention has it, gives 0.0017 too, but takes the decode step below from 30.0 to 31.6 us, the FP8
+// streams from 223 to 248, the trees from 63 to 69 (FP8 193 to 238), prompts from 115 to 130 and FP8 chunks from 180 to 216:
+// not taken.  fp16 would hold 11 bits, but not V's range.
 // FP8 caches: S on e4m3 MMAs, the K pages as they are; a row of q is scaled by a power of two to a maximum in [128,
 // 256) and split into two e4m3 terms (exact but for elements below 2^-10 of the row's largest, which are good to 2^-17 of
 // it).  V is widened to bf16 in shared memory (exact).  A page's k scale multiplies its S and its v scale its P, in fp32.
@@ -40,15 +43,15 @@
 //
 // Measured (32/8 heads of 128, inputs past L2, back to back in a graph; copies run at 6786 GB/s, bf16 products at 1965
 // TFLOP/s): a decode step of 32 sequences, window 1024: 30 us for 133 MB (0.65 of the copy rate); 2048 sequences of 300
-// keys: 389 us (0.86).  128 FP8 streams, window 4096: 226 us (0.67).  Trees of 9 to 24 nodes over 32 contexts of 512 to
-// 4072: 64 us (0.75); of 64 nodes over 16 FP8 contexts of 8k to 16k: 193 us (0.58 of the product rate).  Four 2k prompts,
-// window 512: 116 us, FP8 chunks, window 2048: 175 us (0.27 and 0.35 of the product rate, by the visible pairs; the tiles at
+// keys: 392 us (0.86).  128 FP8 streams, window 4096: 224 us (0.68).  Trees of 9 to 24 nodes over 32 contexts of 512 to
+// 4072: 65 us (0.74); of 64 nodes over 16 FP8 contexts of 8k to 16k: 194 us (0.58 of the product rate).  Four 2k prompts,
+// window 512: 116 us, FP8 chunks, window 2048: 177 us (0.27 and 0.35 of the product rate, by the visible pairs; the tiles at
 // a window's two ends are computed whole).
 // What bounds it: with few rows the copies and, FP8, the widening (1600 of a tile's 2050 clocks); with many the chain S ->
 // P -> P . V of a row tile, 3600 clocks for a key tile of both chains, of which 2560 are reads and writes of shared memory (128
-// bytes a clock; Q is read once for each half of S), and 9000 at a change of item.  Beneath both lies the
-// instruction cache: five roles' code side by side misses it in 18 % of its requests, so that whatever was unrolled or doubled
-// (a masked copy of the softmax, 64 columns an epilogue step) made it slower, and loops outside the inner ones are
+// bytes a clock; Q is read once for each half of S), and 9000 at a change of item.  Beside both, five roles' code shares an
+// instruction cache (4 to 12 % of its requests miss), and times depend on how the code comes out: whatever was unrolled or
+// doubled (a masked copy of the softmax, 64 columns an epilogue step) made it slower, and loops outside the inner ones are
 // kept rolled.
 #include <cuda.h>
 
