@@ -50,8 +50,11 @@ __device__ __forceinline__ bool slot_block(int64_t s, int64_t num_blocks, int64_
     return true;
 }
 
+// (Slots and positions are no read-only data to these kernels, which might be moved before the dependency wait:
+// pkv_block_tables_update ahead of them may write both.)
+
 // Mark the scales of the blocks this call starts (one thread per token and kv-head).
-__global__ void __launch_bounds__(kThreads) mark_kernel(const int64_t* __restrict__ slots, int64_t T, int Hkv,
+__global__ void __launch_bounds__(kThreads) mark_kernel(const int64_t* slots, int64_t T, int Hkv,
                                                         int64_t num_blocks, uint32_t* k_scales, uint32_t* v_scales) {
     griddep_launch();
     griddep_wait();
@@ -71,8 +74,8 @@ __global__ void __launch_bounds__(kThreads) mark_kernel(const int64_t* __restric
 // one warp per kv-head at a time).
 __global__ void __launch_bounds__(kThreads) absmax_kernel(const __nv_bfloat16* __restrict__ k_new,
                                                           const __nv_bfloat16* __restrict__ v_new,
-                                                          const int64_t* __restrict__ slots,
-                                                          const int32_t* __restrict__ positions, double theta,
+                                                          const int64_t* slots,
+                                                          const int32_t* positions, double theta,
                                                           int Hkv, int D, int64_t num_blocks, uint32_t* k_scales,
                                                           uint32_t* v_scales) {
     __shared__ double2 cs[kMaxHalf];
@@ -137,8 +140,8 @@ __device__ __forceinline__ float final_scale(uint32_t* sp, bool owner) {
 // with the page's scale).
 template <int E, bool AUTOSCALE>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(
-    const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new, const int64_t* __restrict__ slots,
-    const int32_t* __restrict__ positions, double theta, __nv_bfloat16* q, int Hq, int Hkv, int D, int64_t num_blocks,
+    const __nv_bfloat16* __restrict__ k_new, const __nv_bfloat16* __restrict__ v_new, const int64_t* slots,
+    const int32_t* positions, double theta, __nv_bfloat16* q, int Hq, int Hkv, int D, int64_t num_blocks,
     uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales, int* err) {
     extern __shared__ __align__(16) uint8_t rope_smem[];
     __shared__ double2 cs[kMaxHalf];

@@ -86,3 +86,65 @@ def test_tables_append_full_attention(dtype, seqs, captured):
             want = torch.einsum("kgt,tkd->kgd", torch.softmax(x, -1), vv).reshape(heads, dim)
             assert ((out[i].double() - want).abs() <= 2e-3 + 1e-2 * want.abs()).all()
             i += 1
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("kind", ["rope", "rope_scales", "norm_rope", "norm_rope_scales"])
+def test_tables_and_appends_that_rotate(kind, captured):
+    """Slots and positions of the call before, in the appends that rotate: the cache and q as with slots and positions that
+    were there long before."""
+    rnd = random.Random(2)
+    seqs, heads, kv, dim, bound = 9, 4, 2, 64, 30
+    dtype = "fp8" if "scales" in kind else "bf16"
+    m = Model(seqs * 14, 12, [rnd.randint(0, 60) for _ in range(seqs)], rnd)
+    pool, table, lens = on_gpu(m)
+    sc = lambda: dict(k_scales=torch.ones(seqs * 14, kv, device="cuda"), v_scales=torch.ones(seqs * 14, kv, device="cuda"))  # noqa: E731
+    caches = [nat.PagedKVCache(seqs * 14, kv, dim, dtype, **(sc() if dtype == "fp8" else {})) for _ in range(2)]
+    for c in caches:
+        c.k.zero_()
+        c.v.zero_()
+    k, v = (torch.randn(bound, kv, dim, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(bound, heads, dim, device="cuda").bfloat16()
+    grow, rope = ints([0] * seqs), nat.Rope(dim)
+    slots, positions = (torch.zeros(bound, dtype=t, device="cuda") for t in (torch.int64, torch.int32))
+
+    def append(cache, slots, positions, q):
+        if kind.startswith("norm"):
+            return nat.append_norm_rope(cache, q, k, v, slots, positions=positions, rope=rope, fp8_scales_from_values="scales" in kind)
+        nat.append_rope(cache, k, v, slots, positions=positions, q=q, fp8_scales_from_values="scales" in kind)
+        return q
+
+    inplace = q.clone()
+
+    def step():
+        nat.update_tables(pool, table, lens, grow, bound, slots=slots, positions=positions, pad=True)
+        return append(caches[0], slots, positions, inplace)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    stream.synchronize()
+    call = step
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = step()
+        call = lambda: graph.replay() or got  # noqa: E731
+    for turn in range(12):
+        change = [rnd.randint(0, 3) if m.lens[b] < 180 else -100 for b in range(seqs)]
+        grow.copy_(ints(change))
+        rows, _, _, code = m.update(change, bound)
+        inplace.copy_(q)
+        slots.fill_(rnd.randrange(seqs * 14 * 16))
+        positions.fill_(rnd.randrange(1000))
+        torch.cuda.synchronize()
+        out = call()
+        torch.cuda.synchronize()
+        n = len(rows)
+        want = append(caches[1], torch.tensor([w[0] for w in rows] + [-1] * (bound - n), device="cuda"),
+                      ints([w[1] for w in rows] + [0] * (bound - n)), q.clone())
+        assert code == 0 and torch.equal(out[:n], want[:n])
+        assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+        if dtype == "fp8":
+            assert torch.equal(caches[0].k_scales, caches[1].k_scales) and torch.equal(caches[0].v_scales, caches[1].v_scales)
